@@ -88,6 +88,14 @@ bool make_layout(int64_t T, int64_t d, int64_t V, int64_t chunk, int dtype, int 
 int choose_splits(int64_t rows, int64_t d, int64_t V, int num_sms);
 int num_sms();
 
+// ----- shared by the entry points (sbp_api.cu) -----
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Records the launches of a successful call (sbp_last_launch_count).
+void set_launch_count(int n);
+// Fills (check = 0) or verifies (check = 1) a workspace's guard zones; nothing in the
+// release build.  Returns an sbp_status and adds its launches.
+int workspace_guards(void* ws, const Guards& g, int check, int32_t* status, cudaStream_t s, int* launches);
+
 // ----- launchers (enqueue only; return cudaError_t of the launch) -----
 
 // tensor-core kernels (bf16 operands), sbp_tc.cu

@@ -485,6 +485,20 @@ inline bool make_map_mn2(CUtensorMap* m, const void* ptr, uint64_t outer, uint64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D bf16 map over head-major attention operands [heads, T, hd] (dims hd, T, heads): boxes
+// of 64 x rows x 1, 128-byte swizzle, zero fill past hd and past T in each head.
+inline bool make_map_heads(CUtensorMap* m, const void* ptr, int64_t T, int64_t heads, int64_t hd, uint32_t rows) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)T, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)T * (cuuint64_t)hd * 2};
+  cuuint32_t box[3] = {64, rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Failure-detection test hook: SBP_FAULT_STALL=1 makes the next forward kernels stall
 // on purpose (read at every launch, so a test can switch it off again).  Together with a
 // short SBP_WAIT_LIMIT_MS it exercises the bounded-wait abort path: status
