@@ -70,6 +70,8 @@ extern "C" {
 #define SBP_ERR_SCRATCH_LIMIT 8 /* sizes need more scratch than sbp_lmhead_sft_noalloc has */
 #define SBP_ERR_WORKSPACE_OVERRUN 9 /* (device, checked build only) a kernel wrote into a guard
                                        zone between workspace regions                     */
+#define SBP_ERR_SEQLENS 10      /* (device) cu_seqlens not 0 at the start, decreasing or past T;
+                                   a negative prefix length                               */
 
 /* operand dtypes */
 #define SBP_BF16 0
@@ -242,6 +244,103 @@ int sbp_attn_causal_backward_gqa(const void* Q, const void* K, const void* V, co
                                  const float* lse, int64_t H, int64_t Hkv, int64_t T, int64_t hd, float scale,
                                  int64_t chunk, void* dQ, float* dK, float* dV, int accumulate,
                                  void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Attention over packed documents, forward and backward: what a training step needs where
+ * several documents share one sequence of T tokens, with capped or distance-biased scores.
+ * Document s holds the tokens [cu_seqlens[s], cu_seqlens[s+1]) (device int32 [n_seq+1], from
+ * 0, non-decreasing, at most T; empty documents are allowed; NULL with n_seq = 0: one
+ * document of T tokens).  Query i sees key j of its own document if j <= i, or if j is one
+ * of the document's first prefix_lens[s] tokens (device int32 [n_seq], or [1] without
+ * cu_seqlens; NULL: none; a longer prefix than the document makes all of it visible both
+ * ways).  Per query head h, with key / value head h / (H / Hkv):
+ *     t = scale q_i . k_j,   x = softcap tanh(t / softcap)  (softcap > 0)  or  t  (softcap = 0),
+ *     x -= slopes[h] |i - j|   (device fp32 [H], constants of the model; NULL: none),
+ *     P = softmax over the visible keys,  O = P V,  lse_i = log sum_j exp(x_ij),
+ * and for dO = dL/dO:  D_i = dO_i . O_i,  dS = P (dO V^T - D) (1 - tanh^2(t / softcap)),
+ *     dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO  (dK, dV summed over the group).
+ *   Q, O, dO, dQ [H, T, hd] bf16;  K, V, dK, dV [Hkv, T, hd] bf16;  lse [H, T] fp32.
+ * Tokens behind the last document see nothing and are seen by nothing: O, dQ, dK and dV
+ * are written as 0 there and lse as -infinity, whatever the inputs hold in those rows.
+ * (Within the documents a value that is not finite may reach rows of a neighbouring
+ * document, as 0 times infinity.)  The backward takes O and lse of the forward with the
+ * same arguments.
+ * hd: a multiple of 8, at most 128.  scale > 0, softcap >= 0, both finite.  Fixed order of
+ * every sum: the same call gives the same bits.  Workspace, stream and error rules as for
+ * the LM-head calls (cu_seqlens and prefix_lens are read by the device only, so a captured
+ * call follows their contents: a bad table sets SBP_ERR_SEQLENS); the workspace query
+ * returns 0 for arguments no call accepts. */
+size_t sbp_attn_packed_workspace_bytes(int64_t H, int64_t Hkv, int64_t T, int64_t hd);
+int sbp_attn_packed_forward(const void* Q, const void* K, const void* V, const int32_t* cu_seqlens,
+                            const int32_t* prefix_lens, int32_t n_seq, const float* slopes,
+                            int64_t H, int64_t Hkv, int64_t T, int64_t hd, float scale, float softcap,
+                            void* O, float* lse,
+                            void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+int sbp_attn_packed_backward(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                             const float* lse, const int32_t* cu_seqlens, const int32_t* prefix_lens,
+                             int32_t n_seq, const float* slopes,
+                             int64_t H, int64_t Hkv, int64_t T, int64_t hd, float scale, float softcap,
+                             void* dQ, void* dK, void* dV,
+                             void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Residual addition and root-mean-square norm (what stands before each sublayer of a
+ * pre-norm model), forward and backward:
+ *     R = X + residual  (residual nullable: R = X),   rstd = 1 / sqrt(mean(R^2) + eps),
+ *     Y = R rstd gamma.
+ * The norm takes the sum before it is rounded to dtype; sums and rstd are fp32.
+ *   X, residual, R, Y [T, d] dtype;  gamma [d] dtype.  R is where the sum is kept (nullable;
+ *   must be NULL without a residual); it may be X or residual itself.
+ * d must be a multiple of 8, at most 16384.  No workspace; nothing only the device could
+ * see can go wrong, so there is no status word. */
+int sbp_rmsnorm_forward(const void* X, const void* residual, const void* gamma, int64_t T, int64_t d,
+                        float eps, int dtype, void* R, void* Y, void* stream);
+
+/* The same with Y in 8 bits: Y8 [T, d] e4m3 (one byte each) and scales [T, ceil(d / 128)]
+ * fp32, one for each 128 columns of a row: Y ~ Y8 * scale, scale = max|Y| / 448 over the
+ * block (1 for a block of zeros).  Half the bytes of a bf16 Y, for the normalised input that
+ * is kept between a sublayer's forward and its backward; sbp_e4m3_expand gives it back in
+ * `dtype` (bf16 for sbp_mlp_swiglu_backward's X). */
+int sbp_rmsnorm_forward_e4m3(const void* X, const void* residual, const void* gamma, int64_t T, int64_t d,
+                             float eps, int dtype, void* R, void* Y8, float* scales, void* stream);
+int sbp_e4m3_expand(const void* Y8, const float* scales, int64_t T, int64_t d, int dtype, void* Y,
+                    void* stream);
+
+/* Gradients of the norm at the stored sum R, with dY = dL/dY and dR = the gradient that
+ * reaches R by the residual stream (nullable: none):
+ *     g = dY gamma,  dX = rstd (g - R rstd^2 mean(g R)) + dR,  dgamma (+)= sum_t dY R rstd.
+ * dX is the gradient of X and of residual alike.
+ *   dY, R, dR, dX [T, d] dtype;  gamma [d] dtype;  dgamma [d] fp32 (overwritten when
+ *   accumulate = 0, added to when 1).  dX may be dY or dR itself.
+ * Fixed order of every sum.  Workspace, stream and error rules as for the LM-head calls. */
+size_t sbp_rmsnorm_backward_workspace_bytes(int64_t T, int64_t d, int dtype);
+int sbp_rmsnorm_backward(const void* dY, const void* R, const void* gamma, const void* dR, int64_t T, int64_t d,
+                         float eps, int dtype, void* dX, float* dgamma, int accumulate,
+                         void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Rotary positions with one to four axes (text: one; images and video: height and width,
+ * time) between a token-major projection and the head-major operands of the attention calls.
+ *   qkv [T, row_stride] bf16: H query, Hkv key and Hkv value heads of hd elements a token;
+ *   row_stride in elements, a multiple of 8 (a slice of a wider buffer is fine).
+ *   positions [n_axes, T] int32 (device).  sections [n_axes] int32 (HOST memory): how many
+ *   of the rot_dim / 2 pairs, in order, turn by each axis; they add up to rot_dim / 2.
+ *   inv_freq [rot_dim / 2] fp64 (HOST memory, nullable): radians a position for each pair;
+ *   NULL: theta^(-2p / rot_dim).
+ *   Pair p of the first rot_dim elements of a head is (p, p + rot_dim / 2), or, interleaved
+ *   = 1, (2p, 2p + 1):  y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a,  a = position
+ *   times inv_freq, exact for positions of any size.  Other elements and the value heads pass.
+ *   Q [H, T, hd], K, V [Hkv, T, hd] bf16.
+ * Backward: dqkv from dQ (bf16), dK and dV (both kv_dtype: SBP_BF16, or SBP_FP32 as
+ * sbp_attn_causal_backward leaves them), turned back; elements between the heads and
+ * row_stride are left as they are.
+ * hd and rot_dim must be multiples of 16, hd at most 256.  The host arrays are read before
+ * the call returns.  No workspace and no status word. */
+int sbp_rope_qkv_forward(const void* qkv, int64_t row_stride, const int32_t* positions, int32_t n_axes,
+                         const int32_t* sections, const double* inv_freq, double theta, int64_t rot_dim,
+                         int interleaved, int64_t T, int64_t H, int64_t Hkv, int64_t hd,
+                         void* Q, void* K, void* V, void* stream);
+int sbp_rope_qkv_backward(const void* dQ, const void* dK, const void* dV, int kv_dtype, const int32_t* positions,
+                          int32_t n_axes, const int32_t* sections, const double* inv_freq, double theta,
+                          int64_t rot_dim, int interleaved, int64_t T, int64_t H, int64_t Hkv, int64_t hd,
+                          void* dqkv, int64_t row_stride, void* stream);
 
 /* Size of the fixed scratch array that sbp_lmhead_sft_noalloc works in (bytes). */
 #define SBP_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)

@@ -1338,6 +1338,11 @@ int noalloc_scratch(void** out) {
   return SBP_OK;
 }
 }  // namespace
+
+void set_launch_count(int n) { g_launches = n; }
+int workspace_guards(void* ws, const Guards& g, int check, int32_t* status, cudaStream_t s, int* launches) {
+  return guard_zones(ws, g, check, status, s, launches);
+}
 }  // namespace sbp
 
 using namespace sbp;
@@ -1514,6 +1519,7 @@ const char* sbp_status_string(int status) {
     case SBP_ERR_UNSUPPORTED: return "SBP_ERR_UNSUPPORTED";
     case SBP_ERR_SCRATCH_LIMIT: return "SBP_ERR_SCRATCH_LIMIT";
     case SBP_ERR_WORKSPACE_OVERRUN: return "SBP_ERR_WORKSPACE_OVERRUN";
+    case SBP_ERR_SEQLENS: return "SBP_ERR_SEQLENS";
     default: return "SBP_ERR_UNKNOWN";
   }
 }

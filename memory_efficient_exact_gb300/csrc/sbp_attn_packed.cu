@@ -1,0 +1,581 @@
+// Attention over packed documents: the preparing kernel, the score policy of the backward
+// kernels (sbp_attn_fused.cuh), and the entry points.  The forward kernel is in
+// sbp_attn_fwd.cu, the definition of what a query sees in sbp_attn_packed.cuh.
+#include <algorithm>
+#include <cmath>
+
+#include "sbp_attn_fused.cuh"
+#include "sbp_attn_packed.cuh"
+
+namespace sbp {
+namespace tc {
+namespace pk {
+
+struct KvParams {
+  int H, Hkv, T, c0, c1, hd, group, n_units;
+  float scale;
+  Scale sc;
+  const float *slopes, *lse, *D;
+  const int32_t *qlo, *qhi;
+  const PackedKvUnit* units;
+  const int32_t* tail;
+  __nv_bfloat16 *dK, *dV;
+  int32_t* status;
+  uint64_t limit_ns;
+};
+struct QParams {
+  int H, T, c0, c1, hd, group, n_units;
+  float scale;
+  Scale sc;
+  const float *slopes, *lse, *D;
+  const int32_t *lo, *hi;
+  const PackedQUnit* units;
+  const int32_t* tail;
+  __nv_bfloat16* dQ;
+  int32_t* status;
+  uint64_t limit_ns;
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Columns [c, c + n) of a row of width hd (a multiple of 8) from fp32 v, times f, in bf16.
+template <int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int hd, int c, const uint32_t (&v)[N], float f) {
+  uint4* o = reinterpret_cast<uint4*>(row + c);
+#pragma unroll
+  for (int k = 0; k < N / 8; ++k)
+    if (c + 8 * k < hd) {
+      const uint32_t* e = &v[8 * k];
+      o[k] = make_uint4(pack2(__uint_as_float(e[0]) * f, __uint_as_float(e[1]) * f),
+                        pack2(__uint_as_float(e[2]) * f, __uint_as_float(e[3]) * f),
+                        pack2(__uint_as_float(e[4]) * f, __uint_as_float(e[5]) * f),
+                        pack2(__uint_as_float(e[6]) * f, __uint_as_float(e[7]) * f));
+    }
+}
+
+// Score policy (see CausalScores): documents, prefixes, cap and distance bias; the units
+// and intervals come from the preparing kernel, and every output element is written once,
+// in bf16 (dK and dV of a key sum over the group's heads in tensor memory).
+template <bool CAP, bool BIAS>
+struct PackedScores {
+  using Kv = KvParams;
+  using Q = QParams;
+  using KvMaps = fa::MapArray<fa::KV_MAPS>;
+  using QMaps = fa::MapArray<fa::Q_MAPS + 1>;
+  // a masked pair's score may be infinite or NaN (another document's values)
+  static constexpr bool kClearMasked = true;
+  static constexpr bool kAddOut = false;
+  using Scale = ScaleZ;
+
+  static __device__ __forceinline__ void kv_unit(const Kv& p, int u, int& zk, int& kp, int& b0, int& nbl) {
+    const int i = u / p.Hkv;
+    zk = u - i * p.Hkv;
+    const int4 w = *reinterpret_cast<const int4*>(p.units + i);
+    kp = w.x; b0 = w.y; nbl = w.z;
+  }
+  static __device__ __forceinline__ void key_range(const Kv& p, int key, int& lo, int& hi) {
+    lo = key < p.T ? p.qlo[key] : p.T;
+    hi = key < p.T ? p.qhi[key] : p.T;
+  }
+  static __device__ __forceinline__ void ends(int lo, int hi, int& lo0, int& lo1, int& hi0, int& hi1) {
+    lo0 = __shfl_sync(0xffffffffu, lo, 0);
+    lo1 = __shfl_sync(0xffffffffu, lo, 31);
+    hi0 = __shfl_sync(0xffffffffu, hi, 0);
+    hi1 = __shfl_sync(0xffffffffu, hi, 31);
+  }
+  static __device__ __forceinline__ void key_warp(const Kv&, int, int lo, int hi, int& lo0, int& lo1, int& hi0,
+                                                  int& hi1) {
+    ends(lo, hi, lo0, lo1, hi0, hi1);
+  }
+  static __device__ __forceinline__ void q_unit(const Q& p, int u, int& z, int& qp, int& j0, int& nj) {
+    const int i = u / p.H;
+    z = u - i * p.H;
+    const int4* s = reinterpret_cast<const int4*>(p.units + i);
+    const int4 a = s[0];
+    qp = a.x;
+    j0 = a.y;
+    nj = max(a.z, s[1].x) - a.y;
+  }
+  static __device__ __forceinline__ void query_range(const Q& p, int q, int& lo, int& hi) {
+    lo = q < p.T ? p.lo[q] : p.T;
+    hi = q < p.T ? p.hi[q] : p.T;
+  }
+  static __device__ __forceinline__ void query_warp(const Q&, int, int lo, int hi, int& lo0, int& lo1, int& hi0,
+                                                    int& hi1) {
+    ends(lo, hi, lo0, lo1, hi0, hi1);
+  }
+  template <class P>
+  static __device__ __forceinline__ int tail_block(const P& p) { return *p.tail; }
+  template <class P>
+  static __device__ __forceinline__ Scale scale_of(const P& p, int z) {
+    return Scale{p.sc.sl2, p.sc.c2, p.sc.k, BIAS ? p.slopes[z] * L2E : 0.f};
+  }
+  static __device__ __forceinline__ float log2p(const Scale& sc, float s, float lz, int dist, float& dc) {
+    float x;
+    if (CAP) {
+      x = capped<true>(sc, s, dc) - lz;
+    } else {
+      dc = 1.f;
+      x = fmaf(s, sc.sl2, -lz);
+    }
+    return BIAS ? fmaf(-sc.slope2, fabsf((float)dist), x) : x;
+  }
+  static __device__ __forceinline__ float grad(float p, float d, float dc) { return CAP ? p * d * dc : p * d; }
+
+  // 64 columns of dV (t = 0) or dK (t = 1) of one key
+  static __device__ __forceinline__ void store_out(const Kv& p, int t, int zk, int key, int c,
+                                                   const uint32_t (&ra)[2][32]) {
+    if (key >= p.T) return;
+    __nv_bfloat16* row = (t ? p.dK : p.dV) + ((int64_t)zk * p.T + key) * p.hd;
+    const float f = t ? p.scale : 1.f;
+    store_row(row, p.hd, c, ra[0], f);
+    store_row(row, p.hd, c + 32, ra[1], f);
+  }
+  static __device__ __forceinline__ void store_zero(const Kv& p, int zk, int key, int c) {
+    const uint32_t z[2][32] = {};
+    store_out(p, 0, zk, key, c, z);
+    store_out(p, 1, zk, key, c, z);
+  }
+  // 32 columns of dQ of one query (row ro of [H, T])
+  static __device__ __forceinline__ void store_dq(const Q& p, int64_t ro, int c, const uint32_t (&ra)[32]) {
+    store_row(p.dQ + ro * p.hd, p.hd, c, ra, p.scale);
+  }
+  static __device__ __forceinline__ void store_dq_zero(const Q& p, int64_t ro, int c) {
+    const uint32_t z[32] = {};
+    store_dq(p, ro, c, z);
+  }
+};
+
+// ------------------------------------------------------------------- preparing kernel
+
+constexpr int PREP_THREADS = 256;
+// Units are put in order of their length up to this many (ranking them is quadratic);
+// above, they keep the order of their rows.
+constexpr int RANK_MAX = 8192;
+
+struct PrepP {
+  const int32_t *cu, *prefix;   // nullable
+  int32_t n_seq;
+  int T, n_units;
+  int32_t *lo, *hi, *qlo, *qhi;
+  PackedQUnit *qraw, *qunits;
+  PackedKvUnit *kvraw, *kvunits;   // nullptr in the forward
+  int32_t* tail;
+  int token_blocks, tail_blocks, hd;
+  // copies of the last block's rows (a block a head): operand i has heads[i] heads
+  const __nv_bfloat16* tsrc[3];
+  __nv_bfloat16* tdst[3];
+  int heads[3];
+  // D = dO . O of the backward
+  const __nv_bfloat16 *O, *dO;
+  int64_t rows;
+  float* D;
+  int32_t* status;
+};
+
+// End of the documents, within [0, T].
+__device__ __forceinline__ int doc_end(const PrepP& p) { return p.cu ? min(max(p.cu[p.n_seq], 0), p.T) : p.T; }
+
+// Document of token t < doc_end: its rows [s, e) and its prefix length.
+__device__ __forceinline__ void doc_of(const PrepP& p, int t, int& s, int& e, int& pre) {
+  int d = 0;
+  if (p.cu) {
+    int a = 0, b = p.n_seq - 1;   // last d with cu[d] <= t (empty documents are passed over)
+    while (a < b) {
+      const int mid = a + (b - a + 1) / 2;
+      if (p.cu[mid] <= t) a = mid; else b = mid - 1;
+    }
+    d = a;
+    s = min(max(p.cu[d], 0), p.T);
+    e = min(max(p.cu[d + 1], s), p.T);
+  } else {
+    s = 0;
+    e = p.T;
+  }
+  pre = p.prefix ? min(max(p.prefix[d], 0), e - s) : 0;
+}
+__device__ __forceinline__ int upper_of(int t, int s, int pre) { return max(t + 1, s + pre); }
+__device__ __forceinline__ int qlower_of(int t, int s, int pre) { return t < s + pre ? s : t; }
+
+// Block 0: checks the documents and lists the units.  Then token_blocks blocks: the four
+// interval ends of each token; tail_blocks blocks: the last block's copies; the others: D.
+__global__ void __launch_bounds__(PREP_THREADS) k_packed_prep(const PrepP p) {
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0) {
+    __shared__ int bad;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    if (p.cu) {
+      bool b = tid == 0 && (p.cu[0] != 0 || p.cu[p.n_seq] > p.T);
+      for (int i = tid; i < p.n_seq; i += PREP_THREADS)
+        b = b || p.cu[i + 1] < p.cu[i] || (p.prefix && p.prefix[i] < 0);
+      if (b) bad = 1;
+    } else if (p.prefix && tid == 0 && p.prefix[0] < 0) {
+      bad = 1;
+    }
+    __syncthreads();
+    const int n_tok = doc_end(p);
+    if (tid == 0) *p.tail = n_tok < p.T && n_tok % 128 ? n_tok / 128 : -1;
+    if (tid == 0) *p.status = bad ? SBP_ERR_SEQLENS : SBP_OK;
+    const int nb = (p.T + 127) / 128;
+    for (int i = tid; i < p.n_units; i += PREP_THREADS) {
+      PackedQUnit w;
+      w.qp = i;
+      int ja[2], jb[2];
+      for (int h = 0; h < 2; ++h) {
+        const int q0 = 256 * i + 128 * h, q1 = min(q0 + 127, n_tok - 1);
+        if (q0 >= n_tok) {
+          ja[h] = jb[h] = h ? jb[0] : 0;
+          continue;
+        }
+        int s, e, pre;
+        doc_of(p, q0, s, e, pre);
+        ja[h] = s / 128;
+        doc_of(p, q1, s, e, pre);
+        jb[h] = min((upper_of(q1, s, pre) + 127) / 128, nb);
+        jb[h] = max(jb[h], ja[h]);
+      }
+      w.ja0 = ja[0];
+      w.jb0 = jb[0];
+      // unbroken for any table: the second range starts within or right behind the first
+      w.ja1 = min(max(ja[1], ja[0]), jb[0]);
+      w.jb1 = max(jb[1], w.ja1);
+      p.qraw[i] = w;
+      if (p.kvraw) {
+        const int k0 = 256 * i, k1 = min(k0 + 255, n_tok - 1);
+        PackedKvUnit v{i, 0, 0, 0};
+        if (k0 < n_tok) {
+          int s, e, pre;
+          doc_of(p, k0, s, e, pre);
+          v.b0 = qlower_of(k0, s, pre) / 128;
+          doc_of(p, k1, s, e, pre);
+          v.nb = max(min((e + 127) / 128, nb) - v.b0, 0);
+        }
+        p.kvraw[i] = v;
+      }
+    }
+    __syncthreads();
+    // longest units first: the last wave then holds the short ones
+    for (int i = tid; i < p.n_units; i += PREP_THREADS) {
+      const PackedQUnit w = p.qraw[i];
+      const int len = (w.jb0 - w.ja0) + (w.jb1 - w.ja1);
+      int r = i;
+      if (p.n_units <= RANK_MAX) {
+        r = 0;
+        for (int k = 0; k < p.n_units; ++k) {
+          const PackedQUnit o = p.qraw[k];
+          const int lo = (o.jb0 - o.ja0) + (o.jb1 - o.ja1);
+          r += lo > len || (lo == len && k < i);
+        }
+      }
+      p.qunits[r] = w;
+      if (p.kvraw) {
+        const PackedKvUnit v = p.kvraw[i];
+        r = i;
+        if (p.n_units <= RANK_MAX) {
+          r = 0;
+          for (int k = 0; k < p.n_units; ++k) {
+            const int lo = p.kvraw[k].nb;
+            r += lo > v.nb || (lo == v.nb && k < i);
+          }
+        }
+        p.kvunits[r] = v;
+      }
+    }
+    return;
+  }
+  if ((int)blockIdx.x <= p.token_blocks) {
+    const int t = ((int)blockIdx.x - 1) * PREP_THREADS + tid;
+    if (t >= p.T) return;
+    int lo = p.T, hi = p.T, qlo = p.T, qhi = p.T;
+    if (t < doc_end(p)) {
+      int s, e, pre;
+      doc_of(p, t, s, e, pre);
+      lo = s;
+      hi = upper_of(t, s, pre);
+      qlo = qlower_of(t, s, pre);
+      qhi = e;
+    }
+    p.lo[t] = lo;
+    p.hi[t] = hi;
+    p.qlo[t] = qlo;
+    p.qhi[t] = qhi;
+    return;
+  }
+  if ((int)blockIdx.x <= p.token_blocks + p.tail_blocks) {
+    const int n_tok = doc_end(p);
+    if (n_tok >= p.T || n_tok % 128 == 0) return;
+    int h = (int)blockIdx.x - 1 - p.token_blocks, i = 0;
+    while (h >= p.heads[i]) h -= p.heads[i++];
+    const int r0 = n_tok / 128 * 128, per = p.hd / 8;
+    for (int k = tid; k < 128 * per; k += PREP_THREADS) {
+      const int r = k / per, c = 8 * (k - r * per);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r0 + r < n_tok) v = *reinterpret_cast<const uint4*>(p.tsrc[i] + ((int64_t)h * p.T + r0 + r) * p.hd + c);
+      *reinterpret_cast<uint4*>(p.tdst[i] + ((int64_t)h * 128 + r) * p.hd + c) = v;
+    }
+    return;
+  }
+  // D: sixteen lanes a row, 16 bytes a lane and operand (hd <= 128)
+  const int64_t r = ((int64_t)blockIdx.x - 1 - p.token_blocks - p.tail_blocks) * (PREP_THREADS / 16) + tid / 16;
+  const int c = 8 * (tid % 16);
+  float acc = 0.f;
+  if (r < p.rows && c < p.hd) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p.O + r * p.hd + c);
+    const uint4 b = *reinterpret_cast<const uint4*>(p.dO + r * p.hd + c);
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack_bf16(av[i]), y = unpack_bf16(bv[i]);
+      acc = fmaf(x.x, y.x, acc);
+      acc = fmaf(x.y, y.y, acc);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (r < p.rows && c == 0) p.D[r] = acc;
+}
+
+}  // namespace pk
+}  // namespace tc
+
+// ========================================================================== host side
+
+namespace {
+
+struct PackedLayout {
+  size_t off_lo = 0, off_hi = 0, off_qlo = 0, off_qhi = 0, off_qraw = 0, off_qunits = 0, off_kvraw = 0,
+         off_kvunits = 0, off_tail = 0, off_tq = 0, off_to = 0, off_tkv = 0, off_d = 0, total = 0;
+  Guards guards;   // checked build only
+};
+
+bool packed_shape(int64_t H, int64_t Hkv, int64_t T, int64_t hd) {
+  return H >= 1 && Hkv >= 1 && Hkv <= H && H % Hkv == 0 && T >= 0 && hd >= 1;
+}
+// 16-byte rows; the kernels' tile is 128 wide; int32 row numbers
+bool packed_supported(int64_t H, int64_t T, int64_t hd) {
+  return hd % 8 == 0 && hd <= 128 && T <= (int64_t)1 << 30 && H <= (int64_t)1 << 20 &&
+         H * ((T + 255) / 256) <= INT32_MAX / 2 && (H * T + 15) / 16 + T / 256 < INT32_MAX / 2;
+}
+
+bool packed_layout(int64_t H, int64_t Hkv, int64_t T, int64_t hd, PackedLayout* L) {
+  if (!packed_shape(H, Hkv, T, hd) || !packed_supported(H, T, hd)) return false;
+  PackedLayout l;
+  const size_t t = (size_t)std::max<int64_t>(T, 1), n = (t + 255) / 256;
+  size_t o = 0;
+  l.off_lo = take_region(o, t * sizeof(int32_t), l.guards);
+  l.off_hi = take_region(o, t * sizeof(int32_t), l.guards);
+  l.off_qlo = take_region(o, t * sizeof(int32_t), l.guards);
+  l.off_qhi = take_region(o, t * sizeof(int32_t), l.guards);
+  l.off_qraw = take_region(o, n * sizeof(PackedQUnit), l.guards);
+  l.off_qunits = take_region(o, n * sizeof(PackedQUnit), l.guards);
+  l.off_kvraw = take_region(o, n * sizeof(PackedKvUnit), l.guards);
+  l.off_kvunits = take_region(o, n * sizeof(PackedKvUnit), l.guards);
+  l.off_tail = take_region(o, sizeof(int32_t), l.guards);
+  l.off_tq = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
+  l.off_to = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
+  l.off_tkv = take_region(o, (size_t)Hkv * 128 * hd * 2, l.guards);
+  l.off_d = take_region(o, (size_t)H * t * sizeof(float), l.guards);
+  l.total = o;
+  *L = l;
+  return true;
+}
+
+// Shared checks of both directions; everything here runs before anything is enqueued.
+int packed_check(const PackedArgs& a, std::initializer_list<const void*> tensors, void* ws, size_t ws_bytes,
+                 PackedLayout* L) {
+  if (!packed_shape(a.H, a.Hkv, a.T, a.hd) || !a.status) return SBP_ERR_INVALID_ARG;
+  if (!(a.scale > 0.f) || std::isinf(a.scale) || !(a.softcap >= 0.f) || std::isinf(a.softcap))
+    return SBP_ERR_INVALID_ARG;
+  if ((a.cu && a.n_seq < 1) || (!a.cu && a.n_seq != 0)) return SBP_ERR_INVALID_ARG;
+  if (!packed_layout(a.H, a.Hkv, a.T, a.hd, L)) return SBP_ERR_UNSUPPORTED;
+  for (const void* q : tensors) {
+    if (!q && a.T > 0) return SBP_ERR_INVALID_ARG;
+    if (!aligned16(q)) return SBP_ERR_ALIGNMENT;
+  }
+  for (const void* q : {(const void*)a.cu, (const void*)a.prefix, (const void*)a.slopes, (const void*)a.status})
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return SBP_ERR_ALIGNMENT;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L->total) return SBP_ERR_WORKSPACE;
+  return SBP_OK;
+}
+
+PackedWork packed_work(const PackedLayout& L, char* w) {
+  PackedWork k;
+  k.lo = reinterpret_cast<int32_t*>(w + L.off_lo);
+  k.hi = reinterpret_cast<int32_t*>(w + L.off_hi);
+  k.qlo = reinterpret_cast<int32_t*>(w + L.off_qlo);
+  k.qhi = reinterpret_cast<int32_t*>(w + L.off_qhi);
+  k.qunits = reinterpret_cast<PackedQUnit*>(w + L.off_qunits);
+  k.kvunits = reinterpret_cast<PackedKvUnit*>(w + L.off_kvunits);
+  k.tail = reinterpret_cast<int32_t*>(w + L.off_tail);
+  k.tail_q = w + L.off_tq;
+  k.tail_do = w + L.off_to;
+  k.tail_kv = w + L.off_tkv;
+  k.D = reinterpret_cast<float*>(w + L.off_d);
+  return k;
+}
+
+cudaError_t packed_prep(const PackedArgs& a, const PackedLayout& L, char* w, bool backward, cudaStream_t s) {
+  tc::pk::PrepP p{};
+  p.cu = a.cu; p.prefix = a.prefix; p.n_seq = a.n_seq;
+  p.T = (int)a.T; p.n_units = (int)((a.T + 255) / 256);
+  p.lo = reinterpret_cast<int32_t*>(w + L.off_lo);
+  p.hi = reinterpret_cast<int32_t*>(w + L.off_hi);
+  p.qlo = reinterpret_cast<int32_t*>(w + L.off_qlo);
+  p.qhi = reinterpret_cast<int32_t*>(w + L.off_qhi);
+  p.qraw = reinterpret_cast<PackedQUnit*>(w + L.off_qraw);
+  p.qunits = reinterpret_cast<PackedQUnit*>(w + L.off_qunits);
+  p.tail = reinterpret_cast<int32_t*>(w + L.off_tail);
+  p.hd = (int)a.hd;
+  p.tsrc[0] = static_cast<const __nv_bfloat16*>(backward ? a.K : a.V);
+  p.tdst[0] = reinterpret_cast<__nv_bfloat16*>(w + L.off_tkv);
+  p.heads[0] = (int)a.Hkv;
+  p.token_blocks = (int)((a.T + tc::pk::PREP_THREADS - 1) / tc::pk::PREP_THREADS);
+  p.status = a.status;
+  if (backward) {
+    p.tsrc[1] = static_cast<const __nv_bfloat16*>(a.Q);
+    p.tdst[1] = reinterpret_cast<__nv_bfloat16*>(w + L.off_tq);
+    p.tsrc[2] = static_cast<const __nv_bfloat16*>(a.dO);
+    p.tdst[2] = reinterpret_cast<__nv_bfloat16*>(w + L.off_to);
+    p.heads[1] = p.heads[2] = (int)a.H;
+  }
+  p.tail_blocks = p.heads[0] + p.heads[1] + p.heads[2];
+  int64_t blocks = 1 + p.token_blocks + p.tail_blocks;
+  if (backward) {
+    p.kvraw = reinterpret_cast<PackedKvUnit*>(w + L.off_kvraw);
+    p.kvunits = reinterpret_cast<PackedKvUnit*>(w + L.off_kvunits);
+    p.O = static_cast<const __nv_bfloat16*>(a.O);
+    p.dO = static_cast<const __nv_bfloat16*>(a.dO);
+    p.rows = a.H * a.T;
+    p.D = reinterpret_cast<float*>(w + L.off_d);
+    blocks += (p.rows + tc::pk::PREP_THREADS / 16 - 1) / (tc::pk::PREP_THREADS / 16);
+  }
+  tc::pk::k_packed_prep<<<(unsigned)blocks, tc::pk::PREP_THREADS, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <bool CAP, bool BIAS>
+cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedWork& w, void* dQ, void* dK, void* dV,
+                                    cudaStream_t s) {
+  using namespace tc::fa;
+  using S = tc::pk::PackedScores<CAP, BIAS>;
+  static int attr_state[64] = {};
+  static std::mutex mu;
+  if (!tc::once_per_device(attr_state, mu, [] {
+        return cudaFuncSetAttribute(k_attn_kv<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_KV) ==
+                   cudaSuccess &&
+               cudaFuncSetAttribute(k_attn_q<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_Q) ==
+                   cudaSuccess;
+      }))
+    return cudaErrorInvalidConfiguration;
+  const int n = (int)((a.T + 255) / 256);
+  MapArray<KV_MAPS> mk;
+  MapArray<Q_MAPS + 1> mq;
+  const struct { CUtensorMap* m; const void* ptr; int64_t T, heads; uint32_t rows; } list[] = {
+      {&mk.m[KV_MK], a.K, a.T, a.Hkv, 128},  {&mk.m[KV_MV], a.V, a.T, a.Hkv, 128},
+      {&mk.m[KV_MQA], a.Q, a.T, a.H, 64},    {&mk.m[KV_MOA], a.dO, a.T, a.H, 64},
+      {&mk.m[KV_MQB], a.Q, a.T, a.H, 128},   {&mk.m[KV_MOB], a.dO, a.T, a.H, 128},
+      {&mk.m[KV_MQT], w.tail_q, 128, a.H, 128}, {&mk.m[KV_MOT], w.tail_do, 128, a.H, 128},
+      {&mq.m[Q_MKA], a.K, a.T, a.Hkv, 64},   {&mq.m[Q_MVA], a.V, a.T, a.Hkv, 64},
+      {&mq.m[Q_MKT], w.tail_kv, 128, a.Hkv, 128}};
+  for (const auto& e : list)
+    if (!tc::make_map_heads(e.m, e.ptr, e.T, e.heads, a.hd, e.rows)) return cudaErrorInvalidValue;
+  mq.m[Q_MQ] = mk.m[KV_MQB];
+  mq.m[Q_MO] = mk.m[KV_MOB];
+  mq.m[Q_MKB] = mk.m[KV_MK];
+  tc::pk::KvParams k;
+  k.H = (int)a.H; k.Hkv = (int)a.Hkv; k.T = (int)a.T; k.c0 = 0; k.c1 = (int)a.T; k.hd = (int)a.hd;
+  k.group = (int)(a.H / a.Hkv); k.n_units = n * k.Hkv;
+  k.scale = a.scale; k.sc = tc::pk::make_scale(a.scale, a.softcap);
+  k.slopes = a.slopes; k.lse = a.lse; k.D = w.D; k.qlo = w.qlo; k.qhi = w.qhi; k.units = w.kvunits; k.tail = w.tail;
+  k.dK = static_cast<__nv_bfloat16*>(dK); k.dV = static_cast<__nv_bfloat16*>(dV);
+  k.status = a.status; k.limit_ns = tc::wait_limit_ns();
+  const int kv_pairs = std::min(tc::max_pairs((const void*)k_attn_kv<S>, SMEM_KV, KV_THREADS), k.n_units);
+  k_attn_kv<S><<<2 * kv_pairs, KV_THREADS, SMEM_KV, s>>>(mk, k);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  tc::pk::QParams q;
+  q.H = k.H; q.T = k.T; q.c0 = 0; q.c1 = k.c1; q.hd = k.hd; q.group = k.group; q.n_units = n * k.H;
+  q.scale = k.scale; q.sc = k.sc; q.slopes = k.slopes; q.lse = k.lse; q.D = k.D; q.lo = w.lo; q.hi = w.hi;
+  q.units = w.qunits; q.tail = w.tail; q.dQ = static_cast<__nv_bfloat16*>(dQ); q.status = k.status; q.limit_ns = k.limit_ns;
+  const int q_pairs = std::min(tc::max_pairs((const void*)k_attn_q<S>, SMEM_Q, Q_THREADS), q.n_units);
+  k_attn_q<S><<<2 * q_pairs, Q_THREADS, SMEM_Q, s>>>(mq, q);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace sbp
+
+using namespace sbp;
+
+extern "C" {
+
+size_t sbp_attn_packed_workspace_bytes(int64_t H, int64_t Hkv, int64_t T, int64_t hd) {
+  PackedLayout L;
+  return packed_layout(H, Hkv, T, hd, &L) ? L.total : 0;
+}
+
+int sbp_attn_packed_forward(const void* Q, const void* K, const void* V, const int32_t* cu_seqlens,
+                            const int32_t* prefix_lens, int32_t n_seq, const float* slopes, int64_t H, int64_t Hkv,
+                            int64_t T, int64_t hd, float scale, float softcap, void* O, float* lse, void* workspace,
+                            size_t ws_bytes, int32_t* dev_status, void* stream) {
+  PackedArgs a{Q, K, V, nullptr, nullptr, nullptr, cu_seqlens, prefix_lens, slopes, H, Hkv, T, hd, n_seq, scale,
+               softcap, dev_status};
+  PackedLayout L;
+  const int rc = packed_check(a, {Q, K, V, O, lse}, workspace, ws_bytes, &L);
+  if (rc != SBP_OK) return rc;
+  NvtxRange nv("sbp_attn_packed_forward");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(workspace);
+  if (T == 0) {
+    set_launch_count(0);
+    return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? SBP_OK : SBP_ERR_CUDA;
+  }
+  int launches = 2;
+  int st = workspace_guards(w, L.guards, 0, dev_status, s, &launches);
+  if (st != SBP_OK) return st;
+  if (packed_prep(a, L, w, false, s) != cudaSuccess) return SBP_ERR_CUDA;
+  if (packed_forward(a, packed_work(L, w), O, lse, s) != cudaSuccess) return SBP_ERR_CUDA;
+  st = workspace_guards(w, L.guards, 1, dev_status, s, &launches);
+  if (st == SBP_OK) set_launch_count(launches);
+  return st;
+}
+
+int sbp_attn_packed_backward(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                             const float* lse, const int32_t* cu_seqlens, const int32_t* prefix_lens, int32_t n_seq,
+                             const float* slopes, int64_t H, int64_t Hkv, int64_t T, int64_t hd, float scale,
+                             float softcap, void* dQ, void* dK, void* dV, void* workspace, size_t ws_bytes,
+                             int32_t* dev_status, void* stream) {
+  PackedArgs a{Q, K, V, O, dO, lse, cu_seqlens, prefix_lens, slopes, H, Hkv, T, hd, n_seq, scale, softcap, dev_status};
+  PackedLayout L;
+  const int rc = packed_check(a, {Q, K, V, O, dO, lse, dQ, dK, dV}, workspace, ws_bytes, &L);
+  if (rc != SBP_OK) return rc;
+  NvtxRange nv("sbp_attn_packed_backward");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(workspace);
+  if (T == 0) {
+    set_launch_count(0);
+    return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? SBP_OK : SBP_ERR_CUDA;
+  }
+  int launches = 3;
+  int st = workspace_guards(w, L.guards, 0, dev_status, s, &launches);
+  if (st != SBP_OK) return st;
+  if (packed_prep(a, L, w, true, s) != cudaSuccess) return SBP_ERR_CUDA;
+  const PackedWork k = packed_work(L, w);
+  cudaError_t e;
+  if (softcap > 0.f)
+    e = slopes ? packed_backward_kernels<true, true>(a, k, dQ, dK, dV, s)
+               : packed_backward_kernels<true, false>(a, k, dQ, dK, dV, s);
+  else
+    e = slopes ? packed_backward_kernels<false, true>(a, k, dQ, dK, dV, s)
+               : packed_backward_kernels<false, false>(a, k, dQ, dK, dV, s);
+  if (e != cudaSuccess) return SBP_ERR_CUDA;
+  st = workspace_guards(w, L.guards, 1, dev_status, s, &launches);
+  if (st == SBP_OK) set_launch_count(launches);
+  return st;
+}
+
+}  // extern "C"

@@ -1,0 +1,87 @@
+// Attention over packed documents (bf16, sm_103a): what its translation units share.
+//
+// The T tokens of a call are documents packed one behind the other, document s holding the
+// rows [cu[s], cu[s+1]); rows at and after cu[n_seq] are padding.  With p_s the prefix
+// length of document s, query i sees key j of its own document when j <= i or j lies in the
+// prefix, so what a query sees is one interval of keys, and what a key is seen by is one
+// interval of queries:
+//   [lo_i, hi_i)   = [cu[s], max(i + 1, cu[s] + p_s))
+//   [qlo_j, qhi_j) = [j < cu[s] + p_s ? cu[s] : j, cu[s+1])
+// All four ends are non-decreasing, so a tile's blocks are found from its first and last
+// row, and a tile is free of masking when its last row's lower end and its first row's
+// upper end lie outside it.
+// The score of a visible pair is  x = cap(scale q.k) - slope_h |i - j|  with
+// cap(t) = c tanh(t / c) (c > 0) or t (c = 0).
+#pragma once
+
+#include "sbp_tc_common.cuh"
+
+namespace sbp {
+
+// Work of one unit of 256 queries: key blocks (of 128) [ja0, jb0) for its first 128
+// queries and [ja1, jb1) for the others; ja0 <= ja1 <= jb0 <= jb1 (no gap between them).
+struct __align__(16) PackedQUnit { int qp, ja0, jb0, ja1, jb1, pad[3]; };
+// Work of one unit of 256 keys: query blocks (of 128) [b0, b0 + nb).
+struct __align__(16) PackedKvUnit { int kp, b0, nb, pad; };
+
+// What the kernels read besides the tensors; pointers into the workspace.
+struct PackedWork {
+  const int32_t *lo, *hi, *qlo, *qhi;   // [T]; rows behind the documents hold T in all four
+  const PackedQUnit* qunits;            // [ceil(T / 256)], the longest first
+  const PackedKvUnit* kvunits;          // [ceil(T / 256)], the longest first (backward)
+  // Where the documents end inside a block of 128 rows and padding follows: that block's
+  // number (else -1), and copies of its rows with the padding zeroed, [heads, 128, hd].  The
+  // products that sum over rows read these: a probability of 0 times whatever the padding
+  // holds would be NaN for an infinity or a NaN.
+  const int32_t* tail;
+  const void *tail_q, *tail_do;         // backward, H heads
+  const void* tail_kv;                  // V in the forward, K in the backward, Hkv heads
+  float* D;                             // [H, T] dO . O (backward)
+};
+
+struct PackedArgs {
+  const void *Q, *K, *V, *O, *dO;
+  const float* lse;
+  const int32_t *cu, *prefix;
+  const float* slopes;
+  int64_t H, Hkv, T, hd;
+  int32_t n_seq;
+  float scale, softcap;
+  int32_t* status;
+};
+
+namespace tc {
+namespace pk {
+
+// Constants of the score in log2 units.  x log2(e) = s sl2 without a cap; with one,
+// c tanh(y) = c - 2 c / (1 + e^(2 y)), y = s scale / c: one exponential and one reciprocal,
+// the absolute error about c 2^-22 (tanh.approx would leave c 2^-11).
+struct Scale { float sl2, c2, k; };
+struct ScaleZ { float sl2, c2, k, slope2; };
+
+template <bool CAP>
+__device__ __forceinline__ float capped(const ScaleZ& sc, float s, float& dc) {
+  if (CAP) {
+    const float w = __fdividef(1.f, 1.f + ex2(s * sc.k));
+    dc = 4.f * w * (1.f - w);   // 1 - tanh^2
+    return fmaf(-2.f * sc.c2, w, sc.c2);
+  }
+  dc = 1.f;
+  return s * sc.sl2;
+}
+
+inline Scale make_scale(float scale, float softcap) {
+  Scale s;
+  s.sl2 = scale * L2E;
+  s.c2 = softcap * L2E;
+  s.k = softcap > 0.f ? 2.f * L2E * scale / softcap : 0.f;
+  return s;
+}
+
+}  // namespace pk
+}  // namespace tc
+
+// O, lse of every row (sbp_attn_fwd.cu)
+cudaError_t packed_forward(const PackedArgs& a, const PackedWork& w, void* O, float* lse, cudaStream_t s);
+
+}  // namespace sbp

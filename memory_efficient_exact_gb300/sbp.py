@@ -8,6 +8,7 @@ has not been built (``__graft_entry__.build()``) -- there is no other code path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -24,7 +25,7 @@ LIB_PATH = os.path.join(_HERE, f"libsbp_{VARIANT}.so" if VARIANT else "libsbp.so
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "sbp.h")
 
 (OK, ERR_INVALID_ARG, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_LABEL_RANGE, ERR_TIMEOUT, ERR_CUDA, ERR_UNSUPPORTED,
- ERR_SCRATCH_LIMIT, ERR_WORKSPACE_OVERRUN) = range(10)
+ ERR_SCRATCH_LIMIT, ERR_WORKSPACE_OVERRUN, ERR_SEQLENS) = range(11)
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 BF16, FP32 = 0, 1
 MODE_SFT, MODE_GRPO, MODE_DPO1, MODE_DPO2 = 0, 1, 2, 3
@@ -43,7 +44,7 @@ def _load() -> ctypes.CDLL:
                           "(the LM-head kernels have no other implementation)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I64, I32, F, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
-    C = ctypes.c_int
+    C, D = ctypes.c_int, ctypes.c_double
     lib.sbp_lmhead_workspace_bytes.restype = SZ
     lib.sbp_lmhead_workspace_bytes.argtypes = [I64, I64, I64, I64, C, C]
     lib.sbp_lmhead_workspace_bytes_lean.restype = SZ
@@ -77,6 +78,27 @@ def _load() -> ctypes.CDLL:
     lib.sbp_attn_causal_backward_gqa.restype = C
     lib.sbp_attn_causal_backward_gqa.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, F, I64, P, P, P, C, P, SZ, P,
                                                  P]
+    lib.sbp_attn_packed_workspace_bytes.restype = SZ
+    lib.sbp_attn_packed_workspace_bytes.argtypes = [I64, I64, I64, I64]
+    lib.sbp_attn_packed_forward.restype = C
+    lib.sbp_attn_packed_forward.argtypes = [P, P, P, P, P, I32, P, I64, I64, I64, I64, F, F, P, P, P, SZ, P, P]
+    lib.sbp_attn_packed_backward.restype = C
+    lib.sbp_attn_packed_backward.argtypes = [P, P, P, P, P, P, P, P, I32, P, I64, I64, I64, I64, F, F, P, P, P, P,
+                                             SZ, P, P]
+    lib.sbp_rmsnorm_forward.restype = C
+    lib.sbp_rmsnorm_forward.argtypes = [P, P, P, I64, I64, F, C, P, P, P]
+    lib.sbp_rmsnorm_forward_e4m3.restype = C
+    lib.sbp_rmsnorm_forward_e4m3.argtypes = [P, P, P, I64, I64, F, C, P, P, P, P]
+    lib.sbp_e4m3_expand.restype = C
+    lib.sbp_e4m3_expand.argtypes = [P, P, I64, I64, C, P, P]
+    lib.sbp_rmsnorm_backward_workspace_bytes.restype = SZ
+    lib.sbp_rmsnorm_backward_workspace_bytes.argtypes = [I64, I64, C]
+    lib.sbp_rmsnorm_backward.restype = C
+    lib.sbp_rmsnorm_backward.argtypes = [P, P, P, P, I64, I64, F, C, P, P, C, P, SZ, P, P]
+    lib.sbp_rope_qkv_forward.restype = C
+    lib.sbp_rope_qkv_forward.argtypes = [P, I64, P, I32, P, P, D, I64, C, I64, I64, I64, I64, P, P, P, P]
+    lib.sbp_rope_qkv_backward.restype = C
+    lib.sbp_rope_qkv_backward.argtypes = [P, P, P, C, P, I32, P, P, D, I64, C, I64, I64, I64, I64, P, I64, P]
     lib.sbp_status_string.restype = ctypes.c_char_p
     lib.sbp_status_string.argtypes = [C]
     lib.sbp_last_launch_count.restype = C
@@ -445,3 +467,259 @@ def attn_causal_backward(Q, K, V, O, dO, lse, scale, chunk, *, dQ=None, dK=None,
                                                  _p(workspace), workspace.numel(), _p(st), _stream(stream)),
                "sbp_attn_causal_backward_gqa")
     return dict(dQ=dQ, dK=dK, dV=dV, status=st)
+
+
+def attn_packed_workspace_bytes(H: int, Hkv: int, T: int, hd: int) -> int:
+    return int(_lib.sbp_attn_packed_workspace_bytes(H, Hkv, T, hd))
+
+
+def _on_device(dev, *ts):
+    """Contiguous tensors of the current device (the library launches on it)."""
+    for t in ts:
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA tensors of one device")
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError("the tensors' device must be the current CUDA device")
+
+
+def _scratch(stream):
+    """What a call allocates belongs to the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream):
+    dev = Q.device
+    _on_device(dev, Q, K, V, cu_seqlens, prefix_lens, slopes, workspace)
+    if Q.dim() != 3 or K.dim() != 3 or K.shape != V.shape or Q.shape[1:] != K.shape[1:]:
+        raise ValueError("shapes: Q [H, T, hd]; K, V [Hkv, T, hd]")
+    if any(t.dtype != torch.bfloat16 for t in (Q, K, V)):
+        raise TypeError("Q, K, V must be bf16")
+    H, T, hd = Q.shape
+    Hkv = K.shape[0]
+    n_seq = 0
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be int32 [n_seq + 1], n_seq >= 1")
+        n_seq = cu_seqlens.numel() - 1
+    if prefix_lens is not None and (prefix_lens.dtype != torch.int32 or prefix_lens.shape != (max(n_seq, 1),)):
+        raise ValueError("prefix_lens must be int32 [n_seq]")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (H,)):
+        raise ValueError("slopes must be float32 [H]")
+    if workspace is None:
+        n = attn_packed_workspace_bytes(H, Hkv, T, hd)
+        if n == 0:
+            raise SbpError(ERR_UNSUPPORTED, "sbp_attn_packed_workspace_bytes")
+        with _scratch(stream):
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    return H, Hkv, T, hd, n_seq, workspace
+
+
+def attn_packed(Q, K, V, scale, *, cu_seqlens=None, prefix_lens=None, slopes=None, softcap=0.0, O=None, lse=None,
+                workspace=None, status=None, stream=None) -> dict:
+    """Attention over packed documents (``sbp_attn_packed_forward``): causal within each
+    document, with optional bidirectional prefixes, tanh-capped scores and distance bias.
+
+    Q [H, T, hd] bf16; K, V [Hkv, T, hd] bf16; cu_seqlens int32 [n_seq + 1] (None: one
+    document); prefix_lens int32 [n_seq]; slopes fp32 [H].  Returns O [H, T, hd] bf16 and
+    lse [H, T] fp32."""
+    H, Hkv, T, hd, n_seq, ws = _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream)
+    dev = Q.device
+    with _scratch(stream):
+        O = torch.empty_like(Q) if O is None else O
+        lse = torch.empty((H, T), dtype=torch.float32, device=dev) if lse is None else lse
+        st = torch.empty((), dtype=torch.int32, device=dev) if status is None else status
+    _on_device(dev, O, lse, st)
+    if O.shape != Q.shape or O.dtype != Q.dtype or lse.shape != (H, T) or lse.dtype != torch.float32:
+        raise ValueError("O bf16 [H, T, hd]; lse fp32 [H, T]")
+    _check(_lib.sbp_attn_packed_forward(_p(Q), _p(K), _p(V), _p(cu_seqlens), _p(prefix_lens), n_seq, _p(slopes), H,
+                                        Hkv, T, hd, float(scale), float(softcap), _p(O), _p(lse), _p(ws), ws.numel(),
+                                        _p(st), _stream(stream)), "sbp_attn_packed_forward")
+    return dict(O=O, lse=lse, status=st)
+
+
+def attn_packed_backward(Q, K, V, O, dO, lse, scale, *, cu_seqlens=None, prefix_lens=None, slopes=None, softcap=0.0,
+                         dQ=None, dK=None, dV=None, workspace=None, status=None, stream=None) -> dict:
+    """Gradients of ``attn_packed`` (``sbp_attn_packed_backward``): dQ [H, T, hd] and dK, dV
+    [Hkv, T, hd] in bf16.  O and lse are the forward's, with the same arguments."""
+    H, Hkv, T, hd, n_seq, ws = _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream)
+    dev = Q.device
+    with _scratch(stream):
+        dQ = torch.empty_like(Q) if dQ is None else dQ
+        dK = torch.empty_like(K) if dK is None else dK
+        dV = torch.empty_like(V) if dV is None else dV
+        st = torch.empty((), dtype=torch.int32, device=dev) if status is None else status
+    _on_device(dev, O, dO, lse, dQ, dK, dV, st)
+    if any(t.shape != Q.shape or t.dtype != torch.bfloat16 for t in (O, dO, dQ)):
+        raise ValueError("O, dO, dQ must be bf16 [H, T, hd]")
+    if any(t.shape != K.shape or t.dtype != torch.bfloat16 for t in (dK, dV)):
+        raise ValueError("dK, dV must be bf16 [Hkv, T, hd]")
+    if lse.shape != (H, T) or lse.dtype != torch.float32:
+        raise ValueError("lse must be fp32 [H, T]")
+    _check(_lib.sbp_attn_packed_backward(_p(Q), _p(K), _p(V), _p(O), _p(dO), _p(lse), _p(cu_seqlens), _p(prefix_lens),
+                                         n_seq, _p(slopes), H, Hkv, T, hd, float(scale), float(softcap), _p(dQ),
+                                         _p(dK), _p(dV), _p(ws), ws.numel(), _p(st), _stream(stream)),
+           "sbp_attn_packed_backward")
+    return dict(dQ=dQ, dK=dK, dV=dV, status=st)
+
+
+def _norm_args(X, gamma, *rows):
+    if X.dim() != 2 or gamma.shape != (X.shape[1],) or gamma.dtype != X.dtype:
+        raise ValueError("shapes: rows [T, d]; gamma [d], all of one dtype")
+    for t in rows:
+        if t is not None and (t.shape != X.shape or t.dtype != X.dtype):
+            raise ValueError("residual and gradients must be shaped and typed like the rows")
+    T, d = X.shape
+    return T, d, _code(X)
+
+
+def _rmsnorm(X, gamma, eps, residual, R, stream, q8, Y, scales):
+    dev = X.device
+    _on_device(dev, X, gamma, residual, R, Y, scales)
+    T, d, dt = _norm_args(X, gamma, residual, R)
+    if residual is None and R is not None:
+        raise ValueError("R is the sum with the residual: pass both or neither")
+    nblk = (d + 127) // 128
+    with _scratch(stream):
+        if residual is not None and R is None:
+            R = torch.empty_like(X)
+        if Y is None:
+            Y = torch.empty((T, d), dtype=torch.float8_e4m3fn if q8 else X.dtype, device=dev)
+        if q8 and scales is None:
+            scales = torch.empty((T, nblk), dtype=torch.float32, device=dev)
+    if Y.shape != X.shape or Y.dtype != (torch.float8_e4m3fn if q8 else X.dtype):
+        raise ValueError("Y must be shaped like X, of its dtype (e4m3 for the 8-bit output)")
+    if q8:
+        if scales.shape != (T, nblk) or scales.dtype != torch.float32:
+            raise ValueError("scales must be float32 [T, ceil(d / 128)]")
+        _check(_lib.sbp_rmsnorm_forward_e4m3(_p(X), _p(residual), _p(gamma), T, d, float(eps), dt, _p(R), _p(Y),
+                                             _p(scales), _stream(stream)), "sbp_rmsnorm_forward_e4m3")
+        return dict(Y8=Y, scales=scales, R=X if residual is None else R)
+    _check(_lib.sbp_rmsnorm_forward(_p(X), _p(residual), _p(gamma), T, d, float(eps), dt, _p(R), _p(Y),
+                                    _stream(stream)), "sbp_rmsnorm_forward")
+    return dict(Y=Y, R=X if residual is None else R)
+
+
+def rmsnorm(X, gamma, eps, *, residual=None, R=None, Y=None, stream=None) -> dict:
+    """R = X + residual and its root-mean-square norm Y (``sbp_rmsnorm_forward``).
+
+    X, residual [T, d] bf16 or fp32, gamma [d] of the same dtype.  R is X itself without a
+    residual; R=residual updates the residual in place."""
+    return _rmsnorm(X, gamma, eps, residual, R, stream, False, Y, None)
+
+
+def rmsnorm_e4m3(X, gamma, eps, *, residual=None, R=None, Y8=None, scales=None, stream=None) -> dict:
+    """``rmsnorm`` with Y in 8 bits (``sbp_rmsnorm_forward_e4m3``): Y8 [T, d] e4m3 and scales
+    [T, ceil(d / 128)] fp32, one for each 128 columns of a row."""
+    return _rmsnorm(X, gamma, eps, residual, R, stream, True, Y8, scales)
+
+
+def e4m3_expand(Y8, scales, dtype=torch.bfloat16, *, Y=None, stream=None) -> dict:
+    """Y8 * scale in bf16 or fp32 (``sbp_e4m3_expand``)."""
+    dev = Y8.device
+    _on_device(dev, Y8, scales, Y)
+    T, d = Y8.shape
+    if Y8.dtype != torch.float8_e4m3fn or scales.shape != (T, (d + 127) // 128) or scales.dtype != torch.float32:
+        raise ValueError("Y8 e4m3 [T, d]; scales fp32 [T, ceil(d / 128)]")
+    if Y is None:
+        with _scratch(stream):
+            Y = torch.empty((T, d), dtype=dtype, device=dev)
+    if Y.shape != (T, d):
+        raise ValueError("Y must be shaped like Y8")
+    _check(_lib.sbp_e4m3_expand(_p(Y8), _p(scales), T, d, _code(Y), _p(Y), _stream(stream)), "sbp_e4m3_expand")
+    return dict(Y=Y)
+
+
+def rmsnorm_backward(dY, R, gamma, eps, *, dR=None, dX=None, dgamma=None, accumulate=False, workspace=None, status=None,
+                     stream=None) -> dict:
+    """Gradients of ``rmsnorm`` at the stored sum R (``sbp_rmsnorm_backward``): dX (of X and of
+    the residual alike; dR, the residual stream's gradient, is added) and dgamma [d] fp32."""
+    dev = R.device
+    _on_device(dev, dY, R, gamma, dR, dX, dgamma, workspace, status)
+    T, d, dt = _norm_args(R, gamma, dY, dR, dX)
+    with _scratch(stream):
+        if workspace is None:
+            n = int(_lib.sbp_rmsnorm_backward_workspace_bytes(T, d, dt))
+            if n == 0:
+                raise SbpError(ERR_UNSUPPORTED, "sbp_rmsnorm_backward_workspace_bytes")
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        dX = torch.empty_like(R) if dX is None else dX
+        dgamma = torch.empty(d, dtype=torch.float32, device=dev) if dgamma is None else dgamma
+        st = torch.empty((), dtype=torch.int32, device=dev) if status is None else status
+    if dgamma.shape != (d,) or dgamma.dtype != torch.float32:
+        raise ValueError("dgamma must be float32 [d]")
+    _check(_lib.sbp_rmsnorm_backward(_p(dY), _p(R), _p(gamma), _p(dR), T, d, float(eps), dt, _p(dX), _p(dgamma),
+                                     int(bool(accumulate)), _p(workspace), workspace.numel(), _p(st),
+                                     _stream(stream)), "sbp_rmsnorm_backward")
+    return dict(dX=dX, dgamma=dgamma, status=st)
+
+
+def _rope_args(positions, T, rot_dim, sections, inv_freq):
+    if positions.dim() != 2 or positions.shape[1] != T or positions.dtype != torch.int32:
+        raise ValueError("positions must be int32 [n_axes, T]")
+    n = positions.shape[0]
+    sections = [rot_dim // 2] if sections is None else list(sections)
+    if len(sections) != n:
+        raise ValueError("one section for each axis of positions")
+    sec = (ctypes.c_int32 * n)(*sections)
+    freq = None
+    if inv_freq is not None:
+        if len(inv_freq) != rot_dim // 2:
+            raise ValueError("inv_freq must have rot_dim / 2 entries")
+        freq = (ctypes.c_double * len(inv_freq))(*[float(f) for f in inv_freq])
+    return n, sec, freq
+
+
+def rope_qkv(qkv, positions, H, Hkv, hd, *, sections=None, rot_dim=None, theta=10000.0, inv_freq=None,
+             interleaved=False, Q=None, K=None, V=None, stream=None) -> dict:
+    """Rotary positions on a token-major projection, given out head-major
+    (``sbp_rope_qkv_forward``).
+
+    qkv [T, >= (H + 2 Hkv) hd] bf16 (rows may be strided); positions int32 [n_axes, T];
+    sections: how many of the rot_dim / 2 pairs turn by each axis.  Returns Q [H, T, hd],
+    K and V [Hkv, T, hd]."""
+    dev = qkv.device
+    _on_device(dev, positions, Q, K, V)
+    if qkv.dim() != 2 or qkv.dtype != torch.bfloat16 or qkv.device != dev or qkv.shape[1] < (H + 2 * Hkv) * hd or (
+            qkv.numel() and qkv.stride(1) != 1):
+        raise ValueError("qkv must be bf16 [T, >= (H + 2 Hkv) hd] with contiguous rows")
+    T = qkv.shape[0]
+    rot_dim = hd if rot_dim is None else rot_dim
+    n, sec, freq = _rope_args(positions, T, rot_dim, sections, inv_freq)
+    with _scratch(stream):
+        Q = torch.empty((H, T, hd), dtype=torch.bfloat16, device=dev) if Q is None else Q
+        K = torch.empty((Hkv, T, hd), dtype=torch.bfloat16, device=dev) if K is None else K
+        V = torch.empty((Hkv, T, hd), dtype=torch.bfloat16, device=dev) if V is None else V
+    if Q.shape != (H, T, hd) or K.shape != (Hkv, T, hd) or V.shape != K.shape or any(
+            t.dtype != torch.bfloat16 for t in (Q, K, V)):
+        raise ValueError("Q bf16 [H, T, hd]; K, V bf16 [Hkv, T, hd]")
+    _check(_lib.sbp_rope_qkv_forward(_p(qkv), qkv.stride(0) if T > 1 else qkv.shape[1], _p(positions), n, sec, freq,
+                                     float(theta), rot_dim, int(bool(interleaved)), T, H, Hkv, hd, _p(Q), _p(K), _p(V),
+                                     _stream(stream)), "sbp_rope_qkv_forward")
+    return dict(Q=Q, K=K, V=V)
+
+
+def rope_qkv_backward(dQ, dK, dV, positions, *, sections=None, rot_dim=None, theta=10000.0, inv_freq=None,
+                      interleaved=False, dqkv=None, stream=None) -> dict:
+    """Gradient of ``rope_qkv`` (``sbp_rope_qkv_backward``): dQ [H, T, hd] bf16; dK, dV
+    [Hkv, T, hd], both bf16 or both fp32.  Returns dqkv [T, (H + 2 Hkv) hd] bf16."""
+    dev = dQ.device
+    _on_device(dev, dQ, dK, dV, positions)
+    if dQ.dim() != 3 or dK.dim() != 3 or dK.shape != dV.shape or dQ.shape[1:] != dK.shape[1:]:
+        raise ValueError("shapes: dQ [H, T, hd]; dK, dV [Hkv, T, hd]")
+    if dQ.dtype != torch.bfloat16 or dK.dtype != dV.dtype:
+        raise TypeError("dQ must be bf16; dK and dV both bf16 or both fp32")
+    H, T, hd = dQ.shape
+    Hkv = dK.shape[0]
+    rot_dim = hd if rot_dim is None else rot_dim
+    n, sec, freq = _rope_args(positions, T, rot_dim, sections, inv_freq)
+    if dqkv is None:
+        with _scratch(stream):
+            dqkv = torch.empty((T, (H + 2 * Hkv) * hd), dtype=torch.bfloat16, device=dev)
+    if dqkv.dim() != 2 or dqkv.shape[0] != T or dqkv.shape[1] < (H + 2 * Hkv) * hd or dqkv.device != dev or (
+            dqkv.dtype != torch.bfloat16) or (dqkv.numel() and dqkv.stride(1) != 1):
+        raise ValueError("dqkv must be bf16 [T, >= (H + 2 Hkv) hd] with contiguous rows")
+    _check(_lib.sbp_rope_qkv_backward(_p(dQ), _p(dK), _p(dV), _code(dK), _p(positions), n, sec, freq, float(theta),
+                                      rot_dim, int(bool(interleaved)), T, H, Hkv, hd, _p(dqkv),
+                                      dqkv.stride(0) if T > 1 else dqkv.shape[1], _stream(stream)),
+           "sbp_rope_qkv_backward")
+    return dict(dqkv=dqkv)

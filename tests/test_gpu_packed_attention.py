@@ -1,0 +1,295 @@
+"""GPU parity of the attention over packed documents against the float64 oracle.
+
+Tolerances are element by element, from the rounding the kernels do (u = 2^-8 is bf16's
+largest relative rounding error, half a step):
+  O     u |O| for its own rounding, u sum_j P |V| for P's, and 2^-11 of that sum for the fp32
+        scores and exponentials (score errors below 2^-12 at these sizes);
+  lse   2^-12 (the scores' fp32 sums) and 2^-20 of its value;
+  dQ, dK, dV  u of the value, and the oracle's bounds for P and dS in bf16 (see there).
+The backward is compared at the O and lse it was given.
+"""
+import numpy as np
+import pytest
+
+from oracle import sublayer as S
+from memory_efficient_exact_gb300 import inputs as I
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def sbp():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from memory_efficient_exact_gb300 import _build
+    _build.build_library()
+    from memory_efficient_exact_gb300 import sbp as mod
+    return mod
+
+
+def dev(x, dt=torch.bfloat16):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda().to(dt).contiguous()
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def make(H, Hkv, T, hd, seed, gain=1.0):
+    g = np.random.default_rng(seed)
+    r = lambda n, k=1.0: I.round_bf16((k * g.standard_normal((n, T, hd))).astype(np.float32))
+    return dict(Q=r(H, gain), K=r(Hkv), V=r(Hkv), dO=r(H))
+
+
+def options(H, lens, prefix, softcap, alibi):
+    cu = None if lens is None else np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    sl = None
+    if alibi:
+        sl = (2.0 ** (-8.0 * np.arange(1, H + 1) / H)).astype(np.float32)
+    kw = dict(softcap=softcap)
+    if cu is not None:
+        kw["cu_seqlens"] = dev(cu, torch.int32)
+    if prefix is not None:
+        kw["prefix_lens"] = dev(np.asarray(prefix, np.int32), torch.int32)
+    if sl is not None:
+        kw["slopes"] = dev(sl, torch.float32)
+    return cu, sl, kw
+
+
+def near(name, got, want, bound):
+    err = np.abs(got - want)
+    assert np.all(err <= bound), (name, float((err / bound).max()), np.argwhere(err > bound)[:4].tolist())
+
+
+def check(sbp, x, kw, cu, prefix, sl, scale):
+    H, T, hd = x["Q"].shape
+    see = S.visible(T, cu, prefix)
+    a = {k: dev(v) for k, v in x.items()}
+    f = sbp.attn_packed(a["Q"], a["K"], a["V"], scale, **kw)
+    b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], scale, **kw)
+    torch.cuda.synchronize()
+    sbp.check_status(f["status"])
+    sbp.check_status(b["status"])
+    cap = kw["softcap"]
+    want = S.attention(x["Q"], x["K"], x["V"], see, scale, cap, sl)
+    O, lse = host(f["O"]), host(f["lse"])
+    near("O", O, want["O"], U * np.abs(want["O"]) + (U + 2.0 ** -11) * want["size"])
+    some = see.any(axis=1)
+    assert np.all(np.isneginf(lse[:, ~some])) and np.all(O[:, ~some] == 0)
+    near("lse", lse[:, some], want["lse"][:, some], 2.0 ** -12 + 2.0 ** -20 * np.abs(want["lse"][:, some]))
+    g = S.attention_backward(x["Q"], x["K"], x["V"], O, x["dO"], lse, see, scale, cap, sl)
+    for k in "QKV":
+        near("d" + k, host(b["d" + k]), g["d" + k], U * np.abs(g["d" + k]) + g["b" + k])
+    seen = see.any(axis=0)
+    assert np.all(host(b["dQ"])[:, ~some] == 0)
+    assert np.all(host(b["dK"])[:, ~seen] == 0) and np.all(host(b["dV"])[:, ~seen] == 0)
+
+
+# one token; lengths around the 64-key, 128-row and 256-row tiles; one document
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 400])
+def test_one_document(sbp, T):
+    x = make(2, 1, T, 128, seed=T)
+    cu, sl, kw = options(2, None, None, 0.0, False)
+    check(sbp, x, kw, cu, None, sl, 128 ** -0.5)
+
+
+# documents that begin and end inside tiles, empty ones first, between and last, single
+# tokens, padding behind them, grouped heads
+@pytest.mark.parametrize("T,lens", [(300, [100, 0, 1, 150, 49]), (520, [0, 130, 126, 1, 1, 200]), (384, [128, 128, 128]),
+                                    (300, [300, 0]), (257, [1]), (260, [0]), (700, [5] * 100), (513, [256, 257])])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (6, 2)])
+def test_documents(sbp, T, lens, H, Hkv):
+    x = make(H, Hkv, T, 64, seed=T + H)
+    cu, sl, kw = options(H, lens, None, 0.0, False)
+    check(sbp, x, kw, cu, None, sl, 0.125)
+
+
+# a prefix of none, part, all and more than its document; with and without documents
+@pytest.mark.parametrize("T,lens,prefix", [(300, None, [140]), (300, [100, 120, 60], [0, 70, 500]), (200, None, [0]),
+                                           (640, [600, 40], [600, 1])])
+def test_prefix(sbp, T, lens, prefix):
+    x = make(2, 1, T, 128, seed=T)
+    cu, sl, kw = options(2, lens, prefix, 0.0, False)
+    check(sbp, x, kw, cu, prefix, sl, 128 ** -0.5)
+
+
+# caps that bind (scores of some 4 x the cap) and hardly bind; distance bias; both
+@pytest.mark.parametrize("softcap,alibi,gain", [(50.0, False, 4.0), (2.0, False, 8.0), (0.0, True, 1.0), (15.0, True, 4.0)])
+@pytest.mark.parametrize("prefix", [None, [20, 130, 0]])
+def test_cap_and_bias(sbp, softcap, alibi, gain, prefix):
+    x = make(4, 2, 330, 128, seed=9, gain=gain)
+    cu, sl, kw = options(4, [90, 140, 80], prefix, softcap, alibi)
+    check(sbp, x, kw, cu, prefix, sl, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("hd", [8, 16, 40, 64, 72, 80, 96, 120, 128])
+def test_head_widths(sbp, hd):
+    x = make(3, 1, 200, hd, seed=hd)
+    cu, sl, kw = options(3, [120, 70], None, 0.0, False)
+    check(sbp, x, kw, cu, None, sl, hd ** -0.5)
+
+
+def test_more_units_than_pairs(sbp):
+    # 48 heads of 3 units: every barrier crosses unit boundaries
+    x = make(48, 8, 600, 128, seed=1)
+    cu, sl, kw = options(48, [300, 290], None, 0.0, False)
+    check(sbp, x, kw, cu, None, sl, 128 ** -0.5)
+
+
+def test_running_maximum_is_raised(sbp):
+    # scores that grow along the keys by far more than the 2^8 the maximum may lag behind
+    x = make(1, 1, 600, 128, seed=2)
+    x["K"] = I.round_bf16((x["K"] * np.linspace(0.05, 6.0, 600)[None, :, None]).astype(np.float32))
+    cu, sl, kw = options(1, None, None, 0.0, False)
+    check(sbp, x, kw, cu, None, sl, 0.25)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_padding_may_hold_anything(sbp, bad):
+    H, Hkv, T, n = 4, 2, 400, 333
+    x = make(H, Hkv, T, 64, seed=3)
+    a = {k: dev(v) for k, v in x.items()}
+    cu = dev(np.array([0, 200, n], np.int32), torch.int32)
+
+    def run():
+        f = sbp.attn_packed(a["Q"], a["K"], a["V"], 0.125, cu_seqlens=cu, softcap=20.0)
+        O, lse = f["O"].clone(), f["lse"].clone()
+        O[:, n:] = bad
+        lse[:, n:] = bad
+        b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], O, a["dO"], lse, 0.125, cu_seqlens=cu, softcap=20.0)
+        return [f["O"], f["lse"], b["dQ"], b["dK"], b["dV"]]
+
+    clean = run()
+    for k in a:
+        a[k][:, n:] = bad
+    dirty = run()
+    torch.cuda.synchronize()
+    for c, d in zip(clean, dirty):
+        assert torch.equal(c, d)
+    assert torch.all(dirty[1][:, n:] == -float("inf")) and all(torch.all(t[:, n:] == 0) for t in dirty[:1] + dirty[2:])
+
+
+def test_infinite_keys_of_another_document_stay_masked(sbp):
+    # an infinite K makes infinite scores for other documents' queries in the same tile; they
+    # are masked before the exponential (V, Q and dO are summed over, so they must be finite)
+    x = make(1, 1, 100, 64, seed=4)
+    a = {k: dev(v) for k, v in x.items()}
+    cu = dev(np.array([0, 60, 100], np.int32), torch.int32)
+    want = sbp.attn_packed(a["Q"], a["K"], a["V"], 0.125, cu_seqlens=cu)["O"][:, :60].clone()
+    a["K"][:, 80] = float("inf")
+    got = sbp.attn_packed(a["Q"], a["K"], a["V"], 0.125, cu_seqlens=cu)["O"][:, :60]
+    assert torch.equal(want, got)
+
+
+def _call(sbp, a, out, **kw):
+    f = sbp.attn_packed(a["Q"], a["K"], a["V"], 0.125, O=out["O"], lse=out["lse"], **kw)
+    b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], 0.125, dQ=out["dQ"], dK=out["dK"],
+                                 dV=out["dV"], **kw)
+    return f["status"], b["status"]
+
+
+def _outputs(a):
+    n = lambda t: torch.full_like(t, 7.0)
+    return dict(O=n(a["Q"]), lse=torch.full(a["Q"].shape[:2], 7.0, device="cuda"), dQ=n(a["Q"]), dK=n(a["K"]), dV=n(a["V"]))
+
+
+def test_same_bits_on_a_stream_and_in_graphs(sbp):
+    H, Hkv, T = 6, 2, 500
+    a = {k: dev(v) for k, v in make(H, Hkv, T, 64, seed=5).items()}
+    cu = dev(np.array([0, 210, 460], np.int32), torch.int32)
+    ref = _outputs(a)
+    _call(sbp, a, ref, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = _outputs(a)
+    side.wait_stream(torch.cuda.current_stream())
+    _call(sbp, a, got, cu_seqlens=cu, stream=side)
+    side.synchronize()
+    assert all(torch.equal(ref[k], got[k]) for k in ref)
+
+    # two captured graphs that share a workspace; the second follows a changed table
+    ws = torch.empty(sbp.attn_packed_workspace_bytes(H, Hkv, T, 64), dtype=torch.uint8, device="cuda")
+    outs, graphs = [_outputs(a), _outputs(a)], []
+    tables = [cu.clone(), cu.clone()]
+    for o, c in zip(outs, tables):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            st = _call(sbp, a, o, cu_seqlens=c, workspace=ws)
+        graphs.append((g, st))
+    tables[1].copy_(dev(np.array([0, 64, 500], np.int32), torch.int32))
+    other = _outputs(a)
+    _call(sbp, a, other, cu_seqlens=tables[1])
+    for _ in range(2):
+        for g, _st in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for want, got in ((ref, outs[0]), (other, outs[1])):
+        assert all(torch.equal(want[k], got[k]) for k in want)
+    for _, st in graphs:
+        for s in st:
+            sbp.check_status(s)
+
+
+def test_calls_on_two_streams_at_once(sbp):
+    a = {k: dev(v) for k, v in make(16, 4, 900, 128, seed=6).items()}
+    ref = _outputs(a)
+    _call(sbp, a, ref)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [_outputs(a) for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for s, o in zip(streams, outs):
+            _call(sbp, a, o, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(ref[k], o[k]) for k in ref)
+
+
+@pytest.mark.parametrize("cu", [[1, 50, 100], [0, 60, 50], [0, 50, 101], [0, -3, 100], [0, 1 << 30, 100]])
+def test_bad_tables_set_the_status(sbp, cu):
+    a = {k: dev(v) for k, v in make(2, 1, 100, 64, seed=7).items()}
+    for st in _call(sbp, a, _outputs(a), cu_seqlens=dev(np.array(cu, np.int32), torch.int32)):
+        torch.cuda.synchronize()
+        with pytest.raises(sbp.SbpError) as e:
+            sbp.check_status(st)
+        assert e.value.code == sbp.ERR_SEQLENS
+    good = dev(np.array([0, 50, 100], np.int32), torch.int32)
+    for st in _call(sbp, a, _outputs(a), cu_seqlens=good, prefix_lens=dev(np.array([3, -1], np.int32), torch.int32)):
+        torch.cuda.synchronize()
+        assert int(st) == sbp.ERR_SEQLENS
+    for st in _call(sbp, a, _outputs(a), cu_seqlens=good):
+        sbp.check_status(st)
+
+
+def test_python_refusals(sbp):
+    a = {k: dev(v) for k, v in make(2, 1, 64, 64, seed=8).items()}
+    Q, K, V = a["Q"], a["K"], a["V"]
+    with pytest.raises(ValueError):
+        sbp.attn_packed(Q.transpose(0, 1), K, V, 0.1)
+    with pytest.raises(ValueError):
+        sbp.attn_packed(Q, K, V[:, :32].contiguous(), 0.1)
+    with pytest.raises(TypeError):
+        sbp.attn_packed(Q.float(), K.float(), V.float(), 0.1)
+    with pytest.raises(ValueError):
+        sbp.attn_packed(Q, K, V, 0.1, cu_seqlens=torch.tensor([0, 64], device="cuda"))
+    with pytest.raises(ValueError):
+        sbp.attn_packed(Q, K, V, 0.1, slopes=torch.zeros(1, device="cuda"))
+    with pytest.raises(ValueError):
+        sbp.attn_packed(Q.cpu(), K, V, 0.1)
+    with pytest.raises(sbp.SbpError):
+        sbp.attn_packed(Q, K, V, 0.0)
+    f = sbp.attn_packed(Q, K, V, 0.1)
+    with pytest.raises(ValueError):
+        sbp.attn_packed_backward(Q, K, V, f["O"], a["dO"], f["lse"].double(), 0.1)
+
+
+def test_no_tokens(sbp):
+    e = lambda n: torch.empty((n, 0, 64), dtype=torch.bfloat16, device="cuda")
+    f = sbp.attn_packed(e(4), e(2), e(2), 0.1)
+    b = sbp.attn_packed_backward(e(4), e(2), e(2), f["O"], e(4), f["lse"], 0.1)
+    sbp.check_status(f["status"])
+    sbp.check_status(b["status"])
+    assert f["O"].shape == (4, 0, 64) and b["dK"].shape == (2, 0, 64)
