@@ -22,24 +22,33 @@ namespace {
 constexpr int MAXW = 32;            // warps of a block
 constexpr int64_t MAX_D = 16384;    // 32 warps x 32 lanes x 2 vectors x 8 elements
 
-// Eight elements of a row.
+// Eight elements of a row: as they lie in memory (16 or 32 bytes) and in fp32.
 struct F8 { float v[8]; };
-__device__ __forceinline__ F8 load8(const __nv_bfloat16* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  F8 f;
+template <typename E> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ F8 f() const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    F8 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    f.v[2 * i] = x.x;
-    f.v[2 * i + 1] = x.y;
+    for (int i = 0; i < 4; ++i) {
+      f.v[2 * i] = __uint_as_float(w[i] << 16);
+      f.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    return f;
   }
-  return f;
-}
-__device__ __forceinline__ F8 load8(const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
+};
+template <> struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ F8 f() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& f) {
   uint32_t w[4];
 #pragma unroll
@@ -60,24 +69,31 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the wpr warps of this warp's row.  Every warp of the block calls it; the slots of
-// two calls in a row are different (flip), so one barrier a call is enough.
-__device__ __forceinline__ float row_sum(float v, float (*red)[MAXW], int flip, int wpr) {
-  v = warp_sum(v);
+// Sums of two values over the lanes of this row: lpr lanes of one warp, or wpr whole warps.
+// Every warp of the block calls it; two calls in a row use different slots (flip), so one
+// barrier a call is enough.
+__device__ __forceinline__ float2 row_sums(float2 v, float2 (*red)[MAXW], int flip, int lpr, int wpr) {
+  for (int o = lpr / 2; o; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
   if (wpr == 1) return v;
   const int warp = threadIdx.x / 32;
   if (threadIdx.x % 32 == 0) red[flip][warp] = v;
   __syncthreads();
   const int w0 = warp / wpr * wpr;
-  float s = 0.f;
-  for (int i = 0; i < wpr; ++i) s += red[flip][w0 + i];
+  float2 s = make_float2(0.f, 0.f);
+  for (int i = 0; i < wpr; ++i) {
+    s.x += red[flip][w0 + i].x;
+    s.y += red[flip][w0 + i].y;
+  }
   return s;
 }
 
 struct FwdP {
   const void *X, *res, *gamma;
   int64_t T;
-  int d, nvec, wpr, rpb;   // 8-element vectors and warps of a row, rows of a block
+  int d, nvec, lpr, wpr, rpb;   // 8-element vectors, lanes and warps of a row, rows of a block
   float eps;
   void *R, *Y;
   float* scales;   // 8-bit output: [T, nblk]
@@ -85,78 +101,99 @@ struct FwdP {
 };
 
 // E: bf16 or fp32.  NV vectors a thread.  Q8: Y in e4m3 with a scale for each 128 columns,
-// the 128 columns of a block being 16 neighbouring lanes of one warp and vector.
-template <typename E, int NV, bool Q8>
-__global__ void __launch_bounds__(1024) k_rmsnorm_fwd(const FwdP p) {
-  __shared__ float red[2][MAXW];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int sub = warp / p.wpr;                                  // row of the block
-  const int t0 = (warp - sub * p.wpr) * 32 + lane;               // thread of the row
-  const int64_t row = (int64_t)blockIdx.x * p.rpb + sub;
-  const bool live = row < p.T;
-  const int step = 32 * p.wpr;
-  const int64_t at = row * p.d;
-  F8 r[NV];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = t0 + i * step;
-    if (live && v < p.nvec) {
-      r[i] = load8(static_cast<const E*>(p.X) + at + 8 * v);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[i].v[k] = 0.f;
-    }
-  }
-  if (p.res) {
+// the 128 columns of a block being 16 neighbouring lanes (or all the row's, if it is
+// narrower) of one warp and vector.
+// Blocks walk the rows; the next row's loads are issued before this row's sum, so that a block
+// always has a row in flight, and the grid is what the SMs hold at once (T = 16384, d = 4096:
+// 79 us, 6840 GB/s; with a third more blocks than that 91 us).
+template <typename E, int NV, bool Q8, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_fwd(const FwdP p) {
+  __shared__ float2 red[2][MAXW];
+  const int step = p.lpr * p.wpr;               // threads of a row
+  const int sub = threadIdx.x / step;           // row of the block
+  const int t0 = threadIdx.x - sub * step;      // thread of the row
+  const float inv_d = 1.f / (float)p.d;
+  Raw<E> x[NV], q[NV], g[NV];
+  auto fetch = [&](int64_t row) {
+    const int nvec = row < p.T ? p.nvec : 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t0 + i * step;
-      if (live && v < p.nvec) {
-        const F8 q = load8(static_cast<const E*>(p.res) + at + 8 * v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) r[i].v[k] += q.v[k];
-        if (p.R) store8(static_cast<E*>(p.R) + at + 8 * v, r[i]);
+      x[i].zero();
+      q[i].zero();
+      if (v < nvec) {
+        const int64_t at = row * p.d + 8 * v;
+        x[i].load(static_cast<const E*>(p.X) + at);
+        if (p.res) q[i].load(static_cast<const E*>(p.res) + at);
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(r[i].v[k], r[i].v[k], ss);
-  ss = row_sum(ss, red, 0, p.wpr);
-  const float rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
+  };
+  fetch((int64_t)blockIdx.x * p.rpb + sub);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = t0 + i * step;
-    const bool in = live && v < p.nvec;
-    if (in) {
-      const F8 g = load8(static_cast<const E*>(p.gamma) + 8 * v);
+    if (v < p.nvec) g[i].load(static_cast<const E*>(p.gamma) + 8 * v);
+    else g[i].zero();
+  }
+  int flip = 0;
+  const int64_t stride = (int64_t)gridDim.x * p.rpb;
+  for (int64_t r0 = (int64_t)blockIdx.x * p.rpb; r0 < p.T; r0 += stride) {
+    const int64_t row = r0 + sub;
+    const int nvec = row < p.T ? p.nvec : 0;
+    const int64_t at = row * p.d;
+    F8 r[NV];
+    float ss = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) r[i].v[k] = r[i].v[k] * rstd * g.v[k];
+    for (int i = 0; i < NV; ++i) {
+      r[i] = x[i].f();
+      const F8 a = q[i].f();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        r[i].v[k] += a.v[k];
+        ss = fmaf(r[i].v[k], r[i].v[k], ss);
+      }
     }
-    if constexpr (!Q8) {
-      if (in) store8(static_cast<E*>(p.Y) + at + 8 * v, r[i]);
-    } else {
-      float a = 0.f;
+    fetch(row + stride);
+    if (p.R) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(r[i].v[k]));
+      for (int i = 0; i < NV; ++i) {
+        const int v = t0 + i * step;
+        if (v < nvec) store8(static_cast<E*>(p.R) + at + 8 * v, r[i]);
+      }
+    }
+    const float rstd = rsqrtf(row_sums(make_float2(ss, 0.f), red, flip, p.lpr, p.wpr).x * inv_d + p.eps);
+    flip ^= 1;
 #pragma unroll
-      for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      // 448: e4m3's largest value.  A block of zeros keeps the scale 1.
-      const float s = a > 0.f ? a / 448.f : 1.f;
-      if (in) {
-        uint32_t w[2];
+    for (int i = 0; i < NV; ++i) {
+      const int v = t0 + i * step;
+      const F8 w = g[i].f();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(r[i].v[4 * k] / s, r[i].v[4 * k + 1] / s),
-                                                       __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(r[i].v[4 * k + 2] / s, r[i].v[4 * k + 3] / s),
-                                                       __NV_SATFINITE, __NV_E4M3);
-          w[k] = lo | (hi << 16);
+      for (int k = 0; k < 8; ++k) r[i].v[k] = r[i].v[k] * rstd * w.v[k];
+      if constexpr (!Q8) {
+        if (v < nvec) store8(static_cast<E*>(p.Y) + at + 8 * v, r[i]);
+      } else {
+        float a = 0.f;
+        if (v < nvec) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(r[i].v[k]));
         }
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.Y) + at + 8 * v) = make_uint2(w[0], w[1]);
-        if (lane % 16 == 0) p.scales[row * p.nblk + v / 16] = s;
+        for (int o = min(8, p.lpr / 2); o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        // 448: e4m3's largest value.  A block of zeros keeps the scale 1.  One division a
+        // block and products instead of a division an element (132 us against 87).
+        const float s = a > 0.f ? a / 448.f : 1.f, inv = 1.f / s;
+        if (v < nvec) {
+          uint32_t w2[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(r[i].v[4 * k] * inv, r[i].v[4 * k + 1] * inv),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(r[i].v[4 * k + 2] * inv, r[i].v[4 * k + 3] * inv),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            w2[k] = lo | (hi << 16);
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.Y) + at + 8 * v) = make_uint2(w2[0], w2[1]);
+          if (v % 16 == 0) p.scales[row * p.nblk + v / 16] = s;
+        }
       }
     }
   }
@@ -165,87 +202,126 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_fwd(const FwdP p) {
 struct BwdP {
   const void *dY, *R, *gamma, *dR;
   int64_t T;
-  int d, nvec, wpr, rpb;
+  int d, nvec, lpr, wpr, rpb;
   float eps;
   void* dX;
-  float* part;   // [gridDim.x * rpb, d]: each row group's share of dgamma
+  float* part;   // [gridDim.x, d]: each block's share of dgamma
 };
 
-// A block walks rows blockIdx.x * rpb + k gridDim.x * rpb; each row group keeps its share of
-// dgamma in registers and leaves it in `part` (summed in a fixed order by k_dgamma).
-// MAXT: the most threads of a block, which sets the registers a thread may have.
-template <typename E, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_rmsnorm_bwd(const BwdP p) {
-  __shared__ float red[4][MAXW];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int sub = warp / p.wpr;
-  const int t0 = (warp - sub * p.wpr) * 32 + lane;
-  const int step = 32 * p.wpr;
+// A block walks rows blockIdx.x * rpb + k gridDim.x * rpb, keeps its share of dgamma in
+// registers and leaves it in `part` (summed in a fixed order by k_dgamma).  The
+// next row's loads are issued before this row's sums, which hide them: without that a block
+// waited for memory and for its barriers in turn (T = 16384, d = 4096: 235 us, now 91).
+// MAXT: the most threads of a block, MINB: how many blocks of it an SM should hold, which set
+// the registers a thread may have.
+template <typename E, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd(const BwdP p) {
+  constexpr bool AHEAD = MAXT <= 512;   // a block of 1024 threads has no registers for it
+  __shared__ float2 red[2][MAXW];
+  const int step = p.lpr * p.wpr;               // threads of a row
+  const int sub = threadIdx.x / step;           // row of the block
+  const int t0 = threadIdx.x - sub * step;      // thread of the row
+  const float inv_d = 1.f / (float)p.d;
   F8 dg[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) dg[i].v[k] = 0.f;
-  int flip = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * p.rpb; r0 < p.T; r0 += (int64_t)gridDim.x * p.rpb) {
-    const int64_t row = r0 + sub;
-    const bool live = row < p.T;
-    const int64_t at = row * p.d;
-    F8 r[NV], y[NV];
-    float ss = 0.f, gr = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = t0 + i * step;
-      if (live && v < p.nvec) {
-        r[i] = load8(static_cast<const E*>(p.R) + at + 8 * v);
-        y[i] = load8(static_cast<const E*>(p.dY) + at + 8 * v);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) r[i].v[k] = y[i].v[k] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = t0 + i * step;
-      F8 g;
-      if (v < p.nvec) g = load8(static_cast<const E*>(p.gamma) + 8 * v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        ss = fmaf(r[i].v[k], r[i].v[k], ss);
-        if (v < p.nvec) gr = fmaf(y[i].v[k] * g.v[k], r[i].v[k], gr);
-      }
-    }
-    ss = row_sum(ss, red, flip, p.wpr);
-    gr = row_sum(gr, red, flip + 1, p.wpr);
-    flip ^= 2;
-    const float rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
-    const float c = rstd * rstd * (gr / (float)p.d);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = t0 + i * step;
-      if (live && v < p.nvec) {
-        const F8 g = load8(static_cast<const E*>(p.gamma) + 8 * v);
-        F8 o;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          dg[i].v[k] = fmaf(y[i].v[k], r[i].v[k] * rstd, dg[i].v[k]);
-          o.v[k] = rstd * (y[i].v[k] * g.v[k] - r[i].v[k] * c);
-        }
-        if (p.dR) {
-          const F8 q = load8(static_cast<const E*>(p.dR) + at + 8 * v);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o.v[k] += q.v[k];
-        }
-        store8(static_cast<E*>(p.dX) + at + 8 * v, o);
-      }
-    }
-  }
-  float* part = p.part + ((int64_t)blockIdx.x * p.rpb + sub) * p.d;
+  Raw<E> g[NV], r[NV], y[NV], q[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = t0 + i * step;
-    if (v < p.nvec) store8(part + 8 * v, dg[i]);
+    if (v < p.nvec) g[i].load(static_cast<const E*>(p.gamma) + 8 * v);
+    else g[i].zero();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dg[i].v[k] = 0.f;
   }
+  auto fetch = [&](int64_t row) {
+    const int nvec = row < p.T ? p.nvec : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t0 + i * step;
+      r[i].zero();
+      y[i].zero();
+      q[i].zero();
+      if (v < nvec) {
+        const int64_t at = row * p.d + 8 * v;
+        r[i].load(static_cast<const E*>(p.R) + at);
+        y[i].load(static_cast<const E*>(p.dY) + at);
+        if (p.dR) q[i].load(static_cast<const E*>(p.dR) + at);
+      }
+    }
+  };
+  int flip = 0;
+  const int64_t stride = (int64_t)gridDim.x * p.rpb;
+  if (AHEAD) fetch((int64_t)blockIdx.x * p.rpb + sub);
+  for (int64_t r0 = (int64_t)blockIdx.x * p.rpb; r0 < p.T; r0 += stride) {
+    const int64_t row = r0 + sub;
+    const int nvec = row < p.T ? p.nvec : 0;
+    if (!AHEAD) fetch(row);
+    Raw<E> cr[NV], cy[NV], cq[NV];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      cr[i] = r[i];
+      cy[i] = y[i];
+      cq[i] = q[i];
+      const F8 a = cr[i].f(), b = cy[i].f(), c = g[i].f();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s.x = fmaf(a.v[k], a.v[k], s.x);
+        s.y = fmaf(b.v[k] * c.v[k], a.v[k], s.y);
+      }
+    }
+    if (AHEAD) fetch(row + stride);
+    s = row_sums(s, red, flip, p.lpr, p.wpr);
+    flip ^= 1;
+    const float rstd = rsqrtf(s.x * inv_d + p.eps);
+    const float c = rstd * rstd * (s.y * inv_d);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t0 + i * step;
+      const F8 a = cr[i].f(), b = cy[i].f(), e = g[i].f(), f = cq[i].f();
+      F8 o;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dg[i].v[k] = fmaf(b.v[k], a.v[k] * rstd, dg[i].v[k]);
+        o.v[k] = fmaf(rstd, b.v[k] * e.v[k] - a.v[k] * c, f.v[k]);
+      }
+      if (v < nvec) store8(static_cast<E*>(p.dX) + row * p.d + 8 * v, o);
+    }
+  }
+  // the block's row groups together, in their order: rows that share a warp by shuffles, then
+  // one group after the other through shared memory (groups are 256 threads at most, so
+  // 256 * NV * 8 columns)
+  float* part = p.part + (int64_t)blockIdx.x * p.d;
+  if (p.rpb == 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t0 + i * step;
+      if (v < p.nvec) store8(part + 8 * v, dg[i]);
+    }
+    return;
+  }
+  __shared__ float acc[MAXT <= 256 ? 256 * NV * 8 : 8];
+  for (int o = p.lpr; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dg[i].v[k] += __shfl_xor_sync(0xffffffffu, dg[i].v[k], o);
+  const bool shared_warp = p.lpr < 32;
+  const int group = shared_warp ? threadIdx.x / 32 : sub, groups = shared_warp ? blockDim.x / 32 : p.rpb;
+  const bool mine = !shared_warp || (int)(threadIdx.x % 32) < p.lpr;
+  for (int n = 0; n < groups; ++n) {
+    if (group == n && mine) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = t0 + i * step;
+        if (v < p.nvec) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[8 * v + k] = n ? acc[8 * v + k] + dg[i].v[k] : dg[i].v[k];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < p.d; i += blockDim.x) part[i] = acc[i];
 }
 
 // dgamma[c] (+)= sum over the n parts, 32 columns a block, 32 threads a column.
@@ -284,17 +360,26 @@ __global__ void __launch_bounds__(256) k_e4m3_expand(const uint8_t* __restrict__
   store8(out + i, f);
 }
 
-// Rows in a block: NV vectors a thread, whole warps a row, up to 8 warps' worth of rows
-// together.
-struct Shape { int nv, wpr, rpb, threads; };
+// Up to 256 elements a row: one vector a thread, a power of two lanes a row, several rows a
+// warp.  Else two vectors a thread (twice the loads in flight of one: T = 16384, d = 4096
+// forward 85 us against 89) and whole warps a row; up to 256 threads' worth of rows a block.
+struct Shape { int nv, lpr, wpr, rpb, threads; };
 Shape shape_of(int64_t d) {
   const int nvec = (int)(d / 8);
   Shape s;
   s.nv = nvec <= 32 ? 1 : 2;
-  s.wpr = (nvec + 32 * s.nv - 1) / (32 * s.nv);
-  s.rpb = std::max(1, 8 / s.wpr);
-  s.threads = 32 * s.wpr * s.rpb;
+  s.lpr = 32;
+  while (s.lpr > 1 && s.lpr / 2 >= nvec) s.lpr /= 2;
+  s.wpr = std::max(1, (nvec + 32 * s.nv - 1) / (32 * s.nv));
+  s.rpb = std::max(1, 256 / (s.lpr * s.wpr));
+  s.threads = s.lpr * s.wpr * s.rpb;
   return s;
+}
+// Blocks of a launch: what the SMs hold at once of a kernel built for `minb` blocks of `maxt`
+// threads, and no more than there are rows.
+int64_t blocks_of(int64_t T, const Shape& s, int maxt, int minb) {
+  return std::max<int64_t>(1, std::min<int64_t>((T + s.rpb - 1) / s.rpb,
+                                                (int64_t)num_sms() * std::max(1, maxt * minb / s.threads)));
 }
 
 int norm_check(int64_t T, int64_t d, int dtype) {
@@ -303,12 +388,17 @@ int norm_check(int64_t T, int64_t d, int dtype) {
   return SBP_OK;
 }
 
+template <typename E, int NV, bool Q8, int MAXT, int MINB>
+cudaError_t launch_fwd1(const FwdP& p, const Shape& s, cudaStream_t st) {
+  k_rmsnorm_fwd<E, NV, Q8, MAXT, MINB><<<(unsigned)blocks_of(p.T, s, MAXT, MINB), s.threads, 0, st>>>(p);
+  return cudaGetLastError();
+}
 template <typename E, bool Q8>
 cudaError_t launch_fwd(const FwdP& p, const Shape& s, cudaStream_t st) {
-  const unsigned grid = (unsigned)((p.T + s.rpb - 1) / s.rpb);
-  if (s.nv == 1) k_rmsnorm_fwd<E, 1, Q8><<<grid, s.threads, 0, st>>>(p);
-  else k_rmsnorm_fwd<E, 2, Q8><<<grid, s.threads, 0, st>>>(p);
-  return cudaGetLastError();
+  if (s.nv == 1) return launch_fwd1<E, 1, Q8, 256, 4>(p, s, st);
+  if (s.threads <= 256) return launch_fwd1<E, 2, Q8, 256, 3>(p, s, st);
+  if (s.threads <= 512) return launch_fwd1<E, 2, Q8, 512, 2>(p, s, st);
+  return launch_fwd1<E, 2, Q8, 1024, 1>(p, s, st);
 }
 
 int run_fwd(const void* X, const void* res, const void* gamma, int64_t T, int64_t d, float eps, int dtype, void* R,
@@ -323,7 +413,7 @@ int run_fwd(const void* X, const void* res, const void* gamma, int64_t T, int64_
   set_launch_count(0);
   if (T == 0) return SBP_OK;
   const Shape sh = shape_of(d);
-  FwdP p{X, res, gamma, T, (int)d, (int)(d / 8), sh.wpr, sh.rpb, eps, R, Y, scales, (int)((d + 127) / 128)};
+  FwdP p{X, res, gamma, T, (int)d, (int)(d / 8), sh.lpr, sh.wpr, sh.rpb, eps, R, Y, scales, (int)((d + 127) / 128)};
   cudaError_t e;
   if (dtype == SBP_BF16)
     e = q8 ? launch_fwd<__nv_bfloat16, true>(p, sh, s) : launch_fwd<__nv_bfloat16, false>(p, sh, s);
@@ -334,10 +424,14 @@ int run_fwd(const void* X, const void* res, const void* gamma, int64_t T, int64_
   return SBP_OK;
 }
 
-// Blocks of the backward: all that fit at once, so that each walks the same number of rows.
-int64_t bwd_blocks(int64_t T, const Shape& s) {
-  const int per_sm = std::max(1, std::min(4, 1024 / s.threads));
-  return std::max<int64_t>(1, std::min<int64_t>((T + s.rpb - 1) / s.rpb, (int64_t)num_sms() * per_sm));
+// The backward's builds: threads and blocks an SM, which set its registers (128 a thread;
+// 64 at more than 512 threads, which leaves none for the loads ahead).  At d = 5120, one block of
+// 320 threads with 128 registers takes 75 us, two with 96 and their spills 85 (T = 8190).
+void bwd_build(const Shape& s, int* maxt, int* minb) {
+  if (s.nv == 1) { *maxt = 256; *minb = 3; }
+  else if (s.threads <= 256) { *maxt = 256; *minb = 2; }
+  else if (s.threads <= 512) { *maxt = 512; *minb = 1; }
+  else { *maxt = 1024; *minb = 1; }
 }
 
 struct BwdLayout {
@@ -349,9 +443,11 @@ bool bwd_layout(int64_t T, int64_t d, int dtype, BwdLayout* L) {
   if (norm_check(T, d, dtype) != SBP_OK) return false;
   BwdLayout l;
   const Shape s = shape_of(d);
-  l.blocks = bwd_blocks(T, s);
+  int maxt, minb;
+  bwd_build(s, &maxt, &minb);
+  l.blocks = blocks_of(T, s, maxt, minb);
   size_t o = 0;
-  l.off_part = take_region(o, (size_t)l.blocks * s.rpb * d * sizeof(float), l.guards);
+  l.off_part = take_region(o, (size_t)l.blocks * d * sizeof(float), l.guards);
   l.total = o;
   *L = l;
   return true;
@@ -359,9 +455,10 @@ bool bwd_layout(int64_t T, int64_t d, int dtype, BwdLayout* L) {
 
 template <typename E>
 cudaError_t launch_bwd(const BwdP& p, const Shape& s, unsigned grid, cudaStream_t st) {
-  if (s.nv == 1) k_rmsnorm_bwd<E, 1, 512><<<grid, s.threads, 0, st>>>(p);
-  else if (s.threads <= 512) k_rmsnorm_bwd<E, 2, 512><<<grid, s.threads, 0, st>>>(p);
-  else k_rmsnorm_bwd<E, 2, 1024><<<grid, s.threads, 0, st>>>(p);
+  if (s.nv == 1) k_rmsnorm_bwd<E, 1, 256, 3><<<grid, s.threads, 0, st>>>(p);
+  else if (s.threads <= 256) k_rmsnorm_bwd<E, 2, 256, 2><<<grid, s.threads, 0, st>>>(p);
+  else if (s.threads <= 512) k_rmsnorm_bwd<E, 2, 512, 1><<<grid, s.threads, 0, st>>>(p);
+  else k_rmsnorm_bwd<E, 2, 1024, 1><<<grid, s.threads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -438,12 +535,11 @@ int sbp_rmsnorm_backward(const void* dY, const void* R, const void* gamma, const
   if (st != SBP_OK) return st;
   const Shape sh = shape_of(d);
   float* part = reinterpret_cast<float*>(w + L.off_part);
-  BwdP p{dY, R, gamma, dR, T, (int)d, (int)(d / 8), sh.wpr, sh.rpb, eps, dX, part};
+  BwdP p{dY, R, gamma, dR, T, (int)d, (int)(d / 8), sh.lpr, sh.wpr, sh.rpb, eps, dX, part};
   const cudaError_t e = dtype == SBP_BF16 ? launch_bwd<__nv_bfloat16>(p, sh, (unsigned)L.blocks, s)
                                           : launch_bwd<float>(p, sh, (unsigned)L.blocks, s);
   if (e != cudaSuccess) return SBP_ERR_CUDA;
-  k_dgamma<<<(unsigned)((d + 31) / 32), 1024, 0, s>>>(part, (int)(L.blocks * sh.rpb), (int)d, accumulate ? 1 : 0,
-                                                      dgamma);
+  k_dgamma<<<(unsigned)((d + 31) / 32), 1024, 0, s>>>(part, (int)L.blocks, (int)d, accumulate ? 1 : 0, dgamma);
   if (cudaGetLastError() != cudaSuccess) return SBP_ERR_CUDA;
   st = workspace_guards(w, L.guards, 1, dev_status, s, &launches);
   if (st == SBP_OK) set_launch_count(launches);

@@ -8,14 +8,16 @@
 // the top 32 bits of the product, in half turns.
 //
 // Bound by device memory: every element is read and written once, 16 bytes at a time.  A
-// block takes TB tokens: their cosines and sines once into shared memory (all heads use the
-// same), then all heads; the lanes run over a head's vectors, then tokens, so that both the
-// token-major and the head-major side move whole 128-byte lines.
+// thread keeps the cosines and sines of its eight pairs of one token in registers and walks
+// the heads, UNROLL of them at a time with their loads issued together; the lanes run over a
+// head's vectors, then tokens, so that both the token-major and the head-major side move
+// whole 128-byte lines.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "sbp_internal.h"
 
@@ -24,6 +26,9 @@ namespace {
 
 constexpr int MAX_PAIRS = 128, MAX_AXES = 4;
 constexpr int TB = 8;   // tokens of a block
+// Heads in flight a thread.  T = 16384, 32 / 8 heads of 128: 72 us with one, 66 with two, 70 with
+// four (registers); neighbouring pairs, T = 8191: 37.5, 39.6, 41.6.
+constexpr int UNROLL = 2;
 
 struct RopeP {
   uint64_t F[MAX_PAIRS];
@@ -36,117 +41,112 @@ struct RopeP {
   void *q, *k, *v;           // head-major side
 };
 
-struct Pack { uint32_t w[4]; };
-__device__ __forceinline__ Pack ldp(const __nv_bfloat16* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  return Pack{{u.x, u.y, u.z, u.w}};
-}
-__device__ __forceinline__ Pack ldp(const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  Pack r;
+// Eight elements: bf16 as they lie in memory, or fp32.
+struct V16 {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
+  }
+  __device__ __forceinline__ void f(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+struct V32 {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    a = q[0];
+    b = q[1];
+  }
+  __device__ __forceinline__ void f(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  return r;
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void stp(__nv_bfloat16* p, const Pack& r) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-}
-__device__ __forceinline__ float2 up(uint32_t w) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-}
-__device__ __forceinline__ uint32_t down(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+
+// Heads h0, h0 + step, ... below h1 of one token: elements e0 .. e0+7 and e1 .. e1+7 of each.
+// The token-major row is tok + h hd, the head-major one side + (h - hbase) T hd.
+template <bool BWD, bool IL, typename V>
+__device__ __forceinline__ void walk(const RopeP& p, int h0, int h1, int step, __nv_bfloat16* tok, void* side, int hbase,
+                                     int64_t t, int e0, int e1, bool turns, const float (&cs)[8], const float (&sn)[8]) {
+  for (int h = h0; h < h1; h += UNROLL * step) {
+    V va[UNROLL], vb[UNROLL];
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      const int hk = h + k * step;
+      if (hk < h1) {
+        const int64_t at = BWD ? ((int64_t)(hk - hbase) * p.T + t) * p.hd : (int64_t)hk * p.hd;
+        va[k].load(BWD ? side : tok, at + e0);
+        vb[k].load(BWD ? side : tok, at + e1);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      const int hk = h + k * step;
+      if (hk < h1) {
+        float a[8], b[8];
+        va[k].f(a);
+        vb[k].f(b);
+        if (turns) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float &x = IL ? (i < 4 ? a[2 * (i & 3)] : b[2 * (i & 3)]) : a[i];   // pairs 8u + i: neighbours (four in
+            float &y = IL ? (i < 4 ? a[2 * (i & 3) + 1] : b[2 * (i & 3) + 1]) : b[i];   // each vector), or halves
+            const float n = x * cs[i] - y * sn[i];
+            y = y * cs[i] + x * sn[i];
+            x = n;
+          }
+        }
+        __nv_bfloat16* d = BWD ? tok + (int64_t)hk * p.hd
+                               : static_cast<__nv_bfloat16*>(side) + ((int64_t)(hk - hbase) * p.T + t) * p.hd;
+        store(d + e0, a);
+        store(d + e1, b);
+      }
+    }
+  }
 }
 
 // BWD: head-major gradients in, token-major gradient out, turned back.  KV32: dK and dV are
-// fp32 (rounded to bf16 when they do not turn; turned in fp32).  IL: the pairs are
-// neighbouring elements (2p, 2p + 1), else (p, p + rot_dim / 2).
+// fp32.  IL: the pairs are neighbouring elements (2p, 2p + 1), else (p, p + rot_dim / 2).
 template <bool BWD, bool KV32, bool IL>
 __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeP p) {
-  __shared__ float2 cs[TB * MAX_PAIRS];
-  const int64_t t0 = (int64_t)blockIdx.x * TB;
-  const int nt = (int)min((int64_t)TB, p.T - t0);
-  for (int i = threadIdx.x; i < nt * p.pairs; i += blockDim.x) {
-    const int tl = i / p.pairs, pr = i - tl * p.pairs;
-    const int64_t pos = p.pos[p.axis[pr] * p.T + t0 + tl];
-    const uint64_t turn = (uint64_t)pos * p.F[pr];
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: in half turns
-    cs[tl * p.pairs + pr] = make_float2(c, BWD ? -s : s);
-  }
-  __syncthreads();
-  const int u = threadIdx.x % p.upr;
-  const int rows = blockDim.x / p.upr;
-  const int heads = p.H + 2 * p.Hkv;
-  const int rot_units = p.pairs / 8;
+  const int u = threadIdx.x % p.upr, r = threadIdx.x / p.upr;
+  const int tl = r % TB, hg = r / TB, groups = blockDim.x / (p.upr * TB);
+  const int64_t t = (int64_t)blockIdx.x * TB + tl;
+  if (t >= p.T || hg >= groups) return;
   // the unit's two vectors: elements e0 and e1
-  const bool turns = u < rot_units;
+  const bool turns = 8 * u < p.pairs;
   const int e0 = turns && !IL ? 8 * u : 16 * u, e1 = turns && !IL ? 8 * u + p.pairs : 16 * u + 8;
-  for (int r = threadIdx.x / p.upr; r < heads * TB; r += rows) {
-    const int tl = r % TB, h = r / TB;
-    if (tl >= nt) continue;
-    const int64_t t = t0 + tl;
-    __nv_bfloat16* tok = p.x + t * p.ld + (int64_t)h * p.hd;
-    const bool isq = h < p.H, isv = h >= p.H + p.Hkv;
-    const int hh = isq ? h : h - p.H - (isv ? p.Hkv : 0);
-    void* side = isq ? p.q : isv ? p.v : p.k;
-    const int64_t ho = ((int64_t)hh * p.T + t) * p.hd;
-    float a[8], b[8];
-    Pack pa, pb;
-    if (BWD && KV32 && !isq) {
-      const float* s = static_cast<const float*>(side) + ho;
-      if (turns && !isv) {
+  float cs[8], sn[8];
+  if (turns) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) { a[i] = s[e0 + i]; b[i] = s[e1 + i]; }
-      } else {
-        pa = ldp(s + e0);
-        pb = ldp(s + e1);
-      }
-    } else {
-      const __nv_bfloat16* s = BWD ? static_cast<const __nv_bfloat16*>(side) + ho : tok;
-      pa = ldp(s + e0);
-      pb = ldp(s + e1);
-      if (turns && !isv) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = up(pa.w[i]), y = up(pb.w[i]);
-          a[2 * i] = x.x; a[2 * i + 1] = x.y;
-          b[2 * i] = y.x; b[2 * i + 1] = y.y;
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int64_t pos = p.pos[p.axis[8 * u + i] * p.T + t];
+      const uint64_t turn = (uint64_t)pos * p.F[8 * u + i];
+      sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31: in half turns
+      if (BWD) sn[i] = -sn[i];
     }
-    if (turns && !isv) {
-      const float2* w = cs + tl * p.pairs + 8 * u;
-      float oa[8], ob[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 c = w[i];
-        if (IL) {   // vector a holds pairs 8u .. 8u + 3, vector b the next four
-          float* x = i < 4 ? a : b;
-          float* o = i < 4 ? oa : ob;
-          const int j = 2 * (i & 3);
-          o[j] = x[j] * c.x - x[j + 1] * c.y;
-          o[j + 1] = x[j + 1] * c.x + x[j] * c.y;
-        } else {
-          oa[i] = a[i] * c.x - b[i] * c.y;
-          ob[i] = b[i] * c.x + a[i] * c.y;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pa.w[i] = down(oa[2 * i], oa[2 * i + 1]);
-        pb.w[i] = down(ob[2 * i], ob[2 * i + 1]);
-      }
-    }
-    __nv_bfloat16* d = BWD ? tok : static_cast<__nv_bfloat16*>(side) + ho;
-    stp(d + e0, pa);
-    stp(d + e1, pb);
   }
+  using KV = typename std::conditional<KV32, V32, V16>::type;
+  __nv_bfloat16* tok = p.x + t * p.ld;
+  const int k0 = p.H, v0 = p.H + p.Hkv, v1 = p.H + 2 * p.Hkv;
+  walk<BWD, IL, V16>(p, hg, k0, groups, tok, p.q, 0, t, e0, e1, turns, cs, sn);
+  walk<BWD, IL, KV>(p, k0 + hg, v0, groups, tok, p.k, k0, t, e0, e1, turns, cs, sn);
+  walk<BWD, IL, KV>(p, v0 + hg, v1, groups, tok, p.v, v0, t, e0, e1, false, cs, sn);
 }
 
 struct RopeArgs {
@@ -194,7 +194,8 @@ int run_rope(const RopeArgs& a, bool bwd, cudaStream_t s) {
   p.x = static_cast<__nv_bfloat16*>(a.x);
   p.q = a.q; p.k = a.k; p.v = a.v;
   const unsigned grid = (unsigned)((a.T + TB - 1) / TB);
-  const int threads = p.upr * (256 / p.upr);
+  // whole heads' rows of TB tokens, as many head groups as fit in 256 threads
+  const int threads = p.upr * TB * std::max(1, 256 / (p.upr * TB));
   const bool kv32 = bwd && a.kv_dtype == SBP_FP32;
   if (!bwd) {
     if (a.interleaved) k_rope<false, false, true><<<grid, threads, 0, s>>>(p);

@@ -8,7 +8,6 @@ has not been built (``__graft_entry__.build()``) -- there is no other code path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -473,29 +472,45 @@ def attn_packed_workspace_bytes(H: int, Hkv: int, T: int, hd: int) -> int:
     return int(_lib.sbp_attn_packed_workspace_bytes(H, Hkv, T, hd))
 
 
-def _on_device(dev, *ts):
-    """Contiguous tensors of the current device (the library launches on it)."""
+# The calls below are short enough for the host to matter (a norm of one token is a few
+# microseconds on the device), so their checks avoid PyTorch's slower queries.
+
+def _on_device(first, *ts):
+    """Contiguous tensors of one device, the current one (the library launches on it)."""
+    i = first.get_device()
+    if i < 0 or i != torch._C._cuda_getDevice() or not first.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors of the current device")
     for t in ts:
-        if t is not None and (t.device != dev or not t.is_contiguous()):
-            raise ValueError("tensors must be contiguous CUDA tensors of one device")
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError("the tensors' device must be the current CUDA device")
+        if t is not None and (t.get_device() != i or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA tensors of one device, the current one")
 
 
-def _scratch(stream):
+def _empty(stream, shape, dtype, dev):
     """What a call allocates belongs to the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _a(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
 def _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream):
-    dev = Q.device
-    _on_device(dev, Q, K, V, cu_seqlens, prefix_lens, slopes, workspace)
-    if Q.dim() != 3 or K.dim() != 3 or K.shape != V.shape or Q.shape[1:] != K.shape[1:]:
+    _on_device(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace)
+    if Q.dim() != 3 or K.dim() != 3 or K.shape != V.shape:
         raise ValueError("shapes: Q [H, T, hd]; K, V [Hkv, T, hd]")
-    if any(t.dtype != torch.bfloat16 for t in (Q, K, V)):
-        raise TypeError("Q, K, V must be bf16")
     H, T, hd = Q.shape
-    Hkv = K.shape[0]
+    Hkv, Tk, hk = K.shape
+    if T != Tk or hd != hk:
+        raise ValueError("shapes: Q [H, T, hd]; K, V [Hkv, T, hd]")
+    if not Q.dtype == K.dtype == V.dtype == torch.bfloat16:
+        raise TypeError("Q, K, V must be bf16")
     n_seq = 0
     if cu_seqlens is not None:
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
@@ -506,11 +521,10 @@ def _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream):
     if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (H,)):
         raise ValueError("slopes must be float32 [H]")
     if workspace is None:
-        n = attn_packed_workspace_bytes(H, Hkv, T, hd)
+        n = _lib.sbp_attn_packed_workspace_bytes(H, Hkv, T, hd)
         if n == 0:
             raise SbpError(ERR_UNSUPPORTED, "sbp_attn_packed_workspace_bytes")
-        with _scratch(stream):
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, n, torch.uint8, Q.device)
     return H, Hkv, T, hd, n_seq, workspace
 
 
@@ -524,16 +538,16 @@ def attn_packed(Q, K, V, scale, *, cu_seqlens=None, prefix_lens=None, slopes=Non
     lse [H, T] fp32."""
     H, Hkv, T, hd, n_seq, ws = _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream)
     dev = Q.device
-    with _scratch(stream):
-        O = torch.empty_like(Q) if O is None else O
-        lse = torch.empty((H, T), dtype=torch.float32, device=dev) if lse is None else lse
-        st = torch.empty((), dtype=torch.int32, device=dev) if status is None else status
-    _on_device(dev, O, lse, st)
-    if O.shape != Q.shape or O.dtype != Q.dtype or lse.shape != (H, T) or lse.dtype != torch.float32:
+    _on_device(Q, O, lse, status)
+    if (O is not None and (O.shape != Q.shape or O.dtype != Q.dtype)) or (
+            lse is not None and (lse.shape != (H, T) or lse.dtype != torch.float32)):
         raise ValueError("O bf16 [H, T, hd]; lse fp32 [H, T]")
-    _check(_lib.sbp_attn_packed_forward(_p(Q), _p(K), _p(V), _p(cu_seqlens), _p(prefix_lens), n_seq, _p(slopes), H,
-                                        Hkv, T, hd, float(scale), float(softcap), _p(O), _p(lse), _p(ws), ws.numel(),
-                                        _p(st), _stream(stream)), "sbp_attn_packed_forward")
+    O = _empty(stream, (H, T, hd), torch.bfloat16, dev) if O is None else O
+    lse = _empty(stream, (H, T), torch.float32, dev) if lse is None else lse
+    st = _empty(stream, (), torch.int32, dev) if status is None else status
+    _check(_lib.sbp_attn_packed_forward(_a(Q), _a(K), _a(V), _a(cu_seqlens), _a(prefix_lens), n_seq, _a(slopes), H,
+                                        Hkv, T, hd, scale, softcap, _a(O), _a(lse), _a(ws), ws.numel(), _a(st),
+                                        _raw(stream, dev)), "sbp_attn_packed_forward")
     return dict(O=O, lse=lse, status=st)
 
 
@@ -543,22 +557,22 @@ def attn_packed_backward(Q, K, V, O, dO, lse, scale, *, cu_seqlens=None, prefix_
     [Hkv, T, hd] in bf16.  O and lse are the forward's, with the same arguments."""
     H, Hkv, T, hd, n_seq, ws = _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream)
     dev = Q.device
-    with _scratch(stream):
-        dQ = torch.empty_like(Q) if dQ is None else dQ
-        dK = torch.empty_like(K) if dK is None else dK
-        dV = torch.empty_like(V) if dV is None else dV
-        st = torch.empty((), dtype=torch.int32, device=dev) if status is None else status
-    _on_device(dev, O, dO, lse, dQ, dK, dV, st)
-    if any(t.shape != Q.shape or t.dtype != torch.bfloat16 for t in (O, dO, dQ)):
-        raise ValueError("O, dO, dQ must be bf16 [H, T, hd]")
-    if any(t.shape != K.shape or t.dtype != torch.bfloat16 for t in (dK, dV)):
-        raise ValueError("dK, dV must be bf16 [Hkv, T, hd]")
+    _on_device(Q, O, dO, lse, dQ, dK, dV, status)
+    for t in (O, dO, dQ):
+        if t is not None and (t.shape != Q.shape or t.dtype != torch.bfloat16):
+            raise ValueError("O, dO, dQ must be bf16 [H, T, hd]")
+    for t in (dK, dV):
+        if t is not None and (t.shape != K.shape or t.dtype != torch.bfloat16):
+            raise ValueError("dK, dV must be bf16 [Hkv, T, hd]")
     if lse.shape != (H, T) or lse.dtype != torch.float32:
         raise ValueError("lse must be fp32 [H, T]")
-    _check(_lib.sbp_attn_packed_backward(_p(Q), _p(K), _p(V), _p(O), _p(dO), _p(lse), _p(cu_seqlens), _p(prefix_lens),
-                                         n_seq, _p(slopes), H, Hkv, T, hd, float(scale), float(softcap), _p(dQ),
-                                         _p(dK), _p(dV), _p(ws), ws.numel(), _p(st), _stream(stream)),
-           "sbp_attn_packed_backward")
+    dQ = _empty(stream, (H, T, hd), torch.bfloat16, dev) if dQ is None else dQ
+    dK = _empty(stream, (Hkv, T, hd), torch.bfloat16, dev) if dK is None else dK
+    dV = _empty(stream, (Hkv, T, hd), torch.bfloat16, dev) if dV is None else dV
+    st = _empty(stream, (), torch.int32, dev) if status is None else status
+    _check(_lib.sbp_attn_packed_backward(_a(Q), _a(K), _a(V), _a(O), _a(dO), _a(lse), _a(cu_seqlens), _a(prefix_lens),
+                                         n_seq, _a(slopes), H, Hkv, T, hd, scale, softcap, _a(dQ), _a(dK), _a(dV),
+                                         _a(ws), ws.numel(), _a(st), _raw(stream, dev)), "sbp_attn_packed_backward")
     return dict(dQ=dQ, dK=dK, dV=dV, status=st)
 
 
@@ -573,29 +587,29 @@ def _norm_args(X, gamma, *rows):
 
 
 def _rmsnorm(X, gamma, eps, residual, R, stream, q8, Y, scales):
-    dev = X.device
-    _on_device(dev, X, gamma, residual, R, Y, scales)
+    _on_device(X, gamma, residual, R, Y, scales)
     T, d, dt = _norm_args(X, gamma, residual, R)
     if residual is None and R is not None:
         raise ValueError("R is the sum with the residual: pass both or neither")
-    nblk = (d + 127) // 128
-    with _scratch(stream):
-        if residual is not None and R is None:
-            R = torch.empty_like(X)
-        if Y is None:
-            Y = torch.empty((T, d), dtype=torch.float8_e4m3fn if q8 else X.dtype, device=dev)
-        if q8 and scales is None:
-            scales = torch.empty((T, nblk), dtype=torch.float32, device=dev)
-    if Y.shape != X.shape or Y.dtype != (torch.float8_e4m3fn if q8 else X.dtype):
+    dev = X.device
+    yt = torch.float8_e4m3fn if q8 else X.dtype
+    if Y is not None and (Y.shape != X.shape or Y.dtype != yt):
         raise ValueError("Y must be shaped like X, of its dtype (e4m3 for the 8-bit output)")
+    if residual is not None and R is None:
+        R = _empty(stream, (T, d), X.dtype, dev)
+    if Y is None:
+        Y = _empty(stream, (T, d), yt, dev)
     if q8:
-        if scales.shape != (T, nblk) or scales.dtype != torch.float32:
+        nblk = (d + 127) // 128
+        if scales is None:
+            scales = _empty(stream, (T, nblk), torch.float32, dev)
+        elif scales.shape != (T, nblk) or scales.dtype != torch.float32:
             raise ValueError("scales must be float32 [T, ceil(d / 128)]")
-        _check(_lib.sbp_rmsnorm_forward_e4m3(_p(X), _p(residual), _p(gamma), T, d, float(eps), dt, _p(R), _p(Y),
-                                             _p(scales), _stream(stream)), "sbp_rmsnorm_forward_e4m3")
+        _check(_lib.sbp_rmsnorm_forward_e4m3(_a(X), _a(residual), _a(gamma), T, d, eps, dt, _a(R), _a(Y), _a(scales),
+                                             _raw(stream, dev)), "sbp_rmsnorm_forward_e4m3")
         return dict(Y8=Y, scales=scales, R=X if residual is None else R)
-    _check(_lib.sbp_rmsnorm_forward(_p(X), _p(residual), _p(gamma), T, d, float(eps), dt, _p(R), _p(Y),
-                                    _stream(stream)), "sbp_rmsnorm_forward")
+    _check(_lib.sbp_rmsnorm_forward(_a(X), _a(residual), _a(gamma), T, d, eps, dt, _a(R), _a(Y), _raw(stream, dev)),
+           "sbp_rmsnorm_forward")
     return dict(Y=Y, R=X if residual is None else R)
 
 
@@ -616,16 +630,15 @@ def rmsnorm_e4m3(X, gamma, eps, *, residual=None, R=None, Y8=None, scales=None, 
 def e4m3_expand(Y8, scales, dtype=torch.bfloat16, *, Y=None, stream=None) -> dict:
     """Y8 * scale in bf16 or fp32 (``sbp_e4m3_expand``)."""
     dev = Y8.device
-    _on_device(dev, Y8, scales, Y)
+    _on_device(Y8, scales, Y)
     T, d = Y8.shape
     if Y8.dtype != torch.float8_e4m3fn or scales.shape != (T, (d + 127) // 128) or scales.dtype != torch.float32:
         raise ValueError("Y8 e4m3 [T, d]; scales fp32 [T, ceil(d / 128)]")
     if Y is None:
-        with _scratch(stream):
-            Y = torch.empty((T, d), dtype=dtype, device=dev)
+        Y = _empty(stream, (T, d), dtype, dev)
     if Y.shape != (T, d):
         raise ValueError("Y must be shaped like Y8")
-    _check(_lib.sbp_e4m3_expand(_p(Y8), _p(scales), T, d, _code(Y), _p(Y), _stream(stream)), "sbp_e4m3_expand")
+    _check(_lib.sbp_e4m3_expand(_a(Y8), _a(scales), T, d, _code(Y), _a(Y), _raw(stream, dev)), "sbp_e4m3_expand")
     return dict(Y=Y)
 
 
@@ -633,23 +646,22 @@ def rmsnorm_backward(dY, R, gamma, eps, *, dR=None, dX=None, dgamma=None, accumu
                      stream=None) -> dict:
     """Gradients of ``rmsnorm`` at the stored sum R (``sbp_rmsnorm_backward``): dX (of X and of
     the residual alike; dR, the residual stream's gradient, is added) and dgamma [d] fp32."""
-    dev = R.device
-    _on_device(dev, dY, R, gamma, dR, dX, dgamma, workspace, status)
+    _on_device(R, dY, gamma, dR, dX, dgamma, workspace, status)
     T, d, dt = _norm_args(R, gamma, dY, dR, dX)
-    with _scratch(stream):
-        if workspace is None:
-            n = int(_lib.sbp_rmsnorm_backward_workspace_bytes(T, d, dt))
-            if n == 0:
-                raise SbpError(ERR_UNSUPPORTED, "sbp_rmsnorm_backward_workspace_bytes")
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        dX = torch.empty_like(R) if dX is None else dX
-        dgamma = torch.empty(d, dtype=torch.float32, device=dev) if dgamma is None else dgamma
-        st = torch.empty((), dtype=torch.int32, device=dev) if status is None else status
-    if dgamma.shape != (d,) or dgamma.dtype != torch.float32:
+    if dgamma is not None and (dgamma.shape != (d,) or dgamma.dtype != torch.float32):
         raise ValueError("dgamma must be float32 [d]")
-    _check(_lib.sbp_rmsnorm_backward(_p(dY), _p(R), _p(gamma), _p(dR), T, d, float(eps), dt, _p(dX), _p(dgamma),
-                                     int(bool(accumulate)), _p(workspace), workspace.numel(), _p(st),
-                                     _stream(stream)), "sbp_rmsnorm_backward")
+    dev = R.device
+    if workspace is None:
+        n = _lib.sbp_rmsnorm_backward_workspace_bytes(T, d, dt)
+        if n == 0:
+            raise SbpError(ERR_UNSUPPORTED, "sbp_rmsnorm_backward_workspace_bytes")
+        workspace = _empty(stream, n, torch.uint8, dev)
+    dX = _empty(stream, (T, d), R.dtype, dev) if dX is None else dX
+    dgamma = _empty(stream, d, torch.float32, dev) if dgamma is None else dgamma
+    st = _empty(stream, (), torch.int32, dev) if status is None else status
+    _check(_lib.sbp_rmsnorm_backward(_a(dY), _a(R), _a(gamma), _a(dR), T, d, eps, dt, _a(dX), _a(dgamma),
+                                     1 if accumulate else 0, _a(workspace), workspace.numel(), _a(st),
+                                     _raw(stream, dev)), "sbp_rmsnorm_backward")
     return dict(dX=dX, dgamma=dgamma, status=st)
 
 
@@ -678,23 +690,22 @@ def rope_qkv(qkv, positions, H, Hkv, hd, *, sections=None, rot_dim=None, theta=1
     sections: how many of the rot_dim / 2 pairs turn by each axis.  Returns Q [H, T, hd],
     K and V [Hkv, T, hd]."""
     dev = qkv.device
-    _on_device(dev, positions, Q, K, V)
-    if qkv.dim() != 2 or qkv.dtype != torch.bfloat16 or qkv.device != dev or qkv.shape[1] < (H + 2 * Hkv) * hd or (
-            qkv.numel() and qkv.stride(1) != 1):
+    _on_device(positions, Q, K, V)
+    if qkv.dim() != 2 or qkv.dtype != torch.bfloat16 or qkv.get_device() != positions.get_device() or (
+            qkv.shape[1] < (H + 2 * Hkv) * hd) or (qkv.numel() and qkv.stride(1) != 1):
         raise ValueError("qkv must be bf16 [T, >= (H + 2 Hkv) hd] with contiguous rows")
     T = qkv.shape[0]
     rot_dim = hd if rot_dim is None else rot_dim
     n, sec, freq = _rope_args(positions, T, rot_dim, sections, inv_freq)
-    with _scratch(stream):
-        Q = torch.empty((H, T, hd), dtype=torch.bfloat16, device=dev) if Q is None else Q
-        K = torch.empty((Hkv, T, hd), dtype=torch.bfloat16, device=dev) if K is None else K
-        V = torch.empty((Hkv, T, hd), dtype=torch.bfloat16, device=dev) if V is None else V
-    if Q.shape != (H, T, hd) or K.shape != (Hkv, T, hd) or V.shape != K.shape or any(
-            t.dtype != torch.bfloat16 for t in (Q, K, V)):
-        raise ValueError("Q bf16 [H, T, hd]; K, V bf16 [Hkv, T, hd]")
-    _check(_lib.sbp_rope_qkv_forward(_p(qkv), qkv.stride(0) if T > 1 else qkv.shape[1], _p(positions), n, sec, freq,
-                                     float(theta), rot_dim, int(bool(interleaved)), T, H, Hkv, hd, _p(Q), _p(K), _p(V),
-                                     _stream(stream)), "sbp_rope_qkv_forward")
+    for t, h in ((Q, H), (K, Hkv), (V, Hkv)):
+        if t is not None and (t.shape != (h, T, hd) or t.dtype != torch.bfloat16):
+            raise ValueError("Q bf16 [H, T, hd]; K, V bf16 [Hkv, T, hd]")
+    Q = _empty(stream, (H, T, hd), torch.bfloat16, dev) if Q is None else Q
+    K = _empty(stream, (Hkv, T, hd), torch.bfloat16, dev) if K is None else K
+    V = _empty(stream, (Hkv, T, hd), torch.bfloat16, dev) if V is None else V
+    _check(_lib.sbp_rope_qkv_forward(_a(qkv), qkv.stride(0) if T > 1 else qkv.shape[1], _a(positions), n, sec, freq,
+                                     theta, rot_dim, 1 if interleaved else 0, T, H, Hkv, hd, _a(Q), _a(K), _a(V),
+                                     _raw(stream, dev)), "sbp_rope_qkv_forward")
     return dict(Q=Q, K=K, V=V)
 
 
@@ -703,7 +714,7 @@ def rope_qkv_backward(dQ, dK, dV, positions, *, sections=None, rot_dim=None, the
     """Gradient of ``rope_qkv`` (``sbp_rope_qkv_backward``): dQ [H, T, hd] bf16; dK, dV
     [Hkv, T, hd], both bf16 or both fp32.  Returns dqkv [T, (H + 2 Hkv) hd] bf16."""
     dev = dQ.device
-    _on_device(dev, dQ, dK, dV, positions)
+    _on_device(dQ, dK, dV, positions)
     if dQ.dim() != 3 or dK.dim() != 3 or dK.shape != dV.shape or dQ.shape[1:] != dK.shape[1:]:
         raise ValueError("shapes: dQ [H, T, hd]; dK, dV [Hkv, T, hd]")
     if dQ.dtype != torch.bfloat16 or dK.dtype != dV.dtype:
@@ -713,13 +724,12 @@ def rope_qkv_backward(dQ, dK, dV, positions, *, sections=None, rot_dim=None, the
     rot_dim = hd if rot_dim is None else rot_dim
     n, sec, freq = _rope_args(positions, T, rot_dim, sections, inv_freq)
     if dqkv is None:
-        with _scratch(stream):
-            dqkv = torch.empty((T, (H + 2 * Hkv) * hd), dtype=torch.bfloat16, device=dev)
-    if dqkv.dim() != 2 or dqkv.shape[0] != T or dqkv.shape[1] < (H + 2 * Hkv) * hd or dqkv.device != dev or (
+        dqkv = _empty(stream, (T, (H + 2 * Hkv) * hd), torch.bfloat16, dev)
+    elif dqkv.dim() != 2 or dqkv.shape[0] != T or dqkv.shape[1] < (H + 2 * Hkv) * hd or dqkv.device != dev or (
             dqkv.dtype != torch.bfloat16) or (dqkv.numel() and dqkv.stride(1) != 1):
         raise ValueError("dqkv must be bf16 [T, >= (H + 2 Hkv) hd] with contiguous rows")
-    _check(_lib.sbp_rope_qkv_backward(_p(dQ), _p(dK), _p(dV), _code(dK), _p(positions), n, sec, freq, float(theta),
-                                      rot_dim, int(bool(interleaved)), T, H, Hkv, hd, _p(dqkv),
-                                      dqkv.stride(0) if T > 1 else dqkv.shape[1], _stream(stream)),
+    _check(_lib.sbp_rope_qkv_backward(_a(dQ), _a(dK), _a(dV), _code(dK), _a(positions), n, sec, freq, theta, rot_dim,
+                                      1 if interleaved else 0, T, H, Hkv, hd, _a(dqkv),
+                                      dqkv.stride(0) if T > 1 else dqkv.shape[1], _raw(stream, dev)),
            "sbp_rope_qkv_backward")
     return dict(dqkv=dqkv)
