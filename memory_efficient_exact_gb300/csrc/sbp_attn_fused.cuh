@@ -319,6 +319,10 @@ struct MapArray {   // in the kernel's parameters
   __device__ __forceinline__ const CUtensorMap* operator[](int i) const { return &m[i]; }
 };
 
+// A unit of k_attn_kv: key / value head zk, keys [256 kp, +256), query blocks [b0, b0 + nbl) of
+// each of the query heads [z0, z0 + nh); `plane` says where its dK and dV go.
+struct KvUnit { int zk, kp, b0, nbl, z0, nh, plane; };
+
 // Chunked causal attention: query i of the chunk [c0, c1) sees the keys 0 .. i.
 struct CausalScores {
   using Kv = KvP;
@@ -329,16 +333,21 @@ struct CausalScores {
   static constexpr bool kAddOut = true;   // dK, dV are added into fp32 outputs
   using Scale = float;                    // scale * log2(e)
 
+  // The unit of round t of SM pair pid.
+  static __device__ __forceinline__ int next_unit(int t, int pid, int npairs) { return t * npairs + pid; }
   // Unit u: key / value head zk, keys [256 kp, 256 kp + 256); query blocks b0 .. nb-1 of
   // the chunk hold at least one query at or after the unit's first key.  The unit walks
   // those nbl blocks for each query head of zk's group, accumulating dV and dK of the
   // shared head.  Key pairs in ascending order, so the longest units start first.
-  static __device__ __forceinline__ void kv_unit(const KvP& p, int u, int& zk, int& kp, int& b0, int& nbl) {
-    kp = u / p.Hkv;
-    zk = u - kp * p.Hkv;
-    const int num = 256 * kp - p.c0 - 127;
-    b0 = num <= 0 ? 0 : (num + 127) / 128;
-    nbl = p.nb - b0;
+  static __device__ __forceinline__ void kv_unit(const KvP& p, int u, KvUnit& w) {
+    w.kp = u / p.Hkv;
+    w.zk = u - w.kp * p.Hkv;
+    const int num = 256 * w.kp - p.c0 - 127;
+    w.b0 = num <= 0 ? 0 : (num + 127) / 128;
+    w.nbl = p.nb - w.b0;
+    w.z0 = w.zk * p.group;
+    w.nh = p.group;
+    w.plane = w.zk;
   }
   // Queries [lo, hi) that see a key; both ends do not decrease with the key.  A warp's 32
   // keys from kw: lowest and highest of each end.
@@ -388,12 +397,11 @@ struct CausalScores {
   static __device__ __forceinline__ int tail_block(const P&) { return -1; }
 };
 
-// Block n of a unit that walks nbl query blocks from b0 for each query head of the group:
-// query head z, query block b.
-__device__ __forceinline__ void kv_block(int group, int zk, int b0, int nbl, int n, int& z, int& b) {
-  const int gh = n / nbl;
-  z = zk * group + gh;
-  b = b0 + (n - gh * nbl);
+// Block n of a unit: query head z, query block b.
+__device__ __forceinline__ void kv_block(const KvUnit& w, int n, int& z, int& b) {
+  const int h = n / w.nbl;
+  z = w.z0 + h;
+  b = w.b0 + (n - h * w.nbl);
 }
 
 template <class S>
@@ -419,26 +427,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       int sa = 0;
       uint32_t pha = 0, phr = 0, iss = 0, lph_a[2] = {0, 0}, lph_r = 0;
       bool ok = true;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
-        int zk, kp, b0, nbl;
-        S::kv_unit(p, u, zk, kp, b0, nbl);
-        const int nblk = p.group * nbl;
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
+        KvUnit w;
+        S::kv_unit(p, u, w);
+        const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
         if (!wait_inl<false>(&c->rempty, phr ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
         const uint32_t fr = mapa(saddr(&c->rfull), 0);
         if (rank == 0) mbar_expect_tx(&c->rfull, 4u * 32768u);
-        const int krow = 256 * kp + 128 * (int)rank;
+        const int krow = 256 * w.kp + 128 * (int)rank;
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
-          tma_load_3d_pair(sb + KV_K + hb * 16384, maps[KV_MK], fr, 64 * hb, krow, zk);
-          tma_load_3d_pair(sb + KV_V + hb * 16384, maps[KV_MV], fr, 64 * hb, krow, zk);
+          tma_load_3d_pair(sb + KV_K + hb * 16384, maps[KV_MK], fr, 64 * hb, krow, w.zk);
+          tma_load_3d_pair(sb + KV_V + hb * 16384, maps[KV_MV], fr, 64 * hb, krow, w.zk);
         }
         iss |= 4u;
         lph_r = phr;
         phr ^= 1u;
         for (int n = 0; n < nblk; ++n) {
           int z, b;
-          kv_block(p.group, zk, b0, nbl, n, z, b);
+          kv_block(w, n, z, b);
           if (!wait_inl<false>(&c->aempty[sa], pha ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
           const uint32_t fa = mapa(saddr(&c->afull[sa]), 0);
           if (rank == 0) mbar_expect_tx(&c->afull[sa], 2u * KV_A_STAGE);
@@ -469,14 +477,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       const int tail = S::tail_block(p);
       uint32_t phb = 0, lph = 0;
       bool ok = true, any = false;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
-        int zk, kp, b0, nbl;
-        S::kv_unit(p, u, zk, kp, b0, nbl);
-        const int nblk = p.group * nbl;
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
+        KvUnit w;
+        S::kv_unit(p, u, w);
+        const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
         for (int n = 0; n < nblk; ++n) {
           int z, b;
-          kv_block(p.group, zk, b0, nbl, n, z, b);
+          kv_block(w, n, z, b);
           if (!wait_inl<false>(&c->bempty[0], phb ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
           const uint32_t fb = mapa(saddr(&c->bfull[0]), 0);
           if (rank == 0) mbar_expect_tx(&c->bfull[0], 4u * 16384u);
@@ -525,10 +533,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         commit2_mc(&c->ofree, 3);
         return true;
       };
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
-        int zk, kp, b0, nbl;
-        S::kv_unit(p, u, zk, kp, b0, nbl);
-        const int nblk = p.group * nbl;
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
+        KvUnit w;
+        S::kv_unit(p, u, w);
+        const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
         if (!wait_inl<false>(&c->rfull, phr, &c->abort, p.limit_ns)) { ok = false; break; }
         phr ^= 1u;
@@ -567,10 +575,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
     if (lane == 0) {
       uint32_t te_seen = 0, or_seen = 0, g = 0;
       bool ok = true;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
-        int zk, kp, b0, nbl;
-        S::kv_unit(p, u, zk, kp, b0, nbl);
-        const int nblk = p.group * nbl;
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
+        KvUnit w;
+        S::kv_unit(p, u, w);
+        const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
         for (int n = 0; n < nblk; ++n, ++g)
           if (!forward_block(c, g, te_seen, or_seen, p.limit_ns)) { ok = false; break; }
@@ -583,14 +591,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
     // refilled once the epilogue warps have read it); loads issued a block ahead
     float* ld = reinterpret_cast<float*>(base + KV_LD);
     uint32_t lempty_seen = 0, g = 0;
-    for (int u = pid; u < p.n_units; u += npairs) {
-      int zk, kp, b0, nbl;
-      S::kv_unit(p, u, zk, kp, b0, nbl);
-      const int nblk = p.group * nbl;
+    for (int rnd = 0, u = pid; u < p.n_units; u = S::next_unit(++rnd, pid, npairs)) {
+      KvUnit w;
+      S::kv_unit(p, u, w);
+      const int nblk = w.nh * w.nbl;
       bool ok = true;
       for (int n = 0; n < nblk; ++n, ++g) {
         int z, b;
-        kv_block(p.group, zk, b0, nbl, n, z, b);
+        kv_block(w, n, z, b);
         float lv[4], dv[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -622,24 +630,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
     uint32_t tfull_seen = 0, ofree_seen = 0, lfull_seen = 0, sfree_seen = 0, g = 0;
     int lu = 0;
     bool ok = true;
-    for (int u = pid; u < p.n_units && ok; u += npairs) {
-      int zk, kp, b0, nbl;
-      S::kv_unit(p, u, zk, kp, b0, nbl);
-      const int nblk = p.group * nbl;
-      const int kw = 256 * kp + 128 * (int)rank + 32 * q;   // this warp's first key
+    for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
+      KvUnit w;
+      S::kv_unit(p, u, w);
+      const int nblk = w.nh * w.nbl;
+      const int kw = 256 * w.kp + 128 * (int)rank + 32 * q;   // this warp's first key
       const int key = kw + lane;
       int lo, hi, lo0, lo1, hi0, hi1;   // queries that see this thread's key; over the warp's keys
       S::key_range(p, key, lo, hi);
       S::key_warp(p, kw, lo, hi, lo0, lo1, hi0, hi1);
       if constexpr (!S::kAddOut) {
         if (nblk == 0) {   // no query sees these keys
-          S::store_zero(p, zk, key, 64 * ch);
+          S::store_zero(p, w.plane, key, 64 * ch);
           continue;
         }
       }
       for (int n = 0; n < nblk; ++n, ++g) {
         int z, b;
-        kv_block(p.group, zk, b0, nbl, n, z, b);
+        kv_block(w, n, z, b);
         const typename S::Scale sc = S::scale_of(p, z);
         if (!warp_wait_n(&c->tfull, tfull_seen, g + 1, c, p.limit_ns) ||
             !warp_wait_n(&c->lfull, lfull_seen, g + 1, c, p.limit_ns)) { ok = false; break; }
@@ -709,7 +717,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
         }
         if constexpr (!S::kAddOut) {
-          S::store_out(p, t, zk, key, 64 * ch, ra);
+          S::store_out(p, t, w.plane, key, 64 * ch, ra);
           continue;
         }
         if (kw >= p.c1) continue;
@@ -731,8 +739,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, 64 * ch, kw, zk);
-          tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg + 4096u, 64 * ch + 32, kw, zk);
+          tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, 64 * ch, kw, w.zk);
+          tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg + 4096u, 64 * ch + 32, kw, w.zk);
           bulk_commit();
         }
       }
@@ -799,7 +807,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       int sa = 0;
       uint32_t pha = 0, phr = 0, iss = 0, lph_a[2] = {0, 0}, lph_r = 0;
       bool ok = true;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
         if (nj == 0) continue;
@@ -846,7 +854,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       int sy = 0;
       uint32_t phy = 0, iss = 0, lph[2] = {0, 0};
       bool ok = true;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
         if (nj == 0) continue;
@@ -895,7 +903,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         if (++sy == 2) { sy = 0; phy ^= 1u; }
         return true;
       };
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
         if (nj == 0) continue;
@@ -934,7 +942,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     if (lane == 0) {
       uint32_t te_seen = 0, or_seen = 0, g = 0;
       bool ok = true;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
         if (nj == 0) continue;
@@ -950,7 +958,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     uint32_t tfull_seen = 0, g = 0;
     uint32_t ds_seen0 = 0, ds_seen1 = 0, ds_uses0 = 0, ds_uses1 = 0;   // per dS buffer: completions waited, blocks written
     bool ok = true;
-    for (int u = pid; u < p.n_units && ok; u += npairs) {
+    for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
       int z, qp, j0, nj;
       S::q_unit(p, u, z, qp, j0, nj);
       const typename S::Scale sc = S::scale_of(p, z);

@@ -1,17 +1,23 @@
 // Forward of the attention over packed documents (bf16 operands, fp32 softmax, sm_103a).
 //
 // k_attn_o  unit = (query head, 256 queries), 128 queries in each CTA of an SM pair, the
-// longest units first.  O stays in tensor memory while the unit walks its blocks of 128 keys:
-//   S = Q K^T            (tensor memory, two buffers)
-//   P = 2^(x - m)        (softmax warps; bf16, two buffers in tensor memory)
+// longest units first.  The unit walks its blocks of 128 keys; two groups of four softmax
+// warps take the blocks in turn, each with its own S buffer, running maximum, sum and O
+// accumulator in tensor memory, so that they exchange nothing until the unit's end:
+//   S = Q K^T            (tensor memory)
+//   P = 2^(x - m)        (one query row a thread; bf16, written over S)
 //   O += P V             (tensor memory; P is the A operand from tensor memory)
-// so nothing of size (queries x keys) leaves the SM.  With two S buffers the next block's S
-// is ready before the softmax warps have finished a block, and O += P V of the block before
-// runs behind it, so that the softmax warps never wait for the tensor pipe.
-// The running maximum m is only raised when a block exceeds it by more than 2^8 (P and its
-// sum stay far from overflow below that), and O is rescaled in tensor memory only then.  The
-// sum l adds the fp32 probabilities; P is rounded to bf16 for the product, the operand type
-// of the tensor pipe at full rate: at most 2^-9 of each probability.
+// While one group works on a block, the tensor pipe runs the other group's O += P V and its
+// next S.  At the end the two accumulators are joined, O = (O0 2^(m0-m) + O1 2^(m1-m)) / l.
+// Nothing of size (queries x keys) leaves the SM.
+// A row's 128 scores are read twice, 64 at a time: once for the maximum, and the second half
+// again for the exponentials, because 128 registers of scores leave none for the rest (12
+// warps, 168 registers a thread).  The maximum is only raised when a block exceeds it by more
+// than 2^8 (P and its sum stay far from overflow below that), and O rescaled only then.
+// Scores capped at up to kStaticCap need no maximum at all: 2^x neither overflows nor, for
+// the row's own key, underflows.  The sum l adds the fp32 probabilities; P is rounded to
+// bf16 for the product, the operand type of the tensor pipe at full rate: at most 2^-8 of
+// each probability.
 //
 // Pair protocol and bounded waits as in the backward kernels (sbp_attn_fused.cuh).
 #include <algorithm>
@@ -27,11 +33,9 @@ using fa::dplus;
 using fa::mma2_bf16_ts;
 using fa::tmem_st_wait;
 
-// Warps: 0 TMA producers, 1 MMA issuer, 2-9 softmax (lane quadrant warp % 4, 64 of the 128
-// columns each), 10 forwarder (turns the CTA's local arrivals into one arrival at the
-// leader), 11 idle: 12 warps, so 168 registers a thread.
-constexpr int EPI = 8;
-constexpr int FWD_WARP = 2 + EPI;
+// Warps: 0 TMA producers, 1 MMA issuer, 2 forwarder (turns the CTA's local arrivals into one
+// arrival at the leader), 3 idle, 4-7 and 8-11 the softmax groups (lane quadrant warp % 4).
+constexpr int FWD_WARP = 2, SOFT_WARP = 4;
 constexpr int THREADS = 384;
 
 // Shared memory, bytes from the 1024-aligned base; tiles are 128-byte swizzled
@@ -40,23 +44,22 @@ constexpr int KV_STAGES = 4;
 constexpr uint32_t O_Q = 0;                              // 2 units: this CTA's 128 queries
 constexpr uint32_t O_K = 65536;                          // this CTA's 64 keys of the block
 constexpr uint32_t O_V = O_K + KV_STAGES * 16384;        // 128 keys x this CTA's 64 of hd
-constexpr uint32_t O_MX = O_V + KV_STAGES * 16384;       // [2][2 halves][128 rows] fp32
-constexpr uint32_t O_CTRL = O_MX + 2048;
-// Tensor memory: S buffers at 0 and 128, O at T_O, P buffers of 64 columns at T_P.
-constexpr uint32_t T_O = 256, T_P = 384;
+constexpr uint32_t O_ML = O_V + KV_STAGES * 16384;       // m, l: [2 units][2 groups][128 rows] float2
+constexpr uint32_t O_CTRL = O_ML + 4096;
+// Tensor memory: S (and P over it) of group b at 128 b, its O at T_O + 128 b.
+constexpr uint32_t T_O = 256;
 constexpr uint32_t IDESC_KK = idesc_bf16(256, 128, false, false);  // A, B K-major
 constexpr uint32_t IDESC_KM = idesc_bf16(256, 128, false, true);   // A K-major, B MN-major
 
 struct Ctrl {
   uint64_t kfull[KV_STAGES], kempty[KV_STAGES], vfull[KV_STAGES], vempty[KV_STAGES];
   uint64_t qfull[2], qempty[2];
-  uint64_t sfull[2];             // S buffer is ready (both CTAs)
-  uint64_t sempty[2];            // leader: both CTAs have read the S buffer
-  uint64_t pready[2];            // leader: both CTAs' P buffer is written
-  uint64_t pfree[2];             // O += P V of the P buffer is done (both CTAs)
-  uint64_t sempty_l[2], pready_l[2];   // the CTA's softmax warps, forwarded
-  uint64_t accempty;             // leader: the unit's O has been read out
-  uint64_t mx[4];                // per lane quadrant: its two warps have left their row values
+  uint64_t sfull[2];      // S of the group's block is ready, and its earlier products are done
+  uint64_t pready[2];     // leader: both CTAs' P is written
+  uint64_t pready_l[2];   // the CTA's four warps of the group, forwarded
+  uint64_t ofull;         // the unit's products are done (both CTAs)
+  uint64_t accempty;      // leader: the unit's O has been read out
+  uint64_t mlx;           // the CTA's eight softmax warps have left m and l
   uint64_t mdone;
   uint32_t tmem_base;
   int abort;
@@ -109,8 +112,76 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 
-// tmVt: the last block's V with zeroed padding (PackedWork::tail)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair(a.x, a.y)), "l"(pair(b.x, b.y)), "l"(pair(c.x, c.y)));
+  return unpair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a.x, a.y)), "l"(pair(b.x, b.y)));
+  return unpair(d);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A row's view of 32 keys: which of them it sees, and how far they are.
+struct Row {
+  int a, b;     // visible: keys k0 + [a, b)
+  float fd;     // query - k0
+};
+
+// 32 scores (keys k0 + c ..) as they enter the exponential, -inf where the row does not see
+// the key.  RAW: left unscaled.
 template <bool CAP, bool BIAS>
+__device__ __forceinline__ void scores32(uint32_t (&r)[32], int c, bool mask, const Row& w, const pk::ScaleZ& sc) {
+  if (CAP || BIAS) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float dc;
+      float x = pk::capped<CAP>(sc, __uint_as_float(r[i]), dc);
+      if (BIAS) x = fmaf(-sc.slope2, fabsf(w.fd - (float)(c + i)), x);
+      r[i] = __float_as_uint(x);
+    }
+  }
+  if (mask) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < w.a || c + i >= w.b) r[i] = 0xff800000u;
+  }
+}
+__device__ __forceinline__ float max32(const uint32_t (&r)[32], float m0) {
+  float m[4] = {m0, __uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2])};
+#pragma unroll
+  for (int i = 3; i + 1 < 32; i += 2)
+    m[(i >> 1) & 3] = max3(m[(i >> 1) & 3], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+  return max3(fmaxf(m[0], m[1]), m[2], fmaxf(m[3], __uint_as_float(r[31])));
+}
+// 32 probabilities 2^(mul x + nm): packed to bf16, their sum added to l.
+__device__ __forceinline__ void probs32(const uint32_t (&r)[32], float mul, float nm, uint32_t* pw, float2& l) {
+  const float2 mul2 = make_float2(mul, mul), nm2 = make_float2(nm, nm);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 x = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), mul2, nm2);
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    l = add2(l, e);
+    pw[i] = pack_bf16(e.x, e.y);
+  }
+}
+
+// tmVt: the last block's V with zeroed padding (PackedWork::tail)
+// FIXED: scores capped low enough for a maximum of 0 throughout.
+template <bool CAP, bool BIAS, bool FIXED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k_attn_o(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVt, const Params p) {
@@ -118,7 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl* c = reinterpret_cast<Ctrl*>(base + O_CTRL);
   const uint32_t sb = saddr(base);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform_warp(), lane = threadIdx.x % 32;
   const uint32_t rank = ctarank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < KV_STAGES; ++i) {
@@ -131,14 +202,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&c->qfull[i], 1);
       mbar_init(&c->qempty[i], 1);
       mbar_init(&c->sfull[i], 1);
-      mbar_init(&c->sempty[i], 2);
       mbar_init(&c->pready[i], 2);
-      mbar_init(&c->pfree[i], 1);
-      mbar_init(&c->sempty_l[i], EPI);
-      mbar_init(&c->pready_l[i], EPI);
+      mbar_init(&c->pready_l[i], 4);
     }
-    mbar_init(&c->accempty, 2 * EPI);
-    for (int i = 0; i < 4; ++i) mbar_init(&c->mx[i], 2);
+    mbar_init(&c->ofull, 1);
+    mbar_init(&c->accempty, 2 * 8);
+    mbar_init(&c->mlx, 8);
     mbar_init(&c->mdone, 1);
     c->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -163,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       prefetch_map(&tmK);
       uint32_t g = 0, lu = 0;   // blocks and units so far
       bool ok = true;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         unit_of(p, u, z, qp, j0, nj);
         if (nj <= 0) continue;
@@ -203,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int tail = *p.tail;
       uint32_t g = 0;
       bool ok = true;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         unit_of(p, u, z, qp, j0, nj);
         for (int j = 0; j < nj; ++j) {
@@ -226,39 +295,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint64_t dQ = sw128_desc(sb + O_Q, 16, 1024), dK = sw128_desc(sb + O_K, 16, 1024),
                      dV = sw128_desc(sb + O_V, 16384, 1024);
       uint32_t g = 0, lu = 0;
       bool ok = true;
-      // O += P V of block gg (the first of its unit overwrites)
-      auto accumulate = [&](uint32_t gg, bool first) -> bool {
+      // S of block gg into its group's buffer: free, since the product that read the P in it
+      // was issued before
+      auto scores = [&](uint32_t gg, uint32_t qs) -> bool {
         const uint32_t s = gg % KV_STAGES, b = gg & 1u;
-        if (!wait1(&c->pready[b], gg >> 1, c, p.limit_ns)) return false;
-        if (!wait1(&c->vfull[s], gg / KV_STAGES, c, p.limit_ns)) return false;
-        if (first && !wait1(&c->accempty, lu ^ 1u, c, p.limit_ns)) return false;
+        if (!warp_wait(&c->kfull[s], gg / KV_STAGES, c, p.limit_ns)) return false;
         tc_fence_after();
-        const uint64_t v0 = dplus(dV, s * 16384u);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma2_bf16_ts(tmem + T_O, tmem + T_P + 64 * b + 8 * k, dplus(v0, k * 2048), IDESC_KM,
-                       (!first || k) ? 1u : 0u);
-        commit2_mc(&c->vempty[s], 3);
-        commit2_mc(&c->pfree[b], 3);
-        return true;
-      };
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
-        int z, qp, j0, nj;
-        unit_of(p, u, z, qp, j0, nj);
-        if (nj <= 0) continue;
-        const uint32_t qs = lu & 1u;
-        if (!wait1(&c->qfull[qs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
-        for (int n = 0; n < nj; ++n, ++g) {
-          const uint32_t s = g % KV_STAGES, b = g & 1u;
-          if (!wait1(&c->sempty[b], (g >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
-          if (!wait1(&c->kfull[s], g / KV_STAGES, c, p.limit_ns)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t q0 = dplus(dQ, qs * 32768u), k0 = dplus(dK, s * 16384u);
+        const uint64_t q0 = dplus(dQ, qs * 32768u), k0 = dplus(dK, s * 16384u);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma2_bf16(tmem + 128 * b, dplus(q0, k * 32), dplus(k0, k * 32), IDESC_KK, k ? 1u : 0u);
@@ -269,15 +318,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           commit2_mc(&c->kempty[s], 3);
           commit2_mc(&c->sfull[b], 3);
-          if (n == nj - 1) commit2_mc(&c->qempty[qs], 3);
-          if (n >= 1 && !accumulate(g - 1, n == 1)) { ok = false; break; }
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
+        int z, qp, j0, nj;
+        unit_of(p, u, z, qp, j0, nj);
+        if (nj <= 0) continue;
+        const uint32_t qs = lu & 1u;
+        if (!warp_wait(&c->qfull[qs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
+        if (!scores(g, qs) || (nj > 1 && !scores(g + 1, qs))) { ok = false; break; }
+        for (int n = 0; n < nj; ++n, ++g) {
+          const uint32_t s = g % KV_STAGES, b = g & 1u;
+          if (!warp_wait(&c->pready[b], g >> 1, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait(&c->vfull[s], g / KV_STAGES, c, p.limit_ns)) { ok = false; break; }
+          if (n == 0 && !warp_wait(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t v0 = dplus(dV, s * 16384u);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma2_bf16_ts(tmem + T_O + 128 * b, tmem + 128 * b + 8 * k, dplus(v0, k * 2048), IDESC_KM,
+                           (n > 1 || k) ? 1u : 0u);   // each group's first block overwrites
+            commit2_mc(&c->vempty[s], 3);
+          }
+          __syncwarp();
+          if (n + 2 < nj && !scores(g + 2, qs)) { ok = false; break; }
+          if ((n + 2 == nj || nj == 1) && elect_one()) commit2_mc(&c->qempty[qs], 3);   // every S of the unit is issued
         }
         if (!ok) break;
-        if (!accumulate(g - 1, nj == 1)) { ok = false; break; }
+        if (elect_one()) commit2_mc(&c->ofull, 3);
         ++lu;
       }
-      if (!ok) fail_o(c, p.status);
-      commit2_mc(&c->mdone, 1);
+      if (elect_one()) {
+        if (!ok) fail_o(c, p.status);
+        commit2_mc(&c->mdone, 1);
+      }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
     }
     __syncwarp();
@@ -285,171 +362,163 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       uint32_t g = 0;
       bool ok = true;
-      for (int u = pid; u < p.n_units && ok; u += npairs) {
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         unit_of(p, u, z, qp, j0, nj);
         for (int j = 0; j < nj; ++j, ++g) {
-          const uint32_t b = g & 1u;
-          if (!wait1(&c->sempty_l[b], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->sempty[b]), 0));
-          if (!wait1(&c->pready_l[b], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->pready[b]), 0));
+          if (!wait1(&c->pready_l[g & 1u], g >> 1, c, p.limit_ns)) { ok = false; break; }
+          arrive_remote(mapa(saddr(&c->pready[g & 1u]), 0));
         }
       }
       if (!ok) fail_o(c, p.status);
     }
     __syncwarp();
-  } else if (warp < FWD_WARP) {
-    const int q = warp & 3, ch = (warp - 2) >> 2;   // lane quadrant; 64-column half
+  } else if (warp >= SOFT_WARP) {
+    const int q = warp & 3, grp = (warp - SOFT_WARP) >> 2;   // lane quadrant; softmax group
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-    float* mxp = reinterpret_cast<float*>(base + O_MX);
+    const uint32_t tS = trow + 128 * grp, tO = trow + T_O + 128 * grp;
     const int lrow = 32 * q + lane;
     // scores stay raw when they only need the scale, which the exponent's FMA applies
     constexpr bool RAW = !CAP && !BIAS;
     const float mul = RAW ? p.sc.sl2 : 1.f;
-    uint32_t g = 0, e = 0;   // blocks and row-value exchanges so far
+    uint32_t g = 0, lu = 0;
     bool ok = true;
-    // v of this row from the warp that has the other 64 columns
-    auto other = [&](float v, float& o) -> bool {
-      float* slot = mxp + (e & 1u) * 256;
-      slot[ch * 128 + lrow] = v;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->mx[q]);
-      if (!warp_wait(&c->mx[q], e, c, p.limit_ns)) return false;
-      o = slot[(ch ^ 1) * 128 + lrow];
-      ++e;
-      return true;
-    };
-    for (int u = pid; u < p.n_units && ok; u += npairs) {
+    for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
       int z, qp, j0, nj;
       unit_of(p, u, z, qp, j0, nj);
       const int row = 256 * qp + 128 * (int)rank + lrow;
       const bool vrow = row < p.T;
       const int64_t ro = (int64_t)z * p.T + row;
       const int lo = vrow ? p.lo[row] : p.T, hi = vrow ? p.hi[row] : p.T;
-      const int lo0 = __shfl_sync(0xffffffffu, lo, 0), lo1 = __shfl_sync(0xffffffffu, lo, 31);
-      const int hi0 = __shfl_sync(0xffffffffu, hi, 0), hi1 = __shfl_sync(0xffffffffu, hi, 31);
+      const int lo1 = __shfl_sync(0xffffffffu, lo, 31), hi0 = __shfl_sync(0xffffffffu, hi, 0);
       const pk::ScaleZ sc{p.sc.sl2, p.sc.c2, p.sc.k, BIAS ? p.slopes[z] * L2E : 0.f};
-      float m = -INFINITY, l = 0.f;
-      for (int n = 0; n < nj; ++n, ++g) {
-        const uint32_t b = g & 1u;
-        if (!warp_wait(&c->sfull[b], g >> 1, c, p.limit_ns)) { ok = false; break; }
+      float m = FIXED ? 0.f : -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int n = (int)((g ^ (uint32_t)grp) & 1u); n < nj; n += 2) {   // this group's blocks
+        if (!warp_wait(&c->sfull[grp], (g + n) >> 1, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
-        uint32_t r[2][32];
-        tmem_ld32(trow + 128 * b + 64 * ch, r[0]);
-        tmem_ld32(trow + 128 * b + 64 * ch + 32, r[1]);
-        tmem_ld_wait();
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->sempty_l[b]);   // S is in registers: its buffer may be refilled
-        const int k0 = 128 * (j0 + n) + 64 * ch;       // this thread's first key
-        if (!RAW) {
-          const float fd = (float)(row - k0);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float dc;
-              float x = pk::capped<CAP>(sc, __uint_as_float(r[h][i]), dc);
-              if (BIAS) x = fmaf(-sc.slope2, fabsf(fd - (float)(32 * h + i)), x);
-              r[h][i] = __float_as_uint(x);
-            }
-        }
-        if (k0 < lo1 || k0 + 63 >= hi0) {   // some row of the warp does not see all 64 keys
-          const int a = lo - k0, t = hi - k0;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * h + i < a || 32 * h + i >= t) r[h][i] = 0xff800000u;   // -inf
-        }
-        float mx[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          mx[h] = __uint_as_float(r[h >> 1][16 * (h & 1)]);
-#pragma unroll
-          for (int i = 1; i < 16; ++i) mx[h] = fmaxf(mx[h], __uint_as_float(r[h >> 1][16 * (h & 1) + i]));
-        }
-        float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mo;
-        if (!other(mb, mo)) { ok = false; break; }
-        mb = fmaxf(mb, mo);
-        float f = 1.f;
-        if (mb > m && (m == -INFINITY || (mb - m) * mul > 8.f)) {
-          f = ex2((m - mb) * mul);   // 0 from m = -inf
-          m = mb;
-        }
-        // both warps of the row take the same decision; each rescales its 64 columns of O
-        if (n > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-          if (!warp_wait(&c->pfree[b ^ 1u], (g - 1) >> 1, c, p.limit_ns)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll 1
-          for (int h = 0; h < 64; h += 32) {
-            uint32_t o[32];
-            tmem_ld32(trow + T_O + 64 * ch + h, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(trow + T_O + 64 * ch + h, o);
+        const int k0 = 128 * (j0 + n);
+        const bool mask = k0 < lo1 || k0 + 127 >= hi0;   // some row of the warp does not see all keys
+        const Row w{lo - k0, hi - k0, (float)(row - k0)};
+        uint32_t ra[32], rb[32], pw[32];
+        if (!FIXED) {
+          tmem_ld32(tS + 64, ra);
+          tmem_ld32(tS + 96, rb);
+          tmem_ld_wait();
+          scores32<CAP, BIAS>(ra, 64, mask, w, sc);
+          scores32<CAP, BIAS>(rb, 96, mask, w, sc);
+          float mb = max32(rb, max32(ra, -INFINITY));
+          tmem_ld32(tS, ra);
+          tmem_ld32(tS + 32, rb);
+          tmem_ld_wait();
+          scores32<CAP, BIAS>(ra, 0, mask, w, sc);
+          scores32<CAP, BIAS>(rb, 32, mask, w, sc);
+          mb = max32(rb, max32(ra, mb));
+          float f = 1.f;
+          if (mb > m && (m == -INFINITY || (mb - m) * mul > 8.f)) {
+            f = ex2((m - mb) * mul);   // 0 from m = -inf
+            m = mb;
           }
-        }
-        l *= f;
-        const float nm = m == -INFINITY ? 0.f : -m * mul;
-        float ls[2] = {0.f, 0.f};
-        uint32_t pw[32];
+          l2.x *= f;
+          l2.y *= f;
+          if (n > 1 && __any_sync(0xffffffffu, f != 1.f)) {   // the group's O so far
+#pragma unroll 1
+            for (int h = 0; h < 128; h += 16) {
+              uint32_t o[16];
+              fa::tmem_ld16(tO + h, o);
+              tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float e0 = ex2(fmaf(__uint_as_float(r[i >> 4][2 * i & 31]), mul, nm));
-          const float e1 = ex2(fmaf(__uint_as_float(r[i >> 4][(2 * i & 31) + 1]), mul, nm));
-          ls[0] += e0;
-          ls[1] += e1;
-          pw[i] = pack_bf16(e0, e1);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              fa::tmem_st16(tO + h, o);
+            }
+          }
+        } else {
+          tmem_ld32(tS, ra);
+          tmem_ld32(tS + 32, rb);
+          tmem_ld_wait();
+          scores32<CAP, BIAS>(ra, 0, mask, w, sc);
+          scores32<CAP, BIAS>(rb, 32, mask, w, sc);
         }
-        l += ls[0] + ls[1];
-        // P into its buffer once the product of two blocks before has read it
-        if (!warp_wait(&c->pfree[b], (g >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
-        tmem_st32(trow + T_P + 64 * b + 32 * ch, pw);
+        __syncwarp();
+        const float nm = m == -INFINITY ? 0.f : -m * mul;
+        probs32(ra, mul, nm, pw, l2);
+        tmem_ld32(tS + 64, ra);
+        probs32(rb, mul, nm, pw + 16, l2);
+        tmem_ld32(tS + 96, rb);
+        tmem_st32(tS, pw);          // keys 0 .. 63: over scores that are in registers
+        tmem_ld_wait();
+        scores32<CAP, BIAS>(ra, 64, mask, w, sc);
+        scores32<CAP, BIAS>(rb, 96, mask, w, sc);
+        probs32(ra, mul, nm, pw, l2);
+        probs32(rb, mul, nm, pw + 16, l2);
+        __syncwarp();
+        tmem_st32(tS + 32, pw);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->pready_l[b]);
+        if (lane == 0) mbar_arrive(&c->pready_l[grp]);
       }
       if (!ok) break;
-      if (nj > 0) {
-        float lx;
-        if (!other(l, lx)) { ok = false; break; }
-        l = ch ? lx + l : l + lx;   // the same order in both warps
-        // the last product covers all earlier ones
-        if (!warp_wait(&c->pfree[(g - 1) & 1u], (g - 1) >> 1, c, p.limit_ns)) { ok = false; break; }
-        tc_fence_after();
+      if (nj <= 0) {   // rows of padding alone
+        if (vrow) {
+          if (grp == 0) p.lse[ro] = -INFINITY;
+          uint4* dst = reinterpret_cast<uint4*>(p.O + ro * p.hd + 64 * grp);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (64 * grp + 8 * k < p.hd) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
       }
-      uint32_t o[2][32];
+      g += (uint32_t)nj;
+      // join the groups: m and l of the row's other group, then 64 columns of both accumulators
+      float2* ml = reinterpret_cast<float2*>(base + O_ML) + (lu & 1u) * 256;
+      ml[grp * 128 + lrow] = make_float2(m, l2.x + l2.y);
       __syncwarp();
-      if (nj > 0) {
-        tmem_ld32(trow + T_O + 64 * ch, o[0]);
-        tmem_ld32(trow + T_O + 64 * ch + 32, o[1]);
-        tmem_ld_wait();
-        tc_fence_before();
+      if (lane == 0) mbar_arrive(&c->mlx);
+      if (!warp_wait(&c->mlx, lu, c, p.limit_ns) || !warp_wait(&c->ofull, lu, c, p.limit_ns)) { ok = false; break; }
+      tc_fence_after();
+      __syncwarp();
+      const float2 s0 = ml[lrow], s1 = ml[128 + lrow];
+      const float mm = fmaxf(s0.x, s1.x);
+      const float f0 = s0.y == 0.f ? 0.f : ex2((s0.x - mm) * mul), f1 = s1.y == 0.f ? 0.f : ex2((s1.x - mm) * mul);
+      const float l = s0.y * f0 + s1.y * f1;
+      const bool none = l == 0.f;   // a row that sees nothing (padding): 0 and -inf
+      const float inv = none ? 0.f : 1.f / l;
+      const float a0 = f0 * inv, a1 = f1 * inv;
+      if (vrow && grp == 0) p.lse[ro] = none ? -INFINITY : (mm * mul + log2f(l)) * 0.6931471805599453f;
+#pragma unroll 1
+      for (int h = 0; h < 64; h += 32) {
+        uint32_t ra[32], rb[32];
         __syncwarp();
-        if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
-      }
-      if (vrow) {
-        // a row that sees nothing (padding): 0 and -inf
-        const bool none = l == 0.f;
-        const float inv = none ? 0.f : 1.f / l;
-        if (ch == 0) p.lse[ro] = none ? -INFINITY : (m * mul + log2f(l)) * 0.6931471805599453f;
-        uint4* dst = reinterpret_cast<uint4*>(p.O + ro * p.hd + 64 * ch);
+        tmem_ld32(trow + T_O + 64 * grp + h, ra);
+        tmem_ld32(trow + T_O + 128 + 64 * grp + h, rb);
+        tmem_ld_wait();
+        if (h == 32) {   // both accumulators are in registers: the next unit may overwrite them
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
+        }
+        if (vrow) {
+          uint4* dst = reinterpret_cast<uint4*>(p.O + ro * p.hd + 64 * grp + h);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t v[4];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = none ? 0u
-                        : pack_bf16(__uint_as_float(o[k >> 2][8 * (k & 3) + 2 * i]) * inv,
-                                    __uint_as_float(o[k >> 2][8 * (k & 3) + 2 * i + 1]) * inv);
-          if (64 * ch + 8 * k < p.hd) dst[k] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int i = 0; i < 4; ++i) {
+              const int e = 8 * k + 2 * i;
+              // a group without a block for the row leaves its accumulator unset: selected out
+              const float x0 = f0 == 0.f ? 0.f : __uint_as_float(ra[e]) * a0;
+              const float x1 = f0 == 0.f ? 0.f : __uint_as_float(ra[e + 1]) * a0;
+              const float y0 = f1 == 0.f ? 0.f : __uint_as_float(rb[e]) * a1;
+              const float y1 = f1 == 0.f ? 0.f : __uint_as_float(rb[e + 1]) * a1;
+              v[i] = pack_bf16(x0 + y0, x1 + y1);
+            }
+            if (64 * grp + h + 8 * k < p.hd) dst[k] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
         }
       }
-      __syncwarp();
+      ++lu;
     }
     if (!ok) fail_o(c, p.status);
   }
@@ -467,13 +536,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 namespace {
 
-template <bool CAP, bool BIAS>
+// Largest cap that needs no running maximum: 2^x of scores within 64 log2(e) = 92 lies in
+// [2^-92, 2^92], and so do sums over any number of keys that fits; a distance bias only lowers
+// other keys than the row's own.
+constexpr float kStaticCap = 64.f;
+
+template <bool CAP, bool BIAS, bool FIXED>
 cudaError_t launch_o(const PackedArgs& a, const PackedWork& w, void* O, float* lse, cudaStream_t s) {
   using namespace tc::fo;
   static int attr_state[64] = {};
   static std::mutex mu;
   if (!tc::once_per_device(attr_state, mu, [] {
-        return cudaFuncSetAttribute(k_attn_o<CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM) ==
+        return cudaFuncSetAttribute(k_attn_o<CAP, BIAS, FIXED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM) ==
                cudaSuccess;
       }))
     return cudaErrorInvalidConfiguration;
@@ -488,17 +562,19 @@ cudaError_t launch_o(const PackedArgs& a, const PackedWork& w, void* O, float* l
       !tc::make_map_heads(&mV, a.V, a.T, a.Hkv, a.hd, 128) ||
       !tc::make_map_heads(&mVt, w.tail_kv, 128, a.Hkv, a.hd, 128))
     return cudaErrorInvalidValue;
-  const int pairs = std::min(tc::max_pairs((const void*)k_attn_o<CAP, BIAS>, SMEM, THREADS), p.n_units);
-  k_attn_o<CAP, BIAS><<<2 * pairs, THREADS, SMEM, s>>>(mQ, mK, mV, mVt, p);
+  const int pairs = std::min(tc::max_pairs((const void*)k_attn_o<CAP, BIAS, FIXED>, SMEM, THREADS), p.n_units);
+  k_attn_o<CAP, BIAS, FIXED><<<2 * pairs, THREADS, SMEM, s>>>(mQ, mK, mV, mVt, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t packed_forward(const PackedArgs& a, const PackedWork& w, void* O, float* lse, cudaStream_t s) {
+  if (a.softcap > 0.f && a.softcap <= kStaticCap)
+    return a.slopes ? launch_o<true, true, true>(a, w, O, lse, s) : launch_o<true, false, true>(a, w, O, lse, s);
   if (a.softcap > 0.f)
-    return a.slopes ? launch_o<true, true>(a, w, O, lse, s) : launch_o<true, false>(a, w, O, lse, s);
-  return a.slopes ? launch_o<false, true>(a, w, O, lse, s) : launch_o<false, false>(a, w, O, lse, s);
+    return a.slopes ? launch_o<true, true, false>(a, w, O, lse, s) : launch_o<true, false, false>(a, w, O, lse, s);
+  return a.slopes ? launch_o<false, true, false>(a, w, O, lse, s) : launch_o<false, false, false>(a, w, O, lse, s);
 }
 
 }  // namespace sbp

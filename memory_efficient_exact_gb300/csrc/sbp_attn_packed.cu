@@ -20,6 +20,10 @@ struct KvParams {
   const PackedKvUnit* units;
   const int32_t* tail;
   __nv_bfloat16 *dK, *dV;
+  // parts > 1: the query heads of a group are shared out to `parts` units of `per_part` heads,
+  // which leave fp32 sums in part_k, part_v [parts, Hkv, T, hd]
+  int parts, per_part;
+  float *part_k, *part_v;
   int32_t* status;
   uint64_t limit_ns;
 };
@@ -70,11 +74,18 @@ struct PackedScores {
   static constexpr bool kAddOut = false;
   using Scale = ScaleZ;
 
-  static __device__ __forceinline__ void kv_unit(const Kv& p, int u, int& zk, int& kp, int& b0, int& nbl) {
-    const int i = u / p.Hkv;
-    zk = u - i * p.Hkv;
-    const int4 w = *reinterpret_cast<const int4*>(p.units + i);
-    kp = w.x; b0 = w.y; nbl = w.z;
+  static __device__ __forceinline__ int next_unit(int t, int pid, int npairs) { return pk::next_unit(t, pid, npairs); }
+  static __device__ __forceinline__ void kv_unit(const Kv& p, int u, fa::KvUnit& w) {
+    const int planes = p.parts * p.Hkv, i = u / planes;
+    w.plane = u - i * planes;
+    const int part = w.plane / p.Hkv, h0 = part * p.per_part;
+    w.zk = w.plane - part * p.Hkv;
+    const int4 v = *reinterpret_cast<const int4*>(p.units + i);
+    w.kp = v.x;
+    w.b0 = v.y;
+    w.nbl = v.z;
+    w.z0 = w.zk * p.group + h0;
+    w.nh = min(p.per_part, p.group - h0);
   }
   static __device__ __forceinline__ void key_range(const Kv& p, int key, int& lo, int& hi) {
     lo = key < p.T ? p.qlo[key] : p.T;
@@ -126,18 +137,30 @@ struct PackedScores {
   static __device__ __forceinline__ float grad(float p, float d, float dc) { return CAP ? p * d * dc : p * d; }
 
   // 64 columns of dV (t = 0) or dK (t = 1) of one key
-  static __device__ __forceinline__ void store_out(const Kv& p, int t, int zk, int key, int c,
+  static __device__ __forceinline__ void store_out(const Kv& p, int t, int plane, int key, int c,
                                                    const uint32_t (&ra)[2][32]) {
     if (key >= p.T) return;
-    __nv_bfloat16* row = (t ? p.dK : p.dV) + ((int64_t)zk * p.T + key) * p.hd;
+    const int64_t row = ((int64_t)plane * p.T + key) * p.hd;
     const float f = t ? p.scale : 1.f;
-    store_row(row, p.hd, c, ra[0], f);
-    store_row(row, p.hd, c + 32, ra[1], f);
+    if (p.parts == 1) {
+      __nv_bfloat16* o = (t ? p.dK : p.dV) + row;
+      store_row(o, p.hd, c, ra[0], f);
+      store_row(o, p.hd, c + 32, ra[1], f);
+      return;
+    }
+    float4* o = reinterpret_cast<float4*>((t ? p.part_k : p.part_v) + row + c);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + 32 * h + 4 * k < p.hd)
+          o[8 * h + k] = make_float4(__uint_as_float(ra[h][4 * k]) * f, __uint_as_float(ra[h][4 * k + 1]) * f,
+                                     __uint_as_float(ra[h][4 * k + 2]) * f, __uint_as_float(ra[h][4 * k + 3]) * f);
   }
-  static __device__ __forceinline__ void store_zero(const Kv& p, int zk, int key, int c) {
+  static __device__ __forceinline__ void store_zero(const Kv& p, int plane, int key, int c) {
     const uint32_t z[2][32] = {};
-    store_out(p, 0, zk, key, c, z);
-    store_out(p, 1, zk, key, c, z);
+    store_out(p, 0, plane, key, c, z);
+    store_out(p, 1, plane, key, c, z);
   }
   // 32 columns of dQ of one query (row ro of [H, T])
   static __device__ __forceinline__ void store_dq(const Q& p, int64_t ro, int c, const uint32_t (&ra)[32]) {
@@ -339,6 +362,24 @@ __global__ void __launch_bounds__(PREP_THREADS) k_packed_prep(const PrepP p) {
   if (r < p.rows && c == 0) p.D[r] = acc;
 }
 
+// dK and dV from the parts' fp32 sums, in the parts' order: eight elements a thread.
+__global__ void __launch_bounds__(256) k_packed_join(const float* __restrict__ pk, const float* __restrict__ pv, int parts,
+                                                     int64_t n, __nv_bfloat16* __restrict__ dK,
+                                                     __nv_bfloat16* __restrict__ dV) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  const float* src = blockIdx.y ? pv : pk;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  for (int k = 0; k < parts; ++k) {
+    const float4* q = reinterpret_cast<const float4*>(src + (int64_t)k * n + i);
+    const float4 x = q[0], y = q[1];
+    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+  }
+  *reinterpret_cast<uint4*>((blockIdx.y ? dV : dK) + i) =
+      make_uint4(pack2(a.x, a.y), pack2(a.z, a.w), pack2(b.x, b.y), pack2(b.z, b.w));
+}
+
 }  // namespace pk
 }  // namespace tc
 
@@ -348,7 +389,8 @@ namespace {
 
 struct PackedLayout {
   size_t off_lo = 0, off_hi = 0, off_qlo = 0, off_qhi = 0, off_qraw = 0, off_qunits = 0, off_kvraw = 0,
-         off_kvunits = 0, off_tail = 0, off_tq = 0, off_to = 0, off_tkv = 0, off_d = 0, total = 0;
+         off_kvunits = 0, off_tail = 0, off_tq = 0, off_to = 0, off_tkv = 0, off_d = 0, off_pk = 0, off_pv = 0, total = 0;
+  int parts = 1, per_part = 1;   // of the backward's query-head groups (k_attn_kv)
   Guards guards;   // checked build only
 };
 
@@ -359,6 +401,21 @@ bool packed_shape(int64_t H, int64_t Hkv, int64_t T, int64_t hd) {
 bool packed_supported(int64_t H, int64_t T, int64_t hd) {
   return hd % 8 == 0 && hd <= 128 && T <= (int64_t)1 << 30 && H <= (int64_t)1 << 20 &&
          H * ((T + 255) / 256) <= INT32_MAX / 2 && (H * T + 15) / 16 + T / 256 < INT32_MAX / 2;
+}
+
+// Query heads of a group that one k_attn_kv unit walks.  All of them where that leaves enough
+// units for the SM pairs (a key's dK and dV are then summed on chip); fewer where key / value
+// heads are few and documents long, the sums joined by k_packed_join.
+int kv_heads_per_part(int64_t H, int64_t Hkv, int64_t T) {
+  const int64_t group = H / Hkv, n = (T + 255) / 256, pairs = std::max(1, num_sms() / 2);
+#ifndef KVU
+#define KVU 4
+#define KVT 512
+#endif
+  const int64_t want = KVU * pairs;
+  if (T < KVT || n * Hkv >= want || group == 1) return (int)group;
+  const int64_t parts = std::min(group, (want + n * Hkv - 1) / (n * Hkv));
+  return (int)((group + parts - 1) / parts);
 }
 
 bool packed_layout(int64_t H, int64_t Hkv, int64_t T, int64_t hd, PackedLayout* L) {
@@ -379,6 +436,12 @@ bool packed_layout(int64_t H, int64_t Hkv, int64_t T, int64_t hd, PackedLayout* 
   l.off_to = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
   l.off_tkv = take_region(o, (size_t)Hkv * 128 * hd * 2, l.guards);
   l.off_d = take_region(o, (size_t)H * t * sizeof(float), l.guards);
+  l.per_part = kv_heads_per_part(H, Hkv, T);
+  l.parts = (int)((H / Hkv + l.per_part - 1) / l.per_part);
+  if (l.parts > 1) {
+    l.off_pk = take_region(o, (size_t)l.parts * Hkv * t * hd * sizeof(float), l.guards);
+    l.off_pv = take_region(o, (size_t)l.parts * Hkv * t * hd * sizeof(float), l.guards);
+  }
   l.total = o;
   *L = l;
   return true;
@@ -458,8 +521,9 @@ cudaError_t packed_prep(const PackedArgs& a, const PackedLayout& L, char* w, boo
 }
 
 template <bool CAP, bool BIAS>
-cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedWork& w, void* dQ, void* dK, void* dV,
-                                    cudaStream_t s) {
+cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedLayout& L, char* base, void* dQ, void* dK,
+                                    void* dV, cudaStream_t s) {
+  const PackedWork w = packed_work(L, base);
   using namespace tc::fa;
   using S = tc::pk::PackedScores<CAP, BIAS>;
   static int attr_state[64] = {};
@@ -488,13 +552,20 @@ cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedWork& w, vo
   mq.m[Q_MKB] = mk.m[KV_MK];
   tc::pk::KvParams k;
   k.H = (int)a.H; k.Hkv = (int)a.Hkv; k.T = (int)a.T; k.c0 = 0; k.c1 = (int)a.T; k.hd = (int)a.hd;
-  k.group = (int)(a.H / a.Hkv); k.n_units = n * k.Hkv;
+  k.group = (int)(a.H / a.Hkv); k.n_units = n * k.Hkv * L.parts;
+  k.parts = L.parts; k.per_part = L.per_part;
+  k.part_k = reinterpret_cast<float*>(base + L.off_pk); k.part_v = reinterpret_cast<float*>(base + L.off_pv);
   k.scale = a.scale; k.sc = tc::pk::make_scale(a.scale, a.softcap);
   k.slopes = a.slopes; k.lse = a.lse; k.D = w.D; k.qlo = w.qlo; k.qhi = w.qhi; k.units = w.kvunits; k.tail = w.tail;
   k.dK = static_cast<__nv_bfloat16*>(dK); k.dV = static_cast<__nv_bfloat16*>(dV);
   k.status = a.status; k.limit_ns = tc::wait_limit_ns();
   const int kv_pairs = std::min(tc::max_pairs((const void*)k_attn_kv<S>, SMEM_KV, KV_THREADS), k.n_units);
   k_attn_kv<S><<<2 * kv_pairs, KV_THREADS, SMEM_KV, s>>>(mk, k);
+  if (L.parts > 1) {
+    const int64_t m = a.Hkv * a.T * a.hd;
+    tc::pk::k_packed_join<<<dim3((unsigned)((m / 8 + 255) / 256), 2), 256, 0, s>>>(k.part_k, k.part_v, L.parts, m, k.dK,
+                                                                                  k.dV);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   tc::pk::QParams q;
@@ -560,18 +631,17 @@ int sbp_attn_packed_backward(const void* Q, const void* K, const void* V, const 
     set_launch_count(0);
     return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? SBP_OK : SBP_ERR_CUDA;
   }
-  int launches = 3;
+  int launches = L.parts > 1 ? 4 : 3;
   int st = workspace_guards(w, L.guards, 0, dev_status, s, &launches);
   if (st != SBP_OK) return st;
   if (packed_prep(a, L, w, true, s) != cudaSuccess) return SBP_ERR_CUDA;
-  const PackedWork k = packed_work(L, w);
   cudaError_t e;
   if (softcap > 0.f)
-    e = slopes ? packed_backward_kernels<true, true>(a, k, dQ, dK, dV, s)
-               : packed_backward_kernels<true, false>(a, k, dQ, dK, dV, s);
+    e = slopes ? packed_backward_kernels<true, true>(a, L, w, dQ, dK, dV, s)
+               : packed_backward_kernels<true, false>(a, L, w, dQ, dK, dV, s);
   else
-    e = slopes ? packed_backward_kernels<false, true>(a, k, dQ, dK, dV, s)
-               : packed_backward_kernels<false, false>(a, k, dQ, dK, dV, s);
+    e = slopes ? packed_backward_kernels<false, true>(a, L, w, dQ, dK, dV, s)
+               : packed_backward_kernels<false, false>(a, L, w, dQ, dK, dV, s);
   if (e != cudaSuccess) return SBP_ERR_CUDA;
   st = workspace_guards(w, L.guards, 1, dev_status, s, &launches);
   if (st == SBP_OK) set_launch_count(launches);

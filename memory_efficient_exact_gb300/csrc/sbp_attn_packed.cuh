@@ -53,6 +53,12 @@ struct PackedArgs {
 namespace tc {
 namespace pk {
 
+// The unit of round t of SM pair pid: the units come longest first, so the rounds alternate
+// in direction, which evens out what the pairs get.
+__device__ __forceinline__ int next_unit(int t, int pid, int npairs) {
+  return (t & 1) ? (t + 1) * npairs - 1 - pid : t * npairs + pid;
+}
+
 // Constants of the score in log2 units.  x log2(e) = s sl2 without a cap; with one,
 // c tanh(y) = c - 2 c / (1 + e^(2 y)), y = s scale / c: one exponential and one reciprocal,
 // the absolute error about c 2^-22 (tanh.approx would leave c 2^-11).
