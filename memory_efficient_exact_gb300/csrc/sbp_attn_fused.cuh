@@ -170,6 +170,10 @@ __device__ __forceinline__ bool warp_wait_n(uint64_t* b, uint32_t& seen, uint32_
   return true;
 }
 
+__device__ __forceinline__ bool warp_wait_f(uint64_t* b, uint32_t parity, CtrlF* c, uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_inl<false>(b, parity, &c->abort, limit));
+}
+
 // The forwarder: for block g, waits for the CTA's 8 epilogue warps on tempty_l, then on
 // oready_l, and passes each on to the leader's barrier.
 __device__ __forceinline__ bool forward_block(CtrlF* c, uint32_t g, uint32_t& te_seen, uint32_t& or_seen,
@@ -411,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   CtrlF* c = reinterpret_cast<CtrlF*>(base + KV_CTRL);
   const uint32_t sb = saddr(base);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform_warp(), lane = threadIdx.x % 32;
   const uint32_t rank = ctarank();
   prologue_f(c, warp, KV_EPI);
   const uint32_t tmem = c->tmem_base;
@@ -507,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {   // the whole warp, converged; one elected lane issues
       int sa = 0, lu = 0;
       uint32_t pha = 0, phb = 0, phr = 0, tempty_seen = 0, oready_seen = 0, acc_seen = 0, g = 0;
       bool ok = true;
@@ -516,21 +520,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
                      dDST = sw128_desc(sb + KV_DST, 16, 1024), dBm = sw128_desc(sb + KV_B, 16384, 1024);
       // dV += P^T dO and dK += dS^T Q for global block gg (the first of its unit overwrites)
       auto accumulate = [&](uint32_t gg, bool first) -> bool {
-        if (!wait_n(&c->oready, oready_seen, gg + 1, c, p.limit_ns)) return false;
-        if (!wait_inl<false>(&c->bfull[0], phb, &c->abort, p.limit_ns)) return false;
+        if (!warp_wait_n(&c->oready, oready_seen, gg + 1, c, p.limit_ns)) return false;
+        if (!warp_wait_f(&c->bfull[0], phb, c, p.limit_ns)) return false;
         phb ^= 1u;
-        if (first && !wait_n(&c->accempty, acc_seen, (uint32_t)lu, c, p.limit_ns)) return false;
+        if (first && !warp_wait_n(&c->accempty, acc_seen, (uint32_t)lu, c, p.limit_ns)) return false;
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma2_bf16(tmem + 256, dplus(dPT, (k >> 2) * 16384 + (k & 3) * 32), dplus(dBm, 16384 + k * 2048), IDESC_KM,
-                    (!first || k) ? 1u : 0u);
+          for (int k = 0; k < 8; ++k)
+            mma2_bf16(tmem + 256, dplus(dPT, (k >> 2) * 16384 + (k & 3) * 32), dplus(dBm, 16384 + k * 2048), IDESC_KM,
+                      (!first || k) ? 1u : 0u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma2_bf16(tmem + 384, dplus(dDST, (k >> 2) * 16384 + (k & 3) * 32), dplus(dBm, k * 2048), IDESC_KM,
-                    (!first || k) ? 1u : 0u);
-        commit2_mc(&c->bempty[0], 3);
-        commit2_mc(&c->ofree, 3);
+          for (int k = 0; k < 8; ++k)
+            mma2_bf16(tmem + 384, dplus(dDST, (k >> 2) * 16384 + (k & 3) * 32), dplus(dBm, k * 2048), IDESC_KM,
+                      (!first || k) ? 1u : 0u);
+          commit2_mc(&c->bempty[0], 3);
+          commit2_mc(&c->ofree, 3);
+        }
+        __syncwarp();
         return true;
       };
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
@@ -538,27 +545,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         S::kv_unit(p, u, w);
         const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
-        if (!wait_inl<false>(&c->rfull, phr, &c->abort, p.limit_ns)) { ok = false; break; }
+        if (!warp_wait_f(&c->rfull, phr, c, p.limit_ns)) { ok = false; break; }
         phr ^= 1u;
         tc_fence_after();
         for (int n = 0; n < nblk; ++n, ++g) {
           // S^T and dP^T of block g; the previous block's accumulation follows, so the
           // epilogue's work on block g overlaps it
-          if (!wait_n(&c->tempty, tempty_seen, g, c, p.limit_ns)) { ok = false; break; }
-          if (!wait_inl<false>(&c->afull[sa], pha, &c->abort, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_n(&c->tempty, tempty_seen, g, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_f(&c->afull[sa], pha, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
           const uint64_t dst = dplus(dA, sa * KV_A_STAGE);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma2_bf16(tmem, dplus(dK, (k >> 2) * 16384 + (k & 3) * 32), dplus(dst, (k >> 2) * 8192 + (k & 3) * 32),
-                      IDESC_KK, k ? 1u : 0u);
+            for (int k = 0; k < 8; ++k)
+              mma2_bf16(tmem, dplus(dK, (k >> 2) * 16384 + (k & 3) * 32), dplus(dst, (k >> 2) * 8192 + (k & 3) * 32),
+                        IDESC_KK, k ? 1u : 0u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma2_bf16(tmem + 128, dplus(dV, (k >> 2) * 16384 + (k & 3) * 32),
-                      dplus(dst, 16384 + (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
-          commit2_mc(&c->aempty[sa], 3);
-          commit2_mc(&c->tfull, 3);
-          if (n == nblk - 1) commit2_mc(&c->rempty, 3);
+            for (int k = 0; k < 8; ++k)
+              mma2_bf16(tmem + 128, dplus(dV, (k >> 2) * 16384 + (k & 3) * 32),
+                        dplus(dst, 16384 + (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+            commit2_mc(&c->aempty[sa], 3);
+            commit2_mc(&c->tfull, 3);
+            if (n == nblk - 1) commit2_mc(&c->rempty, 3);
+          }
+          __syncwarp();
           if (++sa == 2) { sa = 0; pha ^= 1u; }
           if (n >= 1 && !accumulate(g - 1, n == 1)) { ok = false; break; }
         }
@@ -566,8 +576,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         if (!accumulate(g - 1, nblk == 1)) { ok = false; break; }
         ++lu;
       }
-      if (!ok) fail_f(c, p.status);
-      commit2_mc(&c->mdone, 1);
+      if (elect_one()) {
+        if (!ok) fail_f(c, p.status);
+        commit2_mc(&c->mdone, 1);
+      }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
     }
     __syncwarp();
@@ -791,7 +803,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   CtrlF* c = reinterpret_cast<CtrlF*>(base + Q_CTRL);
   const uint32_t sb = saddr(base);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform_warp(), lane = threadIdx.x % 32;
   const uint32_t rank = ctarank();
   prologue_f(c, warp, Q_EPI);
   const uint32_t tmem = c->tmem_base;
@@ -881,7 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {   // the whole warp, converged; one elected lane issues
       int sa = 0, sy = 0, lu = 0;
       uint32_t pha = 0, phy = 0, phr = 0, tempty_seen = 0, oready_seen = 0, acc_seen = 0, g = 0;
       bool ok = true;
@@ -889,17 +901,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
                      dX = sw128_desc(sb + Q_X, 16, 1024), dY = sw128_desc(sb + Q_Y, 16384, 1024);
       // dQ += dS K for global key block gg (the first of its unit overwrites)
       auto accumulate = [&](uint32_t gg, bool first) -> bool {
-        if (!wait_n(&c->oready, oready_seen, gg + 1, c, p.limit_ns)) return false;
-        if (!wait_inl<false>(&c->bfull[sy], phy, &c->abort, p.limit_ns)) return false;
-        if (first && !wait_n(&c->accempty, acc_seen, (uint32_t)lu, c, p.limit_ns)) return false;
+        if (!warp_wait_n(&c->oready, oready_seen, gg + 1, c, p.limit_ns)) return false;
+        if (!warp_wait_f(&c->bfull[sy], phy, c, p.limit_ns)) return false;
+        if (first && !warp_wait_n(&c->accempty, acc_seen, (uint32_t)lu, c, p.limit_ns)) return false;
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma2_bf16_ts(tmem + 256, tmem + Q_TDS + 64 * (gg & 1) + 8 * k,
-                       dplus(dY, sy * Q_Y_STAGE + k * 2048), IDESC_KM,
-                       (!first || k) ? 1u : 0u);
-        commit2_mc(&c->bempty[sy], 3);
-        commit2_mc(&c->dsfree[gg & 1], 3);
+          for (int k = 0; k < 8; ++k)
+            mma2_bf16_ts(tmem + 256, tmem + Q_TDS + 64 * (gg & 1) + 8 * k,
+                         dplus(dY, sy * Q_Y_STAGE + k * 2048), IDESC_KM,
+                         (!first || k) ? 1u : 0u);
+          commit2_mc(&c->bempty[sy], 3);
+          commit2_mc(&c->dsfree[gg & 1], 3);
+        }
+        __syncwarp();
         if (++sy == 2) { sy = 0; phy ^= 1u; }
         return true;
       };
@@ -907,25 +922,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
         if (nj == 0) continue;
-        if (!wait_inl<false>(&c->rfull, phr, &c->abort, p.limit_ns)) { ok = false; break; }
+        if (!warp_wait_f(&c->rfull, phr, c, p.limit_ns)) { ok = false; break; }
         phr ^= 1u;
         tc_fence_after();
         for (int n = 0; n < nj; ++n, ++g) {
-          if (!wait_n(&c->tempty, tempty_seen, g, c, p.limit_ns)) { ok = false; break; }
-          if (!wait_inl<false>(&c->afull[sa], pha, &c->abort, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_n(&c->tempty, tempty_seen, g, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_f(&c->afull[sa], pha, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
           const uint64_t dst = dplus(dX, sa * Q_X_STAGE);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma2_bf16(tmem, dplus(dQd, (k >> 2) * 16384 + (k & 3) * 32), dplus(dst, (k >> 2) * 8192 + (k & 3) * 32),
-                      IDESC_KK, k ? 1u : 0u);
+            for (int k = 0; k < 8; ++k)
+              mma2_bf16(tmem, dplus(dQd, (k >> 2) * 16384 + (k & 3) * 32), dplus(dst, (k >> 2) * 8192 + (k & 3) * 32),
+                        IDESC_KK, k ? 1u : 0u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma2_bf16(tmem + 128, dplus(dOd, (k >> 2) * 16384 + (k & 3) * 32),
-                      dplus(dst, 16384 + (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
-          commit2_mc(&c->aempty[sa], 3);
-          commit2_mc(&c->tfull, 3);
-          if (n == nj - 1) commit2_mc(&c->rempty, 3);
+            for (int k = 0; k < 8; ++k)
+              mma2_bf16(tmem + 128, dplus(dOd, (k >> 2) * 16384 + (k & 3) * 32),
+                        dplus(dst, 16384 + (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+            commit2_mc(&c->aempty[sa], 3);
+            commit2_mc(&c->tfull, 3);
+            if (n == nj - 1) commit2_mc(&c->rempty, 3);
+          }
+          __syncwarp();
           if (++sa == 2) { sa = 0; pha ^= 1u; }
           if (n >= 1 && !accumulate(g - 1, n == 1)) { ok = false; break; }
         }
@@ -933,8 +951,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         if (!accumulate(g - 1, nj == 1)) { ok = false; break; }
         ++lu;
       }
-      if (!ok) fail_f(c, p.status);
-      commit2_mc(&c->mdone, 1);
+      if (elect_one()) {
+        if (!ok) fail_f(c, p.status);
+        commit2_mc(&c->mdone, 1);
+      }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
     }
     __syncwarp();
