@@ -63,20 +63,29 @@ constexpr uint32_t KV_A_STAGE = 32768;
 constexpr uint32_t KV_B = 131072;     // Q then dO of the block, 128 queries x this CTA's 64 of hd
 constexpr uint32_t KV_PT = 163840;    // P^T  [2 query halves][128 keys][128 B]
 constexpr uint32_t KV_DST = 196608;   // dS^T [2 query halves][128 keys][128 B]
-constexpr uint32_t KV_LD = 229376;    // lse * log2(e) [128], then D [128], of the block's queries
+constexpr uint32_t KV_LD = 229376;    // -lse * log2(e) [128], then -D [128], of the block's queries
 constexpr uint32_t KV_CTRL = 230400;
 
-// Shared memory of k_attn_q.
-constexpr uint32_t Q_Q = 0;           // Q rows of the unit (this CTA's 128 queries x 128)
-constexpr uint32_t Q_DO = 32768;      // dO rows
-constexpr uint32_t Q_X = 65536;       // 2 stages: K then V of the key block, this CTA's 64 keys x 128
-constexpr uint32_t Q_X_STAGE = 32768;
-constexpr uint32_t Q_Y = 131072;      // 2 stages: K of the key block, 128 keys x this CTA's 64 of hd
-constexpr uint32_t Q_Y_STAGE = 16384;
-constexpr uint32_t Q_CTRL = 163840;
-// Tensor memory of k_attn_q: S [0, 128), dP [128, 256), dQ [256, 384), and two bf16 dS
-// buffers of 64 columns (128 keys) at Q_TDS and Q_TDS + 64: the A operand of dQ += dS K.
-constexpr uint32_t Q_TDS = 384;
+// Shared memory of k_attn_q: Q and dO of two units, two stages of each key-block operand.
+constexpr uint32_t Q_R = 0;           // Q then dO rows of the unit (this CTA's 128 queries x 128 each)
+constexpr uint32_t Q_K = 131072;      // K of the key block, this CTA's 64 keys x 128 (B of S)
+constexpr uint32_t Q_V = 163840;      // V of the key block, likewise (B of dP)
+constexpr uint32_t Q_Y = 196608;      // K of the key block, 128 keys x this CTA's 64 of hd (B of dQ)
+constexpr uint32_t Q_CTRL = 229376;
+// Tensor memory of k_attn_q: two S buffers (dS over them), dP, dQ.
+constexpr uint32_t QT_DP = 256, QT_DQ = 384;
+
+struct CtrlQ {
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], yfull[2], yempty[2];
+  uint64_t rfull[2], rempty[2];   // the unit's Q and dO
+  uint64_t tfull, tempty;         // S and dP of the block are ready; dP has been read (leader, one per CTA)
+  uint64_t oready[2];             // dS buffer is written (leader, one per CTA)
+  uint64_t tempty_l, oready_l[2]; // the CTA's epilogue warps, forwarded
+  uint64_t dqfull, accempty;      // the unit's dQ is complete; has been read out (leader)
+  uint64_t mdone;
+  uint32_t tmem_base;
+  int abort;
+};
 
 struct CtrlF {
   uint64_t afull[2], aempty[2];  // ring of the S / dP B operands
@@ -85,7 +94,6 @@ struct CtrlF {
   uint64_t tfull, tempty;        // S and dP accumulators (tempty: leader, one arrival per CTA)
   uint64_t oready, ofree;        // P^T, dS^T (or dS) in shared memory (oready: leader, one per CTA)
   uint64_t tempty_l, oready_l;   // the CTA's epilogue warps, forwarded to tempty / oready
-  uint64_t dsfree[2];            // k_attn_q: the dQ GEMM has read dS buffer 0 / 1 (tensor memory)
   uint64_t accempty;             // the unit's accumulators have been read out
   uint64_t lfull, lempty;        // lse / D of the block (k_attn_kv)
   uint64_t sfree;                // the dV / dK staging has left shared memory (k_attn_kv)
@@ -95,10 +103,24 @@ struct CtrlF {
 };
 
 constexpr size_t SMEM_KV = KV_CTRL + sizeof(CtrlF) + 1024;
-constexpr size_t SMEM_Q = Q_CTRL + sizeof(CtrlF) + 1024;
-static_assert(SMEM_KV <= 232448, "k_attn_kv shared memory");
+constexpr size_t SMEM_Q = Q_CTRL + sizeof(CtrlQ) + 1024;
+static_assert(SMEM_KV <= 232448 && SMEM_Q <= 232448, "shared memory of one CTA");
 
-__device__ __forceinline__ void prologue_f(CtrlF* c, int warp, int epi) {
+// Tensor memory and the barriers visible to the pair.
+template <class C>
+__device__ __forceinline__ void prologue_end(C* c, int warp) {
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&c->tmem_base)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+}
+__device__ __forceinline__ void prologue_f(CtrlF* c, int warp) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->afull[i], 1);
@@ -111,32 +133,47 @@ __device__ __forceinline__ void prologue_f(CtrlF* c, int warp, int epi) {
     mbar_init(&c->tfull, 1);
     mbar_init(&c->tempty, 2);
     mbar_init(&c->oready, 2);
-    mbar_init(&c->tempty_l, epi);
-    mbar_init(&c->oready_l, epi);
+    mbar_init(&c->tempty_l, KV_EPI);
+    mbar_init(&c->oready_l, KV_EPI);
     mbar_init(&c->ofree, 1);
-    mbar_init(&c->dsfree[0], 1);
-    mbar_init(&c->dsfree[1], 1);
-    mbar_init(&c->accempty, 2 * epi);
+    mbar_init(&c->accempty, 2 * KV_EPI);
     mbar_init(&c->lfull, 1);
-    mbar_init(&c->lempty, epi);
-    mbar_init(&c->sfree, epi);
+    mbar_init(&c->lempty, KV_EPI);
+    mbar_init(&c->sfree, KV_EPI);
     mbar_init(&c->mdone, 1);
     c->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&c->tmem_base)),
-                 "r"(TMEM_COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  prologue_end(c, warp);
+}
+__device__ __forceinline__ void prologue_q(CtrlQ* c, int warp) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c->kfull[i], 1);
+      mbar_init(&c->kempty[i], 1);
+      mbar_init(&c->vfull[i], 1);
+      mbar_init(&c->vempty[i], 1);
+      mbar_init(&c->yfull[i], 1);
+      mbar_init(&c->yempty[i], 1);
+      mbar_init(&c->rfull[i], 1);
+      mbar_init(&c->rempty[i], 1);
+      mbar_init(&c->oready[i], 2);
+      mbar_init(&c->oready_l[i], Q_EPI);
+    }
+    mbar_init(&c->tfull, 1);
+    mbar_init(&c->tempty, 2);
+    mbar_init(&c->tempty_l, Q_EPI);
+    mbar_init(&c->dqfull, 1);
+    mbar_init(&c->accempty, 2 * Q_EPI);
+    mbar_init(&c->mdone, 1);
+    c->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
-  tc_fence_after();
+  prologue_end(c, warp);
 }
 
-__device__ __forceinline__ void teardown_f(CtrlF* c, int warp) {
+template <class C>
+__device__ __forceinline__ void teardown_f(C* c, int warp) {
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -147,14 +184,16 @@ __device__ __forceinline__ void teardown_f(CtrlF* c, int warp) {
   }
 }
 
-__device__ __forceinline__ void fail_f(CtrlF* c, int32_t* status) {
+template <class C>
+__device__ __forceinline__ void fail_f(C* c, int32_t* status) {
   *(volatile int*)&c->abort = 1;
   if (status) atomicCAS(status, 0, SBP_ERR_TIMEOUT);
 }
 
 // Waits until barrier b has completed `need` phases; `seen` counts the phases this
 // thread already waited for.  Bounded like every other wait.
-__device__ __forceinline__ bool wait_n(uint64_t* b, uint32_t& seen, uint32_t need, CtrlF* c, uint64_t limit) {
+template <class C>
+__device__ __forceinline__ bool wait_n(uint64_t* b, uint32_t& seen, uint32_t need, C* c, uint64_t limit) {
   while (seen < need) {
     if (!wait_inl<true>(b, seen & 1u, &c->abort, limit)) return false;
     ++seen;
@@ -162,7 +201,8 @@ __device__ __forceinline__ bool wait_n(uint64_t* b, uint32_t& seen, uint32_t nee
   return true;
 }
 // The same for a whole warp (seen and need are warp-uniform).
-__device__ __forceinline__ bool warp_wait_n(uint64_t* b, uint32_t& seen, uint32_t need, CtrlF* c, uint64_t limit) {
+template <class C>
+__device__ __forceinline__ bool warp_wait_n(uint64_t* b, uint32_t& seen, uint32_t need, C* c, uint64_t limit) {
   while (seen < need) {
     if (!__all_sync(0xffffffffu, wait_inl<true>(b, seen & 1u, &c->abort, limit))) return false;
     ++seen;
@@ -170,8 +210,19 @@ __device__ __forceinline__ bool warp_wait_n(uint64_t* b, uint32_t& seen, uint32_
   return true;
 }
 
-__device__ __forceinline__ bool warp_wait_f(uint64_t* b, uint32_t parity, CtrlF* c, uint64_t limit) {
-  return __all_sync(0xffffffffu, wait_inl<false>(b, parity, &c->abort, limit));
+// One phase, by its parity: of a barrier that only this CTA or the tensor pipe completes
+// (_f), or that the pair's other CTA may complete (_c).
+template <class C>
+__device__ __forceinline__ bool warp_wait_f(uint64_t* b, uint32_t parity, C* c, uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_inl<false>(b, parity & 1u, &c->abort, limit));
+}
+template <class C>
+__device__ __forceinline__ bool wait_c(uint64_t* b, uint32_t parity, C* c, uint64_t limit) {
+  return wait_inl<true>(b, parity & 1u, &c->abort, limit);
+}
+template <class C>
+__device__ __forceinline__ bool warp_wait_c(uint64_t* b, uint32_t parity, C* c, uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_c(b, parity, c, limit));
 }
 
 // The forwarder: for block g, waits for the CTA's 8 epilogue warps on tempty_l, then on
@@ -258,34 +309,28 @@ template <class S, bool MASK>
 __device__ __forceinline__ void kv_round(const uint32_t (&rs)[32], const uint32_t (&rd)[32], int j0,
                                          const float* lds, const typename S::Scale& sc, int qg, int key, int lo,
                                          int hi, uint32_t* pw, uint32_t* dw) {
-  const float4* l4 = reinterpret_cast<const float4*>(lds);
-  const float4* d4 = reinterpret_cast<const float4*>(lds + 128);
+  const float4* l4 = reinterpret_cast<const float4*>(lds);         // - lse log2 e
+  const float4* d4 = reinterpret_cast<const float4*>(lds + 128);   // - D
 #pragma unroll
   for (int j4 = 0; j4 < 4; ++j4) {
     const float4 L = l4[j4], Dv = d4[j4];
-    const float lz[4] = {L.x, L.y, L.z, L.w}, dz[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
-    float pv[4], sv[4], dc[4];
 #pragma unroll
     for (int e = 0; e < 4; e += 2) {
-      const int j = j0 + 4 * j4 + e;
-      const float2 pp = exp2_pair(S::log2p(sc, __uint_as_float(rs[j]), lz[e], qg + 4 * j4 + e - key, dc[e]),
-                                  S::log2p(sc, __uint_as_float(rs[j + 1]), lz[e + 1], qg + 4 * j4 + e + 1 - key,
-                                           dc[e + 1]));
-      pv[e] = pp.x;
-      pv[e + 1] = pp.y;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
       const int j = 4 * j4 + e;
-      const bool out = MASK && (qg + j < lo || qg + j >= hi);
-      if (out) pv[e] = 0.f;
-      sv[e] = S::grad(pv[e], __uint_as_float(rd[j0 + j]) - dz[e], dc[e]);
-      if (S::kClearMasked && out) sv[e] = 0.f;
+      float2 dc;
+      const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[j0 + j]), __uint_as_float(rs[j0 + j + 1])),
+                                 e ? make_float2(L.z, L.w) : make_float2(L.x, L.y), qg + j - key, 1, dc);
+      float2 pp = exp2_pair(x.x, x.y);
+      const bool o0 = MASK && (qg + j < lo || qg + j >= hi), o1 = MASK && (qg + j + 1 < lo || qg + j + 1 >= hi);
+      if (o0) pp.x = 0.f;
+      if (o1) pp.y = 0.f;
+      float2 sv = S::grad2(pp, add2(make_float2(__uint_as_float(rd[j0 + j]), __uint_as_float(rd[j0 + j + 1])),
+                                    e ? make_float2(Dv.z, Dv.w) : make_float2(Dv.x, Dv.y)), dc);
+      if (S::kClearMasked && o0) sv.x = 0.f;
+      if (S::kClearMasked && o1) sv.y = 0.f;
+      pw[j / 2] = pack_bf16(pp.x, pp.y);
+      dw[j / 2] = pack_bf16(sv.x, sv.y);
     }
-    pw[2 * j4] = pack_bf16(pv[0], pv[1]);
-    pw[2 * j4 + 1] = pack_bf16(pv[2], pv[3]);
-    dw[2 * j4] = pack_bf16(sv[0], sv[1]);
-    dw[2 * j4 + 1] = pack_bf16(sv[2], sv[3]);
   }
 }
 
@@ -390,13 +435,14 @@ struct CausalScores {
 
   template <class P>
   static __device__ __forceinline__ Scale scale_of(const P& p, int) { return p.scale * L2E; }
-  // log2 of a probability from a raw score s, the row's lse in log2 units and the distance
-  // query - key; dc is the factor of the score's gradient.
-  static __device__ __forceinline__ float log2p(Scale sl2, float s, float lz, int, float& dc) {
-    dc = 1.f;
-    return fmaf(s, sl2, -lz);
+  // log2 of the probabilities of two neighbouring pairs from their raw scores s, -lse in log2
+  // units and the distance query - key of the first (the second's is dist + step); dc: the
+  // factors of the scores' gradients.
+  static __device__ __forceinline__ float2 log2p2(Scale sl2, float2 s, float2 nlz, int, int, float2& dc) {
+    dc = make_float2(1.f, 1.f);
+    return fma2(s, make_float2(sl2, sl2), nlz);
   }
-  static __device__ __forceinline__ float grad(float p, float d, float) { return p * d; }
+  static __device__ __forceinline__ float2 grad2(float2 p, float2 d, float2) { return mul2(p, d); }
   template <class P>
   static __device__ __forceinline__ int tail_block(const P&) { return -1; }
 };
@@ -417,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
   const uint32_t sb = saddr(base);
   const int warp = uniform_warp(), lane = threadIdx.x % 32;
   const uint32_t rank = ctarank();
-  prologue_f(c, warp, KV_EPI);
+  prologue_f(c, warp);
   const uint32_t tmem = c->tmem_base;
   const int pid = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
@@ -599,7 +645,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == KV_LD_WARP) {
-    // lse * log2(e) and D of each block's 128 queries into shared memory (one buffer,
+    // -lse * log2(e) and -D of each block's 128 queries into shared memory (one buffer,
     // refilled once the epilogue warps have read it); loads issued a block ahead
     float* ld = reinterpret_cast<float*>(base + KV_LD);
     uint32_t lempty_seen = 0, g = 0;
@@ -623,8 +669,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         if (!warp_wait_n(&c->lempty, lempty_seen, g, c, p.limit_ns)) { ok = false; break; }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          ld[lane + 32 * i] = lv[i];
-          ld[128 + lane + 32 * i] = dv[i];
+          ld[lane + 32 * i] = -lv[i];
+          ld[128 + lane + 32 * i] = -dv[i];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->lfull);
@@ -770,29 +816,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
 
 // ===================================================================== k_attn_q (dQ)
 
-// One round of k_attn_q's epilogue: 16 keys of this thread's query row.  P = 2^(s S -
-// lse log2 e), dS = P (dP - D), packed to bf16 pairs.  MASK: the round holds keys after
-// the query (the diagonal block) or the row is past the chunk's end; the other rounds
-// skip the per-element test.
+// k_attn_q's epilogue: 32 keys of this thread's query row.  P = 2^(s S - lse log2 e), dS =
+// P (dP - D), packed to bf16 pairs.  MASK: some row of the warp does not see all 32 keys;
+// the other blocks skip the per-element test.
 template <class S, bool MASK>
-__device__ __forceinline__ void q_round(const uint32_t (&rs)[16], const uint32_t (&rd)[16],
+__device__ __forceinline__ void q_block(const uint32_t (&rs)[32], const uint32_t (&rd)[32],
                                         const typename S::Scale& sc, float lz, float Dq, int kg, int qr, int lo, int hi,
-                                        uint32_t* dw) {
+                                        uint32_t (&dw)[16]) {
+  const float2 nD = make_float2(-Dq, -Dq);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float dc[2];
-    const float2 pp = exp2_pair(S::log2p(sc, __uint_as_float(rs[2 * i]), lz, qr - kg - 2 * i, dc[0]),
-                                S::log2p(sc, __uint_as_float(rs[2 * i + 1]), lz, qr - kg - 2 * i - 1, dc[1]));
-    float pv[2] = {pp.x, pp.y}, sv[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int jj = 2 * i + e;
-      const bool out = MASK && (kg + jj < lo || kg + jj >= hi);
-      if (out) pv[e] = 0.f;
-      sv[e] = S::grad(pv[e], __uint_as_float(rd[jj]) - Dq, dc[e]);
-      if (S::kClearMasked && out) sv[e] = 0.f;
-    }
-    dw[i] = pack_bf16(sv[0], sv[1]);
+  for (int i = 0; i < 16; ++i) {
+    float2 dc;
+    const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])),
+                               make_float2(-lz, -lz), qr - kg - 2 * i, -1, dc);
+    float2 pp = exp2_pair(x.x, x.y);
+    const bool o0 = MASK && (kg + 2 * i < lo || kg + 2 * i >= hi);
+    const bool o1 = MASK && (kg + 2 * i + 1 < lo || kg + 2 * i + 1 >= hi);
+    if (o0) pp.x = 0.f;
+    if (o1) pp.y = 0.f;
+    float2 sv = S::grad2(pp, add2(make_float2(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])), nD), dc);
+    if (S::kClearMasked && o0) sv.x = 0.f;
+    if (S::kClearMasked && o1) sv.y = 0.f;
+    dw[i] = pack_bf16(sv.x, sv.y);
   }
 }
 
@@ -801,154 +846,171 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     k_attn_q(const __grid_constant__ typename S::QMaps maps, const typename S::Q p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  CtrlF* c = reinterpret_cast<CtrlF*>(base + Q_CTRL);
+  CtrlQ* c = reinterpret_cast<CtrlQ*>(base + Q_CTRL);
   const uint32_t sb = saddr(base);
   const int warp = uniform_warp(), lane = threadIdx.x % 32;
   const uint32_t rank = ctarank();
-  prologue_f(c, warp, Q_EPI);
+  prologue_q(c, warp);
   const uint32_t tmem = c->tmem_base;
   const int pid = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
   if (warp == 0) {
     if (lane == 0) {
-      // the unit's Q and dO, then ring X: K and V of each key block (this CTA's 64 keys)
+      // the unit's Q and dO, then K and V of each key block (this CTA's 64 keys)
       prefetch_map(maps[Q_MQ]);
       prefetch_map(maps[Q_MO]);
       prefetch_map(maps[Q_MKA]);
       prefetch_map(maps[Q_MVA]);
-      int sa = 0;
-      uint32_t pha = 0, phr = 0, iss = 0, lph_a[2] = {0, 0}, lph_r = 0;
+      uint32_t g = 0, gv = 0, lu = 0;   // key blocks (K; V) and units loaded so far
       bool ok = true;
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
         if (nj == 0) continue;
-        if (!wait_inl<false>(&c->rempty, phr ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
-        const uint32_t fr = mapa(saddr(&c->rfull), 0);
-        if (rank == 0) mbar_expect_tx(&c->rfull, 4u * 32768u);
+        const uint32_t rs = lu & 1u;
+        if (!wait_c(&c->rempty[rs], (lu >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
+        const uint32_t fr = mapa(saddr(&c->rfull[rs]), 0);
+        if (rank == 0) mbar_expect_tx(&c->rfull[rs], 4u * 32768u);
         const int qrow = p.c0 + 256 * qp + 128 * (int)rank;
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
-          tma_load_3d_pair(sb + Q_Q + hb * 16384, maps[Q_MQ], fr, 64 * hb, qrow, z);
-          tma_load_3d_pair(sb + Q_DO + hb * 16384, maps[Q_MO], fr, 64 * hb, qrow, z);
+          tma_load_3d_pair(sb + Q_R + rs * 65536u + hb * 16384, maps[Q_MQ], fr, 64 * hb, qrow, z);
+          tma_load_3d_pair(sb + Q_R + rs * 65536u + 32768 + hb * 16384, maps[Q_MO], fr, 64 * hb, qrow, z);
         }
-        iss |= 4u;
-        lph_r = phr;
-        phr ^= 1u;
+        ++lu;
         for (int j = 0; j < nj; ++j) {
-          if (!wait_inl<false>(&c->aempty[sa], pha ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
-          const uint32_t fa = mapa(saddr(&c->afull[sa]), 0);
-          if (rank == 0) mbar_expect_tx(&c->afull[sa], 2u * Q_X_STAGE);
-          const uint32_t st = sb + Q_X + sa * Q_X_STAGE;
           const int krow = 128 * (j0 + j) + 64 * (int)rank;
+          const uint32_t s = g & 1u, ph = (g >> 1) ^ 1u;
+          if (!wait_c(&c->kempty[s], ph, c, p.limit_ns)) { ok = false; break; }
+          const uint32_t fk = mapa(saddr(&c->kfull[s]), 0), fv = mapa(saddr(&c->vfull[s]), 0);
+          if (rank == 0) mbar_expect_tx(&c->kfull[s], 2u * 16384u);
 #pragma unroll
-          for (int hb = 0; hb < 2; ++hb) {
-            tma_load_3d_pair(st + hb * 8192, maps[Q_MKA], fa, 64 * hb, krow, z / p.group);
-            tma_load_3d_pair(st + 16384 + hb * 8192, maps[Q_MVA], fa, 64 * hb, krow, z / p.group);
-          }
-          iss |= 1u << sa;
-          lph_a[sa] = pha;
-          if (++sa == 2) { sa = 0; pha ^= 1u; }
+          for (int hb = 0; hb < 2; ++hb)
+            tma_load_3d_pair(sb + Q_K + s * 16384u + hb * 8192, maps[Q_MKA], fk, 64 * hb, krow, z / p.group);
+          ++g;
+          if (!wait_c(&c->vempty[s], ph, c, p.limit_ns)) { ok = false; break; }
+          if (rank == 0) mbar_expect_tx(&c->vfull[s], 2u * 16384u);
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb)
+            tma_load_3d_pair(sb + Q_V + s * 16384u + hb * 8192, maps[Q_MVA], fv, 64 * hb, krow, z / p.group);
+          ++gv;
         }
       }
-      if (!ok) {
+      if (!ok) {   // wait for the copies in flight
         fail_f(c, p.status);
         if (rank == 0) {
-          if (iss & 4u) wait_inl<false>(&c->rfull, lph_r, nullptr, 200000000ull);
-          for (int s = 0; s < 2; ++s)
-            if (iss & (1u << s)) wait_inl<false>(&c->afull[s], lph_a[s], nullptr, 200000000ull);
+          for (uint32_t i = lu > 2 ? lu - 2 : 0; i < lu; ++i)
+            wait_inl<false>(&c->rfull[i & 1u], (i >> 1) & 1u, nullptr, 200000000ull);
+          for (uint32_t i = g > 2 ? g - 2 : 0; i < g; ++i)
+            wait_inl<false>(&c->kfull[i & 1u], (i >> 1) & 1u, nullptr, 200000000ull);
+          for (uint32_t i = gv > 2 ? gv - 2 : 0; i < gv; ++i)
+            wait_inl<false>(&c->vfull[i & 1u], (i >> 1) & 1u, nullptr, 200000000ull);
         }
       }
     } else if (lane == 16) {
-      // ring Y: K of each key block, 128 keys x this CTA's half of hd (B of dQ += dS K)
+      // K of each key block, 128 keys x this CTA's half of hd (B of dQ += dS K)
       prefetch_map(maps[Q_MKB]);
       const int tail = S::tail_block(p);
-      int sy = 0;
-      uint32_t phy = 0, iss = 0, lph[2] = {0, 0};
+      uint32_t g = 0;
       bool ok = true;
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
-        if (nj == 0) continue;
         for (int j = 0; j < nj; ++j) {
-          if (!wait_inl<false>(&c->bempty[sy], phy ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
-          const uint32_t fb = mapa(saddr(&c->bfull[sy]), 0);
-          if (rank == 0) mbar_expect_tx(&c->bfull[sy], 2u * Q_Y_STAGE);
+          const uint32_t s = g & 1u;
+          if (!wait_c(&c->yempty[s], (g >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
+          const uint32_t fy = mapa(saddr(&c->yfull[s]), 0);
+          if (rank == 0) mbar_expect_tx(&c->yfull[s], 2u * 16384u);
           if (j0 + j == tail) {
             // (Q_MKT is past the last map of policies without a tail block, whose tail is -1)
-            tma_load_3d_pair(sb + Q_Y + sy * Q_Y_STAGE, maps[Q_MKT], fb, 64 * (int)rank, 0, z / p.group);
+            tma_load_3d_pair(sb + Q_Y + s * 16384u, maps[Q_MKT], fy, 64 * (int)rank, 0, z / p.group);
           } else {
-            tma_load_3d_pair(sb + Q_Y + sy * Q_Y_STAGE, maps[Q_MKB], fb, 64 * (int)rank, 128 * (j0 + j), z / p.group);
+            tma_load_3d_pair(sb + Q_Y + s * 16384u, maps[Q_MKB], fy, 64 * (int)rank, 128 * (j0 + j), z / p.group);
           }
-          iss |= 1u << sy;
-          lph[sy] = phy;
-          if (++sy == 2) { sy = 0; phy ^= 1u; }
+          ++g;
         }
       }
       if (!ok) {
         fail_f(c, p.status);
         if (rank == 0)
-          for (int s = 0; s < 2; ++s)
-            if (iss & (1u << s)) wait_inl<false>(&c->bfull[s], lph[s], nullptr, 200000000ull);
+          for (uint32_t i = g > 2 ? g - 2 : 0; i < g; ++i)
+            wait_inl<false>(&c->yfull[i & 1u], (i >> 1) & 1u, nullptr, 200000000ull);
       }
     }
   } else if (warp == 1) {
     if (rank == 0) {   // the whole warp, converged; one elected lane issues
-      int sa = 0, sy = 0, lu = 0;
-      uint32_t pha = 0, phy = 0, phr = 0, tempty_seen = 0, oready_seen = 0, acc_seen = 0, g = 0;
+      const uint64_t dR = sw128_desc(sb + Q_R, 16, 1024), dK = sw128_desc(sb + Q_K, 16, 1024),
+                     dV = sw128_desc(sb + Q_V, 16, 1024), dY = sw128_desc(sb + Q_Y, 16384, 1024);
+      uint32_t g = 0, lu = 0;
       bool ok = true;
-      const uint64_t dQd = sw128_desc(sb + Q_Q, 16, 1024), dOd = sw128_desc(sb + Q_DO, 16, 1024),
-                     dX = sw128_desc(sb + Q_X, 16, 1024), dY = sw128_desc(sb + Q_Y, 16384, 1024);
-      // dQ += dS K for global key block gg (the first of its unit overwrites)
-      auto accumulate = [&](uint32_t gg, bool first) -> bool {
-        if (!warp_wait_n(&c->oready, oready_seen, gg + 1, c, p.limit_ns)) return false;
-        if (!warp_wait_f(&c->bfull[sy], phy, c, p.limit_ns)) return false;
-        if (first && !warp_wait_n(&c->accempty, acc_seen, (uint32_t)lu, c, p.limit_ns)) return false;
+      // S of block gg into its buffer: free, since the dQ product that read the dS in it was
+      // issued before
+      auto scores = [&](uint32_t gg, uint64_t q0) -> bool {
+        const uint32_t s = gg & 1u;
+        if (!warp_wait_f(&c->kfull[s], gg >> 1, c, p.limit_ns)) return false;
         tc_fence_after();
+        const uint64_t k0 = dplus(dK, s * 16384u);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma2_bf16_ts(tmem + 256, tmem + Q_TDS + 64 * (gg & 1) + 8 * k,
-                         dplus(dY, sy * Q_Y_STAGE + k * 2048), IDESC_KM,
-                         (!first || k) ? 1u : 0u);
-          commit2_mc(&c->bempty[sy], 3);
-          commit2_mc(&c->dsfree[gg & 1], 3);
+            mma2_bf16(tmem + 128 * s, dplus(q0, (k >> 2) * 16384 + (k & 3) * 32),
+                      dplus(k0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+          commit2_mc(&c->kempty[s], 3);
         }
         __syncwarp();
-        if (++sy == 2) { sy = 0; phy ^= 1u; }
+        return true;
+      };
+      // dP of block gg, once the previous block's has been read; completes the block's S too
+      auto grads = [&](uint32_t gg, uint64_t o0) -> bool {
+        const uint32_t s = gg & 1u;
+        if (!warp_wait_c(&c->tempty, gg ^ 1u, c, p.limit_ns)) return false;
+        if (!warp_wait_f(&c->vfull[s], gg >> 1, c, p.limit_ns)) return false;
+        tc_fence_after();
+        const uint64_t v0 = dplus(dV, s * 16384u);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma2_bf16(tmem + QT_DP, dplus(o0, (k >> 2) * 16384 + (k & 3) * 32),
+                      dplus(v0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+          commit2_mc(&c->vempty[s], 3);
+          commit2_mc(&c->tfull, 3);
+        }
+        __syncwarp();
         return true;
       };
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
         if (nj == 0) continue;
-        if (!warp_wait_f(&c->rfull, phr, c, p.limit_ns)) { ok = false; break; }
-        phr ^= 1u;
-        tc_fence_after();
+        const uint32_t rs = lu & 1u;
+        if (!warp_wait_f(&c->rfull[rs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
+        const uint64_t q0 = dplus(dR, rs * 65536u), o0 = dplus(q0, 32768);
+        // the tensor pipe always has the next block's S and dP to form while the epilogue
+        // works on a block: S two blocks ahead, dP one
+        if (!scores(g, q0) || !grads(g, o0) || (nj > 1 && !scores(g + 1, q0))) { ok = false; break; }
         for (int n = 0; n < nj; ++n, ++g) {
-          if (!warp_wait_n(&c->tempty, tempty_seen, g, c, p.limit_ns)) { ok = false; break; }
-          if (!warp_wait_f(&c->afull[sa], pha, c, p.limit_ns)) { ok = false; break; }
+          const uint32_t s = g & 1u;
+          if (n + 1 < nj && !grads(g + 1, o0)) { ok = false; break; }
+          if (n == max(nj - 2, 0) && elect_one()) commit2_mc(&c->rempty[rs], 3);   // the unit's last S, dP are issued
+          __syncwarp();
+          if (!warp_wait_c(&c->oready[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_f(&c->yfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
+          if (n == 0 && !warp_wait_c(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t dst = dplus(dX, sa * Q_X_STAGE);
+          const uint64_t y0 = dplus(dY, s * 16384u);
           if (elect_one()) {
+            // dS: 16 columns at the start of each epilogue warp's 32
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma2_bf16(tmem, dplus(dQd, (k >> 2) * 16384 + (k & 3) * 32), dplus(dst, (k >> 2) * 8192 + (k & 3) * 32),
-                        IDESC_KK, k ? 1u : 0u);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma2_bf16(tmem + 128, dplus(dOd, (k >> 2) * 16384 + (k & 3) * 32),
-                        dplus(dst, 16384 + (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
-            commit2_mc(&c->aempty[sa], 3);
-            commit2_mc(&c->tfull, 3);
-            if (n == nj - 1) commit2_mc(&c->rempty, 3);
+              mma2_bf16_ts(tmem + QT_DQ, tmem + 128 * s + 32 * (k >> 1) + 8 * (k & 1), dplus(y0, k * 2048), IDESC_KM,
+                           (n || k) ? 1u : 0u);
+            commit2_mc(&c->yempty[s], 3);
+            if (n == nj - 1) commit2_mc(&c->dqfull, 3);
           }
           __syncwarp();
-          if (++sa == 2) { sa = 0; pha ^= 1u; }
-          if (n >= 1 && !accumulate(g - 1, n == 1)) { ok = false; break; }
+          if (n + 2 < nj && !scores(g + 2, q0)) { ok = false; break; }
         }
         if (!ok) break;
-        if (!accumulate(g - 1, nj == 1)) { ok = false; break; }
         ++lu;
       }
       if (elect_one()) {
@@ -960,23 +1022,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     __syncwarp();
   } else if (warp == Q_FWD_WARP) {
     if (lane == 0) {
-      uint32_t te_seen = 0, or_seen = 0, g = 0;
+      uint32_t g = 0;
       bool ok = true;
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, z, qp, j0, nj);
-        if (nj == 0) continue;
-        for (int j = 0; j < nj; ++j, ++g)
-          if (!forward_block(c, g, te_seen, or_seen, p.limit_ns)) { ok = false; break; }
+        for (int j = 0; j < nj; ++j, ++g) {
+          if (!wait_c(&c->tempty_l, g, c, p.limit_ns)) { ok = false; break; }
+          arrive_remote(mapa(saddr(&c->tempty), 0));
+          if (!wait_c(&c->oready_l[g & 1u], g >> 1, c, p.limit_ns)) { ok = false; break; }
+          arrive_remote(mapa(saddr(&c->oready[g & 1u]), 0));
+        }
       }
       if (!ok) fail_f(c, p.status);
     }
     __syncwarp();
   } else {
     const int q = warp & 3, cg = (warp - 2) >> 2;   // lane quadrant, 32-column group
-    const uint32_t trow = (uint32_t)(q * 32) << 16;
-    uint32_t tfull_seen = 0, g = 0;
-    uint32_t ds_seen0 = 0, ds_seen1 = 0, ds_uses0 = 0, ds_uses1 = 0;   // per dS buffer: completions waited, blocks written
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(32 * cg);
+    uint32_t g = 0, lu = 0;
     bool ok = true;
     for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
       int z, qp, j0, nj;
@@ -998,69 +1062,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         }
       }
       for (int j = 0; j < nj; ++j, ++g) {
-        if (!warp_wait_n(&c->tfull, tfull_seen, g + 1, c, p.limit_ns)) { ok = false; break; }
+        if (!warp_wait_c(&c->tfull, g, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
-        uint32_t dw[16];   // bf16 pairs of dS over this thread's 32 keys
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {   // two rounds of 16 keys
-          uint32_t rs[16], rd[16];
-          tmem_ld16(tmem + trow + (uint32_t)(32 * cg + 16 * r), rs);
-          tmem_ld16(tmem + trow + (uint32_t)(128 + 32 * cg + 16 * r), rd);
-          tmem_ld_wait();
-          if (r == 1) {   // S and dP are in registers: the next block's may be formed
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->tempty_l);
-          }
-          const int kg = 128 * (j0 + j) + 32 * cg + 16 * r;   // first key of the round
-          const bool none = kg + 15 < lo0 || kg >= hi1;
-          const bool all = kg >= lo1 && kg + 15 < hi0;
-          if (none) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dw[8 * r + i] = 0u;
-          } else if (all) {
-            q_round<S, false>(rs, rd, sc, lz, Dq, kg, qr, lo, hi, &dw[8 * r]);
-          } else {
-            q_round<S, true>(rs, rd, sc, lz, Dq, kg, qr, lo, hi, &dw[8 * r]);
-          }
-        }
-        // dS into tensor-memory buffer g % 2 once the dQ GEMM of its previous block has read it
-        const int bf = (int)(g & 1u);
-        if (!(bf ? warp_wait_n(&c->dsfree[1], ds_seen1, ds_uses1, c, p.limit_ns)
-                 : warp_wait_n(&c->dsfree[0], ds_seen0, ds_uses0, c, p.limit_ns))) { ok = false; break; }
-        tmem_st16(tmem + trow + (uint32_t)(Q_TDS + 64 * bf + 16 * cg), dw);
-        tmem_st_wait();
-        if (bf) ++ds_uses1; else ++ds_uses0;
+        uint32_t rs[32], rd[32], dw[16];   // dw: bf16 pairs of dS over this thread's 32 keys
+        tmem_ld32(trow + QT_DP, rd);
+        tmem_ld32(trow + 128 * (g & 1u), rs);
+        tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->oready_l);
+        if (lane == 0) mbar_arrive(&c->tempty_l);   // dP is in registers: the next block's may be formed
+        const int kg = 128 * (j0 + j) + 32 * cg;    // first key
+        if (kg + 31 < lo0 || kg >= hi1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dw[i] = 0u;
+        } else if (kg >= lo1 && kg + 31 < hi0) {
+          q_block<S, false>(rs, rd, sc, lz, Dq, kg, qr, lo, hi, dw);
+        } else {
+          q_block<S, true>(rs, rd, sc, lz, Dq, kg, qr, lo, hi, dw);
+        }
+        __syncwarp();
+        tmem_st16(trow + 128 * (g & 1u), dw);       // over this warp's own scores
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->oready_l[g & 1u]);
       }
       if (!ok) break;
-      // dQ of the unit's queries: s * accumulator, bf16, this thread's row and 32 of hd (the
-      // commit after the last dQ GEMM covers all earlier ones)
-      if (!(((g - 1u) & 1u) ? warp_wait_n(&c->dsfree[1], ds_seen1, ds_uses1, c, p.limit_ns)
-                            : warp_wait_n(&c->dsfree[0], ds_seen0, ds_uses0, c, p.limit_ns))) { ok = false; break; }
+      // dQ of the unit's queries: s * accumulator, bf16, this thread's row and 32 of hd
+      if (!warp_wait_c(&c->dqfull, lu, c, p.limit_ns)) { ok = false; break; }
+      ++lu;
       tc_fence_after();
+      __syncwarp();
       uint32_t ra[32];
-      tmem_ld32(tmem + trow + (uint32_t)(256 + 32 * cg), ra);
+      tmem_ld32(trow + QT_DQ, ra);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
-      if (vrow && S::kAddOut) {
-        uint4* o = reinterpret_cast<uint4*>(p.dQ + ro * 128 + 32 * cg);
+      if constexpr (S::kAddOut) {
+        if (vrow) {
+          uint4* o = reinterpret_cast<uint4*>(p.dQ + ro * 128 + 32 * cg);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t* v = &ra[8 * k];
-          o[k] = make_uint4(pack_bf16(__uint_as_float(v[0]) * p.scale, __uint_as_float(v[1]) * p.scale),
-                            pack_bf16(__uint_as_float(v[2]) * p.scale, __uint_as_float(v[3]) * p.scale),
-                            pack_bf16(__uint_as_float(v[4]) * p.scale, __uint_as_float(v[5]) * p.scale),
-                            pack_bf16(__uint_as_float(v[6]) * p.scale, __uint_as_float(v[7]) * p.scale));
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t* v = &ra[8 * k];
+            o[k] = make_uint4(pack_bf16(__uint_as_float(v[0]) * p.scale, __uint_as_float(v[1]) * p.scale),
+                              pack_bf16(__uint_as_float(v[2]) * p.scale, __uint_as_float(v[3]) * p.scale),
+                              pack_bf16(__uint_as_float(v[4]) * p.scale, __uint_as_float(v[5]) * p.scale),
+                              pack_bf16(__uint_as_float(v[6]) * p.scale, __uint_as_float(v[7]) * p.scale));
+          }
         }
-      }
-      if constexpr (!S::kAddOut) {
+      } else {
         if (vrow) S::store_dq(p, ro, 32 * cg, ra);
       }
+      __syncwarp();
     }
     if (!ok) fail_f(c, p.status);
   }

@@ -124,17 +124,24 @@ struct PackedScores {
   static __device__ __forceinline__ Scale scale_of(const P& p, int z) {
     return Scale{p.sc.sl2, p.sc.c2, p.sc.k, BIAS ? p.slopes[z] * L2E : 0.f};
   }
-  static __device__ __forceinline__ float log2p(const Scale& sc, float s, float lz, int dist, float& dc) {
-    float x;
+  static __device__ __forceinline__ float2 log2p2(const Scale& sc, float2 s, float2 nlz, int dist, int step,
+                                                  float2& dc) {
+    float2 x;
     if (CAP) {
-      x = capped<true>(sc, s, dc) - lz;
+      x = add2(make_float2(capped<true>(sc, s.x, dc.x), capped<true>(sc, s.y, dc.y)), nlz);
     } else {
-      dc = 1.f;
-      x = fmaf(s, sc.sl2, -lz);
+      dc = make_float2(1.f, 1.f);
+      x = fma2(s, make_float2(sc.sl2, sc.sl2), nlz);
     }
-    return BIAS ? fmaf(-sc.slope2, fabsf((float)dist), x) : x;
+    if (BIAS) {
+      x.x = fmaf(-sc.slope2, fabsf((float)dist), x.x);
+      x.y = fmaf(-sc.slope2, fabsf((float)(dist + step)), x.y);
+    }
+    return x;
   }
-  static __device__ __forceinline__ float grad(float p, float d, float dc) { return CAP ? p * d * dc : p * d; }
+  static __device__ __forceinline__ float2 grad2(float2 p, float2 d, float2 dc) {
+    return CAP ? mul2(mul2(p, d), dc) : mul2(p, d);
+  }
 
   // 64 columns of dV (t = 0) or dK (t = 1) of one key
   static __device__ __forceinline__ void store_out(const Kv& p, int t, int plane, int key, int c,
