@@ -8,9 +8,11 @@
 //   k_attn_kv  unit = (head, 256 keys).  dV and dK of those keys stay in tensor memory
 //              while the unit walks the chunk's query blocks of 128:
 //                S^T = K Q^T,  dP^T = V dO^T                      (tensor memory)
-//                P^T = exp(s S^T - lse),  dS^T = P^T (dP^T - D)   (epilogue -> shared memory)
-//                dV += P^T dO,  dK += dS^T Q                      (tensor memory)
-//              then adds dV and s dK into the fp32 outputs (TMA reduce-add).
+//                P^T = exp(s S^T - lse),  dS^T = P^T (dP^T - D)   (written over S^T and dP^T)
+//                dV += P^T dO,  dK += dS^T Q                      (A from tensor memory)
+//              then adds dV and s dK into the fp32 outputs (TMA reduce-add) or writes them.
+//              The two streams S -> P -> dV and dP -> dS -> dK take turns: while the
+//              epilogue works on one, the tensor pipe runs the other's products.
 //   k_attn_q   unit = (head, 256 queries of the chunk).  dQ stays in tensor memory while
 //              the unit walks the key blocks of 128 up to its last query:
 //                S = Q K^T,  dP = dO V^T,  dS = P (dP - D),  dQ += dS K
@@ -41,13 +43,8 @@ namespace fa {
 // epilogue warps arrive on CTA-local barriers; the forwarder turns each completed local
 // phase into one arrival at the leader, which keeps the remote arrival's latency off the
 // epilogue's critical path.
-// k_attn_q: sixteen epilogue warps of 32 of the 128 columns each (19 warps, 85 registers
-// a thread, no spills; eight warps of 64 columns measured the same).
-constexpr int Q_EPI = 16;
-// k_attn_kv: eight epilogue warps of 64 columns each (12 warps in all, so 168 registers a
-// thread): its epilogue measured 1490 cycles per block this way against 2350 for sixteen
-// warps of 32 columns held to 96 registers, the same work spilling.
-constexpr int KV_EPI = 8;
+// Sixteen epilogue warps of 32 of the 128 columns each (96 registers a thread).
+constexpr int Q_EPI = 16, KV_EPI = 16;
 constexpr int KV_LD_WARP = 2 + KV_EPI, KV_FWD_WARP = KV_LD_WARP + 1, Q_FWD_WARP = 2 + Q_EPI;
 constexpr int KV_THREADS = 32 * (KV_FWD_WARP + 1);
 constexpr int Q_THREADS = 32 * (Q_FWD_WARP + 1);
@@ -58,13 +55,15 @@ constexpr uint32_t IDESC_KM = idesc_bf16(256, 128, false, true);   // A K-major,
 // swizzled: [64-element block][rows][128 B].
 constexpr uint32_t KV_K = 0;          // K rows of the unit (this CTA's 128 keys x 128)
 constexpr uint32_t KV_V = 32768;      // V rows
-constexpr uint32_t KV_A = 65536;      // 2 stages: Q then dO of the block, this CTA's 64 queries x 128
-constexpr uint32_t KV_A_STAGE = 32768;
-constexpr uint32_t KV_B = 131072;     // Q then dO of the block, 128 queries x this CTA's 64 of hd
-constexpr uint32_t KV_PT = 163840;    // P^T  [2 query halves][128 keys][128 B]
-constexpr uint32_t KV_DST = 196608;   // dS^T [2 query halves][128 keys][128 B]
-constexpr uint32_t KV_LD = 229376;    // -lse * log2(e) [128], then -D [128], of the block's queries
-constexpr uint32_t KV_CTRL = 230400;
+constexpr uint32_t KV_AQ = 65536;     // 2 stages: Q of the block, this CTA's 64 queries x 128 (B of S^T)
+constexpr uint32_t KV_AO = 98304;     // 2 stages: dO of the block, likewise (B of dP^T)
+constexpr uint32_t KV_BQ = 131072;    // Q of the block, 128 queries x this CTA's 64 of hd (B of dK)
+constexpr uint32_t KV_BO = 147456;    // dO of the block, likewise (B of dV)
+constexpr uint32_t KV_STG = 163840;   // one 32 x 32 fp32 block of dV or dK an epilogue warp
+constexpr uint32_t KV_LD = 229376;    // -lse * log2(e) [2 stages][128], then -D [128], of the block's queries
+constexpr uint32_t KV_CTRL = 230912;
+// Tensor memory of k_attn_kv: S^T (P^T over it), dP^T (dS^T over it), dV, dK.
+constexpr uint32_t KT_DP = 128, KT_DV = 256, KT_DK = 384;
 
 // Shared memory of k_attn_q: Q and dO of two units, two stages of each key-block operand.
 constexpr uint32_t Q_R = 0;           // Q then dO rows of the unit (this CTA's 128 queries x 128 each)
@@ -88,15 +87,14 @@ struct CtrlQ {
 };
 
 struct CtrlF {
-  uint64_t afull[2], aempty[2];  // ring of the S / dP B operands
-  uint64_t bfull[2], bempty[2];  // ring of the B operands of the accumulating GEMMs
-  uint64_t rfull, rempty;        // the unit's resident A operands
-  uint64_t tfull, tempty;        // S and dP accumulators (tempty: leader, one arrival per CTA)
-  uint64_t oready, ofree;        // P^T, dS^T (or dS) in shared memory (oready: leader, one per CTA)
-  uint64_t tempty_l, oready_l;   // the CTA's epilogue warps, forwarded to tempty / oready
-  uint64_t accempty;             // the unit's accumulators have been read out
-  uint64_t lfull, lempty;        // lse / D of the block (k_attn_kv)
-  uint64_t sfree;                // the dV / dK staging has left shared memory (k_attn_kv)
+  uint64_t qfull[2], qempty[2], ofull[2], oempty[2];   // K-major Q and dO of the block
+  uint64_t bqfull, bqempty, bofull, boempty;           // the same 128 queries x half of hd
+  uint64_t rfull, rempty;        // the unit's K and V
+  uint64_t sfull, dpfull;        // S^T / dP^T of the block is ready (both CTAs)
+  uint64_t pready, dsready;      // P^T / dS^T is written (leader, one per CTA)
+  uint64_t pready_l, dsready_l;  // the CTA's epilogue warps, forwarded
+  uint64_t accfull, accempty;    // the unit's dV and dK are complete; have been read out (leader)
+  uint64_t lfull[2], lempty[2], dfull, dempty;   // lse (2 stages) and D of the block
   uint64_t mdone;
   uint32_t tmem_base;
   int abort;
@@ -123,23 +121,29 @@ __device__ __forceinline__ void prologue_end(C* c, int warp) {
 __device__ __forceinline__ void prologue_f(CtrlF* c, int warp) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c->afull[i], 1);
-      mbar_init(&c->aempty[i], 1);
-      mbar_init(&c->bfull[i], 1);
-      mbar_init(&c->bempty[i], 1);
+      mbar_init(&c->qfull[i], 1);
+      mbar_init(&c->qempty[i], 1);
+      mbar_init(&c->ofull[i], 1);
+      mbar_init(&c->oempty[i], 1);
+      mbar_init(&c->lfull[i], 1);
+      mbar_init(&c->lempty[i], KV_EPI);
     }
+    mbar_init(&c->bqfull, 1);
+    mbar_init(&c->bqempty, 1);
+    mbar_init(&c->bofull, 1);
+    mbar_init(&c->boempty, 1);
     mbar_init(&c->rfull, 1);
     mbar_init(&c->rempty, 1);
-    mbar_init(&c->tfull, 1);
-    mbar_init(&c->tempty, 2);
-    mbar_init(&c->oready, 2);
-    mbar_init(&c->tempty_l, KV_EPI);
-    mbar_init(&c->oready_l, KV_EPI);
-    mbar_init(&c->ofree, 1);
+    mbar_init(&c->sfull, 1);
+    mbar_init(&c->dpfull, 1);
+    mbar_init(&c->pready, 2);
+    mbar_init(&c->dsready, 2);
+    mbar_init(&c->pready_l, KV_EPI);
+    mbar_init(&c->dsready_l, KV_EPI);
+    mbar_init(&c->accfull, 1);
     mbar_init(&c->accempty, 2 * KV_EPI);
-    mbar_init(&c->lfull, 1);
-    mbar_init(&c->lempty, KV_EPI);
-    mbar_init(&c->sfree, KV_EPI);
+    mbar_init(&c->dfull, 1);
+    mbar_init(&c->dempty, KV_EPI);
     mbar_init(&c->mdone, 1);
     c->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -225,17 +229,6 @@ __device__ __forceinline__ bool warp_wait_c(uint64_t* b, uint32_t parity, C* c, 
   return __all_sync(0xffffffffu, wait_c(b, parity, c, limit));
 }
 
-// The forwarder: for block g, waits for the CTA's 8 epilogue warps on tempty_l, then on
-// oready_l, and passes each on to the leader's barrier.
-__device__ __forceinline__ bool forward_block(CtrlF* c, uint32_t g, uint32_t& te_seen, uint32_t& or_seen,
-                                              uint64_t limit) {
-  if (!wait_n(&c->tempty_l, te_seen, g + 1, c, limit)) return false;
-  arrive_remote(mapa(saddr(&c->tempty), 0));
-  if (!wait_n(&c->oready_l, or_seen, g + 1, c, limit)) return false;
-  arrive_remote(mapa(saddr(&c->oready), 0));
-  return true;
-}
-
 __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
   asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -257,16 +250,6 @@ __device__ __forceinline__ uint64_t dplus(uint64_t d, uint32_t bytes) {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Half `half` (64 B = 32 bf16) of row `row` of a 128-byte-swizzled K-major tile: 16-byte
-// chunk k of the row sits at chunk k ^ (row % 8), the layout TMA writes and tcgen05.mma
-// reads.
-__device__ __forceinline__ void store_half_row(uint32_t tile, int row, int half, const uint32_t (&w)[16]) {
-  const uint32_t r = tile + (uint32_t)row * 128u;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    sts128(r + ((uint32_t)((4 * half + k) ^ (row & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
 }
 
 // tcgen05.mma with A in tensor memory (each CTA's 128 rows in its lanes, two bf16 of
@@ -300,35 +283,50 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 
 // ================================================================ k_attn_kv (dK, dV)
 
-// One round of k_attn_kv's epilogue: 16 queries (columns j0 .. j0+15 of the thread's
-// 32-column group) of this thread's key row.  P^T = 2^(s S^T - lse log2 e) and
-// dS^T = P^T (dP^T - D), packed to bf16 pairs.  MASK: the round holds queries before the
-// key or past the chunk's end (a diagonal block or the ragged tail), which get P = 0; the
-// other rounds skip the per-element test (the mask costs more than the math it guards).
+// k_attn_kv's epilogue: 32 queries of this thread's key row.  First P^T = 2^(s S^T - lse
+// log2 e), kept in fp32 (over the scores) and packed to bf16 pairs, with the factors of the
+// scores' gradients where a policy has them; then dS^T = P^T (dP^T - D).  MASK: some key of
+// the warp is not seen by all 32 queries; the other blocks skip the per-element test (it
+// costs more than the math it guards).
 template <class S, bool MASK>
-__device__ __forceinline__ void kv_round(const uint32_t (&rs)[32], const uint32_t (&rd)[32], int j0,
-                                         const float* lds, const typename S::Scale& sc, int qg, int key, int lo,
-                                         int hi, uint32_t* pw, uint32_t* dw) {
-  const float4* l4 = reinterpret_cast<const float4*>(lds);         // - lse log2 e
-  const float4* d4 = reinterpret_cast<const float4*>(lds + 128);   // - D
+__device__ __forceinline__ void kv_probs(uint32_t (&rs)[32], const float* nlse, const typename S::Scale& sc, int qg,
+                                         int key, int lo, int hi, uint32_t (&pw)[16], typename S::Factors& fac) {
+  const float4* l4 = reinterpret_cast<const float4*>(nlse);   // - lse log2 e
 #pragma unroll
-  for (int j4 = 0; j4 < 4; ++j4) {
-    const float4 L = l4[j4], Dv = d4[j4];
+  for (int j4 = 0; j4 < 8; ++j4) {
+    const float4 L = l4[j4];
 #pragma unroll
     for (int e = 0; e < 4; e += 2) {
       const int j = 4 * j4 + e;
       float2 dc;
-      const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[j0 + j]), __uint_as_float(rs[j0 + j + 1])),
+      const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[j]), __uint_as_float(rs[j + 1])),
                                  e ? make_float2(L.z, L.w) : make_float2(L.x, L.y), qg + j - key, 1, dc);
       float2 pp = exp2_pair(x.x, x.y);
-      const bool o0 = MASK && (qg + j < lo || qg + j >= hi), o1 = MASK && (qg + j + 1 < lo || qg + j + 1 >= hi);
-      if (o0) pp.x = 0.f;
-      if (o1) pp.y = 0.f;
-      float2 sv = S::grad2(pp, add2(make_float2(__uint_as_float(rd[j0 + j]), __uint_as_float(rd[j0 + j + 1])),
-                                    e ? make_float2(Dv.z, Dv.w) : make_float2(Dv.x, Dv.y)), dc);
-      if (S::kClearMasked && o0) sv.x = 0.f;
-      if (S::kClearMasked && o1) sv.y = 0.f;
+      if (MASK && (qg + j < lo || qg + j >= hi)) pp.x = 0.f;
+      if (MASK && (qg + j + 1 < lo || qg + j + 1 >= hi)) pp.y = 0.f;
       pw[j / 2] = pack_bf16(pp.x, pp.y);
+      S::keep(fac, j / 2, dc);
+      rs[j] = __float_as_uint(pp.x);
+      rs[j + 1] = __float_as_uint(pp.y);
+    }
+  }
+}
+template <class S, bool MASK>
+__device__ __forceinline__ void kv_grads(const uint32_t (&rp)[32], const uint32_t (&rd)[32], const float* nD, int qg, int lo,
+                                         int hi, const typename S::Factors& fac, uint32_t (&dw)[16]) {
+  const float4* d4 = reinterpret_cast<const float4*>(nD);     // - D
+#pragma unroll
+  for (int j4 = 0; j4 < 8; ++j4) {
+    const float4 Dv = d4[j4];
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const int j = 4 * j4 + e;
+      float2 sv = S::grad2(make_float2(__uint_as_float(rp[j]), __uint_as_float(rp[j + 1])),
+                           add2(make_float2(__uint_as_float(rd[j]), __uint_as_float(rd[j + 1])),
+                                e ? make_float2(Dv.z, Dv.w) : make_float2(Dv.x, Dv.y)),
+                           S::kept(fac, j / 2));
+      if (S::kClearMasked && MASK && (qg + j < lo || qg + j >= hi)) sv.x = 0.f;
+      if (S::kClearMasked && MASK && (qg + j + 1 < lo || qg + j + 1 >= hi)) sv.y = 0.f;
       dw[j / 2] = pack_bf16(sv.x, sv.y);
     }
   }
@@ -443,6 +441,10 @@ struct CausalScores {
     return fma2(s, make_float2(sl2, sl2), nlz);
   }
   static __device__ __forceinline__ float2 grad2(float2 p, float2 d, float2) { return mul2(p, d); }
+  // What k_attn_kv keeps of dc between the two halves of its epilogue.
+  struct Factors {};
+  static __device__ __forceinline__ void keep(Factors&, int, float2) {}
+  static __device__ __forceinline__ float2 kept(const Factors&, int) { return make_float2(1.f, 1.f); }
   template <class P>
   static __device__ __forceinline__ int tail_block(const P&) { return -1; }
 };
@@ -469,20 +471,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      // the unit's K and V, then ring A: Q and dO of each block (this CTA's 64 queries)
+      // the unit's K and V, then Q and dO of each block (this CTA's 64 queries)
       prefetch_map(maps[KV_MK]);
       prefetch_map(maps[KV_MV]);
       prefetch_map(maps[KV_MQA]);
       prefetch_map(maps[KV_MOA]);
-      int sa = 0;
-      uint32_t pha = 0, phr = 0, iss = 0, lph_a[2] = {0, 0}, lph_r = 0;
+      uint32_t g = 0, go = 0, lu = 0;   // blocks (Q; dO) and units loaded so far
       bool ok = true;
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         KvUnit w;
         S::kv_unit(p, u, w);
         const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
-        if (!wait_inl<false>(&c->rempty, phr ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
+        if (!wait_c(&c->rempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
         const uint32_t fr = mapa(saddr(&c->rfull), 0);
         if (rank == 0) mbar_expect_tx(&c->rfull, 4u * 32768u);
         const int krow = 256 * w.kp + 128 * (int)rank;
@@ -491,97 +492,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           tma_load_3d_pair(sb + KV_K + hb * 16384, maps[KV_MK], fr, 64 * hb, krow, w.zk);
           tma_load_3d_pair(sb + KV_V + hb * 16384, maps[KV_MV], fr, 64 * hb, krow, w.zk);
         }
-        iss |= 4u;
-        lph_r = phr;
-        phr ^= 1u;
+        ++lu;
         for (int n = 0; n < nblk; ++n) {
           int z, b;
           kv_block(w, n, z, b);
-          if (!wait_inl<false>(&c->aempty[sa], pha ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
-          const uint32_t fa = mapa(saddr(&c->afull[sa]), 0);
-          if (rank == 0) mbar_expect_tx(&c->afull[sa], 2u * KV_A_STAGE);
-          const uint32_t st = sb + KV_A + sa * KV_A_STAGE;
+          const uint32_t s = g & 1u, ph = (g >> 1) ^ 1u;
           const int qrow = p.c0 + 128 * b + 64 * (int)rank;
+          if (!wait_c(&c->qempty[s], ph, c, p.limit_ns)) { ok = false; break; }
+          const uint32_t fq = mapa(saddr(&c->qfull[s]), 0), fo = mapa(saddr(&c->ofull[s]), 0);
+          if (rank == 0) mbar_expect_tx(&c->qfull[s], 2u * 16384u);
 #pragma unroll
-          for (int hb = 0; hb < 2; ++hb) {
-            tma_load_3d_pair(st + hb * 8192, maps[KV_MQA], fa, 64 * hb, qrow, z);
-            tma_load_3d_pair(st + 16384 + hb * 8192, maps[KV_MOA], fa, 64 * hb, qrow, z);
-          }
-          iss |= 1u << sa;
-          lph_a[sa] = pha;
-          if (++sa == 2) { sa = 0; pha ^= 1u; }
+          for (int hb = 0; hb < 2; ++hb)
+            tma_load_3d_pair(sb + KV_AQ + s * 16384u + hb * 8192, maps[KV_MQA], fq, 64 * hb, qrow, z);
+          ++g;
+          if (!wait_c(&c->oempty[s], ph, c, p.limit_ns)) { ok = false; break; }
+          if (rank == 0) mbar_expect_tx(&c->ofull[s], 2u * 16384u);
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb)
+            tma_load_3d_pair(sb + KV_AO + s * 16384u + hb * 8192, maps[KV_MOA], fo, 64 * hb, qrow, z);
+          ++go;
+        }
+      }
+      if (!ok) {   // wait for the copies in flight
+        fail_f(c, p.status);
+        if (rank == 0) {
+          if (lu) wait_inl<false>(&c->rfull, (lu - 1) & 1u, nullptr, 200000000ull);
+          for (uint32_t i = g > 2 ? g - 2 : 0; i < g; ++i)
+            wait_inl<false>(&c->qfull[i & 1u], (i >> 1) & 1u, nullptr, 200000000ull);
+          for (uint32_t i = go > 2 ? go - 2 : 0; i < go; ++i)
+            wait_inl<false>(&c->ofull[i & 1u], (i >> 1) & 1u, nullptr, 200000000ull);
+        }
+      }
+    } else if (lane == 16) {
+      // dO and Q of each block, 128 queries x this CTA's half of hd
+      prefetch_map(maps[KV_MQB]);
+      prefetch_map(maps[KV_MOB]);
+      const int tail = S::tail_block(p);
+      uint32_t g = 0, gq = 0;
+      bool ok = true;
+      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
+        KvUnit w;
+        S::kv_unit(p, u, w);
+        const int nblk = w.nh * w.nbl;
+        for (int n = 0; n < nblk; ++n) {
+          int z, b;
+          kv_block(w, n, z, b);
+          const int qrow = p.c0 + 128 * b;
+          if (!wait_c(&c->boempty, g ^ 1u, c, p.limit_ns)) { ok = false; break; }
+          const uint32_t fo = mapa(saddr(&c->bofull), 0), fq = mapa(saddr(&c->bqfull), 0);
+          if (rank == 0) mbar_expect_tx(&c->bofull, 2u * 16384u);
+          if (b == tail) tma_load_3d_pair(sb + KV_BO, maps[KV_MOT], fo, 64 * (int)rank, 0, z);
+          else tma_load_3d_pair(sb + KV_BO, maps[KV_MOB], fo, 64 * (int)rank, qrow, z);
+          ++g;
+          if (!wait_c(&c->bqempty, gq ^ 1u, c, p.limit_ns)) { ok = false; break; }
+          if (rank == 0) mbar_expect_tx(&c->bqfull, 2u * 16384u);
+          if (b == tail) tma_load_3d_pair(sb + KV_BQ, maps[KV_MQT], fq, 64 * (int)rank, 0, z);
+          else tma_load_3d_pair(sb + KV_BQ, maps[KV_MQB], fq, 64 * (int)rank, qrow, z);
+          ++gq;
         }
       }
       if (!ok) {
         fail_f(c, p.status);
         if (rank == 0) {
-          if (iss & 4u) wait_inl<false>(&c->rfull, lph_r, nullptr, 200000000ull);
-          for (int s = 0; s < 2; ++s)
-            if (iss & (1u << s)) wait_inl<false>(&c->afull[s], lph_a[s], nullptr, 200000000ull);
+          if (g) wait_inl<false>(&c->bofull, (g - 1) & 1u, nullptr, 200000000ull);
+          if (gq) wait_inl<false>(&c->bqfull, (gq - 1) & 1u, nullptr, 200000000ull);
         }
-      }
-    } else if (lane == 16) {
-      // ring B (one stage): Q and dO of the block, 128 queries x this CTA's half of hd
-      prefetch_map(maps[KV_MQB]);
-      prefetch_map(maps[KV_MOB]);
-      const int tail = S::tail_block(p);
-      uint32_t phb = 0, lph = 0;
-      bool ok = true, any = false;
-      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
-        KvUnit w;
-        S::kv_unit(p, u, w);
-        const int nblk = w.nh * w.nbl;
-        if (nblk == 0) continue;
-        for (int n = 0; n < nblk; ++n) {
-          int z, b;
-          kv_block(w, n, z, b);
-          if (!wait_inl<false>(&c->bempty[0], phb ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
-          const uint32_t fb = mapa(saddr(&c->bfull[0]), 0);
-          if (rank == 0) mbar_expect_tx(&c->bfull[0], 4u * 16384u);
-          if (b == tail) {
-            tma_load_3d_pair(sb + KV_B, maps[KV_MQT], fb, 64 * (int)rank, 0, z);
-            tma_load_3d_pair(sb + KV_B + 16384, maps[KV_MOT], fb, 64 * (int)rank, 0, z);
-          } else {
-            const int qrow = p.c0 + 128 * b;
-            tma_load_3d_pair(sb + KV_B, maps[KV_MQB], fb, 64 * (int)rank, qrow, z);
-            tma_load_3d_pair(sb + KV_B + 16384, maps[KV_MOB], fb, 64 * (int)rank, qrow, z);
-          }
-          any = true;
-          lph = phb;
-          phb ^= 1u;
-        }
-      }
-      if (!ok) {
-        fail_f(c, p.status);
-        if (rank == 0 && any) wait_inl<false>(&c->bfull[0], lph, nullptr, 200000000ull);
       }
     }
   } else if (warp == 1) {
     if (rank == 0) {   // the whole warp, converged; one elected lane issues
-      int sa = 0, lu = 0;
-      uint32_t pha = 0, phb = 0, phr = 0, tempty_seen = 0, oready_seen = 0, acc_seen = 0, g = 0;
-      bool ok = true;
       const uint64_t dK = sw128_desc(sb + KV_K, 16, 1024), dV = sw128_desc(sb + KV_V, 16, 1024),
-                     dA = sw128_desc(sb + KV_A, 16, 1024), dPT = sw128_desc(sb + KV_PT, 16, 1024),
-                     dDST = sw128_desc(sb + KV_DST, 16, 1024), dBm = sw128_desc(sb + KV_B, 16384, 1024);
-      // dV += P^T dO and dK += dS^T Q for global block gg (the first of its unit overwrites)
-      auto accumulate = [&](uint32_t gg, bool first) -> bool {
-        if (!warp_wait_n(&c->oready, oready_seen, gg + 1, c, p.limit_ns)) return false;
-        if (!warp_wait_f(&c->bfull[0], phb, c, p.limit_ns)) return false;
-        phb ^= 1u;
-        if (first && !warp_wait_n(&c->accempty, acc_seen, (uint32_t)lu, c, p.limit_ns)) return false;
+                     dAQ = sw128_desc(sb + KV_AQ, 16, 1024), dAO = sw128_desc(sb + KV_AO, 16, 1024),
+                     dBQ = sw128_desc(sb + KV_BQ, 16384, 1024), dBO = sw128_desc(sb + KV_BO, 16384, 1024);
+      uint32_t g = 0, lu = 0;
+      bool ok = true;
+      // S^T (dP^T) of block gg into its one buffer: free, since the product that read the P^T
+      // (dS^T) of the block before in it was issued before
+      auto scores = [&](uint32_t gg) -> bool {
+        const uint32_t s = gg & 1u;
+        if (!warp_wait_f(&c->qfull[s], gg >> 1, c, p.limit_ns)) return false;
         tc_fence_after();
+        const uint64_t q0 = dplus(dAQ, s * 16384u);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma2_bf16(tmem + 256, dplus(dPT, (k >> 2) * 16384 + (k & 3) * 32), dplus(dBm, 16384 + k * 2048), IDESC_KM,
-                      (!first || k) ? 1u : 0u);
+            mma2_bf16(tmem, dplus(dK, (k >> 2) * 16384 + (k & 3) * 32), dplus(q0, (k >> 2) * 8192 + (k & 3) * 32),
+                      IDESC_KK, k ? 1u : 0u);
+          commit2_mc(&c->qempty[s], 3);
+          commit2_mc(&c->sfull, 3);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto grads = [&](uint32_t gg, bool last) -> bool {
+        const uint32_t s = gg & 1u;
+        if (!warp_wait_f(&c->ofull[s], gg >> 1, c, p.limit_ns)) return false;
+        tc_fence_after();
+        const uint64_t o0 = dplus(dAO, s * 16384u);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma2_bf16(tmem + 384, dplus(dDST, (k >> 2) * 16384 + (k & 3) * 32), dplus(dBm, k * 2048), IDESC_KM,
-                      (!first || k) ? 1u : 0u);
-          commit2_mc(&c->bempty[0], 3);
-          commit2_mc(&c->ofree, 3);
+            mma2_bf16(tmem + KT_DP, dplus(dV, (k >> 2) * 16384 + (k & 3) * 32),
+                      dplus(o0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+          commit2_mc(&c->oempty[s], 3);
+          commit2_mc(&c->dpfull, 3);
+          if (last) commit2_mc(&c->rempty, 3);
         }
         __syncwarp();
         return true;
@@ -591,35 +606,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         S::kv_unit(p, u, w);
         const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
-        if (!warp_wait_f(&c->rfull, phr, c, p.limit_ns)) { ok = false; break; }
-        phr ^= 1u;
-        tc_fence_after();
+        if (!warp_wait_f(&c->rfull, lu, c, p.limit_ns)) { ok = false; break; }
+        if (!scores(g) || !grads(g, nblk == 1)) { ok = false; break; }
         for (int n = 0; n < nblk; ++n, ++g) {
-          // S^T and dP^T of block g; the previous block's accumulation follows, so the
-          // epilogue's work on block g overlaps it
-          if (!warp_wait_n(&c->tempty, tempty_seen, g, c, p.limit_ns)) { ok = false; break; }
-          if (!warp_wait_f(&c->afull[sa], pha, c, p.limit_ns)) { ok = false; break; }
+          // dV += P^T dO (the unit's first overwrites)
+          if (!warp_wait_c(&c->pready, g, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_f(&c->bofull, g, c, p.limit_ns)) { ok = false; break; }
+          if (n == 0 && !warp_wait_c(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t dst = dplus(dA, sa * KV_A_STAGE);
+          if (elect_one()) {
+            // P^T: 16 columns at the start of each epilogue warp's 32
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma2_bf16_ts(tmem + KT_DV, tmem + 32 * (k >> 1) + 8 * (k & 1), dplus(dBO, k * 2048), IDESC_KM,
+                           (n || k) ? 1u : 0u);
+            commit2_mc(&c->boempty, 3);
+          }
+          __syncwarp();
+          if (n + 1 < nblk && !scores(g + 1)) { ok = false; break; }
+          // dK += dS^T Q
+          if (!warp_wait_c(&c->dsready, g, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_f(&c->bqfull, g, c, p.limit_ns)) { ok = false; break; }
+          tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma2_bf16(tmem, dplus(dK, (k >> 2) * 16384 + (k & 3) * 32), dplus(dst, (k >> 2) * 8192 + (k & 3) * 32),
-                        IDESC_KK, k ? 1u : 0u);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma2_bf16(tmem + 128, dplus(dV, (k >> 2) * 16384 + (k & 3) * 32),
-                        dplus(dst, 16384 + (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
-            commit2_mc(&c->aempty[sa], 3);
-            commit2_mc(&c->tfull, 3);
-            if (n == nblk - 1) commit2_mc(&c->rempty, 3);
+              mma2_bf16_ts(tmem + KT_DK, tmem + KT_DP + 32 * (k >> 1) + 8 * (k & 1), dplus(dBQ, k * 2048), IDESC_KM,
+                           (n || k) ? 1u : 0u);
+            commit2_mc(&c->bqempty, 3);
+            if (n == nblk - 1) commit2_mc(&c->accfull, 3);
           }
           __syncwarp();
-          if (++sa == 2) { sa = 0; pha ^= 1u; }
-          if (n >= 1 && !accumulate(g - 1, n == 1)) { ok = false; break; }
+          if (n + 1 < nblk && !grads(g + 1, n + 2 == nblk)) { ok = false; break; }
         }
         if (!ok) break;
-        if (!accumulate(g - 1, nblk == 1)) { ok = false; break; }
         ++lu;
       }
       if (elect_one()) {
@@ -631,29 +651,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
     __syncwarp();
   } else if (warp == KV_FWD_WARP) {
     if (lane == 0) {
-      uint32_t te_seen = 0, or_seen = 0, g = 0;
+      uint32_t g = 0;
       bool ok = true;
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         KvUnit w;
         S::kv_unit(p, u, w);
         const int nblk = w.nh * w.nbl;
-        if (nblk == 0) continue;
-        for (int n = 0; n < nblk; ++n, ++g)
-          if (!forward_block(c, g, te_seen, or_seen, p.limit_ns)) { ok = false; break; }
+        for (int n = 0; n < nblk; ++n, ++g) {
+          if (!wait_c(&c->pready_l, g, c, p.limit_ns)) { ok = false; break; }
+          arrive_remote(mapa(saddr(&c->pready), 0));
+          if (!wait_c(&c->dsready_l, g, c, p.limit_ns)) { ok = false; break; }
+          arrive_remote(mapa(saddr(&c->dsready), 0));
+        }
       }
       if (!ok) fail_f(c, p.status);
     }
     __syncwarp();
   } else if (warp == KV_LD_WARP) {
-    // -lse * log2(e) and -D of each block's 128 queries into shared memory (one buffer,
-    // refilled once the epilogue warps have read it); loads issued a block ahead
+    // -lse * log2(e) (two stages) and -D of each block's 128 queries into shared memory;
+    // loads issued a block ahead
     float* ld = reinterpret_cast<float*>(base + KV_LD);
-    uint32_t lempty_seen = 0, g = 0;
-    for (int rnd = 0, u = pid; u < p.n_units; u = S::next_unit(++rnd, pid, npairs)) {
+    uint32_t g = 0;
+    bool ok = true;
+    for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
       KvUnit w;
       S::kv_unit(p, u, w);
       const int nblk = w.nh * w.nbl;
-      bool ok = true;
       for (int n = 0; n < nblk; ++n, ++g) {
         int z, b;
         kv_block(w, n, z, b);
@@ -666,27 +689,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           lv[i] = v ? p.lse[o] * L2E : 0.f;
           dv[i] = v ? p.D[o] : 0.f;
         }
-        if (!warp_wait_n(&c->lempty, lempty_seen, g, c, p.limit_ns)) { ok = false; break; }
+        const uint32_t s = g & 1u;
+        if (!warp_wait_c(&c->lempty[s], (g >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ld[lane + 32 * i] = -lv[i];
-          ld[128 + lane + 32 * i] = -dv[i];
-        }
+        for (int i = 0; i < 4; ++i) ld[128 * s + lane + 32 * i] = -lv[i];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->lfull);
-      }
-      if (!ok) {
-        fail_f(c, p.status);
-        break;
+        if (lane == 0) mbar_arrive(&c->lfull[s]);
+        if (!warp_wait_c(&c->dempty, g ^ 1u, c, p.limit_ns)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ld[256 + lane + 32 * i] = -dv[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->dfull);
       }
     }
+    if (!ok) fail_f(c, p.status);
   } else {
-    const int q = warp & 3, ch = (warp - 2) >> 2;   // lane quadrant; 64-column half of the block
-    const int lrow = q * 32 + lane;
-    const uint32_t trow = (uint32_t)(q * 32) << 16;
+    const int q = warp & 3, cg = (warp - 2) >> 2;   // lane quadrant, 32-column group
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(32 * cg);
     const float* ld = reinterpret_cast<const float*>(base + KV_LD);
-    uint32_t tfull_seen = 0, ofree_seen = 0, lfull_seen = 0, sfree_seen = 0, g = 0;
-    int lu = 0;
+    uint32_t g = 0, lu = 0;
     bool ok = true;
     for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
       KvUnit w;
@@ -699,7 +720,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       S::key_warp(p, kw, lo, hi, lo0, lo1, hi0, hi1);
       if constexpr (!S::kAddOut) {
         if (nblk == 0) {   // no query sees these keys
-          S::store_zero(p, w.plane, key, 64 * ch);
+          S::store_zero(p, w.plane, key, 32 * cg);
           continue;
         }
       }
@@ -707,67 +728,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         int z, b;
         kv_block(w, n, z, b);
         const typename S::Scale sc = S::scale_of(p, z);
-        if (!warp_wait_n(&c->tfull, tfull_seen, g + 1, c, p.limit_ns) ||
-            !warp_wait_n(&c->lfull, lfull_seen, g + 1, c, p.limit_ns)) { ok = false; break; }
+        const int qg = p.c0 + 128 * b + 32 * cg;   // first of this thread's 32 queries
+        const bool none = qg + 31 < lo0 || qg >= hi1, all = qg >= lo1 && qg + 31 < hi0;
+        const uint32_t s = g & 1u;
+        uint32_t rs[32], rd[32], w16[16];
+        typename S::Factors fac;
+        if (!warp_wait_c(&c->sfull, g, c, p.limit_ns) || !warp_wait_f(&c->lfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
-        uint32_t pw[2][16], dw[2][16];   // bf16 pairs of P^T and dS^T over this thread's 64 queries
+        __syncwarp();
+        tmem_ld32(trow, rs);
+        tmem_ld_wait();
+        if (none) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // the half's two 32-column groups, one after the other
-          const int cg = 2 * ch + h;
-          uint32_t rs[32], rd[32];
-          tmem_ld32(tmem + trow + (uint32_t)(32 * cg), rs);
-          tmem_ld32(tmem + trow + (uint32_t)(128 + 32 * cg), rd);
-          tmem_ld_wait();
-          if (h == 1) {   // S^T and dP^T are all in registers: the next block's may be formed
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->tempty_l);
-          }
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {   // two rounds of 16 queries
-            const int qg = p.c0 + 128 * b + 32 * cg + 16 * r;   // first query of the round
-            const bool none = qg + 15 < lo0 || qg >= hi1;
-            const bool all = qg >= lo1 && qg + 15 < hi0;
-            if (none) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) pw[h][8 * r + j] = dw[h][8 * r + j] = 0u;
-            } else if (all) {
-              kv_round<S, false>(rs, rd, 16 * r, ld + 32 * cg + 16 * r, sc, qg, key, lo, hi, &pw[h][8 * r],
-                               &dw[h][8 * r]);
-            } else {
-              kv_round<S, true>(rs, rd, 16 * r, ld + 32 * cg + 16 * r, sc, qg, key, lo, hi, &pw[h][8 * r],
-                              &dw[h][8 * r]);
-            }
-          }
+          for (int i = 0; i < 16; ++i) w16[i] = 0u;
+        } else if (all) {
+          kv_probs<S, false>(rs, ld + 128 * s + 32 * cg, sc, qg, key, lo, hi, w16, fac);
+        } else {
+          kv_probs<S, true>(rs, ld + 128 * s + 32 * cg, sc, qg, key, lo, hi, w16, fac);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->lempty);
-        // the previous block's accumulation has read P^T and dS^T; at a unit's first
-        // block, also the previous unit's dV / dK staging has left this area
-        if (!warp_wait_n(&c->ofree, ofree_seen, g, c, p.limit_ns) ||
-            (n == 0 && !warp_wait_n(&c->sfree, sfree_seen, (uint32_t)lu, c, p.limit_ns))) { ok = false; break; }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          store_half_row(sb + KV_PT + ch * 16384, lrow, h, pw[h]);
-          store_half_row(sb + KV_DST + ch * 16384, lrow, h, dw[h]);
-        }
-        fence_proxy_async();
+        tmem_st16(trow, w16);            // over this warp's own scores
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->oready_l);
+        if (lane == 0) {
+          mbar_arrive(&c->pready_l);
+          mbar_arrive(&c->lempty[s]);
+        }
+        if (!warp_wait_c(&c->dpfull, g, c, p.limit_ns) || !warp_wait_f(&c->dfull, g, c, p.limit_ns)) { ok = false; break; }
+        tc_fence_after();
+        __syncwarp();
+        tmem_ld32(trow + KT_DP, rd);
+        tmem_ld_wait();
+        if (none) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w16[i] = 0u;
+        } else if (all) {
+          kv_grads<S, false>(rs, rd, ld + 256 + 32 * cg, qg, lo, hi, fac, w16);
+        } else {
+          kv_grads<S, true>(rs, rd, ld + 256 + 32 * cg, qg, lo, hi, fac, w16);
+        }
+        __syncwarp();
+        tmem_st16(trow + KT_DP, w16);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&c->dsready_l);
+          mbar_arrive(&c->dempty);
+        }
       }
       if (!ok) break;
-      // the unit's dV and dK: out of tensor memory and, where the outputs are fp32 sums,
-      // through this warp's 8 KB of the P^T / dS^T area (one 4 KB block per 32 columns),
-      // added into them.  Each output element receives one add per launch; rows past T are
-      // clipped by the tensor map, rows in [c1, T) add 0.
-      if (!warp_wait_n(&c->ofree, ofree_seen, g, c, p.limit_ns)) { ok = false; break; }
+      // the unit's dV and dK out of tensor memory, 32 of hd: written, or, where the outputs are
+      // fp32 sums, added into them through this warp's staging block.  Each output element
+      // receives one add per launch; rows past T are clipped by the tensor map, rows in
+      // [c1, T) add 0.
+      if (!warp_wait_c(&c->accfull, lu, c, p.limit_ns)) { ok = false; break; }
+      ++lu;
       tc_fence_after();
-      const uint32_t stg = sb + KV_PT + (uint32_t)(warp - 2) * 8192u;
+      const uint32_t stg = sb + KV_STG + (uint32_t)(warp - 2) * 4096u;
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {   // t = 0: dV, t = 1: s dK
-        uint32_t ra[2][32];
-        tmem_ld32(tmem + trow + (uint32_t)((t ? 384 : 256) + 64 * ch), ra[0]);
-        tmem_ld32(tmem + trow + (uint32_t)((t ? 384 : 256) + 64 * ch + 32), ra[1]);
+        __syncwarp();
+        uint32_t ra[32];
+        tmem_ld32(trow + (t ? KT_DK : KT_DV), ra);
         tmem_ld_wait();
         if (t == 1) {   // both accumulators are in registers: the next unit may overwrite them
           tc_fence_before();
@@ -775,37 +799,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
         }
         if constexpr (!S::kAddOut) {
-          S::store_out(p, t, w.plane, key, 64 * ch, ra);
-          continue;
-        }
-        if (kw >= p.c1) continue;
-        if (t == 1) {
-          if (lane == 0) bulk_wait_read();
+          S::store_out(p, t, w.plane, key, 32 * cg, ra);
+        } else {
+          if (kw >= p.c1) continue;
+          if (lane == 0) bulk_wait_read();   // the block's previous contents have left
           __syncwarp();
-        }
-        const float f = t ? p.scale : 1.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t buf = stg + (uint32_t)h * 4096u + (uint32_t)lane * 128u;
+          const float f = t ? p.scale : 1.f;
+          const uint32_t buf = stg + (uint32_t)lane * 128u;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            sts128(buf + ((uint32_t)(k ^ (lane & 7)) << 4), __float_as_uint(__uint_as_float(ra[h][4 * k]) * f),
-                   __float_as_uint(__uint_as_float(ra[h][4 * k + 1]) * f),
-                   __float_as_uint(__uint_as_float(ra[h][4 * k + 2]) * f),
-                   __float_as_uint(__uint_as_float(ra[h][4 * k + 3]) * f));
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, 64 * ch, kw, w.zk);
-          tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg + 4096u, 64 * ch + 32, kw, w.zk);
-          bulk_commit();
+            sts128(buf + ((uint32_t)(k ^ (lane & 7)) << 4), __float_as_uint(__uint_as_float(ra[4 * k]) * f),
+                   __float_as_uint(__uint_as_float(ra[4 * k + 1]) * f), __float_as_uint(__uint_as_float(ra[4 * k + 2]) * f),
+                   __float_as_uint(__uint_as_float(ra[4 * k + 3]) * f));
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, 32 * cg, kw, w.zk);
+            bulk_commit();
+          }
         }
       }
-      if (lane == 0) bulk_wait_read();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c->sfree);
-      ++lu;
     }
     if (!ok) fail_f(c, p.status);
     if (lane == 0) bulk_wait_all();

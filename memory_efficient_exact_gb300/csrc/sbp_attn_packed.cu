@@ -3,6 +3,7 @@
 // sbp_attn_fwd.cu, the definition of what a query sees in sbp_attn_packed.cuh.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "sbp_attn_fused.cuh"
 #include "sbp_attn_packed.cuh"
@@ -143,29 +144,41 @@ struct PackedScores {
     return CAP ? mul2(mul2(p, d), dc) : mul2(p, d);
   }
 
-  // 64 columns of dV (t = 0) or dK (t = 1) of one key
+  struct NoFactors {};
+  struct CapFactors { uint32_t h[16]; };
+  using Factors = typename std::conditional<CAP, CapFactors, NoFactors>::type;
+  // 1 - tanh^2 of two scores as half-precision numbers in [0, 1]: 2^-11 of the value, an eighth of
+  // what rounding dS to bf16 does to it, and half the registers of fp32.
+  static __device__ __forceinline__ void keep(Factors& f, int i, float2 dc) {
+    if constexpr (CAP) {
+      const __half2 h = __floats2half2_rn(dc.x, dc.y);
+      f.h[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  static __device__ __forceinline__ float2 kept(const Factors& f, int i) {
+    if constexpr (CAP) return __half22float2(*reinterpret_cast<const __half2*>(&f.h[i]));
+    else return make_float2(1.f, 1.f);
+  }
+
+  // 32 columns of dV (t = 0) or dK (t = 1) of one key
   static __device__ __forceinline__ void store_out(const Kv& p, int t, int plane, int key, int c,
-                                                   const uint32_t (&ra)[2][32]) {
+                                                   const uint32_t (&ra)[32]) {
     if (key >= p.T) return;
     const int64_t row = ((int64_t)plane * p.T + key) * p.hd;
     const float f = t ? p.scale : 1.f;
     if (p.parts == 1) {
-      __nv_bfloat16* o = (t ? p.dK : p.dV) + row;
-      store_row(o, p.hd, c, ra[0], f);
-      store_row(o, p.hd, c + 32, ra[1], f);
+      store_row((t ? p.dK : p.dV) + row, p.hd, c, ra, f);
       return;
     }
     float4* o = reinterpret_cast<float4*>((t ? p.part_k : p.part_v) + row + c);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + 32 * h + 4 * k < p.hd)
-          o[8 * h + k] = make_float4(__uint_as_float(ra[h][4 * k]) * f, __uint_as_float(ra[h][4 * k + 1]) * f,
-                                     __uint_as_float(ra[h][4 * k + 2]) * f, __uint_as_float(ra[h][4 * k + 3]) * f);
+    for (int k = 0; k < 8; ++k)
+      if (c + 4 * k < p.hd)
+        o[k] = make_float4(__uint_as_float(ra[4 * k]) * f, __uint_as_float(ra[4 * k + 1]) * f,
+                           __uint_as_float(ra[4 * k + 2]) * f, __uint_as_float(ra[4 * k + 3]) * f);
   }
   static __device__ __forceinline__ void store_zero(const Kv& p, int plane, int key, int c) {
-    const uint32_t z[2][32] = {};
+    const uint32_t z[32] = {};
     store_out(p, 0, plane, key, c, z);
     store_out(p, 1, plane, key, c, z);
   }
