@@ -264,8 +264,8 @@ int sbp_attn_causal_backward_gqa(const void* Q, const void* K, const void* V, co
  * (Within the documents a value that is not finite may reach rows of a neighbouring
  * document, as 0 times infinity.)  The backward takes O and lse of the forward with the
  * same arguments.
- * hd: a multiple of 8, at most 128.  scale > 0, softcap >= 0, both finite.  Fixed order of
- * every sum: the same call gives the same bits.  Workspace, stream and error rules as for
+ * hd: a multiple of 8, at most 128.  scale > 0 and finite; softcap 0 or in [1e-6, 1e6].  Fixed
+ * order of every sum: the same call gives the same bits.  Workspace, stream and error rules as for
  * the LM-head calls (cu_seqlens and prefix_lens are read by the device only, so a captured
  * call follows their contents: a bad table sets SBP_ERR_SEQLENS); the workspace query
  * returns 0 for arguments no call accepts. */

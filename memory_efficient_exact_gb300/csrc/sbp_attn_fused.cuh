@@ -292,6 +292,7 @@ template <class S, bool MASK>
 __device__ __forceinline__ void kv_probs(uint32_t (&rs)[32], const float* nlse, const typename S::Scale& sc, int qg,
                                          int key, int lo, int hi, uint32_t (&pw)[16], typename S::Factors& fac) {
   const float4* l4 = reinterpret_cast<const float4*>(nlse);   // - lse log2 e
+  const float fd = (float)(qg - key);
 #pragma unroll
   for (int j4 = 0; j4 < 8; ++j4) {
     const float4 L = l4[j4];
@@ -300,7 +301,7 @@ __device__ __forceinline__ void kv_probs(uint32_t (&rs)[32], const float* nlse, 
       const int j = 4 * j4 + e;
       float2 dc;
       const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[j]), __uint_as_float(rs[j + 1])),
-                                 e ? make_float2(L.z, L.w) : make_float2(L.x, L.y), qg + j - key, 1, dc);
+                                 e ? make_float2(L.z, L.w) : make_float2(L.x, L.y), fd, (float)j, (float)(j + 1), dc);
       float2 pp = exp2_pair(x.x, x.y);
       if (MASK && (qg + j < lo || qg + j >= hi)) pp.x = 0.f;
       if (MASK && (qg + j + 1 < lo || qg + j + 1 >= hi)) pp.y = 0.f;
@@ -434,9 +435,9 @@ struct CausalScores {
   template <class P>
   static __device__ __forceinline__ Scale scale_of(const P& p, int) { return p.scale * L2E; }
   // log2 of the probabilities of two neighbouring pairs from their raw scores s, -lse in log2
-  // units and the distance query - key of the first (the second's is dist + step); dc: the
-  // factors of the scores' gradients.
-  static __device__ __forceinline__ float2 log2p2(Scale sl2, float2 s, float2 nlz, int, int, float2& dc) {
+  // units and their distances query - key, d + o0 and d + o1; dc: the factors of the scores'
+  // gradients.
+  static __device__ __forceinline__ float2 log2p2(Scale sl2, float2 s, float2 nlz, float, float, float, float2& dc) {
     dc = make_float2(1.f, 1.f);
     return fma2(s, make_float2(sl2, sl2), nlz);
   }
@@ -449,11 +450,12 @@ struct CausalScores {
   static __device__ __forceinline__ int tail_block(const P&) { return -1; }
 };
 
-// Block n of a unit: query head z, query block b.
-__device__ __forceinline__ void kv_block(const KvUnit& w, int n, int& z, int& b) {
-  const int h = n / w.nbl;
-  z = w.z0 + h;
-  b = w.b0 + (n - h * w.nbl);
+// A unit's blocks in order: query head z, query block b.  Returns whether z is another.
+__device__ __forceinline__ bool kv_next(const KvUnit& w, int& z, int& b) {
+  if (++b < w.b0 + w.nbl) return false;
+  b = w.b0;
+  ++z;
+  return true;
 }
 
 template <class S>
@@ -493,9 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           tma_load_3d_pair(sb + KV_V + hb * 16384, maps[KV_MV], fr, 64 * hb, krow, w.zk);
         }
         ++lu;
-        for (int n = 0; n < nblk; ++n) {
-          int z, b;
-          kv_block(w, n, z, b);
+        for (int n = 0, z = w.z0, b = w.b0; n < nblk; ++n, kv_next(w, z, b)) {
           const uint32_t s = g & 1u, ph = (g >> 1) ^ 1u;
           const int qrow = p.c0 + 128 * b + 64 * (int)rank;
           if (!wait_c(&c->qempty[s], ph, c, p.limit_ns)) { ok = false; break; }
@@ -534,9 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         KvUnit w;
         S::kv_unit(p, u, w);
         const int nblk = w.nh * w.nbl;
-        for (int n = 0; n < nblk; ++n) {
-          int z, b;
-          kv_block(w, n, z, b);
+        for (int n = 0, z = w.z0, b = w.b0; n < nblk; ++n, kv_next(w, z, b)) {
           const int qrow = p.c0 + 128 * b;
           if (!wait_c(&c->boempty, g ^ 1u, c, p.limit_ns)) { ok = false; break; }
           const uint32_t fo = mapa(saddr(&c->bofull), 0), fq = mapa(saddr(&c->bqfull), 0);
@@ -677,9 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       KvUnit w;
       S::kv_unit(p, u, w);
       const int nblk = w.nh * w.nbl;
-      for (int n = 0; n < nblk; ++n, ++g) {
-        int z, b;
-        kv_block(w, n, z, b);
+      for (int n = 0, z = w.z0, b = w.b0; n < nblk; ++n, ++g, kv_next(w, z, b)) {
         float lv[4], dv[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -724,10 +720,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           continue;
         }
       }
-      for (int n = 0; n < nblk; ++n, ++g) {
-        int z, b;
-        kv_block(w, n, z, b);
-        const typename S::Scale sc = S::scale_of(p, z);
+      typename S::Scale sc = S::scale_of(p, w.z0);
+      for (int n = 0, z = w.z0, b = w.b0; n < nblk; ++n, ++g) {
         const int qg = p.c0 + 128 * b + 32 * cg;   // first of this thread's 32 queries
         const bool none = qg + 31 < lo0 || qg >= hi1, all = qg >= lo1 && qg + 31 < hi0;
         const uint32_t s = g & 1u;
@@ -777,6 +771,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           mbar_arrive(&c->dsready_l);
           mbar_arrive(&c->dempty);
         }
+        if (kv_next(w, z, b) && n + 1 < nblk) sc = S::scale_of(p, z);
       }
       if (!ok) break;
       // the unit's dV and dK out of tensor memory, 32 of hd: written, or, where the outputs are
@@ -837,12 +832,13 @@ template <class S, bool MASK>
 __device__ __forceinline__ void q_block(const uint32_t (&rs)[32], const uint32_t (&rd)[32],
                                         const typename S::Scale& sc, float lz, float Dq, int kg, int qr, int lo, int hi,
                                         uint32_t (&dw)[16]) {
-  const float2 nD = make_float2(-Dq, -Dq);
+  const float2 nD = make_float2(-Dq, -Dq), nlz = make_float2(-lz, -lz);
+  const float fd = (float)(qr - kg);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float2 dc;
-    const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])),
-                               make_float2(-lz, -lz), qr - kg - 2 * i, -1, dc);
+    const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])), nlz, fd,
+                               (float)(-2 * i), (float)(-2 * i - 1), dc);
     float2 pp = exp2_pair(x.x, x.y);
     const bool o0 = MASK && (kg + 2 * i < lo || kg + 2 * i >= hi);
     const bool o1 = MASK && (kg + 2 * i + 1 < lo || kg + 2 * i + 1 >= hi);

@@ -131,11 +131,14 @@ __device__ __forceinline__ void scores32(uint32_t (&r)[32], int c, bool mask, co
   if (CAP || BIAS) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      float dc;
-      float x = pk::capped<CAP>(sc, __uint_as_float(r[i]), dc);
-      if (BIAS) x = fmaf(-sc.slope2, fabsf(w.fd - (float)(c + i)), x);
-      r[i] = __float_as_uint(x);
+      const float x = __uint_as_float(r[i]);
+      r[i] = __float_as_uint(CAP ? pk::capped(sc, x) : x * sc.sl2);
     }
+  }
+  if (BIAS) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      r[i] = __float_as_uint(fmaf(-sc.slope2, fabsf(w.fd - (float)(c + i)), __uint_as_float(r[i])));
   }
   if (mask) {
 #pragma unroll
@@ -150,12 +153,14 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], float m0) {
     m[(i >> 1) & 3] = max3(m[(i >> 1) & 3], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
   return max3(fmaxf(m[0], m[1]), m[2], fmaxf(m[3], __uint_as_float(r[31])));
 }
-// 32 probabilities 2^(mul x + nm): packed to bf16, their sum added to l.
+// 32 probabilities 2^(mul x + nm) (PLAIN: 2^x): packed to bf16, their sum added to l.
+template <bool PLAIN>
 __device__ __forceinline__ void probs32(const uint32_t (&r)[32], float mul, float nm, uint32_t* pw, float2& l) {
-  const float2 mul2 = make_float2(mul, mul), nm2 = make_float2(nm, nm);
+  const float2 m2 = make_float2(mul, mul), nm2 = make_float2(nm, nm);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float2 x = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), mul2, nm2);
+    float2 x = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    if (!PLAIN) x = fma2(x, m2, nm2);
     const float2 e = make_float2(ex2(x.x), ex2(x.y));
     l = add2(l, e);
     pw[i] = pack_bf16(e.x, e.y);
@@ -374,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int64_t ro = (int64_t)z * p.T + row;
       const int lo = vrow ? p.lo[row] : p.T, hi = vrow ? p.hi[row] : p.T;
       const int lo1 = __shfl_sync(0xffffffffu, lo, 31), hi0 = __shfl_sync(0xffffffffu, hi, 0);
-      const pk::ScaleZ sc{p.sc.sl2, p.sc.c2, p.sc.k, BIAS ? p.slopes[z] * L2E : 0.f};
+      const pk::ScaleZ sc = pk::scale_z(p.sc, BIAS ? p.slopes[z] : 0.f);
       float m = FIXED ? 0.f : -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       for (int n = (int)((g ^ (uint32_t)grp) & 1u); n < nj; n += 2) {   // this group's blocks
@@ -425,16 +430,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
         const float nm = m == -INFINITY ? 0.f : -m * mul;
-        probs32(ra, mul, nm, pw, l2);
+        probs32<FIXED>(ra, mul, nm, pw, l2);
         tmem_ld32(tS + 64, ra);
-        probs32(rb, mul, nm, pw + 16, l2);
+        probs32<FIXED>(rb, mul, nm, pw + 16, l2);
         tmem_ld32(tS + 96, rb);
         tmem_st32(tS, pw);          // keys 0 .. 63: over scores that are in registers
         tmem_ld_wait();
         scores32<CAP, BIAS>(ra, 64, mask, w, sc);
         scores32<CAP, BIAS>(rb, 96, mask, w, sc);
-        probs32(ra, mul, nm, pw, l2);
-        probs32(rb, mul, nm, pw + 16, l2);
+        probs32<FIXED>(ra, mul, nm, pw, l2);
+        probs32<FIXED>(rb, mul, nm, pw + 16, l2);
         __syncwarp();
         tmem_st32(tS + 32, pw);
         tmem_st_wait();

@@ -123,20 +123,23 @@ struct PackedScores {
   static __device__ __forceinline__ int tail_block(const P& p) { return *p.tail; }
   template <class P>
   static __device__ __forceinline__ Scale scale_of(const P& p, int z) {
-    return Scale{p.sc.sl2, p.sc.c2, p.sc.k, BIAS ? p.slopes[z] * L2E : 0.f};
+    return scale_z(p.sc, BIAS ? p.slopes[z] : 0.f);
   }
-  static __device__ __forceinline__ float2 log2p2(const Scale& sc, float2 s, float2 nlz, int dist, int step,
+  static __device__ __forceinline__ float2 log2p2(const Scale& sc, float2 s, float2 nlz, float d, float o0, float o1,
                                                   float2& dc) {
     float2 x;
     if (CAP) {
-      x = add2(make_float2(capped<true>(sc, s.x, dc.x), capped<true>(sc, s.y, dc.y)), nlz);
+      x = make_float2(capped(sc, s.x), capped(sc, s.y));
+      const float2 th = mul2(x, make_float2(sc.ic2, sc.ic2));
+      dc = fma2(make_float2(-th.x, -th.y), th, make_float2(1.f, 1.f));   // 1 - tanh^2
+      x = add2(x, nlz);
     } else {
       dc = make_float2(1.f, 1.f);
       x = fma2(s, make_float2(sc.sl2, sc.sl2), nlz);
     }
     if (BIAS) {
-      x.x = fmaf(-sc.slope2, fabsf((float)dist), x.x);
-      x.y = fmaf(-sc.slope2, fabsf((float)(dist + step)), x.y);
+      x.x = fmaf(-sc.slope2, fabsf(d + o0), x.x);
+      x.y = fmaf(-sc.slope2, fabsf(d + o1), x.y);
     }
     return x;
   }
@@ -474,6 +477,7 @@ int packed_check(const PackedArgs& a, std::initializer_list<const void*> tensors
   if (!(a.scale > 0.f) || std::isinf(a.scale) || !(a.softcap >= 0.f) || std::isinf(a.softcap))
     return SBP_ERR_INVALID_ARG;
   if ((a.cu && a.n_seq < 1) || (!a.cu && a.n_seq != 0)) return SBP_ERR_INVALID_ARG;
+  if (a.softcap > 0.f && (a.softcap < 1e-6f || a.softcap > 1e6f)) return SBP_ERR_UNSUPPORTED;
   if (!packed_layout(a.H, a.Hkv, a.T, a.hd, L)) return SBP_ERR_UNSUPPORTED;
   for (const void* q : tensors) {
     if (!q && a.T > 0) return SBP_ERR_INVALID_ARG;

@@ -35,7 +35,7 @@ def test_attention(sbp, backward):
     cases = [(I, dict(Q=None)), (I, dict(lse=None)), (I, dict(st=None)), (I, dict(T=-1)), (I, dict(H=0)), (I, dict(Hkv=3)),
              (I, dict(Hkv=8)), (I, dict(hd=0)), (I, dict(n=0)), (I, dict(cu=None)), (I, dict(scale=0.0)),
              (I, dict(scale=-1.0)), (I, dict(scale=float("nan"))), (I, dict(scale=float("inf"))), (I, dict(cap=-1.0)),
-             (I, dict(cap=float("nan"))), (I, dict(cap=float("inf"))), (U, dict(hd=60)), (U, dict(hd=136)),
+             (I, dict(cap=float("nan"))), (I, dict(cap=float("inf"))), (U, dict(cap=1e-7)), (U, dict(cap=1e7)), (U, dict(hd=60)), (U, dict(hd=136)),
              (U, dict(T=1 << 31)), (L, dict(K=0x2008)), (L, dict(cu=0x7002)), (L, dict(sl=0x7001)),
              (W, dict(ws=0x100010)), (W, dict(wsb=16)), (W, dict(ws=None))]
     if backward:
