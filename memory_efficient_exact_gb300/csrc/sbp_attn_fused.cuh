@@ -281,54 +281,79 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// 16 lanes (rows) x 32 columns as accumulator fragments: of column group g (8 columns) thread t
+// holds row t / 4, columns 2 (t % 4) and + 1, in r[4 g] and r[4 g + 1], and row t / 4 + 8 in the
+// next two.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// The same fragment packed to bf16 pairs, 16 columns: of group g row t / 4 in r[2 g], row
+// t / 4 + 8 in r[2 g + 1], at column 4 g + t % 4.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // ================================================================ k_attn_kv (dK, dV)
 
-// k_attn_kv's epilogue: 32 queries of this thread's key row.  First P^T = 2^(s S^T - lse
-// log2 e), kept in fp32 (over the scores) and packed to bf16 pairs, with the factors of the
-// scores' gradients where a policy has them; then dS^T = P^T (dP^T - D).  MASK: some key of
-// the warp is not seen by all 32 queries; the other blocks skip the per-element test (it
-// costs more than the math it guards).
+// k_attn_kv's epilogue, a warp's 32 keys x 32 queries.  First P^T = 2^(s S^T - lse log2 e), kept
+// in fp32 (over the scores) and packed to bf16 pairs, with the factors of the scores' gradients
+// where a policy has them; then dS^T = P^T (dP^T - D).  The scores are held as accumulator
+// fragments, [half of 16 keys][tmem_ld_frag], so that a thread meets 8 of the 32 queries
+// only: their lse and D come from shared memory in 8 loads a block, where a key row a thread
+// took 64 floats, a wavefront each, and the two kept the shared-memory pipe busy for
+// half of the epilogue.
+// MASK: some key of the warp is not seen by all 32 queries; the other blocks skip the
+// per-element test (it costs more than the math it guards).
+struct KvRows {
+  int lo[4], hi[4];   // queries that see the thread's keys kw + 16 h + 8 e + lane / 4, at 2 h + e
+  float key[4];       // those keys
+};
 template <class S, bool MASK>
-__device__ __forceinline__ void kv_probs(uint32_t (&rs)[32], const float* nlse, const typename S::Scale& sc, int qg,
-                                         int key, int lo, int hi, uint32_t (&pw)[16], typename S::Factors& fac) {
-  const float4* l4 = reinterpret_cast<const float4*>(nlse);   // - lse log2 e
-  const float fd = (float)(qg - key);
+__device__ __forceinline__ void kv_probs(uint32_t (&rs)[2][16], const float2 (&nlse)[4], const typename S::Scale& sc, int q0,
+                                         const KvRows& w, uint32_t (&pw)[2][8], typename S::Factors& fac) {
 #pragma unroll
-  for (int j4 = 0; j4 < 8; ++j4) {
-    const float4 L = l4[j4];
+  for (int he = 0; he < 4; ++he) {
+    const int h = he >> 1, e = he & 1;
+    const float fd = (float)q0 - w.key[he];
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      const int j = 4 * j4 + e;
+    for (int g = 0; g < 4; ++g) {
+      uint32_t &r0 = rs[h][4 * g + 2 * e], &r1 = rs[h][4 * g + 2 * e + 1];
       float2 dc;
-      const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[j]), __uint_as_float(rs[j + 1])),
-                                 e ? make_float2(L.z, L.w) : make_float2(L.x, L.y), fd, (float)j, (float)(j + 1), dc);
+      const float2 x = S::log2p2(sc, make_float2(__uint_as_float(r0), __uint_as_float(r1)), nlse[g], fd, (float)(8 * g),
+                                 (float)(8 * g + 1), dc);
       float2 pp = exp2_pair(x.x, x.y);
-      if (MASK && (qg + j < lo || qg + j >= hi)) pp.x = 0.f;
-      if (MASK && (qg + j + 1 < lo || qg + j + 1 >= hi)) pp.y = 0.f;
-      pw[j / 2] = pack_bf16(pp.x, pp.y);
-      S::keep(fac, j / 2, dc);
-      rs[j] = __float_as_uint(pp.x);
-      rs[j + 1] = __float_as_uint(pp.y);
+      const int q = q0 + 8 * g;
+      if (MASK && (q < w.lo[he] || q >= w.hi[he])) pp.x = 0.f;
+      if (MASK && (q + 1 < w.lo[he] || q + 1 >= w.hi[he])) pp.y = 0.f;
+      pw[h][2 * g + e] = pack_bf16(pp.x, pp.y);
+      S::keep(fac, 4 * he + g, dc);
+      r0 = __float_as_uint(pp.x);
+      r1 = __float_as_uint(pp.y);
     }
   }
 }
 template <class S, bool MASK>
-__device__ __forceinline__ void kv_grads(const uint32_t (&rp)[32], const uint32_t (&rd)[32], const float* nD, int qg, int lo,
-                                         int hi, const typename S::Factors& fac, uint32_t (&dw)[16]) {
-  const float4* d4 = reinterpret_cast<const float4*>(nD);     // - D
+__device__ __forceinline__ void kv_grads(const uint32_t (&rp)[2][16], const uint32_t (&rd)[2][16], const float2 (&nD)[4], int q0,
+                                         const KvRows& w, const typename S::Factors& fac, uint32_t (&dw)[2][8]) {
 #pragma unroll
-  for (int j4 = 0; j4 < 8; ++j4) {
-    const float4 Dv = d4[j4];
+  for (int he = 0; he < 4; ++he) {
+    const int h = he >> 1, e = he & 1;
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      const int j = 4 * j4 + e;
-      float2 sv = S::grad2(make_float2(__uint_as_float(rp[j]), __uint_as_float(rp[j + 1])),
-                           add2(make_float2(__uint_as_float(rd[j]), __uint_as_float(rd[j + 1])),
-                                e ? make_float2(Dv.z, Dv.w) : make_float2(Dv.x, Dv.y)),
-                           S::kept(fac, j / 2));
-      if (S::kClearMasked && MASK && (qg + j < lo || qg + j >= hi)) sv.x = 0.f;
-      if (S::kClearMasked && MASK && (qg + j + 1 < lo || qg + j + 1 >= hi)) sv.y = 0.f;
-      dw[j / 2] = pack_bf16(sv.x, sv.y);
+    for (int g = 0; g < 4; ++g) {
+      const int i = 4 * g + 2 * e;
+      float2 sv = S::grad2(make_float2(__uint_as_float(rp[h][i]), __uint_as_float(rp[h][i + 1])),
+                           add2(make_float2(__uint_as_float(rd[h][i]), __uint_as_float(rd[h][i + 1])), nD[g]),
+                           S::kept(fac, 4 * he + g));
+      const int q = q0 + 8 * g;
+      if (S::kClearMasked && MASK && (q < w.lo[he] || q >= w.hi[he])) sv.x = 0.f;
+      if (S::kClearMasked && MASK && (q + 1 < w.lo[he] || q + 1 >= w.hi[he])) sv.y = 0.f;
+      dw[h][2 * g + e] = pack_bf16(sv.x, sv.y);
     }
   }
 }
@@ -714,6 +739,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       int lo, hi, lo0, lo1, hi0, hi1;   // queries that see this thread's key; over the warp's keys
       S::key_range(p, key, lo, hi);
       S::key_warp(p, kw, lo, hi, lo0, lo1, hi0, hi1);
+      KvRows rows;
+#pragma unroll
+      for (int he = 0; he < 4; ++he) {
+        rows.lo[he] = __shfl_sync(0xffffffffu, lo, 8 * he + lane / 4);
+        rows.hi[he] = __shfl_sync(0xffffffffu, hi, 8 * he + lane / 4);
+        rows.key[he] = (float)(kw + 8 * he + lane / 4);
+      }
       if constexpr (!S::kAddOut) {
         if (nblk == 0) {   // no query sees these keys
           S::store_zero(p, w.plane, key, 32 * cg);
@@ -725,23 +757,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         const int qg = p.c0 + 128 * b + 32 * cg;   // first of this thread's 32 queries
         const bool none = qg + 31 < lo0 || qg >= hi1, all = qg >= lo1 && qg + 31 < hi0;
         const uint32_t s = g & 1u;
-        uint32_t rs[32], rd[32], w16[16];
+        uint32_t rs[2][16], rd[2][16], pk[2][8];
+        float2 st[4];                              // lse, then D, of the thread's queries
+        const int q0 = qg + 2 * (lane & 3);        // the first of them
+        const float2* ldq = reinterpret_cast<const float2*>(ld) + 16 * cg + (lane & 3);
         typename S::Factors fac;
         if (!warp_wait_c(&c->sfull, g, c, p.limit_ns) || !warp_wait_f(&c->lfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         __syncwarp();
-        tmem_ld32(trow, rs);
+        tmem_ld_frag(trow, rs[0]);
+        tmem_ld_frag(trow + (16u << 16), rs[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[i] = ldq[64 * s + 4 * i];
         tmem_ld_wait();
         if (none) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w16[i] = 0u;
+          for (int i = 0; i < 8; ++i) pk[0][i] = pk[1][i] = 0u;
         } else if (all) {
-          kv_probs<S, false>(rs, ld + 128 * s + 32 * cg, sc, qg, key, lo, hi, w16, fac);
+          kv_probs<S, false>(rs, st, sc, q0, rows, pk, fac);
         } else {
-          kv_probs<S, true>(rs, ld + 128 * s + 32 * cg, sc, qg, key, lo, hi, w16, fac);
+          kv_probs<S, true>(rs, st, sc, q0, rows, pk, fac);
         }
         __syncwarp();
-        tmem_st16(trow, w16);            // over this warp's own scores
+        tmem_st_frag(trow, pk[0]);                 // over this warp's own scores
+        tmem_st_frag(trow + (16u << 16), pk[1]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -752,18 +791,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         if (!warp_wait_c(&c->dpfull, g, c, p.limit_ns) || !warp_wait_f(&c->dfull, g, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         __syncwarp();
-        tmem_ld32(trow + KT_DP, rd);
+        tmem_ld_frag(trow + KT_DP, rd[0]);
+        tmem_ld_frag(trow + KT_DP + (16u << 16), rd[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[i] = ldq[128 + 4 * i];
         tmem_ld_wait();
         if (none) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w16[i] = 0u;
+          for (int i = 0; i < 8; ++i) pk[0][i] = pk[1][i] = 0u;
         } else if (all) {
-          kv_grads<S, false>(rs, rd, ld + 256 + 32 * cg, qg, lo, hi, fac, w16);
+          kv_grads<S, false>(rs, rd, st, q0, rows, fac, pk);
         } else {
-          kv_grads<S, true>(rs, rd, ld + 256 + 32 * cg, qg, lo, hi, fac, w16);
+          kv_grads<S, true>(rs, rd, st, q0, rows, fac, pk);
         }
         __syncwarp();
-        tmem_st16(trow + KT_DP, w16);
+        tmem_st_frag(trow + KT_DP, pk[0]);
+        tmem_st_frag(trow + KT_DP + (16u << 16), pk[1]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
