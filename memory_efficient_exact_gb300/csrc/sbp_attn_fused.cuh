@@ -38,16 +38,16 @@ namespace sbp {
 namespace tc {
 namespace fa {
 
-// Warps: 0 TMA producers, 1 MMA issuer, then the epilogue warps (lane quadrant warp % 4),
-// then (k_attn_kv) one warp that stages lse and D per block, and one forwarder warp.  The
-// epilogue warps arrive on CTA-local barriers; the forwarder turns each completed local
+// Warps: 0 TMA producers, 1 MMA issuer (leader CTA) or forwarder (the other CTA), then the
+// epilogue warps (lane quadrant warp % 4, 32 of the 128 columns each), then (k_attn_kv) one
+// warp that stages lse and D per block.  The epilogue warps arrive on CTA-local barriers,
+// which the leader's MMA warp waits on; the other CTA's forwarder turns each completed local
 // phase into one arrival at the leader, which keeps the remote arrival's latency off the
 // epilogue's critical path.
-// Sixteen epilogue warps of 32 of the 128 columns each (96 registers a thread).
 constexpr int Q_EPI = 16, KV_EPI = 16;
-constexpr int KV_LD_WARP = 2 + KV_EPI, KV_FWD_WARP = KV_LD_WARP + 1, Q_FWD_WARP = 2 + Q_EPI;
-constexpr int KV_THREADS = 32 * (KV_FWD_WARP + 1);
-constexpr int Q_THREADS = 32 * (Q_FWD_WARP + 1);
+constexpr int KV_LD_WARP = 2 + KV_EPI;
+constexpr int KV_THREADS = 32 * (KV_LD_WARP + 1);   // five warps a scheduler: 96 registers a thread
+constexpr int Q_THREADS = 32 * (2 + Q_EPI);
 constexpr uint32_t IDESC_KK = idesc_bf16(256, 128, false, false);  // A, B K-major
 constexpr uint32_t IDESC_KM = idesc_bf16(256, 128, false, true);   // A K-major, B MN-major
 
@@ -77,9 +77,9 @@ constexpr uint32_t QT_DP = 256, QT_DQ = 384;
 struct CtrlQ {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], yfull[2], yempty[2];
   uint64_t rfull[2], rempty[2];   // the unit's Q and dO
-  uint64_t tfull, tempty;         // S and dP of the block are ready; dP has been read (leader, one per CTA)
-  uint64_t oready[2];             // dS buffer is written (leader, one per CTA)
-  uint64_t tempty_l, oready_l[2]; // the CTA's epilogue warps, forwarded
+  uint64_t tfull;                 // S and dP of the block are ready
+  uint64_t tempty_l, oready_l[2]; // dP has been read, dS buffer is written: the CTA's epilogue warps
+  uint64_t tempty_r, oready_r[2]; // the same of the other CTA (leader)
   uint64_t dqfull, accempty;      // the unit's dQ is complete; has been read out (leader)
   uint64_t mdone;
   uint32_t tmem_base;
@@ -91,8 +91,8 @@ struct CtrlF {
   uint64_t bqfull, bqempty, bofull, boempty;           // the same 128 queries x half of hd
   uint64_t rfull, rempty;        // the unit's K and V
   uint64_t sfull, dpfull;        // S^T / dP^T of the block is ready (both CTAs)
-  uint64_t pready, dsready;      // P^T / dS^T is written (leader, one per CTA)
-  uint64_t pready_l, dsready_l;  // the CTA's epilogue warps, forwarded
+  uint64_t pready_l, dsready_l;  // P^T / dS^T is written: the CTA's epilogue warps
+  uint64_t pready_r, dsready_r;  // the same of the other CTA (leader)
   uint64_t accfull, accempty;    // the unit's dV and dK are complete; have been read out (leader)
   uint64_t lfull[2], lempty[2], dfull, dempty;   // lse (2 stages) and D of the block
   uint64_t mdone;
@@ -136,8 +136,8 @@ __device__ __forceinline__ void prologue_f(CtrlF* c, int warp) {
     mbar_init(&c->rempty, 1);
     mbar_init(&c->sfull, 1);
     mbar_init(&c->dpfull, 1);
-    mbar_init(&c->pready, 2);
-    mbar_init(&c->dsready, 2);
+    mbar_init(&c->pready_r, 1);
+    mbar_init(&c->dsready_r, 1);
     mbar_init(&c->pready_l, KV_EPI);
     mbar_init(&c->dsready_l, KV_EPI);
     mbar_init(&c->accfull, 1);
@@ -161,11 +161,11 @@ __device__ __forceinline__ void prologue_q(CtrlQ* c, int warp) {
       mbar_init(&c->yempty[i], 1);
       mbar_init(&c->rfull[i], 1);
       mbar_init(&c->rempty[i], 1);
-      mbar_init(&c->oready[i], 2);
+      mbar_init(&c->oready_r[i], 1);
       mbar_init(&c->oready_l[i], Q_EPI);
     }
     mbar_init(&c->tfull, 1);
-    mbar_init(&c->tempty, 2);
+    mbar_init(&c->tempty_r, 1);
     mbar_init(&c->tempty_l, Q_EPI);
     mbar_init(&c->dqfull, 1);
     mbar_init(&c->accempty, 2 * Q_EPI);
@@ -227,6 +227,11 @@ __device__ __forceinline__ bool wait_c(uint64_t* b, uint32_t parity, C* c, uint6
 template <class C>
 __device__ __forceinline__ bool warp_wait_c(uint64_t* b, uint32_t parity, C* c, uint64_t limit) {
   return __all_sync(0xffffffffu, wait_c(b, parity, c, limit));
+}
+// The leader's wait for both CTAs' epilogue warps: its own barrier and the forwarded one.
+template <class C>
+__device__ __forceinline__ bool warp_wait_pair(uint64_t* local, uint64_t* remote, uint32_t parity, C* c, uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_inl<false>(local, parity & 1u, &c->abort, limit) && wait_c(remote, parity, c, limit));
 }
 
 __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
@@ -311,49 +316,59 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
 // MASK: some key of the warp is not seen by all 32 queries; the other blocks skip the
 // per-element test (it costs more than the math it guards).
 struct KvRows {
-  int lo[4], hi[4];   // queries that see the thread's keys kw + 16 h + 8 e + lane / 4, at 2 h + e
-  float key[4];       // those keys
+  int lo, hi;     // queries that see key kw + lane; fragment row 2 h + e is key kw + 16 h + 8 e + lane / 4
+  float key;      // fragment row 0
 };
 template <class S, bool MASK>
-__device__ __forceinline__ void kv_probs(uint32_t (&rs)[2][16], const float2 (&nlse)[4], const typename S::Scale& sc, int q0,
-                                         const KvRows& w, uint32_t (&pw)[2][8], typename S::Factors& fac) {
+__device__ __forceinline__ void kv_probs(uint32_t (&r)[16], int h, const float2 (&nlse)[4], const typename S::Scale& sc,
+                                         int q0, const KvRows& w, uint32_t (&pw)[8], typename S::Factors& fac) {
 #pragma unroll
-  for (int he = 0; he < 4; ++he) {
-    const int h = he >> 1, e = he & 1;
-    const float fd = (float)q0 - w.key[he];
+  for (int e = 0; e < 2; ++e) {
+    const int row = 16 * h + 8 * e;
+    const float fd = (float)q0 - (w.key + (float)row);
+    int lo = 0, hi = 0;
+    if (MASK) {
+      lo = __shfl_sync(0xffffffffu, w.lo, row + (threadIdx.x & 31) / 4);
+      hi = __shfl_sync(0xffffffffu, w.hi, row + (threadIdx.x & 31) / 4);
+    }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      uint32_t &r0 = rs[h][4 * g + 2 * e], &r1 = rs[h][4 * g + 2 * e + 1];
+      uint32_t &r0 = r[4 * g + 2 * e], &r1 = r[4 * g + 2 * e + 1];
       float2 dc;
       const float2 x = S::log2p2(sc, make_float2(__uint_as_float(r0), __uint_as_float(r1)), nlse[g], fd, (float)(8 * g),
                                  (float)(8 * g + 1), dc);
       float2 pp = exp2_pair(x.x, x.y);
       const int q = q0 + 8 * g;
-      if (MASK && (q < w.lo[he] || q >= w.hi[he])) pp.x = 0.f;
-      if (MASK && (q + 1 < w.lo[he] || q + 1 >= w.hi[he])) pp.y = 0.f;
-      pw[h][2 * g + e] = pack_bf16(pp.x, pp.y);
-      S::keep(fac, 4 * he + g, dc);
+      if (MASK && (q < lo || q >= hi)) pp.x = 0.f;
+      if (MASK && (q + 1 < lo || q + 1 >= hi)) pp.y = 0.f;
+      pw[2 * g + e] = pack_bf16(pp.x, pp.y);
+      S::keep(fac, 8 * h + 4 * e + g, dc);
       r0 = __float_as_uint(pp.x);
       r1 = __float_as_uint(pp.y);
     }
   }
 }
 template <class S, bool MASK>
-__device__ __forceinline__ void kv_grads(const uint32_t (&rp)[2][16], const uint32_t (&rd)[2][16], const float2 (&nD)[4], int q0,
-                                         const KvRows& w, const typename S::Factors& fac, uint32_t (&dw)[2][8]) {
+__device__ __forceinline__ void kv_grads(const uint32_t (&rp)[16], const uint32_t (&rd)[16], int h, const float2 (&nD)[4],
+                                         int q0, const KvRows& w, const typename S::Factors& fac, uint32_t (&dw)[8]) {
 #pragma unroll
-  for (int he = 0; he < 4; ++he) {
-    const int h = he >> 1, e = he & 1;
+  for (int e = 0; e < 2; ++e) {
+    const int row = 16 * h + 8 * e;
+    int lo = 0, hi = 0;
+    if (S::kClearMasked && MASK) {
+      lo = __shfl_sync(0xffffffffu, w.lo, row + (threadIdx.x & 31) / 4);
+      hi = __shfl_sync(0xffffffffu, w.hi, row + (threadIdx.x & 31) / 4);
+    }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int i = 4 * g + 2 * e;
-      float2 sv = S::grad2(make_float2(__uint_as_float(rp[h][i]), __uint_as_float(rp[h][i + 1])),
-                           add2(make_float2(__uint_as_float(rd[h][i]), __uint_as_float(rd[h][i + 1])), nD[g]),
-                           S::kept(fac, 4 * he + g));
+      float2 sv = S::grad2(make_float2(__uint_as_float(rp[i]), __uint_as_float(rp[i + 1])),
+                           add2(make_float2(__uint_as_float(rd[i]), __uint_as_float(rd[i + 1])), nD[g]),
+                           S::kept(fac, 8 * h + 4 * e + g));
       const int q = q0 + 8 * g;
-      if (S::kClearMasked && MASK && (q < w.lo[he] || q >= w.hi[he])) sv.x = 0.f;
-      if (S::kClearMasked && MASK && (q + 1 < w.lo[he] || q + 1 >= w.hi[he])) sv.y = 0.f;
-      dw[h][2 * g + e] = pack_bf16(sv.x, sv.y);
+      if (S::kClearMasked && MASK && (q < lo || q >= hi)) sv.x = 0.f;
+      if (S::kClearMasked && MASK && (q + 1 < lo || q + 1 >= hi)) sv.y = 0.f;
+      dw[2 * g + e] = pack_bf16(sv.x, sv.y);
     }
   }
 }
@@ -633,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         if (!scores(g) || !grads(g, nblk == 1)) { ok = false; break; }
         for (int n = 0; n < nblk; ++n, ++g) {
           // dV += P^T dO (the unit's first overwrites)
-          if (!warp_wait_c(&c->pready, g, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_pair(&c->pready_l, &c->pready_r, g, c, p.limit_ns)) { ok = false; break; }
           if (!warp_wait_f(&c->bofull, g, c, p.limit_ns)) { ok = false; break; }
           if (n == 0 && !warp_wait_c(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
@@ -648,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           __syncwarp();
           if (n + 1 < nblk && !scores(g + 1)) { ok = false; break; }
           // dK += dS^T Q
-          if (!warp_wait_c(&c->dsready, g, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_pair(&c->dsready_l, &c->dsready_r, g, c, p.limit_ns)) { ok = false; break; }
           if (!warp_wait_f(&c->bqfull, g, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
@@ -670,10 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         commit2_mc(&c->mdone, 1);
       }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
-    }
-    __syncwarp();
-  } else if (warp == KV_FWD_WARP) {
-    if (lane == 0) {
+    } else if (lane == 0) {   // forwarder
       uint32_t g = 0;
       bool ok = true;
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
@@ -682,9 +694,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         const int nblk = w.nh * w.nbl;
         for (int n = 0; n < nblk; ++n, ++g) {
           if (!wait_c(&c->pready_l, g, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->pready), 0));
+          arrive_remote(mapa(saddr(&c->pready_r), 0));
           if (!wait_c(&c->dsready_l, g, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->dsready), 0));
+          arrive_remote(mapa(saddr(&c->dsready_r), 0));
         }
       }
       if (!ok) fail_f(c, p.status);
@@ -736,16 +748,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       const int nblk = w.nh * w.nbl;
       const int kw = 256 * w.kp + 128 * (int)rank + 32 * q;   // this warp's first key
       const int key = kw + lane;
-      int lo, hi, lo0, lo1, hi0, hi1;   // queries that see this thread's key; over the warp's keys
+      int lo, hi;   // queries that see this thread's key
       S::key_range(p, key, lo, hi);
-      S::key_warp(p, kw, lo, hi, lo0, lo1, hi0, hi1);
-      KvRows rows;
-#pragma unroll
-      for (int he = 0; he < 4; ++he) {
-        rows.lo[he] = __shfl_sync(0xffffffffu, lo, 8 * he + lane / 4);
-        rows.hi[he] = __shfl_sync(0xffffffffu, hi, 8 * he + lane / 4);
-        rows.key[he] = (float)(kw + 8 * he + lane / 4);
-      }
+      const KvRows rows{lo, hi, (float)(kw + lane / 4)};
       if constexpr (!S::kAddOut) {
         if (nblk == 0) {   // no query sees these keys
           S::store_zero(p, w.plane, key, 32 * cg);
@@ -755,32 +760,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       typename S::Scale sc = S::scale_of(p, w.z0);
       for (int n = 0, z = w.z0, b = w.b0; n < nblk; ++n, ++g) {
         const int qg = p.c0 + 128 * b + 32 * cg;   // first of this thread's 32 queries
+        int lo0, lo1, hi0, hi1;   // over the warp's keys
+        S::key_warp(p, kw, lo, hi, lo0, lo1, hi0, hi1);
         const bool none = qg + 31 < lo0 || qg >= hi1, all = qg >= lo1 && qg + 31 < hi0;
         const uint32_t s = g & 1u;
-        uint32_t rs[2][16], rd[2][16], pk[2][8];
-        float2 st[4];                              // lse, then D, of the thread's queries
-        const int q0 = qg + 2 * (lane & 3);        // the first of them
+        uint32_t rs[2][16];                        // scores, then probabilities
+        const int q0 = qg + 2 * (lane & 3);        // the first of the thread's queries
         const float2* ldq = reinterpret_cast<const float2*>(ld) + 16 * cg + (lane & 3);
         typename S::Factors fac;
         if (!warp_wait_c(&c->sfull, g, c, p.limit_ns) || !warp_wait_f(&c->lfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         __syncwarp();
-        tmem_ld_frag(trow, rs[0]);
-        tmem_ld_frag(trow + (16u << 16), rs[1]);
+        {
+          float2 nl[4];
+          tmem_ld_frag(trow, rs[0]);
+          tmem_ld_frag(trow + (16u << 16), rs[1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st[i] = ldq[64 * s + 4 * i];
-        tmem_ld_wait();
-        if (none) {
+          for (int i = 0; i < 4; ++i) nl[i] = ldq[64 * s + 4 * i];
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) pk[0][i] = pk[1][i] = 0u;
-        } else if (all) {
-          kv_probs<S, false>(rs, st, sc, q0, rows, pk, fac);
-        } else {
-          kv_probs<S, true>(rs, st, sc, q0, rows, pk, fac);
+          for (int h = 0; h < 2; ++h) {            // 16 keys at a time, over this warp's own scores
+            uint32_t pk[8] = {};
+            if (all) kv_probs<S, false>(rs[h], h, nl, sc, q0, rows, pk, fac);
+            else if (!none) kv_probs<S, true>(rs[h], h, nl, sc, q0, rows, pk, fac);
+            __syncwarp();
+            tmem_st_frag(trow + ((uint32_t)(16 * h) << 16), pk);
+          }
         }
-        __syncwarp();
-        tmem_st_frag(trow, pk[0]);                 // over this warp's own scores
-        tmem_st_frag(trow + (16u << 16), pk[1]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -791,22 +797,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         if (!warp_wait_c(&c->dpfull, g, c, p.limit_ns) || !warp_wait_f(&c->dfull, g, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         __syncwarp();
-        tmem_ld_frag(trow + KT_DP, rd[0]);
-        tmem_ld_frag(trow + KT_DP + (16u << 16), rd[1]);
+        {
+          float2 nD[4];
+          uint32_t rd[2][16];
+          tmem_ld_frag(trow + KT_DP, rd[0]);
+          tmem_ld_frag(trow + KT_DP + (16u << 16), rd[1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st[i] = ldq[128 + 4 * i];
-        tmem_ld_wait();
-        if (none) {
+          for (int i = 0; i < 4; ++i) nD[i] = ldq[128 + 4 * i];
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) pk[0][i] = pk[1][i] = 0u;
-        } else if (all) {
-          kv_grads<S, false>(rs, rd, st, q0, rows, fac, pk);
-        } else {
-          kv_grads<S, true>(rs, rd, st, q0, rows, fac, pk);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[8] = {};
+            if (all) kv_grads<S, false>(rs[h], rd[h], h, nD, q0, rows, fac, pk);
+            else if (!none) kv_grads<S, true>(rs[h], rd[h], h, nD, q0, rows, fac, pk);
+            __syncwarp();
+            tmem_st_frag(trow + KT_DP + ((uint32_t)(16 * h) << 16), pk);
+          }
         }
-        __syncwarp();
-        tmem_st_frag(trow + KT_DP, pk[0]);
-        tmem_st_frag(trow + KT_DP + (16u << 16), pk[1]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -1016,7 +1023,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       // dP of block gg, once the previous block's has been read; completes the block's S too
       auto grads = [&](uint32_t gg, uint64_t o0) -> bool {
         const uint32_t s = gg & 1u;
-        if (!warp_wait_c(&c->tempty, gg ^ 1u, c, p.limit_ns)) return false;
+        if (!warp_wait_pair(&c->tempty_l, &c->tempty_r, gg ^ 1u, c, p.limit_ns)) return false;
         if (!warp_wait_f(&c->vfull[s], gg >> 1, c, p.limit_ns)) return false;
         tc_fence_after();
         const uint64_t v0 = dplus(dV, s * 16384u);
@@ -1046,7 +1053,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
           if (n + 1 < nj && !grads(g + 1, o0)) { ok = false; break; }
           if (n == max(nj - 2, 0) && elect_one()) commit2_mc(&c->rempty[rs], 3);   // the unit's last S, dP are issued
           __syncwarp();
-          if (!warp_wait_c(&c->oready[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
+          if (!warp_wait_pair(&c->oready_l[s], &c->oready_r[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
           if (!warp_wait_f(&c->yfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
           if (n == 0 && !warp_wait_c(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
@@ -1071,10 +1078,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         commit2_mc(&c->mdone, 1);
       }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
-    }
-    __syncwarp();
-  } else if (warp == Q_FWD_WARP) {
-    if (lane == 0) {
+    } else if (lane == 0) {   // forwarder
       uint32_t g = 0;
       bool ok = true;
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
@@ -1082,9 +1086,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         S::q_unit(p, u, z, qp, j0, nj);
         for (int j = 0; j < nj; ++j, ++g) {
           if (!wait_c(&c->tempty_l, g, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->tempty), 0));
+          arrive_remote(mapa(saddr(&c->tempty_r), 0));
           if (!wait_c(&c->oready_l[g & 1u], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->oready[g & 1u]), 0));
+          arrive_remote(mapa(saddr(&c->oready_r[g & 1u]), 0));
         }
       }
       if (!ok) fail_f(c, p.status);

@@ -33,9 +33,9 @@ using fa::dplus;
 using fa::mma2_bf16_ts;
 using fa::tmem_st_wait;
 
-// Warps: 0 TMA producers, 1 MMA issuer, 2 forwarder (turns the CTA's local arrivals into one
-// arrival at the leader), 3 idle, 4-7 and 8-11 the softmax groups (lane quadrant warp % 4).
-constexpr int FWD_WARP = 2, SOFT_WARP = 4;
+// Warps: 0 TMA producers, 1 MMA issuer (leader) or forwarder (the other CTA), 2 and 3 idle, 4-7
+// and 8-11 the softmax groups (lane quadrant warp % 4).
+constexpr int SOFT_WARP = 4;
 constexpr int THREADS = 384;
 
 // Shared memory, bytes from the 1024-aligned base; tiles are 128-byte swizzled
@@ -55,8 +55,8 @@ struct Ctrl {
   uint64_t kfull[KV_STAGES], kempty[KV_STAGES], vfull[KV_STAGES], vempty[KV_STAGES];
   uint64_t qfull[2], qempty[2];
   uint64_t sfull[2];      // S of the group's block is ready, and its earlier products are done
-  uint64_t pready[2];     // leader: both CTAs' P is written
-  uint64_t pready_l[2];   // the CTA's four warps of the group, forwarded
+  uint64_t pready_l[2];   // P is written: the CTA's four warps of the group
+  uint64_t pready_r[2];   // the same of the other CTA (leader)
   uint64_t ofull;         // the unit's products are done (both CTAs)
   uint64_t accempty;      // leader: the unit's O has been read out
   uint64_t mlx;           // the CTA's eight softmax warps have left m and l
@@ -190,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&c->qfull[i], 1);
       mbar_init(&c->qempty[i], 1);
       mbar_init(&c->sfull[i], 1);
-      mbar_init(&c->pready[i], 2);
+      mbar_init(&c->pready_r[i], 1);
       mbar_init(&c->pready_l[i], 4);
     }
     mbar_init(&c->ofull, 1);
@@ -319,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!scores(g, qs) || (nj > 1 && !scores(g + 1, qs))) { ok = false; break; }
         for (int n = 0; n < nj; ++n, ++g) {
           const uint32_t s = g % KV_STAGES, b = g & 1u;
-          if (!warp_wait(&c->pready[b], g >> 1, c, p.limit_ns)) { ok = false; break; }
+          if (!fa::warp_wait_pair(&c->pready_l[b], &c->pready_r[b], g >> 1, c, p.limit_ns)) { ok = false; break; }
           if (!warp_wait(&c->vfull[s], g / KV_STAGES, c, p.limit_ns)) { ok = false; break; }
           if (n == 0 && !warp_wait(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
@@ -344,10 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         commit2_mc(&c->mdone, 1);
       }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
-    }
-    __syncwarp();
-  } else if (warp == FWD_WARP) {
-    if (lane == 0) {
+    } else if (lane == 0) {   // forwarder
       uint32_t g = 0;
       bool ok = true;
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
@@ -355,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         unit_of(p, u, z, qp, j0, nj);
         for (int j = 0; j < nj; ++j, ++g) {
           if (!wait1(&c->pready_l[g & 1u], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->pready[g & 1u]), 0));
+          arrive_remote(mapa(saddr(&c->pready_r[g & 1u]), 0));
         }
       }
       if (!ok) fail_o(c, p.status);
