@@ -398,14 +398,35 @@ struct QP {
 // of a block), Q, dO (128 queries x half of hd), and the fp32 outputs dK, dV;
 // k_attn_q: Q, dO (128-query rows), K, V (64 keys of a block), K (128 keys x half of hd).
 // A policy may name one block (tail_block) whose rows the accumulating products take from
-// other maps (one block a head): Q, dO (in the place of the fp32 outputs) and K.
-enum { KV_MK, KV_MV, KV_MQA, KV_MOA, KV_MQB, KV_MOB, KV_MDK, KV_MDV, KV_MAPS, KV_MQT = KV_MDK, KV_MOT = KV_MDV };
+// other maps (one block a head): Q, dO (in the place of the fp32 outputs) and K; and have
+// output maps of its own behind.
+enum { KV_MK, KV_MV, KV_MQA, KV_MOA, KV_MQB, KV_MOB, KV_MDK, KV_MDV, KV_MAPS, KV_MQT = KV_MDK, KV_MOT = KV_MDV,
+       KV_MOUTK = KV_MAPS, KV_MOUTV };
 enum { Q_MQ, Q_MO, Q_MKA, Q_MVA, Q_MKB, Q_MAPS, Q_MKT = Q_MAPS };
 template <int N>
 struct MapArray {   // in the kernel's parameters
   CUtensorMap m[N];
   __device__ __forceinline__ const CUtensorMap* operator[](int i) const { return &m[i]; }
 };
+
+// Row `lane` of a warp's 32 x 32 staging block, times f: fp32 with the 128-byte swizzle, or
+// bf16 rows of 64 bytes.
+__device__ __forceinline__ void stage_f32(const uint32_t (&ra)[32], float f, uint32_t stg, int lane) {
+  const uint32_t buf = stg + (uint32_t)lane * 128u;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    sts128(buf + ((uint32_t)(k ^ (lane & 7)) << 4), __float_as_uint(__uint_as_float(ra[4 * k]) * f),
+           __float_as_uint(__uint_as_float(ra[4 * k + 1]) * f), __float_as_uint(__uint_as_float(ra[4 * k + 2]) * f),
+           __float_as_uint(__uint_as_float(ra[4 * k + 3]) * f));
+}
+__device__ __forceinline__ void stage_bf16(const uint32_t (&ra)[32], float f, uint32_t stg, int lane) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack_bf16(__uint_as_float(ra[2 * i]) * f, __uint_as_float(ra[2 * i + 1]) * f);
+  const uint32_t buf = stg + (uint32_t)lane * 64u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sts128(buf + 16u * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+}
 
 // A unit of k_attn_kv: key / value head zk, keys [256 kp, +256), query blocks [b0, b0 + nbl) of
 // each of the query heads [z0, z0 + nh); `plane` says where its dK and dV go.
@@ -427,7 +448,11 @@ struct CausalScores {
   // the chunk hold at least one query at or after the unit's first key.  The unit walks
   // those nbl blocks for each query head of zk's group, accumulating dV and dK of the
   // shared head.  Key pairs in ascending order, so the longest units start first.
-  static __device__ __forceinline__ void kv_unit(const KvP& p, int u, KvUnit& w) {
+  // (a policy whose units come from memory loads them ahead: kv_raw, q_raw)
+  struct Raw {};
+  static __device__ __forceinline__ Raw kv_raw(const KvP&, int) { return Raw{}; }
+  static __device__ __forceinline__ Raw q_raw(const QP&, int) { return Raw{}; }
+  static __device__ __forceinline__ void kv_unit(const KvP& p, int u, Raw, KvUnit& w) {
     w.kp = u / p.Hkv;
     w.zk = u - w.kp * p.Hkv;
     const int num = 256 * w.kp - p.c0 - 127;
@@ -452,7 +477,7 @@ struct CausalScores {
 
   // Unit u: head z, queries [c0 + 256 qp, +256) of the chunk, key blocks j0 .. j0+nj-1 (128
   // keys each) up to the unit's last query.  Later query pairs (more keys) first.
-  static __device__ __forceinline__ void q_unit(const QP& p, int u, int& z, int& qp, int& j0, int& nj) {
+  static __device__ __forceinline__ void q_unit(const QP& p, int u, Raw, int& z, int& qp, int& j0, int& nj) {
     const int i = u / p.H;
     z = u - i * p.H;
     qp = p.n_qp - 1 - i;
@@ -488,6 +513,20 @@ struct CausalScores {
   static __device__ __forceinline__ float2 kept(const Factors&, int) { return make_float2(1.f, 1.f); }
   template <class P>
   static __device__ __forceinline__ int tail_block(const P&) { return -1; }
+
+  // How a warp's 32 x 32 block of dV (t = 0) or dK (t = 1) leaves: whether it does, one row of
+  // it into the warp's staging block, and the copy out of that (fp32, 128-byte swizzle; added
+  // into the outputs).  Rows past T are clipped by the tensor map, rows in [c1, T) add 0.
+  static __device__ __forceinline__ bool kv_leaves(const KvP& p, int kw, int) { return kw < p.c1; }
+  static __device__ __forceinline__ void kv_stage(const KvP& p, int t, const uint32_t (&ra)[32], uint32_t stg, int lane) {
+    stage_f32(ra, t ? p.scale : 1.f, stg, lane);
+  }
+  static __device__ __forceinline__ void kv_copy(const KvMaps& maps, const KvP&, int t, uint32_t stg, int c, int kw,
+                                                 const KvUnit& w) {
+    tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, c, kw, w.zk);
+  }
+  // The same of dQ: no staging, 32 columns of a row from registers.
+  static constexpr bool kStageQ = false;
 };
 
 // A unit's blocks in order: query head z, query block b.  Returns whether z is another.
@@ -520,9 +559,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       prefetch_map(maps[KV_MOA]);
       uint32_t g = 0, go = 0, lu = 0;   // blocks (Q; dO) and units loaded so far
       bool ok = true;
+      typename S::Raw raw = S::kv_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         KvUnit w;
-        S::kv_unit(p, u, w);
+        S::kv_unit(p, u, raw, w);
+        raw = S::kv_raw(p, S::next_unit(rnd + 1, pid, npairs));
         const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
         if (!wait_c(&c->rempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
@@ -570,9 +611,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       const int tail = S::tail_block(p);
       uint32_t g = 0, gq = 0;
       bool ok = true;
+      typename S::Raw raw = S::kv_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         KvUnit w;
-        S::kv_unit(p, u, w);
+        S::kv_unit(p, u, raw, w);
+        raw = S::kv_raw(p, S::next_unit(rnd + 1, pid, npairs));
         const int nblk = w.nh * w.nbl;
         for (int n = 0, z = w.z0, b = w.b0; n < nblk; ++n, kv_next(w, z, b)) {
           const int qrow = p.c0 + 128 * b;
@@ -639,9 +682,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         __syncwarp();
         return true;
       };
+      typename S::Raw raw = S::kv_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         KvUnit w;
-        S::kv_unit(p, u, w);
+        S::kv_unit(p, u, raw, w);
+        raw = S::kv_raw(p, S::next_unit(rnd + 1, pid, npairs));
         const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
         if (!warp_wait_f(&c->rfull, lu, c, p.limit_ns)) { ok = false; break; }
@@ -688,9 +733,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
     } else if (lane == 0) {   // forwarder
       uint32_t g = 0;
       bool ok = true;
+      typename S::Raw raw = S::kv_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         KvUnit w;
-        S::kv_unit(p, u, w);
+        S::kv_unit(p, u, raw, w);
+        raw = S::kv_raw(p, S::next_unit(rnd + 1, pid, npairs));
         const int nblk = w.nh * w.nbl;
         for (int n = 0; n < nblk; ++n, ++g) {
           if (!wait_c(&c->pready_l, g, c, p.limit_ns)) { ok = false; break; }
@@ -708,9 +755,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
     float* ld = reinterpret_cast<float*>(base + KV_LD);
     uint32_t g = 0;
     bool ok = true;
+    typename S::Raw raw = S::kv_raw(p, pid);
     for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
       KvUnit w;
-      S::kv_unit(p, u, w);
+      S::kv_unit(p, u, raw, w);
+      raw = S::kv_raw(p, S::next_unit(rnd + 1, pid, npairs));
       const int nblk = w.nh * w.nbl;
       for (int n = 0, z = w.z0, b = w.b0; n < nblk; ++n, ++g, kv_next(w, z, b)) {
         float lv[4], dv[4];
@@ -742,18 +791,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
     const float* ld = reinterpret_cast<const float*>(base + KV_LD);
     uint32_t g = 0, lu = 0;
     bool ok = true;
+    // the next unit's entry and key ranges are loaded while this one's outputs leave
+    auto first_key = [&](const KvUnit& x) { return 256 * x.kp + 128 * (int)rank + 32 * q; };   // this warp's
+    KvUnit w;
+    int lo, hi;   // queries that see this thread's key
+    S::kv_unit(p, pid, S::kv_raw(p, pid), w);
+    S::key_range(p, first_key(w) + lane, lo, hi);
     for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
-      KvUnit w;
-      S::kv_unit(p, u, w);
       const int nblk = w.nh * w.nbl;
-      const int kw = 256 * w.kp + 128 * (int)rank + 32 * q;   // this warp's first key
-      const int key = kw + lane;
-      int lo, hi;   // queries that see this thread's key
-      S::key_range(p, key, lo, hi);
+      const int kw = first_key(w), key = kw + lane;
+      const int un = S::next_unit(rnd + 1, pid, npairs);
       const KvRows rows{lo, hi, (float)(kw + lane / 4)};
       if constexpr (!S::kAddOut) {
         if (nblk == 0) {   // no query sees these keys
           S::store_zero(p, w.plane, key, 32 * cg);
+          S::kv_unit(p, un, S::kv_raw(p, un), w);
+          S::key_range(p, first_key(w) + lane, lo, hi);
           continue;
         }
       }
@@ -824,14 +877,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         if (kv_next(w, z, b) && n + 1 < nblk) sc = S::scale_of(p, z);
       }
       if (!ok) break;
-      // the unit's dV and dK out of tensor memory, 32 of hd: written, or, where the outputs are
-      // fp32 sums, added into them through this warp's staging block.  Each output element
-      // receives one add per launch; rows past T are clipped by the tensor map, rows in
-      // [c1, T) add 0.
+      // the unit's dV and dK, 32 of hd, out of tensor memory and through this warp's staging
+      // block: asynchronous copies of whole rows (row-per-thread stores of them took 9100 cycles
+      // a unit, as long as three blocks)
+      const typename S::Raw raw = S::kv_raw(p, un);
       if (!warp_wait_c(&c->accfull, lu, c, p.limit_ns)) { ok = false; break; }
       ++lu;
       tc_fence_after();
+      const KvUnit done = w;
+      S::kv_unit(p, un, raw, w);
+      S::key_range(p, first_key(w) + lane, lo, hi);
       const uint32_t stg = sb + KV_STG + (uint32_t)(warp - 2) * 4096u;
+      const bool leaves = S::kv_leaves(p, kw, 32 * cg);
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {   // t = 0: dV, t = 1: s dK
         __syncwarp();
@@ -843,25 +900,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           __syncwarp();
           if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
         }
-        if constexpr (!S::kAddOut) {
-          S::store_out(p, t, w.plane, key, 32 * cg, ra);
-        } else {
-          if (kw >= p.c1) continue;
-          if (lane == 0) bulk_wait_read();   // the block's previous contents have left
-          __syncwarp();
-          const float f = t ? p.scale : 1.f;
-          const uint32_t buf = stg + (uint32_t)lane * 128u;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            sts128(buf + ((uint32_t)(k ^ (lane & 7)) << 4), __float_as_uint(__uint_as_float(ra[4 * k]) * f),
-                   __float_as_uint(__uint_as_float(ra[4 * k + 1]) * f), __float_as_uint(__uint_as_float(ra[4 * k + 2]) * f),
-                   __float_as_uint(__uint_as_float(ra[4 * k + 3]) * f));
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, 32 * cg, kw, w.zk);
-            bulk_commit();
-          }
+        if (!leaves) continue;
+        if (lane == 0) bulk_wait_read();   // the block's previous contents have left
+        __syncwarp();
+        S::kv_stage(p, t, ra, stg, lane);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          S::kv_copy(maps, p, t, stg, 32 * cg, kw, done);
+          bulk_commit();
         }
       }
       __syncwarp();
@@ -923,9 +970,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       prefetch_map(maps[Q_MVA]);
       uint32_t g = 0, gv = 0, lu = 0;   // key blocks (K; V) and units loaded so far
       bool ok = true;
+      typename S::Raw raw = S::q_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
-        S::q_unit(p, u, z, qp, j0, nj);
+        S::q_unit(p, u, raw, z, qp, j0, nj);
+        raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
         if (nj == 0) continue;
         const uint32_t rs = lu & 1u;
         if (!wait_c(&c->rempty[rs], (lu >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
@@ -973,9 +1022,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       const int tail = S::tail_block(p);
       uint32_t g = 0;
       bool ok = true;
+      typename S::Raw raw = S::q_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
-        S::q_unit(p, u, z, qp, j0, nj);
+        S::q_unit(p, u, raw, z, qp, j0, nj);
+        raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
         for (int j = 0; j < nj; ++j) {
           const uint32_t s = g & 1u;
           if (!wait_c(&c->yempty[s], (g >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
@@ -1038,9 +1089,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         __syncwarp();
         return true;
       };
+      typename S::Raw raw = S::q_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
-        S::q_unit(p, u, z, qp, j0, nj);
+        S::q_unit(p, u, raw, z, qp, j0, nj);
+        raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
         if (nj == 0) continue;
         const uint32_t rs = lu & 1u;
         if (!warp_wait_f(&c->rfull[rs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
@@ -1081,9 +1134,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     } else if (lane == 0) {   // forwarder
       uint32_t g = 0;
       bool ok = true;
+      typename S::Raw raw = S::q_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
-        S::q_unit(p, u, z, qp, j0, nj);
+        S::q_unit(p, u, raw, z, qp, j0, nj);
+        raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
         for (int j = 0; j < nj; ++j, ++g) {
           if (!wait_c(&c->tempty_l, g, c, p.limit_ns)) { ok = false; break; }
           arrive_remote(mapa(saddr(&c->tempty_r), 0));
@@ -1099,9 +1154,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(32 * cg);
     uint32_t g = 0, lu = 0;
     bool ok = true;
+    typename S::Raw raw = S::q_raw(p, pid);
     for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
       int z, qp, j0, nj;
-      S::q_unit(p, u, z, qp, j0, nj);
+      S::q_unit(p, u, raw, z, qp, j0, nj);
+      raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
       const typename S::Scale sc = S::scale_of(p, z);
       const int qw = p.c0 + 256 * qp + 128 * (int)rank + 32 * q;   // this warp's first query
       const int qr = qw + lane;                                     // this thread's query

@@ -68,7 +68,7 @@ template <bool CAP, bool BIAS>
 struct PackedScores {
   using Kv = KvParams;
   using Q = QParams;
-  using KvMaps = fa::MapArray<fa::KV_MAPS>;
+  using KvMaps = fa::MapArray<fa::KV_MAPS + 2>;
   using QMaps = fa::MapArray<fa::Q_MAPS + 1>;
   // a masked pair's score may be infinite or NaN (another document's values)
   static constexpr bool kClearMasked = true;
@@ -76,12 +76,22 @@ struct PackedScores {
   using Scale = ScaleZ;
 
   static __device__ __forceinline__ int next_unit(int t, int pid, int npairs) { return pk::next_unit(t, pid, npairs); }
-  static __device__ __forceinline__ void kv_unit(const Kv& p, int u, fa::KvUnit& w) {
+  using Raw = int4;   // a unit's list entry: {qp, ja0, jb0 or jb1} or {kp, b0, nb}
+  static __device__ __forceinline__ Raw kv_raw(const Kv& p, int u) {
+    return u < p.n_units ? *reinterpret_cast<const int4*>(p.units + u / (p.parts * p.Hkv)) : make_int4(0, 0, 0, 0);
+  }
+  static __device__ __forceinline__ Raw q_raw(const Q& p, int u) {
+    if (u >= p.n_units) return make_int4(0, 0, 0, 0);
+    const int4* s = reinterpret_cast<const int4*>(p.units + u / p.H);
+    int4 a = s[0];
+    a.z = max(a.z, s[1].x);
+    return a;
+  }
+  static __device__ __forceinline__ void kv_unit(const Kv& p, int u, Raw v, fa::KvUnit& w) {
     const int planes = p.parts * p.Hkv, i = u / planes;
     w.plane = u - i * planes;
     const int part = w.plane / p.Hkv, h0 = part * p.per_part;
     w.zk = w.plane - part * p.Hkv;
-    const int4 v = *reinterpret_cast<const int4*>(p.units + i);
     w.kp = v.x;
     w.b0 = v.y;
     w.nbl = v.z;
@@ -102,14 +112,11 @@ struct PackedScores {
                                                   int& hi1) {
     ends(lo, hi, lo0, lo1, hi0, hi1);
   }
-  static __device__ __forceinline__ void q_unit(const Q& p, int u, int& z, int& qp, int& j0, int& nj) {
-    const int i = u / p.H;
-    z = u - i * p.H;
-    const int4* s = reinterpret_cast<const int4*>(p.units + i);
-    const int4 a = s[0];
-    qp = a.x;
-    j0 = a.y;
-    nj = max(a.z, s[1].x) - a.y;
+  static __device__ __forceinline__ void q_unit(const Q& p, int u, Raw v, int& z, int& qp, int& j0, int& nj) {
+    z = u % p.H;
+    qp = v.x;
+    j0 = v.y;
+    nj = v.z - v.y;
   }
   static __device__ __forceinline__ void query_range(const Q& p, int q, int& lo, int& hi) {
     lo = q < p.T ? p.lo[q] : p.T;
@@ -163,27 +170,35 @@ struct PackedScores {
     else return make_float2(1.f, 1.f);
   }
 
-  // 32 columns of dV (t = 0) or dK (t = 1) of one key
-  static __device__ __forceinline__ void store_out(const Kv& p, int t, int plane, int key, int c,
-                                                   const uint32_t (&ra)[32]) {
-    if (key >= p.T) return;
-    const int64_t row = ((int64_t)plane * p.T + key) * p.hd;
-    const float f = t ? p.scale : 1.f;
-    if (p.parts == 1) {
-      store_row((t ? p.dK : p.dV) + row, p.hd, c, ra, f);
-      return;
-    }
-    float4* o = reinterpret_cast<float4*>((t ? p.part_k : p.part_v) + row + c);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + 4 * k < p.hd)
-        o[k] = make_float4(__uint_as_float(ra[4 * k]) * f, __uint_as_float(ra[4 * k + 1]) * f,
-                           __uint_as_float(ra[4 * k + 2]) * f, __uint_as_float(ra[4 * k + 3]) * f);
+  // How 32 x 32 blocks of dV (t = 0) and dK (t = 1) leave (see CausalScores): bf16, or the parts'
+  // fp32 sums.
+  static __device__ __forceinline__ bool kv_leaves(const Kv& p, int kw, int c) { return kw < p.T && c < p.hd; }
+  static __device__ __forceinline__ void kv_stage(const Kv& p, int t, const uint32_t (&ra)[32], uint32_t stg, int lane) {
+    if (p.parts == 1) fa::stage_bf16(ra, t ? p.scale : 1.f, stg, lane);
+    else fa::stage_f32(ra, t ? p.scale : 1.f, stg, lane);
   }
+  static __device__ __forceinline__ void kv_copy(const KvMaps& maps, const Kv&, int t, uint32_t stg, int c, int kw,
+                                                 const fa::KvUnit& w) {
+    tma_store_3d(maps[t ? fa::KV_MOUTK : fa::KV_MOUTV], stg, c, kw, w.plane);
+  }
+  // Keys that no query sees: 32 columns of 0.
   static __device__ __forceinline__ void store_zero(const Kv& p, int plane, int key, int c) {
-    const uint32_t z[32] = {};
-    store_out(p, 0, plane, key, c, z);
-    store_out(p, 1, plane, key, c, z);
+    if (key >= p.T) return;
+    const int64_t row = ((int64_t)plane * p.T + key) * p.hd + c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + 8 * k < p.hd) {
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        if (p.parts == 1) {
+          *reinterpret_cast<uint4*>(p.dV + row + 8 * k) = z;
+          *reinterpret_cast<uint4*>(p.dK + row + 8 * k) = z;
+        } else {
+          for (float* o : {p.part_v + row + 8 * k, p.part_k + row + 8 * k}) {
+            *reinterpret_cast<uint4*>(o) = z;
+            *reinterpret_cast<uint4*>(o + 4) = z;
+          }
+        }
+      }
   }
   // 32 columns of dQ of one query (row ro of [H, T])
   static __device__ __forceinline__ void store_dq(const Q& p, int64_t ro, int c, const uint32_t (&ra)[32]) {
@@ -432,7 +447,7 @@ bool packed_supported(int64_t H, int64_t T, int64_t hd) {
 int kv_heads_per_part(int64_t H, int64_t Hkv, int64_t T) {
   const int64_t group = H / Hkv, n = (T + 255) / 256, pairs = std::max(1, num_sms() / 2);
 #ifndef KVU
-#define KVU 4
+#define KVU 2
 #define KVT 512
 #endif
   const int64_t want = KVU * pairs;
@@ -560,7 +575,7 @@ cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedLayout& L, 
       }))
     return cudaErrorInvalidConfiguration;
   const int n = (int)((a.T + 255) / 256);
-  MapArray<KV_MAPS> mk;
+  MapArray<KV_MAPS + 2> mk;
   MapArray<Q_MAPS + 1> mq;
   const struct { CUtensorMap* m; const void* ptr; int64_t T, heads; uint32_t rows; } list[] = {
       {&mk.m[KV_MK], a.K, a.T, a.Hkv, 128},  {&mk.m[KV_MV], a.V, a.T, a.Hkv, 128},
@@ -571,6 +586,13 @@ cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedLayout& L, 
       {&mq.m[Q_MKT], w.tail_kv, 128, a.Hkv, 128}};
   for (const auto& e : list)
     if (!tc::make_map_heads(e.m, e.ptr, e.T, e.heads, a.hd, e.rows)) return cudaErrorInvalidValue;
+  // outputs: dK and dV in bf16, or the parts' sums
+  for (int t = 0; t < 2; ++t) {
+    CUtensorMap* m = &mk.m[t ? KV_MOUTV : KV_MOUTK];
+    const bool ok = L.parts == 1 ? tc::make_map_out(m, t ? dV : dK, a.T, a.Hkv, a.hd, 2)
+                                 : tc::make_map_out(m, base + (t ? L.off_pv : L.off_pk), a.T, L.parts * a.Hkv, a.hd, 4);
+    if (!ok) return cudaErrorInvalidValue;
+  }
   mq.m[Q_MQ] = mk.m[KV_MQB];
   mq.m[Q_MO] = mk.m[KV_MOB];
   mq.m[Q_MKB] = mk.m[KV_MK];

@@ -531,6 +531,20 @@ inline bool make_map_heads(CUtensorMap* m, const void* ptr, int64_t T, int64_t h
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D map over head-major outputs [heads, T, hd] of `esize` bytes an element: 32 x 32 x 1 boxes,
+// bf16 rows of 64 bytes unswizzled, fp32 rows of 128 bytes with the 128-byte swizzle.
+inline bool make_map_out(CUtensorMap* m, void* ptr, int64_t T, int64_t heads, int64_t hd, int esize) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)T, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)(hd * esize), (cuuint64_t)T * (cuuint64_t)(hd * esize)};
+  cuuint32_t box[3] = {32, 32, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides,
+             box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, esize == 2 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Failure-detection test hook: SBP_FAULT_STALL=1 makes the next forward kernels stall
 // on purpose (read at every launch, so a test can switch it off again).  Together with a
 // short SBP_WAIT_LIMIT_MS it exercises the bounded-wait abort path: status
