@@ -75,12 +75,13 @@ cudaError_t attn_fused_q(const AttnFusedPlan& plan, int64_t c0, int64_t c1, floa
   p.n_qp = (int)((c1 - c0 + 255) / 256);
   p.n_units = p.n_qp * p.H;
   p.group = (int)(plan.H / plan.Hkv);
-  p.scale = scale; p.lse = lse; p.D = D; p.dQ = static_cast<__nv_bfloat16*>(dQ);
-  p.status = status; p.limit_ns = wait_limit_ns();
+  p.scale = scale; p.lse = lse; p.D = D; p.status = status; p.limit_ns = wait_limit_ns();
   int pairs = max_pairs((const void*)k_attn_q<CausalScores>, SMEM_Q, Q_THREADS);
   if (pairs > p.n_units) pairs = p.n_units;
-  k_attn_q<CausalScores><<<2 * pairs, Q_THREADS, SMEM_Q, s>>>(
-      MapArray<Q_MAPS>{{plan.Q128, plan.O128, plan.K64, plan.V64, plan.K128}}, p);
+  MapArray<Q_MAPS> maps{{plan.Q128, plan.O128, plan.K64, plan.V64, plan.K128}};
+  // the chunk's rows of dQ and no later ones
+  if (!make_map_out(&maps.m[Q_MOUT], dQ, c1, plan.T, plan.H, 128, 2)) return cudaErrorInvalidValue;
+  k_attn_q<CausalScores><<<2 * pairs, Q_THREADS, SMEM_Q, s>>>(maps, p);
   return cudaGetLastError();
 }
 

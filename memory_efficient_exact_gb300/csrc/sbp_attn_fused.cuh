@@ -76,7 +76,7 @@ constexpr uint32_t QT_DP = 256, QT_DQ = 384;
 
 struct CtrlQ {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], yfull[2], yempty[2];
-  uint64_t rfull[2], rempty[2];   // the unit's Q and dO
+  uint64_t rfull[2], rempty[2];   // the unit's Q and dO; free: their products are done, and dQ has left
   uint64_t tfull;                 // S and dP of the block are ready
   uint64_t tempty_l, oready_l[2]; // dP has been read, dS buffer is written: the CTA's epilogue warps
   uint64_t tempty_r, oready_r[2]; // the same of the other CTA (leader)
@@ -160,7 +160,7 @@ __device__ __forceinline__ void prologue_q(CtrlQ* c, int warp) {
       mbar_init(&c->yfull[i], 1);
       mbar_init(&c->yempty[i], 1);
       mbar_init(&c->rfull[i], 1);
-      mbar_init(&c->rempty[i], 1);
+      mbar_init(&c->rempty[i], 1 + Q_EPI);
       mbar_init(&c->oready_r[i], 1);
       mbar_init(&c->oready_l[i], Q_EPI);
     }
@@ -192,26 +192,6 @@ template <class C>
 __device__ __forceinline__ void fail_f(C* c, int32_t* status) {
   *(volatile int*)&c->abort = 1;
   if (status) atomicCAS(status, 0, SBP_ERR_TIMEOUT);
-}
-
-// Waits until barrier b has completed `need` phases; `seen` counts the phases this
-// thread already waited for.  Bounded like every other wait.
-template <class C>
-__device__ __forceinline__ bool wait_n(uint64_t* b, uint32_t& seen, uint32_t need, C* c, uint64_t limit) {
-  while (seen < need) {
-    if (!wait_inl<true>(b, seen & 1u, &c->abort, limit)) return false;
-    ++seen;
-  }
-  return true;
-}
-// The same for a whole warp (seen and need are warp-uniform).
-template <class C>
-__device__ __forceinline__ bool warp_wait_n(uint64_t* b, uint32_t& seen, uint32_t need, C* c, uint64_t limit) {
-  while (seen < need) {
-    if (!__all_sync(0xffffffffu, wait_inl<true>(b, seen & 1u, &c->abort, limit))) return false;
-    ++seen;
-  }
-  return true;
 }
 
 // One phase, by its parity: of a barrier that only this CTA or the tensor pipe completes
@@ -306,9 +286,9 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
 
 // ================================================================ k_attn_kv (dK, dV)
 
-// k_attn_kv's epilogue, a warp's 32 keys x 32 queries.  First P^T = 2^(s S^T - lse log2 e), kept
-// in fp32 (over the scores) and packed to bf16 pairs, with the factors of the scores' gradients
-// where a policy has them; then dS^T = P^T (dP^T - D).  The scores are held as accumulator
+// k_attn_kv's epilogue, a warp's 32 keys x 32 queries.  First P^T = 2^(s S^T - lse log2 e), packed
+// to bf16 pairs and kept in fp32 (over the scores, times the factors of the scores' gradients
+// where a policy has them); then dS^T = P^T (dP^T - D).  The scores are held as accumulator
 // fragments, [half of 16 keys][tmem_ld_frag], so that a thread meets 8 of the 32 queries
 // only: their lse and D come from shared memory in 8 loads a block, where a key row a thread
 // took 64 floats, a wavefront each, and the two kept the shared-memory pipe busy for
@@ -321,7 +301,7 @@ struct KvRows {
 };
 template <class S, bool MASK>
 __device__ __forceinline__ void kv_probs(uint32_t (&r)[16], int h, const float2 (&nlse)[4], const typename S::Scale& sc,
-                                         int q0, const KvRows& w, uint32_t (&pw)[8], typename S::Factors& fac) {
+                                         int q0, const KvRows& w, uint32_t (&pw)[8]) {
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int row = 16 * h + 8 * e;
@@ -342,7 +322,7 @@ __device__ __forceinline__ void kv_probs(uint32_t (&r)[16], int h, const float2 
       if (MASK && (q < lo || q >= hi)) pp.x = 0.f;
       if (MASK && (q + 1 < lo || q + 1 >= hi)) pp.y = 0.f;
       pw[2 * g + e] = pack_bf16(pp.x, pp.y);
-      S::keep(fac, 8 * h + 4 * e + g, dc);
+      pp = S::fold(pp, dc);
       r0 = __float_as_uint(pp.x);
       r1 = __float_as_uint(pp.y);
     }
@@ -350,7 +330,7 @@ __device__ __forceinline__ void kv_probs(uint32_t (&r)[16], int h, const float2 
 }
 template <class S, bool MASK>
 __device__ __forceinline__ void kv_grads(const uint32_t (&rp)[16], const uint32_t (&rd)[16], int h, const float2 (&nD)[4],
-                                         int q0, const KvRows& w, const typename S::Factors& fac, uint32_t (&dw)[8]) {
+                                         int q0, const KvRows& w, uint32_t (&dw)[8]) {
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int row = 16 * h + 8 * e;
@@ -362,9 +342,8 @@ __device__ __forceinline__ void kv_grads(const uint32_t (&rp)[16], const uint32_
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int i = 4 * g + 2 * e;
-      float2 sv = S::grad2(make_float2(__uint_as_float(rp[i]), __uint_as_float(rp[i + 1])),
-                           add2(make_float2(__uint_as_float(rd[i]), __uint_as_float(rd[i + 1])), nD[g]),
-                           S::kept(fac, 8 * h + 4 * e + g));
+      float2 sv = mul2(make_float2(__uint_as_float(rp[i]), __uint_as_float(rp[i + 1])),
+                       add2(make_float2(__uint_as_float(rd[i]), __uint_as_float(rd[i + 1])), nD[g]));
       const int q = q0 + 8 * g;
       if (S::kClearMasked && MASK && (q < lo || q >= hi)) sv.x = 0.f;
       if (S::kClearMasked && MASK && (q + 1 < lo || q + 1 >= hi)) sv.y = 0.f;
@@ -389,20 +368,20 @@ struct QP {
   float scale;
   const float* lse;
   const float* D;
-  __nv_bfloat16* dQ;  // [H, T, 128]
   int32_t* status;
   uint64_t limit_ns;
 };
 
 // Tensor maps of the kernels.  k_attn_kv: K, V (the unit's 128-key rows), Q, dO (64 queries
 // of a block), Q, dO (128 queries x half of hd), and the fp32 outputs dK, dV;
-// k_attn_q: Q, dO (128-query rows), K, V (64 keys of a block), K (128 keys x half of hd).
+// k_attn_q: Q, dO (128-query rows), K, V (64 keys of a block), K (128 keys x half of hd), and the
+// output dQ.
 // A policy may name one block (tail_block) whose rows the accumulating products take from
 // other maps (one block a head): Q, dO (in the place of the fp32 outputs) and K; and have
 // output maps of its own behind.
 enum { KV_MK, KV_MV, KV_MQA, KV_MOA, KV_MQB, KV_MOB, KV_MDK, KV_MDV, KV_MAPS, KV_MQT = KV_MDK, KV_MOT = KV_MDV,
        KV_MOUTK = KV_MAPS, KV_MOUTV };
-enum { Q_MQ, Q_MO, Q_MKA, Q_MVA, Q_MKB, Q_MAPS, Q_MKT = Q_MAPS };
+enum { Q_MQ, Q_MO, Q_MKA, Q_MVA, Q_MKB, Q_MOUT, Q_MAPS, Q_MKT = Q_MAPS };
 template <int N>
 struct MapArray {   // in the kernel's parameters
   CUtensorMap m[N];
@@ -506,11 +485,8 @@ struct CausalScores {
     dc = make_float2(1.f, 1.f);
     return fma2(s, make_float2(sl2, sl2), nlz);
   }
-  static __device__ __forceinline__ float2 grad2(float2 p, float2 d, float2) { return mul2(p, d); }
-  // What k_attn_kv keeps of dc between the two halves of its epilogue.
-  struct Factors {};
-  static __device__ __forceinline__ void keep(Factors&, int, float2) {}
-  static __device__ __forceinline__ float2 kept(const Factors&, int) { return make_float2(1.f, 1.f); }
+  // A probability times the factor of its score's gradient.
+  static __device__ __forceinline__ float2 fold(float2 p, float2) { return p; }
   template <class P>
   static __device__ __forceinline__ int tail_block(const P&) { return -1; }
 
@@ -525,8 +501,10 @@ struct CausalScores {
                                                  const KvUnit& w) {
     tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, c, kw, w.zk);
   }
-  // The same of dQ: no staging, 32 columns of a row from registers.
-  static constexpr bool kStageQ = false;
+  // Whether the products that sum over hd have columns past 64; hd.
+  template <class P>
+  static __device__ __forceinline__ bool wide(const P&) { return true; }
+  static __device__ __forceinline__ int width(const QP&) { return 128; }
 };
 
 // A unit's blocks in order: query head z, query block b.  Returns whether z is another.
@@ -645,6 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       const uint64_t dK = sw128_desc(sb + KV_K, 16, 1024), dV = sw128_desc(sb + KV_V, 16, 1024),
                      dAQ = sw128_desc(sb + KV_AQ, 16, 1024), dAO = sw128_desc(sb + KV_AO, 16, 1024),
                      dBQ = sw128_desc(sb + KV_BQ, 16384, 1024), dBO = sw128_desc(sb + KV_BO, 16384, 1024);
+      const bool wide = S::wide(p);
       uint32_t g = 0, lu = 0;
       bool ok = true;
       // S^T (dP^T) of block gg into its one buffer: free, since the product that read the P^T
@@ -656,9 +635,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         const uint64_t q0 = dplus(dAQ, s * 16384u);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 8; ++k) {
+            if (k == 4 && !wide) break;
             mma2_bf16(tmem, dplus(dK, (k >> 2) * 16384 + (k & 3) * 32), dplus(q0, (k >> 2) * 8192 + (k & 3) * 32),
-                      IDESC_KK, k ? 1u : 0u);
+                    IDESC_KK, k ? 1u : 0u);
+          }
           commit2_mc(&c->qempty[s], 3);
           commit2_mc(&c->sfull, 3);
         }
@@ -672,9 +653,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         const uint64_t o0 = dplus(dAO, s * 16384u);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 8; ++k) {
+            if (k == 4 && !wide) break;
             mma2_bf16(tmem + KT_DP, dplus(dV, (k >> 2) * 16384 + (k & 3) * 32),
-                      dplus(o0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+                    dplus(o0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+          }
           commit2_mc(&c->oempty[s], 3);
           commit2_mc(&c->dpfull, 3);
           if (last) commit2_mc(&c->rempty, 3);
@@ -820,7 +803,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         uint32_t rs[2][16];                        // scores, then probabilities
         const int q0 = qg + 2 * (lane & 3);        // the first of the thread's queries
         const float2* ldq = reinterpret_cast<const float2*>(ld) + 16 * cg + (lane & 3);
-        typename S::Factors fac;
         if (!warp_wait_c(&c->sfull, g, c, p.limit_ns) || !warp_wait_f(&c->lfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         __syncwarp();
@@ -834,8 +816,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {            // 16 keys at a time, over this warp's own scores
             uint32_t pk[8] = {};
-            if (all) kv_probs<S, false>(rs[h], h, nl, sc, q0, rows, pk, fac);
-            else if (!none) kv_probs<S, true>(rs[h], h, nl, sc, q0, rows, pk, fac);
+            if (all) kv_probs<S, false>(rs[h], h, nl, sc, q0, rows, pk);
+            else if (!none) kv_probs<S, true>(rs[h], h, nl, sc, q0, rows, pk);
             __syncwarp();
             tmem_st_frag(trow + ((uint32_t)(16 * h) << 16), pk);
           }
@@ -861,8 +843,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t pk[8] = {};
-            if (all) kv_grads<S, false>(rs[h], rd[h], h, nD, q0, rows, fac, pk);
-            else if (!none) kv_grads<S, true>(rs[h], rd[h], h, nD, q0, rows, fac, pk);
+            if (all) kv_grads<S, false>(rs[h], rd[h], h, nD, q0, rows, pk);
+            else if (!none) kv_grads<S, true>(rs[h], rd[h], h, nD, q0, rows, pk);
             __syncwarp();
             tmem_st_frag(trow + KT_DP + ((uint32_t)(16 * h) << 16), pk);
           }
@@ -941,7 +923,7 @@ __device__ __forceinline__ void q_block(const uint32_t (&rs)[32], const uint32_t
     const bool o1 = MASK && (kg + 2 * i + 1 < lo || kg + 2 * i + 1 >= hi);
     if (o0) pp.x = 0.f;
     if (o1) pp.y = 0.f;
-    float2 sv = S::grad2(pp, add2(make_float2(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])), nD), dc);
+    float2 sv = mul2(S::fold(pp, dc), add2(make_float2(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])), nD));
     if (S::kClearMasked && o0) sv.x = 0.f;
     if (S::kClearMasked && o1) sv.y = 0.f;
     dw[i] = pack_bf16(sv.x, sv.y);
@@ -1052,6 +1034,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     if (rank == 0) {   // the whole warp, converged; one elected lane issues
       const uint64_t dR = sw128_desc(sb + Q_R, 16, 1024), dK = sw128_desc(sb + Q_K, 16, 1024),
                      dV = sw128_desc(sb + Q_V, 16, 1024), dY = sw128_desc(sb + Q_Y, 16384, 1024);
+      const bool wide = S::wide(p);
       uint32_t g = 0, lu = 0;
       bool ok = true;
       // S of block gg into its buffer: free, since the dQ product that read the dS in it was
@@ -1063,9 +1046,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         const uint64_t k0 = dplus(dK, s * 16384u);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 8; ++k) {
+            if (k == 4 && !wide) break;
             mma2_bf16(tmem + 128 * s, dplus(q0, (k >> 2) * 16384 + (k & 3) * 32),
-                      dplus(k0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+                    dplus(k0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+          }
           commit2_mc(&c->kempty[s], 3);
         }
         __syncwarp();
@@ -1080,9 +1065,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         const uint64_t v0 = dplus(dV, s * 16384u);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 8; ++k) {
+            if (k == 4 && !wide) break;
             mma2_bf16(tmem + QT_DP, dplus(o0, (k >> 2) * 16384 + (k & 3) * 32),
-                      dplus(v0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+                    dplus(v0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
+          }
           commit2_mc(&c->vempty[s], 3);
           commit2_mc(&c->tfull, 3);
         }
@@ -1154,24 +1141,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(32 * cg);
     uint32_t g = 0, lu = 0;
     bool ok = true;
-    typename S::Raw raw = S::q_raw(p, pid);
-    for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
-      int z, qp, j0, nj;
-      S::q_unit(p, u, raw, z, qp, j0, nj);
-      raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
-      const typename S::Scale sc = S::scale_of(p, z);
-      const int qw = p.c0 + 256 * qp + 128 * (int)rank + 32 * q;   // this warp's first query
-      const int qr = qw + lane;                                     // this thread's query
-      const bool vrow = qr < p.c1;
+    // the next unit's entry is loaded during this one, its rows' values while this one's dQ leaves
+    int z, qp, j0, nj, qw, lo, hi;   // qw: this warp's first query; keys this thread's query sees
+    float lz, Dq;
+    auto rows_of = [&](int u, typename S::Raw r) {
+      S::q_unit(p, u, r, z, qp, j0, nj);
+      qw = p.c0 + 256 * qp + 128 * (int)rank + 32 * q;
+      const int qr = qw + lane;
+      const bool v = u < p.n_units && qr < p.c1;
       const int64_t ro = (int64_t)z * p.T + qr;
-      const float lz = vrow ? p.lse[ro] * L2E : 0.f;
-      const float Dq = vrow ? p.D[ro] : 0.f;
-      int lo, hi, lo0, lo1, hi0, hi1;   // keys this thread's query sees; over the warp's queries
+      lz = v ? p.lse[ro] : 0.f;
+      Dq = v ? p.D[ro] : 0.f;
       S::query_range(p, qr, lo, hi);
+    };
+    uint32_t left = 0;   // units whose dQ has left its staging block (the unit's own Q)
+    auto release = [&]() {
+      if (left == lu) return;
+      if (lane == 0) {
+        bulk_wait_read();
+        mbar_arrive(&c->rempty[left & 1u]);
+      }
+      left = lu;
+    };
+    rows_of(pid, S::q_raw(p, pid));
+    for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
+      const int un = S::next_unit(rnd + 1, pid, npairs);
+      const typename S::Raw raw = S::q_raw(p, un);
+      const typename S::Scale sc = S::scale_of(p, z);
+      const int qr = qw + lane;   // this thread's query
+      const float lz2 = lz * L2E;
+      int lo0, lo1, hi0, hi1;     // over the warp's queries
       S::query_warp(p, qw, lo, hi, lo0, lo1, hi0, hi1);
       if constexpr (!S::kAddOut) {
         if (nj == 0) {   // queries that see no key
-          if (vrow) S::store_dq_zero(p, ro, 32 * cg);
+          if (qr < p.c1) S::store_dq_zero(p, (int64_t)z * p.T + qr, 32 * cg);
+          rows_of(un, raw);
           continue;
         }
       }
@@ -1190,9 +1194,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) dw[i] = 0u;
         } else if (kg >= lo1 && kg + 31 < hi0) {
-          q_block<S, false>(rs, rd, sc, lz, Dq, kg, qr, lo, hi, dw);
+          q_block<S, false>(rs, rd, sc, lz2, Dq, kg, qr, lo, hi, dw);
         } else {
-          q_block<S, true>(rs, rd, sc, lz, Dq, kg, qr, lo, hi, dw);
+          q_block<S, true>(rs, rd, sc, lz2, Dq, kg, qr, lo, hi, dw);
         }
         __syncwarp();
         tmem_st16(trow + 128 * (g & 1u), dw);       // over this warp's own scores
@@ -1200,9 +1204,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->oready_l[g & 1u]);
+        release();
       }
       if (!ok) break;
-      // dQ of the unit's queries: s * accumulator, bf16, this thread's row and 32 of hd
+      // dQ of the unit's queries, s * accumulator in bf16: this warp's 32 rows and 32 of hd leave
+      // through the space of the unit's Q, which no product reads any more
+      const int zu = z, qu = qw;
+      const uint32_t stg = sb + Q_R + (lu & 1u) * 65536u + (uint32_t)(warp - 2) * 2048u;
+      rows_of(un, raw);
       if (!warp_wait_c(&c->dqfull, lu, c, p.limit_ns)) { ok = false; break; }
       ++lu;
       tc_fence_after();
@@ -1213,23 +1222,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
-      if constexpr (S::kAddOut) {
-        if (vrow) {
-          uint4* o = reinterpret_cast<uint4*>(p.dQ + ro * 128 + 32 * cg);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t* v = &ra[8 * k];
-            o[k] = make_uint4(pack_bf16(__uint_as_float(v[0]) * p.scale, __uint_as_float(v[1]) * p.scale),
-                              pack_bf16(__uint_as_float(v[2]) * p.scale, __uint_as_float(v[3]) * p.scale),
-                              pack_bf16(__uint_as_float(v[4]) * p.scale, __uint_as_float(v[5]) * p.scale),
-                              pack_bf16(__uint_as_float(v[6]) * p.scale, __uint_as_float(v[7]) * p.scale));
-          }
+      if (qu < p.c1 && 32 * cg < S::width(p)) {
+        stage_bf16(ra, p.scale, stg, lane);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(maps[Q_MOUT], stg, 32 * cg, qu, zu);
+          bulk_commit();
         }
-      } else {
-        if (vrow) S::store_dq(p, ro, 32 * cg, ra);
       }
       __syncwarp();
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
     if (!ok) fail_f(c, p.status);
   }
   teardown_f(c, warp);

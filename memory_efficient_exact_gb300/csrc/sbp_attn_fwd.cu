@@ -14,8 +14,8 @@
 // again for the exponentials, because 128 registers of scores leave none for the rest (12
 // warps, 168 registers a thread).  The maximum is only raised when a block exceeds it by more
 // than 2^8 (P and its sum stay far from overflow below that), and O rescaled only then.
-// Scores capped at up to kStaticCap need no maximum at all: 2^x neither overflows nor, for
-// the row's own key, underflows.  The sum l adds the fp32 probabilities; P is rounded to
+// Scores capped at up to kStaticCap need no maximum (0, or the row's largest bias): 2^x neither
+// overflows nor, for at least one key, underflows.  The sum l adds the fp32 probabilities; P is rounded to
 // bf16 for the product, the operand type of the tensor pipe at full rate: at most 2^-8 of
 // each probability.
 //
@@ -45,7 +45,8 @@ constexpr uint32_t O_Q = 0;                              // 2 units: this CTA's 
 constexpr uint32_t O_K = 65536;                          // this CTA's 64 keys of the block
 constexpr uint32_t O_V = O_K + KV_STAGES * 16384;        // 128 keys x this CTA's 64 of hd
 constexpr uint32_t O_ML = O_V + KV_STAGES * 16384;       // m, l: [2 units][2 groups][128 rows] float2
-constexpr uint32_t O_CTRL = O_ML + 4096;
+constexpr uint32_t O_STG = O_ML + 4096;                  // one 32 x 32 bf16 block of O a softmax warp
+constexpr uint32_t O_CTRL = O_STG + 8 * 2048;
 // Tensor memory: S (and P over it) of group b at 128 b, its O at T_O + 128 b.
 constexpr uint32_t T_O = 256;
 constexpr uint32_t IDESC_KK = idesc_bf16(256, 128, false, false);  // A, B K-major
@@ -79,15 +80,14 @@ struct Params {
   uint64_t limit_ns;
 };
 
-// Unit u: head z, queries [256 qp, +256), key blocks [j0, j0 + nj).
-__device__ __forceinline__ void unit_of(const Params& p, int u, int& z, int& qp, int& j0, int& nj) {
+// Unit u: head z, queries [256 qp, +256), key blocks [j0, j0 + nj); none past the last.
+struct Unit { int z, qp, j0, nj; };
+__device__ __forceinline__ Unit unit_of(const Params& p, int u) {
+  if (u >= p.n_units) return Unit{0, 0, 0, 0};
   const int i = u / p.H;
-  z = u - i * p.H;
   const int4* s = reinterpret_cast<const int4*>(p.units + i);
   const int4 a = s[0];
-  qp = a.x;
-  j0 = a.y;
-  nj = max(a.z, s[1].x) - a.y;
+  return Unit{u - i * p.H, a.x, a.y, max(a.z, s[1].x) - a.y};
 }
 
 __device__ __forceinline__ void fail_o(Ctrl* c, int32_t* status) {
@@ -122,6 +122,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct Row {
   int a, b;     // visible: keys k0 + [a, b)
   float fd;     // query - k0
+  float top;    // the cap, less a fixed maximum
 };
 
 // 32 scores (keys k0 + c ..) as they enter the exponential, -inf where the row does not see
@@ -132,7 +133,7 @@ __device__ __forceinline__ void scores32(uint32_t (&r)[32], int c, bool mask, co
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       const float x = __uint_as_float(r[i]);
-      r[i] = __float_as_uint(CAP ? pk::capped(sc, x) : x * sc.sl2);
+      r[i] = __float_as_uint(CAP ? pk::capped(sc, x, w.top) : x * sc.sl2);
     }
   }
   if (BIAS) {
@@ -168,11 +169,12 @@ __device__ __forceinline__ void probs32(const uint32_t (&r)[32], float mul, floa
 }
 
 // tmVt: the last block's V with zeroed padding (PackedWork::tail)
-// FIXED: scores capped low enough for a maximum of 0 throughout.
+// FIXED: scores capped low enough for a maximum that is known beforehand.
 template <bool CAP, bool BIAS, bool FIXED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k_attn_o(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-             const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVt, const Params p) {
+             const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVt,
+             const __grid_constant__ CUtensorMap tmO, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl* c = reinterpret_cast<Ctrl*>(base + O_CTRL);
@@ -220,9 +222,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       prefetch_map(&tmK);
       uint32_t g = 0, lu = 0;   // blocks and units so far
       bool ok = true;
+      Unit next = unit_of(p, pid);   // loaded a unit ahead
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
-        int z, qp, j0, nj;
-        unit_of(p, u, z, qp, j0, nj);
+        const auto [z, qp, j0, nj] = next;
+        next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
         if (nj <= 0) continue;
         const uint32_t qs = lu & 1u;
         if (!wait1(&c->qempty[qs], (lu >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
@@ -260,9 +263,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int tail = *p.tail;
       uint32_t g = 0;
       bool ok = true;
+      Unit next = unit_of(p, pid);   // loaded a unit ahead
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
-        int z, qp, j0, nj;
-        unit_of(p, u, z, qp, j0, nj);
+        const auto [z, qp, j0, nj] = next;
+        next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
         for (int j = 0; j < nj; ++j) {
           const uint32_t s = g % KV_STAGES;
           if (!wait1(&c->vempty[s], (g / KV_STAGES) ^ 1u, c, p.limit_ns)) { ok = false; break; }
@@ -310,9 +314,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
         return true;
       };
+      Unit next = unit_of(p, pid);   // loaded a unit ahead
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
-        int z, qp, j0, nj;
-        unit_of(p, u, z, qp, j0, nj);
+        const auto [z, qp, j0, nj] = next;
+        next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
         if (nj <= 0) continue;
         const uint32_t qs = lu & 1u;
         if (!warp_wait(&c->qfull[qs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
@@ -347,9 +352,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (lane == 0) {   // forwarder
       uint32_t g = 0;
       bool ok = true;
+      Unit next = unit_of(p, pid);   // loaded a unit ahead
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
-        int z, qp, j0, nj;
-        unit_of(p, u, z, qp, j0, nj);
+        const auto [z, qp, j0, nj] = next;
+        next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
         for (int j = 0; j < nj; ++j, ++g) {
           if (!wait1(&c->pready_l[g & 1u], g >> 1, c, p.limit_ns)) { ok = false; break; }
           arrive_remote(mapa(saddr(&c->pready_r[g & 1u]), 0));
@@ -368,16 +374,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const float mul = RAW ? p.sc.sl2 : 1.f;
     uint32_t g = 0, lu = 0;
     bool ok = true;
+    const uint32_t stg = sb + O_STG + (uint32_t)(warp - SOFT_WARP) * 2048u;
+    Unit next = unit_of(p, pid);   // the next unit's entry and this thread's row of it
+    int nrow, nlo, nhi;
+    auto row_ahead = [&]() {
+      nrow = 256 * next.qp + 128 * (int)rank + lrow;
+      nlo = nrow < p.T ? p.lo[nrow] : p.T;
+      nhi = nrow < p.T ? p.hi[nrow] : p.T;
+    };
+    row_ahead();
     for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
-      int z, qp, j0, nj;
-      unit_of(p, u, z, qp, j0, nj);
-      const int row = 256 * qp + 128 * (int)rank + lrow;
+      const auto [z, qp, j0, nj] = next;
+      const int row = nrow, lo = nlo, hi = nhi;   // the row sees the keys [lo, hi)
       const bool vrow = row < p.T;
       const int64_t ro = (int64_t)z * p.T + row;
-      const int lo = vrow ? p.lo[row] : p.T, hi = vrow ? p.hi[row] : p.T;
+      next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
       const int lo1 = __shfl_sync(0xffffffffu, lo, 31), hi0 = __shfl_sync(0xffffffffu, hi, 0);
       const pk::ScaleZ sc = pk::scale_z(p.sc, BIAS ? p.slopes[z] : 0.f);
-      float m = FIXED ? 0.f : -INFINITY;
+      // FIXED: the bias of the farthest key where the bias rises with the distance, else 0
+      float m = FIXED ? (BIAS ? fmaxf(0.f, -sc.slope2 * (float)max(row - lo, hi - 1 - row)) : 0.f) : -INFINITY;
+      const float top = sc.c2 - (FIXED ? m : 0.f);
       float2 l2 = make_float2(0.f, 0.f);
       for (int n = (int)((g ^ (uint32_t)grp) & 1u); n < nj; n += 2) {   // this group's blocks
         if (!warp_wait(&c->sfull[grp], (g + n) >> 1, c, p.limit_ns)) { ok = false; break; }
@@ -385,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
         const int k0 = 128 * (j0 + n);
         const bool mask = k0 < lo1 || k0 + 127 >= hi0;   // some row of the warp does not see all keys
-        const Row w{lo - k0, hi - k0, (float)(row - k0)};
+        const Row w{lo - k0, hi - k0, (float)(row - k0), top};
         uint32_t ra[32], rb[32], pw[32];
         if (!FIXED) {
           tmem_ld32(tS + 64, ra);
@@ -453,6 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int k = 0; k < 8; ++k)
             if (64 * grp + 8 * k < p.hd) dst[k] = make_uint4(0u, 0u, 0u, 0u);
         }
+        row_ahead();
         continue;
       }
       g += (uint32_t)nj;
@@ -461,6 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       ml[grp * 128 + lrow] = make_float2(m, l2.x + l2.y);
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->mlx);
+      row_ahead();
       if (!warp_wait(&c->mlx, lu, c, p.limit_ns) || !warp_wait(&c->ofull, lu, c, p.limit_ns)) { ok = false; break; }
       tc_fence_after();
       __syncwarp();
@@ -484,28 +502,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
         }
-        if (vrow) {
-          uint4* dst = reinterpret_cast<uint4*>(p.O + ro * p.hd + 64 * grp + h);
+        // through this warp's staging block: whole rows, clipped to the tensor
+        if (lane == 0) bulk_wait_read();   // the block's previous contents have left
+        __syncwarp();
+        uint32_t v[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t v[4];
+        for (int i = 0; i < 16; ++i) {
+          // a group without a block for the row leaves its accumulator unset: selected out
+          const float x0 = f0 == 0.f ? 0.f : __uint_as_float(ra[2 * i]) * a0;
+          const float x1 = f0 == 0.f ? 0.f : __uint_as_float(ra[2 * i + 1]) * a0;
+          const float y0 = f1 == 0.f ? 0.f : __uint_as_float(rb[2 * i]) * a1;
+          const float y1 = f1 == 0.f ? 0.f : __uint_as_float(rb[2 * i + 1]) * a1;
+          v[i] = pack_bf16(x0 + y0, x1 + y1);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 8 * k + 2 * i;
-              // a group without a block for the row leaves its accumulator unset: selected out
-              const float x0 = f0 == 0.f ? 0.f : __uint_as_float(ra[e]) * a0;
-              const float x1 = f0 == 0.f ? 0.f : __uint_as_float(ra[e + 1]) * a0;
-              const float y0 = f1 == 0.f ? 0.f : __uint_as_float(rb[e]) * a1;
-              const float y1 = f1 == 0.f ? 0.f : __uint_as_float(rb[e + 1]) * a1;
-              v[i] = pack_bf16(x0 + y0, x1 + y1);
-            }
-            if (64 * grp + h + 8 * k < p.hd) dst[k] = make_uint4(v[0], v[1], v[2], v[3]);
-          }
+        for (int k = 0; k < 4; ++k)
+          sts128(stg + 64u * lane + 16u * k, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        fence_proxy_async();
+        __syncwarp();
+        const int row0 = row - lane, col = 64 * grp + h;
+        if (lane == 0 && row0 < p.T && col < p.hd) {
+          tma_store_3d(&tmO, stg, col, row0, z);
+          bulk_commit();
         }
       }
       ++lu;
     }
     if (!ok) fail_o(c, p.status);
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -522,8 +547,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 namespace {
 
 // Largest cap that needs no running maximum: 2^x of scores within 64 log2(e) = 92 lies in
-// [2^-92, 2^92], and so do sums over any number of keys that fits; a distance bias only lowers
-// other keys than the row's own.
+// [2^-92, 2^92], and sums over any number of keys that fits stay far from overflow.  With a
+// distance bias the scores less the row's largest bias take the place of x: none is above 92,
+// and the key with that bias (the row's own, or the farthest) is not below -92.
 constexpr float kStaticCap = 64.f;
 
 template <bool CAP, bool BIAS, bool FIXED>
@@ -542,13 +568,13 @@ cudaError_t launch_o(const PackedArgs& a, const PackedWork& w, void* O, float* l
   p.sc = tc::pk::make_scale(a.scale, a.softcap);
   p.slopes = a.slopes; p.units = w.qunits; p.lo = w.lo; p.hi = w.hi; p.tail = w.tail;
   p.O = static_cast<__nv_bfloat16*>(O); p.lse = lse; p.status = a.status; p.limit_ns = tc::wait_limit_ns();
-  CUtensorMap mQ, mK, mV, mVt;
+  CUtensorMap mQ, mK, mV, mVt, mO;
   if (!tc::make_map_heads(&mQ, a.Q, a.T, a.H, a.hd, 128) || !tc::make_map_heads(&mK, a.K, a.T, a.Hkv, a.hd, 64) ||
       !tc::make_map_heads(&mV, a.V, a.T, a.Hkv, a.hd, 128) ||
-      !tc::make_map_heads(&mVt, w.tail_kv, 128, a.Hkv, a.hd, 128))
+      !tc::make_map_heads(&mVt, w.tail_kv, 128, a.Hkv, a.hd, 128) || !tc::make_map_out(&mO, O, a.T, a.T, a.H, a.hd, 2))
     return cudaErrorInvalidValue;
   const int pairs = std::min(tc::max_pairs((const void*)k_attn_o<CAP, BIAS, FIXED>, SMEM, THREADS), p.n_units);
-  k_attn_o<CAP, BIAS, FIXED><<<2 * pairs, THREADS, SMEM, s>>>(mQ, mK, mV, mVt, p);
+  k_attn_o<CAP, BIAS, FIXED><<<2 * pairs, THREADS, SMEM, s>>>(mQ, mK, mV, mVt, mO, p);
   return cudaGetLastError();
 }
 

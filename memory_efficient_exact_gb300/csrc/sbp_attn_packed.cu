@@ -3,7 +3,6 @@
 // sbp_attn_fwd.cu, the definition of what a query sees in sbp_attn_packed.cuh.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "sbp_attn_fused.cuh"
 #include "sbp_attn_packed.cuh"
@@ -46,21 +45,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Columns [c, c + n) of a row of width hd (a multiple of 8) from fp32 v, times f, in bf16.
-template <int N>
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, int hd, int c, const uint32_t (&v)[N], float f) {
-  uint4* o = reinterpret_cast<uint4*>(row + c);
-#pragma unroll
-  for (int k = 0; k < N / 8; ++k)
-    if (c + 8 * k < hd) {
-      const uint32_t* e = &v[8 * k];
-      o[k] = make_uint4(pack2(__uint_as_float(e[0]) * f, __uint_as_float(e[1]) * f),
-                        pack2(__uint_as_float(e[2]) * f, __uint_as_float(e[3]) * f),
-                        pack2(__uint_as_float(e[4]) * f, __uint_as_float(e[5]) * f),
-                        pack2(__uint_as_float(e[6]) * f, __uint_as_float(e[7]) * f));
-    }
-}
-
 // Score policy (see CausalScores): documents, prefixes, cap and distance bias; the units
 // and intervals come from the preparing kernel, and every output element is written once,
 // in bf16 (dK and dV of a key sum over the group's heads in tensor memory).
@@ -69,7 +53,7 @@ struct PackedScores {
   using Kv = KvParams;
   using Q = QParams;
   using KvMaps = fa::MapArray<fa::KV_MAPS + 2>;
-  using QMaps = fa::MapArray<fa::Q_MAPS + 1>;
+  using QMaps = fa::MapArray<fa::Q_MAPS + 1>;   // + the last block's K
   // a masked pair's score may be infinite or NaN (another document's values)
   static constexpr bool kClearMasked = true;
   static constexpr bool kAddOut = false;
@@ -136,7 +120,7 @@ struct PackedScores {
                                                   float2& dc) {
     float2 x;
     if (CAP) {
-      x = make_float2(capped(sc, s.x), capped(sc, s.y));
+      x = make_float2(capped(sc, s.x, sc.c2), capped(sc, s.y, sc.c2));
       const float2 th = mul2(x, make_float2(sc.ic2, sc.ic2));
       dc = fma2(make_float2(-th.x, -th.y), th, make_float2(1.f, 1.f));   // 1 - tanh^2
       x = add2(x, nlz);
@@ -150,25 +134,7 @@ struct PackedScores {
     }
     return x;
   }
-  static __device__ __forceinline__ float2 grad2(float2 p, float2 d, float2 dc) {
-    return CAP ? mul2(mul2(p, d), dc) : mul2(p, d);
-  }
-
-  struct NoFactors {};
-  struct CapFactors { uint32_t h[16]; };
-  using Factors = typename std::conditional<CAP, CapFactors, NoFactors>::type;
-  // 1 - tanh^2 of two scores as half-precision numbers in [0, 1]: 2^-11 of the value, an eighth of
-  // what rounding dS to bf16 does to it, and half the registers of fp32.
-  static __device__ __forceinline__ void keep(Factors& f, int i, float2 dc) {
-    if constexpr (CAP) {
-      const __half2 h = __floats2half2_rn(dc.x, dc.y);
-      f.h[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  static __device__ __forceinline__ float2 kept(const Factors& f, int i) {
-    if constexpr (CAP) return __half22float2(*reinterpret_cast<const __half2*>(&f.h[i]));
-    else return make_float2(1.f, 1.f);
-  }
+  static __device__ __forceinline__ float2 fold(float2 p, float2 dc) { return CAP ? mul2(p, dc) : p; }
 
   // How 32 x 32 blocks of dV (t = 0) and dK (t = 1) leave (see CausalScores): bf16, or the parts'
   // fp32 sums.
@@ -200,14 +166,15 @@ struct PackedScores {
         }
       }
   }
-  // 32 columns of dQ of one query (row ro of [H, T])
-  static __device__ __forceinline__ void store_dq(const Q& p, int64_t ro, int c, const uint32_t (&ra)[32]) {
-    store_row(p.dQ + ro * p.hd, p.hd, c, ra, p.scale);
-  }
+  // 32 columns of dQ of a query that sees no key (row ro of [H, T])
   static __device__ __forceinline__ void store_dq_zero(const Q& p, int64_t ro, int c) {
-    const uint32_t z[32] = {};
-    store_dq(p, ro, c, z);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + 8 * k < p.hd) *reinterpret_cast<uint4*>(p.dQ + ro * p.hd + c + 8 * k) = make_uint4(0u, 0u, 0u, 0u);
   }
+  template <class P>
+  static __device__ __forceinline__ bool wide(const P& p) { return p.hd > 64; }
+  static __device__ __forceinline__ int width(const Q& p) { return p.hd; }
 };
 
 // ------------------------------------------------------------------- preparing kernel
@@ -441,18 +408,16 @@ bool packed_supported(int64_t H, int64_t T, int64_t hd) {
          H * ((T + 255) / 256) <= INT32_MAX / 2 && (H * T + 15) / 16 + T / 256 < INT32_MAX / 2;
 }
 
-// Query heads of a group that one k_attn_kv unit walks.  All of them where that leaves enough
-// units for the SM pairs (a key's dK and dV are then summed on chip); fewer where key / value
-// heads are few and documents long, the sums joined by k_packed_join.
+// Query heads of a group that one k_attn_kv unit walks: all of them where that leaves two units
+// or more for each SM pair (a key's dK and dV are then summed on chip), else as few as give four,
+// the sums joined by k_packed_join.  The backward with and without (H / Hkv x tokens, hd 128):
+// 16/1 x 128 36 and 55 us, 32/8 x 256 36 and 42, 32/8 x 1024 68 and 92, 20/4 x 4099 265 and
+// 350; the other way at two units a pair, 32/8 x 8192 in documents, 492 and 480 (the join reads
+// and writes the sums again).
 int kv_heads_per_part(int64_t H, int64_t Hkv, int64_t T) {
-  const int64_t group = H / Hkv, n = (T + 255) / 256, pairs = std::max(1, num_sms() / 2);
-#ifndef KVU
-#define KVU 2
-#define KVT 512
-#endif
-  const int64_t want = KVU * pairs;
-  if (T < KVT || n * Hkv >= want || group == 1) return (int)group;
-  const int64_t parts = std::min(group, (want + n * Hkv - 1) / (n * Hkv));
+  const int64_t group = H / Hkv, units = std::max<int64_t>(1, (T + 255) / 256 * Hkv), pairs = std::max(1, num_sms() / 2);
+  if (units >= 2 * pairs) return (int)group;
+  const int64_t parts = std::min(group, (4 * pairs + units - 1) / units);
   return (int)((group + parts - 1) / parts);
 }
 
@@ -589,13 +554,14 @@ cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedLayout& L, 
   // outputs: dK and dV in bf16, or the parts' sums
   for (int t = 0; t < 2; ++t) {
     CUtensorMap* m = &mk.m[t ? KV_MOUTV : KV_MOUTK];
-    const bool ok = L.parts == 1 ? tc::make_map_out(m, t ? dV : dK, a.T, a.Hkv, a.hd, 2)
-                                 : tc::make_map_out(m, base + (t ? L.off_pv : L.off_pk), a.T, L.parts * a.Hkv, a.hd, 4);
+    const bool ok = L.parts == 1 ? tc::make_map_out(m, t ? dV : dK, a.T, a.T, a.Hkv, a.hd, 2)
+                                 : tc::make_map_out(m, base + (t ? L.off_pv : L.off_pk), a.T, a.T, L.parts * a.Hkv, a.hd, 4);
     if (!ok) return cudaErrorInvalidValue;
   }
   mq.m[Q_MQ] = mk.m[KV_MQB];
   mq.m[Q_MO] = mk.m[KV_MOB];
   mq.m[Q_MKB] = mk.m[KV_MK];
+  if (!tc::make_map_out(&mq.m[Q_MOUT], dQ, a.T, a.T, a.H, a.hd, 2)) return cudaErrorInvalidValue;
   tc::pk::KvParams k;
   k.H = (int)a.H; k.Hkv = (int)a.Hkv; k.T = (int)a.T; k.c0 = 0; k.c1 = (int)a.T; k.hd = (int)a.hd;
   k.group = (int)(a.H / a.Hkv); k.n_units = n * k.Hkv * L.parts;

@@ -74,11 +74,11 @@ __device__ __forceinline__ ScaleZ scale_z(const Scale& s, float slope) {
   return z;
 }
 
-// The capped score in log2 units.
-__device__ __forceinline__ float capped(const Scale& sc, float s) {
+// The capped score in log2 units, `top` for the largest.
+__device__ __forceinline__ float capped(const Scale& sc, float s, float top) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(s * sc.k)));
-  return fmaf(-2.f * sc.c2, r, sc.c2);
+  return fmaf(-2.f * sc.c2, r, top);
 }
 
 inline Scale make_scale(float scale, float softcap) {

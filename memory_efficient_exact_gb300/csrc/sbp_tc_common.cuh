@@ -531,12 +531,13 @@ inline bool make_map_heads(CUtensorMap* m, const void* ptr, int64_t T, int64_t h
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D map over head-major outputs [heads, T, hd] of `esize` bytes an element: 32 x 32 x 1 boxes,
-// bf16 rows of 64 bytes unswizzled, fp32 rows of 128 bytes with the 128-byte swizzle.
-inline bool make_map_out(CUtensorMap* m, void* ptr, int64_t T, int64_t heads, int64_t hd, int esize) {
+// 3-D map over the first `rows` rows of each head of head-major outputs [heads, T, hd], `esize`
+// bytes an element: 32 x 32 x 1 boxes, bf16 rows of 64 bytes unswizzled, fp32 rows of 128 bytes
+// with the 128-byte swizzle.
+inline bool make_map_out(CUtensorMap* m, void* ptr, int64_t rows, int64_t T, int64_t heads, int64_t hd, int esize) {
   auto enc = encoder();
   if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)T, (cuuint64_t)heads};
+  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)rows, (cuuint64_t)heads};
   cuuint64_t strides[2] = {(cuuint64_t)(hd * esize), (cuuint64_t)T * (cuuint64_t)(hd * esize)};
   cuuint32_t box[3] = {32, 32, 1};
   cuuint32_t es[3] = {1, 1, 1};

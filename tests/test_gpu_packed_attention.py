@@ -124,6 +124,16 @@ def test_cap_and_bias(sbp, softcap, alibi, gain, prefix):
     check(sbp, x, kw, cu, prefix, sl, 128 ** -0.5)
 
 
+# slopes below 0 favour far keys: by more than 2^127 for the first head
+@pytest.mark.parametrize("softcap", [0.0, 15.0, 100.0])
+@pytest.mark.parametrize("prefix", [None, [200, 0]])
+def test_slopes_of_either_sign(sbp, softcap, prefix):
+    x = make(4, 2, 420, 128, seed=10)
+    cu, _, kw = options(4, [300, 100], prefix, softcap, False)
+    sl = np.array([-0.5, 0.25, -0.03125, 0.0], np.float32)
+    check(sbp, x, {**kw, "slopes": dev(sl, torch.float32)}, cu, prefix, sl, 128 ** -0.5)
+
+
 @pytest.mark.parametrize("hd", [8, 16, 40, 64, 72, 80, 96, 120, 128])
 def test_head_widths(sbp, hd):
     x = make(3, 1, 200, hd, seed=hd)
@@ -136,6 +146,13 @@ def test_more_units_than_pairs(sbp):
     x = make(48, 8, 600, 128, seed=1)
     cu, sl, kw = options(48, [300, 290], None, 0.0, False)
     check(sbp, x, kw, cu, None, sl, 128 ** -0.5)
+
+
+def test_units_without_a_token(sbp):
+    # most units are padding alone: their rows are cleared between and behind the others
+    x = make(48, 8, 1100, 64, seed=11)
+    cu, sl, kw = options(48, [130, 170], None, 0.0, False)
+    check(sbp, x, kw, cu, None, sl, 0.125)
 
 
 def test_running_maximum_is_raised(sbp):
