@@ -315,7 +315,7 @@ __device__ __forceinline__ void kv_probs(uint32_t (&r)[16], int h, const float2 
     for (int g = 0; g < 4; ++g) {
       uint32_t &r0 = r[4 * g + 2 * e], &r1 = r[4 * g + 2 * e + 1];
       float2 dc;
-      const float2 x = S::log2p2(sc, make_float2(__uint_as_float(r0), __uint_as_float(r1)), nlse[g], fd, (float)(8 * g),
+      const float2 x = S::template log2p2<MASK>(sc, make_float2(__uint_as_float(r0), __uint_as_float(r1)), nlse[g], fd, (float)(8 * g),
                                  (float)(8 * g + 1), dc);
       float2 pp = exp2_pair(x.x, x.y);
       const int q = q0 + 8 * g;
@@ -480,7 +480,8 @@ struct CausalScores {
   static __device__ __forceinline__ Scale scale_of(const P& p, int) { return p.scale * L2E; }
   // log2 of the probabilities of two neighbouring pairs from their raw scores s, -lse in log2
   // units and their distances query - key, d + o0 and d + o1; dc: the factors of the scores'
-  // gradients.
+  // gradients.  MASK: one of the two may be masked.
+  template <bool>
   static __device__ __forceinline__ float2 log2p2(Scale sl2, float2 s, float2 nlz, float, float, float, float2& dc) {
     dc = make_float2(1.f, 1.f);
     return fma2(s, make_float2(sl2, sl2), nlz);
@@ -916,7 +917,7 @@ __device__ __forceinline__ void q_block(const uint32_t (&rs)[32], const uint32_t
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float2 dc;
-    const float2 x = S::log2p2(sc, make_float2(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])), nlz, fd,
+    const float2 x = S::template log2p2<MASK>(sc, make_float2(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])), nlz, fd,
                                (float)(-2 * i), (float)(-2 * i - 1), dc);
     float2 pp = exp2_pair(x.x, x.y);
     const bool o0 = MASK && (kg + 2 * i < lo || kg + 2 * i >= hi);

@@ -10,10 +10,11 @@
 // While one group works on a block, the tensor pipe runs the other group's O += P V and its
 // next S.  At the end the two accumulators are joined, O = (O0 2^(m0-m) + O1 2^(m1-m)) / l.
 // Nothing of size (queries x keys) leaves the SM.
-// A row's 128 scores are read twice, 64 at a time: once for the maximum, and the second half
-// again for the exponentials, because 128 registers of scores leave none for the rest (12
-// warps, 168 registers a thread).  The maximum is only raised when a block exceeds it by more
-// than 2^8 (P and its sum stay far from overflow below that), and O rescaled only then.
+// The exponentials are taken from the maximum of earlier blocks, while the block's own is found
+// beside them: any reference serves the quotient as long as neither overflows.  Only a block
+// that exceeds it by 2^kLag or holds a row's first keys is read once more beforehand, to raise
+// the maximum and rescale O and l.  (The maximum first, for every block, took 1.67 ms in place
+// of TIME at 32 heads, 16384 tokens: a second pass over the scores.)
 // Scores capped at up to kStaticCap need no maximum (0, or the row's largest bias): 2^x neither
 // overflows nor, for at least one key, underflows.  The sum l adds the fp32 probabilities; P is rounded to
 // bf16 for the product, the operand type of the tensor pipe at full rate: at most 2^-8 of
@@ -37,6 +38,8 @@ using fa::tmem_st_wait;
 // and 8-11 the softmax groups (lane quadrant warp % 4).
 constexpr int SOFT_WARP = 4;
 constexpr int THREADS = 384;
+// The running maximum may lag behind the scores by this many powers of two.
+constexpr float kLag = 16.f;
 
 // Shared memory, bytes from the 1024-aligned base; tiles are 128-byte swizzled
 // [64-element block][rows][128 B].
@@ -45,8 +48,7 @@ constexpr uint32_t O_Q = 0;                              // 2 units: this CTA's 
 constexpr uint32_t O_K = 65536;                          // this CTA's 64 keys of the block
 constexpr uint32_t O_V = O_K + KV_STAGES * 16384;        // 128 keys x this CTA's 64 of hd
 constexpr uint32_t O_ML = O_V + KV_STAGES * 16384;       // m, l: [2 units][2 groups][128 rows] float2
-constexpr uint32_t O_STG = O_ML + 4096;                  // one 32 x 32 bf16 block of O a softmax warp
-constexpr uint32_t O_CTRL = O_STG + 8 * 2048;
+constexpr uint32_t O_CTRL = O_ML + 4096;
 // Tensor memory: S (and P over it) of group b at 128 b, its O at T_O + 128 b.
 constexpr uint32_t T_O = 256;
 constexpr uint32_t IDESC_KK = idesc_bf16(256, 128, false, false);  // A, B K-major
@@ -54,7 +56,7 @@ constexpr uint32_t IDESC_KM = idesc_bf16(256, 128, false, true);   // A K-major,
 
 struct Ctrl {
   uint64_t kfull[KV_STAGES], kempty[KV_STAGES], vfull[KV_STAGES], vempty[KV_STAGES];
-  uint64_t qfull[2], qempty[2];
+  uint64_t qfull[2], qempty[2];   // Q of the unit; free: its products are done, and O has left
   uint64_t sfull[2];      // S of the group's block is ready, and its earlier products are done
   uint64_t pready_l[2];   // P is written: the CTA's four warps of the group
   uint64_t pready_r[2];   // the same of the other CTA (leader)
@@ -101,7 +103,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, Ctrl* c,
   return __all_sync(0xffffffffu, wait_inl<true>(b, parity & 1u, &c->abort, limit));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
       "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
@@ -118,33 +120,49 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// A row's view of 32 keys: which of them it sees, and how far they are.
+// A row's view of a block's keys k0 .., and what its warp's rows have in common.
 struct Row {
-  int a, b;     // visible: keys k0 + [a, b)
-  float fd;     // query - k0
-  float top;    // the cap, less a fixed maximum
+  int a, b;           // the row sees the keys k0 + [a, b)
+  int all_a, all_b;   // every row of the warp sees k0 + [all_a, all_b)
+  int first;          // the warp's first query - k0
+  float fd;           // the query - k0
+  float top;          // the cap, less a fixed maximum
+  __device__ __forceinline__ bool masked(int c, int n) const { return c < all_a || c + n > all_b; }   // keys c .. c + n - 1
+  // some row does not see all 128 keys, or (BIAS) they lie on both sides of the warp's queries
+  template <bool BIAS>
+  __device__ __forceinline__ bool edge() const { return masked(0, 128) || (BIAS && first < 127 && first + 31 > 0); }
 };
+// The lowest n bits, n from 0 to 32 after clamping.
+__device__ __forceinline__ uint32_t low_bits(int n) { return (uint32_t)((1ull << min(max(n, 0), 32)) - 1); }
 
-// 32 scores (keys k0 + c ..) as they enter the exponential, -inf where the row does not see
-// the key.  RAW: left unscaled.
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ void scores32(uint32_t (&r)[32], int c, bool mask, const Row& w, const pk::ScaleZ& sc) {
+// 32 scores (keys k0 + c ..) as they enter the exponential (left unscaled without cap and bias).
+// EDGE: -inf where the row does not see the key, and the bias by each key's distance; else its
+// products with the distance are linear in the key.
+template <bool CAP, bool BIAS, bool EDGE>
+__device__ __forceinline__ void scores32(uint32_t (&r)[32], int c, const Row& w, const pk::ScaleZ& sc) {
+  auto f2 = [&](int i) { return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); };
+  const float m = CAP ? -2.f * sc.c2 : sc.sl2, top = CAP ? w.top : 0.f;
+  float fd = w.fd - (float)c;
+  if (BIAS) asm volatile("" : "+f"(fd));   // 128 distances are not worth keeping for a second pass
+  const float step = w.first > 0 ? sc.slope2 : -sc.slope2, at0 = fmaf(-step, fd, top);
+  auto add = [&](int i) {   // the bias of key i
+    if (!BIAS) return top;
+    return EDGE ? fmaf(-sc.slope2, fabsf(fd - (float)i), top) : fmaf(step, (float)i, at0);
+  };
   if (CAP || BIAS) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float x = __uint_as_float(r[i]);
-      r[i] = __float_as_uint(CAP ? pk::capped(sc, x, w.top) : x * sc.sl2);
+    for (int i = 0; i < 16; ++i) {
+      const float2 v = fma2(CAP ? pk::cap_parts<EDGE>(sc, f2(i)) : f2(i), make_float2(m, m),
+                            make_float2(add(2 * i), add(2 * i + 1)));
+      r[2 * i] = __float_as_uint(v.x);
+      r[2 * i + 1] = __float_as_uint(v.y);
     }
   }
-  if (BIAS) {
+  if (EDGE && w.masked(c, 32)) {
+    const uint32_t see = low_bits(w.b - c) & ~low_bits(w.a - c);
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      r[i] = __float_as_uint(fmaf(-sc.slope2, fabsf(w.fd - (float)(c + i)), __uint_as_float(r[i])));
-  }
-  if (mask) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c + i < w.a || c + i >= w.b) r[i] = 0xff800000u;
+      if (!(see & (1u << i))) r[i] = 0xff800000u;
   }
 }
 __device__ __forceinline__ float max32(const uint32_t (&r)[32], float m0) {
@@ -155,6 +173,8 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], float m0) {
   return max3(fmaxf(m[0], m[1]), m[2], fmaxf(m[3], __uint_as_float(r[31])));
 }
 // 32 probabilities 2^(mul x + nm) (PLAIN: 2^x): packed to bf16, their sum added to l.
+// (Keeping a quarter or more of them off the special-function unit, by a polynomial, took
+// longer at every share: 1.67 ms against 2.08 at 32 heads, 16384 tokens.)
 template <bool PLAIN>
 __device__ __forceinline__ void probs32(const uint32_t (&r)[32], float mul, float nm, uint32_t* pw, float2& l) {
   const float2 m2 = make_float2(mul, mul), nm2 = make_float2(nm, nm);
@@ -166,6 +186,75 @@ __device__ __forceinline__ void probs32(const uint32_t (&r)[32], float mul, floa
     l = add2(l, e);
     pw[i] = pack_bf16(e.x, e.y);
   }
+}
+
+// A block of 128 scores of a row (tensor memory tS) into its probabilities there; m and l are the
+// row's running maximum and sum, tO the group's accumulator, `fresh` while that holds nothing.
+template <bool CAP, bool BIAS, bool FIXED, bool EDGE>
+__device__ __forceinline__ void soft_block(uint32_t tS, uint32_t tO, bool fresh, const Row& w, const pk::ScaleZ& sc,
+                                           float mul, float& m, float2& l) {
+  uint32_t ra[32], rb[32], pw[64];
+  float2 lb;   // the block's sums
+  // whether the maximum has to be found before the exponentials
+  bool raise = !FIXED && __any_sync(0xffffffffu, m == -INFINITY && w.a < 128 && w.b > 0);
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (raise) {
+      float mb = m;
+#pragma unroll 1
+      for (int h = 0; h < 128; h += 32) {
+        __syncwarp();
+        tmem_ld32(tS + h, ra);
+        tmem_ld_wait();
+        scores32<CAP, BIAS, true>(ra, h, w, sc);
+        mb = max32(ra, mb);
+      }
+      const float f = mb > m ? ex2((m - mb) * mul) : 1.f;   // 0 from m = -inf
+      if (mb > m) m = mb;
+      l.x *= f;
+      l.y *= f;
+      if (!fresh && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+        for (int h = 0; h < 128; h += 16) {
+          uint32_t o[16];
+          fa::tmem_ld16(tO + h, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          fa::tmem_st16(tO + h, o);
+        }
+      }
+    }
+    const float nm = m == -INFINITY ? 0.f : -m * mul;
+    float mb = -INFINITY;
+    lb = make_float2(0.f, 0.f);
+    auto part = [&](uint32_t (&r)[32], int c, uint32_t* out) {
+      scores32<CAP, BIAS, EDGE>(r, c, w, sc);
+      if (!FIXED) mb = max32(r, mb);
+      probs32<FIXED>(r, mul, nm, out, lb);
+    };
+    __syncwarp();
+    tmem_ld32(tS, ra);
+    tmem_ld32(tS + 32, rb);
+    tmem_ld_wait();
+    part(ra, 0, pw);
+    __syncwarp();
+    tmem_ld32(tS + 64, ra);
+    part(rb, 32, pw + 16);
+    __syncwarp();
+    tmem_ld32(tS + 96, rb);
+    if (FIXED) tmem_st32(tS, pw);   // over scores that are in registers
+    tmem_ld_wait();
+    part(ra, 64, pw + 32);
+    part(rb, 96, pw + 48);
+    raise = !FIXED && __any_sync(0xffffffffu, (mb - m) * mul > kLag);
+    if (!raise) break;   // always so after a pass that found the maximum
+  }
+  l = add2(l, lb);
+  __syncwarp();
+  if (!FIXED) tmem_st32(tS, pw);    // all the scores have been read
+  tmem_st32(tS + 32, pw + 32);
+  tmem_st_wait();
 }
 
 // tmVt: the last block's V with zeroed padding (PackedWork::tail)
@@ -190,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->qfull[i], 1);
-      mbar_init(&c->qempty[i], 1);
+      mbar_init(&c->qempty[i], 1 + 8);
       mbar_init(&c->sfull[i], 1);
       mbar_init(&c->pready_r[i], 1);
       mbar_init(&c->pready_l[i], 4);
@@ -294,9 +383,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       // S of block gg into its group's buffer: free, since the product that read the P in it
       // was issued before
-      auto scores = [&](uint32_t gg, uint32_t qs) -> bool {
+      auto wait_k = [&](uint32_t gg) { return fa::warp_wait_f(&c->kfull[gg % KV_STAGES], gg / KV_STAGES, c, p.limit_ns); };
+      auto scores = [&](uint32_t gg, uint32_t qs) {
         const uint32_t s = gg % KV_STAGES, b = gg & 1u;
-        if (!warp_wait(&c->kfull[s], gg / KV_STAGES, c, p.limit_ns)) return false;
         tc_fence_after();
         const uint64_t q0 = dplus(dQ, qs * 32768u), k0 = dplus(dK, s * 16384u);
         if (elect_one()) {
@@ -312,7 +401,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           commit2_mc(&c->sfull[b], 3);
         }
         __syncwarp();
-        return true;
       };
       Unit next = unit_of(p, pid);   // loaded a unit ahead
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
@@ -320,12 +408,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
         if (nj <= 0) continue;
         const uint32_t qs = lu & 1u;
-        if (!warp_wait(&c->qfull[qs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
-        if (!scores(g, qs) || (nj > 1 && !scores(g + 1, qs))) { ok = false; break; }
+        if (!fa::warp_wait_f(&c->qfull[qs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
+        if (!wait_k(g)) { ok = false; break; }
+        scores(g, qs);
+        if (nj > 1) {
+          if (!wait_k(g + 1)) { ok = false; break; }
+          scores(g + 1, qs);
+        }
         for (int n = 0; n < nj; ++n, ++g) {
           const uint32_t s = g % KV_STAGES, b = g & 1u;
+          // the operands first: they come long before P does
+          if (!fa::warp_wait_f(&c->vfull[s], g / KV_STAGES, c, p.limit_ns)) { ok = false; break; }
+          if (n + 2 < nj && !wait_k(g + 2)) { ok = false; break; }
           if (!fa::warp_wait_pair(&c->pready_l[b], &c->pready_r[b], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          if (!warp_wait(&c->vfull[s], g / KV_STAGES, c, p.limit_ns)) { ok = false; break; }
           if (n == 0 && !warp_wait(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
           const uint64_t v0 = dplus(dV, s * 16384u);
@@ -337,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             commit2_mc(&c->vempty[s], 3);
           }
           __syncwarp();
-          if (n + 2 < nj && !scores(g + 2, qs)) { ok = false; break; }
+          if (n + 2 < nj) scores(g + 2, qs);
           if ((n + 2 == nj || nj == 1) && elect_one()) commit2_mc(&c->qempty[qs], 3);   // every S of the unit is issued
         }
         if (!ok) break;
@@ -374,7 +469,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const float mul = RAW ? p.sc.sl2 : 1.f;
     uint32_t g = 0, lu = 0;
     bool ok = true;
-    const uint32_t stg = sb + O_STG + (uint32_t)(warp - SOFT_WARP) * 2048u;
     Unit next = unit_of(p, pid);   // the next unit's entry and this thread's row of it
     int nrow, nlo, nhi;
     auto row_ahead = [&]() {
@@ -383,103 +477,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       nhi = nrow < p.T ? p.hi[nrow] : p.T;
     };
     row_ahead();
-    for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
-      const auto [z, qp, j0, nj] = next;
-      const int row = nrow, lo = nlo, hi = nhi;   // the row sees the keys [lo, hi)
-      const bool vrow = row < p.T;
-      const int64_t ro = (int64_t)z * p.T + row;
-      next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
-      const int lo1 = __shfl_sync(0xffffffffu, lo, 31), hi0 = __shfl_sync(0xffffffffu, hi, 0);
-      const pk::ScaleZ sc = pk::scale_z(p.sc, BIAS ? p.slopes[z] : 0.f);
-      // FIXED: the bias of the farthest key where the bias rises with the distance, else 0
-      float m = FIXED ? (BIAS ? fmaxf(0.f, -sc.slope2 * (float)max(row - lo, hi - 1 - row)) : 0.f) : -INFINITY;
-      const float top = sc.c2 - (FIXED ? m : 0.f);
-      float2 l2 = make_float2(0.f, 0.f);
-      for (int n = (int)((g ^ (uint32_t)grp) & 1u); n < nj; n += 2) {   // this group's blocks
-        if (!warp_wait(&c->sfull[grp], (g + n) >> 1, c, p.limit_ns)) { ok = false; break; }
-        tc_fence_after();
-        __syncwarp();
-        const int k0 = 128 * (j0 + n);
-        const bool mask = k0 < lo1 || k0 + 127 >= hi0;   // some row of the warp does not see all keys
-        const Row w{lo - k0, hi - k0, (float)(row - k0), top};
-        uint32_t ra[32], rb[32], pw[32];
-        if (!FIXED) {
-          tmem_ld32(tS + 64, ra);
-          tmem_ld32(tS + 96, rb);
-          tmem_ld_wait();
-          scores32<CAP, BIAS>(ra, 64, mask, w, sc);
-          scores32<CAP, BIAS>(rb, 96, mask, w, sc);
-          float mb = max32(rb, max32(ra, -INFINITY));
-          tmem_ld32(tS, ra);
-          tmem_ld32(tS + 32, rb);
-          tmem_ld_wait();
-          scores32<CAP, BIAS>(ra, 0, mask, w, sc);
-          scores32<CAP, BIAS>(rb, 32, mask, w, sc);
-          mb = max32(rb, max32(ra, mb));
-          float f = 1.f;
-          if (mb > m && (m == -INFINITY || (mb - m) * mul > 8.f)) {
-            f = ex2((m - mb) * mul);   // 0 from m = -inf
-            m = mb;
-          }
-          l2.x *= f;
-          l2.y *= f;
-          if (n > 1 && __any_sync(0xffffffffu, f != 1.f)) {   // the group's O so far
-#pragma unroll 1
-            for (int h = 0; h < 128; h += 16) {
-              uint32_t o[16];
-              fa::tmem_ld16(tO + h, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              fa::tmem_st16(tO + h, o);
-            }
-          }
-        } else {
-          tmem_ld32(tS, ra);
-          tmem_ld32(tS + 32, rb);
-          tmem_ld_wait();
-          scores32<CAP, BIAS>(ra, 0, mask, w, sc);
-          scores32<CAP, BIAS>(rb, 32, mask, w, sc);
-        }
-        __syncwarp();
-        const float nm = m == -INFINITY ? 0.f : -m * mul;
-        probs32<FIXED>(ra, mul, nm, pw, l2);
-        tmem_ld32(tS + 64, ra);
-        probs32<FIXED>(rb, mul, nm, pw + 16, l2);
-        tmem_ld32(tS + 96, rb);
-        tmem_st32(tS, pw);          // keys 0 .. 63: over scores that are in registers
-        tmem_ld_wait();
-        scores32<CAP, BIAS>(ra, 64, mask, w, sc);
-        scores32<CAP, BIAS>(rb, 96, mask, w, sc);
-        probs32<FIXED>(ra, mul, nm, pw, l2);
-        probs32<FIXED>(rb, mul, nm, pw + 16, l2);
-        __syncwarp();
-        tmem_st32(tS + 32, pw);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->pready_l[grp]);
-      }
-      if (!ok) break;
-      if (nj <= 0) {   // rows of padding alone
-        if (vrow) {
-          if (grp == 0) p.lse[ro] = -INFINITY;
-          uint4* dst = reinterpret_cast<uint4*>(p.O + ro * p.hd + 64 * grp);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (64 * grp + 8 * k < p.hd) dst[k] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        row_ahead();
-        continue;
-      }
-      g += (uint32_t)nj;
-      // join the groups: m and l of the row's other group, then 64 columns of both accumulators
-      float2* ml = reinterpret_cast<float2*>(base + O_ML) + (lu & 1u) * 256;
-      ml[grp * 128 + lrow] = make_float2(m, l2.x + l2.y);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->mlx);
-      row_ahead();
-      if (!warp_wait(&c->mlx, lu, c, p.limit_ns) || !warp_wait(&c->ofull, lu, c, p.limit_ns)) { ok = false; break; }
+    // The end of a unit waits until the group's first block of the next one is done: its products
+    // then run meanwhile.  It joins the groups: m and l of the row's other group, then 64 columns
+    // of both accumulators.
+    uint32_t done = 0, left = 0;   // units joined; units whose O has left its staging block
+    int zf = 0, rowf = 0;          // the unit's head, this thread's row
+    auto finish = [&]() -> bool {
+      if (done == lu) return true;
+      const float2* ml = reinterpret_cast<const float2*>(base + O_ML) + (done & 1u) * 256;
+      if (!warp_wait(&c->mlx, done, c, p.limit_ns) || !warp_wait(&c->ofull, done, c, p.limit_ns)) return false;
       tc_fence_after();
       __syncwarp();
       const float2 s0 = ml[lrow], s1 = ml[128 + lrow];
@@ -489,23 +495,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const bool none = l == 0.f;   // a row that sees nothing (padding): 0 and -inf
       const float inv = none ? 0.f : 1.f / l;
       const float a0 = f0 * inv, a1 = f1 * inv;
-      if (vrow && grp == 0) p.lse[ro] = none ? -INFINITY : (mm * mul + log2f(l)) * 0.6931471805599453f;
-#pragma unroll 1
+      if (rowf < p.T && grp == 0) p.lse[(int64_t)zf * p.T + rowf] = none ? -INFINITY : (mm * mul + log2f(l)) * 0.6931471805599453f;
+      // O leaves through the space of the unit's Q, which no product reads any more: two blocks
+      // of 32 x 32 a warp
+      const uint32_t stg = sb + O_Q + (done & 1u) * 32768u + (uint32_t)(warp - SOFT_WARP) * 4096u;
+#pragma unroll
       for (int h = 0; h < 64; h += 32) {
-        uint32_t ra[32], rb[32];
+        uint32_t ra[32], rb[32], v[16];
         __syncwarp();
         tmem_ld32(trow + T_O + 64 * grp + h, ra);
         tmem_ld32(trow + T_O + 128 + 64 * grp + h, rb);
         tmem_ld_wait();
-        if (h == 32) {   // both accumulators are in registers: the next unit may overwrite them
+        if (h == 32) {   // both accumulators have been read: the next unit may overwrite them
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_remote(mapa(saddr(&c->accempty), 0));
         }
-        // through this warp's staging block: whole rows, clipped to the tensor
-        if (lane == 0) bulk_wait_read();   // the block's previous contents have left
-        __syncwarp();
-        uint32_t v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           // a group without a block for the row leaves its accumulator unset: selected out
@@ -517,16 +522,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          sts128(stg + 64u * lane + 16u * k, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        fence_proxy_async();
-        __syncwarp();
-        const int row0 = row - lane, col = 64 * grp + h;
-        if (lane == 0 && row0 < p.T && col < p.hd) {
-          tma_store_3d(&tmO, stg, col, row0, z);
-          bulk_commit();
-        }
+          sts128(stg + 64u * h + 64u * lane + 16u * k, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
       }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0 && rowf < p.T) {
+        const int col = 64 * grp;
+        if (col < p.hd) tma_store_3d(&tmO, stg, col, rowf, zf);
+        if (col + 32 < p.hd) tma_store_3d(&tmO, stg + 2048, col + 32, rowf, zf);
+        bulk_commit();
+      }
+      ++done;
+      return true;
+    };
+    auto release = [&]() {   // the Q buffer, once its O has left
+      if (left == done) return;
+      if (lane == 0) {
+        bulk_wait_read();
+        mbar_arrive(&c->qempty[left & 1u]);
+      }
+      ++left;
+    };
+    for (int rnd = 0, u = pid; ok; u = pk::next_unit(++rnd, pid, npairs)) {
+      const bool end = u >= p.n_units;   // a last round joins the last unit
+      const auto [z, qp, j0, nj] = next;
+      const int row = nrow, lo = nlo, hi = nhi;   // the row sees the keys [lo, hi)
+      const bool vrow = row < p.T;
+      next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
+      const int lo1 = __shfl_sync(0xffffffffu, lo, 31), hi0 = __shfl_sync(0xffffffffu, hi, 0);
+      const pk::ScaleZ sc = pk::scale_z(p.sc, BIAS ? p.slopes[z] : 0.f);
+      // FIXED: the bias of the farthest key where the bias rises with the distance, else 0
+      float m = FIXED ? (BIAS ? fmaxf(0.f, -sc.slope2 * (float)max(row - lo, hi - 1 - row)) : 0.f) : -INFINITY;
+      const float top = sc.c2 - (FIXED ? m : 0.f);
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int n = (int)((g ^ (uint32_t)grp) & 1u);; n += 2) {   // this group's blocks
+        if (n < nj) {
+          if (!warp_wait(&c->sfull[grp], (g + n) >> 1, c, p.limit_ns)) { ok = false; break; }
+          tc_fence_after();
+          __syncwarp();
+          const int k0 = 128 * (j0 + n);
+          const Row w{lo - k0, hi - k0, lo1 - k0, hi0 - k0, row - lane - k0, (float)(row - k0), top};
+          if (w.edge<BIAS>()) soft_block<CAP, BIAS, FIXED, true>(tS, tO, n < 2, w, sc, mul, m, l2);
+          else soft_block<CAP, BIAS, FIXED, false>(tS, tO, n < 2, w, sc, mul, m, l2);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->pready_l[grp]);
+        }
+        release();
+        if (!finish()) { ok = false; break; }
+        if (n + 2 >= nj) break;
+      }
+      if (!ok || end) break;
+      release();
+      if (nj <= 0) {   // rows of padding alone
+        if (vrow) {
+          const int64_t ro = (int64_t)z * p.T + row;
+          if (grp == 0) p.lse[ro] = -INFINITY;
+          uint4* dst = reinterpret_cast<uint4*>(p.O + ro * p.hd + 64 * grp);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (64 * grp + 8 * k < p.hd) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        row_ahead();
+        continue;
+      }
+      g += (uint32_t)nj;
+      float2* ml = reinterpret_cast<float2*>(base + O_ML) + (lu & 1u) * 256;
+      ml[grp * 128 + lrow] = make_float2(m, l2.x + l2.y);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->mlx);
       ++lu;
+      zf = z;
+      rowf = row;
+      row_ahead();
     }
     if (!ok) fail_o(c, p.status);
     if (lane == 0) bulk_wait_all();

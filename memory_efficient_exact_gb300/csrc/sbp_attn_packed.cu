@@ -116,11 +116,12 @@ struct PackedScores {
   static __device__ __forceinline__ Scale scale_of(const P& p, int z) {
     return scale_z(p.sc, BIAS ? p.slopes[z] : 0.f);
   }
+  template <bool MASK>
   static __device__ __forceinline__ float2 log2p2(const Scale& sc, float2 s, float2 nlz, float d, float o0, float o1,
                                                   float2& dc) {
     float2 x;
     if (CAP) {
-      x = make_float2(capped(sc, s.x, sc.c2), capped(sc, s.y, sc.c2));
+      x = fma2(cap_parts<MASK>(sc, s), make_float2(-2.f * sc.c2, -2.f * sc.c2), make_float2(sc.c2, sc.c2));
       const float2 th = mul2(x, make_float2(sc.ic2, sc.ic2));
       dc = fma2(make_float2(-th.x, -th.y), th, make_float2(1.f, 1.f));   // 1 - tanh^2
       x = add2(x, nlz);
@@ -411,9 +412,9 @@ bool packed_supported(int64_t H, int64_t T, int64_t hd) {
 // Query heads of a group that one k_attn_kv unit walks: all of them where that leaves two units
 // or more for each SM pair (a key's dK and dV are then summed on chip), else as few as give four,
 // the sums joined by k_packed_join.  The backward with and without (H / Hkv x tokens, hd 128):
-// 16/1 x 128 36 and 55 us, 32/8 x 256 36 and 42, 32/8 x 1024 68 and 92, 20/4 x 4099 265 and
-// 350; the other way at two units a pair, 32/8 x 8192 in documents, 492 and 480 (the join reads
-// and writes the sums again).
+// 16/1 x 128 36 and 55 us, 32/8 x 256 36 and 42, 32/8 x 1024 68 and 92; 20/4 x 4099 in
+// two parts 281, in five 271; the other way from two units a pair on, 32/8 x 8192 in documents,
+// 492 and 480 (the join reads and writes the sums again).
 int kv_heads_per_part(int64_t H, int64_t Hkv, int64_t T) {
   const int64_t group = H / Hkv, units = std::max<int64_t>(1, (T + 255) / 256 * Hkv), pairs = std::max(1, num_sms() / 2);
   if (units >= 2 * pairs) return (int)group;

@@ -74,11 +74,31 @@ __device__ __forceinline__ ScaleZ scale_z(const Scale& s, float slope) {
   return z;
 }
 
-// The capped score in log2 units, `top` for the largest.
-__device__ __forceinline__ float capped(const Scale& sc, float s, float top) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(s * sc.k)));
-  return fmaf(-2.f * sc.c2, r, top);
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float rcp(float a) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(a));
+  return d;
+}
+
+// r = 1 / (1 + 2^(k s)) of two raw scores, tanh being 1 - 2 r.  The special-function unit bounds
+// capped scores, so the two share a reciprocal: 1 / a = b / (a b), with a and b below 2^60 (r is
+// under half a step of fp32 from 0 there).  A NaN then reaches both: the two belong to one row of
+// every sum they enter, but where one of them may be masked (MASK) each has its own.
+template <bool MASK>
+__device__ __forceinline__ float2 cap_parts(const Scale& sc, float2 s) {
+  const float2 t = mul2(s, make_float2(sc.k, sc.k));
+  if (MASK) {
+    const float2 e = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+    return make_float2(rcp(e.x), rcp(e.y));
+  }
+  const float2 e = add2(make_float2(ex2(min_nan(t.x, 60.f)), ex2(min_nan(t.y, 60.f))), make_float2(1.f, 1.f));
+  const float q = rcp(e.x * e.y);
+  return make_float2(e.y * q, e.x * q);
 }
 
 inline Scale make_scale(float scale, float softcap) {
