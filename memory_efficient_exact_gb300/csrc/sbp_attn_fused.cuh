@@ -208,10 +208,35 @@ template <class C>
 __device__ __forceinline__ bool warp_wait_c(uint64_t* b, uint32_t parity, C* c, uint64_t limit) {
   return __all_sync(0xffffffffu, wait_c(b, parity, c, limit));
 }
-// The leader's wait for both CTAs' epilogue warps: its own barrier and the forwarded one.
-template <class C>
-__device__ __forceinline__ bool warp_wait_pair(uint64_t* local, uint64_t* remote, uint32_t parity, C* c, uint64_t limit) {
-  return __all_sync(0xffffffffu, wait_inl<false>(local, parity & 1u, &c->abort, limit) && wait_c(remote, parity, c, limit));
+// Several phases at once: a wait costs the MMA warp some 150 cycles even when its phase has
+// completed, and with one wait for each operand that warp, not the tensor pipe, set the pace.
+// The tests go out together; only what is not there yet is waited for.
+template <bool CLUSTER>
+struct Phase {
+  uint64_t* b;
+  uint32_t parity;
+  bool need;   // false: passes
+  __device__ __forceinline__ bool test() const {
+    return !need || (CLUSTER ? mbar_test<true>(b, parity & 1u) : mbar_test<false>(b, parity & 1u));
+  }
+  __device__ __forceinline__ bool wait(const volatile int* abort_flag, uint64_t limit) const {
+    return wait_inl<CLUSTER>(b, parity & 1u, abort_flag, limit);
+  }
+};
+// (see warp_wait_f and warp_wait_c)
+__device__ __forceinline__ Phase<false> phase_f(uint64_t* b, uint32_t parity, bool need = true) { return {b, parity, need}; }
+__device__ __forceinline__ Phase<true> phase_c(uint64_t* b, uint32_t parity, bool need = true) { return {b, parity, need}; }
+template <class C, class... P>
+__device__ __forceinline__ bool warp_wait_all(C* c, uint64_t limit, const P&... ph) {
+  bool there[] = {ph.test()...};
+  int i = 0;
+  bool all = true;
+  ((all = all && there[i++], (void)ph), ...);
+  if (__all_sync(0xffffffffu, all)) return true;
+  i = 0;
+  bool ok = true;
+  ((ok = ok && (there[i++] || ph.wait(&c->abort, limit))), ...);
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
@@ -629,43 +654,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       bool ok = true;
       // S^T (dP^T) of block gg into its one buffer: free, since the product that read the P^T
       // (dS^T) of the block before in it was issued before
-      auto scores = [&](uint32_t gg) -> bool {
+      auto scores = [&](uint32_t gg) {   // by the elected lane
         const uint32_t s = gg & 1u;
-        if (!warp_wait_f(&c->qfull[s], gg >> 1, c, p.limit_ns)) return false;
-        tc_fence_after();
         const uint64_t q0 = dplus(dAQ, s * 16384u);
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (k == 4 && !wide) break;
-            mma2_bf16(tmem, dplus(dK, (k >> 2) * 16384 + (k & 3) * 32), dplus(q0, (k >> 2) * 8192 + (k & 3) * 32),
+        for (int k = 0; k < 8; ++k) {
+          if (k == 4 && !wide) break;
+          mma2_bf16(tmem, dplus(dK, (k >> 2) * 16384 + (k & 3) * 32), dplus(q0, (k >> 2) * 8192 + (k & 3) * 32),
                     IDESC_KK, k ? 1u : 0u);
-          }
-          commit2_mc(&c->qempty[s], 3);
-          commit2_mc(&c->sfull, 3);
         }
-        __syncwarp();
-        return true;
+        commit2_mc(&c->qempty[s], 3);
+        commit2_mc(&c->sfull, 3);
       };
-      auto grads = [&](uint32_t gg, bool last) -> bool {
+      auto grads = [&](uint32_t gg, bool last) {
         const uint32_t s = gg & 1u;
-        if (!warp_wait_f(&c->ofull[s], gg >> 1, c, p.limit_ns)) return false;
-        tc_fence_after();
         const uint64_t o0 = dplus(dAO, s * 16384u);
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (k == 4 && !wide) break;
-            mma2_bf16(tmem + KT_DP, dplus(dV, (k >> 2) * 16384 + (k & 3) * 32),
+        for (int k = 0; k < 8; ++k) {
+          if (k == 4 && !wide) break;
+          mma2_bf16(tmem + KT_DP, dplus(dV, (k >> 2) * 16384 + (k & 3) * 32),
                     dplus(o0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
-          }
-          commit2_mc(&c->oempty[s], 3);
-          commit2_mc(&c->dpfull, 3);
-          if (last) commit2_mc(&c->rempty, 3);
         }
-        __syncwarp();
-        return true;
+        commit2_mc(&c->oempty[s], 3);
+        commit2_mc(&c->dpfull, 3);
+        if (last) commit2_mc(&c->rempty, 3);
       };
+      auto q_of = [&](uint32_t gg, bool need) { return phase_f(&c->qfull[gg & 1u], gg >> 1, need); };
+      auto o_of = [&](uint32_t gg, bool need) { return phase_f(&c->ofull[gg & 1u], gg >> 1, need); };
       typename S::Raw raw = S::kv_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         KvUnit w;
@@ -673,13 +688,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         raw = S::kv_raw(p, S::next_unit(rnd + 1, pid, npairs));
         const int nblk = w.nh * w.nbl;
         if (nblk == 0) continue;
-        if (!warp_wait_f(&c->rfull, lu, c, p.limit_ns)) { ok = false; break; }
-        if (!scores(g) || !grads(g, nblk == 1)) { ok = false; break; }
+        if (!warp_wait_all(c, p.limit_ns, phase_f(&c->rfull, lu), q_of(g, true))) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) scores(g);
+        __syncwarp();
+        if (!warp_wait_all(c, p.limit_ns, o_of(g, true))) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) grads(g, nblk == 1);
+        __syncwarp();
         for (int n = 0; n < nblk; ++n, ++g) {
-          // dV += P^T dO (the unit's first overwrites)
-          if (!warp_wait_pair(&c->pready_l, &c->pready_r, g, c, p.limit_ns)) { ok = false; break; }
-          if (!warp_wait_f(&c->bofull, g, c, p.limit_ns)) { ok = false; break; }
-          if (n == 0 && !warp_wait_c(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
+          const bool more = n + 1 < nblk;
+          // dV += P^T dO (the unit's first overwrites), then the next block's S^T
+          if (!warp_wait_all(c, p.limit_ns, phase_f(&c->pready_l, g), phase_c(&c->pready_r, g), phase_f(&c->bofull, g),
+                             q_of(g + 1, more), phase_c(&c->accempty, lu ^ 1u, n == 0))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           if (elect_one()) {
             // P^T: 16 columns at the start of each epilogue warp's 32
@@ -688,12 +712,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
               mma2_bf16_ts(tmem + KT_DV, tmem + 32 * (k >> 1) + 8 * (k & 1), dplus(dBO, k * 2048), IDESC_KM,
                            (n || k) ? 1u : 0u);
             commit2_mc(&c->boempty, 3);
+            if (more) scores(g + 1);
           }
           __syncwarp();
-          if (n + 1 < nblk && !scores(g + 1)) { ok = false; break; }
-          // dK += dS^T Q
-          if (!warp_wait_pair(&c->dsready_l, &c->dsready_r, g, c, p.limit_ns)) { ok = false; break; }
-          if (!warp_wait_f(&c->bqfull, g, c, p.limit_ns)) { ok = false; break; }
+          // dK += dS^T Q, then the next block's dP^T
+          if (!warp_wait_all(c, p.limit_ns, phase_f(&c->dsready_l, g), phase_c(&c->dsready_r, g), phase_f(&c->bqfull, g),
+                             o_of(g + 1, more))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -701,10 +728,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
               mma2_bf16_ts(tmem + KT_DK, tmem + KT_DP + 32 * (k >> 1) + 8 * (k & 1), dplus(dBQ, k * 2048), IDESC_KM,
                            (n || k) ? 1u : 0u);
             commit2_mc(&c->bqempty, 3);
-            if (n == nblk - 1) commit2_mc(&c->accfull, 3);
+            if (more) grads(g + 1, n + 2 == nblk);
+            else commit2_mc(&c->accfull, 3);
           }
           __syncwarp();
-          if (n + 1 < nblk && !grads(g + 1, n + 2 == nblk)) { ok = false; break; }
         }
         if (!ok) break;
         ++lu;
@@ -1040,43 +1067,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       bool ok = true;
       // S of block gg into its buffer: free, since the dQ product that read the dS in it was
       // issued before
-      auto scores = [&](uint32_t gg, uint64_t q0) -> bool {
+      auto scores = [&](uint32_t gg, uint64_t q0) {   // by the elected lane
         const uint32_t s = gg & 1u;
-        if (!warp_wait_f(&c->kfull[s], gg >> 1, c, p.limit_ns)) return false;
-        tc_fence_after();
         const uint64_t k0 = dplus(dK, s * 16384u);
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (k == 4 && !wide) break;
-            mma2_bf16(tmem + 128 * s, dplus(q0, (k >> 2) * 16384 + (k & 3) * 32),
+        for (int k = 0; k < 8; ++k) {
+          if (k == 4 && !wide) break;
+          mma2_bf16(tmem + 128 * s, dplus(q0, (k >> 2) * 16384 + (k & 3) * 32),
                     dplus(k0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
-          }
-          commit2_mc(&c->kempty[s], 3);
         }
-        __syncwarp();
-        return true;
+        commit2_mc(&c->kempty[s], 3);
       };
       // dP of block gg, once the previous block's has been read; completes the block's S too
-      auto grads = [&](uint32_t gg, uint64_t o0) -> bool {
+      auto grads = [&](uint32_t gg, uint64_t o0) {
         const uint32_t s = gg & 1u;
-        if (!warp_wait_pair(&c->tempty_l, &c->tempty_r, gg ^ 1u, c, p.limit_ns)) return false;
-        if (!warp_wait_f(&c->vfull[s], gg >> 1, c, p.limit_ns)) return false;
-        tc_fence_after();
         const uint64_t v0 = dplus(dV, s * 16384u);
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (k == 4 && !wide) break;
-            mma2_bf16(tmem + QT_DP, dplus(o0, (k >> 2) * 16384 + (k & 3) * 32),
+        for (int k = 0; k < 8; ++k) {
+          if (k == 4 && !wide) break;
+          mma2_bf16(tmem + QT_DP, dplus(o0, (k >> 2) * 16384 + (k & 3) * 32),
                     dplus(v0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
-          }
-          commit2_mc(&c->vempty[s], 3);
-          commit2_mc(&c->tfull, 3);
         }
-        __syncwarp();
-        return true;
+        commit2_mc(&c->vempty[s], 3);
+        commit2_mc(&c->tfull, 3);
       };
+      auto k_of = [&](uint32_t gg, bool need) { return phase_f(&c->kfull[gg & 1u], gg >> 1, need); };
+      auto v_of = [&](uint32_t gg) { return phase_f(&c->vfull[gg & 1u], gg >> 1); };
       typename S::Raw raw = S::q_raw(p, pid);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
@@ -1084,19 +1100,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
         if (nj == 0) continue;
         const uint32_t rs = lu & 1u;
-        if (!warp_wait_f(&c->rfull[rs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
         const uint64_t q0 = dplus(dR, rs * 65536u), o0 = dplus(q0, 32768);
         // the tensor pipe always has the next block's S and dP to form while the epilogue
         // works on a block: S two blocks ahead, dP one
-        if (!scores(g, q0) || !grads(g, o0) || (nj > 1 && !scores(g + 1, q0))) { ok = false; break; }
+        if (!warp_wait_all(c, p.limit_ns, phase_f(&c->rfull[rs], lu >> 1), k_of(g, true), v_of(g),
+                           phase_f(&c->tempty_l, g ^ 1u), phase_c(&c->tempty_r, g ^ 1u), k_of(g + 1, nj > 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          scores(g, q0);
+          grads(g, o0);
+          if (nj > 1) scores(g + 1, q0);
+        }
+        __syncwarp();
         for (int n = 0; n < nj; ++n, ++g) {
           const uint32_t s = g & 1u;
-          if (n + 1 < nj && !grads(g + 1, o0)) { ok = false; break; }
-          if (n == max(nj - 2, 0) && elect_one()) commit2_mc(&c->rempty[rs], 3);   // the unit's last S, dP are issued
+          if (n + 1 < nj) {
+            if (!warp_wait_all(c, p.limit_ns, phase_f(&c->tempty_l, g), phase_c(&c->tempty_r, g), v_of(g + 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (elect_one()) {
+            if (n + 1 < nj) grads(g + 1, o0);
+            if (n == max(nj - 2, 0)) commit2_mc(&c->rempty[rs], 3);   // the unit's last S, dP are issued
+          }
           __syncwarp();
-          if (!warp_wait_pair(&c->oready_l[s], &c->oready_r[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          if (!warp_wait_f(&c->yfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          if (n == 0 && !warp_wait_c(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
+          const bool more = n + 2 < nj;
+          if (!warp_wait_all(c, p.limit_ns, phase_f(&c->oready_l[s], g >> 1), phase_c(&c->oready_r[s], g >> 1),
+                             phase_f(&c->yfull[s], g >> 1), k_of(g + 2, more), phase_c(&c->accempty, lu ^ 1u, n == 0))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint64_t y0 = dplus(dY, s * 16384u);
           if (elect_one()) {
@@ -1107,9 +1145,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
                            (n || k) ? 1u : 0u);
             commit2_mc(&c->yempty[s], 3);
             if (n == nj - 1) commit2_mc(&c->dqfull, 3);
+            if (more) scores(g + 2, q0);
           }
           __syncwarp();
-          if (n + 2 < nj && !scores(g + 2, q0)) { ok = false; break; }
         }
         if (!ok) break;
         ++lu;

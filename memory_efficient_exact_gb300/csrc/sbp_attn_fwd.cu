@@ -82,6 +82,11 @@ struct Params {
   uint64_t limit_ns;
 };
 
+// Block n of a unit: behind to front with a distance bias, so that the maximum is found early (its
+// slopes are positive as a rule).
+template <bool BIAS>
+__device__ __forceinline__ int block_at(int j0, int nj, int n) { return BIAS ? j0 + nj - 1 - n : j0 + n; }
+
 // Unit u: head z, queries [256 qp, +256), key blocks [j0, j0 + nj); none past the last.
 struct Unit { int z, qp, j0, nj; };
 __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
@@ -197,6 +202,8 @@ __device__ __forceinline__ void soft_block(uint32_t tS, uint32_t tO, bool fresh,
   float2 lb;   // the block's sums
   // whether the maximum has to be found before the exponentials
   bool raise = !FIXED && __any_sync(0xffffffffu, m == -INFINITY && w.a < 128 && w.b > 0);
+  if (BIAS && !FIXED)   // and whether the bias alone lifts it there from the group's block before
+    raise = raise || (fabsf(sc.slope2) * 256.f > kLag && (sc.slope2 > 0.f ? w.first < 127 : w.first > -31));
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (raise) {
@@ -330,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (!wait1(&c->kempty[s], (g / KV_STAGES) ^ 1u, c, p.limit_ns)) { ok = false; break; }
           const uint32_t fk = mapa(saddr(&c->kfull[s]), 0);
           if (rank == 0) mbar_expect_tx(&c->kfull[s], 2u * 16384u);
-          const int krow = 128 * (j0 + j) + 64 * (int)rank;
+          const int krow = 128 * block_at<BIAS>(j0, nj, j) + 64 * (int)rank;
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb)
             tma_load_3d_pair(sb + O_K + s * 16384u + hb * 8192, &tmK, fk, 64 * hb, krow, z / p.group);
@@ -361,10 +368,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (!wait1(&c->vempty[s], (g / KV_STAGES) ^ 1u, c, p.limit_ns)) { ok = false; break; }
           const uint32_t fv = mapa(saddr(&c->vfull[s]), 0);
           if (rank == 0) mbar_expect_tx(&c->vfull[s], 2u * 16384u);
-          if (j0 + j == tail)
+          const int blk = block_at<BIAS>(j0, nj, j);
+          if (blk == tail)
             tma_load_3d_pair(sb + O_V + s * 16384u, &tmVt, fv, 64 * (int)rank, 0, z / p.group);
           else
-            tma_load_3d_pair(sb + O_V + s * 16384u, &tmV, fv, 64 * (int)rank, 128 * (j0 + j), z / p.group);
+            tma_load_3d_pair(sb + O_V + s * 16384u, &tmV, fv, 64 * (int)rank, 128 * blk, z / p.group);
           ++g;
         }
       }
@@ -383,24 +391,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       // S of block gg into its group's buffer: free, since the product that read the P in it
       // was issued before
-      auto wait_k = [&](uint32_t gg) { return fa::warp_wait_f(&c->kfull[gg % KV_STAGES], gg / KV_STAGES, c, p.limit_ns); };
-      auto scores = [&](uint32_t gg, uint32_t qs) {
+      auto k_of = [&](uint32_t gg, bool need) {
+        return fa::phase_f(&c->kfull[gg % KV_STAGES], gg / KV_STAGES, need);
+      };
+      auto scores = [&](uint32_t gg, uint32_t qs) {   // by the elected lane
         const uint32_t s = gg % KV_STAGES, b = gg & 1u;
-        tc_fence_after();
         const uint64_t q0 = dplus(dQ, qs * 32768u), k0 = dplus(dK, s * 16384u);
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma2_bf16(tmem + 128 * b, dplus(q0, k * 32), dplus(k0, k * 32), IDESC_KK, k ? 1u : 0u);
-          if (p.hd > 64) {   // the second 64 columns of a row (zero past hd)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma2_bf16(tmem + 128 * b, dplus(q0, 16384 + k * 32), dplus(k0, 8192 + k * 32), IDESC_KK, 1u);
-          }
-          commit2_mc(&c->kempty[s], 3);
-          commit2_mc(&c->sfull[b], 3);
+        for (int k = 0; k < 8; ++k) {
+          if (k == 4 && p.hd <= 64) break;   // the other columns of a row are zero
+          mma2_bf16(tmem + 128 * b, dplus(q0, (k >> 2) * 16384 + (k & 3) * 32),
+                    dplus(k0, (k >> 2) * 8192 + (k & 3) * 32), IDESC_KK, k ? 1u : 0u);
         }
-        __syncwarp();
+        commit2_mc(&c->kempty[s], 3);
+        commit2_mc(&c->sfull[b], 3);
       };
       Unit next = unit_of(p, pid);   // loaded a unit ahead
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
@@ -408,20 +412,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
         if (nj <= 0) continue;
         const uint32_t qs = lu & 1u;
-        if (!fa::warp_wait_f(&c->qfull[qs], lu >> 1, c, p.limit_ns)) { ok = false; break; }
-        if (!wait_k(g)) { ok = false; break; }
-        scores(g, qs);
-        if (nj > 1) {
-          if (!wait_k(g + 1)) { ok = false; break; }
-          scores(g + 1, qs);
+        if (!fa::warp_wait_all(c, p.limit_ns, fa::phase_f(&c->qfull[qs], lu >> 1), k_of(g, true), k_of(g + 1, nj > 1))) {
+          ok = false;
+          break;
         }
+        tc_fence_after();
+        if (elect_one()) {
+          scores(g, qs);
+          if (nj > 1) scores(g + 1, qs);
+        }
+        __syncwarp();
         for (int n = 0; n < nj; ++n, ++g) {
           const uint32_t s = g % KV_STAGES, b = g & 1u;
-          // the operands first: they come long before P does
-          if (!fa::warp_wait_f(&c->vfull[s], g / KV_STAGES, c, p.limit_ns)) { ok = false; break; }
-          if (n + 2 < nj && !wait_k(g + 2)) { ok = false; break; }
-          if (!fa::warp_wait_pair(&c->pready_l[b], &c->pready_r[b], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          if (n == 0 && !warp_wait(&c->accempty, lu ^ 1u, c, p.limit_ns)) { ok = false; break; }
+          const bool more = n + 2 < nj;
+          if (!fa::warp_wait_all(c, p.limit_ns, fa::phase_f(&c->pready_l[b], g >> 1), fa::phase_c(&c->pready_r[b], g >> 1),
+                                 fa::phase_f(&c->vfull[s], g / KV_STAGES), k_of(g + 2, more),
+                                 fa::phase_c(&c->accempty, lu ^ 1u, n == 0))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint64_t v0 = dplus(dV, s * 16384u);
           if (elect_one()) {
@@ -430,10 +439,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               mma2_bf16_ts(tmem + T_O + 128 * b, tmem + 128 * b + 8 * k, dplus(v0, k * 2048), IDESC_KM,
                            (n > 1 || k) ? 1u : 0u);   // each group's first block overwrites
             commit2_mc(&c->vempty[s], 3);
+            if (more) scores(g + 2, qs);
+            if (n + 2 == nj || nj == 1) commit2_mc(&c->qempty[qs], 3);   // every S of the unit is issued
           }
           __syncwarp();
-          if (n + 2 < nj) scores(g + 2, qs);
-          if ((n + 2 == nj || nj == 1) && elect_one()) commit2_mc(&c->qempty[qs], 3);   // every S of the unit is issued
         }
         if (!ok) break;
         if (elect_one()) commit2_mc(&c->ofull, 3);
@@ -560,7 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (!warp_wait(&c->sfull[grp], (g + n) >> 1, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
           __syncwarp();
-          const int k0 = 128 * (j0 + n);
+          const int k0 = 128 * block_at<BIAS>(j0, nj, n);
           const Row w{lo - k0, hi - k0, lo1 - k0, hi0 - k0, row - lane - k0, (float)(row - k0), top};
           if (w.edge<BIAS>()) soft_block<CAP, BIAS, FIXED, true>(tS, tO, n < 2, w, sc, mul, m, l2);
           else soft_block<CAP, BIAS, FIXED, false>(tS, tO, n < 2, w, sc, mul, m, l2);

@@ -228,6 +228,25 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, const
   if (try_cluster(b, parity)) return true;
   return wait_cluster_slow(b, parity, abort_flag, limit_ns);
 }
+// Whether a phase has completed, without waiting.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  if (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(saddr(b)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(saddr(b)), "r"(parity)
+        : "memory");
+  return ok;
+}
 // The same two waits with the spin loop inlined instead of called: no call-site register
 // saves (the fused attention kernels use these: k_attn_q then needs no local memory, and
 // the pair ran about 1% faster).  A register split between warpgroups (setmaxnreg) also
