@@ -136,8 +136,8 @@ __device__ __forceinline__ void prologue_f(CtrlF* c, int warp) {
     mbar_init(&c->rempty, 1);
     mbar_init(&c->sfull, 1);
     mbar_init(&c->dpfull, 1);
-    mbar_init(&c->pready_r, 1);
-    mbar_init(&c->dsready_r, 1);
+    mbar_init(&c->pready_r, KV_EPI);
+    mbar_init(&c->dsready_r, KV_EPI);
     mbar_init(&c->pready_l, KV_EPI);
     mbar_init(&c->dsready_l, KV_EPI);
     mbar_init(&c->accfull, 1);
@@ -161,11 +161,11 @@ __device__ __forceinline__ void prologue_q(CtrlQ* c, int warp) {
       mbar_init(&c->yempty[i], 1);
       mbar_init(&c->rfull[i], 1);
       mbar_init(&c->rempty[i], 1 + Q_EPI);
-      mbar_init(&c->oready_r[i], 1);
+      mbar_init(&c->oready_r[i], Q_EPI);
       mbar_init(&c->oready_l[i], Q_EPI);
     }
     mbar_init(&c->tfull, 1);
-    mbar_init(&c->tempty_r, 1);
+    mbar_init(&c->tempty_r, Q_EPI);
     mbar_init(&c->tempty_l, Q_EPI);
     mbar_init(&c->dqfull, 1);
     mbar_init(&c->accempty, 2 * Q_EPI);
@@ -208,6 +208,12 @@ template <class C>
 __device__ __forceinline__ bool warp_wait_c(uint64_t* b, uint32_t parity, C* c, uint64_t limit) {
   return __all_sync(0xffffffffu, wait_c(b, parity, c, limit));
 }
+// An epilogue warp's arrival at the leader: on its barrier for its own warps or for the other CTA's.
+__device__ __forceinline__ void arrive_leader(uint32_t rank, uint64_t* local, uint64_t* remote) {
+  if (rank == 0) mbar_arrive(local);
+  else arrive_remote(mapa(saddr(remote), 0));
+}
+
 // Several phases at once: a wait costs the MMA warp some 150 cycles even when its phase has
 // completed, and with one wait for each operand that warp, not the tensor pipe, set the pace.
 // The tests go out together; only what is not there yet is waited for.
@@ -741,23 +747,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         commit2_mc(&c->mdone, 1);
       }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
-    } else if (lane == 0) {   // forwarder
-      uint32_t g = 0;
-      bool ok = true;
-      typename S::Raw raw = S::kv_raw(p, pid);
-      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
-        KvUnit w;
-        S::kv_unit(p, u, raw, w);
-        raw = S::kv_raw(p, S::next_unit(rnd + 1, pid, npairs));
-        const int nblk = w.nh * w.nbl;
-        for (int n = 0; n < nblk; ++n, ++g) {
-          if (!wait_c(&c->pready_l, g, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->pready_r), 0));
-          if (!wait_c(&c->dsready_l, g, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->dsready_r), 0));
-        }
-      }
-      if (!ok) fail_f(c, p.status);
     }
     __syncwarp();
   } else if (warp == KV_LD_WARP) {
@@ -854,7 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&c->pready_l);
+          arrive_leader(rank, &c->pready_l, &c->pready_r);
           mbar_arrive(&c->lempty[s]);
         }
         if (!warp_wait_c(&c->dpfull, g, c, p.limit_ns) || !warp_wait_f(&c->dfull, g, c, p.limit_ns)) { ok = false; break; }
@@ -881,7 +870,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&c->dsready_l);
+          arrive_leader(rank, &c->dsready_l, &c->dsready_r);
           mbar_arrive(&c->dempty);
         }
         if (kv_next(w, z, b) && n + 1 < nblk) sc = S::scale_of(p, z);
@@ -1157,22 +1146,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         commit2_mc(&c->mdone, 1);
       }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
-    } else if (lane == 0) {   // forwarder
-      uint32_t g = 0;
-      bool ok = true;
-      typename S::Raw raw = S::q_raw(p, pid);
-      for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
-        int z, qp, j0, nj;
-        S::q_unit(p, u, raw, z, qp, j0, nj);
-        raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
-        for (int j = 0; j < nj; ++j, ++g) {
-          if (!wait_c(&c->tempty_l, g, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->tempty_r), 0));
-          if (!wait_c(&c->oready_l[g & 1u], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->oready_r[g & 1u]), 0));
-        }
-      }
-      if (!ok) fail_f(c, p.status);
     }
     __syncwarp();
   } else {
@@ -1227,7 +1200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->tempty_l);   // dP is in registers: the next block's may be formed
+        if (lane == 0) arrive_leader(rank, &c->tempty_l, &c->tempty_r);   // dP is in registers: the next block's may be formed
         const int kg = 128 * (j0 + j) + 32 * cg;    // first key
         if (kg + 31 < lo0 || kg >= hi1) {
 #pragma unroll
@@ -1242,7 +1215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c->oready_l[g & 1u]);
+        if (lane == 0) arrive_leader(rank, &c->oready_l[g & 1u], &c->oready_r[g & 1u]);
         release();
       }
       if (!ok) break;

@@ -288,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&c->qfull[i], 1);
       mbar_init(&c->qempty[i], 1 + 8);
       mbar_init(&c->sfull[i], 1);
-      mbar_init(&c->pready_r[i], 1);
+      mbar_init(&c->pready_r[i], 4);
       mbar_init(&c->pready_l[i], 4);
     }
     mbar_init(&c->ofull, 1);
@@ -453,19 +453,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         commit2_mc(&c->mdone, 1);
       }
       wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
-    } else if (lane == 0) {   // forwarder
-      uint32_t g = 0;
-      bool ok = true;
-      Unit next = unit_of(p, pid);   // loaded a unit ahead
-      for (int rnd = 0, u = pid; u < p.n_units && ok; u = pk::next_unit(++rnd, pid, npairs)) {
-        const auto [z, qp, j0, nj] = next;
-        next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
-        for (int j = 0; j < nj; ++j, ++g) {
-          if (!wait1(&c->pready_l[g & 1u], g >> 1, c, p.limit_ns)) { ok = false; break; }
-          arrive_remote(mapa(saddr(&c->pready_r[g & 1u]), 0));
-        }
-      }
-      if (!ok) fail_o(c, p.status);
     }
     __syncwarp();
   } else if (warp >= SOFT_WARP) {
@@ -575,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           else soft_block<CAP, BIAS, FIXED, false>(tS, tO, n < 2, w, sc, mul, m, l2);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&c->pready_l[grp]);
+          if (lane == 0) fa::arrive_leader(rank, &c->pready_l[grp], &c->pready_r[grp]);
         }
         release();
         if (!finish()) { ok = false; break; }
