@@ -557,6 +557,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
   const int warp = uniform_warp(), lane = threadIdx.x % 32;
   const uint32_t rank = ctarank();
   prologue_f(c, warp);
+  wait_for_primary();
+  dependents_may_start();
   const uint32_t tmem = c->tmem_base;
   const int pid = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
@@ -1249,6 +1251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     __syncwarp();
     if (!ok) fail_f(c, p.status);
   }
+  wait_for_primary();   // k_attn_kv, of which nothing is read
   teardown_f(c, warp);
 }
 

@@ -308,6 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  wait_for_primary();   // the preparing kernel
   const uint32_t tmem = c->tmem_base;
   const int pid = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
@@ -638,8 +639,7 @@ cudaError_t launch_o(const PackedArgs& a, const PackedWork& w, void* O, float* l
       !tc::make_map_heads(&mVt, w.tail_kv, 128, a.Hkv, a.hd, 128) || !tc::make_map_out(&mO, O, a.T, a.T, a.H, a.hd, 2))
     return cudaErrorInvalidValue;
   const int pairs = std::min(tc::max_pairs((const void*)k_attn_o<CAP, BIAS, FIXED>, SMEM, THREADS), p.n_units);
-  k_attn_o<CAP, BIAS, FIXED><<<2 * pairs, THREADS, SMEM, s>>>(mQ, mK, mV, mVt, mO, p);
-  return cudaGetLastError();
+  return tc::launch_early(k_attn_o<CAP, BIAS, FIXED>, 2 * pairs, THREADS, SMEM, s, mQ, mK, mV, mVt, mO, p);
 }
 
 }  // namespace

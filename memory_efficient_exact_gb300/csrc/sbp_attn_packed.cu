@@ -233,6 +233,7 @@ __device__ __forceinline__ int qlower_of(int t, int s, int pre) { return t < s +
 // interval ends of each token; tail_blocks blocks: the last block's copies; the others: D.
 __global__ void __launch_bounds__(PREP_THREADS) k_packed_prep(const PrepP p) {
   const int tid = threadIdx.x;
+  dependents_may_start();
   if (blockIdx.x == 0) {
     __shared__ int bad;
     if (tid == 0) bad = 0;
@@ -573,20 +574,21 @@ cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedLayout& L, 
   k.dK = static_cast<__nv_bfloat16*>(dK); k.dV = static_cast<__nv_bfloat16*>(dV);
   k.status = a.status; k.limit_ns = tc::wait_limit_ns();
   const int kv_pairs = std::min(tc::max_pairs((const void*)k_attn_kv<S>, SMEM_KV, KV_THREADS), k.n_units);
-  k_attn_kv<S><<<2 * kv_pairs, KV_THREADS, SMEM_KV, s>>>(mk, k);
-  if (L.parts > 1) {
-    const int64_t m = a.Hkv * a.T * a.hd;
-    tc::pk::k_packed_join<<<dim3((unsigned)((m / 8 + 255) / 256), 2), 256, 0, s>>>(k.part_k, k.part_v, L.parts, m, k.dK,
-                                                                                  k.dV);
-  }
-  cudaError_t e = cudaGetLastError();
+  // k_attn_q needs nothing of k_attn_kv's and starts as its pairs of SMs end
+  cudaError_t e = tc::launch_early(k_attn_kv<S>, 2 * kv_pairs, KV_THREADS, SMEM_KV, s, mk, k);
   if (e != cudaSuccess) return e;
   tc::pk::QParams q;
   q.H = k.H; q.T = k.T; q.c0 = 0; q.c1 = k.c1; q.hd = k.hd; q.group = k.group; q.n_units = n * k.H;
   q.scale = k.scale; q.sc = k.sc; q.slopes = k.slopes; q.lse = k.lse; q.D = k.D; q.lo = w.lo; q.hi = w.hi;
   q.units = w.qunits; q.tail = w.tail; q.dQ = static_cast<__nv_bfloat16*>(dQ); q.status = k.status; q.limit_ns = k.limit_ns;
   const int q_pairs = std::min(tc::max_pairs((const void*)k_attn_q<S>, SMEM_Q, Q_THREADS), q.n_units);
-  k_attn_q<S><<<2 * q_pairs, Q_THREADS, SMEM_Q, s>>>(mq, q);
+  e = tc::launch_early(k_attn_q<S>, 2 * q_pairs, Q_THREADS, SMEM_Q, s, mq, q);
+  if (e != cudaSuccess) return e;
+  if (L.parts > 1) {
+    const int64_t m = a.Hkv * a.T * a.hd;
+    tc::pk::k_packed_join<<<dim3((unsigned)((m / 8 + 255) / 256), 2), 256, 0, s>>>(k.part_k, k.part_v, L.parts, m, k.dK,
+                                                                                  k.dV);
+  }
   return cudaGetLastError();
 }
 

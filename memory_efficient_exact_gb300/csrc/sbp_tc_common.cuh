@@ -565,6 +565,27 @@ inline bool make_map_out(CUtensorMap* m, void* ptr, int64_t rows, int64_t T, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may begin while the stream's kernel before it still runs, once all of that one's
+// blocks have called dependents_may_start(): it calls wait_for_primary() before it reads what the
+// other writes, or, where it reads nothing of the kind, before it ends (the kernels behind it then
+// find both complete).
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Failure-detection test hook: SBP_FAULT_STALL=1 makes the next forward kernels stall
 // on purpose (read at every launch, so a test can switch it off again).  Together with a
 // short SBP_WAIT_LIMIT_MS it exercises the bounded-wait abort path: status
