@@ -264,7 +264,8 @@ int sbp_attn_causal_backward_gqa(const void* Q, const void* K, const void* V, co
  * (Within the documents a value that is not finite may reach rows of a neighbouring
  * document, as 0 times infinity.)  The backward takes O and lse of the forward with the
  * same arguments.
- * hd: a multiple of 8, at most 128.  scale > 0 and finite; softcap 0 or in [1e-6, 1e6].  Fixed
+ * hd: a multiple of 8, at most 128.  scale > 0, finite, and scale / softcap too;
+ * softcap 0 or in [1e-6, 256] (the scores' error grows with it, to 2^-14 there).  Fixed
  * order of every sum: the same call gives the same bits.  Workspace, stream and error rules as for
  * the LM-head calls (cu_seqlens and prefix_lens are read by the device only, so a captured
  * call follows their contents: a bad table sets SBP_ERR_SEQLENS); the workspace query
@@ -296,7 +297,7 @@ int sbp_rmsnorm_forward(const void* X, const void* residual, const void* gamma, 
 
 /* The same with Y in 8 bits: Y8 [T, d] e4m3 (one byte each) and scales [T, ceil(d / 128)]
  * fp32, one for each 128 columns of a row: Y ~ Y8 * scale, scale = max|Y| / 448 over the
- * block (1 for a block of zeros).  Half the bytes of a bf16 Y, for the normalised input that
+ * block (1 for a block of zeros; at least 2^-126, so that it has an inverse).  Half the bytes of a bf16 Y, for the normalised input that
  * is kept between a sublayer's forward and its backward; sbp_e4m3_expand gives it back in
  * `dtype` (bf16 for sbp_mlp_swiglu_backward's X). */
 int sbp_rmsnorm_forward_e4m3(const void* X, const void* residual, const void* gamma, int64_t T, int64_t d,

@@ -81,6 +81,7 @@ struct CtrlQ {
   uint64_t tempty_l, oready_l[2]; // dP has been read, dS buffer is written: the CTA's epilogue warps
   uint64_t tempty_r, oready_r[2]; // the same of the other CTA (leader)
   uint64_t dqfull, accempty;      // the unit's dQ is complete; has been read out (leader)
+  uint64_t sums[4];               // the four warps of a lane quadrant have left their rows' sums
   uint64_t mdone;
   uint32_t tmem_base;
   int abort;
@@ -168,6 +169,7 @@ __device__ __forceinline__ void prologue_q(CtrlQ* c, int warp) {
     mbar_init(&c->tempty_r, Q_EPI);
     mbar_init(&c->tempty_l, Q_EPI);
     mbar_init(&c->dqfull, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&c->sums[i], Q_EPI / 4);
     mbar_init(&c->accempty, 2 * Q_EPI);
     mbar_init(&c->mdone, 1);
     c->abort = 0;
@@ -286,6 +288,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -533,6 +541,10 @@ struct CausalScores {
                                                  const KvUnit& w) {
     tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, c, kw, w.zk);
   }
+  // A unit's first block: from -nj on where the blocks are walked twice, the first time for the
+  // rows' sums of P (dP - D) alone.
+  static constexpr bool kSumFirst = false;
+  static __device__ __forceinline__ int q_first(int) { return 0; }
   // Whether the products that sum over hd have columns past 64; hd.
   template <class P>
   static __device__ __forceinline__ bool wide(const P&) { return true; }
@@ -558,7 +570,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
   const uint32_t rank = ctarank();
   prologue_f(c, warp);
   wait_for_primary();
-  dependents_may_start();
   const uint32_t tmem = c->tmem_base;
   const int pid = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
@@ -925,11 +936,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
 
 // k_attn_q's epilogue: 32 keys of this thread's query row.  P = 2^(s S - lse log2 e), dS =
 // P (dP - D), packed to bf16 pairs.  MASK: some row of the warp does not see all 32 keys;
-// the other blocks skip the per-element test.
-template <class S, bool MASK>
+// the other blocks skip the per-element test.  SUM: adds P (dP - D) into `sum` instead.
+template <class S, bool MASK, bool SUM>
 __device__ __forceinline__ void q_block(const uint32_t (&rs)[32], const uint32_t (&rd)[32],
                                         const typename S::Scale& sc, float lz, float Dq, int kg, int qr, int lo, int hi,
-                                        uint32_t (&dw)[16]) {
+                                        uint32_t (&dw)[16], float2& sum) {
   const float2 nD = make_float2(-Dq, -Dq), nlz = make_float2(-lz, -lz);
   const float fd = (float)(qr - kg);
 #pragma unroll
@@ -942,10 +953,12 @@ __device__ __forceinline__ void q_block(const uint32_t (&rs)[32], const uint32_t
     const bool o1 = MASK && (kg + 2 * i + 1 < lo || kg + 2 * i + 1 >= hi);
     if (o0) pp.x = 0.f;
     if (o1) pp.y = 0.f;
-    float2 sv = mul2(S::fold(pp, dc), add2(make_float2(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])), nD));
+    float2 sv = mul2(SUM ? pp : S::fold(pp, dc),
+                     add2(make_float2(__uint_as_float(rd[2 * i]), __uint_as_float(rd[2 * i + 1])), nD));
     if (S::kClearMasked && o0) sv.x = 0.f;
     if (S::kClearMasked && o1) sv.y = 0.f;
-    dw[i] = pack_bf16(sv.x, sv.y);
+    if (SUM) sum = add2(sum, sv);
+    else dw[i] = pack_bf16(sv.x, sv.y);
   }
 }
 
@@ -959,6 +972,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
   const int warp = uniform_warp(), lane = threadIdx.x % 32;
   const uint32_t rank = ctarank();
   prologue_q(c, warp);
+  wait_for_primary();
+  dependents_may_start();
   const uint32_t tmem = c->tmem_base;
   const int pid = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
@@ -988,8 +1003,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
           tma_load_3d_pair(sb + Q_R + rs * 65536u + 32768 + hb * 16384, maps[Q_MO], fr, 64 * hb, qrow, z);
         }
         ++lu;
-        for (int j = 0; j < nj; ++j) {
-          const int krow = 128 * (j0 + j) + 64 * (int)rank;
+        for (int n = S::q_first(nj); n < nj; ++n) {
+          const int krow = 128 * (j0 + (n < 0 ? n + nj : n)) + 64 * (int)rank;
           const uint32_t s = g & 1u, ph = (g >> 1) ^ 1u;
           if (!wait_c(&c->kempty[s], ph, c, p.limit_ns)) { ok = false; break; }
           const uint32_t fk = mapa(saddr(&c->kfull[s]), 0), fv = mapa(saddr(&c->vfull[s]), 0);
@@ -1054,7 +1069,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       const uint64_t dR = sw128_desc(sb + Q_R, 16, 1024), dK = sw128_desc(sb + Q_K, 16, 1024),
                      dV = sw128_desc(sb + Q_V, 16, 1024), dY = sw128_desc(sb + Q_Y, 16384, 1024);
       const bool wide = S::wide(p);
-      uint32_t g = 0, lu = 0;
+      uint32_t g = 0, gy = 0, lu = 0;   // blocks, blocks with a dQ product, units
       bool ok = true;
       // S of block gg into its buffer: free, since the dQ product that read the dS in it was
       // issued before
@@ -1091,11 +1106,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
         if (nj == 0) continue;
         const uint32_t rs = lu & 1u;
+        const int first = S::q_first(nj);
         const uint64_t q0 = dplus(dR, rs * 65536u), o0 = dplus(q0, 32768);
         // the tensor pipe always has the next block's S and dP to form while the epilogue
         // works on a block: S two blocks ahead, dP one
         if (!warp_wait_all(c, p.limit_ns, phase_f(&c->rfull[rs], lu >> 1), k_of(g, true), v_of(g),
-                           phase_f(&c->tempty_l, g ^ 1u), phase_c(&c->tempty_r, g ^ 1u), k_of(g + 1, nj > 1))) {
+                           phase_f(&c->tempty_l, g ^ 1u), phase_c(&c->tempty_r, g ^ 1u), k_of(g + 1, nj - first > 1))) {
           ok = false;
           break;
         }
@@ -1103,10 +1119,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         if (elect_one()) {
           scores(g, q0);
           grads(g, o0);
-          if (nj > 1) scores(g + 1, q0);
+          if (nj - first > 1) scores(g + 1, q0);
         }
         __syncwarp();
-        for (int n = 0; n < nj; ++n, ++g) {
+        for (int n = first; n < nj; ++n, ++g) {
           const uint32_t s = g & 1u;
           if (n + 1 < nj) {
             if (!warp_wait_all(c, p.limit_ns, phase_f(&c->tempty_l, g), phase_c(&c->tempty_r, g), v_of(g + 1))) {
@@ -1117,28 +1133,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
           }
           if (elect_one()) {
             if (n + 1 < nj) grads(g + 1, o0);
-            if (n == max(nj - 2, 0)) commit2_mc(&c->rempty[rs], 3);   // the unit's last S, dP are issued
+            if (n == max(nj - 2, first)) commit2_mc(&c->rempty[rs], 3);   // the unit's last S, dP are issued
           }
           __syncwarp();
           const bool more = n + 2 < nj;
           if (!warp_wait_all(c, p.limit_ns, phase_f(&c->oready_l[s], g >> 1), phase_c(&c->oready_r[s], g >> 1),
-                             phase_f(&c->yfull[s], g >> 1), k_of(g + 2, more), phase_c(&c->accempty, lu ^ 1u, n == 0))) {
+                             phase_f(&c->yfull[gy & 1u], gy >> 1, n >= 0), k_of(g + 2, more),
+                             phase_c(&c->accempty, lu ^ 1u, n == 0))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t y0 = dplus(dY, s * 16384u);
           if (elect_one()) {
-            // dS: 16 columns at the start of each epilogue warp's 32
+            if (n >= 0) {
+              // dS: 16 columns at the start of each epilogue warp's 32
+              const uint64_t y0 = dplus(dY, (gy & 1u) * 16384u);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma2_bf16_ts(tmem + QT_DQ, tmem + 128 * s + 32 * (k >> 1) + 8 * (k & 1), dplus(y0, k * 2048), IDESC_KM,
-                           (n || k) ? 1u : 0u);
-            commit2_mc(&c->yempty[s], 3);
-            if (n == nj - 1) commit2_mc(&c->dqfull, 3);
+              for (int k = 0; k < 8; ++k)
+                mma2_bf16_ts(tmem + QT_DQ, tmem + 128 * s + 32 * (k >> 1) + 8 * (k & 1), dplus(y0, k * 2048), IDESC_KM,
+                             (n || k) ? 1u : 0u);
+              commit2_mc(&c->yempty[gy & 1u], 3);
+              if (n == nj - 1) commit2_mc(&c->dqfull, 3);
+            }
             if (more) scores(g + 2, q0);
           }
           __syncwarp();
+          gy += n >= 0;
         }
         if (!ok) break;
         ++lu;
@@ -1153,7 +1173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
   } else {
     const int q = warp & 3, cg = (warp - 2) >> 2;   // lane quadrant, 32-column group
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(32 * cg);
-    uint32_t g = 0, lu = 0;
+    uint32_t g = 0, lu = 0, ns = 0;   // blocks, units, units that summed first
     bool ok = true;
     // the next unit's entry is loaded during this one, its rows' values while this one's dQ leaves
     int z, qp, j0, nj, qw, lo, hi;   // qw: this warp's first query; keys this thread's query sees
@@ -1193,7 +1213,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
           continue;
         }
       }
-      for (int j = 0; j < nj; ++j, ++g) {
+      float Dv = Dq;
+      float2 sum = make_float2(0.f, 0.f);
+      for (int n = S::q_first(nj); n < nj; ++n, ++g) {
         if (!warp_wait_c(&c->tfull, g, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         uint32_t rs[32], rd[32], dw[16];   // dw: bf16 pairs of dS over this thread's 32 keys
@@ -1203,18 +1225,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_leader(rank, &c->tempty_l, &c->tempty_r);   // dP is in registers: the next block's may be formed
-        const int kg = 128 * (j0 + j) + 32 * cg;    // first key
-        if (kg + 31 < lo0 || kg >= hi1) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dw[i] = 0u;
-        } else if (kg >= lo1 && kg + 31 < hi0) {
-          q_block<S, false>(rs, rd, sc, lz2, Dq, kg, qr, lo, hi, dw);
-        } else {
-          q_block<S, true>(rs, rd, sc, lz2, Dq, kg, qr, lo, hi, dw);
+        const bool sums = S::kSumFirst && n < 0;
+        const int kg = 128 * (j0 + (sums ? n + nj : n)) + 32 * cg;    // first key
+        const bool none = kg + 31 < lo0 || kg >= hi1, all = kg >= lo1 && kg + 31 < hi0;
+        if constexpr (S::kSumFirst) {
+          if (sums && all) q_block<S, false, true>(rs, rd, sc, lz2, Dv, kg, qr, lo, hi, dw, sum);
+          else if (sums && !none) q_block<S, true, true>(rs, rd, sc, lz2, Dv, kg, qr, lo, hi, dw, sum);
         }
-        __syncwarp();
-        tmem_st16(trow + 128 * (g & 1u), dw);       // over this warp's own scores
-        tmem_st_wait();
+        if (!sums) {
+          if (none) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dw[i] = 0u;
+          } else if (all) {
+            q_block<S, false, false>(rs, rd, sc, lz2, Dv, kg, qr, lo, hi, dw, sum);
+          } else {
+            q_block<S, true, false>(rs, rd, sc, lz2, Dv, kg, qr, lo, hi, dw, sum);
+          }
+          __syncwarp();
+          tmem_st16(trow + 128 * (g & 1u), dw);       // over this warp's own scores
+          tmem_st_wait();
+        }
+        if constexpr (S::kSumFirst) {
+          if (n == -1) {   // the rows' sums over the four column groups, by way of the scores' place
+            __syncwarp();
+            tmem_st1(trow + 128 * (g & 1u), __float_as_uint(sum.x + sum.y));
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->sums[q]);
+            if (!warp_wait_f(&c->sums[q], ns++, c, p.limit_ns)) { ok = false; break; }
+            tc_fence_after();
+            __syncwarp();
+            uint32_t part[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_ld1(trow + 128 * (g & 1u) + 32 * (k - cg), part[k]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) Dv += __uint_as_float(part[k]);
+            if (cg == 0 && qr < p.c1) p.D[(int64_t)z * p.T + qr] = Dv;
+          }
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_leader(rank, &c->oready_l[g & 1u], &c->oready_r[g & 1u]);
@@ -1251,7 +1301,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     __syncwarp();
     if (!ok) fail_f(c, p.status);
   }
-  wait_for_primary();   // k_attn_kv, of which nothing is read
   teardown_f(c, warp);
 }
 

@@ -13,12 +13,18 @@
 // The exponentials are taken from the maximum of earlier blocks, while the block's own is found
 // beside them: any reference serves the quotient as long as neither overflows.  Only a block
 // that exceeds it by 2^kLag or holds a row's first keys is read once more beforehand, to raise
-// the maximum and rescale O and l.  (The maximum first, for every block, took 1.67 ms in place
-// of TIME at 32 heads, 16384 tokens: a second pass over the scores.)
+// the maximum and rescale O and l.
 // Scores capped at up to kStaticCap need no maximum (0, or the row's largest bias): 2^x neither
-// overflows nor, for at least one key, underflows.  The sum l adds the fp32 probabilities; P is rounded to
-// bf16 for the product, the operand type of the tensor pipe at full rate: at most 2^-8 of
-// each probability.
+// overflows nor, for at least one key, underflows.  The sum l adds the fp32 probabilities; P is
+// rounded to bf16 for the product, the operand type of the tensor pipe at full rate: at most
+// 2^-8 of each probability.
+// The end of a unit, the wait for its last products and the join, comes behind the next unit's
+// first block.
+// What bounds it: 32 / 8 heads of 128, 16384 tokens, take 1.49 ms (1475 TFLOP/s over the visible
+// pairs); the tensor pipe is busy 1034 of about 1550 cycles a block, the rest is the handoff from
+// P to O += P V to the group's next S, which the other group hides in part.  Documents of 1000 to
+// 2500 tokens: 156 us (812 TFLOP/s; a quarter of the products lie outside the documents or
+// behind the diagonal), capped at 50: 250 us, the special-function unit's time.
 //
 // Pair protocol and bounded waits as in the backward kernels (sbp_attn_fused.cuh).
 #include <algorithm>
@@ -34,7 +40,7 @@ using fa::dplus;
 using fa::mma2_bf16_ts;
 using fa::tmem_st_wait;
 
-// Warps: 0 TMA producers, 1 MMA issuer (leader) or forwarder (the other CTA), 2 and 3 idle, 4-7
+// Warps: 0 TMA producers, 1 MMA issuer (leader), 2 and 3 idle, 4-7
 // and 8-11 the softmax groups (lane quadrant warp % 4).
 constexpr int SOFT_WARP = 4;
 constexpr int THREADS = 384;
@@ -58,7 +64,7 @@ struct Ctrl {
   uint64_t kfull[KV_STAGES], kempty[KV_STAGES], vfull[KV_STAGES], vempty[KV_STAGES];
   uint64_t qfull[2], qempty[2];   // Q of the unit; free: its products are done, and O has left
   uint64_t sfull[2];      // S of the group's block is ready, and its earlier products are done
-  uint64_t pready_l[2];   // P is written: the CTA's four warps of the group
+  uint64_t pready_l[2];   // P is written: the leader's four warps of the group
   uint64_t pready_r[2];   // the same of the other CTA (leader)
   uint64_t ofull;         // the unit's products are done (both CTAs)
   uint64_t accempty;      // leader: the unit's O has been read out
@@ -178,8 +184,8 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], float m0) {
   return max3(fmaxf(m[0], m[1]), m[2], fmaxf(m[3], __uint_as_float(r[31])));
 }
 // 32 probabilities 2^(mul x + nm) (PLAIN: 2^x): packed to bf16, their sum added to l.
-// (Keeping a quarter or more of them off the special-function unit, by a polynomial, took
-// longer at every share: 1.67 ms against 2.08 at 32 heads, 16384 tokens.)
+// (Keeping some of them off the special-function unit, by a polynomial, took longer at every
+// share: a quarter 2.08 ms against 1.67 at 32 heads, 16384 tokens.)
 template <bool PLAIN>
 __device__ __forceinline__ void probs32(const uint32_t (&r)[32], float mul, float nm, uint32_t* pw, float2& l) {
   const float2 m2 = make_float2(mul, mul), nm2 = make_float2(nm, nm);
@@ -611,11 +617,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 namespace {
 
-// Largest cap that needs no running maximum: 2^x of scores within 64 log2(e) = 92 lies in
-// [2^-92, 2^92], and sums over any number of keys that fits stay far from overflow.  With a
-// distance bias the scores less the row's largest bias take the place of x: none is above 92,
-// and the key with that bias (the row's own, or the farthest) is not below -92.
-constexpr float kStaticCap = 64.f;
+// Largest cap that needs no running maximum: 2^x of scores within 50 log2(e) = 72 lies in
+// [2^-72, 2^72], which leaves 2^40 either way for V and for sums over any number of keys that
+// fits.  With a distance bias the scores less the row's largest bias take the place of x: none
+// is above 72, and the key with that bias (the row's own, or the farthest) is not below -72.
+// (Cap 50, 8192 tokens in documents: 250 us, 300 with the maximum.)
+constexpr float kStaticCap = 50.f;
 
 template <bool CAP, bool BIAS, bool FIXED>
 cudaError_t launch_o(const PackedArgs& a, const PackedWork& w, void* O, float* lse, cudaStream_t s) {

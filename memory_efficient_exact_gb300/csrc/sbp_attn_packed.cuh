@@ -61,7 +61,8 @@ __device__ __forceinline__ int next_unit(int t, int pid, int npairs) {
 
 // Constants of the score in log2 units: with a cap, c tanh(y) = c - 2 c / (1 + e^(2 y)),
 // y = s scale / c: one exponential and one reciprocal, the absolute error about c 2^-22
-// (tanh.approx would leave c 2^-11).  An odd polynomial of degree 11, where all of a warp's
+// (tanh.approx would leave c 2^-11; caps above 256, where it would pass 2^-14, are refused).  An
+// odd polynomial of degree 11, where all of a warp's
 // scores are within it, was slower: nine operations at the rate of the FMA pipe against two
 // special-function ones (forward of 8192 tokens, cap 50: 408 us against 309).
 struct Scale { float sl2, c2, k, ic2; };

@@ -485,6 +485,14 @@ def _on_device(first, *ts):
             raise ValueError("tensors must be contiguous CUDA tensors of one device, the current one")
 
 
+def _status_word(status, stream, dev):
+    if status is None:
+        return _empty(stream, (), torch.int32, dev)
+    if status.dtype != torch.int32 or status.numel() != 1:
+        raise ValueError("status must be one int32")
+    return status
+
+
 def _empty(stream, shape, dtype, dev):
     """What a call allocates belongs to the stream it runs on."""
     if stream is None:
@@ -544,7 +552,7 @@ def attn_packed(Q, K, V, scale, *, cu_seqlens=None, prefix_lens=None, slopes=Non
         raise ValueError("O bf16 [H, T, hd]; lse fp32 [H, T]")
     O = _empty(stream, (H, T, hd), torch.bfloat16, dev) if O is None else O
     lse = _empty(stream, (H, T), torch.float32, dev) if lse is None else lse
-    st = _empty(stream, (), torch.int32, dev) if status is None else status
+    st = _status_word(status, stream, dev)
     _check(_lib.sbp_attn_packed_forward(_a(Q), _a(K), _a(V), _a(cu_seqlens), _a(prefix_lens), n_seq, _a(slopes), H,
                                         Hkv, T, hd, scale, softcap, _a(O), _a(lse), _a(ws), ws.numel(), _a(st),
                                         _raw(stream, dev)), "sbp_attn_packed_forward")
@@ -569,7 +577,7 @@ def attn_packed_backward(Q, K, V, O, dO, lse, scale, *, cu_seqlens=None, prefix_
     dQ = _empty(stream, (H, T, hd), torch.bfloat16, dev) if dQ is None else dQ
     dK = _empty(stream, (Hkv, T, hd), torch.bfloat16, dev) if dK is None else dK
     dV = _empty(stream, (Hkv, T, hd), torch.bfloat16, dev) if dV is None else dV
-    st = _empty(stream, (), torch.int32, dev) if status is None else status
+    st = _status_word(status, stream, dev)
     _check(_lib.sbp_attn_packed_backward(_a(Q), _a(K), _a(V), _a(O), _a(dO), _a(lse), _a(cu_seqlens), _a(prefix_lens),
                                          n_seq, _a(slopes), H, Hkv, T, hd, scale, softcap, _a(dQ), _a(dK), _a(dV),
                                          _a(ws), ws.numel(), _a(st), _raw(stream, dev)), "sbp_attn_packed_backward")
@@ -658,7 +666,7 @@ def rmsnorm_backward(dY, R, gamma, eps, *, dR=None, dX=None, dgamma=None, accumu
         workspace = _empty(stream, n, torch.uint8, dev)
     dX = _empty(stream, (T, d), R.dtype, dev) if dX is None else dX
     dgamma = _empty(stream, d, torch.float32, dev) if dgamma is None else dgamma
-    st = _empty(stream, (), torch.int32, dev) if status is None else status
+    st = _status_word(status, stream, dev)
     _check(_lib.sbp_rmsnorm_backward(_a(dY), _a(R), _a(gamma), _a(dR), T, d, eps, dt, _a(dX), _a(dgamma),
                                      1 if accumulate else 0, _a(workspace), workspace.numel(), _a(st),
                                      _raw(stream, dev)), "sbp_rmsnorm_backward")

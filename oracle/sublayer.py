@@ -104,10 +104,11 @@ def attention(Q, K, V, see, scale, softcap=0.0, slopes=None):
     return dict(O=O, lse=lse, size=size)
 
 
-def attention_backward(Q, K, V, O, dO, lse, see, scale, softcap=0.0, slopes=None):
+def attention_backward(Q, K, V, O, dO, lse, see, scale, softcap=0.0, slopes=None, errO=None):
     """dQ, dK, dV at the given O and lse, and bounds of what rounding P and dS to bf16 (2^-8 of
     each) and fp32 sums (2^-11 of the terms of dS; 2^-11 of P, from the scores' and the
-    exponential's error) can do to them: bQ, bK, bV."""
+    exponential's error) can do to them: bQ, bK, bV.  errO: what the O that D = dO . O is taken
+    from may be off by (per element; default 0)."""
     Q, K, V, O, dO, lse = (_f64(a) for a in (Q, K, V, O, dO, lse))
     grp = Q.shape[0] // K.shape[0]
     out = dict(dQ=np.zeros_like(Q), dK=np.zeros_like(K), dV=np.zeros_like(V),
@@ -121,6 +122,8 @@ def attention_backward(Q, K, V, O, dO, lse, see, scale, softcap=0.0, slopes=None
         dS = P * (dP - D[:, None]) * d
         terms = P * (np.abs(dO[h]) @ np.abs(V[z]).T + np.abs(dO[h] * O[h]).sum(axis=1)[:, None])
         err = 2.0 ** -8 * np.abs(dS) + 2.0 ** -11 * terms
+        if errO is not None:
+            err += P * d * (np.abs(dO[h]) * errO[h]).sum(axis=1)[:, None]
         out["dQ"][h] = scale * dS @ K[z]
         out["bQ"][h] = scale * err @ np.abs(K[z])
         out["dK"][z] += scale * dS.T @ Q[h]

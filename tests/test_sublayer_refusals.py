@@ -44,6 +44,13 @@ def test_attention(sbp, backward):
         assert attn(sbp, backward, **kw) == code, kw
 
 
+@pytest.mark.parametrize("backward", [False, True])
+def test_attention_scores_out_of_range(sbp, backward):
+    # caps whose scores would lose accuracy, and scales that are infinite in fp32 log2 units
+    for kw in [dict(cap=257.0), dict(scale=3e38), dict(scale=1e33, cap=1e-6)]:
+        assert attn(sbp, backward, **kw) == sbp.ERR_UNSUPPORTED, kw
+
+
 def test_attention_workspace(sbp):
     f = sbp.attn_packed_workspace_bytes
     assert f(4, 3, 16, 64) == 0 and f(4, 2, 16, 60) == 0 and f(4, 2, -1, 64) == 0
