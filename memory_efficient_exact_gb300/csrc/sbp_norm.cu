@@ -14,7 +14,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "sbp_internal.h"
+#include "sbp_tc_common.cuh"
 
 namespace sbp {
 namespace {
@@ -178,9 +178,10 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_fwd(const FwdP p) {
           for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(r[i].v[k]));
         }
         for (int o = min(8, p.lpr / 2); o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        // 448: e4m3's largest value.  A block of zeros keeps the scale 1.  One division a
+        // 448: e4m3's largest value.  A block of zeros keeps the scale 1; a scale that is not
+        // normal would have no inverse.  One division a
         // block and products instead of a division an element (132 us against 87).
-        const float s = a > 0.f ? a / 448.f : 1.f, inv = 1.f / s;
+        const float s = a > 0.f ? fmaxf(a / 448.f, 1.17549435e-38f) : 1.f, inv = 1.f / s;
         if (v < nvec) {
           uint32_t w2[2];
 #pragma unroll
@@ -211,7 +212,7 @@ struct BwdP {
 // A block walks rows blockIdx.x * rpb + k gridDim.x * rpb, keeps its share of dgamma in
 // registers and leaves it in `part` (summed in a fixed order by k_dgamma).  The
 // next row's loads are issued before this row's sums, which hide them: without that a block
-// waited for memory and for its barriers in turn (T = 16384, d = 4096: 235 us, now 91).
+// waited for memory and for its barriers in turn (T = 16384, d = 4096: 235 us, 92 with).
 // MAXT: the most threads of a block, MINB: how many blocks of it an SM should hold, which set
 // the registers a thread may have.
 template <typename E, int NV, int MAXT, int MINB>
@@ -324,6 +325,126 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd(const BwdP p) {
   for (int i = threadIdx.x; i < p.d; i += blockDim.x) part[i] = acc[i];
 }
 
+// The same where a block works on one row (d > 2048), whose R, dY and dR come by bulk copies into a
+// ring of `stages` rows in shared memory: whole rows stay in flight however many registers their
+// threads have.  A row's place is filled again behind the next row's barrier.  bf16, from
+// registers and from the ring: 16384 x 2560 63 and 60 us, 16384 x 4096 92 and 88 (6120 GB/s),
+// 8190 x 5120 74 and 67, 8190 x 8192 95 and 87 (6190 GB/s); 4096 x 16384, two rows of 1024
+// threads, 151 and 146.
+struct RingP {
+  BwdP b;
+  int stages;
+  int32_t* status;
+  uint64_t limit_ns;
+};
+constexpr int MAX_STAGES = 4;
+constexpr int RING_BYTES = 208 * 1024;   // of an SM
+template <typename E, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd_ring(const RingP a) {
+  constexpr int NV = 2;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][MAXW];
+  __shared__ uint64_t full[MAX_STAGES];
+  __shared__ int abort;
+  const BwdP& p = a.b;
+  const int step = blockDim.x, t0 = threadIdx.x;
+  const uint32_t bytes = (uint32_t)(p.d * sizeof(E));   // of an operand's row
+  const float inv_d = 1.f / (float)p.d;
+  const int64_t stride = gridDim.x;
+  auto load = [&](int64_t row, int slot) {   // by one thread
+    if (row >= p.T) return;
+    uint8_t* dst = ring + (size_t)slot * 3 * bytes;
+    tc::mbar_expect_tx(&full[slot], (p.dR ? 3u : 2u) * bytes);
+    tc::bulk_load(tc::saddr(dst), static_cast<const E*>(p.R) + row * p.d, bytes, &full[slot]);
+    tc::bulk_load(tc::saddr(dst + bytes), static_cast<const E*>(p.dY) + row * p.d, bytes, &full[slot]);
+    if (p.dR) tc::bulk_load(tc::saddr(dst + 2 * bytes), static_cast<const E*>(p.dR) + row * p.d, bytes, &full[slot]);
+  };
+  if (t0 == 0) {
+    abort = 0;
+    for (int i = 0; i < a.stages; ++i) tc::mbar_init(&full[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < a.stages; ++i) load(blockIdx.x + i * stride, i);
+  }
+  F8 dg[NV];
+  Raw<E> g[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = t0 + i * step;
+    if (v < p.nvec) g[i].load(static_cast<const E*>(p.gamma) + 8 * v);
+    else g[i].zero();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dg[i].v[k] = 0.f;
+  }
+  __syncthreads();
+  int flip = 0, slot = 0;
+  uint32_t phase = 0;
+  for (int64_t row = blockIdx.x; row < p.T; row += stride) {
+    const E* r = reinterpret_cast<const E*>(ring + (size_t)slot * 3 * bytes);
+    const E *y = r + p.d, *q = y + p.d;
+    const bool ok = tc::wait_inl<false>(&full[slot], phase, &abort, a.limit_ns);
+    if (!ok) *(volatile int*)&abort = 1;
+    Raw<E> cr[NV], cy[NV];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t0 + i * step;
+      cr[i].zero();
+      cy[i].zero();
+      if (v < p.nvec) {
+        cr[i].load(r + 8 * v);
+        cy[i].load(y + 8 * v);
+      }
+      const F8 x = cr[i].f(), b = cy[i].f(), c = g[i].f();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s.x = fmaf(x.v[k], x.v[k], s.x);
+        s.y = fmaf(b.v[k] * c.v[k], x.v[k], s.y);
+      }
+    }
+    s = row_sums(s, red, flip, 32, step / 32);
+    flip ^= 1;
+    if (*(volatile int*)&abort) break;   // every thread's, behind the barrier
+    // the row before this one has been read by all
+    if (t0 == 0 && row != blockIdx.x) load(row + (a.stages - 1) * stride, slot ? slot - 1 : a.stages - 1);
+    const float rstd = rsqrtf(s.x * inv_d + p.eps);
+    const float c = rstd * rstd * (s.y * inv_d);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t0 + i * step;
+      if (v < p.nvec) {
+        Raw<E> cq;
+        cq.zero();
+        if (p.dR) cq.load(q + 8 * v);
+        const F8 x = cr[i].f(), b = cy[i].f(), e = g[i].f(), f = cq.f();
+        F8 o;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          dg[i].v[k] = fmaf(b.v[k], x.v[k] * rstd, dg[i].v[k]);
+          o.v[k] = fmaf(rstd, b.v[k] * e.v[k] - x.v[k] * c, f.v[k]);
+        }
+        store8(static_cast<E*>(p.dX) + row * p.d + 8 * v, o);
+      }
+    }
+    if (++slot == a.stages) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+  if (*(volatile int*)&abort) {   // the copies in flight come to rest before the block ends
+    if (t0 == 0) {
+      atomicCAS(a.status, 0, SBP_ERR_TIMEOUT);
+      for (int i = 0; i < a.stages; ++i) tc::wait_inl<false>(&full[i], phase ^ (i < slot ? 1u : 0u), nullptr, 200000000ull);
+    }
+    __syncthreads();
+  }
+  float* part = p.part + (int64_t)blockIdx.x * p.d;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = t0 + i * step;
+    if (v < p.nvec) store8(part + 8 * v, dg[i]);
+  }
+}
+
 // dgamma[c] (+)= sum over the n parts, 32 columns a block, 32 threads a column.
 __global__ void __launch_bounds__(1024) k_dgamma(const float* __restrict__ part, int n, int d, int accumulate,
                                                  float* __restrict__ out) {
@@ -424,9 +545,8 @@ int run_fwd(const void* X, const void* res, const void* gamma, int64_t T, int64_
   return SBP_OK;
 }
 
-// The backward's builds: threads and blocks an SM, which set its registers (128 a thread;
-// 64 at more than 512 threads, which leaves none for the loads ahead).  At d = 5120, one block of
-// 320 threads with 128 registers takes 75 us, two with 96 and their spills 85 (T = 8190).
+// The register builds: threads and blocks an SM, which set the registers of a thread (128; 64 at
+// more than 512 threads, which leaves none for the loads ahead).
 void bwd_build(const Shape& s, int* maxt, int* minb) {
   if (s.nv == 1) { *maxt = 256; *minb = 3; }
   else if (s.threads <= 256) { *maxt = 256; *minb = 2; }
@@ -434,9 +554,20 @@ void bwd_build(const Shape& s, int* maxt, int* minb) {
   else { *maxt = 1024; *minb = 1; }
 }
 
+// The ring's rows and its blocks an SM; no rows where several rows share a block or fewer than
+// three fit (fp32, 8190 x 8192: 221 us with two, 186 from registers; two are kept where the
+// registers hold no row ahead).
+int ring_stages(const Shape& s, int64_t d, int dtype, int* per_sm) {
+  *per_sm = std::max(1, 512 / s.threads);
+  if (s.rpb > 1) return 0;
+  const int64_t n = RING_BYTES / *per_sm / (3 * d * (dtype == SBP_BF16 ? 2 : 4));
+  return n < (s.threads <= 512 ? 3 : 2) ? 0 : (int)std::min<int64_t>(n, MAX_STAGES);
+}
+
 struct BwdLayout {
   size_t off_part = 0, total = 0;
   int64_t blocks = 0;
+  int stages = 0;
   Guards guards;   // checked build only
 };
 bool bwd_layout(int64_t T, int64_t d, int dtype, BwdLayout* L) {
@@ -445,7 +576,9 @@ bool bwd_layout(int64_t T, int64_t d, int dtype, BwdLayout* L) {
   const Shape s = shape_of(d);
   int maxt, minb;
   bwd_build(s, &maxt, &minb);
-  l.blocks = blocks_of(T, s, maxt, minb);
+  int per_sm;
+  l.stages = ring_stages(s, d, dtype, &per_sm);
+  l.blocks = l.stages ? std::max<int64_t>(1, std::min<int64_t>(T, (int64_t)num_sms() * per_sm)) : blocks_of(T, s, maxt, minb);
   size_t o = 0;
   l.off_part = take_region(o, (size_t)l.blocks * d * sizeof(float), l.guards);
   l.total = o;
@@ -460,6 +593,25 @@ cudaError_t launch_bwd(const BwdP& p, const Shape& s, unsigned grid, cudaStream_
   else if (s.threads <= 512) k_rmsnorm_bwd<E, 2, 512, 1><<<grid, s.threads, 0, st>>>(p);
   else k_rmsnorm_bwd<E, 2, 1024, 1><<<grid, s.threads, 0, st>>>(p);
   return cudaGetLastError();
+}
+
+template <typename E, int MAXT, int MINB>
+cudaError_t launch_ring1(const RingP& r, const Shape& s, unsigned grid, cudaStream_t st) {
+  static int attr_state[64] = {};
+  static std::mutex mu;
+  if (!tc::once_per_device(attr_state, mu, [] {
+        return cudaFuncSetAttribute(k_rmsnorm_bwd_ring<E, MAXT, MINB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    RING_BYTES / MINB) == cudaSuccess;
+      }))
+    return cudaErrorInvalidConfiguration;
+  k_rmsnorm_bwd_ring<E, MAXT, MINB><<<grid, s.threads, (size_t)r.stages * 3 * r.b.d * sizeof(E), st>>>(r);
+  return cudaGetLastError();
+}
+template <typename E>
+cudaError_t launch_ring(const RingP& r, const Shape& s, unsigned grid, cudaStream_t st) {
+  if (s.threads <= 256) return launch_ring1<E, 256, 2>(r, s, grid, st);
+  if (s.threads <= 512) return launch_ring1<E, 512, 1>(r, s, grid, st);
+  return launch_ring1<E, 1024, 1>(r, s, grid, st);
 }
 
 }  // namespace
@@ -536,8 +688,15 @@ int sbp_rmsnorm_backward(const void* dY, const void* R, const void* gamma, const
   const Shape sh = shape_of(d);
   float* part = reinterpret_cast<float*>(w + L.off_part);
   BwdP p{dY, R, gamma, dR, T, (int)d, (int)(d / 8), sh.lpr, sh.wpr, sh.rpb, eps, dX, part};
-  const cudaError_t e = dtype == SBP_BF16 ? launch_bwd<__nv_bfloat16>(p, sh, (unsigned)L.blocks, s)
-                                          : launch_bwd<float>(p, sh, (unsigned)L.blocks, s);
+  cudaError_t e;
+  if (L.stages) {
+    const RingP r{p, L.stages, dev_status, tc::wait_limit_ns()};
+    e = dtype == SBP_BF16 ? launch_ring<__nv_bfloat16>(r, sh, (unsigned)L.blocks, s)
+                          : launch_ring<float>(r, sh, (unsigned)L.blocks, s);
+  } else {
+    e = dtype == SBP_BF16 ? launch_bwd<__nv_bfloat16>(p, sh, (unsigned)L.blocks, s)
+                          : launch_bwd<float>(p, sh, (unsigned)L.blocks, s);
+  }
   if (e != cudaSuccess) return SBP_ERR_CUDA;
   k_dgamma<<<(unsigned)((d + 31) / 32), 1024, 0, s>>>(part, (int)L.blocks, (int)d, accumulate ? 1 : 0, dgamma);
   if (cudaGetLastError() != cudaSuccess) return SBP_ERR_CUDA;

@@ -50,7 +50,9 @@ def rows(T, d, seed, dtype, n):
 
 
 SHAPES = [(1, 8), (1, 4096), (3, 16), (9, 128), (5, 136), (17, 248), (70, 264), (33, 1000), (300, 2560), (7, 5120),
-          (2, 8192), (3, 8200), (2, 16384), (2000, 64)]
+          (2, 8192), (3, 8200), (2, 16384), (2000, 64),
+          # more rows than blocks and ring places
+          (1000, 2056), (1700, 4096), (900, 5120), (430, 8536), (400, 16384)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -103,6 +105,18 @@ def test_norm_in_8_bits_of_zeros(sbp):
     assert torch.all(f["scales"][[0, 2]] == 1) and f["scales"][1, 1] == 1 and f["scales"][1, 0] > 0
     y = sbp.e4m3_expand(f["Y8"], f["scales"])["Y"]
     assert torch.isfinite(y).all() and (y != 0).sum() == 1
+
+
+@pytest.mark.parametrize("tiny", [2.0 ** -120, 2.0 ** -126, 2.0 ** -130, 2.0 ** -133])
+def test_norm_in_8_bits_of_tiny_values(sbp, tiny):
+    # the scale of a block stays a normal number: off by half of e4m3's smallest step of it
+    X = torch.ones((2, 256), device="cuda") * torch.tensor([1.0, -1.0], device="cuda")[:, None]
+    X[:, ::3] = 0.0
+    g = torch.full((256,), tiny, device="cuda")
+    want = host(sbp.rmsnorm(X, g, 0.0)["Y"])
+    f = sbp.rmsnorm_e4m3(X, g, 0.0)
+    got = host(sbp.e4m3_expand(f["Y8"], f["scales"], torch.float32)["Y"])
+    near("Y", got, want, np.maximum(2.0 ** -4 * np.abs(want) * (1 + 2.0 ** -16), 2.0 ** -10 * 2.0 ** -126) + 2.0 ** -149)
 
 
 def test_norm_nan_stays_in_its_row(sbp):
