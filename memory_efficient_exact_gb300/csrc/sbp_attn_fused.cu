@@ -8,19 +8,6 @@ namespace sbp {
 
 namespace {
 
-// 3-D fp32 map over [H, T, 128] for the dK / dV reduce-adds: 32 x 32 x 1 boxes.
-bool map3_f32(CUtensorMap* m, void* ptr, int64_t T, int64_t H) {
-  auto enc = tc::encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {128, (cuuint64_t)T, (cuuint64_t)H};
-  cuuint64_t strides[2] = {128 * 4, (cuuint64_t)T * 128 * 4};
-  cuuint32_t box[3] = {32, 32, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool fused_attrs() {
   static int attr_state[64] = {};
   static std::mutex mu;
@@ -40,10 +27,12 @@ bool AttnFusedPlan::init(const void* Q, const void* K, const void* V, const void
   H = H_;
   Hkv = Hkv_;
   // query-side operands over H heads, key / value side (and dK, dV) over Hkv heads
-  return tc::make_map_heads(&K128, K, T, Hkv, 128, 128) && tc::make_map_heads(&V128, V, T, Hkv, 128, 128) && tc::make_map_heads(&Q64, Q, T, H, 128, 64) &&
-         tc::make_map_heads(&O64, dO, T, H, 128, 64) && tc::make_map_heads(&Q128, Q, T, H, 128, 128) && tc::make_map_heads(&O128, dO, T, H, 128, 128) &&
-         tc::make_map_heads(&K64, K, T, Hkv, 128, 64) && tc::make_map_heads(&V64, V, T, Hkv, 128, 64) && map3_f32(&dK, dK_, T, Hkv) &&
-         map3_f32(&dV, dV_, T, Hkv);
+  using tc::make_map_heads;
+  return make_map_heads(&K128, K, T, Hkv, 128, 128) && make_map_heads(&V128, V, T, Hkv, 128, 128) &&
+         make_map_heads(&Q64, Q, T, H, 128, 64) && make_map_heads(&O64, dO, T, H, 128, 64) &&
+         make_map_heads(&Q128, Q, T, H, 128, 128) && make_map_heads(&O128, dO, T, H, 128, 128) &&
+         make_map_heads(&K64, K, T, Hkv, 128, 64) && make_map_heads(&V64, V, T, Hkv, 128, 64) &&
+         tc::make_map_out(&dK, dK_, T, T, Hkv, 128, 4) && tc::make_map_out(&dV, dV_, T, T, Hkv, 128, 4);
 }
 
 cudaError_t attn_fused_kv(const AttnFusedPlan& plan, int64_t c0, int64_t c1, float scale, const float* lse,
