@@ -835,15 +835,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
         uint32_t rs[2][16];                        // scores, then probabilities
         const int q0 = qg + 2 * (lane & 3);        // the first of the thread's queries
         const float2* ldq = reinterpret_cast<const float2*>(ld) + 16 * cg + (lane & 3);
-        if (!warp_wait_c(&c->sfull, g, c, p.limit_ns) || !warp_wait_f(&c->lfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
+        // what is there long before comes before the wait that is not
+        if (!warp_wait_f(&c->lfull[s], g >> 1, c, p.limit_ns)) { ok = false; break; }
+        float2 nl[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nl[i] = ldq[64 * s + 4 * i];
+        if (!warp_wait_c(&c->sfull, g, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         __syncwarp();
         {
-          float2 nl[4];
           tmem_ld_frag(trow, rs[0]);
           tmem_ld_frag(trow + (16u << 16), rs[1]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) nl[i] = ldq[64 * s + 4 * i];
           tmem_ld_wait();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {            // 16 keys at a time, over this warp's own scores
@@ -861,16 +863,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           arrive_leader(rank, &c->pready_l, &c->pready_r);
           mbar_arrive(&c->lempty[s]);
         }
-        if (!warp_wait_c(&c->dpfull, g, c, p.limit_ns) || !warp_wait_f(&c->dfull, g, c, p.limit_ns)) { ok = false; break; }
+        if (!warp_wait_f(&c->dfull, g, c, p.limit_ns)) { ok = false; break; }
+        float2 nD[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nD[i] = ldq[128 + 4 * i];
+        if (!warp_wait_c(&c->dpfull, g, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         __syncwarp();
         {
-          float2 nD[4];
           uint32_t rd[2][16];
           tmem_ld_frag(trow + KT_DP, rd[0]);
           tmem_ld_frag(trow + KT_DP + (16u << 16), rd[1]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) nD[i] = ldq[128 + 4 * i];
           tmem_ld_wait();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
