@@ -122,10 +122,9 @@ struct PackedScores {
                                                   float2& dc) {
     float2 x;
     if (CAP) {
-      x = fma2(cap_parts<MASK>(sc, s), make_float2(-2.f * sc.c2, -2.f * sc.c2), make_float2(sc.c2, sc.c2));
-      const float2 th = mul2(x, make_float2(sc.ic2, sc.ic2));
-      dc = fma2(make_float2(-th.x, -th.y), th, make_float2(1.f, 1.f));   // 1 - tanh^2
-      x = add2(x, nlz);
+      const float2 r = cap_parts<MASK>(sc, s);
+      dc = mul2(r, fma2(r, make_float2(-4.f, -4.f), make_float2(4.f, 4.f)));   // 1 - tanh^2 = 4 r (1 - r)
+      x = fma2(r, make_float2(-2.f * sc.c2, -2.f * sc.c2), add2(nlz, make_float2(sc.c2, sc.c2)));
     } else {
       dc = make_float2(1.f, 1.f);
       x = fma2(s, make_float2(sc.sl2, sc.sl2), nlz);

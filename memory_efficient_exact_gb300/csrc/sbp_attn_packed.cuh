@@ -62,10 +62,10 @@ __device__ __forceinline__ int next_unit(int t, int pid, int npairs) {
 // Constants of the score in log2 units: with a cap, c tanh(y) = c - 2 c / (1 + e^(2 y)),
 // y = s scale / c: one exponential and one reciprocal, the absolute error about c 2^-22
 // (tanh.approx would leave c 2^-11; caps above 256, where it would pass 2^-14, are refused).  An
-// odd polynomial of degree 11, where all of a warp's
-// scores are within it, was slower: nine operations at the rate of the FMA pipe against two
-// special-function ones (forward of 8192 tokens, cap 50: 408 us against 309).
-struct Scale { float sl2, c2, k, ic2; };
+// odd polynomial of degree 11, where all of a warp's scores are within it, was slower: nine
+// operations at the rate of the FMA pipe against two special-function ones (forward of 8192
+// tokens, cap 50: 408 us against 309).
+struct Scale { float sl2, c2, k; };
 struct ScaleZ : Scale { float slope2; };
 
 __device__ __forceinline__ ScaleZ scale_z(const Scale& s, float slope) {
@@ -106,10 +106,7 @@ inline Scale make_scale(float scale, float softcap) {
   Scale s{};
   s.sl2 = scale * L2E;
   s.c2 = softcap * L2E;
-  if (softcap > 0.f) {
-    s.k = 2.f * L2E * scale / softcap;
-    s.ic2 = 1.f / s.c2;
-  }
+  if (softcap > 0.f) s.k = 2.f * L2E * scale / softcap;
   return s;
 }
 
