@@ -178,9 +178,8 @@ int run_rope(const RopeArgs& a, bool bwd, cudaStream_t s) {
   for (int i = 0; i < p.pairs; ++i) {
     const double f = a.inv_freq ? a.inv_freq[i] : std::pow(a.theta, -2.0 * i / (double)a.rot_dim);
     if (std::isnan(f) || std::isinf(f)) return SBP_ERR_INVALID_ARG;
-    double turn = std::fmod(f / 6.283185307179586476925, 1.0);   // whole turns of a step do not matter
-    if (turn < 0.0) turn += 1.0;
-    const double fx = std::ldexp(turn, 64);
+    const double turn = f / 6.283185307179586476925;
+    const double fx = (turn - std::floor(turn)) * 18446744073709551616.0;   // whole turns of a step do not matter
     p.F[i] = fx >= 18446744073709551616.0 ? 0u : (uint64_t)fx;
   }
   if (a.T > 0 && (!a.pos || !a.x || !a.q || (a.Hkv > 0 && (!a.k || !a.v)))) return SBP_ERR_INVALID_ARG;

@@ -673,14 +673,18 @@ def rmsnorm_backward(dY, R, gamma, eps, *, dR=None, dX=None, dgamma=None, accumu
     return dict(dX=dX, dgamma=dgamma, status=st)
 
 
+_INT32S = [ctypes.c_int32 * n for n in range(5)]   # (making an array type costs more than the array)
+
+
 def _rope_args(positions, T, rot_dim, sections, inv_freq):
     if positions.dim() != 2 or positions.shape[1] != T or positions.dtype != torch.int32:
         raise ValueError("positions must be int32 [n_axes, T]")
     n = positions.shape[0]
-    sections = [rot_dim // 2] if sections is None else list(sections)
+    if sections is None:
+        sections = (rot_dim // 2,)
     if len(sections) != n:
         raise ValueError("one section for each axis of positions")
-    sec = (ctypes.c_int32 * n)(*sections)
+    sec = (_INT32S[n] if n < 5 else ctypes.c_int32 * n)(*sections)
     freq = None
     if inv_freq is not None:
         if len(inv_freq) != rot_dim // 2:
