@@ -13,7 +13,7 @@
 //              then adds dV and s dK into the fp32 outputs (TMA reduce-add) or writes them.
 //              The two streams S -> P -> dV and dP -> dS -> dK take turns: while the
 //              epilogue works on one, the tensor pipe runs the other's products.  A block takes
-//              about 3200 cycles, 2070 of them the tensor pipe's; the epilogue's work is as
+//              about 3000 cycles, 2070 of them the tensor pipe's; the epilogue's work is as
 //              long, and the handoffs between the two show (32 / 8 heads, 8192 tokens, one
 //              document: tensor pipe 69% active, k_attn_q 80%).
 //   k_attn_q   unit = (head, 256 queries of the chunk).  dQ stays in tensor memory while
@@ -45,7 +45,7 @@ namespace fa {
 // warp % 4, 32 of the 128 columns each), then (k_attn_kv) one warp that stages lse and D per
 // block.  The epilogue warps arrive at the leader's barriers, one for its own warps and one
 // for the other CTA's.  (One lane of that CTA turning local phases into one remote arrival
-// each: causal benchmark 6.10M tokens/s against 6.25M.)
+// each: causal benchmark 6.10M tokens/s, 6.25M without.)
 constexpr int Q_EPI = 16, KV_EPI = 16;
 constexpr int KV_LD_WARP = 2 + KV_EPI;
 constexpr int KV_THREADS = 32 * (KV_LD_WARP + 1);   // five warps a scheduler: 96 registers a thread

@@ -214,6 +214,30 @@ def test_padding_may_hold_anything(sbp, bad):
     assert torch.all(dirty[1][:, n:] == -float("inf")) and all(torch.all(t[:, n:] == 0) for t in dirty[:1] + dirty[2:])
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("softcap,alibi", [(0.0, False), (0.0, True), (30.0, True), (90.0, True)])
+@pytest.mark.parametrize("hd,lens", [(128, [130, 3, 480]), (72, [77])])
+def test_padding_of_every_kernel_may_hold_anything(sbp, bad, softcap, alibi, hd, lens):
+    # an odd end inside a block of 128, long and short units, padding that fills whole units
+    H, Hkv, T, n = 4, 2, 1000, sum(lens)
+    a = {k: dev(v) for k, v in make(H, Hkv, T, hd, seed=13).items()}
+    _, _, kw = options(H, lens, None, softcap, alibi)
+
+    def run():
+        f = sbp.attn_packed(a["Q"], a["K"], a["V"], 0.1, **kw)
+        b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], 0.1, **kw)
+        return [f["O"], f["lse"], b["dQ"], b["dK"], b["dV"]]
+
+    clean = run()
+    for k in a:
+        a[k][:, n:] = bad
+    dirty = run()
+    torch.cuda.synchronize()
+    for c, d in zip(clean, dirty):
+        assert torch.equal(c, d)
+    assert all(torch.isfinite(t[:, :n]).all() for t in dirty)
+
+
 def test_infinite_keys_of_another_document_stay_masked(sbp):
     # an infinite K makes infinite scores for other documents' queries in the same tile; they
     # are masked before the exponential (V, Q and dO are summed over, so they must be finite)
