@@ -201,15 +201,12 @@ __device__ __forceinline__ void probs32(const uint32_t (&r)[32], float mul, floa
 
 // A block of 128 scores of a row (tensor memory tS) into its probabilities there; m and l are the
 // row's running maximum and sum, tO the group's accumulator, `fresh` while that holds nothing.
+// `raise`: the maximum has to be found before the exponentials.
 template <bool CAP, bool BIAS, bool FIXED, bool EDGE>
-__device__ __forceinline__ void soft_block(uint32_t tS, uint32_t tO, bool fresh, const Row& w, const pk::ScaleZ& sc,
-                                           float mul, float& m, float2& l) {
+__device__ __forceinline__ void soft_block(uint32_t tS, uint32_t tO, bool fresh, bool raise, const Row& w,
+                                           const pk::ScaleZ& sc, float mul, float& m, float2& l) {
   uint32_t ra[32], rb[32], pw[64];
   float2 lb;   // the block's sums
-  // whether the maximum has to be found before the exponentials
-  bool raise = !FIXED && __any_sync(0xffffffffu, m == -INFINITY && w.a < 128 && w.b > 0);
-  if (BIAS && !FIXED)   // and whether the bias alone lifts it there from the group's block before
-    raise = raise || (fabsf(sc.slope2) * 256.f > kLag && (sc.slope2 > 0.f ? w.first < 127 : w.first > -31));
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (raise) {
@@ -560,13 +557,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       float2 l2 = make_float2(0.f, 0.f);
       for (int n = (int)((g ^ (uint32_t)grp) & 1u);; n += 2) {   // this group's blocks
         if (n < nj) {
+          const int k0 = 128 * block_at<BIAS>(j0, nj, n);
+          const Row w{lo - k0, hi - k0, lo1 - k0, hi0 - k0, row - lane - k0, (float)(row - k0), top};
+          const bool edge = w.edge<BIAS>();
+          // the row's first keys, or a bias that alone lifts the maximum from the group's block before
+          bool raise = !FIXED && __any_sync(0xffffffffu, m == -INFINITY && w.a < 128 && w.b > 0);
+          if (BIAS && !FIXED)
+            raise = raise || (fabsf(sc.slope2) * 256.f > kLag && (sc.slope2 > 0.f ? w.first < 127 : w.first > -31));
           if (!warp_wait(&c->sfull[grp], (g + n) >> 1, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
           __syncwarp();
-          const int k0 = 128 * block_at<BIAS>(j0, nj, n);
-          const Row w{lo - k0, hi - k0, lo1 - k0, hi0 - k0, row - lane - k0, (float)(row - k0), top};
-          if (w.edge<BIAS>()) soft_block<CAP, BIAS, FIXED, true>(tS, tO, n < 2, w, sc, mul, m, l2);
-          else soft_block<CAP, BIAS, FIXED, false>(tS, tO, n < 2, w, sc, mul, m, l2);
+          if (edge) soft_block<CAP, BIAS, FIXED, true>(tS, tO, n < 2, raise, w, sc, mul, m, l2);
+          else soft_block<CAP, BIAS, FIXED, false>(tS, tO, n < 2, raise, w, sc, mul, m, l2);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) fa::arrive_leader(rank, &c->pready_l[grp], &c->pready_r[grp]);
