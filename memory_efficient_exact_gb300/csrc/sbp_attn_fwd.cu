@@ -3,7 +3,8 @@
 // k_attn_o  unit = (query head, 256 queries), 128 queries in each CTA of an SM pair, the
 // longest units first.  The unit walks its blocks of 128 keys; two groups of four softmax
 // warps take the blocks in turn, each with its own S buffer, running maximum, sum and O
-// accumulator in tensor memory, so that they exchange nothing until the unit's end:
+// accumulator in tensor memory, so that they exchange nothing until the unit's end (buffers and
+// accumulator are shared where the maximum is known, see Tmem):
 //   S = Q K^T            (tensor memory)
 //   P = 2^(x - m)        (one query row a thread; bf16, written over S)
 //   O += P V             (tensor memory; P is the A operand from tensor memory)
@@ -24,7 +25,7 @@
 // pairs); the tensor pipe is busy 1034 of about 1550 cycles a block, the rest is the handoff from
 // P to O += P V to the group's next S, which the other group hides in part.  Documents of 1000 to
 // 2500 tokens: 156 us (812 TFLOP/s; a quarter of the products lie outside the documents or
-// behind the diagonal), capped at 50: 250 us, the special-function unit's time.
+// behind the diagonal), capped at 50: 222 us, the special-function unit's time.
 //
 // Pair protocol and bounded waits as in the backward kernels (sbp_attn_fused.cuh).
 #include <algorithm>
@@ -55,17 +56,24 @@ constexpr uint32_t O_K = 65536;                          // this CTA's 64 keys o
 constexpr uint32_t O_V = O_K + KV_STAGES * 16384;        // 128 keys x this CTA's 64 of hd
 constexpr uint32_t O_ML = O_V + KV_STAGES * 16384;       // m, l: [2 units][2 groups][128 rows] float2
 constexpr uint32_t O_CTRL = O_ML + 4096;
-// Tensor memory: S (and P over it) of group b at 128 b, its O at T_O + 128 b.
-constexpr uint32_t T_O = 256;
+// Tensor memory: NB buffers of S (and P over it), block g's at 128 (g % NB), then O.  Two buffers,
+// one a group, and an O each; or, where the maximum is known beforehand and both groups' P
+// have the same reference, three and one O for both: a group's next S is then formed before its
+// P is multiplied (cap 50, 8192 tokens: 222 us, 248 with two).
+template <bool FIXED>
+struct Tmem {
+  static constexpr uint32_t NB = FIXED ? 3 : 2;
+  static constexpr uint32_t O = 128 * NB;
+};
 constexpr uint32_t IDESC_KK = idesc_bf16(256, 128, false, false);  // A, B K-major
 constexpr uint32_t IDESC_KM = idesc_bf16(256, 128, false, true);   // A K-major, B MN-major
 
 struct Ctrl {
   uint64_t kfull[KV_STAGES], kempty[KV_STAGES], vfull[KV_STAGES], vempty[KV_STAGES];
   uint64_t qfull[2], qempty[2];   // Q of the unit; free: its products are done, and O has left
-  uint64_t sfull[2];      // S of the group's block is ready, and its earlier products are done
-  uint64_t pready_l[2];   // P is written: the leader's four warps of the group
-  uint64_t pready_r[2];   // the same of the other CTA (leader)
+  uint64_t sfull[3];      // S of the buffer is ready, and the products before it are done
+  uint64_t pready_l[3];   // P is written over it: the leader's four warps of the block's group
+  uint64_t pready_r[3];   // the same of the other CTA (leader)
   uint64_t ofull;         // the unit's products are done (both CTAs)
   uint64_t accempty;      // leader: the unit's O has been read out
   uint64_t mlx;           // the CTA's eight softmax warps have left m and l
@@ -290,6 +298,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->qfull[i], 1);
       mbar_init(&c->qempty[i], 1 + 8);
+    }
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&c->sfull[i], 1);
       mbar_init(&c->pready_r[i], 4);
       mbar_init(&c->pready_l[i], 4);
@@ -393,13 +403,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                      dV = sw128_desc(sb + O_V, 16384, 1024);
       uint32_t g = 0, lu = 0;
       bool ok = true;
-      // S of block gg into its group's buffer: free, since the product that read the P in it
-      // was issued before
+      constexpr uint32_t NB = Tmem<FIXED>::NB;
+      // S of block gg into its buffer: free, since the product that read the P in it was issued
+      // before
       auto k_of = [&](uint32_t gg, bool need) {
         return fa::phase_f(&c->kfull[gg % KV_STAGES], gg / KV_STAGES, need);
       };
       auto scores = [&](uint32_t gg, uint32_t qs) {   // by the elected lane
-        const uint32_t s = gg % KV_STAGES, b = gg & 1u;
+        const uint32_t s = gg % KV_STAGES, b = gg % NB;
         const uint64_t q0 = dplus(dQ, qs * 32768u), k0 = dplus(dK, s * 16384u);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -416,21 +427,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         next = unit_of(p, pk::next_unit(rnd + 1, pid, npairs));
         if (nj <= 0) continue;
         const uint32_t qs = lu & 1u;
-        if (!fa::warp_wait_all(c, p.limit_ns, fa::phase_f(&c->qfull[qs], lu >> 1), k_of(g, true), k_of(g + 1, nj > 1))) {
+        if (!fa::warp_wait_all(c, p.limit_ns, fa::phase_f(&c->qfull[qs], lu >> 1), k_of(g, true), k_of(g + 1, nj > 1),
+                               k_of(g + 2, NB > 2 && nj > 2))) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (elect_one()) {
-          scores(g, qs);
-          if (nj > 1) scores(g + 1, qs);
+          for (uint32_t i = 0; i < NB && (int)i < nj; ++i) scores(g + i, qs);
         }
         __syncwarp();
         for (int n = 0; n < nj; ++n, ++g) {
-          const uint32_t s = g % KV_STAGES, b = g & 1u;
-          const bool more = n + 2 < nj;
-          if (!fa::warp_wait_all(c, p.limit_ns, fa::phase_f(&c->pready_l[b], g >> 1), fa::phase_c(&c->pready_r[b], g >> 1),
-                                 fa::phase_f(&c->vfull[s], g / KV_STAGES), k_of(g + 2, more),
+          const uint32_t s = g % KV_STAGES, b = g % NB;
+          const bool more = n + (int)NB < nj;
+          if (!fa::warp_wait_all(c, p.limit_ns, fa::phase_f(&c->pready_l[b], g / NB), fa::phase_c(&c->pready_r[b], g / NB),
+                                 fa::phase_f(&c->vfull[s], g / KV_STAGES), k_of(g + NB, more),
                                  fa::phase_c(&c->accempty, lu ^ 1u, n == 0))) {
             ok = false;
             break;
@@ -440,11 +451,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma2_bf16_ts(tmem + T_O + 128 * b, tmem + 128 * b + 8 * k, dplus(v0, k * 2048), IDESC_KM,
-                           (n > 1 || k) ? 1u : 0u);   // each group's first block overwrites
+              mma2_bf16_ts(tmem + Tmem<FIXED>::O + (FIXED ? 0 : 128 * b), tmem + 128 * b + 8 * k, dplus(v0, k * 2048),
+                           IDESC_KM, (n > (FIXED ? 0 : 1) || k) ? 1u : 0u);   // the accumulator's first block overwrites
             commit2_mc(&c->vempty[s], 3);
-            if (more) scores(g + 2, qs);
-            if (n + 2 == nj || nj == 1) commit2_mc(&c->qempty[qs], 3);   // every S of the unit is issued
+            if (more) scores(g + NB, qs);
+            if (n == max(nj - (int)NB, 0)) commit2_mc(&c->qempty[qs], 3);   // every S of the unit is issued
           }
           __syncwarp();
         }
@@ -462,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp >= SOFT_WARP) {
     const int q = warp & 3, grp = (warp - SOFT_WARP) >> 2;   // lane quadrant; softmax group
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-    const uint32_t tS = trow + 128 * grp, tO = trow + T_O + 128 * grp;
+    constexpr uint32_t NB = Tmem<FIXED>::NB, T_O = Tmem<FIXED>::O;
     const int lrow = 32 * q + lane;
     // scores stay raw when they only need the scale, which the exponent's FMA applies
     constexpr bool RAW = !CAP && !BIAS;
@@ -504,7 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         uint32_t ra[32], rb[32], v[16];
         __syncwarp();
         tmem_ld32(trow + T_O + 64 * grp + h, ra);
-        tmem_ld32(trow + T_O + 128 + 64 * grp + h, rb);
+        if (!FIXED) tmem_ld32(trow + T_O + 128 + 64 * grp + h, rb);
         tmem_ld_wait();
         if (h == 32) {   // both accumulators have been read: the next unit may overwrite them
           tc_fence_before();
@@ -513,6 +524,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
+          if (FIXED) {   // one accumulator, over one reference
+            v[i] = none ? 0u : pack_bf16(__uint_as_float(ra[2 * i]) * inv, __uint_as_float(ra[2 * i + 1]) * inv);
+            continue;
+          }
           // a group without a block for the row leaves its accumulator unset: selected out
           const float x0 = f0 == 0.f ? 0.f : __uint_as_float(ra[2 * i]) * a0;
           const float x1 = f0 == 0.f ? 0.f : __uint_as_float(ra[2 * i + 1]) * a0;
@@ -564,14 +579,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           bool raise = !FIXED && __any_sync(0xffffffffu, m == -INFINITY && w.a < 128 && w.b > 0);
           if (BIAS && !FIXED)
             raise = raise || (fabsf(sc.slope2) * 256.f > kLag && (sc.slope2 > 0.f ? w.first < 127 : w.first > -31));
-          if (!warp_wait(&c->sfull[grp], (g + n) >> 1, c, p.limit_ns)) { ok = false; break; }
+          const uint32_t b = (g + n) % NB, tS = trow + 128 * b, tO = trow + T_O + 128 * grp;
+          if (!warp_wait(&c->sfull[b], (g + n) / NB, c, p.limit_ns)) { ok = false; break; }
           tc_fence_after();
           __syncwarp();
           if (edge) soft_block<CAP, BIAS, FIXED, true>(tS, tO, n < 2, raise, w, sc, mul, m, l2);
           else soft_block<CAP, BIAS, FIXED, false>(tS, tO, n < 2, raise, w, sc, mul, m, l2);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) fa::arrive_leader(rank, &c->pready_l[grp], &c->pready_r[grp]);
+          if (lane == 0) fa::arrive_leader(rank, &c->pready_l[b], &c->pready_r[b]);
         }
         release();
         if (!finish()) { ok = false; break; }
@@ -623,7 +639,7 @@ namespace {
 // [2^-72, 2^72], which leaves 2^40 either way for V and for sums over any number of keys that
 // fits.  With a distance bias the scores less the row's largest bias take the place of x: none
 // is above 72, and the key with that bias (the row's own, or the farthest) is not below -72.
-// (Cap 50, 8192 tokens in documents: 250 us, 300 with the maximum.)
+// (8192 tokens in documents: cap 50 222 us, cap 50.5 314 us.)
 constexpr float kStaticCap = 50.f;
 
 template <bool CAP, bool BIAS, bool FIXED>
