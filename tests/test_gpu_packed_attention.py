@@ -7,7 +7,7 @@ largest relative rounding error, half a step):
   lse   2^-12 (the scores' fp32 sums) and 2^-20 of its value;
   dQ, dK, dV  u of the value, and the oracle's bounds for P and dS in bf16 (see there).
 The backward is compared at the exact O and the lse it was given.  Its D = dO . O is that of the O
-it was given, off by O's bound, but for units of 256 queries that see up to four blocks of 128
+it was given, off by O's bound, but for units of 256 queries that see up to three blocks of 128
 keys, which have it from P and dP.
 """
 import numpy as np
@@ -84,7 +84,7 @@ def check(sbp, x, kw, cu, prefix, sl, scale):
     errO = U * np.abs(want["O"]) + (U + 2.0 ** -11) * want["size"]
     for q in range(0, T, 256):
         keys = np.flatnonzero(see[q:q + 256].any(axis=0))
-        if len(keys) == 0 or keys[-1] // 128 - keys[0] // 128 < 4:
+        if len(keys) == 0 or keys[-1] // 128 - keys[0] // 128 < 3:
             errO[:, q:q + 256] = 0.0
     g = S.attention_backward(x["Q"], x["K"], x["V"], want["O"], x["dO"], lse, see, scale, cap, sl, errO)
     for k in "QKV":
@@ -153,6 +153,15 @@ def test_more_units_than_pairs(sbp):
     x = make(48, 8, 600, 128, seed=1)
     cu, sl, kw = options(48, [300, 290], None, 0.0, False)
     check(sbp, x, kw, cu, None, sl, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("softcap,alibi", [(30.0, False), (30.0, True), (0.0, True), (100.0, False)])
+def test_more_units_than_pairs_of_every_kernel(sbp, softcap, alibi):
+    # units of one, two, three and more blocks behind one another: score buffers and barriers
+    # start a unit at any of their phases
+    x = make(48, 8, 900, 64, seed=14, gain=2.0)
+    cu, sl, kw = options(48, [40, 90, 300, 20, 400], None, softcap, alibi)
+    check(sbp, x, kw, cu, None, sl, 0.125)
 
 
 @pytest.mark.parametrize("docs,softcap", [([16] * 20, 30.0), ([16] * 20, 0.0), ([3, 1, 7, 40, 2, 90], 50.0), ([400], 30.0)])
