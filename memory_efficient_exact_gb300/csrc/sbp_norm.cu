@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd(const BwdP p) {
     if (AHEAD) fetch(row + stride);
     s = row_sums(s, red, flip, p.lpr, p.wpr);
     flip ^= 1;
-    const float rstd = rsqrtf(s.x * inv_d + p.eps);
+    // a row past the last one is zeros: 0 times the infinite root of eps = 0 must not reach dgamma
+    const float rstd = row < p.T ? rsqrtf(s.x * inv_d + p.eps) : 0.f;
     const float c = rstd * rstd * (s.y * inv_d);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

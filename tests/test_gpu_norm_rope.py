@@ -81,6 +81,21 @@ def test_norm(sbp, T, d, residual, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,d", [(1, 8), (1, 256), (3, 16), (5, 136), (33, 1000), (70, 264), (1001, 512), (3, 2048), (9, 4096)])
+def test_norm_gradients_without_eps(sbp, T, d, dtype):
+    # rows of a block past the last one are rows of zeros, whose 1 / sqrt(0 + eps) is infinite at
+    # eps = 0: nothing of them may reach dgamma
+    dt, u = TY[dtype]
+    (R, dY), gamma = rows(T, d, T + d, dtype, 2)
+    b = sbp.rmsnorm_backward(dev(dY, dt), dev(R, dt), dev(gamma, dt), 0.0)
+    torch.cuda.synchronize()
+    sbp.check_status(b["status"])
+    g = S.rmsnorm_backward(dY, R, gamma, 0.0)
+    near("dX", host(b["dX"]), g["dX"], u * np.abs(g["dX"]) + 2.0 ** -17 * g["terms"])
+    near("dgamma", host(b["dgamma"]), g["dgamma"], (T + 128) * 2.0 ** -24 * g["dgamma_terms"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("T,d", [(1, 8), (5, 136), (33, 1000), (9, 5120), (3, 16384)])
 def test_norm_in_8_bits(sbp, T, d, dtype):
     dt, _ = TY[dtype]
