@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd(const BwdP p) {
 struct RingP {
   BwdP b;
   int stages;
+  int stall;   // test hook: a block's second row is never loaded, so that the wait for it runs out
   int32_t* status;
   uint64_t limit_ns;
 };
@@ -346,14 +347,17 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd_ring(const RingP a) 
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][MAXW];
   __shared__ uint64_t full[MAX_STAGES];
-  __shared__ int abort;
+  // A wait of this row (two rows in turn) ran out.  Set before the row's barrier and read behind
+  // it, so that every thread leaves at the same row: one flag for all rows could be set by a
+  // thread a row ahead, and threads would stop at different barriers.
+  __shared__ int late[2];
   const BwdP& p = a.b;
   const int step = blockDim.x, t0 = threadIdx.x;
   const uint32_t bytes = (uint32_t)(p.d * sizeof(E));   // of an operand's row
   const float inv_d = 1.f / (float)p.d;
   const int64_t stride = gridDim.x;
   auto load = [&](int64_t row, int slot) {   // by one thread
-    if (row >= p.T) return;
+    if (row >= p.T || (a.stall && row == blockIdx.x + stride)) return;
     uint8_t* dst = ring + (size_t)slot * 3 * bytes;
     tc::mbar_expect_tx(&full[slot], (p.dR ? 3u : 2u) * bytes);
     tc::bulk_load(tc::saddr(dst), static_cast<const E*>(p.R) + row * p.d, bytes, &full[slot]);
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd_ring(const RingP a) 
     if (p.dR) tc::bulk_load(tc::saddr(dst + 2 * bytes), static_cast<const E*>(p.dR) + row * p.d, bytes, &full[slot]);
   };
   if (t0 == 0) {
-    abort = 0;
+    late[0] = late[1] = 0;
     for (int i = 0; i < a.stages; ++i) tc::mbar_init(&full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     for (int i = 0; i < a.stages; ++i) load(blockIdx.x + i * stride, i);
@@ -379,11 +383,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd_ring(const RingP a) 
   __syncthreads();
   int flip = 0, slot = 0;
   uint32_t phase = 0;
+  bool out = false;
   for (int64_t row = blockIdx.x; row < p.T; row += stride) {
     const E* r = reinterpret_cast<const E*>(ring + (size_t)slot * 3 * bytes);
     const E *y = r + p.d, *q = y + p.d;
-    const bool ok = tc::wait_inl<false>(&full[slot], phase, &abort, a.limit_ns);
-    if (!ok) *(volatile int*)&abort = 1;
+    volatile int* mark = &late[flip];
+    if (!tc::wait_inl<false>(&full[slot], phase, mark, a.limit_ns)) *mark = 1;
     Raw<E> cr[NV], cy[NV];
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
@@ -404,7 +409,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd_ring(const RingP a) 
     }
     s = row_sums(s, red, flip, 32, step / 32);
     flip ^= 1;
-    if (*(volatile int*)&abort) break;   // every thread's, behind the barrier
+    out = *mark != 0;
+    if (out) break;
     // the row before this one has been read by all
     if (t0 == 0 && row != blockIdx.x) load(row + (a.stages - 1) * stride, slot ? slot - 1 : a.stages - 1);
     const float rstd = rsqrtf(s.x * inv_d + p.eps);
@@ -431,7 +437,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_bwd_ring(const RingP a) 
       phase ^= 1;
     }
   }
-  if (*(volatile int*)&abort) {   // the copies in flight come to rest before the block ends
+  if (out) {   // the copies in flight come to rest before the block ends
     if (t0 == 0) {
       atomicCAS(a.status, 0, SBP_ERR_TIMEOUT);
       for (int i = 0; i < a.stages; ++i) tc::wait_inl<false>(&full[i], phase ^ (i < slot ? 1u : 0u), nullptr, 200000000ull);
@@ -691,7 +697,7 @@ int sbp_rmsnorm_backward(const void* dY, const void* R, const void* gamma, const
   BwdP p{dY, R, gamma, dR, T, (int)d, (int)(d / 8), sh.lpr, sh.wpr, sh.rpb, eps, dX, part};
   cudaError_t e;
   if (L.stages) {
-    const RingP r{p, L.stages, dev_status, tc::wait_limit_ns()};
+    const RingP r{p, L.stages, tc::fault_stall_requested(), dev_status, tc::wait_limit_ns()};
     e = dtype == SBP_BF16 ? launch_ring<__nv_bfloat16>(r, sh, (unsigned)L.blocks, s)
                           : launch_ring<float>(r, sh, (unsigned)L.blocks, s);
   } else {

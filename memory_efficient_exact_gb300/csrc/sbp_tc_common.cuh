@@ -593,8 +593,8 @@ cudaError_t launch_early(void (*kernel)(P...), int grid, int threads, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Failure-detection test hook: SBP_FAULT_STALL=1 makes the next forward kernels stall
-// on purpose (read at every launch, so a test can switch it off again).  Together with a
+// Failure-detection test hook: SBP_FAULT_STALL=1 makes the next LM-head forward kernels
+// and norm backward kernels (rows of more than 2048 columns) stall on purpose (read at every launch, so a test can switch it off again).  Together with a
 // short SBP_WAIT_LIMIT_MS it exercises the bounded-wait abort path: status
 // SBP_ERR_TIMEOUT, copies drained, tensor memory freed, the context still usable.
 inline int fault_stall_requested() {

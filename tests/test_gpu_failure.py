@@ -50,3 +50,41 @@ def test_bounded_wait_runs_out_and_context_survives():
     assert res["first"] == sbp.ERR_TIMEOUT
     assert res["second"] == sbp.OK
     assert res["dW_err"] <= 2e-2 and res["loss_err"] <= 1e-3
+
+
+NORM_CHILD = r"""
+import json, os, sys
+sys.path.insert(0, sys.argv[1])
+import numpy as np, torch
+from memory_efficient_exact_gb300 import _build
+_build.build_library()
+from memory_efficient_exact_gb300 import sbp
+from oracle import sublayer as S
+g = torch.Generator(device="cuda").manual_seed(1)
+res = []
+for T, d, dt in [(1000, 2056, torch.bfloat16), (900, 5120, torch.bfloat16), (400, 16384, torch.bfloat16), (700, 5120, torch.float32)]:
+    n = lambda *s: torch.randn(s, generator=g, device="cuda").to(dt)
+    dY, R, gamma, dR = n(T, d), n(T, d), n(d), n(T, d)
+    os.environ["SBP_FAULT_STALL"] = "1"
+    a = sbp.rmsnorm_backward(dY, R, gamma, 1e-6, dR=dR); torch.cuda.synchronize()
+    os.environ["SBP_FAULT_STALL"] = "0"
+    b = sbp.rmsnorm_backward(dY, R, gamma, 1e-6, dR=dR); torch.cuda.synchronize()
+    f = lambda t: t.double().cpu().numpy()
+    w = S.rmsnorm_backward(f(dY), f(R), f(gamma), 1e-6, f(dR))
+    e = float(np.max(np.abs(f(b["dgamma"]) - w["dgamma"]) / w["dgamma_terms"]))
+    res.append([int(a["status"].item()), int(b["status"].item()), e])
+print(json.dumps(res))
+"""
+
+
+def test_norm_rows_that_never_arrive():
+    # the norm's ring of rows in shared memory: the wait for a row that nothing loads runs out, every
+    # thread leaves at that row, and the next call is right.  (dgamma: T + 128 roundings of 2^-24)
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    env = dict(os.environ, SBP_WAIT_LIMIT_MS="100")
+    r = subprocess.run([sys.executable, "-c", NORM_CHILD, ROOT], env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    from memory_efficient_exact_gb300 import sbp
+    for first, second, err in json.loads(r.stdout.strip().splitlines()[-1]):
+        assert first == sbp.ERR_TIMEOUT and second == sbp.OK and err <= (1000 + 128) * 2.0 ** -24
