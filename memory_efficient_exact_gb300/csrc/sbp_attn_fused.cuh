@@ -452,6 +452,10 @@ __device__ __forceinline__ void stage_bf16(const uint32_t (&ra)[32], float f, ui
 // each of the query heads [z0, z0 + nh); `plane` says where its dK and dV go.
 struct KvUnit { int zk, kp, b0, nbl, z0, nh, plane; };
 
+// The key blocks [j, j + n) that a unit of k_attn_q walks before its own, for the rows' sums of
+// P (dP - D) alone.
+struct SumBlocks { int j, n; };
+
 // Chunked causal attention: query i of the chunk [c0, c1) sees the keys 0 .. i.
 struct CausalScores {
   using Kv = KvP;
@@ -543,10 +547,8 @@ struct CausalScores {
                                                  const KvUnit& w) {
     tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, c, kw, w.zk);
   }
-  // A unit's first block: from -nj on where the blocks are walked twice, the first time for the
-  // rows' sums of P (dP - D) alone.
   static constexpr bool kSumFirst = false;
-  static __device__ __forceinline__ int q_first(int) { return 0; }
+  static __device__ __forceinline__ SumBlocks q_sums(Raw) { return SumBlocks{0, 0}; }
   // Whether the products that sum over hd have columns past 64; hd.
   template <class P>
   static __device__ __forceinline__ bool wide(const P&) { return true; }
@@ -995,6 +997,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, raw, z, qp, j0, nj);
+        const SumBlocks pre = S::q_sums(raw);
         raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
         if (nj == 0) continue;
         const uint32_t rs = lu & 1u;
@@ -1008,8 +1011,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
           tma_load_3d_pair(sb + Q_R + rs * 65536u + 32768 + hb * 16384, maps[Q_MO], fr, 64 * hb, qrow, z);
         }
         ++lu;
-        for (int n = S::q_first(nj); n < nj; ++n) {
-          const int krow = 128 * (j0 + (n < 0 ? n + nj : n)) + 64 * (int)rank;
+        for (int n = -pre.n; n < nj; ++n) {
+          const int krow = 128 * (n < 0 ? pre.j + pre.n + n : j0 + n) + 64 * (int)rank;
           const uint32_t s = g & 1u, ph = (g >> 1) ^ 1u;
           if (!wait_c(&c->kempty[s], ph, c, p.limit_ns)) { ok = false; break; }
           const uint32_t fk = mapa(saddr(&c->kfull[s]), 0), fv = mapa(saddr(&c->vfull[s]), 0);
@@ -1108,10 +1111,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, raw, z, qp, j0, nj);
+        const int first = -S::q_sums(raw).n;
         raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
         if (nj == 0) continue;
         const uint32_t rs = lu & 1u;
-        const int first = S::q_first(nj);
         const uint64_t q0 = dplus(dR, rs * 65536u), o0 = dplus(q0, 32768);
         // the tensor pipe always has the next block's S and dP to form while the epilogue
         // works on a block: S two blocks ahead, dP one
@@ -1178,13 +1181,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
   } else {
     const int q = warp & 3, cg = (warp - 2) >> 2;   // lane quadrant, 32-column group
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(32 * cg);
-    uint32_t g = 0, lu = 0, ns = 0;   // blocks, units, units that summed first
+    uint32_t g = 0, lu = 0, summed = 0;   // blocks, units, units that summed first
     bool ok = true;
     // the next unit's entry is loaded during this one, its rows' values while this one's dQ leaves
     int z, qp, j0, nj, qw, lo, hi;   // qw: this warp's first query; keys this thread's query sees
+    SumBlocks pre;
     float lz, Dq;
     auto rows_of = [&](int u, typename S::Raw r) {
       S::q_unit(p, u, r, z, qp, j0, nj);
+      pre = S::q_sums(r);
       qw = p.c0 + 256 * qp + 128 * (int)rank + 32 * q;
       const int qr = qw + lane;
       const bool v = u < p.n_units && qr < p.c1;
@@ -1220,7 +1225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       }
       float Dv = Dq;
       float2 sum = make_float2(0.f, 0.f);
-      for (int n = S::q_first(nj); n < nj; ++n, ++g) {
+      for (int n = -pre.n; n < nj; ++n, ++g) {
         if (!warp_wait_c(&c->tfull, g, c, p.limit_ns)) { ok = false; break; }
         tc_fence_after();
         uint32_t rs[32], rd[32], dw[16];   // dw: bf16 pairs of dS over this thread's 32 keys
@@ -1231,7 +1236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
         __syncwarp();
         if (lane == 0) arrive_leader(rank, &c->tempty_l, &c->tempty_r);   // dP is in registers: the next block's may be formed
         const bool sums = S::kSumFirst && n < 0;
-        const int kg = 128 * (j0 + (sums ? n + nj : n)) + 32 * cg;    // first key
+        const int kg = 128 * (sums ? pre.j + pre.n + n : j0 + n) + 32 * cg;    // first key
         const bool none = kg + 31 < lo0 || kg >= hi1, all = kg >= lo1 && kg + 31 < hi0;
         if constexpr (S::kSumFirst) {
           if (sums && all) q_block<S, false, true>(rs, rd, sc, lz2, Dv, kg, qr, lo, hi, dw, sum);
@@ -1258,15 +1263,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->sums[q]);
-            if (!warp_wait_f(&c->sums[q], ns++, c, p.limit_ns)) { ok = false; break; }
+            if (!warp_wait_f(&c->sums[q], summed++, c, p.limit_ns)) { ok = false; break; }
             tc_fence_after();
             __syncwarp();
             uint32_t part[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) tmem_ld1(trow + 128 * (g & 1u) + 32 * (k - cg), part[k]);
             tmem_ld_wait();
+            if (lo >= 128 * pre.j && hi <= 128 * (pre.j + pre.n)) {   // all of the row's keys were in the sum
 #pragma unroll
-            for (int k = 0; k < 4; ++k) Dv += __uint_as_float(part[k]);
+              for (int k = 0; k < 4; ++k) Dv += __uint_as_float(part[k]);
+            }
             if (cg == 0 && qr < p.c1) p.D[(int64_t)z * p.T + qr] = Dv;
           }
         }

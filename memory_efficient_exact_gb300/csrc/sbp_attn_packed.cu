@@ -61,15 +61,17 @@ struct PackedScores {
   using Scale = ScaleZ;
 
   static __device__ __forceinline__ int next_unit(int t, int pid, int npairs) { return pk::next_unit(t, pid, npairs); }
-  using Raw = int4;   // a unit's list entry: {qp, ja0, jb0 or jb1} or {kp, b0, nb}
+  using Raw = int4;   // a unit's list entry: {qp, ja0, jb0 or jb1, sums} or {kp, b0, nb}
   static __device__ __forceinline__ Raw kv_raw(const Kv& p, int u) {
     return u < p.n_units ? *reinterpret_cast<const int4*>(p.units + u / (p.parts * p.Hkv)) : make_int4(0, 0, 0, 0);
   }
   static __device__ __forceinline__ Raw q_raw(const Q& p, int u) {
     if (u >= p.n_units) return make_int4(0, 0, 0, 0);
     const int4* s = reinterpret_cast<const int4*>(p.units + u / p.H);
+    const int4 b = s[1];
     int4 a = s[0];
-    a.z = max(a.z, s[1].x);
+    a.z = max(a.z, b.x);
+    a.w = b.y;
     return a;
   }
   static __device__ __forceinline__ void kv_unit(const Kv& p, int u, Raw v, fa::KvUnit& w) {
@@ -175,13 +177,15 @@ struct PackedScores {
   }
   // D as dO . O is off by O's rounding to bf16, up to 2^-9 |dO| |O|, which dS = P (dP - D)
   // does not outgrow where a few keys hold nearly all of a row: at documents of 16 tokens and scores
-  // of +-30, dQ and dK were off by 0.9%, 0.25% with D = sum P dP.  Units of up to kSumBlocks
-  // blocks, which hold every document of up to 128 tokens, walk them once more for the sum of
-  // P (dP - D) and correct D by it, for themselves and for k_attn_kv; in longer ones the
-  // error stays below 0.46% without.  (All units twice would be two products in seven.)
+  // of +-30, dQ and dK were off by 0.9%, 0.25% with D = sum P dP.  So units walk some of their
+  // blocks once more for the sum of P (dP - D), and rows whose keys all lie in those correct D by
+  // it, for themselves and for k_attn_kv.  Units of up to kSumBlocks blocks walk all of them;
+  // longer ones those around their own rows, from one block before to one behind, where some
+  // row's keys all lie: what a document of up to 128 tokens sees is within them wherever it
+  // stands.  For other rows the error stays below 0.46%.  (All units twice would be two products in
+  // seven.)
   static constexpr bool kSumFirst = true;
-  static constexpr int kSumBlocks = 3;
-  static __device__ __forceinline__ int q_first(int nj) { return nj <= kSumBlocks ? -nj : 0; }
+  static __device__ __forceinline__ fa::SumBlocks q_sums(Raw v) { return fa::SumBlocks{v.w >> 3, v.w & 7}; }
   template <class P>
   static __device__ __forceinline__ bool wide(const P& p) { return p.hd > 64; }
   static __device__ __forceinline__ int width(const Q& p) { return p.hd; }
@@ -282,6 +286,22 @@ __global__ void __launch_bounds__(PREP_THREADS) k_packed_prep(const PrepP p) {
       // unbroken for any table: the second range starts within or right behind the first
       w.ja1 = min(max(ja[1], ja[0]), jb[0]);
       w.jb1 = max(jb[1], w.ja1);
+      const int j0 = w.ja0, j1 = max(w.jb0, w.jb1);
+      int s0 = j0, s1 = j1;
+      if (j1 - j0 > kSumBlocks) {
+        s0 = max(j0, 2 * i - 1);
+        s1 = min(j1, 2 * i + 3);
+        // the ends of the rows' intervals do not decrease: the first row that begins at s0 or
+        // behind, of the unit's first document or of the one after it, is the one to ask
+        int q = 256 * i, s, e, pre;
+        doc_of(p, q, s, e, pre);
+        if (s < 128 * s0) {
+          q = e;
+          if (q < min(256 * i + 256, n_tok)) doc_of(p, q, s, e, pre);
+        }
+        if (q >= min(256 * i + 256, n_tok) || upper_of(q, s, pre) > 128 * s1) s1 = s0;
+      }
+      w.sums = 8 * s0 + max(s1 - s0, 0);
       p.qraw[i] = w;
       if (p.kvraw) {
         const int k0 = 256 * i, k1 = min(k0 + 255, n_tok - 1);

@@ -20,7 +20,10 @@ namespace sbp {
 
 // Work of one unit of 256 queries: key blocks (of 128) [ja0, jb0) for its first 128
 // queries and [ja1, jb1) for the others; ja0 <= ja1 <= jb0 <= jb1 (no gap between them).
-struct __align__(16) PackedQUnit { int qp, ja0, jb0, ja1, jb1, pad[3]; };
+// sums: the blocks that the dQ kernel walks first (see kSumBlocks), 8 * the first + how many.
+struct __align__(16) PackedQUnit { int qp, ja0, jb0, ja1, jb1, sums, pad[2]; };
+// A unit of up to this many key blocks walks them all first.
+constexpr int kSumBlocks = 3;
 // Work of one unit of 256 keys: query blocks (of 128) [b0, b0 + nb).
 struct __align__(16) PackedKvUnit { int kp, b0, nb, pad; };
 

@@ -182,6 +182,41 @@ def test_peaked_rows_keep_their_gradients(sbp, docs, softcap):
         e = np.linalg.norm(host(b["d" + k]) - g["d" + k]) / np.linalg.norm(g["d" + k])
         assert e < 2.0 ** -8, (k, e)
 
+def _document(x, a, b):
+    """The operands of the document [a, b) alone."""
+    return {k: v[:, a:b] for k, v in x.items()}
+
+
+@pytest.mark.parametrize("lens,prefix,short", [
+    ([2000] + [16] * 16, None, range(1, 4)),                        # behind a long one, in its last unit
+    ([16] * 10 + [1500], [0] * 10 + [1500], range(10)),             # before one whose prefix reaches far ahead
+    ([700, 128, 300, 120, 900], [0, 128, 0, 120, 900], [1, 3]),     # between, over the ends of the units of 256 rows
+    ([1300, 40, 7, 1, 90, 128, 1200], None, [1, 2, 3, 4, 5])])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_short_documents_beside_long_ones_keep_their_gradients(sbp, lens, prefix, short, softcap):
+    # as test_peaked_rows_keep_their_gradients, whatever shares the unit with a short document
+    T, sc = sum(lens) + 30, 128 ** -0.5
+    x = make(4, 2, T, 128, seed=15, gain=4.0)
+    cu, _, kw = options(4, lens, prefix, softcap, False)
+    a = {k: dev(v) for k, v in x.items()}
+    f = sbp.attn_packed(a["Q"], a["K"], a["V"], sc, **kw)
+    b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], sc, **kw)
+    torch.cuda.synchronize()
+    sbp.check_status(b["status"])
+    err, size = dict.fromkeys("QKV", 0.0), dict.fromkeys("QKV", 0.0)
+    for s in short:
+        d = _document(x, cu[s], cu[s + 1])
+        see = S.visible(lens[s], None, None if prefix is None else [prefix[s]])
+        w = S.attention(d["Q"], d["K"], d["V"], see, sc, softcap, None)
+        g = S.attention_backward(d["Q"], d["K"], d["V"], w["O"], d["dO"], w["lse"], see, sc, softcap, None)
+        for k in "QKV":
+            got = host(b["d" + k])[:, cu[s]:cu[s + 1]]
+            err[k] += np.sum((got - g["d" + k]) ** 2)
+            size[k] += np.sum(g["d" + k] ** 2)
+    for k in "QKV":
+        e = np.sqrt(err[k] / size[k])
+        assert e < 2.0 ** -8, (k, e)
+
 
 def test_units_without_a_token(sbp):
     # most units are padding alone: their rows are cleared between and behind the others
