@@ -266,11 +266,23 @@ int sbp_attn_causal_backward_gqa(const void* Q, const void* K, const void* V, co
  * same arguments.
  * hd: a multiple of 8, at most 128.  scale > 0, finite, and scale / softcap too;
  * softcap 0 or in [1e-6, 256] (the scores' error grows with it, to 2^-14 there).  Fixed
- * order of every sum: the same call gives the same bits.  Workspace, stream and error rules as for
- * the LM-head calls (cu_seqlens and prefix_lens are read by the device only, so a captured
- * call follows their contents: a bad table sets SBP_ERR_SEQLENS); the workspace query
- * returns 0 for arguments no call accepts. */
+ * order of every sum: the same call with a workspace of the same size gives the same bits.
+ * Stream and error rules as for the LM-head calls (cu_seqlens and prefix_lens are read by the
+ * device only, so a captured call follows their contents: a bad table sets SBP_ERR_SEQLENS).
+ *
+ * Workspace, 256-byte aligned; the queries return 0 for arguments no call accepts.
+ *   sbp_attn_packed_forward_workspace_bytes: what the forward needs; it grows with T.
+ *   sbp_attn_packed_workspace_bytes: the backward's for the fastest schedule (enough for the
+ *     forward too).  Where few keys stand against many query heads (grouped heads, shorter
+ *     sequences) it holds fp32 sums of dK and dV, so that it may be smaller for a larger T.
+ *   sbp_attn_packed_workspace_bytes_lean: the smallest the backward accepts, without such
+ *     sums; it grows with T.  With a workspace between the two the backward shares a group's
+ *     heads out to as many sums as fit (dK and dV then differ in the rounding of their sums).
+ * So one workspace of the first or second query at the largest T serves the forward, and one of
+ * the second or third the backward, of every shorter batch of the same heads. */
 size_t sbp_attn_packed_workspace_bytes(int64_t H, int64_t Hkv, int64_t T, int64_t hd);
+size_t sbp_attn_packed_workspace_bytes_lean(int64_t H, int64_t Hkv, int64_t T, int64_t hd);
+size_t sbp_attn_packed_forward_workspace_bytes(int64_t H, int64_t Hkv, int64_t T, int64_t hd);
 int sbp_attn_packed_forward(const void* Q, const void* K, const void* V, const int32_t* cu_seqlens,
                             const int32_t* prefix_lens, int32_t n_seq, const float* slopes,
                             int64_t H, int64_t Hkv, int64_t T, int64_t hd, float scale, float softcap,

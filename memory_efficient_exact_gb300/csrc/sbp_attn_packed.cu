@@ -426,7 +426,7 @@ namespace {
 struct PackedLayout {
   size_t off_lo = 0, off_hi = 0, off_qlo = 0, off_qhi = 0, off_qraw = 0, off_qunits = 0, off_kvraw = 0,
          off_kvunits = 0, off_tail = 0, off_tq = 0, off_to = 0, off_tkv = 0, off_d = 0, off_pk = 0, off_pv = 0, total = 0;
-  int parts = 1, per_part = 1;   // of the backward's query-head groups (k_attn_kv)
+  int parts = 1, per_part = 1;   // of the backward's query-head groups (k_attn_kv); backward only, as what follows off_tkv
   Guards guards;   // checked build only
 };
 
@@ -452,10 +452,15 @@ int kv_heads_per_part(int64_t H, int64_t Hkv, int64_t T) {
   return (int)((group + parts - 1) / parts);
 }
 
-bool packed_layout(int64_t H, int64_t Hkv, int64_t T, int64_t hd, PackedLayout* L) {
+// Regions of a call's workspace.  The forward has its own, without what only the backward writes.
+// The backward with `per_part` query heads a unit of k_attn_kv: 0 for the choice above, the whole
+// group for the smallest workspace, whose size does not fall as T grows.
+enum class Pass { FORWARD, BACKWARD };
+bool packed_layout(int64_t H, int64_t Hkv, int64_t T, int64_t hd, Pass pass, int per_part, PackedLayout* L) {
   if (!packed_shape(H, Hkv, T, hd) || !packed_supported(H, T, hd)) return false;
   PackedLayout l;
   const size_t t = (size_t)std::max<int64_t>(T, 1), n = (t + 255) / 256;
+  const bool bwd = pass == Pass::BACKWARD;
   size_t o = 0;
   l.off_lo = take_region(o, t * sizeof(int32_t), l.guards);
   l.off_hi = take_region(o, t * sizeof(int32_t), l.guards);
@@ -463,26 +468,39 @@ bool packed_layout(int64_t H, int64_t Hkv, int64_t T, int64_t hd, PackedLayout* 
   l.off_qhi = take_region(o, t * sizeof(int32_t), l.guards);
   l.off_qraw = take_region(o, n * sizeof(PackedQUnit), l.guards);
   l.off_qunits = take_region(o, n * sizeof(PackedQUnit), l.guards);
-  l.off_kvraw = take_region(o, n * sizeof(PackedKvUnit), l.guards);
-  l.off_kvunits = take_region(o, n * sizeof(PackedKvUnit), l.guards);
   l.off_tail = take_region(o, sizeof(int32_t), l.guards);
-  l.off_tq = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
-  l.off_to = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
   l.off_tkv = take_region(o, (size_t)Hkv * 128 * hd * 2, l.guards);
-  l.off_d = take_region(o, (size_t)H * t * sizeof(float), l.guards);
-  l.per_part = kv_heads_per_part(H, Hkv, T);
-  l.parts = (int)((H / Hkv + l.per_part - 1) / l.per_part);
-  if (l.parts > 1) {
-    l.off_pk = take_region(o, (size_t)l.parts * Hkv * t * hd * sizeof(float), l.guards);
-    l.off_pv = take_region(o, (size_t)l.parts * Hkv * t * hd * sizeof(float), l.guards);
+  if (bwd) {
+    l.off_kvraw = take_region(o, n * sizeof(PackedKvUnit), l.guards);
+    l.off_kvunits = take_region(o, n * sizeof(PackedKvUnit), l.guards);
+    l.off_tq = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
+    l.off_to = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
+    l.off_d = take_region(o, (size_t)H * t * sizeof(float), l.guards);
+    l.per_part = per_part ? per_part : kv_heads_per_part(H, Hkv, T);
+    l.parts = (int)((H / Hkv + l.per_part - 1) / l.per_part);
+    if (l.parts > 1) {
+      l.off_pk = take_region(o, (size_t)l.parts * Hkv * t * hd * sizeof(float), l.guards);
+      l.off_pv = take_region(o, (size_t)l.parts * Hkv * t * hd * sizeof(float), l.guards);
+    }
   }
   l.total = o;
   *L = l;
   return true;
 }
+// The backward's layout in `bytes`: the fastest one that fits, the sums of a group shared out to
+// fewer parts where the workspace is smaller; else the smallest.
+bool packed_layout_within(int64_t H, int64_t Hkv, int64_t T, int64_t hd, size_t bytes, PackedLayout* L) {
+  if (!packed_layout(H, Hkv, T, hd, Pass::BACKWARD, 0, L)) return false;
+  for (int parts = L->parts; L->total > bytes && parts > 1;) {
+    const int64_t group = H / Hkv;
+    --parts;
+    packed_layout(H, Hkv, T, hd, Pass::BACKWARD, (int)((group + parts - 1) / parts), L);
+  }
+  return true;
+}
 
 // Shared checks of both directions; everything here runs before anything is enqueued.
-int packed_check(const PackedArgs& a, std::initializer_list<const void*> tensors, void* ws, size_t ws_bytes,
+int packed_check(const PackedArgs& a, std::initializer_list<const void*> tensors, Pass pass, void* ws, size_t ws_bytes,
                  PackedLayout* L) {
   if (!packed_shape(a.H, a.Hkv, a.T, a.hd) || !a.status) return SBP_ERR_INVALID_ARG;
   if (!(a.scale > 0.f) || std::isinf(a.scale) || !(a.softcap >= 0.f) || std::isinf(a.softcap))
@@ -491,7 +509,9 @@ int packed_check(const PackedArgs& a, std::initializer_list<const void*> tensors
   if (a.softcap > 0.f && (a.softcap < 1e-6f || a.softcap > 256.f)) return SBP_ERR_UNSUPPORTED;
   const tc::pk::Scale sc = tc::pk::make_scale(a.scale, a.softcap);
   if (std::isinf(sc.sl2) || std::isinf(sc.k)) return SBP_ERR_UNSUPPORTED;
-  if (!packed_layout(a.H, a.Hkv, a.T, a.hd, L)) return SBP_ERR_UNSUPPORTED;
+  if (pass == Pass::FORWARD ? !packed_layout(a.H, a.Hkv, a.T, a.hd, pass, 0, L)
+                            : !packed_layout_within(a.H, a.Hkv, a.T, a.hd, ws_bytes, L))
+    return SBP_ERR_UNSUPPORTED;
   for (const void* q : tensors) {
     if (!q && a.T > 0) return SBP_ERR_INVALID_ARG;
     if (!aligned16(q)) return SBP_ERR_ALIGNMENT;
@@ -632,7 +652,17 @@ extern "C" {
 
 size_t sbp_attn_packed_workspace_bytes(int64_t H, int64_t Hkv, int64_t T, int64_t hd) {
   PackedLayout L;
-  return packed_layout(H, Hkv, T, hd, &L) ? L.total : 0;
+  return packed_layout(H, Hkv, T, hd, Pass::BACKWARD, 0, &L) ? L.total : 0;
+}
+
+size_t sbp_attn_packed_workspace_bytes_lean(int64_t H, int64_t Hkv, int64_t T, int64_t hd) {
+  PackedLayout L;
+  return packed_layout_within(H, Hkv, T, hd, 0, &L) ? L.total : 0;
+}
+
+size_t sbp_attn_packed_forward_workspace_bytes(int64_t H, int64_t Hkv, int64_t T, int64_t hd) {
+  PackedLayout L;
+  return packed_layout(H, Hkv, T, hd, Pass::FORWARD, 0, &L) ? L.total : 0;
 }
 
 int sbp_attn_packed_forward(const void* Q, const void* K, const void* V, const int32_t* cu_seqlens,
@@ -642,7 +672,7 @@ int sbp_attn_packed_forward(const void* Q, const void* K, const void* V, const i
   PackedArgs a{Q, K, V, nullptr, nullptr, nullptr, cu_seqlens, prefix_lens, slopes, H, Hkv, T, hd, n_seq, scale,
                softcap, dev_status};
   PackedLayout L;
-  const int rc = packed_check(a, {Q, K, V, O, lse}, workspace, ws_bytes, &L);
+  const int rc = packed_check(a, {Q, K, V, O, lse}, Pass::FORWARD, workspace, ws_bytes, &L);
   if (rc != SBP_OK) return rc;
   NvtxRange nv("sbp_attn_packed_forward");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -668,7 +698,7 @@ int sbp_attn_packed_backward(const void* Q, const void* K, const void* V, const 
                              int32_t* dev_status, void* stream) {
   PackedArgs a{Q, K, V, O, dO, lse, cu_seqlens, prefix_lens, slopes, H, Hkv, T, hd, n_seq, scale, softcap, dev_status};
   PackedLayout L;
-  const int rc = packed_check(a, {Q, K, V, O, dO, lse, dQ, dK, dV}, workspace, ws_bytes, &L);
+  const int rc = packed_check(a, {Q, K, V, O, dO, lse, dQ, dK, dV}, Pass::BACKWARD, workspace, ws_bytes, &L);
   if (rc != SBP_OK) return rc;
   NvtxRange nv("sbp_attn_packed_backward");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -77,8 +77,10 @@ def _load() -> ctypes.CDLL:
     lib.sbp_attn_causal_backward_gqa.restype = C
     lib.sbp_attn_causal_backward_gqa.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, F, I64, P, P, P, C, P, SZ, P,
                                                  P]
-    lib.sbp_attn_packed_workspace_bytes.restype = SZ
-    lib.sbp_attn_packed_workspace_bytes.argtypes = [I64, I64, I64, I64]
+    for query in (lib.sbp_attn_packed_workspace_bytes, lib.sbp_attn_packed_workspace_bytes_lean,
+                  lib.sbp_attn_packed_forward_workspace_bytes):
+        query.restype = SZ
+        query.argtypes = [I64, I64, I64, I64]
     lib.sbp_attn_packed_forward.restype = C
     lib.sbp_attn_packed_forward.argtypes = [P, P, P, P, P, I32, P, I64, I64, I64, I64, F, F, P, P, P, SZ, P, P]
     lib.sbp_attn_packed_backward.restype = C
@@ -469,7 +471,17 @@ def attn_causal_backward(Q, K, V, O, dO, lse, scale, chunk, *, dQ=None, dK=None,
 
 
 def attn_packed_workspace_bytes(H: int, Hkv: int, T: int, hd: int) -> int:
+    """Bytes of the backward's workspace for its fastest schedule (the forward needs less)."""
     return int(_lib.sbp_attn_packed_workspace_bytes(H, Hkv, T, hd))
+
+
+def attn_packed_workspace_bytes_lean(H: int, Hkv: int, T: int, hd: int) -> int:
+    """The smallest workspace the backward accepts; it grows with T."""
+    return int(_lib.sbp_attn_packed_workspace_bytes_lean(H, Hkv, T, hd))
+
+
+def attn_packed_forward_workspace_bytes(H: int, Hkv: int, T: int, hd: int) -> int:
+    return int(_lib.sbp_attn_packed_forward_workspace_bytes(H, Hkv, T, hd))
 
 
 # The calls below are short enough for the host to matter (a norm of one token is a few
@@ -509,7 +521,7 @@ def _raw(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
-def _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream):
+def _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, query, stream):
     _on_device(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace)
     if Q.dim() != 3 or K.dim() != 3 or K.shape != V.shape:
         raise ValueError("shapes: Q [H, T, hd]; K, V [Hkv, T, hd]")
@@ -529,9 +541,9 @@ def _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream):
     if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (H,)):
         raise ValueError("slopes must be float32 [H]")
     if workspace is None:
-        n = _lib.sbp_attn_packed_workspace_bytes(H, Hkv, T, hd)
+        n = query(H, Hkv, T, hd)
         if n == 0:
-            raise SbpError(ERR_UNSUPPORTED, "sbp_attn_packed_workspace_bytes")
+            raise SbpError(ERR_UNSUPPORTED, "packed attention's workspace query")
         workspace = _empty(stream, n, torch.uint8, Q.device)
     return H, Hkv, T, hd, n_seq, workspace
 
@@ -544,7 +556,8 @@ def attn_packed(Q, K, V, scale, *, cu_seqlens=None, prefix_lens=None, slopes=Non
     Q [H, T, hd] bf16; K, V [Hkv, T, hd] bf16; cu_seqlens int32 [n_seq + 1] (None: one
     document); prefix_lens int32 [n_seq]; slopes fp32 [H].  Returns O [H, T, hd] bf16 and
     lse [H, T] fp32."""
-    H, Hkv, T, hd, n_seq, ws = _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream)
+    H, Hkv, T, hd, n_seq, ws = _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace,
+                                            _lib.sbp_attn_packed_forward_workspace_bytes, stream)
     dev = Q.device
     _on_device(Q, O, lse, status)
     if (O is not None and (O.shape != Q.shape or O.dtype != Q.dtype)) or (
@@ -563,7 +576,8 @@ def attn_packed_backward(Q, K, V, O, dO, lse, scale, *, cu_seqlens=None, prefix_
                          dQ=None, dK=None, dV=None, workspace=None, status=None, stream=None) -> dict:
     """Gradients of ``attn_packed`` (``sbp_attn_packed_backward``): dQ [H, T, hd] and dK, dV
     [Hkv, T, hd] in bf16.  O and lse are the forward's, with the same arguments."""
-    H, Hkv, T, hd, n_seq, ws = _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace, stream)
+    H, Hkv, T, hd, n_seq, ws = _packed_args(Q, K, V, cu_seqlens, prefix_lens, slopes, workspace,
+                                            _lib.sbp_attn_packed_workspace_bytes, stream)
     dev = Q.device
     _on_device(Q, O, dO, lse, dQ, dK, dV, status)
     for t in (O, dO, dQ):

@@ -343,6 +343,56 @@ def test_same_bits_on_a_stream_and_in_graphs(sbp):
             sbp.check_status(s)
 
 
+@pytest.mark.parametrize("softcap,alibi", [(0.0, False), (30.0, True)])
+def test_smaller_workspaces(sbp, softcap, alibi):
+    # a group's query heads shared out to one, some or as many sums of dK and dV as the workspace
+    # holds, the change of head inside a unit with its slope among them; guard bytes behind it
+    H, Hkv, T, hd = 16, 2, 600, 64
+    x = make(H, Hkv, T, hd, seed=17)
+    cu, sl, kw = options(H, [300, 5, 280], None, softcap, alibi)
+    full, lean = sbp.attn_packed_workspace_bytes(H, Hkv, T, hd), sbp.attn_packed_workspace_bytes_lean(H, Hkv, T, hd)
+    part = 2 * Hkv * T * hd * 4
+    assert full == lean + 8 * part              # (T hd is a multiple of the regions' 256 bytes)
+    see = S.visible(T, cu)
+    a = {k: dev(v) for k, v in x.items()}
+    want = S.attention(x["Q"], x["K"], x["V"], see, 0.125, softcap, sl)
+    errO = U * np.abs(want["O"]) + (U + 2.0 ** -11) * want["size"]
+    few = torch.full((sbp.attn_packed_forward_workspace_bytes(H, Hkv, T, hd) + 64,), 9, dtype=torch.uint8, device="cuda")
+    f = sbp.attn_packed(a["Q"], a["K"], a["V"], 0.125, workspace=few[:-64], **kw)
+    near("O", host(f["O"]), want["O"], U * np.abs(want["O"]) + (U + 2.0 ** -11) * want["size"])
+    assert torch.all(few[-64:] == 9)
+    for n in (full, full - 1, lean + 2 * part, lean + 2 * part - 1, lean, sbp.attn_packed_workspace_bytes(H, Hkv, 4 * T, hd)):
+        ws = torch.full((n + 64,), 9, dtype=torch.uint8, device="cuda")
+        b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], 0.125, workspace=ws[:n], **kw)
+        torch.cuda.synchronize()
+        sbp.check_status(b["status"])
+        assert torch.all(ws[n:] == 9)
+        g = S.attention_backward(x["Q"], x["K"], x["V"], want["O"], x["dO"], host(f["lse"]), see, 0.125, softcap, sl, errO)
+        for k in "QKV":
+            near(f"d{k} in {n}", host(b["d" + k]), g["d" + k], U * np.abs(g["d" + k]) + g["b" + k])
+    with pytest.raises(sbp.SbpError):
+        sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], 0.125, workspace=ws[:lean - 1], **kw)
+
+
+def test_one_workspace_for_shorter_batches(sbp):
+    # sized for the longest, where a unit takes a group's heads together, used where it would not
+    H, Hkv, hd = 32, 8, 64
+    ws = torch.empty(sbp.attn_packed_workspace_bytes(H, Hkv, 5120, hd), dtype=torch.uint8, device="cuda")
+    for T in (5120, 700, 40):
+        assert T == 5120 or ws.numel() < sbp.attn_packed_workspace_bytes(H, Hkv, 2560, hd)
+        x = make(H, Hkv, T, hd, seed=T) if T < 5120 else {k: np.zeros((H if k in "QdO" else Hkv, T, hd), np.float32) for k in ("Q", "K", "V", "dO")}
+        a = {k: dev(v) for k, v in x.items()}
+        f = sbp.attn_packed(a["Q"], a["K"], a["V"], 0.125, workspace=ws)
+        b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], 0.125, workspace=ws)
+        torch.cuda.synchronize()
+        sbp.check_status(b["status"])
+        c = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], 0.125)
+        # the same sums, in fp32 in another order, each rounded to bf16 once
+        for k in ("dQ", "dK", "dV"):
+            d = (b[k].double() - c[k].double()).abs()
+            assert torch.all(d <= 2 * U * c[k].double().abs() + 2.0 ** -16 * c[k].double().abs().max()), (T, k)
+
+
 def test_calls_on_two_streams_at_once(sbp):
     a = {k: dev(v) for k, v in make(16, 4, 900, 128, seed=6).items()}
     ref = _outputs(a)

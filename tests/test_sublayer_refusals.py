@@ -59,6 +59,23 @@ def test_attention_workspace(sbp):
     assert f(32, 8, 65536, 128) - f(32, 8, 32768, 128) <= 32768 * (16 + 4 * 32 + 1)
 
 
+@pytest.mark.parametrize("H,Hkv,hd", [(32, 8, 128), (32, 8, 64), (20, 4, 128), (16, 1, 128), (7, 7, 72), (48, 8, 8)])
+def test_attention_workspace_of_the_longest_serves_all(sbp, H, Hkv, hd):
+    # lengths on both sides of every change in how a group's heads are shared out
+    full, lean, fwd = (getattr(sbp, f"attn_packed_{n}") for n in ("workspace_bytes", "workspace_bytes_lean",
+                                                                  "forward_workspace_bytes"))
+    Ts = sorted({0, 1, 127, 128, 255, 256, 257} | {256 * n + r for n in range(1, 200, 3) for r in (0, 1, 255)} | {1 << 20})
+    for a, b in zip(Ts, Ts[1:]):
+        assert 0 < fwd(H, Hkv, a, hd) <= lean(H, Hkv, a, hd) <= full(H, Hkv, a, hd)
+        assert fwd(H, Hkv, a, hd) <= fwd(H, Hkv, b, hd) and lean(H, Hkv, a, hd) <= lean(H, Hkv, b, hd)
+        for f, backward in ((fwd, False), (lean, True)):
+            assert attn(sbp, backward, H=H, Hkv=Hkv, T=a, hd=hd, wsb=f(H, Hkv, a, hd) - 1) == sbp.ERR_WORKSPACE
+    # the forward: four interval ends, two unit lists (one entry for 256 tokens) and a block a head
+    assert fwd(H, Hkv, 8192, hd) <= 8192 * 16 + 64 * 32 + Hkv * 128 * hd * 2 + 9 * 256
+    for f in (full, lean, fwd):
+        assert f(H, Hkv, 16, hd + 4) == 0 and f(H, H + 1, 16, hd) == 0
+
+
 def norm(sbp, which, **kw):
     a = dict(X=0x1000, res=0x2000, g=0x3000, T=4, d=64, eps=1e-6, dt=0, R=0x4000, Y=0x5000, s=0x6000, dR=0x7000, dX=0x8000,
              dg=0x9000, ws=0x100000, wsb=1 << 30, st=0xb000)
