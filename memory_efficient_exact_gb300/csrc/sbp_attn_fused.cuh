@@ -338,7 +338,7 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
 // per-element test (it costs more than the math it guards).
 struct KvRows {
   int lo, hi;     // queries that see key kw + lane; fragment row 2 h + e is key kw + 16 h + 8 e + lane / 4
-  float key;      // fragment row 0
+  int key;        // fragment row 0
 };
 template <class S, bool MASK>
 __device__ __forceinline__ void kv_probs(uint32_t (&r)[16], int h, const float2 (&nlse)[4], const typename S::Scale& sc,
@@ -346,7 +346,7 @@ __device__ __forceinline__ void kv_probs(uint32_t (&r)[16], int h, const float2 
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int row = 16 * h + 8 * e;
-    const float fd = (float)q0 - (w.key + (float)row);
+    const float fd = (float)(q0 - (w.key + row));   // (past 2^24 the rows themselves are not fp32 values)
     int lo = 0, hi = 0;
     if (MASK) {
       lo = __shfl_sync(0xffffffffu, w.lo, row + (threadIdx.x & 31) / 4);
@@ -818,7 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       const int nblk = w.nh * w.nbl;
       const int kw = first_key(w), key = kw + lane;
       const int un = S::next_unit(rnd + 1, pid, npairs);
-      const KvRows rows{lo, hi, (float)(kw + lane / 4)};
+      const KvRows rows{lo, hi, kw + lane / 4};
       if constexpr (!S::kAddOut) {
         if (nblk == 0) {   // no query sees these keys
           S::store_zero(p, w.plane, key, 32 * cg);

@@ -218,6 +218,34 @@ def test_short_documents_beside_long_ones_keep_their_gradients(sbp, lens, prefix
         assert e < 2.0 ** -8, (k, e)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_distances_of_far_rows(sbp, softcap):
+    # rows past 2^24, which fp32 no longer tells from their neighbours: the bias goes by i - j
+    n, base = 300, 2 ** 24 + 1
+    T = base + n
+    cu = np.concatenate([np.arange(0, 2 ** 24 + 1, 256), [base, T]]).astype(np.int32)
+    x = make(1, 1, n, 8, seed=16)
+    sl = np.array([1.0], np.float32)
+    a = {k: torch.zeros((1, T, 8), dtype=torch.bfloat16, device="cuda") for k in x}
+    for k in x:
+        a[k][:, base:] = dev(x[k])
+    kw = dict(cu_seqlens=dev(cu, torch.int32), slopes=dev(sl, torch.float32), softcap=softcap)
+    f = sbp.attn_packed(a["Q"], a["K"], a["V"], 0.3, **kw)
+    b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], 0.3, **kw)
+    torch.cuda.synchronize()
+    sbp.check_status(f["status"])
+    sbp.check_status(b["status"])
+    see = S.visible(n)
+    want = S.attention(x["Q"], x["K"], x["V"], see, 0.3, softcap, sl)
+    lse = host(f["lse"][:, base:])
+    near("O", host(f["O"][:, base:]), want["O"], U * np.abs(want["O"]) + (U + 2.0 ** -11) * want["size"])
+    near("lse", lse, want["lse"], 2.0 ** -12 + 2.0 ** -20 * np.abs(want["lse"]))
+    errO = U * np.abs(want["O"]) + (U + 2.0 ** -11) * want["size"]
+    g = S.attention_backward(x["Q"], x["K"], x["V"], want["O"], x["dO"], lse, see, 0.3, softcap, sl, errO)
+    for k in "QKV":
+        near("d" + k, host(b["d" + k][:, base:]), g["d" + k], U * np.abs(g["d" + k]) + g["b" + k])
+
+
 def test_units_without_a_token(sbp):
     # most units are padding alone: their rows are cleared between and behind the others
     x = make(48, 8, 1100, 64, seed=11)
