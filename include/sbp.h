@@ -335,11 +335,13 @@ int sbp_rmsnorm_backward(const void* dY, const void* R, const void* gamma, const
  *   row_stride in elements, a multiple of 8 (a slice of a wider buffer is fine).
  *   positions [n_axes, T] int32 (device).  sections [n_axes] int32 (HOST memory): how many
  *   of the rot_dim / 2 pairs, in order, turn by each axis; they add up to rot_dim / 2.
- *   inv_freq [rot_dim / 2] fp64 (HOST memory, nullable): radians a position for each pair;
- *   NULL: theta^(-2p / rot_dim).
+ *   inv_freq [rot_dim / 2] fp64 (HOST memory, nullable): radians a position for each pair, up
+ *   to 2^40 in magnitude (SBP_ERR_UNSUPPORTED above); NULL: theta^(-2p / rot_dim).
  *   Pair p of the first rot_dim elements of a head is (p, p + rot_dim / 2), or, interleaved
  *   = 1, (2p, 2p + 1):  y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a,  a = position
- *   times inv_freq, exact for positions of any size.  Other elements and the value heads pass.
+ *   times inv_freq.  Whole turns leave a exactly and the rest is within 2^-24 of a turn of the
+ *   fp64 frequency's, for every int32 position; cos and sin are fp32.  Other elements and the
+ *   value heads pass.
  *   Q [H, T, hd], K, V [Hkv, T, hd] bf16.
  * Backward: dqkv from dQ (bf16), dK and dV (both kv_dtype: SBP_BF16, or SBP_FP32 as
  * sbp_attn_causal_backward leaves them), turned back; elements between the heads and

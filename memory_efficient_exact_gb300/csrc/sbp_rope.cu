@@ -3,9 +3,10 @@
 //
 // Pair p of a head's first rot_dim elements turns by the angle pos[axis(p)][t] f_p.  The
 // angle is kept as a fraction of a full turn in 64-bit fixed point, F_p = 2^64 f_p / (2 pi):
-// pos F_p wraps modulo 2^64 exactly as the angle wraps modulo 2 pi, so far positions lose
-// nothing (an fp32 angle at position 10^6 is off by 0.03), and the cosine and sine come from
-// the top 32 bits of the product, in half turns.
+// pos F_p wraps modulo 2^64 exactly as the angle wraps modulo 2 pi, so far positions cost no
+// precision (an fp32 angle at position 10^6 is off by 0.03), and the cosine and sine come from
+// the top 32 bits of the product, in half turns, rounded to fp32: 2^-25 of a turn.  F_p is within
+// 2^-63 of a turn of the fp64 frequency's (turns_of), 2^-32 at the ends of int32.
 //
 // Bound by device memory: every element is read and written once, 16 bytes at a time.  A
 // thread keeps the cosines and sines of its eight pairs of one token in registers and walks
@@ -149,6 +150,19 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeP p) {
   walk<BWD, IL, KV>(p, v0 + hg, v1, groups, tok, p.v, v0, t, e0, e1, false, cs, sn);
 }
 
+// f / (2 pi) less its whole part, in 2^-64 of a turn.  Whole turns of a step do not matter, and
+// they take bits: 1 / (2 pi) is two fp64 values, the product's rounding is kept (fma), and the whole
+// part leaves exactly, which makes the rest good to 2^-63 for |f| up to 2^40.  (With one product in
+// fp64 a frequency of 10^6 was off by 0.05 turns at position 2^31.)
+constexpr double MAX_FREQ = 1099511627776.0;   // 2^40
+uint64_t turns_of(double f) {
+  constexpr double C1 = 0x1.45f306dc9c883p-3, C2 = -0x1.6b01ec5417056p-57;   // 1 / (2 pi) = C1 + C2
+  const double a = std::fabs(f), hi = a * C1, lo = std::fma(a, C1, -hi) + a * C2;
+  const uint64_t t = (uint64_t)((hi - std::floor(hi)) * 18446744073709551616.0) +
+                     (uint64_t)(int64_t)std::floor(lo * 18446744073709551616.0);
+  return f < 0 ? 0u - t : t;
+}
+
 struct RopeArgs {
   const int32_t* pos; int32_t n_axes; const int32_t* sections; const double* inv_freq; double theta;
   int64_t rot_dim; int interleaved;
@@ -178,9 +192,8 @@ int run_rope(const RopeArgs& a, bool bwd, cudaStream_t s) {
   for (int i = 0; i < p.pairs; ++i) {
     const double f = a.inv_freq ? a.inv_freq[i] : std::pow(a.theta, -2.0 * i / (double)a.rot_dim);
     if (std::isnan(f) || std::isinf(f)) return SBP_ERR_INVALID_ARG;
-    const double turn = f / 6.283185307179586476925;
-    const double fx = (turn - std::floor(turn)) * 18446744073709551616.0;   // whole turns of a step do not matter
-    p.F[i] = fx >= 18446744073709551616.0 ? 0u : (uint64_t)fx;
+    if (std::fabs(f) > MAX_FREQ) return SBP_ERR_UNSUPPORTED;
+    p.F[i] = turns_of(f);
   }
   if (a.T > 0 && (!a.pos || !a.x || !a.q || (a.Hkv > 0 && (!a.k || !a.v)))) return SBP_ERR_INVALID_ARG;
   for (const void* q : {(const void*)a.x, (const void*)a.q, (const void*)a.k, (const void*)a.v})

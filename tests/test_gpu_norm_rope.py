@@ -210,6 +210,51 @@ def test_rope(sbp, T, H, Hkv, hd, rot, sections, il):
         near("dqkv", got[:H + Hkv], back, bound(back, dd[:H + Hkv].astype(np.float64)))
         near("dv", got[H + Hkv:], dd[H + Hkv:], 2.0 ** -8 * np.abs(dd[H + Hkv:]))
 
+def _turns(positions, freqs):
+    """position * frequency / (2 pi) less its whole part, [T, pairs]: in integers, 1 / (2 pi) to
+    300 bits from pi = 16 atan(1 / 5) - 4 atan(1 / 239)."""
+    bits = 320
+
+    def atan_inv(n):
+        t, s, k, sign = (1 << bits) // n, 0, 1, 1
+        while t:
+            s += sign * (t // k)
+            t //= n * n
+            k += 2
+            sign = -sign
+        return s
+
+    two_pi = 8 * (4 * atan_inv(5) - atan_inv(239))          # scaled by 2^bits
+    out = np.zeros((len(positions), len(freqs)))
+    for j, f in enumerate(freqs):
+        num, den = float(f).as_integer_ratio()
+        for i, p in enumerate(positions):
+            turn = ((int(p) * num) << (2 * bits)) // (den * two_pi)      # scaled by 2^bits
+            out[i, j] = ((turn % (1 << bits)) >> (bits - 64)) * 2.0 ** -64
+    return out
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_of_fast_frequencies_at_far_positions(sbp, interleaved):
+    # the angle keeps its precision however many turns it has made: within 2^-24 of a turn, 2^-21
+    # in radians, and the cosine and sine 2^-22
+    freqs = [1.0, 0.7310585786300049, 1e3, 12345.678, 1e6, -98765.4321, 2.0 ** 31 + 0.3, 2.0 ** 39]
+    pos = [0, 1, 2, 77777, 2 ** 24 + 1, 2 ** 31 - 1, -(2 ** 31), -123456789]
+    T, H, Hkv, hd = len(pos), 2, 1, 32
+    x = I.round_bf16(np.random.default_rng(5).standard_normal((T, 4 * hd)).astype(np.float32))
+    kw = dict(rot_dim=16, inv_freq=freqs, interleaved=interleaved)
+    p = dev(np.array([pos], np.int32), torch.int32)
+    f = sbp.rope_qkv(dev(x), p, H, Hkv, hd, **kw)
+    xh = x.reshape(T, 4, hd).transpose(1, 0, 2)[:3]
+    ang = 2 * np.pi * _turns(pos, freqs)
+    size = np.abs(xh).max(axis=2, keepdims=True) * 2
+    want = S.rope(xh, ang, interleaved)
+    got = np.concatenate([host(f["Q"]), host(f["K"])])
+    near("QK", got, want, 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * size)
+    b = sbp.rope_qkv_backward(f["Q"], f["K"], f["V"], p, **kw)
+    want = S.rope(got, ang, interleaved, inverse=True)
+    near("dqkv", host(b["dqkv"]).reshape(T, 4, hd).transpose(1, 0, 2)[:3], want, 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * size)
+
 
 def test_rope_rows_of_a_wider_buffer_and_own_frequencies(sbp):
     g = np.random.default_rng(0)

@@ -140,6 +140,14 @@ def test_rope(sbp, backward):
         assert rope(sbp, True, kvdt=5) == I
 
 
+@pytest.mark.parametrize("backward", [False, True])
+def test_rope_frequencies_past_the_angles_precision(sbp, backward):
+    # (a call without tokens reads its frequencies and enqueues nothing)
+    for f, code in ((2.0 ** 40, sbp.OK), (-(2.0 ** 40), sbp.OK), (2.0 ** 41, sbp.ERR_UNSUPPORTED), (-1e300, sbp.ERR_UNSUPPORTED)):
+        assert rope(sbp, backward, inv=[f] + [1.0] * 31, T=0) == code, f
+    assert rope(sbp, backward, theta=1e-300, T=0) == sbp.ERR_UNSUPPORTED
+
+
 def test_empty_calls_are_accepted_without_a_gpu(sbp):
     # T = 0 enqueues nothing where there is no status word to clear
     assert norm(sbp, "fwd", T=0) == sbp.OK and norm(sbp, "e4m3", T=0) == sbp.OK and norm(sbp, "expand", T=0) == sbp.OK
