@@ -264,6 +264,13 @@ int sbp_attn_causal_backward_gqa(const void* Q, const void* K, const void* V, co
  * (Within the documents a value that is not finite may reach rows of a neighbouring
  * document, as 0 times infinity.)  The backward takes O and lse of the forward with the
  * same arguments.
+ * Scores, exponentials and sums are fp32.  P and dS enter their products in bf16 (off by up to
+ * 2^-8 of each element), and D is that of the O given, which is bf16; rows whose keys lie near them
+ * (every document of up to 128 tokens) take D = sum_j P dP instead.
+ * The sums of O are divided by the row's at the end.  Before that they hold up to
+ * e^softcap sum |V| for a softcap of up to 50 and 2^16 sum |V| otherwise, which has to stay
+ * below 2^127: |V| up to 2^54 / T and 2^111 / T is safe (2^40 and 2^97 at 16384 tokens).  With a
+ * softcap of up to 50 they may also lose what is below 2^-53 of O.
  * hd: a multiple of 8, at most 128.  scale > 0, finite, and scale / softcap too;
  * softcap 0 or in [1e-6, 256] (the scores' error grows with it, to 2^-14 there).  Fixed
  * order of every sum: the same call with a workspace of the same size gives the same bits.
@@ -309,9 +316,11 @@ int sbp_rmsnorm_forward(const void* X, const void* residual, const void* gamma, 
 
 /* The same with Y in 8 bits: Y8 [T, d] e4m3 (one byte each) and scales [T, ceil(d / 128)]
  * fp32, one for each 128 columns of a row: Y ~ Y8 * scale, scale = max|Y| / 448 over the
- * block (1 for a block of zeros; at least 2^-126, so that it has an inverse).  Half the bytes of a bf16 Y, for the normalised input that
- * is kept between a sublayer's forward and its backward; sbp_e4m3_expand gives it back in
- * `dtype` (bf16 for sbp_mlp_swiglu_backward's X). */
+ * block (1 for a block of zeros; at least 2^-126, so that it has an inverse).  Y8 is Y times the
+ * scale's fp32 inverse, rounded: a value within 2^-22 of the middle between two e4m3 neighbours may
+ * take either.  Half the bytes of a bf16 Y, for the normalised input that is kept between a
+ * sublayer's forward and its backward; sbp_e4m3_expand gives it back in `dtype` (bf16 for
+ * sbp_mlp_swiglu_backward's X). */
 int sbp_rmsnorm_forward_e4m3(const void* X, const void* residual, const void* gamma, int64_t T, int64_t d,
                              float eps, int dtype, void* R, void* Y8, float* scales, void* stream);
 int sbp_e4m3_expand(const void* Y8, const float* scales, int64_t T, int64_t d, int dtype, void* Y,

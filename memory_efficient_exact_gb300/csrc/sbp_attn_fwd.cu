@@ -635,9 +635,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 namespace {
 
-// Largest cap that needs no running maximum: 2^x of scores within 50 log2(e) = 72 lies in
-// [2^-72, 2^72], which leaves 2^40 either way for V and for sums over any number of keys that
-// fits.  With a distance bias the scores less the row's largest bias take the place of x: none
+// Largest cap that needs no running maximum: 2^x of scores within 50 log2(e) = 72.1 lies in
+// [2^-72.2, 2^72.2], which leaves 2^55 for the sums of |V| over a row's keys and 2^-53 for the
+// smallest that counts (the header states both).  With a distance bias the scores less the row's largest bias take the place of x: none
 // is above 72, and the key with that bias (the row's own, or the farthest) is not below -72.
 // (8192 tokens in documents: cap 50 222 us, cap 50.5 314 us.)
 constexpr float kStaticCap = 50.f;

@@ -261,6 +261,26 @@ def test_running_maximum_is_raised(sbp):
     check(sbp, x, kw, cu, None, sl, 0.25)
 
 
+@pytest.mark.parametrize("softcap,alibi", [(50.0, False), (50.0, True), (30.0, False), (51.0, False), (0.0, False)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_values_at_the_ends_of_their_range(sbp, softcap, alibi, sign):
+    # rows whose scores are all at the cap, or all at its negative (without one: all at +-60), and V as
+    # large and as small as the header allows (2^54 / T, 2^111 / T; 2^-30: the sums lose 2^-53)
+    T, fixed = 512, 0.0 < softcap <= 50.0
+    x = make(2, 1, T, 64, seed=18)
+    x["Q"] = np.full_like(x["Q"], sign)
+    x["K"] = np.full_like(x["K"], 60.0 if softcap == 0 else 4096.0)     # scale 1/64: scores of +-60, +-4096
+    for k in (2.0 ** (45 if fixed else 102), 2.0 ** -30):
+        y = dict(x, V=I.round_bf16((np.clip(x["V"], -1, 1) * k).astype(np.float32)))
+        cu, sl, kw = options(2, [300, 212], None, softcap, alibi)
+        a = {n: dev(v) for n, v in y.items()}
+        f = sbp.attn_packed(a["Q"], a["K"], a["V"], 1.0 / 64, **kw)
+        torch.cuda.synchronize()
+        sbp.check_status(f["status"])
+        want = S.attention(y["Q"], y["K"], y["V"], S.visible(T, cu), 1.0 / 64, softcap, sl)
+        near("O", host(f["O"]), want["O"], U * np.abs(want["O"]) + (U + 2.0 ** -11) * want["size"] + 2.0 ** -53)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_padding_may_hold_anything(sbp, bad):
     H, Hkv, T, n = 4, 2, 400, 333
