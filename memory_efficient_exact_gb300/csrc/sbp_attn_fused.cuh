@@ -417,8 +417,8 @@ struct QP {
 // of a block), Q, dO (128 queries x half of hd), and the fp32 outputs dK, dV;
 // k_attn_q: Q, dO (128-query rows), K, V (64 keys of a block), K (128 keys x half of hd), and the
 // output dQ.
-// A policy may name one block (tail_block) whose rows the accumulating products take from
-// other maps (one block a head): Q, dO (in the place of the fp32 outputs) and K; and have
+// A policy with kTail names one block (tail_block) whose rows the accumulating products take from
+// other maps (one block a head): Q, dO (in the place of the fp32 outputs) and K; it may have
 // output maps of its own behind.
 enum { KV_MK, KV_MV, KV_MQA, KV_MOA, KV_MQB, KV_MOB, KV_MDK, KV_MDV, KV_MAPS, KV_MQT = KV_MDK, KV_MOT = KV_MDV,
        KV_MOUTK = KV_MAPS, KV_MOUTV };
@@ -427,6 +427,11 @@ template <int N>
 struct MapArray {   // in the kernel's parameters
   CUtensorMap m[N];
   __device__ __forceinline__ const CUtensorMap* operator[](int i) const { return &m[i]; }
+  template <int I>
+  __device__ __forceinline__ const CUtensorMap* at() const {
+    static_assert(I < N, "a map that this policy does not have");
+    return &m[I];
+  }
 };
 
 // Row `lane` of a warp's 32 x 32 staging block, times f: fp32 with the 128-byte swizzle, or
@@ -533,8 +538,7 @@ struct CausalScores {
   }
   // A probability times the factor of its score's gradient.
   static __device__ __forceinline__ float2 fold(float2 p, float2) { return p; }
-  template <class P>
-  static __device__ __forceinline__ int tail_block(const P&) { return -1; }
+  static constexpr bool kTail = false;
 
   // How a warp's 32 x 32 block of dV (t = 0) or dK (t = 1) leaves: whether it does, one row of
   // it into the warp's staging block, and the copy out of that (fp32, 128-byte swizzle; added
@@ -635,7 +639,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
       // dO and Q of each block, 128 queries x this CTA's half of hd
       prefetch_map(maps[KV_MQB]);
       prefetch_map(maps[KV_MOB]);
-      const int tail = S::tail_block(p);
+      int tail = -1;
+      if constexpr (S::kTail) tail = S::tail_block(p);
       uint32_t g = 0, gq = 0;
       bool ok = true;
       typename S::Raw raw = S::kv_raw(p, pid);
@@ -649,13 +654,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KV_THREADS, 1)
           if (!wait_c(&c->boempty, g ^ 1u, c, p.limit_ns)) { ok = false; break; }
           const uint32_t fo = mapa(saddr(&c->bofull), 0), fq = mapa(saddr(&c->bqfull), 0);
           if (rank == 0) mbar_expect_tx(&c->bofull, 2u * 16384u);
-          if (b == tail) tma_load_3d_pair(sb + KV_BO, maps[KV_MOT], fo, 64 * (int)rank, 0, z);
-          else tma_load_3d_pair(sb + KV_BO, maps[KV_MOB], fo, 64 * (int)rank, qrow, z);
+          const CUtensorMap *mo = maps[KV_MOB], *mq = maps[KV_MQB];
+          int row = qrow;
+          if constexpr (S::kTail)
+            if (b == tail) {
+              mo = maps.template at<KV_MOT>();
+              mq = maps.template at<KV_MQT>();
+              row = 0;
+            }
+          tma_load_3d_pair(sb + KV_BO, mo, fo, 64 * (int)rank, row, z);
           ++g;
           if (!wait_c(&c->bqempty, gq ^ 1u, c, p.limit_ns)) { ok = false; break; }
           if (rank == 0) mbar_expect_tx(&c->bqfull, 2u * 16384u);
-          if (b == tail) tma_load_3d_pair(sb + KV_BQ, maps[KV_MQT], fq, 64 * (int)rank, 0, z);
-          else tma_load_3d_pair(sb + KV_BQ, maps[KV_MQB], fq, 64 * (int)rank, qrow, z);
+          tma_load_3d_pair(sb + KV_BQ, mq, fq, 64 * (int)rank, row, z);
           ++gq;
         }
       }
@@ -1043,7 +1054,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     } else if (lane == 16) {
       // K of each key block, 128 keys x this CTA's half of hd (B of dQ += dS K)
       prefetch_map(maps[Q_MKB]);
-      const int tail = S::tail_block(p);
+      int tail = -1;
+      if constexpr (S::kTail) tail = S::tail_block(p);
       uint32_t g = 0;
       bool ok = true;
       typename S::Raw raw = S::q_raw(p, pid);
@@ -1056,12 +1068,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
           if (!wait_c(&c->yempty[s], (g >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
           const uint32_t fy = mapa(saddr(&c->yfull[s]), 0);
           if (rank == 0) mbar_expect_tx(&c->yfull[s], 2u * 16384u);
-          if (j0 + j == tail) {
-            // (Q_MKT is past the last map of policies without a tail block, whose tail is -1)
-            tma_load_3d_pair(sb + Q_Y + s * 16384u, maps[Q_MKT], fy, 64 * (int)rank, 0, z / p.group);
-          } else {
-            tma_load_3d_pair(sb + Q_Y + s * 16384u, maps[Q_MKB], fy, 64 * (int)rank, 128 * (j0 + j), z / p.group);
-          }
+          const CUtensorMap* mk = maps[Q_MKB];
+          int row = 128 * (j0 + j);
+          if constexpr (S::kTail)
+            if (j0 + j == tail) {
+              mk = maps.template at<Q_MKT>();
+              row = 0;
+            }
+          tma_load_3d_pair(sb + Q_Y + s * 16384u, mk, fy, 64 * (int)rank, row, z / p.group);
           ++g;
         }
       }

@@ -113,6 +113,7 @@ struct PackedScores {
                                                     int& hi1) {
     ends(lo, hi, lo0, lo1, hi0, hi1);
   }
+  static constexpr bool kTail = true;
   template <class P>
   static __device__ __forceinline__ int tail_block(const P& p) { return *p.tail; }
   template <class P>
