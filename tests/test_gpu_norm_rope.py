@@ -163,6 +163,28 @@ def test_norm_in_place_accumulate_and_repeat(sbp):
     sbp.check_status(g["status"])
 
 
+def test_norm_of_elements_past_2_31(sbp):
+    T, d = 2 ** 17 + 5, 16384
+    g = torch.Generator(device="cuda").manual_seed(4)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)
+    X, res, gamma, dY = n(T, d), n(T, d), n(d), n(T, d)
+    f = sbp.rmsnorm(X, gamma, 1e-6, residual=res)
+    q = sbp.rmsnorm_e4m3(X, gamma, 1e-6, residual=res)
+    e = sbp.e4m3_expand(q["Y8"], q["scales"])["Y"]
+    b = sbp.rmsnorm_backward(dY, f["R"], gamma, 1e-6)
+    torch.cuda.synchronize()
+    sbp.check_status(b["status"])
+    for s in (slice(0, 4), slice(2 ** 17 - 2, T)):
+        R = host(X[s]) + host(res[s])
+        Y, _ = S.rmsnorm(R, host(gamma), 1e-6)
+        near("R", host(f["R"][s]), R, 2.0 ** -8 * np.abs(R))
+        near("Y", host(f["Y"][s]), Y, (2.0 ** -8 + 2.0 ** -18) * np.abs(Y))
+        amax = np.abs(Y).reshape(len(Y), -1, 128).max(axis=2).repeat(128, axis=1)
+        near("Y8", host(e[s]), Y, np.maximum(2.0 ** -4 * np.abs(Y), 2.0 ** -10 * amax / 448) * (1 + 2.0 ** -7 + 2.0 ** -16) + 2.0 ** -8 * np.abs(Y))
+        w = S.rmsnorm_backward(host(dY[s]), host(f["R"][s]), host(gamma), 1e-6)
+        near("dX", host(b["dX"][s]), w["dX"], 2.0 ** -8 * np.abs(w["dX"]) + 2.0 ** -17 * w["terms"])
+
+
 ROPE = [(1, 1, 1, 16, 16, (8,), 0), (7, 8, 2, 128, 128, (64,), 0), (5, 3, 1, 64, 32, (16,), 1), (9, 4, 2, 128, 128, (16, 24, 24), 1),
         (33, 2, 2, 96, 48, (0, 24), 0), (3, 2, 1, 256, 256, (64, 32, 0, 32), 0), (130, 5, 1, 80, 80, (40,), 1),
         (4, 2, 0, 64, 64, (32,), 0), (6, 2, 1, 48, 0, (0,), 0)]
@@ -274,6 +296,25 @@ def test_rope_rows_of_a_wider_buffer_and_own_frequencies(sbp):
     torch.cuda.synchronize()
     assert torch.all(out[:, 256:] == 3.0)
     near("there and back", host(out[:, :256]), host(wide[:, :256]), 2.0 ** -5)
+
+
+def test_rope_of_elements_past_2_31(sbp):
+    T, H, Hkv, hd = 2 ** 18 + 3, 96, 16, 64
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn((T, (H + 2 * Hkv) * hd), generator=g, device="cuda", dtype=torch.bfloat16)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")[None]
+    f = sbp.rope_qkv(x, pos, H, Hkv, hd)
+    b = sbp.rope_qkv_backward(f["Q"], f["K"], f["V"], pos)
+    for s in (slice(0, 3), slice(T - 5, T)):
+        xh = host(x[s]).reshape(-1, H + 2 * Hkv, hd).transpose(1, 0, 2)
+        ang = S.rope_angles(host(pos[:, s]), [hd // 2], 10000.0 ** (-2.0 * np.arange(hd // 2) / hd))
+        want = S.rope(xh[:H + Hkv], ang, False)
+        got = np.concatenate([host(f["Q"][:, s]), host(f["K"][:, s])])
+        near("QK", got, want, 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * 16)
+        assert np.array_equal(host(f["V"][:, s]), xh[H + Hkv:])
+        back = S.rope(got, ang, False, inverse=True)
+        near("dqkv", host(b["dqkv"][s]).reshape(-1, H + 2 * Hkv, hd).transpose(1, 0, 2)[:H + Hkv], back,
+             2.0 ** -8 * np.abs(back) + 2.0 ** -20 * 16)
 
 
 def test_streams_and_graphs(sbp):

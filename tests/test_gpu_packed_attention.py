@@ -502,3 +502,77 @@ def test_no_tokens(sbp):
     sbp.check_status(f["status"])
     sbp.check_status(b["status"])
     assert f["O"].shape == (4, 0, 64) and b["dK"].shape == (2, 0, 64)
+
+
+def _check_document(name, x, f, b, rows, heads, z, scale, softcap, sl):
+    """Outputs of the document `rows` and the query heads that share key / value head z."""
+    a, e = rows
+    cut = lambda t, h: host(t[h, a:e])
+    kv = slice(z, z + 1)
+    q, dO = cut(x["Q"], heads), cut(x["dO"], heads)
+    k, v = cut(x["K"], kv), cut(x["V"], kv)
+    see = np.tril(np.ones((e - a, e - a), dtype=bool))
+    w = S.attention(q, k, v, see, scale, softcap, None if sl is None else sl[heads])
+    near(name + " O", cut(f["O"], heads), w["O"], U * np.abs(w["O"]) + (U + 2.0 ** -11) * w["size"])
+    lse = cut(f["lse"], heads)
+    near(name + " lse", lse, w["lse"], 2.0 ** -12 + 2.0 ** -20 * np.abs(w["lse"]))
+    errO = U * np.abs(w["O"]) + (U + 2.0 ** -11) * w["size"]
+    g = S.attention_backward(q, k, v, w["O"], dO, lse, see, scale, softcap, None if sl is None else sl[heads], errO)
+    near(name + " dQ", cut(b["dQ"], heads), g["dQ"], U * np.abs(g["dQ"]) + g["bQ"])
+    for t in "KV":
+        near(f"{name} d{t}", cut(b["d" + t], kv), g["d" + t], U * np.abs(g["d" + t]) + g["b" + t])
+
+
+@pytest.mark.parametrize("softcap,alibi", [(0.0, False), (30.0, True)])
+def test_a_training_step_of_8192_tokens(sbp, softcap, alibi):
+    # enough units that one of them walks all four query heads of a group, each with its slope, and
+    # dK and dV are summed on chip; documents are independent, so some of them stand for all
+    H, Hkv, T, hd, lens = 32, 8, 8192, 128, [1024, 2048, 777, 1, 2500, 1800]
+    assert sbp.attn_packed_workspace_bytes(H, Hkv, T, hd) == sbp.attn_packed_workspace_bytes_lean(H, Hkv, T, hd)
+    cu, sl, kw = options(H, lens, None, softcap, alibi)
+    x = {k: dev(v) for k, v in make(H, Hkv, T, hd, seed=19, gain=2.0).items()}
+    f = sbp.attn_packed(x["Q"], x["K"], x["V"], hd ** -0.5, **kw)
+    b = sbp.attn_packed_backward(x["Q"], x["K"], x["V"], f["O"], x["dO"], f["lse"], hd ** -0.5, **kw)
+    torch.cuda.synchronize()
+    sbp.check_status(f["status"])
+    sbp.check_status(b["status"])
+    for z, docs in ((0, (0, 2)), (5, (3, 4)), (7, (2, 5))):
+        for d in docs:
+            _check_document(f"head {z} document {d}", x, f, b, (cu[d], cu[d + 1]), slice(4 * z, 4 * z + 4), z, hd ** -0.5,
+                            softcap, sl)
+    end = cu[-1]
+    assert torch.all(f["O"][:, end:] == 0) and torch.all(b["dQ"][:, end:] == 0) and torch.all(b["dK"][:, end:] == 0)
+
+
+def test_elements_past_2_31(sbp):
+    H, Hkv, hd, n = 16, 2, 128, 512
+    T = 2 ** 20 + 300
+    assert (H - 1) * T * hd < 2 ** 31 < H * T * hd
+    g = torch.Generator(device="cuda").manual_seed(20)
+    r = lambda h: torch.randn((h, T, hd), generator=g, device="cuda", dtype=torch.bfloat16)
+    x = dict(Q=r(H), K=r(Hkv), V=r(Hkv), dO=r(H))
+    cu, sl, kw = options(H, [n] * (T // n) + [T % n], None, 0.0, True)
+    f = sbp.attn_packed(x["Q"], x["K"], x["V"], hd ** -0.5, **kw)
+    b = sbp.attn_packed_backward(x["Q"], x["K"], x["V"], f["O"], x["dO"], f["lse"], hd ** -0.5, **kw)
+    torch.cuda.synchronize()
+    sbp.check_status(f["status"])
+    sbp.check_status(b["status"])
+    for z, d in ((0, 0), (1, 1000), (1, len(cu) - 3), (1, len(cu) - 2)):
+        _check_document(f"head {z} document {d}", x, f, b, (cu[d], cu[d + 1]), slice(8 * z, 8 * z + 8), z, hd ** -0.5, 0.0, sl)
+
+
+def test_forward_of_the_causal_backward(sbp):
+    # attn_causal_backward takes O and lse as a forward saves them: this one, of one document
+    H, Hkv, T, hd = 4, 2, 600, 128
+    x = make(H, Hkv, T, hd, seed=21)
+    a = {k: dev(v) for k, v in x.items()}
+    f = sbp.attn_packed(a["Q"], a["K"], a["V"], hd ** -0.5)
+    b = sbp.attn_causal_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], hd ** -0.5, 256)
+    torch.cuda.synchronize()
+    sbp.check_status(b["status"])
+    see = S.visible(T)
+    w = S.attention(x["Q"], x["K"], x["V"], see, hd ** -0.5)
+    errO = U * np.abs(w["O"]) + (U + 2.0 ** -11) * w["size"]
+    g = S.attention_backward(x["Q"], x["K"], x["V"], w["O"], x["dO"], host(f["lse"]), see, hd ** -0.5, errO=errO)
+    for k in "QKV":
+        near("d" + k, host(b["d" + k]), g["d" + k], U * np.abs(g["d" + k]) + g["b" + k])
