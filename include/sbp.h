@@ -265,8 +265,9 @@ int sbp_attn_causal_backward_gqa(const void* Q, const void* K, const void* V, co
  * document, as 0 times infinity.)  The backward takes O and lse of the forward with the
  * same arguments.
  * Scores, exponentials and sums are fp32.  P and dS enter their products in bf16 (off by up to
- * 2^-8 of each element), and D is that of the O given, which is bf16; rows whose keys lie near them
- * (every document of up to 128 tokens) take D = sum_j P dP instead.
+ * 2^-8 of each element).  D is that of the O given, which is bf16, but for rows it would be too
+ * coarse for, in documents of up to 128 tokens and where O is large against V: they take
+ * D = sum_j P dP instead.
  * The sums of O are divided by the row's at the end.  Before that they hold up to
  * e^softcap sum |V| for a softcap of up to 50 and 2^16 sum |V| otherwise, which has to stay
  * below 2^127: |V| up to 2^54 / T and 2^111 / T is safe (2^40 and 2^97 at 16384 tokens).  With a

@@ -552,7 +552,9 @@ struct CausalScores {
     tma_reduce_add_3d(maps[t ? KV_MDK : KV_MDV], stg, c, kw, w.zk);
   }
   static constexpr bool kSumFirst = false;
-  static __device__ __forceinline__ SumBlocks q_sums(Raw) { return SumBlocks{0, 0}; }
+  struct Large {};
+  static __device__ __forceinline__ Large q_large(const QP&, int, Raw) { return Large{}; }
+  static __device__ __forceinline__ SumBlocks q_sums(Raw, Large) { return SumBlocks{0, 0}; }
   // Whether the products that sum over hd have columns past 64; hd.
   template <class P>
   static __device__ __forceinline__ bool wide(const P&) { return true; }
@@ -1005,12 +1007,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       uint32_t g = 0, gv = 0, lu = 0;   // key blocks (K; V) and units loaded so far
       bool ok = true;
       typename S::Raw raw = S::q_raw(p, pid);
+      typename S::Large large = S::q_large(p, pid, raw);   // the next unit's, loaded once its entry is there
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, raw, z, qp, j0, nj);
-        const SumBlocks pre = S::q_sums(raw);
-        raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
-        if (nj == 0) continue;
+        const SumBlocks pre = S::q_sums(raw, large);
+        const int un = S::next_unit(rnd + 1, pid, npairs);
+        raw = S::q_raw(p, un);
+        if (nj == 0) {
+          large = S::q_large(p, un, raw);
+          continue;
+        }
         const uint32_t rs = lu & 1u;
         if (!wait_c(&c->rempty[rs], (lu >> 1) ^ 1u, c, p.limit_ns)) { ok = false; break; }
         const uint32_t fr = mapa(saddr(&c->rfull[rs]), 0);
@@ -1038,6 +1045,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
           for (int hb = 0; hb < 2; ++hb)
             tma_load_3d_pair(sb + Q_V + s * 16384u + hb * 8192, maps[Q_MVA], fv, 64 * hb, krow, z / p.group);
           ++gv;
+          if (n == -pre.n) large = S::q_large(p, un, raw);
         }
       }
       if (!ok) {   // wait for the copies in flight
@@ -1122,12 +1130,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
       auto k_of = [&](uint32_t gg, bool need) { return phase_f(&c->kfull[gg & 1u], gg >> 1, need); };
       auto v_of = [&](uint32_t gg) { return phase_f(&c->vfull[gg & 1u], gg >> 1); };
       typename S::Raw raw = S::q_raw(p, pid);
+      typename S::Large large = S::q_large(p, pid, raw);
       for (int rnd = 0, u = pid; u < p.n_units && ok; u = S::next_unit(++rnd, pid, npairs)) {
         int z, qp, j0, nj;
         S::q_unit(p, u, raw, z, qp, j0, nj);
-        const int first = -S::q_sums(raw).n;
-        raw = S::q_raw(p, S::next_unit(rnd + 1, pid, npairs));
-        if (nj == 0) continue;
+        const int first = -S::q_sums(raw, large).n, un = S::next_unit(rnd + 1, pid, npairs);
+        raw = S::q_raw(p, un);
+        if (nj == 0) {
+          large = S::q_large(p, un, raw);
+          continue;
+        }
         const uint32_t rs = lu & 1u;
         const uint64_t q0 = dplus(dR, rs * 65536u), o0 = dplus(q0, 32768);
         // the tensor pipe always has the next block's S and dP to form while the epilogue
@@ -1180,6 +1192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
             if (more) scores(g + 2, q0);
           }
           __syncwarp();
+          if (n == first) large = S::q_large(p, un, raw);
           gy += n >= 0;
         }
         if (!ok) break;
@@ -1199,11 +1212,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
     bool ok = true;
     // the next unit's entry is loaded during this one, its rows' values while this one's dQ leaves
     int z, qp, j0, nj, qw, lo, hi;   // qw: this warp's first query; keys this thread's query sees
-    SumBlocks pre;
+    typename S::Raw entry;
+    typename S::Large large;
     float lz, Dq;
     auto rows_of = [&](int u, typename S::Raw r) {
       S::q_unit(p, u, r, z, qp, j0, nj);
-      pre = S::q_sums(r);
+      entry = r;
+      large = S::q_large(p, u, r);
       qw = p.c0 + 256 * qp + 128 * (int)rank + 32 * q;
       const int qr = qw + lane;
       const bool v = u < p.n_units && qr < p.c1;
@@ -1237,6 +1252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q_THREADS, 1)
           continue;
         }
       }
+      const SumBlocks pre = S::q_sums(entry, large);
       float Dv = Dq;
       float2 sum = make_float2(0.f, 0.f);
       for (int n = -pre.n; n < nj; ++n, ++g) {

@@ -35,6 +35,7 @@ struct QParams {
   float* D;
   const int32_t *lo, *hi;
   const PackedQUnit* units;
+  const uint32_t* large;   // [H, n_units / H]
   const int32_t* tail;
   __nv_bfloat16* dQ;
   int32_t* status;
@@ -45,6 +46,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+constexpr int D_ROWS = 64;   // rows of D a block of the preparing kernel: one byte of `large`
 
 // Score policy (see CausalScores): documents, prefixes, cap and distance bias; the units
 // and intervals come from the preparing kernel, and every output element is written once,
@@ -183,11 +186,23 @@ struct PackedScores {
   // it, for themselves and for k_attn_kv.  Units of up to kSumBlocks blocks walk all of them;
   // longer ones those around their own rows, from the first document that lies in the unit or in the
   // block before it to one block behind the unit: what a document of up to 128 tokens sees is
-  // within them wherever it stands.  For other rows the error stays below 0.46%.  (All units twice
-  // would be two products in seven; documents of 2000, 3, 1700 and 200 tokens, capped and biased,
-  // forward and backward: 353 us without the longer units' part, 359 with it.)
+  // within them wherever it stands.  Of the rows with more keys those need it whose O is large
+  // against V (over half of it in norm): few keys hold the row, or V has a part in common that
+  // dP - D does not see.  A unit with such a row walks all of its blocks first; the rest of the rows
+  // add less than a tenth to the error that the two roundings to bf16 leave (0.24% in norm).
+  // All units twice would be two products in seven: 16384 tokens forward and backward 7640 us, 6220
+  // with this rule (normal inputs: no unit but the first).  4099 tokens with scores of +-10, a cap
+  // and a bias: 429 us, 359 where long units look at their short documents alone, whose error is
+  // then 0.38%; values with a mean of four times their deviation: 0.9% without.
   static constexpr bool kSumFirst = true;
-  static __device__ __forceinline__ fa::SumBlocks q_sums(Raw v) { return fa::SumBlocks{v.w >> 3, v.w & 7}; }
+  using Large = uint32_t;   // loaded once the unit's entry is there, looked at when the unit begins
+  static __device__ __forceinline__ Large q_large(const Q& p, int u, Raw v) {
+    static_assert(D_ROWS == 64, "four bytes a unit");
+    return u < p.n_units ? p.large[(int64_t)(u % p.H) * (p.n_units / p.H) + v.x] : 0u;
+  }
+  static __device__ __forceinline__ fa::SumBlocks q_sums(Raw v, Large large) {
+    return fa::SumBlocks{large ? v.y : v.w >> 3, large ? v.z - v.y : v.w & 7};
+  }
   template <class P>
   static __device__ __forceinline__ bool wide(const P& p) { return p.hd > 64; }
   static __device__ __forceinline__ int width(const Q& p) { return p.hd; }
@@ -213,10 +228,11 @@ struct PrepP {
   const __nv_bfloat16* tsrc[3];
   __nv_bfloat16* tdst[3];
   int heads[3];
-  // D = dO . O of the backward
-  const __nv_bfloat16 *O, *dO;
-  int64_t rows;
+  // D = dO . O of the backward, and which rows have an O that is large against V
+  const __nv_bfloat16 *O, *dO, *V;
+  int group;
   float* D;
+  uint8_t* large;
   int32_t* status;
 };
 
@@ -381,24 +397,77 @@ __global__ void __launch_bounds__(PREP_THREADS) k_packed_prep(const PrepP p) {
     }
     return;
   }
-  // D: sixteen lanes a row, 16 bytes a lane and operand (hd <= 128)
-  const int64_t r = ((int64_t)blockIdx.x - 1 - p.token_blocks - p.tail_blocks) * (PREP_THREADS / 16) + tid / 16;
-  const int c = 8 * (tid % 16);
-  float acc = 0.f;
-  if (r < p.rows && c < p.hd) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p.O + r * p.hd + c);
-    const uint4 b = *reinterpret_cast<const uint4*>(p.dO + r * p.hd + c);
-    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+  // D: 64 rows of a head, sixteen lanes a row, 16 bytes a lane and operand (hd <= 128)
+  constexpr int K = D_ROWS / 16;
+  static_assert(PREP_THREADS == 256 && 256 % D_ROWS == 0, "sixteen rows at a time, whole blocks a unit");
+  const int blk = (int)blockIdx.x - 1 - p.token_blocks - p.tail_blocks, per_head = 256 / D_ROWS * p.n_units;
+  const int h = blk / per_head, t0 = D_ROWS * (blk - h * per_head), c = 8 * (tid % 16);
+  if (t0 >= p.T) {
+    if (tid == 0) p.large[blk] = 0;
+    return;
+  }
+  uint4 a[K] = {}, b[K] = {}, v = {};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int t = t0 + tid / 16 + 16 * k;
+    if (t < p.T && c < p.hd) {
+      const int64_t r = ((int64_t)h * p.T + t) * p.hd + c;
+      a[k] = *reinterpret_cast<const uint4*>(p.O + r);
+      b[k] = *reinterpret_cast<const uint4*>(p.dO + r);
+      if (k == 0) v = *reinterpret_cast<const uint4*>(p.V + ((int64_t)(h / p.group) * p.T + t) * p.hd + c);
+    }
+  }
+  const int n_tok = doc_end(p);
+  float acc[K] = {}, o2[K] = {}, v2 = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const uint32_t av[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, bv[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 x = unpack_bf16(av[i]), y = unpack_bf16(bv[i]);
-      acc = fmaf(x.x, y.x, acc);
-      acc = fmaf(x.y, y.y, acc);
+      acc[k] = fmaf(x.x, y.x, acc[k]);
+      acc[k] = fmaf(x.y, y.y, acc[k]);
+      o2[k] = fmaf(x.x, x.x, fmaf(x.y, x.y, o2[k]));
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
+      acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+      o2[k] += __shfl_xor_sync(0xffffffffu, o2[k], o);
     }
   }
+  // |O|^2 > |V|^2 / 4, with the mean of the first sixteen rows for |V|^2; rows that their unit's
+  // first walk covers anyway do not count
+  __shared__ float norms[8];
+  const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int o = 8; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (r < p.rows && c == 0) p.D[r] = acc;
+  for (int i = 0; i < 4; ++i) {
+    const float2 z = unpack_bf16(vv[i]);
+    if (t0 + tid / 16 < n_tok) v2 = fmaf(z.x, z.x, fmaf(z.y, z.y, v2));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v2 += __shfl_xor_sync(0xffffffffu, v2, o);
+  if (tid % 32 == 0) norms[tid / 32] = v2;
+  __syncthreads();
+  bool need = false;
+  if (c == 0) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += norms[i];
+    const float count = (float)(4 * min(16, n_tok - t0));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int t = t0 + tid / 16 + 16 * k;
+      if (t < p.T) p.D[(int64_t)h * p.T + t] = acc[k];
+      if (t < n_tok && o2[k] * count > sum) {
+        int s, e, pre;
+        doc_of(p, t, s, e, pre);
+        const int unit = t / 256;
+        need = need || s < 128 * (2 * unit - 1) || upper_of(t, s, pre) > 128 * (2 * unit + 3);
+      }
+    }
+  }
+  const int any = __syncthreads_or(need);
+  if (tid == 0) p.large[blk] = any ? 1 : 0;
 }
 
 // dK and dV from the parts' fp32 sums, in the parts' order: eight elements a thread.
@@ -428,7 +497,7 @@ namespace {
 
 struct PackedLayout {
   size_t off_lo = 0, off_hi = 0, off_qlo = 0, off_qhi = 0, off_qraw = 0, off_qunits = 0, off_kvraw = 0,
-         off_kvunits = 0, off_tail = 0, off_tq = 0, off_to = 0, off_tkv = 0, off_d = 0, off_pk = 0, off_pv = 0, total = 0;
+         off_kvunits = 0, off_tail = 0, off_tq = 0, off_to = 0, off_tkv = 0, off_d = 0, off_large = 0, off_pk = 0, off_pv = 0, total = 0;
   int parts = 1, per_part = 1;   // of the backward's query-head groups (k_attn_kv); backward only, as what follows off_tkv
   Guards guards;   // checked build only
 };
@@ -439,7 +508,7 @@ bool packed_shape(int64_t H, int64_t Hkv, int64_t T, int64_t hd) {
 // 16-byte rows; the kernels' tile is 128 wide; int32 row numbers
 bool packed_supported(int64_t H, int64_t T, int64_t hd) {
   return hd % 8 == 0 && hd <= 128 && T <= (int64_t)1 << 30 && H <= (int64_t)1 << 20 &&
-         H * ((T + 255) / 256) <= INT32_MAX / 2 && (H * T + 15) / 16 + T / 256 < INT32_MAX / 2;
+         H * (256 / tc::pk::D_ROWS * ((T + 255) / 256) + 3) + T / 256 < INT32_MAX / 2;   // blocks of the preparing kernel
 }
 
 // Query heads of a group that one k_attn_kv unit walks: all of them where that leaves two units
@@ -479,6 +548,7 @@ bool packed_layout(int64_t H, int64_t Hkv, int64_t T, int64_t hd, Pass pass, int
     l.off_tq = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
     l.off_to = take_region(o, (size_t)H * 128 * hd * 2, l.guards);
     l.off_d = take_region(o, (size_t)H * t * sizeof(float), l.guards);
+    l.off_large = take_region(o, (size_t)H * n * (256 / tc::pk::D_ROWS), l.guards);
     l.per_part = per_part ? per_part : kv_heads_per_part(H, Hkv, T);
     l.parts = (int)((H / Hkv + l.per_part - 1) / l.per_part);
     if (l.parts > 1) {
@@ -538,6 +608,7 @@ PackedWork packed_work(const PackedLayout& L, char* w) {
   k.tail_do = w + L.off_to;
   k.tail_kv = w + L.off_tkv;
   k.D = reinterpret_cast<float*>(w + L.off_d);
+  k.large = reinterpret_cast<uint8_t*>(w + L.off_large);
   return k;
 }
 
@@ -572,9 +643,11 @@ cudaError_t packed_prep(const PackedArgs& a, const PackedLayout& L, char* w, boo
     p.kvunits = reinterpret_cast<PackedKvUnit*>(w + L.off_kvunits);
     p.O = static_cast<const __nv_bfloat16*>(a.O);
     p.dO = static_cast<const __nv_bfloat16*>(a.dO);
-    p.rows = a.H * a.T;
+    p.V = static_cast<const __nv_bfloat16*>(a.V);
+    p.group = (int)(a.H / a.Hkv);
     p.D = reinterpret_cast<float*>(w + L.off_d);
-    blocks += (p.rows + tc::pk::PREP_THREADS / 16 - 1) / (tc::pk::PREP_THREADS / 16);
+    p.large = reinterpret_cast<uint8_t*>(w + L.off_large);
+    blocks += a.H * p.n_units * (256 / tc::pk::D_ROWS);
   }
   tc::pk::k_packed_prep<<<(unsigned)blocks, tc::pk::PREP_THREADS, 0, s>>>(p);
   return cudaGetLastError();
@@ -631,7 +704,7 @@ cudaError_t packed_backward_kernels(const PackedArgs& a, const PackedLayout& L, 
   tc::pk::QParams q;
   q.H = k.H; q.T = k.T; q.c0 = 0; q.c1 = k.c1; q.hd = k.hd; q.group = k.group; q.n_units = n * k.H;
   q.scale = k.scale; q.sc = k.sc; q.slopes = k.slopes; q.lse = k.lse; q.D = w.D; q.lo = w.lo; q.hi = w.hi;
-  q.units = w.qunits; q.tail = w.tail; q.dQ = static_cast<__nv_bfloat16*>(dQ); q.status = k.status; q.limit_ns = k.limit_ns;
+  q.units = w.qunits; q.large = reinterpret_cast<const uint32_t*>(w.large); q.tail = w.tail; q.dQ = static_cast<__nv_bfloat16*>(dQ); q.status = k.status; q.limit_ns = k.limit_ns;
   const int q_pairs = std::min(tc::max_pairs((const void*)k_attn_q<S>, SMEM_Q, Q_THREADS), q.n_units);
   // k_attn_q first: it corrects D; k_attn_kv starts as its pairs of SMs end, and waits for it
   cudaError_t e = tc::launch_early(k_attn_q<S>, 2 * q_pairs, Q_THREADS, SMEM_Q, s, mq, q);

@@ -40,6 +40,9 @@ struct PackedWork {
   const void *tail_q, *tail_do;         // backward, H heads
   const void* tail_kv;                  // V in the forward, K in the backward, Hkv heads
   float* D;                             // [H, T] dO . O (backward)
+  // [H, ceil(T / 256), 4] bytes: whether some of 64 queries need D from all of their keys (see
+  // PackedScores::q_sums)
+  const uint8_t* large;
 };
 
 struct PackedArgs {

@@ -218,6 +218,36 @@ def test_short_documents_beside_long_ones_keep_their_gradients(sbp, lens, prefix
         assert e < 2.0 ** -8, (k, e)
 
 
+@pytest.mark.parametrize("gain,shift,softcap,alibi", [(4.0, 0.0, 50.0, False), (4.0, 0.0, 0.0, True), (3.0, 0.0, 30.0, True),
+                                                      (1.0, 4.0, 0.0, False), (1.0, 0.0, 0.0, False)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_rows_of_long_documents_keep_their_gradients(sbp, gain, shift, softcap, alibi, hd):
+    # rows that few of many keys hold, and values with a common part, which the O they leave shows and
+    # dP - D does not: D is not that of the rounded O there.  Then dQ and dK have the roundings of dS
+    # and of the result to bf16, 2^-8 / sqrt(3) of the norm each if all were as large as can be
+    H, Hkv, T, sc = 4, 2, 1900, hd ** -0.5
+    x = make(H, Hkv, T, hd, seed=22, gain=gain)
+    x["V"] = I.round_bf16((x["V"] + shift).astype(np.float32))
+    cu, sl, kw = options(H, [1100, 760], None, softcap, alibi)
+    if alibi:
+        sl = np.array([0.7, 0.25, 0.05, 0.001], np.float32)
+        kw["slopes"] = dev(sl, torch.float32)
+    a = {k: dev(v) for k, v in x.items()}
+    f = sbp.attn_packed(a["Q"], a["K"], a["V"], sc, **kw)
+    b = sbp.attn_packed_backward(a["Q"], a["K"], a["V"], f["O"], a["dO"], f["lse"], sc, **kw)
+    torch.cuda.synchronize()
+    sbp.check_status(b["status"])
+    for s in range(2):
+        d, see = _document(x, cu[s], cu[s + 1]), np.tril(np.ones((cu[s + 1] - cu[s],) * 2, dtype=bool))
+        w = S.attention(d["Q"], d["K"], d["V"], see, sc, softcap, sl)
+        g = S.attention_backward(d["Q"], d["K"], d["V"], w["O"], d["dO"], w["lse"], see, sc, softcap, sl)
+        for k in "QK":
+            for h in range(H if k == "Q" else Hkv):
+                got, want = host(b["d" + k])[h, cu[s]:cu[s + 1]], g["d" + k][h]
+                e = np.linalg.norm(got - want) / np.linalg.norm(want)
+                assert e < 2.0 ** -8 * np.sqrt(2.0 / 3.0), (s, k, h, e)
+
+
 @pytest.mark.parametrize("softcap", [0.0, 20.0])
 def test_distances_of_far_rows(sbp, softcap):
     # rows past 2^24, which fp32 no longer tells from their neighbours: the bias goes by i - j
