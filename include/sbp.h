@@ -271,7 +271,7 @@ int sbp_attn_causal_backward_gqa(const void* Q, const void* K, const void* V, co
  * The sums of O are divided by the row's at the end.  Before that they hold up to
  * e^softcap sum |V| for a softcap of up to 50 and 2^16 sum |V| otherwise, which has to stay
  * below 2^127: |V| up to 2^54 / T and 2^111 / T is safe (2^40 and 2^97 at 16384 tokens).  With a
- * softcap of up to 50 they may also lose what is below 2^-53 of O.
+ * softcap of up to 50 parts of O below 2^-53 in magnitude may also be lost.
  * hd: a multiple of 8, at most 128.  scale > 0, finite, and scale / softcap too;
  * softcap 0 or in [1e-6, 256] (the scores' error grows with it, to 2^-14 there).  Fixed
  * order of every sum: the same call with a workspace of the same size gives the same bits.
