@@ -71,11 +71,14 @@ extern "C" {
 #define SBP_ERR_WORKSPACE_OVERRUN 9 /* (device, checked build only) a kernel wrote into a guard
                                        zone between workspace regions                     */
 #define SBP_ERR_SEQLENS 10      /* (device) cu_seqlens not 0 at the start, decreasing or past T;
-                                   a negative prefix length                               */
+                                   a negative prefix length; an expert table (offsets) of
+                                   that kind                                              */
+#define SBP_ERR_EXPERT_RANGE 11 /* (device) an expert id past the last expert             */
 
 /* operand dtypes */
 #define SBP_BF16 0
 #define SBP_FP32 1
+#define SBP_E4M3 2              /* sbp_expert_gather only                                 */
 
 /* workspace modes */
 #define SBP_MODE_SFT 0
@@ -366,6 +369,91 @@ int sbp_rope_qkv_backward(const void* dQ, const void* dK, const void* dV, int kv
                           int32_t n_axes, const int32_t* sections, const double* inv_freq, double theta,
                           int64_t rot_dim, int interleaved, int64_t T, int64_t H, int64_t Hkv, int64_t hd,
                           void* dqkv, int64_t row_stride, void* stream);
+
+/* An MLP of experts in 8 bits: tokens sorted by expert and back, quantisers, and the matrix
+ * product with a scale for each block of 128 (which serves a dense layer as well: E = 1 and
+ * offsets NULL).  A training step of one expert layer, Y_e = X_e W_e^T, is
+ *     sort, gather                     the tokens' rows in the order of their experts
+ *     quant_e4m3_rows(X), quant_e4m3_weight(W), matmul_e4m3                    Y
+ *     quant_e4m3_columns(dY, rows too), matmul_e4m3 with Wt8                   dX
+ *     quant_e4m3_columns(X, tiles), matmul_e4m3_columns                        dW
+ *     combine                          the experts' rows back in token order, weighted
+ * Rows of expert e are offsets[e] .. offsets[e+1] (device int32 [E+1], from 0, non-decreasing, at
+ * most T; SBP_ERR_SEQLENS in the status otherwise and nothing is computed).  The table is read by
+ * the device only, so a captured call follows its contents.  Experts without rows are allowed; rows
+ * behind offsets[E] belong to none and outputs are left as they were there.  E is at most 1024.
+ * Fixed order of every sum.  Stream and error rules as for the LM-head calls.
+ *
+ * Sort: ids [T, k] int32 (device), the experts of each token's k slots; a slot with a negative id
+ * is dropped (an id >= E too, with SBP_ERR_EXPERT_RANGE).  Slots (t, j) are put in the order of
+ * their experts and, within one, of t k + j:
+ *   rows    [T, k] int32      the place of slot (t, j), -1 for a dropped one
+ *   slots   [T k] int32       the slot t k + j at each place (entries behind offsets[E] untouched)
+ *   offsets [E+1] int32       where each expert's places begin
+ * T k at most 2^30. */
+size_t sbp_expert_sort_workspace_bytes(int64_t T, int64_t k, int64_t E);
+int sbp_expert_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* rows, int32_t* slots,
+                    int32_t* offsets, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Xs[rows[t, j]] = X[t].  X [T, d], Xs [n_rows, d] dtype (SBP_BF16, SBP_FP32, or SBP_E4M3 with scales
+ * [T, ceil(d / 128)] fp32, which go to scales_s [n_rows, ceil(d / 128)]; NULL otherwise).  A place
+ * outside [0, n_rows) is left out; rows of Xs that no slot goes to are left as they were.  d: a
+ * multiple of 8 (e4m3: 16), at most 16384.  No workspace and no status word, here and below; the
+ * gradient is sbp_expert_combine of dXs without weights. */
+int sbp_expert_gather(const void* X, const float* scales, const int32_t* rows, int64_t T, int64_t k, int64_t n_rows,
+                      int64_t d, int dtype, void* Xs, float* scales_s, void* stream);
+
+/* Y[t] = residual[t] + sum_j weights[t, j] Ys[rows[t, j]], summed in fp32 in the order of j and
+ * rounded once.  Ys [n_rows, d], residual (nullable: 0), Y [T, d] bf16 or fp32; weights [T, k] fp32
+ * (nullable: ones).  Slots with a place outside [0, n_rows) add nothing.  Y may be residual itself.
+ * Backward: dYs[rows[t, j]] = weights[t, j] dY[t] (other rows of dYs untouched) and
+ * dweights[t, j] = dY[t] . Ys[rows[t, j]] fp32 (0 for a slot left out). */
+int sbp_expert_combine(const void* Ys, const int32_t* rows, const float* weights, const void* residual, int64_t T,
+                       int64_t k, int64_t n_rows, int64_t d, int dtype, void* Y, void* stream);
+int sbp_expert_combine_backward(const void* dY, const void* Ys, const int32_t* rows, const float* weights, int64_t T,
+                                int64_t k, int64_t n_rows, int64_t d, int dtype, void* dYs, float* dweights,
+                                void* stream);
+
+/* Quantisers: over each block s = max|x| / 448 (fp32; 1 for a block of zeros, at least 2^-126) and
+ * q = e4m3(x fl(1 / s)), to nearest, ties to even.  A NaN stays one; an infinity makes its block's
+ * scale infinite and what the block stands for NaN.  X bf16 or fp32.
+ *   rows: blocks of 128 columns of a row (as sbp_rmsnorm_forward_e4m3 leaves Y): Y8 [T, d], scales
+ *     [T, ceil(d / 128)].  sbp_e4m3_expand gives the values back.
+ *   columns: blocks of 128 tokens, each expert's from its first row on, transposed.  With
+ *     nb = sbp_token_blocks(T, E) (the most blocks T rows of E experts can make up) Yt8 is
+ *     [d, 128 nb]: the tokens of expert e begin at 128 times the number of blocks of the experts
+ *     before it, zeros follow its last token up to the end of the block, and what lies behind the
+ *     last expert's blocks is left as it was.  tiles = 0: a scale for each block of each column,
+ *     scales_t [d, nb] (the left operand of sbp_matmul_e4m3_columns); tiles = 1: one for each 128
+ *     columns x 128 tokens, scales_t [ceil(d / 128), nb] (the right one).  Y8 and scales
+ *     (nullable, both): the rows' quantiser's output as well, from the same read (rows of no expert
+ *     are left as they were).
+ *   weight: W [E, N, K] in 128 x 128 tiles of each expert's matrix: W8 [E, N, K] with scales
+ *     [E, ceil(N / 128), ceil(K / 128)], and transposed Wt8 [E, K, N] with scales_t
+ *     [E, ceil(K / 128), ceil(N / 128)].
+ * d must be a multiple of 8; N and K of 16. */
+int64_t sbp_token_blocks(int64_t T, int64_t E);
+int sbp_quant_e4m3_rows(const void* X, int64_t T, int64_t d, int dtype, void* Y8, float* scales, void* stream);
+int sbp_quant_e4m3_columns(const void* X, const int32_t* offsets, int64_t E, int64_t T, int64_t d, int dtype,
+                           int tiles, void* Y8, float* scales, void* Yt8, float* scales_t, int32_t* dev_status,
+                           void* stream);
+int sbp_quant_e4m3_weight(const void* W, int64_t E, int64_t N, int64_t K, int dtype, void* W8, float* scales,
+                          void* Wt8, float* scales_t, void* stream);
+
+/* C[i, n] = sum_b sa[i, b] sb[e, n / 128, b] sum_k A8[i, k] B8[e, n, k] over the blocks b of 128 k,
+ * for the rows i of expert e.  A8 [T, K] e4m3 with sa [T, ceil(K / 128)]; B8 [E, N, K] with sb
+ * [E, ceil(N / 128), ceil(K / 128)]; C [T, N] bf16 or fp32 (out_dtype).  A block's sum and the sum
+ * over the blocks are fp32.  K must be a multiple of 16, N of 8.
+ * columns: dW[e] (+)= sum over expert e's tokens of At8 and Bt8, both as sbp_quant_e4m3_columns
+ * leaves them for these offsets (At8 [N, 128 nb] without tiles, Bt8 [K, 128 nb] with): dW [E, N, K]
+ * fp32, overwritten (accumulate = 0; zeros for an expert without rows) or added to (1).
+ * N and K must be multiples of 8. */
+int sbp_matmul_e4m3(const void* A8, const float* sa, const void* B8, const float* sb, const int32_t* offsets,
+                    int64_t E, int64_t T, int64_t N, int64_t K, int out_dtype, void* C, int32_t* dev_status,
+                    void* stream);
+int sbp_matmul_e4m3_columns(const void* At8, const float* sat, const void* Bt8, const float* sbt,
+                            const int32_t* offsets, int64_t E, int64_t T, int64_t N, int64_t K, float* dW,
+                            int accumulate, int32_t* dev_status, void* stream);
 
 /* Size of the fixed scratch array that sbp_lmhead_sft_noalloc works in (bytes). */
 #define SBP_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)

@@ -1520,6 +1520,7 @@ const char* sbp_status_string(int status) {
     case SBP_ERR_SCRATCH_LIMIT: return "SBP_ERR_SCRATCH_LIMIT";
     case SBP_ERR_WORKSPACE_OVERRUN: return "SBP_ERR_WORKSPACE_OVERRUN";
     case SBP_ERR_SEQLENS: return "SBP_ERR_SEQLENS";
+    case SBP_ERR_EXPERT_RANGE: return "SBP_ERR_EXPERT_RANGE";
     default: return "SBP_ERR_UNKNOWN";
   }
 }

@@ -1,0 +1,224 @@
+// Matrix products in 8 bits (e4m3) with a scale for each block of 128 (sm_103a).
+//
+//   rows     C[i, n] = sum_b sa[i, b] sb[e, n / 128, b] sum_{k in block b} A[i, k] B[e, n, k]
+//            for the rows i of expert e (one expert: a linear layer; its dX with B transposed)
+//   columns  dW[e, m, n] (+)= the same sum over the blocks b of expert e's tokens, A and B being
+//            what the column quantiser leaves
+//
+// A has a scale for each row and block of 128, B one for each 128 x 128 tile.  The products of one
+// block are exact in fp32 but for the order of the sum; a block's sum is scaled and added in fp32.
+#include <algorithm>
+
+#include "sbp_groups.cuh"
+#include "sbp_mm8.cuh"
+#include "sbp_rows.cuh"
+#include "sbp_tc_common.cuh"
+
+namespace sbp {
+namespace mm8 {
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr int FEW_WARPS = 8;
+
+// Few rows: what bounds the call is reading B once.  A block has 16 rows of B against 8 NT rows of
+// A, its warps sharing out the blocks of 128; they go straight from device memory into the
+// operands' registers.  (The order of k within a block of 128 is that of the 32 bytes a thread
+// loads, the same for A and B.)
+template <int NT>
+__global__ void __launch_bounds__(32 * FEW_WARPS) k_mm8_few(const P p) {
+  __shared__ float red[FEW_WARPS][8 * NT][17];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int strips = (p.nb + 15) / 16;
+  bool bad = false;
+  int total;
+  if (p.columns) {
+    const Group u = find_unit(p.offsets, p.E, p.T, 128, 0);
+    bad = u.bad;
+    total = p.E * ((p.na + 8 * NT - 1) / (8 * NT));
+  } else {
+    const Group u = find_unit(p.offsets, p.E, p.T, 8 * NT, 0);
+    bad = u.bad;
+    total = u.total;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = bad ? SBP_ERR_SEQLENS : SBP_OK;
+  if (bad) return;
+  const int64_t items = (int64_t)total * strips;
+  const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  int have = -1;
+  Unit w{};
+  for (int64_t item = i0; item < i1; ++item) {
+    const int u = (int)(item / strips), strip = (int)(item - (int64_t)u * strips);
+    if (u != have) {
+      w = unit_of(p, 8 * NT, u);
+      have = u;
+    }
+    const int n0 = strip * 16;
+    const int rb0 = min(n0 + g, p.nb - 1), rb1 = min(n0 + g + 8, p.nb - 1);
+    const uint8_t* b0 = p.B + (int64_t)w.e * p.b_stride + (int64_t)rb0 * p.ldb + 32 * t;
+    const uint8_t* b1 = p.B + (int64_t)w.e * p.b_stride + (int64_t)rb1 * p.ldb + 32 * t;
+    const uint8_t* a[NT];
+    const float* sa[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      a[i] = p.A + (int64_t)(w.row0 + min(8 * i + g, w.rows - 1)) * p.lda + 32 * t;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sa[i][h] = p.sa + (int64_t)(w.row0 + min(8 * i + 2 * t + h, w.rows - 1)) * p.sa_pitch;
+    }
+    const float* sb = p.sb + (int64_t)w.e * p.sb_stride + (int64_t)(n0 / 128) * p.sb_pitch;
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int kb = w.kb0 + warp; kb < w.kb1; kb += FEW_WARPS) {
+      const int64_t at = (int64_t)kb * 128;
+      const int64_t left = p.K - at - 32 * t;   // bytes of this thread's 32 that are inside the row
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      uint4 x[4];
+      x[0] = left > 0 ? *reinterpret_cast<const uint4*>(b0 + at) : z;
+      x[1] = left > 16 ? *reinterpret_cast<const uint4*>(b0 + at + 16) : z;
+      x[2] = left > 0 ? *reinterpret_cast<const uint4*>(b1 + at) : z;
+      x[3] = left > 16 ? *reinterpret_cast<const uint4*>(b1 + at + 16) : z;
+      const float s = sb[kb];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if (8 * i >= w.rows) break;
+        const uint4 y0 = left > 0 ? *reinterpret_cast<const uint4*>(a[i] + at) : z;
+        const uint4 y1 = left > 16 ? *reinterpret_cast<const uint4*>(a[i] + at + 16) : z;
+        const float s0 = s * sa[i][0][kb], s1 = s * sa[i][1][kb];
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_e4m3(c, x[0].x, x[2].x, x[0].y, x[2].y, y0.x, y0.y);
+        mma_e4m3(c, x[0].z, x[2].z, x[0].w, x[2].w, y0.z, y0.w);
+        mma_e4m3(c, x[1].x, x[3].x, x[1].y, x[3].y, y1.x, y1.y);
+        mma_e4m3(c, x[1].z, x[3].z, x[1].w, x[3].w, y1.z, y1.w);
+        acc[i][0] = fmaf(c[0], s0, acc[i][0]);
+        acc[i][1] = fmaf(c[1], s1, acc[i][1]);
+        acc[i][2] = fmaf(c[2], s0, acc[i][2]);
+        acc[i][3] = fmaf(c[3], s1, acc[i][3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      red[warp][8 * i + 2 * t][g] = acc[i][0];
+      red[warp][8 * i + 2 * t + 1][g] = acc[i][1];
+      red[warp][8 * i + 2 * t][g + 8] = acc[i][2];
+      red[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < 128 * NT; o += 32 * FEW_WARPS) {
+      const int r = o / 16, n = o % 16;
+      if (r < w.rows && n0 + n < p.nb) {
+        float v = red[0][r][n];
+#pragma unroll
+        for (int i = 1; i < FEW_WARPS; ++i) v += red[i][r][n];
+        const int64_t at = (int64_t)w.e * p.c_stride + (int64_t)(w.row0 + r) * p.nb + n0 + n;
+        if (p.out == SBP_BF16) {
+          static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
+        } else {
+          float* c = static_cast<float*>(p.C) + at;
+          *c = p.accumulate ? *c + v : v;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int NT>
+cudaError_t launch_few(const P& p, int64_t units, cudaStream_t s) {
+  const int64_t items = units * ((p.nb + 15) / 16);
+  const int64_t most = (int64_t)num_sms() * 4;
+  k_mm8_few<NT><<<(unsigned)std::max<int64_t>(1, std::min(items, most)), 32 * FEW_WARPS, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Rows of A that one block takes: as many as an expert has on average, in tiles of 8.
+cudaError_t few(const P& p, cudaStream_t s) {
+  const int64_t rows = p.columns ? p.na : (p.T + p.E - 1) / p.E;
+  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  const int64_t units = p.columns ? (int64_t)p.E * ((p.na + 8 * nt - 1) / (8 * nt)) : max_units(p.T, p.E, 8 * nt);
+  if (nt == 1) return launch_few<1>(p, units, s);
+  if (nt == 2) return launch_few<2>(p, units, s);
+  return launch_few<4>(p, units, s);
+}
+
+int check_common(int64_t E, int64_t T, int64_t N, int64_t K, const void* A8, const void* sa, const void* B8,
+                 const void* sb, const int32_t* offsets, const void* C, const int32_t* status) {
+  for (const void* q : {A8, B8, C})
+    if (!aligned16(q)) return SBP_ERR_ALIGNMENT;
+  for (const void* q : {sa, sb, (const void*)offsets, (const void*)status})
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return SBP_ERR_ALIGNMENT;
+  return SBP_OK;
+}
+
+}  // namespace mm8
+}  // namespace sbp
+
+using namespace sbp;
+
+extern "C" {
+
+int sbp_matmul_e4m3(const void* A8, const float* sa, const void* B8, const float* sb, const int32_t* offsets,
+                    int64_t E, int64_t T, int64_t N, int64_t K, int out_dtype, void* C, int32_t* dev_status,
+                    void* stream) {
+  if (E < 1 || T < 0 || N < 1 || K < 1 || (!offsets && E != 1) || (out_dtype != SBP_BF16 && out_dtype != SBP_FP32))
+    return SBP_ERR_INVALID_ARG;
+  if (E > MAX_GROUPS || K % 16 != 0 || N % 8 != 0 || T > (int64_t(1) << 30) || N > mm8::MAX_SIDE || K > mm8::MAX_SIDE ||
+      E * N > INT32_MAX - 256)
+    return SBP_ERR_UNSUPPORTED;
+  if (!dev_status || (T > 0 && (!A8 || !sa || !B8 || !sb || !C))) return SBP_ERR_INVALID_ARG;
+  const int rc = mm8::check_common(E, T, N, K, A8, sa, B8, sb, offsets, C, dev_status);
+  if (rc != SBP_OK) return rc;
+  NvtxRange nv("sbp_matmul_e4m3");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  set_launch_count(0);
+  if (T == 0) return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? SBP_OK : SBP_ERR_CUDA;
+  mm8::P p;
+  const int64_t kb = (K + 127) / 128, nb = (N + 127) / 128;
+  p.A = static_cast<const uint8_t*>(A8); p.sa = sa; p.lda = K; p.sa_pitch = kb;
+  p.B = static_cast<const uint8_t*>(B8); p.sb = sb; p.ldb = K; p.sb_pitch = kb;
+  p.b_stride = N * K; p.sb_stride = nb * kb; p.c_stride = 0;
+  p.offsets = offsets; p.E = (int)E; p.T = T; p.na = 0; p.nb = (int)N; p.K = K; p.kblocks = (int)kb;
+  p.columns = 0; p.out = out_dtype; p.accumulate = 0; p.C = C; p.status = dev_status;
+  if (mm8::few(p, s) != cudaSuccess) return SBP_ERR_CUDA;
+  set_launch_count(1);
+  return SBP_OK;
+}
+
+int sbp_matmul_e4m3_columns(const void* At8, const float* sat, const void* Bt8, const float* sbt,
+                            const int32_t* offsets, int64_t E, int64_t T, int64_t N, int64_t K, float* dW,
+                            int accumulate, int32_t* dev_status, void* stream) {
+  if (E < 1 || T < 0 || N < 1 || K < 1 || (!offsets && E != 1)) return SBP_ERR_INVALID_ARG;
+  if (E > MAX_GROUPS || K % 8 != 0 || N % 8 != 0 || T > (int64_t(1) << 30) || N > mm8::MAX_SIDE || K > mm8::MAX_SIDE)
+    return SBP_ERR_UNSUPPORTED;
+  if (!dev_status || !dW || (T > 0 && (!At8 || !sat || !Bt8 || !sbt))) return SBP_ERR_INVALID_ARG;
+  const int rc = mm8::check_common(E, T, N, K, At8, sat, Bt8, sbt, offsets, dW, dev_status);
+  if (rc != SBP_OK) return rc;
+  NvtxRange nv("sbp_matmul_e4m3_columns");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  set_launch_count(0);
+  if (T == 0) {
+    if (cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return SBP_ERR_CUDA;
+    if (!accumulate && cudaMemsetAsync(dW, 0, (size_t)E * N * K * sizeof(float), s) != cudaSuccess) return SBP_ERR_CUDA;
+    return SBP_OK;
+  }
+  mm8::P p;
+  const int64_t blocks = max_units(T, E, 128);
+  p.A = static_cast<const uint8_t*>(At8); p.sa = sat; p.lda = blocks * 128; p.sa_pitch = blocks;
+  p.B = static_cast<const uint8_t*>(Bt8); p.sb = sbt; p.ldb = blocks * 128; p.sb_pitch = blocks;
+  p.b_stride = 0; p.sb_stride = 0; p.c_stride = N * K;
+  p.offsets = offsets; p.E = (int)E; p.T = T; p.na = (int)N; p.nb = (int)K; p.K = blocks * 128; p.kblocks = (int)blocks;
+  p.columns = 1; p.out = SBP_FP32; p.accumulate = accumulate ? 1 : 0; p.C = dW; p.status = dev_status;
+  if (mm8::few(p, s) != cudaSuccess) return SBP_ERR_CUDA;
+  set_launch_count(1);
+  return SBP_OK;
+}
+
+}  // extern "C"

@@ -7,13 +7,10 @@
 // All three kernels are bound by device memory: each row is read once into registers (16
 // bytes a load, every load of the row issued before the first sum), reduced by its WPR
 // warps, and written once.  A block holds several rows of few warps, or one row of many.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-#include <cuda_runtime.h>
-
 #include <algorithm>
 #include <cmath>
 
+#include "sbp_rows.cuh"
 #include "sbp_tc_common.cuh"
 
 namespace sbp {
@@ -21,47 +18,6 @@ namespace {
 
 constexpr int MAXW = 32;            // warps of a block
 constexpr int64_t MAX_D = 16384;    // 32 warps x 32 lanes x 2 vectors x 8 elements
-
-// Eight elements of a row: as they lie in memory (16 or 32 bytes) and in fp32.
-struct F8 { float v[8]; };
-template <typename E> struct Raw;
-template <> struct Raw<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ F8 f() const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    F8 f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f.v[2 * i] = __uint_as_float(w[i] << 16);
-      f.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-    return f;
-  }
-};
-template <> struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ F8 f() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
-};
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f.v[2 * i], f.v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float* p, const F8& f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
-}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -178,20 +134,13 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_fwd(const FwdP p) {
           for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(r[i].v[k]));
         }
         for (int o = min(8, p.lpr / 2); o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        // 448: e4m3's largest value.  A block of zeros keeps the scale 1; a scale that is not
-        // normal would have no inverse.  One division a
-        // block and products instead of a division an element (132 us against 87).
-        const float s = a > 0.f ? fmaxf(a / 448.f, 1.17549435e-38f) : 1.f, inv = 1.f / s;
+        // One division a block and products instead of a division an element (132 us against 87).
+        const float s = e4m3_scale(a), inv = 1.f / s;
         if (v < nvec) {
           uint32_t w2[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(r[i].v[4 * k] * inv, r[i].v[4 * k + 1] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(r[i].v[4 * k + 2] * inv, r[i].v[4 * k + 3] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            w2[k] = lo | (hi << 16);
-          }
+          for (int k = 0; k < 2; ++k)
+            w2[k] = e4m3_pack(r[i].v[4 * k], r[i].v[4 * k + 1], r[i].v[4 * k + 2], r[i].v[4 * k + 3], inv);
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.Y) + at + 8 * v) = make_uint2(w2[0], w2[1]);
           if (v % 16 == 0) p.scales[row * p.nblk + v / 16] = s;
         }

@@ -1,0 +1,314 @@
+// Quantisers to 8 bits (e4m3) with one scale for each block of 128 (sm_103a): what the block-scaled
+// product takes.
+//
+//   s = max(max|x| / 448, 2^-126) over the block (1 for a block of zeros),  q = e4m3(x * fl(1 / s))
+//
+//   rows      blocks of 128 columns of a row
+//   columns   blocks of 128 tokens of one column, or tiles of 128 tokens x 128 columns, written
+//             transposed (the tokens run along the rows, as a product that sums over tokens wants
+//             them), each expert's tokens from a multiple of 128 on
+//   weight    tiles of 128 x 128, written in both orders
+//
+// All are bound by device memory.
+#include <algorithm>
+
+#include "sbp_groups.cuh"
+#include "sbp_rows.cuh"
+#include "sbp_tc_common.cuh"
+
+namespace sbp {
+namespace {
+
+constexpr int64_t MAX_D = 1 << 20;
+
+template <typename E>
+__device__ __forceinline__ float amax8(const Raw<E>& r) {
+  const F8 f = r.f();
+  float a = fabsf(f.v[0]);
+#pragma unroll
+  for (int k = 1; k < 8; ++k) a = fmaxf(a, fabsf(f.v[k]));
+  return a;
+}
+
+struct RowsP {
+  const void* X;
+  uint32_t units;       // blocks of 128 columns of all rows
+  uint32_t nblk, d;
+  uint8_t* Y8;
+  float* scales;
+};
+
+constexpr int ROW_UNITS = 4;   // blocks of 16 lanes, all loads in flight
+
+// 16 lanes a block of 128 columns, 8 columns a lane.
+template <typename E>
+__global__ void __launch_bounds__(256) k_quant_rows(const RowsP p) {
+  const uint32_t lane = threadIdx.x % 16;
+  const uint64_t u0 = (uint64_t)blockIdx.x * (16 * ROW_UNITS) + threadIdx.x / 16;
+  Raw<E> x[ROW_UNITS];
+  int64_t at[ROW_UNITS];
+#pragma unroll
+  for (int i = 0; i < ROW_UNITS; ++i) {
+    const uint64_t u = u0 + 16 * i;
+    x[i].zero();
+    at[i] = -1;
+    if (u < p.units) {
+      const uint32_t row = (uint32_t)u / p.nblk, c = ((uint32_t)u - row * p.nblk) * 128 + 8 * lane;
+      if (c < p.d) {
+        at[i] = (int64_t)row * p.d + c;
+        x[i].load(static_cast<const E*>(p.X) + at[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROW_UNITS; ++i) {
+    float a = amax8(x[i]);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const float s = e4m3_scale(a), inv = 1.f / s;
+    if (at[i] < 0) continue;
+    const F8 f = x[i].f();
+    *reinterpret_cast<uint2*>(p.Y8 + at[i]) =
+        make_uint2(e4m3_pack(f.v[0], f.v[1], f.v[2], f.v[3], inv), e4m3_pack(f.v[4], f.v[5], f.v[6], f.v[7], inv));
+    if (lane == 0) p.scales[u0 + 16 * i] = s;
+  }
+}
+
+struct TileP {
+  const void* X;            // [rows, d]
+  const int32_t* offsets;   // columns: the experts' rows (null: one expert)
+  int64_t T;
+  int E, d, nf;             // nf: blocks of 128 columns
+  int wrows, wblocks;       // weight: rows and row blocks of an expert (0: columns)
+  uint8_t* Y8;              // row order
+  float* scales;
+  uint8_t* Yt8;             // transposed
+  int64_t pitch;
+  float* scales_t;
+  int nbt;                  // scales of a transposed row
+  int32_t* status;
+};
+
+// One CTA a tile of 128 tokens x 128 columns, held in registers: thread (g, c) has 8 columns of
+// 8 neighbouring tokens, so that its 64 values make 8 transposed words of 8 bytes.  They are
+// exchanged through 16 KB of shared memory (the 8-byte chunk of a token group xored with the column
+// group, both ways without bank conflicts) and leave as rows of 128 bytes.
+// ROWS: 0 none, 1 blocks of 128 columns of a row, 2 tiles.  COLS: 1 blocks of 128 tokens of a
+// column, 2 tiles.
+template <typename E, int ROWS, int COLS>
+__global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
+  __shared__ uint2 tile[128 * 16];
+  __shared__ float cmax[8][128];
+  __shared__ float sinv[128];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, c8 = tid % 16, g8 = tid / 16;
+  const int b = (int)(blockIdx.x / p.nf), f = (int)(blockIdx.x - (unsigned)b * p.nf), f0 = f * 128;
+  int64_t row0;
+  int rows, e = 0, ib = b;
+  if (p.wblocks) {
+    e = b / p.wblocks;
+    ib = b - e * p.wblocks;
+    row0 = (int64_t)e * p.wrows + ib * 128;
+    rows = min(128, p.wrows - ib * 128);
+  } else {
+    const Group g = find_unit(p.offsets, p.E, p.T, 128, b);
+    if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = g.bad ? SBP_ERR_SEQLENS : SBP_OK;
+    if (g.bad || !g.found) return;
+    row0 = (int64_t)g.row0 + g.i * 128;
+    rows = min(128, g.rows - g.i * 128);
+  }
+  const int col = f0 + 8 * c8;
+  Raw<E> x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = g8 * 8 + i;
+    x[i].zero();
+    if (r < rows && col < p.d) x[i].load(static_cast<const E*>(p.X) + (row0 + r) * p.d + col);
+  }
+  float tinv = 1.f;
+  if (COLS == 1) {
+    F8 m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m.v[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const F8 v = x[i].f();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m.v[j] = fmaxf(m.v[j], fabsf(v.v[j]));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m.v[j] = fmaxf(m.v[j], __shfl_xor_sync(0xffffffffu, m.v[j], 16));
+    if (lane < 16) {
+      float4* q = reinterpret_cast<float4*>(&cmax[warp][8 * c8]);
+      q[0] = make_float4(m.v[0], m.v[1], m.v[2], m.v[3]);
+      q[1] = make_float4(m.v[4], m.v[5], m.v[6], m.v[7]);
+    }
+    __syncthreads();
+    if (tid < 128) {
+      float a = cmax[0][tid];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) a = fmaxf(a, cmax[w][tid]);
+      const float s = e4m3_scale(a);
+      sinv[tid] = 1.f / s;
+      if (f0 + tid < p.d) p.scales_t[(int64_t)(f0 + tid) * p.nbt + b] = s;
+    }
+    __syncthreads();
+  } else {
+    float a = amax8(x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) a = fmaxf(a, amax8(x[i]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if (lane == 0) cmax[0][warp] = a;
+    __syncthreads();
+    a = cmax[0][0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) a = fmaxf(a, cmax[0][w]);
+    const float s = e4m3_scale(a);
+    tinv = 1.f / s;
+    if (tid == 0) {
+      if (p.wblocks) {
+        p.scales[((int64_t)e * p.wblocks + ib) * p.nf + f] = s;
+        p.scales_t[((int64_t)e * p.nf + f) * p.wblocks + ib] = s;
+      } else {
+        p.scales_t[(int64_t)f * p.nbt + b] = s;
+      }
+    }
+  }
+  if (ROWS != 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = g8 * 8 + i;
+      float inv = tinv;
+      if (ROWS == 1) {
+        float a = amax8(x[i]);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        const float s = e4m3_scale(a);
+        inv = 1.f / s;
+        if (c8 == 0 && r < rows) p.scales[(row0 + r) * p.nf + f] = s;
+      }
+      if (r < rows && col < p.d) {
+        const F8 v = x[i].f();
+        *reinterpret_cast<uint2*>(p.Y8 + (row0 + r) * p.d + col) =
+            make_uint2(e4m3_pack(v.v[0], v.v[1], v.v[2], v.v[3], inv), e4m3_pack(v.v[4], v.v[5], v.v[6], v.v[7], inv));
+      }
+    }
+  }
+  float ci[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) ci[j] = COLS == 1 ? sinv[8 * c8 + j] : tinv;
+  {
+    F8 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = x[i].f();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      tile[(8 * c8 + j) * 16 + (g8 ^ c8)] =
+          make_uint2(e4m3_pack(v[0].v[j], v[1].v[j], v[2].v[j], v[3].v[j], ci[j]),
+                     e4m3_pack(v[4].v[j], v[5].v[j], v[6].v[j], v[7].v[j], ci[j]));
+  }
+  __syncthreads();
+  // transposed rows: 128 bytes each (an expert's padding is zeros), in pieces of 16
+  uint8_t* out = p.Yt8 + (p.wblocks ? (int64_t)e * p.d * p.pitch + ib * 128 : (int64_t)b * 128);
+  const int wide = p.wblocks ? rows : 128;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int q = k * 256 + tid, r = q / 8, m = q % 8, sw = r / 8;
+    if (f0 + r < p.d && 16 * m < wide) {
+      const uint2 lo = tile[r * 16 + ((2 * m) ^ sw)], hi = tile[r * 16 + ((2 * m + 1) ^ sw)];
+      *reinterpret_cast<uint4*>(out + (int64_t)(f0 + r) * p.pitch + 16 * m) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ host side
+
+int quant_check(int64_t T, int64_t d, int dtype) {
+  if (T < 0 || d < 1 || (dtype != SBP_BF16 && dtype != SBP_FP32)) return SBP_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > MAX_D || T > (int64_t(1) << 30)) return SBP_ERR_UNSUPPORTED;
+  return SBP_OK;
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int launched() {
+  if (cudaGetLastError() != cudaSuccess) return SBP_ERR_CUDA;
+  set_launch_count(1);
+  return SBP_OK;
+}
+
+template <int ROWS, int COLS>
+int launch_tile(const TileP& p, int64_t blocks, int dtype, cudaStream_t s) {
+  if (blocks > INT32_MAX) return SBP_ERR_UNSUPPORTED;
+  if (dtype == SBP_BF16) k_quant_tile<__nv_bfloat16, ROWS, COLS><<<(unsigned)blocks, 256, 0, s>>>(p);
+  else k_quant_tile<float, ROWS, COLS><<<(unsigned)blocks, 256, 0, s>>>(p);
+  return launched();
+}
+
+}  // namespace
+}  // namespace sbp
+
+using namespace sbp;
+
+extern "C" {
+
+int64_t sbp_token_blocks(int64_t T, int64_t E) {
+  return T < 0 || E < 1 || T > (int64_t(1) << 30) || E > MAX_GROUPS ? -1 : max_units(T, E, 128);
+}
+
+int sbp_quant_e4m3_rows(const void* X, int64_t T, int64_t d, int dtype, void* Y8, float* scales, void* stream) {
+  const int rc = quant_check(T, d, dtype);
+  if (rc != SBP_OK) return rc;
+  const int64_t nblk = (d + 127) / 128;
+  if (T * nblk > INT32_MAX) return SBP_ERR_UNSUPPORTED;
+  if (T > 0 && (!X || !Y8 || !scales)) return SBP_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y8) || !aligned4(scales)) return SBP_ERR_ALIGNMENT;
+  NvtxRange nv("sbp_quant_e4m3_rows");
+  set_launch_count(0);
+  if (T == 0) return SBP_OK;
+  const RowsP p{X, (uint32_t)(T * nblk), (uint32_t)nblk, (uint32_t)d, static_cast<uint8_t*>(Y8), scales};
+  const unsigned grid = (unsigned)((T * nblk + 16 * ROW_UNITS - 1) / (16 * ROW_UNITS));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == SBP_BF16) k_quant_rows<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+  else k_quant_rows<float><<<grid, 256, 0, s>>>(p);
+  return launched();
+}
+
+int sbp_quant_e4m3_columns(const void* X, const int32_t* offsets, int64_t E, int64_t T, int64_t d, int dtype,
+                           int tiles, void* Y8, float* scales, void* Yt8, float* scales_t, int32_t* dev_status,
+                           void* stream) {
+  const int rc = quant_check(T, d, dtype);
+  if (rc != SBP_OK) return rc;
+  if (E < 1 || (!offsets && E != 1) || (tiles != 0 && tiles != 1)) return SBP_ERR_INVALID_ARG;
+  if (E > MAX_GROUPS) return SBP_ERR_UNSUPPORTED;
+  if ((Y8 == nullptr) != (scales == nullptr) || !dev_status || (T > 0 && (!X || !Yt8 || !scales_t)))
+    return SBP_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y8) || !aligned16(Yt8)) return SBP_ERR_ALIGNMENT;
+  for (const void* q : {(const void*)offsets, (const void*)scales, (const void*)scales_t, (const void*)dev_status})
+    if (!aligned4(q)) return SBP_ERR_ALIGNMENT;
+  NvtxRange nv("sbp_quant_e4m3_columns");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  set_launch_count(0);
+  if (T == 0) return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? SBP_OK : SBP_ERR_CUDA;
+  const int64_t nb = max_units(T, E, 128), nf = (d + 127) / 128;
+  TileP p{X, offsets, T, (int)E, (int)d, (int)nf, 0, 0, static_cast<uint8_t*>(Y8), scales,
+          static_cast<uint8_t*>(Yt8), nb * 128, scales_t, (int)nb, dev_status};
+  if (Y8) return tiles ? launch_tile<1, 2>(p, nb * nf, dtype, s) : launch_tile<1, 1>(p, nb * nf, dtype, s);
+  return tiles ? launch_tile<0, 2>(p, nb * nf, dtype, s) : launch_tile<0, 1>(p, nb * nf, dtype, s);
+}
+
+int sbp_quant_e4m3_weight(const void* W, int64_t E, int64_t N, int64_t K, int dtype, void* W8, float* scales,
+                          void* Wt8, float* scales_t, void* stream) {
+  if (E < 1 || N < 1 || K < 1 || (dtype != SBP_BF16 && dtype != SBP_FP32)) return SBP_ERR_INVALID_ARG;
+  if (E > MAX_GROUPS || N % 16 != 0 || K % 16 != 0 || N > MAX_D || K > MAX_D) return SBP_ERR_UNSUPPORTED;
+  if (!W || !W8 || !scales || !Wt8 || !scales_t) return SBP_ERR_INVALID_ARG;
+  if (!aligned16(W) || !aligned16(W8) || !aligned16(Wt8) || !aligned4(scales) || !aligned4(scales_t))
+    return SBP_ERR_ALIGNMENT;
+  NvtxRange nv("sbp_quant_e4m3_weight");
+  set_launch_count(0);
+  const int64_t nn = (N + 127) / 128, nk = (K + 127) / 128;
+  TileP p{W, nullptr, E * N, (int)E, (int)K, (int)nk, (int)N, (int)nn, static_cast<uint8_t*>(W8), scales,
+          static_cast<uint8_t*>(Wt8), N, scales_t, (int)nn, nullptr};
+  return launch_tile<2, 2>(p, E * nn * nk, dtype, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

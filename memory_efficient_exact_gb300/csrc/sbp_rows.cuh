@@ -1,0 +1,65 @@
+// Rows of bf16, fp32 and e4m3 values, eight elements at a time, and the quantiser's arithmetic:
+// shared by the norm, quantiser and expert-routing kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace sbp {
+
+// Eight elements of a row: as they lie in memory (16 or 32 bytes) and in fp32.
+struct F8 { float v[8]; };
+template <typename E> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ F8 f() const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    F8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f.v[2 * i] = __uint_as_float(w[i] << 16);
+      f.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    return f;
+  }
+};
+template <> struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ F8 f() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+};
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.v[2 * i], f.v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const F8& f) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+}
+
+// The scale of a block whose largest magnitude is `a`, in 8 bits.  448: e4m3's largest value.  A
+// block of zeros keeps the scale 1; a scale that is not normal would have no inverse.
+__device__ __forceinline__ float e4m3_scale(float a) {
+  return a > 0.f ? fmaxf(a / 448.f, 1.17549435e-38f) : 1.f;
+}
+// Four values times the scale's inverse, as e4m3.
+__device__ __forceinline__ uint32_t e4m3_pack(float a, float b, float c, float d, float inv) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+}  // namespace sbp

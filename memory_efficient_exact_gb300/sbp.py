@@ -24,9 +24,9 @@ LIB_PATH = os.path.join(_HERE, f"libsbp_{VARIANT}.so" if VARIANT else "libsbp.so
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "sbp.h")
 
 (OK, ERR_INVALID_ARG, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_LABEL_RANGE, ERR_TIMEOUT, ERR_CUDA, ERR_UNSUPPORTED,
- ERR_SCRATCH_LIMIT, ERR_WORKSPACE_OVERRUN, ERR_SEQLENS) = range(11)
+ ERR_SCRATCH_LIMIT, ERR_WORKSPACE_OVERRUN, ERR_SEQLENS, ERR_EXPERT_RANGE) = range(12)
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
-BF16, FP32 = 0, 1
+BF16, FP32, E4M3 = 0, 1, 2
 MODE_SFT, MODE_GRPO, MODE_DPO1, MODE_DPO2 = 0, 1, 2, 3
 IGNORE_INDEX = -100
 
@@ -100,6 +100,28 @@ def _load() -> ctypes.CDLL:
     lib.sbp_rope_qkv_forward.argtypes = [P, I64, P, I32, P, P, D, I64, C, I64, I64, I64, I64, P, P, P, P]
     lib.sbp_rope_qkv_backward.restype = C
     lib.sbp_rope_qkv_backward.argtypes = [P, P, P, C, P, I32, P, P, D, I64, C, I64, I64, I64, I64, P, I64, P]
+    lib.sbp_expert_sort_workspace_bytes.restype = SZ
+    lib.sbp_expert_sort_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.sbp_expert_sort.restype = C
+    lib.sbp_expert_sort.argtypes = [P, I64, I64, I64, P, P, P, P, SZ, P, P]
+    lib.sbp_expert_gather.restype = C
+    lib.sbp_expert_gather.argtypes = [P, P, P, I64, I64, I64, I64, C, P, P, P]
+    lib.sbp_expert_combine.restype = C
+    lib.sbp_expert_combine.argtypes = [P, P, P, P, I64, I64, I64, I64, C, P, P]
+    lib.sbp_expert_combine_backward.restype = C
+    lib.sbp_expert_combine_backward.argtypes = [P, P, P, P, I64, I64, I64, I64, C, P, P, P]
+    lib.sbp_token_blocks.restype = I64
+    lib.sbp_token_blocks.argtypes = [I64, I64]
+    lib.sbp_quant_e4m3_rows.restype = C
+    lib.sbp_quant_e4m3_rows.argtypes = [P, I64, I64, C, P, P, P]
+    lib.sbp_quant_e4m3_columns.restype = C
+    lib.sbp_quant_e4m3_columns.argtypes = [P, P, I64, I64, I64, C, C, P, P, P, P, P, P]
+    lib.sbp_quant_e4m3_weight.restype = C
+    lib.sbp_quant_e4m3_weight.argtypes = [P, I64, I64, I64, C, P, P, P, P, P]
+    lib.sbp_matmul_e4m3.restype = C
+    lib.sbp_matmul_e4m3.argtypes = [P, P, P, P, P, I64, I64, I64, I64, C, P, P, P]
+    lib.sbp_matmul_e4m3_columns.restype = C
+    lib.sbp_matmul_e4m3_columns.argtypes = [P, P, P, P, P, I64, I64, I64, I64, P, C, P, P]
     lib.sbp_status_string.restype = ctypes.c_char_p
     lib.sbp_status_string.argtypes = [C]
     lib.sbp_last_launch_count.restype = C
@@ -759,3 +781,247 @@ def rope_qkv_backward(dQ, dK, dV, positions, *, sections=None, rot_dim=None, the
                                       dqkv.stride(0) if T > 1 else dqkv.shape[1], _raw(stream, dev)),
            "sbp_rope_qkv_backward")
     return dict(dqkv=dqkv)
+
+
+# --------------------------------------------------------------- an MLP of experts in 8 bits
+
+_FP8 = torch.float8_e4m3fn
+
+
+def _shaped(t, shape, dtype, what):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError(f"{what} must be {str(dtype)[6:]} {list(shape)}")
+
+
+def _out(t, shape, dtype, what, stream, dev):
+    if t is None:
+        return _empty(stream, shape, dtype, dev)
+    _shaped(t, shape, dtype, what)
+    return t
+
+
+def _table(offsets):
+    """E of an experts' table (None: one expert of all rows)."""
+    if offsets is None:
+        return 1
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be int32 [E + 1], E >= 1")
+    return offsets.numel() - 1
+
+
+def expert_sort(ids, E, *, rows=None, slots=None, offsets=None, workspace=None, status=None, stream=None) -> dict:
+    """Slots in the order of their experts (``sbp_expert_sort``).
+
+    ids [T, k] int32, negative: dropped.  Returns rows [T, k] (each slot's place, -1 if dropped),
+    slots [T k] (the slot at each place) and offsets [E + 1] (each expert's first place), int32."""
+    _on_device(ids, rows, slots, offsets, workspace, status)
+    if ids.dim() != 2 or ids.dtype != torch.int32:
+        raise ValueError("ids must be int32 [T, k]")
+    T, k = ids.shape
+    dev = ids.device
+    if workspace is None:
+        n = _lib.sbp_expert_sort_workspace_bytes(T, k, E)
+        if n == 0:
+            raise SbpError(ERR_UNSUPPORTED, "sbp_expert_sort_workspace_bytes")
+        workspace = _empty(stream, n, torch.uint8, dev)
+    rows = _out(rows, (T, k), torch.int32, "rows", stream, dev)
+    slots = _out(slots, (T * k,), torch.int32, "slots", stream, dev)
+    offsets = _out(offsets, (E + 1,), torch.int32, "offsets", stream, dev)
+    st = _status_word(status, stream, dev)
+    _check(_lib.sbp_expert_sort(_a(ids), T, k, E, _a(rows), _a(slots), _a(offsets), _a(workspace), workspace.numel(),
+                                _a(st), _raw(stream, dev)), "sbp_expert_sort")
+    return dict(rows=rows, slots=slots, offsets=offsets, status=st)
+
+
+def _routed(rows, first, *ts):
+    _on_device(rows, first, *ts)
+    if rows.dim() != 2 or rows.dtype != torch.int32 or first.dim() != 2:
+        raise ValueError("rows must be int32 [T, k], the values two-dimensional")
+
+
+def expert_gather(X, rows, *, scales=None, n_rows=None, Xs=None, scales_s=None, stream=None) -> dict:
+    """Xs[rows[t, j]] = X[t] (``sbp_expert_gather``): X [T, d] bf16 or fp32, or e4m3 with scales
+    [T, ceil(d / 128)].  Xs has n_rows rows (T k by default)."""
+    _routed(rows, X, scales, Xs, scales_s)
+    T, k = rows.shape
+    d = X.shape[1]
+    q8 = X.dtype == _FP8
+    if X.shape[0] != T or q8 != (scales is not None):
+        raise ValueError("X [T, d] with rows [T, k]; scales belong to e4m3 rows")
+    if n_rows is None:
+        n_rows = T * k if Xs is None else Xs.shape[0]
+    dev = X.device
+    if q8:
+        nblk = (d + 127) // 128
+        _shaped(scales, (T, nblk), torch.float32, "scales")
+        scales_s = _out(scales_s, (n_rows, nblk), torch.float32, "scales_s", stream, dev)
+    elif scales_s is not None:
+        raise ValueError("scales_s belongs to e4m3 rows")
+    Xs = _out(Xs, (n_rows, d), X.dtype, "Xs", stream, dev)
+    _check(_lib.sbp_expert_gather(_a(X), _a(scales), _a(rows), T, k, n_rows, d, E4M3 if q8 else _code(X), _a(Xs),
+                                  _a(scales_s), _raw(stream, dev)), "sbp_expert_gather")
+    return dict(Xs=Xs, scales=scales_s) if q8 else dict(Xs=Xs)
+
+
+def expert_combine(Ys, rows, weights=None, *, residual=None, Y=None, stream=None) -> dict:
+    """Y[t] = residual[t] + sum_j weights[t, j] Ys[rows[t, j]] (``sbp_expert_combine``): Ys
+    [n_rows, d] bf16 or fp32, weights [T, k] fp32 (None: ones).  Y=residual adds in place."""
+    _routed(rows, Ys, weights, residual, Y)
+    T, k = rows.shape
+    n_rows, d = Ys.shape
+    dev = Ys.device
+    _shaped(weights, (T, k), torch.float32, "weights")
+    _shaped(residual, (T, d), Ys.dtype, "residual")
+    Y = _out(Y, (T, d), Ys.dtype, "Y", stream, dev)
+    _check(_lib.sbp_expert_combine(_a(Ys), _a(rows), _a(weights), _a(residual), T, k, n_rows, d, _code(Ys), _a(Y),
+                                   _raw(stream, dev)), "sbp_expert_combine")
+    return dict(Y=Y)
+
+
+def expert_gather_backward(dXs, rows, *, dX=None, stream=None) -> dict:
+    """Gradient of ``expert_gather``: dX[t] = sum_j dXs[rows[t, j]] (``sbp_expert_combine`` without
+    weights)."""
+    return dict(dX=expert_combine(dXs, rows, Y=dX, stream=stream)["Y"])
+
+
+def expert_combine_backward(dY, Ys, rows, weights, *, dYs=None, dweights=None, stream=None) -> dict:
+    """Gradients of ``expert_combine`` (``sbp_expert_combine_backward``): dYs [n_rows, d] (rows that
+    no slot came from are left as they were) and dweights [T, k] fp32.  The residual's is dY."""
+    _routed(rows, Ys, dY, weights, dYs, dweights)
+    T, k = rows.shape
+    n_rows, d = Ys.shape
+    dev = Ys.device
+    _shaped(dY, (T, d), Ys.dtype, "dY")
+    _shaped(weights, (T, k), torch.float32, "weights")
+    dYs = _out(dYs, (n_rows, d), Ys.dtype, "dYs", stream, dev)
+    dweights = _out(dweights, (T, k), torch.float32, "dweights", stream, dev)
+    _check(_lib.sbp_expert_combine_backward(_a(dY), _a(Ys), _a(rows), _a(weights), T, k, n_rows, d, _code(Ys), _a(dYs),
+                                            _a(dweights), _raw(stream, dev)), "sbp_expert_combine_backward")
+    return dict(dYs=dYs, dweights=dweights)
+
+
+def token_blocks(T: int, E: int = 1) -> int:
+    """The most blocks of 128 tokens that T rows of E experts make up (``sbp_token_blocks``)."""
+    return int(_lib.sbp_token_blocks(T, E))
+
+
+def quant_e4m3(X, *, Y8=None, scales=None, stream=None) -> dict:
+    """X [T, d] bf16 or fp32 in 8 bits (``sbp_quant_e4m3_rows``): Y8 [T, d] e4m3 and scales
+    [T, ceil(d / 128)] fp32, as ``rmsnorm_e4m3`` leaves its Y."""
+    _on_device(X, Y8, scales)
+    if X.dim() != 2:
+        raise ValueError("X must be [T, d]")
+    T, d = X.shape
+    dev = X.device
+    code = _code(X)
+    Y8 = _out(Y8, (T, d), _FP8, "Y8", stream, dev)
+    scales = _out(scales, (T, (d + 127) // 128), torch.float32, "scales", stream, dev)
+    _check(_lib.sbp_quant_e4m3_rows(_a(X), T, d, code, _a(Y8), _a(scales), _raw(stream, dev)), "sbp_quant_e4m3_rows")
+    return dict(Y8=Y8, scales=scales)
+
+
+def quant_e4m3_columns(X, *, offsets=None, tiles=False, rows=False, Yt8=None, scales_t=None, Y8=None, scales=None,
+                       status=None, stream=None) -> dict:
+    """X [T, d] in 8 bits and transposed (``sbp_quant_e4m3_columns``), blocks of 128 tokens beginning
+    anew with each expert: Yt8 [d, 128 nb] and scales_t [d, nb] (tiles: [ceil(d / 128), nb]),
+    nb = token_blocks(T, E).  rows=True: Y8 and scales of ``quant_e4m3`` as well."""
+    _on_device(X, offsets, Yt8, scales_t, Y8, scales, status)
+    if X.dim() != 2:
+        raise ValueError("X must be [T, d]")
+    T, d = X.shape
+    dev = X.device
+    code = _code(X)
+    E = _table(offsets)
+    nb = _lib.sbp_token_blocks(T, E)
+    if nb < 0:
+        raise SbpError(ERR_UNSUPPORTED, "sbp_token_blocks")
+    nd = (d + 127) // 128
+    Yt8 = _out(Yt8, (d, 128 * nb), _FP8, "Yt8", stream, dev)
+    scales_t = _out(scales_t, (nd if tiles else d, nb), torch.float32, "scales_t", stream, dev)
+    if rows:
+        Y8 = _out(Y8, (T, d), _FP8, "Y8", stream, dev)
+        scales = _out(scales, (T, nd), torch.float32, "scales", stream, dev)
+    elif Y8 is not None or scales is not None:
+        raise ValueError("Y8 and scales are outputs of rows=True")
+    st = _status_word(status, stream, dev)
+    _check(_lib.sbp_quant_e4m3_columns(_a(X), _a(offsets), E, T, d, code, 1 if tiles else 0, _a(Y8), _a(scales),
+                                       _a(Yt8), _a(scales_t), _a(st), _raw(stream, dev)), "sbp_quant_e4m3_columns")
+    out = dict(Yt8=Yt8, scales_t=scales_t, status=st)
+    if rows:
+        out.update(Y8=Y8, scales=scales)
+    return out
+
+
+def quant_e4m3_weight(W, *, W8=None, scales=None, Wt8=None, scales_t=None, stream=None) -> dict:
+    """W [N, K] or [E, N, K] in 8 bits with a scale for each 128 x 128 tile, in both orders
+    (``sbp_quant_e4m3_weight``): W8 as W and Wt8 [.., K, N], with scales and scales_t."""
+    _on_device(W, W8, scales, Wt8, scales_t)
+    if W.dim() not in (2, 3):
+        raise ValueError("W must be [N, K] or [E, N, K]")
+    lead = tuple(W.shape[:-2])
+    N, K = W.shape[-2:]
+    E = W.shape[0] if lead else 1
+    nn, nk = (N + 127) // 128, (K + 127) // 128
+    dev = W.device
+    code = _code(W)
+    W8 = _out(W8, lead + (N, K), _FP8, "W8", stream, dev)
+    Wt8 = _out(Wt8, lead + (K, N), _FP8, "Wt8", stream, dev)
+    scales = _out(scales, lead + (nn, nk), torch.float32, "scales", stream, dev)
+    scales_t = _out(scales_t, lead + (nk, nn), torch.float32, "scales_t", stream, dev)
+    _check(_lib.sbp_quant_e4m3_weight(_a(W), E, N, K, code, _a(W8), _a(scales), _a(Wt8), _a(scales_t),
+                                      _raw(stream, dev)), "sbp_quant_e4m3_weight")
+    return dict(W8=W8, scales=scales, Wt8=Wt8, scales_t=scales_t)
+
+
+def matmul_e4m3(A8, sa, B8, sb, *, offsets=None, dtype=torch.bfloat16, C=None, status=None, stream=None) -> dict:
+    """C = A8 B8^T with a scale for each block of 128 (``sbp_matmul_e4m3``).
+
+    A8 [T, K] e4m3, sa [T, ceil(K / 128)]; B8 [N, K] with sb [ceil(N / 128), ceil(K / 128)], or with
+    offsets [E + 1] B8 [E, N, K] with sb [E, ..]: the rows of each expert against its matrix.
+    C [T, N] bf16 or fp32 (rows of no expert are left as they were)."""
+    _on_device(A8, sa, B8, sb, offsets, C, status)
+    E = _table(offsets)
+    lead = () if offsets is None else (E,)
+    if A8.dim() != 2 or B8.dim() != 2 + len(lead) or not A8.dtype == B8.dtype == _FP8:
+        raise ValueError("A8 e4m3 [T, K]; B8 e4m3 [N, K], or [E, N, K] with offsets [E + 1]")
+    T, K = A8.shape
+    N = B8.shape[-2]
+    nk = (K + 127) // 128
+    _shaped(B8, lead + (N, K), _FP8, "B8")
+    _shaped(sa, (T, nk), torch.float32, "sa")
+    _shaped(sb, lead + ((N + 127) // 128, nk), torch.float32, "sb")
+    dev = A8.device
+    if C is None:
+        C = _empty(stream, (T, N), dtype, dev)
+    elif C.shape != (T, N):
+        raise ValueError("C must be [T, N]")
+    st = _status_word(status, stream, dev)
+    _check(_lib.sbp_matmul_e4m3(_a(A8), _a(sa), _a(B8), _a(sb), _a(offsets), E, T, N, K, _code(C), _a(C), _a(st),
+                                _raw(stream, dev)), "sbp_matmul_e4m3")
+    return dict(C=C, status=st)
+
+
+def matmul_e4m3_columns(At8, sat, Bt8, sbt, T, *, offsets=None, dW=None, accumulate=False, status=None,
+                        stream=None) -> dict:
+    """dW = sum over each expert's tokens of At8 and Bt8 (``sbp_matmul_e4m3_columns``), both as
+    ``quant_e4m3_columns`` leaves them for T tokens and these offsets: At8 [N, 128 nb] without tiles,
+    Bt8 [K, 128 nb] with.  dW [N, K], or [E, N, K] with offsets, fp32."""
+    _on_device(At8, sat, Bt8, sbt, offsets, dW, status)
+    E = _table(offsets)
+    lead = () if offsets is None else (E,)
+    nb = _lib.sbp_token_blocks(T, E)
+    if nb < 0:
+        raise SbpError(ERR_UNSUPPORTED, "sbp_token_blocks")
+    if At8.dim() != 2 or Bt8.dim() != 2:
+        raise ValueError("At8 e4m3 [N, 128 nb]; Bt8 e4m3 [K, 128 nb]")
+    N, K = At8.shape[0], Bt8.shape[0]
+    _shaped(At8, (N, 128 * nb), _FP8, "At8")
+    _shaped(Bt8, (K, 128 * nb), _FP8, "Bt8")
+    _shaped(sat, (N, nb), torch.float32, "sat")
+    _shaped(sbt, ((K + 127) // 128, nb), torch.float32, "sbt")
+    dev = At8.device
+    dW = _out(dW, lead + (N, K), torch.float32, "dW", stream, dev)
+    st = _status_word(status, stream, dev)
+    _check(_lib.sbp_matmul_e4m3_columns(_a(At8), _a(sat), _a(Bt8), _a(sbt), _a(offsets), E, T, N, K, _a(dW),
+                                        1 if accumulate else 0, _a(st), _raw(stream, dev)), "sbp_matmul_e4m3_columns")
+    return dict(dW=dW, status=st)
