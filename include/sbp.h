@@ -414,11 +414,11 @@ int sbp_expert_combine_backward(const void* dY, const void* Ys, const int32_t* r
                                 int64_t k, int64_t n_rows, int64_t d, int dtype, void* dYs, float* dweights,
                                 void* stream);
 
-/* Quantisers: over each block s = max|x| / 448 (fp32; 1 for a block of zeros, at least 2^-126) and
- * q = e4m3(x fl(1 / s)), to nearest, ties to even.  A NaN stays one; an infinity makes its block's
+/* Quantisers: over each block s = max|x| fl(1 / 448) (fp32; 1 for a block of zeros, at least 2^-126)
+ * and q = e4m3(x fl(1 / s)), to nearest, ties to even.  A NaN stays one; an infinity makes its block's
  * scale infinite and what the block stands for NaN.  X bf16 or fp32.
  *   rows: blocks of 128 columns of a row (as sbp_rmsnorm_forward_e4m3 leaves Y): Y8 [T, d], scales
- *     [T, ceil(d / 128)].  sbp_e4m3_expand gives the values back.
+ *     [T, ceil(d / 128)].
  *   columns: blocks of 128 tokens, each expert's from its first row on, transposed.  With
  *     nb = sbp_token_blocks(T, E) (the most blocks T rows of E experts can make up) Yt8 is
  *     [d, 128 nb]: the tokens of expert e begin at 128 times the number of blocks of the experts
@@ -431,12 +431,17 @@ int sbp_expert_combine_backward(const void* dY, const void* Ys, const int32_t* r
  *   weight: W [E, N, K] in 128 x 128 tiles of each expert's matrix: W8 [E, N, K] with scales
  *     [E, ceil(N / 128), ceil(K / 128)], and transposed Wt8 [E, K, N] with scales_t
  *     [E, ceil(K / 128), ceil(N / 128)].
- * d must be a multiple of 8; N and K of 16. */
+ *   expand: the values back, Y = q s in bf16 or fp32, rows of any of these arrays with a scale for
+ *     each 128 columns of a row (tiles = 0: scales [T, ceil(d / 128)]) or for each 128 rows x 128
+ *     columns (tiles = 1: [ceil(T / 128), ceil(d / 128)]).
+ * d must be a multiple of 8, at most 2^20; N and K of 16. */
 int64_t sbp_token_blocks(int64_t T, int64_t E);
 int sbp_quant_e4m3_rows(const void* X, int64_t T, int64_t d, int dtype, void* Y8, float* scales, void* stream);
 int sbp_quant_e4m3_columns(const void* X, const int32_t* offsets, int64_t E, int64_t T, int64_t d, int dtype,
                            int tiles, void* Y8, float* scales, void* Yt8, float* scales_t, int32_t* dev_status,
                            void* stream);
+int sbp_quant_e4m3_expand(const void* Y8, const float* scales, int64_t T, int64_t d, int tiles, int dtype, void* Y,
+                          void* stream);
 int sbp_quant_e4m3_weight(const void* W, int64_t E, int64_t N, int64_t K, int dtype, void* W8, float* scales,
                           void* Wt8, float* scales_t, void* stream);
 

@@ -134,8 +134,10 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rmsnorm_fwd(const FwdP p) {
           for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(r[i].v[k]));
         }
         for (int o = min(8, p.lpr / 2); o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        // One division a block and products instead of a division an element (132 us against 87).
-        const float s = e4m3_scale(a), inv = 1.f / s;
+        // 448: e4m3's largest value.  A block of zeros keeps the scale 1; a scale that is not
+        // normal would have no inverse.  One division a
+        // block and products instead of a division an element (132 us against 87).
+        const float s = a > 0.f ? fmaxf(a / 448.f, 1.17549435e-38f) : 1.f, inv = 1.f / s;
         if (v < nvec) {
           uint32_t w2[2];
 #pragma unroll

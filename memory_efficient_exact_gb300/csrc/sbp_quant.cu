@@ -1,7 +1,7 @@
 // Quantisers to 8 bits (e4m3) with one scale for each block of 128 (sm_103a): what the block-scaled
 // product takes.
 //
-//   s = max(max|x| / 448, 2^-126) over the block (1 for a block of zeros),  q = e4m3(x * fl(1 / s))
+//   s = max(max|x| * fl(1 / 448), 2^-126) over the block (1 for a block of zeros),  q = e4m3(x * fl(1 / s))
 //
 //   rows      blocks of 128 columns of a row
 //   columns   blocks of 128 tokens of one column, or tiles of 128 tokens x 128 columns, written
@@ -20,6 +20,12 @@ namespace sbp {
 namespace {
 
 constexpr int64_t MAX_D = 1 << 20;
+
+// The scale of a block whose largest magnitude is `a`.  448: e4m3's largest value.  A block of zeros
+// keeps the scale 1; a scale that is not normal would have no inverse.
+__device__ __forceinline__ float block_scale(float a) {
+  return a > 0.f ? fmaxf(a * (1.f / 448.f), 1.17549435e-38f) : 1.f;
+}
 
 template <typename E>
 __device__ __forceinline__ float amax8(const Raw<E>& r) {
@@ -65,7 +71,7 @@ __global__ void __launch_bounds__(256) k_quant_rows(const RowsP p) {
     float a = amax8(x[i]);
 #pragma unroll
     for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float s = e4m3_scale(a), inv = 1.f / s;
+    const float s = block_scale(a), inv = 1.f / s;
     if (at[i] < 0) continue;
     const F8 f = x[i].f();
     *reinterpret_cast<uint2*>(p.Y8 + at[i]) =
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
       float a = cmax[0][tid];
 #pragma unroll
       for (int w = 1; w < 8; ++w) a = fmaxf(a, cmax[w][tid]);
-      const float s = e4m3_scale(a);
+      const float s = block_scale(a);
       sinv[tid] = 1.f / s;
       if (f0 + tid < p.d) p.scales_t[(int64_t)(f0 + tid) * p.nbt + b] = s;
     }
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
     a = cmax[0][0];
 #pragma unroll
     for (int w = 1; w < 8; ++w) a = fmaxf(a, cmax[0][w]);
-    const float s = e4m3_scale(a);
+    const float s = block_scale(a);
     tinv = 1.f / s;
     if (tid == 0) {
       if (p.wblocks) {
@@ -183,7 +189,7 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
         float a = amax8(x[i]);
 #pragma unroll
         for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const float s = e4m3_scale(a);
+        const float s = block_scale(a);
         inv = 1.f / s;
         if (c8 == 0 && r < rows) p.scales[(row0 + r) * p.nf + f] = s;
       }
@@ -218,6 +224,42 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
       const uint2 lo = tile[r * 16 + ((2 * m) ^ sw)], hi = tile[r * 16 + ((2 * m + 1) ^ sw)];
       *reinterpret_cast<uint4*>(out + (int64_t)(f0 + r) * p.pitch + 16 * m) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
+  }
+}
+
+// Y = q * scale: blocks of `tall` rows x 128 columns, 16 elements a thread (n16 of them a row).
+template <typename O>
+__global__ void __launch_bounds__(256) k_quant_expand(const uint8_t* __restrict__ q, const float* __restrict__ scales,
+                                                      int64_t n, uint32_t n16, int d, int shift, int nblk,
+                                                      O* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const int64_t row = i / n16;
+  const int c = (int)(i - row * n16) * 16;
+  const float s = scales[(row >> shift) * nblk + c / 128];
+  const int64_t at = row * d + c;
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  const uint2 lo = *reinterpret_cast<const uint2*>(q + at);
+  w[0] = lo.x;
+  w[1] = lo.y;
+  const bool two = c + 8 < d;   // d is a multiple of 8
+  if (two) {
+    const uint2 hi = *reinterpret_cast<const uint2*>(q + at + 8);
+    w[2] = hi.x;
+    w[3] = hi.y;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    F8 f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2_raw r =
+          __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[2 * h + k / 2] >> (16 * (k % 2))), __NV_E4M3);
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&r));
+      f.v[2 * k] = x.x * s;
+      f.v[2 * k + 1] = x.y * s;
+    }
+    if (h == 0 || two) store8(out + at + 8 * h, f);
   }
 }
 
@@ -270,6 +312,29 @@ int sbp_quant_e4m3_rows(const void* X, int64_t T, int64_t d, int dtype, void* Y8
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == SBP_BF16) k_quant_rows<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
   else k_quant_rows<float><<<grid, 256, 0, s>>>(p);
+  return launched();
+}
+
+int sbp_quant_e4m3_expand(const void* Y8, const float* scales, int64_t T, int64_t d, int tiles, int dtype, void* Y,
+                          void* stream) {
+  const int rc = quant_check(T, d, dtype);
+  if (rc != SBP_OK) return rc;
+  if ((tiles != 0 && tiles != 1) || (T > 0 && (!Y8 || !scales || !Y))) return SBP_ERR_INVALID_ARG;
+  const int64_t n16 = (d + 15) / 16;
+  if ((T * n16 + 255) / 256 > INT32_MAX) return SBP_ERR_UNSUPPORTED;
+  if (!aligned16(Y8) || !aligned16(Y) || !aligned4(scales)) return SBP_ERR_ALIGNMENT;
+  NvtxRange nv("sbp_quant_e4m3_expand");
+  set_launch_count(0);
+  if (T == 0) return SBP_OK;
+  const unsigned grid = (unsigned)((T * n16 + 255) / 256);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint8_t* q = static_cast<const uint8_t*>(Y8);
+  if (dtype == SBP_BF16)
+    k_quant_expand<<<grid, 256, 0, s>>>(q, scales, T * n16, (uint32_t)n16, (int)d, tiles ? 7 : 0, (int)((d + 127) / 128),
+                                        static_cast<__nv_bfloat16*>(Y));
+  else
+    k_quant_expand<<<grid, 256, 0, s>>>(q, scales, T * n16, (uint32_t)n16, (int)d, tiles ? 7 : 0, (int)((d + 127) / 128),
+                                        static_cast<float*>(Y));
   return launched();
 }
 

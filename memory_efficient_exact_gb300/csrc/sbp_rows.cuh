@@ -50,12 +50,7 @@ __device__ __forceinline__ void store8(float* p, const F8& f) {
   reinterpret_cast<float4*>(p)[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
 }
 
-// The scale of a block whose largest magnitude is `a`, in 8 bits.  448: e4m3's largest value.  A
-// block of zeros keeps the scale 1; a scale that is not normal would have no inverse.
-__device__ __forceinline__ float e4m3_scale(float a) {
-  return a > 0.f ? fmaxf(a / 448.f, 1.17549435e-38f) : 1.f;
-}
-// Four values times the scale's inverse, as e4m3.
+// Four values times a scale's inverse, as e4m3.
 __device__ __forceinline__ uint32_t e4m3_pack(float a, float b, float c, float d, float inv) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);

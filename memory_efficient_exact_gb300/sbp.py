@@ -116,6 +116,8 @@ def _load() -> ctypes.CDLL:
     lib.sbp_quant_e4m3_rows.argtypes = [P, I64, I64, C, P, P, P]
     lib.sbp_quant_e4m3_columns.restype = C
     lib.sbp_quant_e4m3_columns.argtypes = [P, P, I64, I64, I64, C, C, P, P, P, P, P, P]
+    lib.sbp_quant_e4m3_expand.restype = C
+    lib.sbp_quant_e4m3_expand.argtypes = [P, P, I64, I64, C, C, P, P]
     lib.sbp_quant_e4m3_weight.restype = C
     lib.sbp_quant_e4m3_weight.argtypes = [P, I64, I64, I64, C, P, P, P, P, P]
     lib.sbp_matmul_e4m3.restype = C
@@ -907,7 +909,7 @@ def token_blocks(T: int, E: int = 1) -> int:
 
 def quant_e4m3(X, *, Y8=None, scales=None, stream=None) -> dict:
     """X [T, d] bf16 or fp32 in 8 bits (``sbp_quant_e4m3_rows``): Y8 [T, d] e4m3 and scales
-    [T, ceil(d / 128)] fp32, as ``rmsnorm_e4m3`` leaves its Y."""
+    [T, ceil(d / 128)] fp32, laid out as ``rmsnorm_e4m3`` leaves its Y."""
     _on_device(X, Y8, scales)
     if X.dim() != 2:
         raise ValueError("X must be [T, d]")
@@ -950,6 +952,23 @@ def quant_e4m3_columns(X, *, offsets=None, tiles=False, rows=False, Yt8=None, sc
     if rows:
         out.update(Y8=Y8, scales=scales)
     return out
+
+
+def quant_e4m3_expand(Y8, scales, dtype=torch.bfloat16, *, tiles=False, Y=None, stream=None) -> dict:
+    """What the quantisers' outputs stand for (``sbp_quant_e4m3_expand``): Y8 [T, d] with scales
+    [T, ceil(d / 128)], or [ceil(T / 128), ceil(d / 128)] with tiles=True, in bf16 or fp32."""
+    _on_device(Y8, scales, Y)
+    if Y8.dim() != 2 or Y8.dtype != _FP8:
+        raise ValueError("Y8 must be e4m3 [T, d]")
+    T, d = Y8.shape
+    _shaped(scales, ((T + 127) // 128 if tiles else T, (d + 127) // 128), torch.float32, "scales")
+    if Y is None:
+        Y = _empty(stream, (T, d), dtype, Y8.device)
+    elif Y.shape != (T, d):
+        raise ValueError("Y must be shaped like Y8")
+    _check(_lib.sbp_quant_e4m3_expand(_a(Y8), _a(scales), T, d, 1 if tiles else 0, _code(Y), _a(Y),
+                                      _raw(stream, Y8.device)), "sbp_quant_e4m3_expand")
+    return dict(Y=Y)
 
 
 def quant_e4m3_weight(W, *, W8=None, scales=None, Wt8=None, scales_t=None, stream=None) -> dict:

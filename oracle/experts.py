@@ -87,7 +87,7 @@ def block(x):
     """(values in 8 bits, scale) of one block of float32 values."""
     x = np.asarray(x, dtype=np.float32)
     m = np.max(np.abs(x)) if x.size else np.float32(0)
-    s = np.maximum(m / np.float32(448), np.float32(2.0 ** -126)) if m > 0 else np.float32(1)
+    s = np.maximum(m * (np.float32(1) / np.float32(448)), np.float32(2.0 ** -126)) if m > 0 else np.float32(1)
     return round_e4m3(x * (np.float32(1) / s)), s
 
 

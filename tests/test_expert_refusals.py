@@ -30,6 +30,7 @@ COMB = dict(Ys=0x1000, Rows=0x2000, W=0x3000, Res=None, t=4, k=2, n=8, d=64, dt=
 CBWD = dict(DY=0x1000, Ys=0x2000, Rows=0x3000, W=0x4000, t=4, k=2, n=8, d=64, dt=0, DYs=0x5000, DW=0x6000)
 QROWS = dict(X=0x1000, t=4, d=64, dt=0, Y=0x2000, S=0x3000)
 QCOLS = dict(X=0x1000, Off=0x2000, e=2, t=4, d=64, dt=0, tiles=0, Y=None, S=None, Yt=0x3000, St=0x4000, Status=0x5000)
+QEXP = dict(Y8=0x1000, S=0x2000, t=4, d=64, tiles=0, dt=0, Y=0x3000)
 QWEI = dict(W=0x1000, e=2, n=32, k=64, dt=0, W8=0x2000, S=0x3000, Wt=0x4000, St=0x5000)
 MM = dict(A=0x1000, Sa=0x2000, B=0x3000, Sb=0x4000, Off=0x5000, e=2, t=4, n=32, k=64, dt=0, C=0x6000, Status=0x7000)
 MMC = dict(A=0x1000, Sa=0x2000, B=0x3000, Sb=0x4000, Off=0x5000, e=2, t=4, n=32, k=64, DW=0x6000, acc=0,
@@ -63,6 +64,9 @@ def test_calls(sbp):
          [(I, dict(t=-1)), (I, dict(d=0)), (I, dict(dt=2)), (I, dict(e=0)), (U, dict(e=1025)), (I, dict(Off=None)), (I, dict(tiles=2)),
           (U, dict(d=12)), (I, dict(X=None)), (I, dict(Yt=None)), (I, dict(St=None)), (I, dict(Status=None)), (I, dict(Y=0x8000)),
           (I, dict(S=0x8000)), (L, dict(Yt=0x3008)), (L, dict(Off=0x2001))]),
+        (sbp._lib.sbp_quant_e4m3_expand, QEXP,
+         [(I, dict(t=-1)), (I, dict(d=0)), (I, dict(dt=2)), (I, dict(tiles=2)), (U, dict(d=12)), (U, dict(d=(1 << 20) + 8)),
+          (I, dict(Y8=None)), (I, dict(S=None)), (I, dict(Y=None)), (L, dict(Y8=0x1004)), (L, dict(Y=0x3008)), (L, dict(S=0x2002))]),
         (sbp._lib.sbp_quant_e4m3_weight, QWEI,
          [(I, dict(e=0)), (I, dict(n=0)), (I, dict(k=0)), (I, dict(dt=2)), (U, dict(e=1025)), (U, dict(n=24)), (U, dict(k=72)),
           (I, dict(W=None)), (I, dict(W8=None)), (I, dict(Wt=None)), (I, dict(S=None)), (I, dict(St=None)), (L, dict(Wt=0x4008))]),
@@ -108,7 +112,7 @@ def test_binding_refuses_host_tensors_and_shapes(sbp):
     x, r = torch.zeros((4, 64), dtype=bf), torch.zeros((4, 2), dtype=torch.int32)
     for f in [lambda: sbp.expert_sort(ids, 4), lambda: sbp.expert_gather(x, r), lambda: sbp.expert_combine(x, r),
               lambda: sbp.expert_combine_backward(x, x, r, torch.zeros(4, 2)), lambda: sbp.quant_e4m3(x),
-              lambda: sbp.quant_e4m3_columns(x), lambda: sbp.quant_e4m3_weight(x),
+              lambda: sbp.quant_e4m3_columns(x), lambda: sbp.quant_e4m3_weight(x), lambda: sbp.quant_e4m3_expand(x.to(f8), torch.zeros(4, 1)),
               lambda: sbp.matmul_e4m3(x.to(f8), torch.zeros(4, 1), x.to(f8), torch.zeros(1, 1)),
               lambda: sbp.matmul_e4m3_columns(x.to(f8), torch.zeros(4, 1), x.to(f8), torch.zeros(1, 1), 4)]:
         with pytest.raises(ValueError):

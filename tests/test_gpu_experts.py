@@ -200,7 +200,7 @@ def test_quant_extremes(sbp):
         wq, ws = X.quant(x[i:i + 1])
         assert np.array_equal(q[i:i + 1], wq) and np.array_equal(s[i:i + 1], ws.astype(np.float64)), i
     assert np.isinf(s[2, 1]) and s[2, 0] == 1 and np.isnan(q[2, 130] * s[2, 1]) and np.isnan(q[3, 0])
-    assert s[3, 0] == np.float32(2.0) / np.float32(448.0) and q[3, 1] == 448
+    assert s[3, 0] == np.float32(2.0) * (np.float32(1.0) / np.float32(448.0)) and q[3, 1] == 448
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -237,6 +237,17 @@ def test_quant_weight(sbp, E, N, K, dtype):
         at = (lambda t: host(t)[e]) if E else host
         assert np.array_equal(at(r["W8"]), q) and np.array_equal(at(r["scales"]), s.astype(np.float64))
         assert np.array_equal(at(r["Wt8"]), q.T) and np.array_equal(at(r["scales_t"]), s.T.astype(np.float64))
+
+
+@pytest.mark.parametrize("T,d,tiles", [(1, 8, False), (5, 136, False), (9, 24, True), (130, 264, True), (300, 2568, False), (2, 20480, False),
+                                       (257, 20488, True)])
+def test_expand(sbp, T, d, tiles):
+    g = np.random.default_rng(T + d)
+    q, s = X.quant(wide(g, (T, d), "fp32"), 128 if tiles else 1)
+    v = (q.astype(np.float32) * X.expand(np.ones_like(q), s, 128 if tiles else 1).astype(np.float32))
+    for ty in (F32, BF):
+        y = sbp.quant_e4m3_expand(dev(q, F8), dev(s, F32), ty, tiles=tiles)["Y"]
+        assert torch.equal(y, torch.from_numpy(v).cuda().to(ty))
 
 
 # ------------------------------------------------------------------------------ products
