@@ -226,10 +226,9 @@ def _own(s, case):
         g = sbp.quant_e4m3_columns(s["dY"], offsets=s["offsets"], rows=True)
         x = sbp.quant_e4m3_columns(s["X"], offsets=s["offsets"], tiles=True)
         m = sum((n + 127) // 128 for n in s["lens"])     # blocks of tokens in use
-        each = x["scales_t"].repeat_interleave(128, dim=0)[:case["d"]].contiguous()
         return [sbp.e4m3_expand(g["Y8"], g["scales"], BF16)["Y"], g["scales"],
-                sbp.e4m3_expand(g["Yt8"], g["scales_t"], BF16)["Y"][:, :128 * m], g["scales_t"][:, :m],
-                sbp.e4m3_expand(x["Yt8"], each, BF16)["Y"][:, :128 * m], x["scales_t"][:, :m]]
+                sbp.quant_e4m3_expand(g["Yt8"], g["scales_t"], BF16)["Y"][:, :128 * m], g["scales_t"][:, :m],
+                sbp.quant_e4m3_expand(x["Yt8"], x["scales_t"], BF16, tiles=True)["Y"][:, :128 * m], x["scales_t"][:, :m]]
     if case["op"] == "product":
         return sbp.matmul_e4m3(s["A8"], s["sa"], s["B8"], s["sb"], offsets=s["offsets"],
                                dtype=BF16 if case["out"] == "bf16" else FP32)["C"]
