@@ -11,7 +11,6 @@
 
 #include "sbp_groups.cuh"
 #include "sbp_mm8.cuh"
-#include "sbp_rows.cuh"
 #include "sbp_tc_common.cuh"
 
 namespace sbp {
@@ -149,6 +148,15 @@ cudaError_t few(const P& p, cudaStream_t s) {
   return launch_few<4>(p, units, s);
 }
 
+// Few rows an expert: k_mm8_few, which reads B at the memory's rate; else the tensor cores' tiles.
+bool is_few(const P& p) { return p.columns ? p.na <= 32 : p.T <= 32 * (int64_t)p.E; }
+
+int run(const P& p, cudaStream_t s) {
+  if ((is_few(p) ? few(p, s) : many(p, s)) != cudaSuccess) return SBP_ERR_CUDA;
+  set_launch_count(1);
+  return SBP_OK;
+}
+
 int check_common(int64_t E, int64_t T, int64_t N, int64_t K, const void* A8, const void* sa, const void* B8,
                  const void* sb, const int32_t* offsets, const void* C, const int32_t* status) {
   for (const void* q : {A8, B8, C})
@@ -180,16 +188,14 @@ int sbp_matmul_e4m3(const void* A8, const float* sa, const void* B8, const float
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   set_launch_count(0);
   if (T == 0) return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? SBP_OK : SBP_ERR_CUDA;
-  mm8::P p;
+  mm8::P p{};
   const int64_t kb = (K + 127) / 128, nb = (N + 127) / 128;
   p.A = static_cast<const uint8_t*>(A8); p.sa = sa; p.lda = K; p.sa_pitch = kb;
   p.B = static_cast<const uint8_t*>(B8); p.sb = sb; p.ldb = K; p.sb_pitch = kb;
   p.b_stride = N * K; p.sb_stride = nb * kb; p.c_stride = 0;
   p.offsets = offsets; p.E = (int)E; p.T = T; p.na = 0; p.nb = (int)N; p.K = K; p.kblocks = (int)kb;
   p.columns = 0; p.out = out_dtype; p.accumulate = 0; p.C = C; p.status = dev_status;
-  if (mm8::few(p, s) != cudaSuccess) return SBP_ERR_CUDA;
-  set_launch_count(1);
-  return SBP_OK;
+  return mm8::run(p, s);
 }
 
 int sbp_matmul_e4m3_columns(const void* At8, const float* sat, const void* Bt8, const float* sbt,
@@ -209,16 +215,14 @@ int sbp_matmul_e4m3_columns(const void* At8, const float* sat, const void* Bt8, 
     if (!accumulate && cudaMemsetAsync(dW, 0, (size_t)E * N * K * sizeof(float), s) != cudaSuccess) return SBP_ERR_CUDA;
     return SBP_OK;
   }
-  mm8::P p;
+  mm8::P p{};
   const int64_t blocks = max_units(T, E, 128);
   p.A = static_cast<const uint8_t*>(At8); p.sa = sat; p.lda = blocks * 128; p.sa_pitch = blocks;
   p.B = static_cast<const uint8_t*>(Bt8); p.sb = sbt; p.ldb = blocks * 128; p.sb_pitch = blocks;
   p.b_stride = 0; p.sb_stride = 0; p.c_stride = N * K;
   p.offsets = offsets; p.E = (int)E; p.T = T; p.na = (int)N; p.nb = (int)K; p.K = blocks * 128; p.kblocks = (int)blocks;
   p.columns = 1; p.out = SBP_FP32; p.accumulate = accumulate ? 1 : 0; p.C = dW; p.status = dev_status;
-  if (mm8::few(p, s) != cudaSuccess) return SBP_ERR_CUDA;
-  set_launch_count(1);
-  return SBP_OK;
+  return mm8::run(p, s);
 }
 
 }  // extern "C"

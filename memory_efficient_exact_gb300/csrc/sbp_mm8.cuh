@@ -63,5 +63,8 @@ __device__ __forceinline__ Unit unit_of(const P& p, int unit, int u) {
   return w;
 }
 
+// The kernel for many rows (sbp_mm8_tc.cu): enqueues the status word's reset and the product.
+cudaError_t many(const P& p, cudaStream_t s);
+
 }  // namespace mm8
 }  // namespace sbp

@@ -341,7 +341,8 @@ __device__ __forceinline__ void fail(Ctrl* c, int32_t* status) {
   if (status) atomicCAS(status, 0, SBP_ERR_TIMEOUT);
 }
 
-__device__ __forceinline__ void prologue(Ctrl* c, int warp) {
+// epi_warps: the epilogue warps of one CTA, which release an accumulator.
+__device__ __forceinline__ void prologue(Ctrl* c, int warp, int epi_warps = NUM_EPI_WARPS) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&c->full[i], 1);
@@ -349,7 +350,7 @@ __device__ __forceinline__ void prologue(Ctrl* c, int warp) {
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->tfull[i], 1);
-      mbar_init(&c->tempty[i], 2 * NUM_EPI_WARPS);
+      mbar_init(&c->tempty[i], 2 * epi_warps);
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&c->rfull[i], 1);
