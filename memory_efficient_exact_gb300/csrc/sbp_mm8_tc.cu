@@ -1,21 +1,32 @@
 // The block-scaled 8-bit product on tcgen05 (sm_103a): many rows.
 //
-// SM pairs compute 256 x 256 tiles of C; one stage of the operand ring is one block of 128 of the
-// sum, which is also one 128-byte swizzled row.  Tensor memory holds one block's sum at a time, in
-// two buffers: the epilogue warps read each block's 128 x 256 accumulators out, scale them by
-// sa[row] sb[column block] and add them to the tile's sums, which stay in their registers (128 a
-// thread), while the next block is multiplied.  Roles, pair protocol and bounded waits are those
-// of the LM-head kernels.
+// SM pairs compute tiles of 256 rows x 128 HALVES columns of C; one stage of the operand ring is one
+// block of 128 of the sum, which is also one 128-byte swizzled row.  Tensor memory holds sums of
+// single blocks, four accumulators of 128 columns in turn: the epilogue warps read each out, give
+// it back, and add it, times sa[row] sb[column block], to the tile's sums in their registers.
+//
+// What bounds it is not the products (512 cycles a block of a 256 x 256 tile) but this exchange:
+// 512 columns of tensor memory are in flight, and an accumulator takes some 1700 cycles from the
+// products' issue over the commit, the read and the arrival of both CTAs' warps to the next issue
+// (850 a block); the additions come on top in part (1080).  Hence the shape of the loops: two warps
+// issue, so that one tests its barriers while the other's products run; an epilogue warp asks for
+// its whole share of an accumulator at once (64 registers) and releases it before it adds anything
+// up; its loop is unrolled over the accumulators with no branches but the waits'; the scales are
+// multiplied and put in place by a warp of their own.  16384 x 24576 x 4096: 4130 us with two
+// accumulators of 256 columns, 16 epilogue warps that loaded 16 columns at a time and scales read
+// by each; 1785 with four accumulators of 128 and the scales' warp; 1717 with two issuing warps;
+// 1383 with eight epilogue warps of 224 registers and the unrolled loop; 1350 with the scales
+// multiplied in advance (2440 TFLOP/s; 1066 without the additions).  Not faster: packed additions of two values (1599
+// against 1620 TFLOP/s in an earlier form), 16 epilogue warps (1405), the next accumulator's load
+// before this one's additions (1456, and 1946 against 1453 with narrow tiles).
+#include <algorithm>
+
 #include "sbp_mm8.cuh"
 #include "sbp_rows.cuh"
 #include "sbp_tc_common.cuh"
 
 namespace sbp {
 namespace tc {
-
-// Instruction descriptor of tcgen05.mma kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B e4m3 (bits
-// 7-9 and 10-12 = 0), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
-constexpr uint32_t IDESC_E4M3 = (1u << 4) | (uint32_t(256 >> 3) << 17) | (uint32_t(256 >> 4) << 24);
 
 __device__ __forceinline__ void mma2_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -25,45 +36,81 @@ __device__ __forceinline__ void mma2_e4m3(uint32_t d_tmem, uint64_t a, uint64_t 
       : "memory");
 }
 
-// Warp 0 loads, warp 1 multiplies, warps 4 to 19 are the epilogue's: 32 rows x 64 columns each, so
-// that a thread's 64 sums fit into the 96 registers that 640 threads may have.
-constexpr int MM8_EPI = 16, MM8_THREADS = 128 + 32 * MM8_EPI;
+// Warp 0 loads the operands, warps 1 and 2 multiply, warp 3 loads the scales, warps 4 to 11 are the
+// epilogue's: 32 rows x 64 columns of each accumulator.  The block's 12 x 32 threads are launched
+// with 168 registers each; the epilogue's 128 sums and 64 values in flight need more, so the first
+// four warps hand theirs over.  (Waits are inlined: a call would not know of the split.)
+constexpr int MM8_EPI = 8, MM8_THREADS = 128 + 32 * MM8_EPI;
+constexpr int REGS_LAUNCH = 168, REGS_FEW = 56, REGS_MANY = 224;
+static_assert(128 * REGS_FEW + 32 * MM8_EPI * REGS_MANY <= MM8_THREADS * REGS_LAUNCH, "no more than the block has");
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// blocks of 128 of both operands in shared memory: 32 KB each, or 24 KB with half the columns
+constexpr int mm8_stages(int halves) { return halves == 2 ? 6 : 8; }
+constexpr uint32_t mm8_stage_bytes(int halves) { return A_BYTES + halves * B_BYTES / 2; }
+constexpr int BUFS = 4, BUF_N = 128;     // accumulators of one block: 128 columns each
+constexpr int SC_KB = 4;                 // blocks of a stage of the scales' ring
+constexpr uint32_t STG_MM8 = 32 * 64;    // a warp's staging block: 32 rows of 64 bytes
+// Instruction descriptor of tcgen05.mma kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B e4m3 (bits
+// 7-9 and 10-12 = 0), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
+constexpr uint32_t IDESC_E4M3 = (1u << 4) | (uint32_t(BUF_N >> 3) << 17) | (uint32_t(256 >> 4) << 24);
+
+struct Mm8Ctrl {
+  uint64_t full[8], empty[8];
+  uint64_t tfull[BUFS], tempty_l[BUFS], tempty_r[BUFS];   // released by the leader's own warps, by the other CTA's
+  uint64_t sfull[2], sempty[2];
+  uint64_t mdone[2];
+  uint32_t tmem_base;
+  int abort;
+  float4 scale[2][2][128];   // [stage][column block][row]: SC_KB blocks
+};
+constexpr size_t SMEM_MM8 = 6 * STAGE_BYTES + MM8_EPI * STG_MM8 + sizeof(Mm8Ctrl) + 1024;
+static_assert(mm8_stages(1) * mm8_stage_bytes(1) == 6 * STAGE_BYTES && mm8_stages(2) * mm8_stage_bytes(2) == 6 * STAGE_BYTES &&
+                  SMEM_MM8 <= 232448,
+              "shared memory budget of one CTA");
+
+__device__ __forceinline__ void fail_mm8(Mm8Ctrl* c, int32_t* status) {
+  *(volatile int*)&c->abort = 1;
+  if (status) atomicCAS(status, 0, SBP_ERR_TIMEOUT);
 }
-
-constexpr uint32_t STG_MM8 = 32 * 64;   // a warp's staging block: 32 rows of 64 bytes
-constexpr size_t SMEM_MM8 = STAGES * STAGE_BYTES + MM8_EPI * STG_MM8 + sizeof(Ctrl) + 1024;
-static_assert(SMEM_MM8 <= 232448, "shared memory budget of one CTA");
+// An arrival on a barrier of this CTA, or on one of the pair's (no branch).
+__device__ __forceinline__ void arrive_if(bool here, uint32_t local, bool there, uint32_t remote) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t@q mbarrier.arrive.shared::cluster.b64 _, [%3];\n\t}" ::"r"(
+          (int)here),
+      "r"(local), "r"((int)there), "r"(remote)
+      : "memory");
+}
+template <bool CLUSTER>
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, Mm8Ctrl* c, uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_inl<CLUSTER>(b, parity & 1u, &c->abort, limit));
+}
 // Tiles are walked in bands of this many units of 256 rows, all columns of a band before the next:
-// the 76 pairs' tiles then share 8 blocks of A's rows and 9 or 10 of B's.
+// the 76 pairs' tiles then share 8 blocks of A's rows and 9 or 10 of B's.  (16: 2% slower.)
 constexpr int BAND = 8;
 
 struct Tile {
   mm8::Unit w;
   int n0;
 };
-__device__ __forceinline__ Tile tile_of(const mm8::P& p, int units, int ntn, int t) {
+__device__ __forceinline__ Tile tile_of(const mm8::P& p, int units, int ntn, int bn, int t) {
   const int band = t / (BAND * ntn), r = t - band * BAND * ntn;
   const int high = min(BAND, units - band * BAND);
   Tile o;
   o.w = mm8::unit_of(p, 256, band * BAND + r % high);
-  o.n0 = r / high * BN;
+  o.n0 = r / high * bn;
   return o;
 }
 
-template <int OUT, bool ACC>
+template <int HALVES, int OUT, bool ACC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
     k_mm8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const mm8::P p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* stg_base = base + STAGES * STAGE_BYTES;
-  Ctrl* c = reinterpret_cast<Ctrl*>(stg_base + MM8_EPI * STG_MM8);
+  constexpr int MM8_STAGES = mm8_stages(HALVES);
+  constexpr uint32_t STAGE = mm8_stage_bytes(HALVES);
+  uint8_t* stg_base = base + MM8_STAGES * STAGE;
+  Mm8Ctrl* c = reinterpret_cast<Mm8Ctrl*>(stg_base + MM8_EPI * STG_MM8);
   const int warp = uniform_warp(), lane = threadIdx.x % 32;
   const uint32_t rank = ctarank();
   const Group first = find_unit(p.offsets, p.E, p.T, p.columns ? 128 : 256, 0);
@@ -72,132 +119,233 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
     return;
   }
   const int units = p.columns ? p.E * ((p.na + 255) / 256) : first.total;
-  const int ntn = (p.nb + BN - 1) / BN;
+  const int ntn = (p.nb + 128 * HALVES - 1) / (128 * HALVES);
   const int total = units * ntn;
   const int pid = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  prologue(c, warp, MM8_EPI);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < MM8_STAGES; ++i) {
+      mbar_init(&c->full[i], 1);
+      mbar_init(&c->empty[i], HALVES);
+    }
+    for (int i = 0; i < BUFS; ++i) {
+      mbar_init(&c->tfull[i], 1);
+      mbar_init(&c->tempty_l[i], MM8_EPI);
+      mbar_init(&c->tempty_r[i], MM8_EPI);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c->sfull[i], 1);
+      mbar_init(&c->mdone[i], 1);
+      mbar_init(&c->sempty[i], MM8_EPI);
+    }
+    c->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&c->tmem_base)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
   const uint32_t tmem = c->tmem_base;
 
-  if (warp == 0) {
-    int stage = 0;
-    uint32_t phase = 0, issued = 0, last = 0;   // stages in use, the parity of each one's last use
-    if (lane == 0) {
-      prefetch_map(&tmA);
-      prefetch_map(&tmB);
-    }
-    for (int t = pid; t < total; t += npairs) {
-      const Tile o = tile_of(p, units, ntn, t);
+  // The accumulators a block uses: buffers HALVES g and on, group g counting from 0 with each tile.
+  constexpr int GROUPS = BUFS / HALVES;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FEW));
+    if (warp == 0) {
+      // (the warp stays converged and one elected lane issues, with operands that the compiler can
+      // keep uniform)
+      uint32_t stage = 0, phase = 0, issued = 0, last = 0;   // stages in use, the parity of each one's last use
       bool ok = true;
       if (lane == 0) {
-        const int arow = o.w.row0 + (int)rank * 128;
-        const int brow = (p.columns ? 0 : o.w.e * p.nb) + o.n0 + (int)rank * 128;
-        for (int kb = o.w.kb0; kb < o.w.kb1; ++kb) {
-          if (!wait_inl<false>(&c->empty[stage], phase ^ 1u, &c->abort, p.limit_ns)) { ok = false; break; }
-          const uint32_t sa = saddr(base + stage * STAGE_BYTES), sb = sa + A_BYTES;
-          const uint32_t fb = mapa(saddr(&c->full[stage]), 0);
-          if (rank == 0) mbar_expect_tx(&c->full[stage], PAIR_TX);
-          tma_load_2d_pair(sa, &tmA, fb, kb * 128, arow);
-          tma_load_2d_pair(sb, &tmB, fb, kb * 128, brow);
+        prefetch_map(&tmA);
+        prefetch_map(&tmB);
+      }
+      const uint32_t ring = saddr(base), fb = mapa(saddr(&c->full[0]), 0);
+      for (int t = pid; t < total && ok; t += npairs) {
+        const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
+        const int arow = __shfl_sync(0xffffffffu, o.w.row0 + (int)rank * 128, 0);
+        // of each 128 of the tile's columns, this CTA's 64 rows of B
+        const int brow = __shfl_sync(0xffffffffu, (p.columns ? 0 : o.w.e * p.nb) + o.n0 + (int)rank * 64, 0);
+        const int kb1 = __shfl_sync(0xffffffffu, o.w.kb1, 0);
+        for (int kb = __shfl_sync(0xffffffffu, o.w.kb0, 0); kb < kb1; ++kb) {
+          ok = warp_wait<false>(&c->empty[stage], phase ^ 1u, c, p.limit_ns);
+          if (!ok) break;
+          if (elect_one()) {
+            const uint32_t sa = ring + stage * STAGE, sb = sa + A_BYTES, bar = fb + stage * (uint32_t)sizeof(uint64_t);
+            if (rank == 0) mbar_expect_tx(&c->full[stage], 2 * STAGE);
+            tma_load_2d_pair(sa, &tmA, bar, kb * 128, arow);
+            tma_load_2d_pair(sb, &tmB, bar, kb * 128, brow);
+            if (HALVES == 2) tma_load_2d_pair(sb + B_BYTES / 2, &tmB, bar, kb * 128, brow + 128);
+          }
           issued |= 1u << stage;
           last = (last & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-        }
-        if (!ok) {
-          fail(c, p.status);
-          if (rank == 0) {   // no copy may be in flight when the block ends
-#pragma unroll
-            for (int i = 0; i < STAGES; ++i)
-              if (issued & (1u << i)) wait_inl<false>(&c->full[i], (last >> i) & 1u, nullptr, 200000000ull);
-          }
-        }
-      }
-      if (!__shfl_sync(0xffffffffu, (int)ok, 0)) break;
-    }
-  } else if (warp == 1) {
-    if (rank == 0) {
-      int stage = 0;
-      uint32_t phase = 0, it = 0;   // it: blocks multiplied so far
-      bool ok = true;
-      for (int t = pid; t < total && ok; t += npairs) {
-        const Tile o = tile_of(p, units, ntn, t);
-        for (int kb = o.w.kb0; kb < o.w.kb1; ++kb, ++it) {
-          const int buf = it & 1;
-          ok = wait_inl<true>(&c->tempty[buf], ((it >> 1) & 1u) ^ 1u, &c->abort, p.limit_ns) &&
-               wait_inl<false>(&c->full[stage], phase, &c->abort, p.limit_ns);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t sa = saddr(base + stage * STAGE_BYTES), sb = sa + A_BYTES;
-            const uint32_t dt = tmem + (uint32_t)(buf * BN);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma2_e4m3(dt, sw128_desc(sa + k * 32, 16, 1024), sw128_desc(sb + k * 32, 16, 1024), IDESC_E4M3, k != 0);
-            commit2_mc(&c->empty[stage], 3);
-            commit2_mc(&c->tfull[buf], 3);
-          }
-          __syncwarp();
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-        }
-      }
-      if (lane == 0) {
-        if (!ok) fail(c, p.status);
-        commit2_mc(&c->mdone, 1);
-        wait_inl<false>(&c->mdone, 0, nullptr, 200000000ull);
-      }
-      __syncwarp();
-    }
-  } else if (warp >= 4) {
-    const int q = warp & 3, h = (warp - 4) >> 2;
-    const uint32_t stg = saddr(stg_base + (warp - 4) * STG_MM8);
-    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 64);
-    const uint32_t te0 = mapa(saddr(&c->tempty[0]), 0), te1 = mapa(saddr(&c->tempty[1]), 0);
-    uint32_t it = 0;
-    bool ok = true;
-    for (int t = pid; t < total && ok; t += npairs) {
-      const Tile o = tile_of(p, units, ntn, t);
-      const int r0 = (int)rank * 128 + q * 32;            // this warp's first row of the unit
-      const int rows = min(32, o.w.rows - r0);            // how many of them are (may be none)
-      const float* sa = p.sa + (int64_t)(o.w.row0 + min(r0 + lane, o.w.rows - 1)) * p.sa_pitch;
-      const int nb128 = min(o.n0 / 128 + h / 2, (p.nb - 1) / 128);
-      const float* sb = p.sb + (int64_t)o.w.e * p.sb_stride + (int64_t)nb128 * p.sb_pitch;
-      float2 acc[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.f, 0.f);
-      // scales two blocks ahead
-      const int k0 = o.w.kb0, k1 = o.w.kb1;
-      float s0 = k0 < k1 ? sa[k0] * sb[k0] : 0.f;
-      float a1 = k0 + 1 < k1 ? sa[k0 + 1] : 0.f, b1 = k0 + 1 < k1 ? sb[k0 + 1] : 0.f;
-      for (int kb = k0; kb < k1; ++kb, ++it) {
-        const float s = s0;
-        s0 = a1 * b1;
-        if (kb + 2 < k1) {
-          a1 = sa[kb + 2];
-          b1 = sb[kb + 2];
-        }
-        const int buf = it & 1;
-        ok = __all_sync(0xffffffffu, wait_inl<true>(&c->tfull[buf], (it >> 1) & 1u, &c->abort, p.limit_ns));
-        if (!ok) break;
-        tc_fence_after();
-        const float2 s2 = make_float2(s, s);
-        const uint32_t tc = tb + (uint32_t)(buf * BN);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t r[16];
-          tmem_ld16(tc + (uint32_t)(16 * j), r);
-          tmem_ld_wait();
-          if (j == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_remote(buf ? te1 : te0);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc[8 * j + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2, acc[8 * j + i]);
+          if (++stage == MM8_STAGES) { stage = 0; phase ^= 1u; }
         }
       }
       if (!ok) {
-        if (lane == 0) fail(c, p.status);
+        if (lane == 0) fail_mm8(c, p.status);
+        if (rank == 0) {   // no copy may be in flight when the block ends
+          for (int i = 0; i < MM8_STAGES; ++i)
+            if (issued & (1u << i)) wait_inl<false>(&c->full[i], (last >> i) & 1u, nullptr, 200000000ull);
+        }
+        __syncwarp();
+      }
+    } else if (warp < 3) {
+      // Two warps issue: one the first 128 columns of each tile and the other the second, or, with
+      // one accumulator a block, every other block.  While one's products run, the other tests its
+      // barriers.
+      if (rank == 0) {
+        const int j = warp - 1;
+        uint32_t done = 0, use = 15;   // blocks of the tiles before; the parity of each group's last release
+        bool ok = true;
+        for (int t = pid; t < total && ok; t += npairs) {
+          const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
+          const int nkb = o.w.kb1 - o.w.kb0;
+          for (int kb = HALVES == 2 ? 0 : j; kb < nkb; kb += HALVES == 2 ? 1 : 2) {
+            const uint32_t n = done + kb, stage = n % MM8_STAGES, phase = (n / MM8_STAGES) & 1u;
+            const uint32_t sa = saddr(base + stage * STAGE), sb = sa + A_BYTES + (HALVES == 2 ? j * (B_BYTES / 2) : 0);
+            const uint32_t g = (uint32_t)kb % GROUPS, buf = HALVES == 2 ? HALVES * g + j : g, ep = (use >> g) & 1u;
+            use ^= 1u << g;
+            // the tests go out together; only what is not there yet is waited for
+            const bool tl = mbar_test<false>(&c->tempty_l[buf], ep), tr = mbar_test<true>(&c->tempty_r[buf], ep);
+            const bool tf = mbar_test<false>(&c->full[stage], phase);
+            if (!__all_sync(0xffffffffu, tl && tr && tf))
+              ok = warp_wait<false>(&c->tempty_l[buf], ep, c, p.limit_ns) &&
+                   warp_wait<true>(&c->tempty_r[buf], ep, c, p.limit_ns) &&
+                   warp_wait<false>(&c->full[stage], phase, c, p.limit_ns);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma2_e4m3(tmem + buf * BUF_N, sw128_desc(sa + k * 32, 16, 1024), sw128_desc(sb + k * 32, 16, 1024),
+                          IDESC_E4M3, k != 0);
+              commit2_mc(&c->tfull[buf], 3);
+              commit2_mc(&c->empty[stage], 3);
+            }
+            __syncwarp();
+          }
+          done += (uint32_t)nkb;
+        }
+        if (lane == 0 && !ok) fail_mm8(c, p.status);
+        __syncwarp();
+        if (elect_one()) commit2_mc(&c->mdone[j], 1);
+        wait_inl<false>(&c->mdone[j], 0, nullptr, 200000000ull);
+        __syncwarp();
+      }
+    } else {
+      // scales: SC_KB blocks of this CTA's 128 rows at a time, four rows a lane, times those of the
+      // tile's column blocks.  All loads of a stage are in flight together, before its place is
+      // waited for: with a row after the other they took 1000 cycles a block and set the pace.
+      uint32_t n = 0;
+      bool ok = true;
+      const bool quads = p.sa_pitch % SC_KB == 0 && reinterpret_cast<uintptr_t>(p.sa) % 16 == 0;
+      for (int t = pid; t < total && ok; t += npairs) {
+        const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
+        const float* sa[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sa[i] = p.sa + (int64_t)(o.w.row0 + min((int)rank * 128 + lane + 32 * i, o.w.rows - 1)) * p.sa_pitch;
+        const float* sb0 = p.sb + (int64_t)o.w.e * p.sb_stride + (int64_t)(o.n0 / 128) * p.sb_pitch;
+        const float* sb1 = HALVES == 2 && o.n0 + 128 < p.nb ? sb0 + p.sb_pitch : sb0;
+        for (int kb = o.w.kb0; kb < o.w.kb1; kb += SC_KB, ++n) {
+          const uint32_t s = n & 1u;
+          const int left = o.w.kb1 - kb;
+          auto four = [&](const float* q) {
+            return make_float4(q[0], left > 1 ? q[1] : 0.f, left > 2 ? q[2] : 0.f, left > 3 ? q[3] : 0.f);
+          };
+          float4 x[4];
+          if (quads && kb % SC_KB == 0 && left >= SC_KB) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(sa[i] + kb);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = four(sa[i] + kb);
+          }
+          const float4 b0 = four(sb0 + kb), b1 = HALVES == 2 ? four(sb1 + kb) : b0;
+          ok = warp_wait<false>(&c->sempty[s], ((n >> 1) & 1u) ^ 1u, c, p.limit_ns);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            c->scale[s][0][lane + 32 * i] = make_float4(x[i].x * b0.x, x[i].y * b0.y, x[i].z * b0.z, x[i].w * b0.w);
+            if (HALVES == 2)
+              c->scale[s][1][lane + 32 * i] = make_float4(x[i].x * b1.x, x[i].y * b1.y, x[i].z * b1.z, x[i].w * b1.w);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->sfull[s]);
+        }
+      }
+      if (!ok && lane == 0) fail_mm8(c, p.status);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_MANY));
+    // warps 4 to 7: the first 64 columns of each accumulator, warps 8 to 11: the second
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t stg = saddr(stg_base + (warp - 4) * STG_MM8);
+    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 64);
+    // where this warp's lane 0 says that it has read an accumulator: on the leader's barrier for its
+    // own warps or for the other CTA's
+    const bool p0 = lane == 0 && rank == 0, p1 = lane == 0 && rank != 0;
+    const uint32_t rel_l = saddr(&c->tempty_l[0]), rel_r = mapa(saddr(&c->tempty_r[0]), 0);
+    uint32_t n = 0, use = 0;   // stages of scales so far; the parity of each group's next accumulators
+    bool ok = true;
+    for (int t = pid; t < total && ok; t += npairs) {
+      const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
+      const int r0 = (int)rank * 128 + q * 32;            // this warp's first row of the unit
+      const int rows = min(32, o.w.rows - r0);            // how many of them are (may be none)
+      float acc[HALVES][64];
+#pragma unroll
+      for (int j = 0; j < HALVES; ++j)
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[j][i] = 0.f;
+      for (int kb = o.w.kb0; kb < o.w.kb1; kb += SC_KB, ++n) {
+        const uint32_t ss = n & 1u;
+        ok = wait_inl<false>(&c->sfull[ss], (n >> 1) & 1u, &c->abort, p.limit_ns) && ok;
+        float sk[HALVES][SC_KB];
+#pragma unroll
+        for (int j = 0; j < HALVES; ++j) {
+          const float4 v = c->scale[ss][j][q * 32 + lane];
+          sk[j][0] = v.x;
+          sk[j][1] = v.y;
+          sk[j][2] = v.z;
+          sk[j][3] = v.w;
+        }
+        __syncwarp();
+        arrive_if(lane == 0, saddr(&c->sempty[ss]), false, 0);
+#pragma unroll
+        for (int k = 0; k < SC_KB; ++k) {
+          if (kb + k >= o.w.kb1) break;
+#pragma unroll
+          for (int j = 0; j < HALVES; ++j) {
+            constexpr uint32_t S = sizeof(uint64_t);
+            const uint32_t g = k % GROUPS, buf = HALVES * g + j;
+            ok = wait_inl<false>(&c->tfull[buf], (use >> g) & 1u, &c->abort, p.limit_ns) && ok;
+            __syncwarp();
+            tc_fence_after();
+            uint32_t r[2][32];
+            tmem_ld32(tb + buf * BUF_N, r[0]);
+            tmem_ld32(tb + buf * BUF_N + 32, r[1]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            arrive_if(p0, rel_l + buf * S, p1, rel_r + buf * S);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                acc[j][32 * x + i] = fmaf(__uint_as_float(r[x][i]), sk[j][k], acc[j][32 * x + i]);
+          }
+          use ^= 1u << (k % GROUPS);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) fail_mm8(c, p.status);
         break;
       }
       // the tile's sums leave through the staging block, so that a warp writes 64-byte pieces of
@@ -205,7 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
       // at chunk k ^ (r / 2 % 4), without bank conflicts either way
       constexpr int ES = OUT == SBP_BF16 ? 2 : 4, PASS = 64 / ES;   // columns a pass
 #pragma unroll
-      for (int g = 0; g < 64 / PASS; ++g) {
+      for (int gg = 0; gg < HALVES * 64 / PASS; ++gg) {
+        const int j = gg / (64 / PASS), g = gg % (64 / PASS);
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -213,17 +362,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (OUT == SBP_BF16) {
-              const float2 f = acc[g * PASS / 2 + 4 * k + i];
+              const int ai = g * PASS + 8 * k + 2 * i;
+              const float2 f = make_float2(acc[j][ai], acc[j][ai + 1]);
               v[i] = pack_bf16(f.x, f.y);
             } else {
-              const float2 f = acc[g * PASS / 2 + 2 * k + i / 2];
+              const int ai = g * PASS + 4 * k + (i & 2);
+              const float2 f = make_float2(acc[j][ai], acc[j][ai + 1]);
               v[i] = __float_as_uint(i & 1 ? f.y : f.x);
             }
           }
           sts128(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
         }
         __syncwarp();
-        const int col = o.n0 + h * 64 + g * PASS + (lane % 4) * (16 / ES);
+        const int col = o.n0 + j * 128 + h * 64 + g * PASS + (lane % 4) * (16 / ES);
         uint8_t* out = static_cast<uint8_t*>(p.C) +
                        ((int64_t)o.w.e * p.c_stride + (int64_t)(o.w.row0 + r0 + lane / 4) * p.nb + col) * ES;
 #pragma unroll
@@ -248,16 +399,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
       }
     }
   }
-  teardown(c, warp);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(c->tmem_base), "r"(TMEM_COLS)
+                 : "memory");
+  }
 }
 
-// Map over a row-major array of bytes, 128 x 128 boxes, 128-byte swizzle, zeros outside.
-inline bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch) {
+// Map over a row-major array of bytes, boxes of 128 bytes x `rows`, 128-byte swizzle, zeros outside.
+inline bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
+                        uint32_t rows) {
   auto enc = encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {pitch};
-  cuuint32_t box[2] = {128, 128};
+  cuuint32_t box[2] = {128, rows};
   cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -268,38 +427,48 @@ inline bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_
 
 namespace mm8 {
 
-cudaError_t many(const P& p, cudaStream_t s) {
+// Units of 256 rows of A: the most there can be.
+int64_t units_many(const P& p) {
+  return p.columns ? (int64_t)p.E * ((p.na + 255) / 256) : max_units(p.T, p.E, 256);
+}
+
+template <int HALVES, int OUT, bool ACC>
+cudaError_t launch_many(const P& p, cudaStream_t s) {
   using namespace tc;
   static int attr_state[64] = {};
   static std::mutex mu;
-  if (!once_per_device(attr_state, mu, [] {
-        const void* ks[] = {(const void*)k_mm8<SBP_BF16, false>, (const void*)k_mm8<SBP_FP32, false>,
-                            (const void*)k_mm8<SBP_FP32, true>};
-        for (const void* k : ks)
-          if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MM8) != cudaSuccess)
-            return false;
-        return true;
+  const auto kern = k_mm8<HALVES, OUT, ACC>;
+  if (!once_per_device(attr_state, mu, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MM8) == cudaSuccess;
       }))
     return cudaErrorInvalidConfiguration;
   CUtensorMap mA, mB;
-  if (!make_map_u8(&mA, p.A, (uint64_t)p.K, (uint64_t)(p.columns ? p.na : p.T), (uint64_t)p.lda) ||
-      !make_map_u8(&mB, p.B, (uint64_t)p.K, p.columns ? (uint64_t)p.nb : (uint64_t)p.E * p.nb, (uint64_t)p.ldb))
+  if (!make_map_u8(&mA, p.A, (uint64_t)p.K, (uint64_t)(p.columns ? p.na : p.T), (uint64_t)p.lda, 128) ||
+      !make_map_u8(&mB, p.B, (uint64_t)p.K, p.columns ? (uint64_t)p.nb : (uint64_t)p.E * p.nb, (uint64_t)p.ldb, 64))
     return cudaErrorInvalidValue;
   if (cudaMemsetAsync(p.status, 0, sizeof(int32_t), s) != cudaSuccess) return cudaErrorUnknown;
   P q = p;
   q.limit_ns = wait_limit_ns();
-  const void* kern = p.out == SBP_BF16 ? (const void*)k_mm8<SBP_BF16, false>
-                     : p.accumulate    ? (const void*)k_mm8<SBP_FP32, true>
-                                       : (const void*)k_mm8<SBP_FP32, false>;
-  const int64_t units = p.columns ? (int64_t)p.E * ((p.na + 255) / 256) : max_units(p.T, p.E, 256);
-  const int64_t tiles = units * ((p.nb + BN - 1) / BN);
+  const int64_t tiles = units_many(p) * ((p.nb + 128 * HALVES - 1) / (128 * HALVES));
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  int pairs = max_pairs(kern, SMEM_MM8, MM8_THREADS);
-  if (pairs > tiles) pairs = (int)tiles;
-  if (p.out == SBP_BF16) k_mm8<SBP_BF16, false><<<2 * pairs, MM8_THREADS, SMEM_MM8, s>>>(mA, mB, q);
-  else if (p.accumulate) k_mm8<SBP_FP32, true><<<2 * pairs, MM8_THREADS, SMEM_MM8, s>>>(mA, mB, q);
-  else k_mm8<SBP_FP32, false><<<2 * pairs, MM8_THREADS, SMEM_MM8, s>>>(mA, mB, q);
+  const int pairs = (int)std::min<int64_t>(max_pairs((const void*)kern, SMEM_MM8, MM8_THREADS), tiles);
+  kern<<<2 * pairs, MM8_THREADS, SMEM_MM8, s>>>(mA, mB, q);
   return cudaGetLastError();
+}
+template <int HALVES>
+cudaError_t launch_many(const P& p, cudaStream_t s) {
+  if (p.out == SBP_BF16) return launch_many<HALVES, SBP_BF16, false>(p, s);
+  return p.accumulate ? launch_many<HALVES, SBP_FP32, true>(p, s) : launch_many<HALVES, SBP_FP32, false>(p, s);
+}
+
+cudaError_t many(const P& p, cudaStream_t s) {
+  // Tiles of 256 columns take 522 ns a block on all pairs at once, tiles of 128 columns 281 (16384 x
+  // 24576 x 4096: 1350 and 1453 us); the narrow ones leave fewer pairs idle (501 x 4096 x 12288: 53
+  // and 33 us).  The shorter sum of rounds is taken, for experts whose last units are half full.
+  const int64_t units = p.columns ? units_many(p) : (p.T + 255) / 256 + (std::min<int64_t>(p.E, p.T) - 1) / 2;
+  const int64_t pairs = num_sms() / 2;
+  auto rounds = [&](int64_t bn) { return (units * ((p.nb + bn - 1) / bn) + pairs - 1) / pairs; };
+  return rounds(256) * 522 <= rounds(128) * 281 ? launch_many<2>(p, s) : launch_many<1>(p, s);
 }
 
 }  // namespace mm8
