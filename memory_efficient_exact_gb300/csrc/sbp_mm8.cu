@@ -24,14 +24,24 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Weights are read once: past the L1 cache, which keeps A and the scales.
+__device__ __forceinline__ uint4 load_once(const uint8_t* q) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(q));
+  return v;
+}
 constexpr int FEW_WARPS = 8;
 
 // Few rows: what bounds the call is reading B once.  A block has 16 rows of B against 8 NT rows of
 // A, its warps sharing out the blocks of 128; they go straight from device memory into the
 // operands' registers.  (The order of k within a block of 128 is that of the 32 bytes a thread
-// loads, the same for A and B.)
-template <int NT>
-__global__ void __launch_bounds__(32 * FEW_WARPS) k_mm8_few(const P p) {
+// loads, the same for A and B.)  8 rows x 24576 x 4096: 19.6 us, 5.2 TB/s.  Several blocks of 128 in
+// flight a warp, at the price of blocks an SM, were slower (28 us with two, 31 with four).
+// MINB blocks are resident an SM, and so many are launched.
+template <int NT, int MINB>
+__global__ void __launch_bounds__(32 * FEW_WARPS, MINB) k_mm8_few(const P p) {
   __shared__ float red[FEW_WARPS][8 * NT][17];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int strips = (p.nb + 15) / 16;
@@ -59,39 +69,39 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_mm8_few(const P p) {
       have = u;
     }
     const int n0 = strip * 16;
-    const int rb0 = min(n0 + g, p.nb - 1), rb1 = min(n0 + g + 8, p.nb - 1);
-    const uint8_t* b0 = p.B + (int64_t)w.e * p.b_stride + (int64_t)rb0 * p.ldb + 32 * t;
-    const uint8_t* b1 = p.B + (int64_t)w.e * p.b_stride + (int64_t)rb1 * p.ldb + 32 * t;
+    const int64_t first = (int64_t)(w.kb0 + warp) * 128 + 32 * t;
+    const uint8_t* b0 = p.B + (int64_t)w.e * p.b_stride + (int64_t)min(n0 + g, p.nb - 1) * p.ldb + first;
+    const int64_t to1 = (int64_t)(min(n0 + g + 8, p.nb - 1) - min(n0 + g, p.nb - 1)) * p.ldb;
     const uint8_t* a[NT];
-    const float* sa[NT][2];
+    const float* sa[NT];
+    int64_t to_next[NT];   // from the scale of the first of this thread's two columns to the second's
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      a[i] = p.A + (int64_t)(w.row0 + min(8 * i + g, w.rows - 1)) * p.lda + 32 * t;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) sa[i][h] = p.sa + (int64_t)(w.row0 + min(8 * i + 2 * t + h, w.rows - 1)) * p.sa_pitch;
+      a[i] = p.A + (int64_t)(w.row0 + min(8 * i + g, w.rows - 1)) * p.lda + first;
+      const int r = min(8 * i + 2 * t, w.rows - 1);
+      sa[i] = p.sa + (int64_t)(w.row0 + r) * p.sa_pitch + w.kb0 + warp;
+      to_next[i] = min(8 * i + 2 * t + 1, w.rows - 1) == r ? 0 : p.sa_pitch;
     }
-    const float* sb = p.sb + (int64_t)w.e * p.sb_stride + (int64_t)(n0 / 128) * p.sb_pitch;
+    const float* sb = p.sb + (int64_t)w.e * p.sb_stride + (int64_t)(n0 / 128) * p.sb_pitch + w.kb0 + warp;
     float acc[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    for (int kb = w.kb0 + warp; kb < w.kb1; kb += FEW_WARPS) {
-      const int64_t at = (int64_t)kb * 128;
-      const int64_t left = p.K - at - 32 * t;   // bytes of this thread's 32 that are inside the row
+    auto block = [&](bool in0, bool in1) {   // which 16 bytes of this thread's 32 are inside the row
       const uint4 z = make_uint4(0u, 0u, 0u, 0u);
       uint4 x[4];
-      x[0] = left > 0 ? *reinterpret_cast<const uint4*>(b0 + at) : z;
-      x[1] = left > 16 ? *reinterpret_cast<const uint4*>(b0 + at + 16) : z;
-      x[2] = left > 0 ? *reinterpret_cast<const uint4*>(b1 + at) : z;
-      x[3] = left > 16 ? *reinterpret_cast<const uint4*>(b1 + at + 16) : z;
-      const float s = sb[kb];
+      x[0] = in0 ? load_once(b0) : z;
+      x[1] = in1 ? load_once(b0 + 16) : z;
+      x[2] = in0 ? load_once(b0 + to1) : z;
+      x[3] = in1 ? load_once(b0 + to1 + 16) : z;
+      const float s = *sb;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        if (8 * i >= w.rows) break;
-        const uint4 y0 = left > 0 ? *reinterpret_cast<const uint4*>(a[i] + at) : z;
-        const uint4 y1 = left > 16 ? *reinterpret_cast<const uint4*>(a[i] + at + 16) : z;
-        const float s0 = s * sa[i][0][kb], s1 = s * sa[i][1][kb];
+        if (i && 8 * i >= w.rows) break;
+        const uint4 y0 = in0 ? *reinterpret_cast<const uint4*>(a[i]) : z;
+        const uint4 y1 = in1 ? *reinterpret_cast<const uint4*>(a[i] + 16) : z;
+        const float s0 = s * sa[i][0], s1 = s * sa[i][to_next[i]];
         float c[4] = {0.f, 0.f, 0.f, 0.f};
         mma_e4m3(c, x[0].x, x[2].x, x[0].y, x[2].y, y0.x, y0.y);
         mma_e4m3(c, x[0].z, x[2].z, x[0].w, x[2].w, y0.z, y0.w);
@@ -101,7 +111,19 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_mm8_few(const P p) {
         acc[i][1] = fmaf(c[1], s1, acc[i][1]);
         acc[i][2] = fmaf(c[2], s0, acc[i][2]);
         acc[i][3] = fmaf(c[3], s1, acc[i][3]);
+        a[i] += FEW_WARPS * 128;
+        sa[i] += FEW_WARPS;
       }
+      b0 += FEW_WARPS * 128;
+      sb += FEW_WARPS;
+    };
+    const int whole = min(w.kb1, (int)(p.K / 128));
+    int kb = w.kb0 + warp;
+#pragma unroll 1
+    for (; kb < whole; kb += FEW_WARPS) block(true, true);
+    if (kb < w.kb1) {
+      const int64_t left = p.K - (int64_t)kb * 128 - 32 * t;
+      block(left > 0, left > 16);
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -130,26 +152,40 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_mm8_few(const P p) {
   }
 }
 
-template <int NT>
+template <int NT, int MINB>
 cudaError_t launch_few(const P& p, int64_t units, cudaStream_t s) {
   const int64_t items = units * ((p.nb + 15) / 16);
-  const int64_t most = (int64_t)num_sms() * 4;
-  k_mm8_few<NT><<<(unsigned)std::max<int64_t>(1, std::min(items, most)), 32 * FEW_WARPS, 0, s>>>(p);
+  const int64_t most = (int64_t)num_sms() * MINB;
+  k_mm8_few<NT, MINB><<<(unsigned)std::max<int64_t>(1, std::min(items, most)), 32 * FEW_WARPS, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 // Rows of A that one block takes: as many as an expert has on average, in tiles of 8.
-cudaError_t few(const P& p, cudaStream_t s) {
+int few_tiles(const P& p) {
   const int64_t rows = p.columns ? p.na : (p.T + p.E - 1) / p.E;
-  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+cudaError_t few(const P& p, cudaStream_t s) {
+  const int nt = few_tiles(p);
   const int64_t units = p.columns ? (int64_t)p.E * ((p.na + 8 * nt - 1) / (8 * nt)) : max_units(p.T, p.E, 8 * nt);
-  if (nt == 1) return launch_few<1>(p, units, s);
-  if (nt == 2) return launch_few<2>(p, units, s);
-  return launch_few<4>(p, units, s);
+  // (blocks an SM, with the registers that leaves: 5 and 3 and 3 instead of 4 and 2 and 2 take 21.7
+  // against 19.6 us for 8 rows and 16.2 against 10.9 for 32, N = 24576 and 4096, K = 4096)
+  if (nt == 1) return launch_few<1, 4>(p, units, s);
+  if (nt == 2) return launch_few<2, 2>(p, units, s);
+  return launch_few<4, 2>(p, units, s);
 }
 
-// Few rows an expert: k_mm8_few, which reads B at the memory's rate; else the tensor cores' tiles.
-bool is_few(const P& p) { return p.columns ? p.na <= 32 : p.T <= 32 * (int64_t)p.E; }
+// k_mm8_few reads each unit's matrix at 5.2 TB/s (8 rows x 24576 x 4096: 19.6 us), more slowly where
+// more rows share the conversions; the tensor cores' tiles cost the same for 1 row as for 256.  The
+// rule takes what these say; both measured, few and many: 32 rows x 4096 x 4096 10.7 and 16.4 us; 64
+// experts, 4096 x 2560: 192 rows 120 and 137, 400 rows 149 and 140, 1000 rows 297 and 165; 8 experts,
+// 4096 x 4096: 64 rows 33 and 41, 128 rows 58 and 42.
+bool is_few(const P& p) {
+  const int nt = few_tiles(p);
+  const int64_t bytes = (int64_t)p.nb * about_blocks(p) * 128;
+  const int64_t ns = about_units(p, 8 * nt) * bytes / 5200 * (nt == 1 ? 20 : nt == 2 ? 23 : 32) / 20;
+  return 4000 + ns <= many_ns(p);
+}
 
 int run(const P& p, cudaStream_t s) {
   if ((is_few(p) ? few(p, s) : many(p, s)) != cudaSuccess) return SBP_ERR_CUDA;

@@ -63,8 +63,22 @@ __device__ __forceinline__ Unit unit_of(const P& p, int unit, int u) {
   return w;
 }
 
+// How many units of `unit` rows of A the call has, as far as the host knows: experts that few rows
+// go to have at least one each, long ones a last unit that is half full on average.
+inline int64_t about_units(const P& p, int64_t unit) {
+  if (p.columns) return (int64_t)p.E * ((p.na + unit - 1) / unit);
+  if (p.E == 1) return (p.T + unit - 1) / unit;
+  const int64_t used = p.E < p.T ? p.E : p.T, more = p.T / unit + p.E / 2;
+  return used > more ? used : more;
+}
+// Blocks of 128 that a unit sums over, on average.
+inline int64_t about_blocks(const P& p) {
+  return p.columns ? (p.kblocks + p.E - 1) / p.E : p.kblocks;
+}
+
 // The kernel for many rows (sbp_mm8_tc.cu): enqueues the status word's reset and the product.
 cudaError_t many(const P& p, cudaStream_t s);
+int64_t many_ns(const P& p);   // about how long it takes
 
 }  // namespace mm8
 }  // namespace sbp

@@ -461,14 +461,17 @@ cudaError_t launch_many(const P& p, cudaStream_t s) {
   return p.accumulate ? launch_many<HALVES, SBP_FP32, true>(p, s) : launch_many<HALVES, SBP_FP32, false>(p, s);
 }
 
+// Tiles of 256 columns take 522 ns a block on all pairs at once, tiles of 128 columns 281 (16384 x
+// 24576 x 4096: 1350 and 1453 us); the narrow ones leave fewer pairs idle (501 x 4096 x 12288: 53
+// and 33 us).  The shorter of the two sums of rounds is taken.
+int64_t rounds_ns(const P& p, int halves) {
+  const int64_t bn = 128 * halves, pairs = num_sms() / 2;
+  return (about_units(p, 256) * ((p.nb + bn - 1) / bn) + pairs - 1) / pairs * about_blocks(p) * (halves == 2 ? 522 : 281);
+}
+int64_t many_ns(const P& p) { return 6000 + std::min(rounds_ns(p, 1), rounds_ns(p, 2)); }
+
 cudaError_t many(const P& p, cudaStream_t s) {
-  // Tiles of 256 columns take 522 ns a block on all pairs at once, tiles of 128 columns 281 (16384 x
-  // 24576 x 4096: 1350 and 1453 us); the narrow ones leave fewer pairs idle (501 x 4096 x 12288: 53
-  // and 33 us).  The shorter sum of rounds is taken, for experts whose last units are half full.
-  const int64_t units = p.columns ? units_many(p) : (p.T + 255) / 256 + (std::min<int64_t>(p.E, p.T) - 1) / 2;
-  const int64_t pairs = num_sms() / 2;
-  auto rounds = [&](int64_t bn) { return (units * ((p.nb + bn - 1) / bn) + pairs - 1) / pairs; };
-  return rounds(256) * 522 <= rounds(128) * 281 ? launch_many<2>(p, s) : launch_many<1>(p, s);
+  return rounds_ns(p, 2) <= rounds_ns(p, 1) ? launch_many<2>(p, s) : launch_many<1>(p, s);
 }
 
 }  // namespace mm8
