@@ -62,6 +62,7 @@ struct Mm8Ctrl {
   uint32_t tmem_base;
   int abort;
   float4 scale[2][2][128];   // [stage][column block][row]: SC_KB blocks
+  int4 tile[2][2];           // with a tile's first stage: its expert, rows, columns and blocks
 };
 constexpr size_t SMEM_MM8 = 6 * STAGE_BYTES + MM8_EPI * STG_MM8 + sizeof(Mm8Ctrl) + 1024;
 static_assert(mm8_stages(1) * mm8_stage_bytes(1) == 6 * STAGE_BYTES && mm8_stages(2) * mm8_stage_bytes(2) == 6 * STAGE_BYTES &&
@@ -253,11 +254,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
           sa[i] = p.sa + (int64_t)(o.w.row0 + min((int)rank * 128 + lane + 32 * i, o.w.rows - 1)) * p.sa_pitch;
         const float* sb0 = p.sb + (int64_t)o.w.e * p.sb_stride + (int64_t)(o.n0 / 128) * p.sb_pitch;
         const float* sb1 = HALVES == 2 && o.n0 + 128 < p.nb ? sb0 + p.sb_pitch : sb0;
-        for (int kb = o.w.kb0; kb < o.w.kb1; kb += SC_KB, ++n) {
+        // (a tile without blocks has a stage too, which says so)
+        for (int kb = o.w.kb0; kb < o.w.kb1 || kb == o.w.kb0; kb += SC_KB, ++n) {
           const uint32_t s = n & 1u;
           const int left = o.w.kb1 - kb;
           auto four = [&](const float* q) {
-            return make_float4(q[0], left > 1 ? q[1] : 0.f, left > 2 ? q[2] : 0.f, left > 3 ? q[3] : 0.f);
+            return make_float4(left > 0 ? q[0] : 0.f, left > 1 ? q[1] : 0.f, left > 2 ? q[2] : 0.f, left > 3 ? q[3] : 0.f);
           };
           float4 x[4];
           if (quads && kb % SC_KB == 0 && left >= SC_KB) {
@@ -275,6 +277,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
             c->scale[s][0][lane + 32 * i] = make_float4(x[i].x * b0.x, x[i].y * b0.y, x[i].z * b0.z, x[i].w * b0.w);
             if (HALVES == 2)
               c->scale[s][1][lane + 32 * i] = make_float4(x[i].x * b1.x, x[i].y * b1.y, x[i].z * b1.z, x[i].w * b1.w);
+          }
+          if (lane == 0 && kb == o.w.kb0) {
+            c->tile[s][0] = make_int4(o.w.e, o.w.row0, o.w.rows, o.n0);
+            c->tile[s][1] = make_int4(o.w.kb1 - o.w.kb0, 0, 0, 0);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&c->sfull[s]);
@@ -295,17 +301,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
     uint32_t n = 0, use = 0;   // stages of scales so far; the parity of each group's next accumulators
     bool ok = true;
     for (int t = pid; t < total && ok; t += npairs) {
-      const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
-      const int r0 = (int)rank * 128 + q * 32;            // this warp's first row of the unit
-      const int rows = min(32, o.w.rows - r0);            // how many of them are (may be none)
       float acc[HALVES][64];
 #pragma unroll
       for (int j = 0; j < HALVES; ++j)
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[j][i] = 0.f;
-      for (int kb = o.w.kb0; kb < o.w.kb1; kb += SC_KB, ++n) {
+      int4 tile;
+      int nkb = 1;
+      for (int kb = 0; kb < nkb; kb += SC_KB, ++n) {
         const uint32_t ss = n & 1u;
         ok = wait_inl<false>(&c->sfull[ss], (n >> 1) & 1u, &c->abort, p.limit_ns) && ok;
+        if (kb == 0) {   // what the tile is comes with its first scales, not from the table again
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;   // (nothing came)
+          tile = c->tile[ss][0];
+          nkb = c->tile[ss][1].x;
+        }
         float sk[HALVES][SC_KB];
 #pragma unroll
         for (int j = 0; j < HALVES; ++j) {
@@ -319,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
         arrive_if(lane == 0, saddr(&c->sempty[ss]), false, 0);
 #pragma unroll
         for (int k = 0; k < SC_KB; ++k) {
-          if (kb + k >= o.w.kb1) break;
+          if (kb + k >= nkb) break;
 #pragma unroll
           for (int j = 0; j < HALVES; ++j) {
             constexpr uint32_t S = sizeof(uint64_t);
@@ -352,9 +363,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
       // eight rows at a time (rows past the unit's last are masked); 16-byte chunk k of row r lies
       // at chunk k ^ (r / 2 % 4), without bank conflicts either way
       constexpr int ES = OUT == SBP_BF16 ? 2 : 4, PASS = 64 / ES;   // columns a pass
+      const int r0 = (int)rank * 128 + q * 32;            // this warp's first row of the unit
+      const int rows = tile.z - r0 - lane / 4;            // how many there are from this lane's first on
+      const int col0 = tile.w + h * 64 + (lane % 4) * (16 / ES);
+      uint8_t* out = static_cast<uint8_t*>(p.C) +
+                     ((int64_t)tile.x * p.c_stride + (int64_t)(tile.y + r0 + lane / 4) * p.nb + col0) * ES;
+      const int64_t down = (int64_t)8 * p.nb * ES;
 #pragma unroll
       for (int gg = 0; gg < HALVES * 64 / PASS; ++gg) {
-        const int j = gg / (64 / PASS), g = gg % (64 / PASS);
+        const int j = gg / (64 / PASS), g = gg % (64 / PASS), cc = j * 128 + g * PASS;
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -363,38 +380,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
           for (int i = 0; i < 4; ++i) {
             if (OUT == SBP_BF16) {
               const int ai = g * PASS + 8 * k + 2 * i;
-              const float2 f = make_float2(acc[j][ai], acc[j][ai + 1]);
-              v[i] = pack_bf16(f.x, f.y);
+              v[i] = pack_bf16(acc[j][ai], acc[j][ai + 1]);
             } else {
-              const int ai = g * PASS + 4 * k + (i & 2);
-              const float2 f = make_float2(acc[j][ai], acc[j][ai + 1]);
-              v[i] = __float_as_uint(i & 1 ? f.y : f.x);
+              v[i] = __float_as_uint(acc[j][g * PASS + 4 * k + i]);
             }
           }
           sts128(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
         }
         __syncwarp();
-        const int col = o.n0 + j * 128 + h * 64 + g * PASS + (lane % 4) * (16 / ES);
-        uint8_t* out = static_cast<uint8_t*>(p.C) +
-                       ((int64_t)o.w.e * p.c_stride + (int64_t)(o.w.row0 + r0 + lane / 4) * p.nb + col) * ES;
+        uint32_t v[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = i * 8 + lane / 4;
-          uint32_t v[4];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
                        : "r"(stg + r * 64 + (((lane % 4) ^ ((r >> 1) & 3)) << 4))
                        : "memory");
-          if (r < rows && col < p.nb) {
+        }
+        if (col0 + cc < p.nb) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (8 * i >= rows) break;
+            uint8_t* at = out + cc * ES + i * down;
             if (ACC) {
-              const float4 old = *reinterpret_cast<const float4*>(out);
-              *reinterpret_cast<float4*>(out) = make_float4(old.x + __uint_as_float(v[0]), old.y + __uint_as_float(v[1]),
-                                                            old.z + __uint_as_float(v[2]), old.w + __uint_as_float(v[3]));
+              const float4 old = *reinterpret_cast<const float4*>(at);
+              *reinterpret_cast<float4*>(at) =
+                  make_float4(old.x + __uint_as_float(v[i][0]), old.y + __uint_as_float(v[i][1]),
+                              old.z + __uint_as_float(v[i][2]), old.w + __uint_as_float(v[i][3]));
             } else {
-              *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(at) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
             }
           }
-          out += (int64_t)8 * p.nb * ES;
         }
       }
     }
