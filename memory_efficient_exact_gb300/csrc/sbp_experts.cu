@@ -18,7 +18,7 @@ namespace sbp {
 namespace {
 
 constexpr int64_t MAX_EXPERTS = 1024, MAX_D = 16384;
-constexpr int SORT_WARPS = 16, SORT_PER_LANE = 8;
+constexpr int SORT_WARPS = 16, SORT_PER_LANE = 4;
 constexpr int SORT_THREADS = 32 * SORT_WARPS;
 constexpr int SORT_SLOTS = SORT_THREADS * SORT_PER_LANE;   // slots of a block
 
@@ -50,9 +50,9 @@ __global__ void __launch_bounds__(SORT_THREADS) k_expert_count(const SortP p) {
   for (int e = threadIdx.x; e < p.E; e += SORT_THREADS) p.counts[(int64_t)blockIdx.x * p.E + e] = hist[e];
 }
 
-// Each warp counts its 256 slots by expert, 32 at a time (lanes of one expert find one another
-// with match_any); the counts' prefix over experts, blocks and warps is where each warp's slots
-// of an expert begin, and a second walk over the same ids, kept in registers, places them.
+// Each warp counts its 128 slots by expert, 32 at a time (lanes of one expert find one another
+// with match_any, once); the counts' prefix over experts, blocks and warps is where each warp's
+// slots of an expert begin, and a second walk over ids and lanes, kept in registers, places them.
 __global__ void __launch_bounds__(SORT_THREADS) k_expert_place(const SortP p) {
   extern __shared__ int sh[];
   int* total = sh;                 // [E] of all blocks, then the experts' first rows
@@ -75,10 +75,13 @@ __global__ void __launch_bounds__(SORT_THREADS) k_expert_place(const SortP p) {
   bad = __syncthreads_or(bad);
   if (p.blocks == 1 && threadIdx.x == 0) *p.status = bad ? SBP_ERR_EXPERT_RANGE : SBP_OK;
   int* mine = wcnt + warp * p.E;
+  uint32_t same[SORT_PER_LANE];   // lanes of the same expert
 #pragma unroll
   for (int i = 0; i < SORT_PER_LANE; ++i) {
-    const uint32_t m = __match_any_sync(0xffffffffu, id[i]);
-    if (id[i] >= 0 && (m & ((1u << lane) - 1u)) == 0) mine[id[i]] += __popc(m);
+    same[i] = 0;
+    if (w0 + 32 * i >= p.n) continue;
+    same[i] = __match_any_sync(0xffffffffu, id[i]);
+    if (id[i] >= 0 && (same[i] & ((1u << lane) - 1u)) == 0) mine[id[i]] += __popc(same[i]);
     __syncwarp();
   }
   __syncthreads();
@@ -126,9 +129,9 @@ __global__ void __launch_bounds__(SORT_THREADS) k_expert_place(const SortP p) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < SORT_PER_LANE; ++i) {
+    if (w0 + 32 * i >= p.n) break;
     const int64_t s = w0 + 32 * i + lane;
-    const uint32_t m = __match_any_sync(0xffffffffu, id[i]);
-    const int rank = __popc(m & ((1u << lane) - 1u));
+    const int rank = __popc(same[i] & ((1u << lane) - 1u));
     int at = -1;
     if (id[i] >= 0) {
       at = total[id[i]] + mine[id[i]] + rank;
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(SORT_THREADS) k_expert_place(const SortP p) {
     }
     if (s < p.n) p.rows[s] = at;
     __syncwarp();
-    if (id[i] >= 0 && rank == 0) mine[id[i]] += __popc(m);
+    if (id[i] >= 0 && rank == 0) mine[id[i]] += __popc(same[i]);
     __syncwarp();
   }
 }
@@ -187,31 +190,34 @@ struct CombineP {
   void* Y;
 };
 
-// KU slots' rows in flight at a time.
+// KU slots' rows in flight at a time: first where they lie and their weights, then the rows, then
+// the sum.  Six blocks an SM and four rows in flight a thread do better than fewer blocks with eight
+// (8192 tokens, 8 slots, d = 4096: 88 us, 6850 GB/s; 103 to 117).
 template <typename E, int KU>
-__global__ void __launch_bounds__(256) k_expert_combine(const CombineP p) {
+__global__ void __launch_bounds__(256, 6) k_expert_combine(const CombineP p) {
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int c = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
   if (t >= p.T || c >= p.d) return;
-  F8 acc;
   Raw<E> res;
   res.zero();
   if (p.residual) res.load(static_cast<const E*>(p.residual) + t * p.d + c);
-  acc = res.f();
+  F8 acc = res.f();
+  const int32_t* rows = p.rows + t * p.k;
+  const float* weights = p.w ? p.w + t * p.k : nullptr;
   for (int j0 = 0; j0 < p.k; j0 += KU) {
-    Raw<E> y[KU];
+    int r[KU];
     float w[KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
-      const int j = j0 + u;
-      const int64_t r = j < p.k ? p.rows[t * p.k + j] : -1;
-      const bool on = r >= 0 && r < p.n_rows;
+      r[u] = j0 + u < p.k ? rows[j0 + u] : -1;
+      w[u] = weights && j0 + u < p.k ? weights[j0 + u] : 1.f;
+    }
+    Raw<E> y[KU];
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
       y[u].zero();
-      w[u] = 0.f;
-      if (on) {
-        y[u].load(static_cast<const E*>(p.Ys) + r * p.d + c);
-        w[u] = p.w ? p.w[t * p.k + j] : 1.f;
-      }
+      if (r[u] >= 0 && r[u] < p.n_rows) y[u].load(static_cast<const E*>(p.Ys) + (int64_t)r[u] * p.d + c);
+      else w[u] = 0.f;
     }
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
@@ -235,16 +241,17 @@ struct CombineBwdP {
 
 // blockDim.x threads a token (a power of two, 8 to 256), blockDim.y tokens a block, KU slots at a
 // time.  The products of a slot are summed by the thread, then over the lanes, then over the
-// token's warps.
+// token's warps.  (8192 tokens, 8 slots, d = 4096, bf16: 174 us, 6560 GB/s, with three blocks an SM,
+// 202 with two.)
 template <typename E, int KU>
-__global__ void __launch_bounds__(256) k_expert_combine_bwd(const CombineBwdP p) {
+__global__ void __launch_bounds__(256, KU <= 2 ? 4 : 3) k_expert_combine_bwd(const CombineBwdP p) {
   __shared__ float red[8][KU];
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = t < p.T;
   const int tx = blockDim.x, lanes = min(tx, 32);
   const int warp = (threadIdx.y * tx + threadIdx.x) / 32;
   for (int j0 = 0; j0 < p.k; j0 += KU) {
-    int64_t r[KU];
+    int r[KU];
     float w[KU], dot[KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(256) k_expert_combine_bwd(const CombineBwdP p)
       g.load(static_cast<const E*>(p.dY) + t * p.d + c);
 #pragma unroll
       for (int u = 0; u < KU; ++u)
-        if (r[u] >= 0) y[u].load(static_cast<const E*>(p.Ys) + r[u] * p.d + c);
+        if (r[u] >= 0) y[u].load(static_cast<const E*>(p.Ys) + (int64_t)r[u] * p.d + c);
         else y[u].zero();
       const F8 gf = g.f();
 #pragma unroll
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(256) k_expert_combine_bwd(const CombineBwdP p)
           dot[u] = fmaf(gf.v[i], yf.v[i], dot[u]);
           o.v[i] = w[u] * gf.v[i];
         }
-        store8(static_cast<E*>(p.dYs) + r[u] * p.d + c, o);
+        store8(static_cast<E*>(p.dYs) + (int64_t)r[u] * p.d + c, o);
       }
     }
 #pragma unroll
@@ -344,8 +351,7 @@ void launch_combine(const CombineP& p, cudaStream_t s) {
   const dim3 b = token_block(vecs), g((unsigned)((p.T + b.y - 1) / b.y), (unsigned)((vecs + b.x - 1) / b.x));
   if (p.k == 1) k_expert_combine<E, 1><<<g, b, 0, s>>>(p);
   else if (p.k == 2) k_expert_combine<E, 2><<<g, b, 0, s>>>(p);
-  else if (p.k <= 4 || sizeof(E) == 4) k_expert_combine<E, 4><<<g, b, 0, s>>>(p);
-  else k_expert_combine<E, 8><<<g, b, 0, s>>>(p);
+  else k_expert_combine<E, 4><<<g, b, 0, s>>>(p);
 }
 template <typename E>
 void launch_combine_bwd(const CombineBwdP& p, cudaStream_t s) {
