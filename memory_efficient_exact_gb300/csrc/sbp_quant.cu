@@ -36,6 +36,93 @@ __device__ __forceinline__ float amax8(const Raw<E>& r) {
   return a;
 }
 
+// Largest magnitudes of two pairs of bf16 values at a time (a NaN is passed over, as by fmaxf).
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t abs2(uint32_t a) { return a & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t amax2(const Raw<__nv_bfloat16>& r) {
+  return max2(max2(abs2(r.u.x), abs2(r.u.y)), max2(abs2(r.u.z), abs2(r.u.w)));
+}
+__device__ __forceinline__ float low2(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high2(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+// The largest magnitude of each of eight rows over the 16 lanes that share them: in lane c that of
+// row c % 8.
+__device__ __forceinline__ float row_amax(const Raw<__nv_bfloat16> (&x)[8], int c) {
+  uint32_t m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {   // rows 2i and 2i + 1 in one word
+    const uint32_t a = amax2(x[2 * i]), b = amax2(x[2 * i + 1]);
+    m[i] = max2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+  }
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = max2(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+  const uint32_t v = c & 4 ? (c & 2 ? m[3] : m[2]) : (c & 2 ? m[1] : m[0]);
+  return c & 1 ? high2(v) : low2(v);
+}
+__device__ __forceinline__ float row_amax(const Raw<float> (&x)[8], int c) {
+  float m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = amax8(x[i]);
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+  float v = m[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v = (c & 7) == i ? m[i] : v;
+  return v;
+}
+// The largest magnitude of each of eight columns over the eight rows of this thread and those of
+// the other half of the warp.
+__device__ __forceinline__ F8 col_amax(const Raw<__nv_bfloat16> (&x)[8]) {
+  uint32_t m[4] = {abs2(x[0].u.x), abs2(x[0].u.y), abs2(x[0].u.z), abs2(x[0].u.w)};
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    m[0] = max2(m[0], abs2(x[i].u.x));
+    m[1] = max2(m[1], abs2(x[i].u.y));
+    m[2] = max2(m[2], abs2(x[i].u.z));
+    m[3] = max2(m[3], abs2(x[i].u.w));
+  }
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = max2(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+    f.v[2 * i] = low2(m[i]);
+    f.v[2 * i + 1] = high2(m[i]);
+  }
+  return f;
+}
+__device__ __forceinline__ F8 col_amax(const Raw<float> (&x)[8]) {
+  F8 m = x[0].f();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m.v[j] = fabsf(m.v[j]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const F8 v = x[i].f();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m.v[j] = fmaxf(m.v[j], fabsf(v.v[j]));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m.v[j] = fmaxf(m.v[j], __shfl_xor_sync(0xffffffffu, m.v[j], 16));
+  return m;
+}
+__device__ __forceinline__ float all_amax(const Raw<__nv_bfloat16> (&x)[8]) {
+  uint32_t m = amax2(x[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max2(m, amax2(x[i]));
+  return fmaxf(low2(m), high2(m));
+}
+__device__ __forceinline__ float all_amax(const Raw<float> (&x)[8]) {
+  float a = amax8(x[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) a = fmaxf(a, amax8(x[i]));
+  return a;
+}
+
 struct RowsP {
   const void* X;
   uint32_t units;       // blocks of 128 columns of all rows
@@ -124,25 +211,16 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
   }
   const int col = f0 + 8 * c8;
   Raw<E> x[8];
+  const E* in = static_cast<const E*>(p.X) + (row0 + g8 * 8) * p.d + col;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = g8 * 8 + i;
     x[i].zero();
-    if (r < rows && col < p.d) x[i].load(static_cast<const E*>(p.X) + (row0 + r) * p.d + col);
+    if (r < rows && col < p.d) x[i].load(in + (int64_t)i * p.d);
   }
   float tinv = 1.f;
   if (COLS == 1) {
-    F8 m;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m.v[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const F8 v = x[i].f();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m.v[j] = fmaxf(m.v[j], fabsf(v.v[j]));
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m.v[j] = fmaxf(m.v[j], __shfl_xor_sync(0xffffffffu, m.v[j], 16));
+    const F8 m = col_amax(x);
     if (lane < 16) {
       float4* q = reinterpret_cast<float4*>(&cmax[warp][8 * c8]);
       q[0] = make_float4(m.v[0], m.v[1], m.v[2], m.v[3]);
@@ -159,9 +237,7 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
     }
     __syncthreads();
   } else {
-    float a = amax8(x[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) a = fmaxf(a, amax8(x[i]));
+    float a = all_amax(x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     if (lane == 0) cmax[0][warp] = a;
@@ -181,21 +257,19 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
     }
   }
   if (ROWS != 0) {
+    float rinv = tinv;
+    if (ROWS == 1) {   // each lane one row's scale: a division costs more than a shuffle
+      const float s = block_scale(row_amax(x, c8));
+      rinv = 1.f / s;
+      if (c8 < 8 && g8 * 8 + c8 < rows) p.scales[(row0 + g8 * 8 + c8) * p.nf + f] = s;
+    }
+    uint8_t* out = p.Y8 + (row0 + g8 * 8) * p.d + col;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = g8 * 8 + i;
-      float inv = tinv;
-      if (ROWS == 1) {
-        float a = amax8(x[i]);
-#pragma unroll
-        for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const float s = block_scale(a);
-        inv = 1.f / s;
-        if (c8 == 0 && r < rows) p.scales[(row0 + r) * p.nf + f] = s;
-      }
-      if (r < rows && col < p.d) {
+      const float inv = ROWS == 1 ? __shfl_sync(0xffffffffu, rinv, i, 16) : tinv;
+      if (g8 * 8 + i < rows && col < p.d) {
         const F8 v = x[i].f();
-        *reinterpret_cast<uint2*>(p.Y8 + (row0 + r) * p.d + col) =
+        *reinterpret_cast<uint2*>(out + (int64_t)i * p.d) =
             make_uint2(e4m3_pack(v.v[0], v.v[1], v.v[2], v.v[3], inv), e4m3_pack(v.v[4], v.v[5], v.v[6], v.v[7], inv));
       }
     }
