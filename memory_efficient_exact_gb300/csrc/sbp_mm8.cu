@@ -175,16 +175,17 @@ cudaError_t few(const P& p, cudaStream_t s) {
   return launch_few<4, 2>(p, units, s);
 }
 
-// k_mm8_few reads each unit's matrix at 5.2 TB/s (8 rows x 24576 x 4096: 19.6 us), more slowly where
-// more rows share the conversions; the tensor cores' tiles cost the same for 1 row as for 256.  The
-// rule takes what these say; both measured, few and many: 32 rows x 4096 x 4096 10.7 and 16.4 us; 64
-// experts, 4096 x 2560: 192 rows 120 and 137, 400 rows 149 and 140, 1000 rows 297 and 165; 8 experts,
-// 4096 x 4096: 64 rows 33 and 41, 128 rows 58 and 42.
+// k_mm8_few reads each unit's matrix at 5.2 TB/s (8 rows x 24576 x 4096: 19.6 us), and takes 1.55
+// and 2.65 times as long for units of 16 and 32 rows, whose values are converted for every strip;
+// the tensor cores' tiles cost the same for 1 row as for 256.  The rule compares what that comes to;
+// measured, few and many, in us: 4096 x 4096, 32 rows 10.7 and 16.4, 48 rows 16.2 and 16.5, 64 rows
+// 19.3 and 16.5; 512 x 512, 300 rows 5.7 and 10.3, 1000 rows 9.9 and 10.3; 64 experts of 4096 x 2560,
+// 192 rows 120 and 137, 400 rows 149 and 140, 1000 rows 297 and 165; 8 experts of 4096 x 4096, 64
+// rows 33 and 41, 128 rows 58 and 42.
 bool is_few(const P& p) {
   const int nt = few_tiles(p);
   const int64_t bytes = (int64_t)p.nb * about_blocks(p) * 128;
-  const int64_t ns = about_units(p, 8 * nt) * bytes / 5200 * (nt == 1 ? 20 : nt == 2 ? 23 : 32) / 20;
-  return 4000 + ns <= many_ns(p);
+  return 4000 + about_units(p, 8 * nt) * bytes / 5200 * (nt == 1 ? 100 : nt == 2 ? 155 : 265) / 100 <= many_ns(p);
 }
 
 int run(const P& p, cudaStream_t s) {

@@ -24,6 +24,7 @@ struct P {
   void* C;
   int32_t* status;
   uint64_t limit_ns;
+  int stall;          // failure-detection hook: the products wait for what never comes
 };
 
 // A unit's rows of A (row0 .., at most `unit`), its expert, its blocks of 128 of the sum.

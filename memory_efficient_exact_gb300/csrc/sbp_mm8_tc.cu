@@ -203,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
       if (rank == 0) {
         const int j = warp - 1;
         uint32_t done = 0, use = 15;   // blocks of the tiles before; the parity of each group's last release
-        bool ok = true;
+        bool ok = !p.stall || warp_wait<false>(&c->mdone[j], 0, c, p.limit_ns);
         for (int t = pid; t < total && ok; t += npairs) {
           const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
           const int nkb = o.w.kb1 - o.w.kb0;
@@ -465,6 +465,7 @@ cudaError_t launch_many(const P& p, cudaStream_t s) {
   if (cudaMemsetAsync(p.status, 0, sizeof(int32_t), s) != cudaSuccess) return cudaErrorUnknown;
   P q = p;
   q.limit_ns = wait_limit_ns();
+  q.stall = fault_stall_requested();
   const int64_t tiles = units_many(p) * ((p.nb + 128 * HALVES - 1) / (128 * HALVES));
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   const int pairs = (int)std::min<int64_t>(max_pairs((const void*)kern, SMEM_MM8, MM8_THREADS), tiles);
@@ -484,7 +485,7 @@ int64_t rounds_ns(const P& p, int halves) {
   const int64_t bn = 128 * halves, pairs = num_sms() / 2;
   return (about_units(p, 256) * ((p.nb + bn - 1) / bn) + pairs - 1) / pairs * about_blocks(p) * (halves == 2 ? 522 : 281);
 }
-int64_t many_ns(const P& p) { return 6000 + std::min(rounds_ns(p, 1), rounds_ns(p, 2)); }
+int64_t many_ns(const P& p) { return 8000 + std::min(rounds_ns(p, 1), rounds_ns(p, 2)); }
 
 cudaError_t many(const P& p, cudaStream_t s) {
   return rounds_ns(p, 2) <= rounds_ns(p, 1) ? launch_many<2>(p, s) : launch_many<1>(p, s);

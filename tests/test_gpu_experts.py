@@ -287,6 +287,26 @@ def test_product(sbp, T, N, K, dtype):
     check_product(sbp, [0, T], N, K, dtype, T + N + K)
 
 
+# sizes that go to the tensor cores' tiles (of 256 and of 128 columns), ragged in every way: blocks
+# of the sum from one to more than the operands' ring holds, odd numbers of them, last ones cut off
+MANY = [(1500, 4104, 128), (1025, 4096, 144), (2049, 2056, 400), (700, 2568, 1040), (513, 4096, 2576), (300, 5128, 4112),
+        (5000, 4104, 272), (3001, 8200, 656), (70, 8192, 4096)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,N,K", MANY)
+def test_product_of_many_rows(sbp, T, N, K, dtype):
+    check_product(sbp, [0, T], N, K, dtype, T + N + K)
+
+
+@pytest.mark.parametrize("lens,N,K,behind", [
+    ([1000, 0, 1, 255, 256, 257, 0, 900], 2056, 656, 0), ([1500, 1500], 4104, 528, 70), ([0, 3000, 0], 2056, 1168, 5),
+    ([40] * 60, 2568, 400, 11), ([600, 0, 1300, 513, 7], 2056, 2064, 0)])
+def test_product_of_experts_with_many_rows(sbp, lens, N, K, behind):
+    off = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    check_product(sbp, off, N, K, "bf16", N + K + len(lens), T=off[-1] + behind)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("lens,N,K,behind", [
     ([1, 0, 2], 264, 272, 0), ([0, 0, 5, 0], 128, 128, 3), ([3] * 40, 136, 400, 0), ([0, 9, 17, 33, 1, 0], 512, 2064, 1),
@@ -299,7 +319,9 @@ def test_product_of_experts(sbp, lens, N, K, behind, dtype):
 
 @pytest.mark.parametrize("lens,N,K", [
     ([1], 8, 8), ([5], 128, 128), ([128], 264, 136), ([129], 520, 72), ([1000], 256, 512), ([0, 3, 0], 136, 264),
-    ([300, 0, 1, 127, 128, 129, 0], 264, 392), ([2000, 70], 512, 776), ([1] * 70, 72, 128)])
+    ([300, 0, 1, 127, 128, 129, 0], 264, 392), ([2000, 70], 512, 776), ([1] * 70, 72, 128),
+    # the tensor cores' tiles
+    ([3000], 1032, 1800), ([1000, 0, 1700, 1, 128], 1544, 1032), ([5000, 70], 520, 776)])
 def test_product_of_columns(sbp, lens, N, K):
     g = np.random.default_rng(N + K + len(lens))
     off = np.concatenate([[0], np.cumsum(lens)])
@@ -340,15 +362,15 @@ def test_nothing_to_do(sbp):
     assert (host(keep) == 3).all()
 
 
-@pytest.mark.parametrize("T", [6, 900])
+@pytest.mark.parametrize("T,N", [(6, 256), (2000, 4096)])
 @pytest.mark.parametrize("bad", [[1, 2, 4], [0, 5, 4], [0, 2, 100000], [0, -1, 4], [-2, 2, 4]])
-def test_bad_tables(sbp, bad, T):
+def test_bad_tables(sbp, bad, T, N):
     """A status, and nothing is read or written by a bad table."""
     off = torch.tensor(bad, dtype=torch.int32, device="cuda")
     x = torch.randn(T, 128, device="cuda")
-    w = sbp.quant_e4m3_weight(torch.randn(2, 256, 128, device="cuda"))
+    w = sbp.quant_e4m3_weight(torch.randn(2, N, 128, device="cuda"))
     q = sbp.quant_e4m3(x)
-    C = torch.full((T, 256), 5.0, device="cuda")
+    C = torch.full((T, N), 5.0, device="cuda")
     r = sbp.matmul_e4m3(q["Y8"], q["scales"], w["W8"], w["scales"], offsets=off, C=C)
     nb = sbp.token_blocks(T, 2)
     yt = torch.zeros((128, 128 * nb), device="cuda").to(F8)
@@ -365,8 +387,8 @@ def test_bad_tables(sbp, bad, T):
 def test_values_that_are_not_finite(sbp):
     """A NaN reaches its own row and column of the product, and no other."""
     g = np.random.default_rng(8)
-    for T in (5, 300):
-        a, sa, b, sb = operands(g, T, 264, 256, 1)
+    for T, N in ((5, 264), (300, 264), (1100, 4104)):
+        a, sa, b, sb = operands(g, T, N, 256, 1)
         A, B = dev(a, F8), dev(b[0], F8)
         clean = host(sbp.matmul_e4m3(A, dev(sa, F32), B, dev(sb[0], F32))["C"])
         A.view(torch.uint8)[3, 200] = 0x7f
@@ -380,11 +402,11 @@ def test_values_that_are_not_finite(sbp):
 def test_same_bits_and_neighbours(sbp):
     """The same call gives the same bits; a row's result does not depend on the other rows."""
     g = np.random.default_rng(11)
-    a, sa, b, sb = operands(g, 700, 520, 656, 1)
+    a, sa, b, sb = operands(g, 1700, 4104, 656, 1)
     args = [dev(a, F8), dev(sa, F32), dev(b[0], F8), dev(sb[0], F32)]
     one, two = (sbp.matmul_e4m3(*args)["C"] for _ in range(2))
     assert torch.equal(one, two)
-    split = [0, 300, 700]
+    split = [0, 700, 1700]
     bb = torch.stack([args[2].view(torch.uint8)] * 2).view(F8)
     part = sbp.matmul_e4m3(args[0], args[1], bb, torch.stack([args[3]] * 2),
                            offsets=torch.tensor(split, dtype=torch.int32, device="cuda"))["C"]
