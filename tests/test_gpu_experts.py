@@ -413,6 +413,39 @@ def test_same_bits_and_neighbours(sbp):
     assert torch.equal(part, one)
 
 
+def test_elements_past_2_31(sbp):
+    """Rows of arrays of more than 2^31 elements: the same bits as the same rows alone."""
+    T, d, K = 524800, 4104, 128
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    last = slice(T - 384, T)
+    A, W = torch.randn(T, K, generator=gen, device="cuda").to(BF), torch.randn(d, K, generator=gen, device="cuda")
+    a, w = sbp.quant_e4m3(A), sbp.quant_e4m3_weight(torch.cat([W, W[:8]]))     # (weights in sixteens)
+    B8, sb = w["W8"][:d].contiguous(), w["scales"][:(d + 127) // 128].contiguous()
+    r = sbp.matmul_e4m3(a["Y8"], a["scales"], B8, sb)
+    ok(r)
+    few = sbp.matmul_e4m3(a["Y8"][last].contiguous(), a["scales"][last].contiguous(), B8, sb, dtype=F32)["C"]
+    C = r["C"]
+    assert T * d > 2 ** 31
+    near("C", host(C[last]), host(few), 2.0 ** -8 * np.abs(host(few)) + 1e-6)
+    q, p = sbp.quant_e4m3(C), sbp.quant_e4m3(C[last].contiguous())
+    assert torch.equal(q["Y8"][last].view(torch.uint8), p["Y8"].view(torch.uint8))
+    assert torch.equal(q["scales"][last], p["scales"])
+    del q
+    for tiles in (False, True):
+        t, u = sbp.quant_e4m3_columns(C, tiles=tiles), sbp.quant_e4m3_columns(C[last].contiguous(), tiles=tiles)
+        assert torch.equal(t["Yt8"][:, -384:].contiguous().view(torch.uint8), u["Yt8"].view(torch.uint8))
+        assert torch.equal(t["scales_t"][:, -3:], u["scales_t"])
+        del t
+    rows = torch.arange(T, device="cuda", dtype=torch.int32).flip(0).view(T // 2, 2).contiguous()
+    X = C[:T // 2].contiguous()
+    xs = sbp.expert_gather(X, rows)["Xs"]
+    assert torch.equal(xs[:2], X[-1:].expand(2, d)) and torch.equal(xs[-2:], X[:1].expand(2, d))
+    wt = torch.full((T // 2, 2), 0.5, device="cuda")
+    assert torch.equal(sbp.expert_combine(xs, rows, wt)["Y"], X)
+    dys = sbp.expert_combine_backward(X, xs, rows, wt)["dYs"]
+    assert torch.equal(dys[-2:], (0.5 * X[:1].float()).to(BF).expand(2, d))
+
+
 # ---------------------------------------------------------------- streams, graphs, a run
 
 def test_other_stream_and_graph_follows_its_table(sbp):
