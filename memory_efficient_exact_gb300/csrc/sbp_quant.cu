@@ -131,7 +131,7 @@ struct RowsP {
   float* scales;
 };
 
-constexpr int ROW_UNITS = 4;   // blocks of 16 lanes, all loads in flight
+constexpr int ROW_UNITS = 2;   // blocks of 16 lanes, all loads in flight (16384 x 4096: 34 us; 35 with four, 41 with one)
 
 // 16 lanes a block of 128 columns, 8 columns a lane.
 template <typename E>
