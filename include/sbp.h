@@ -390,7 +390,7 @@ int sbp_rope_qkv_backward(const void* dQ, const void* dK, const void* dV, int kv
  *   rows    [T, k] int32      the place of slot (t, j), -1 for a dropped one
  *   slots   [T k] int32       the slot t k + j at each place (entries behind offsets[E] untouched)
  *   offsets [E+1] int32       where each expert's places begin
- * T k at most 2^30. */
+ * T k at most 2^30.  Up to 2048 slots no workspace is needed (NULL will do). */
 size_t sbp_expert_sort_workspace_bytes(int64_t T, int64_t k, int64_t E);
 int sbp_expert_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* rows, int32_t* slots,
                     int32_t* offsets, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);

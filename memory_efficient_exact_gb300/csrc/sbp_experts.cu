@@ -318,8 +318,8 @@ int sort_layout(int64_t T, int64_t k, int64_t E, SortLayout* L) {
   L->n = T * k;
   L->blocks = (L->n + SORT_SLOTS - 1) / SORT_SLOTS;
   size_t o = 0;
-  L->off_counts = take_region(o, (size_t)(L->blocks > 1 ? L->blocks : 1) * E * sizeof(int32_t), L->guards);
-  L->total = o;
+  if (L->blocks > 1) L->off_counts = take_region(o, (size_t)L->blocks * E * sizeof(int32_t), L->guards);
+  L->total = o;   // 0: one block keeps its counts to itself
   return SBP_OK;
 }
 
@@ -371,7 +371,7 @@ extern "C" {
 
 size_t sbp_expert_sort_workspace_bytes(int64_t T, int64_t k, int64_t E) {
   SortLayout L;
-  return sort_layout(T, k, E, &L) == SBP_OK ? L.total : 0;
+  return sort_layout(T, k, E, &L) == SBP_OK ? std::max<size_t>(L.total, 256) : 0;
 }
 
 int sbp_expert_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* rows, int32_t* slots,
@@ -383,7 +383,8 @@ int sbp_expert_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t
   for (const void* q : {(const void*)ids, (const void*)rows, (const void*)slots, (const void*)offsets,
                         (const void*)dev_status})
     if (!aligned4(q)) return SBP_ERR_ALIGNMENT;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || ws_bytes < L.total) return SBP_ERR_WORKSPACE;
+  if (L.total > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || ws_bytes < L.total))
+    return SBP_ERR_WORKSPACE;
   NvtxRange nv("sbp_expert_sort");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(workspace);
@@ -398,9 +399,8 @@ int sbp_expert_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t
     return SBP_ERR_CUDA;
   SortP p{ids, L.n, (int)E, (int)std::max<int64_t>(L.blocks, 1), rows, slots, offsets,
           reinterpret_cast<int32_t*>(w + L.off_counts), dev_status};
+  // (a block alone writes the status itself)
   if (p.blocks > 1 && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return SBP_ERR_CUDA;
-  // (the only block writes the status itself: before the guard zones' kernels it must be set too)
-  if (kGuardBytes && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return SBP_ERR_CUDA;
   int st = workspace_guards(w, L.guards, 0, dev_status, s, &launches);
   if (st != SBP_OK) return st;
   if (p.blocks > 1) {

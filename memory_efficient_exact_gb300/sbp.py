@@ -820,18 +820,19 @@ def expert_sort(ids, E, *, rows=None, slots=None, offsets=None, workspace=None, 
     if ids.dim() != 2 or ids.dtype != torch.int32:
         raise ValueError("ids must be int32 [T, k]")
     T, k = ids.shape
-    dev = ids.device
+    n, dev = T * k, ids.device
     if workspace is None:
-        n = _lib.sbp_expert_sort_workspace_bytes(T, k, E)
-        if n == 0:
+        nw = _lib.sbp_expert_sort_workspace_bytes(T, k, E)
+        if nw == 0:
             raise SbpError(ERR_UNSUPPORTED, "sbp_expert_sort_workspace_bytes")
-        workspace = _empty(stream, n, torch.uint8, dev)
+        if n > 2048:
+            workspace = _empty(stream, nw, torch.uint8, dev)
     rows = _out(rows, (T, k), torch.int32, "rows", stream, dev)
-    slots = _out(slots, (T * k,), torch.int32, "slots", stream, dev)
+    slots = _out(slots, (n,), torch.int32, "slots", stream, dev)
     offsets = _out(offsets, (E + 1,), torch.int32, "offsets", stream, dev)
     st = _status_word(status, stream, dev)
-    _check(_lib.sbp_expert_sort(_a(ids), T, k, E, _a(rows), _a(slots), _a(offsets), _a(workspace), workspace.numel(),
-                                _a(st), _raw(stream, dev)), "sbp_expert_sort")
+    _check(_lib.sbp_expert_sort(_a(ids), T, k, E, _a(rows), _a(slots), _a(offsets), _a(workspace),
+                                0 if workspace is None else workspace.numel(), _a(st), _raw(stream, dev)), "sbp_expert_sort")
     return dict(rows=rows, slots=slots, offsets=offsets, status=st)
 
 

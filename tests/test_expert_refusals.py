@@ -44,7 +44,7 @@ def test_calls(sbp):
         (sbp._lib.sbp_expert_sort, SORT,
          [(I, dict(t=-1)), (I, dict(k=0)), (I, dict(e=0)), (U, dict(e=1025)), (U, dict(t=BIG)), (U, dict(t=1 << 20, k=1 << 12)),
           (I, dict(Ids=None)), (I, dict(Rows=None)), (I, dict(Slots=None)), (I, dict(Off=None)), (I, dict(St=None)),
-          (L, dict(Ids=0x1002)), (W, dict(Ws=None)), (W, dict(Ws=0x100010)), (W, dict(wsb=16))]),
+          (L, dict(Ids=0x1002)), (W, dict(t=2000, Ws=None)), (W, dict(t=2000, Ws=0x100010)), (W, dict(t=2000, wsb=16))]),
         (sbp._lib.sbp_expert_gather, GATHER,
          [(I, dict(t=-1)), (I, dict(k=0)), (I, dict(n=-1)), (I, dict(d=0)), (I, dict(dt=3)), (U, dict(d=60)), (U, dict(d=16392)),
           (U, dict(dt=2, d=72, S=0x4000, Ss=0x5000)), (U, dict(t=BIG)), (I, dict(X=None)), (I, dict(Rows=None)),
@@ -88,7 +88,7 @@ def test_calls(sbp):
 def test_queries(sbp):
     f = sbp._lib.sbp_expert_sort_workspace_bytes
     assert f(-1, 2, 8) == 0 and f(4, 0, 8) == 0 and f(4, 2, 0) == 0 and f(4, 2, 1025) == 0 and f(1 << 30, 2, 8) == 0
-    assert f(0, 2, 8) > 0 and f(1 << 20, 8, 256) <= (1 << 23) // 4096 * 256 * 4 + 1024
+    assert f(0, 2, 8) > 0 and f(1 << 20, 8, 256) <= (1 << 23) // 2048 * 256 * 4 + 1024
     assert sbp.token_blocks(0, 3) == 0 and sbp.token_blocks(1, 1) == 1 and sbp.token_blocks(129, 1) == 2
     assert sbp.token_blocks(5, 8) == 5 and sbp.token_blocks(256, 3) == (256 + 3 * 127) // 128
     assert sbp.token_blocks(-1, 1) == -1 and sbp.token_blocks(4, 0) == -1 and sbp.token_blocks(4, 1025) == -1
