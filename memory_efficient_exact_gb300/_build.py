@@ -21,7 +21,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsbp.so")
 SOURCES = ["sbp_api.cu", "sbp_simt.cu", "sbp_tc.cu", "sbp_mlp.cu", "sbp_attn.cu", "sbp_attn_fused.cu",
            "sbp_attn_packed.cu", "sbp_attn_fwd.cu", "sbp_norm.cu", "sbp_rope.cu", "sbp_experts.cu",
-           "sbp_quant.cu", "sbp_mm8.cu", "sbp_mm8_tc.cu"]
+           "sbp_quant.cu", "sbp_mm8.cu", "sbp_mm8_tc.cu", "sbp_mm8_swap.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include"),
          "--expt-relaxed-constexpr"]

@@ -176,20 +176,22 @@ cudaError_t few(const P& p, cudaStream_t s) {
 }
 
 // k_mm8_few reads each unit's matrix at 5.2 TB/s (8 rows x 24576 x 4096: 19.6 us), and takes 1.55
-// and 2.65 times as long for units of 16 and 32 rows, whose values are converted for every strip;
-// the tensor cores' tiles cost the same for 1 row as for 256.  The rule compares what that comes to;
-// measured, few and many, in us: 4096 x 4096, 32 rows 10.7 and 16.4, 48 rows 16.2 and 16.5, 64 rows
-// 19.3 and 16.5; 512 x 512, 300 rows 5.7 and 10.3, 1000 rows 9.9 and 10.3; 64 experts of 4096 x 2560,
-// 192 rows 120 and 137, 400 rows 149 and 140, 1000 rows 297 and 165; 8 experts of 4096 x 4096, 64
-// rows 33 and 41, 128 rows 58 and 42.
-bool is_few(const P& p) {
+// and 2.65 times as long for units of 16 and 32 rows, whose values are converted for every strip.
+int64_t few_ns(const P& p) {
   const int nt = few_tiles(p);
   const int64_t bytes = (int64_t)p.nb * about_blocks(p) * 128;
-  return 4000 + about_units(p, 8 * nt) * bytes / 5200 * (nt == 1 ? 100 : nt == 2 ? 155 : 265) / 100 <= many_ns(p);
+  return 4000 + about_units(p, 8 * nt) * bytes / 5200 * (nt == 1 ? 100 : nt == 2 ? 155 : 265) / 100;
 }
 
+// The kernel that takes the least time by the three rules.  Measured, few / many / swap, in us:
+//   4096 x 4096, rows 1, 32, 48, 64:            6.8 17 16,  11 16 18,  16 16 18,  19 17 18
+//   24576 x 4096, rows 8, 32, 64:               21 33 23,  (33) 33 28,  - 34 39
+//   512 x 512, rows 300, 1000:                  5.7 10 -,  9.9 10 -
+//   64 experts, 4096 x 2560, rows 64, 192, 400, 1000, 2000:  74 92 68,  120 131 95,  149 133 97,  297 156 114,  555 159 139
+//   8 experts, 4096 x 4096, rows 16, 64, 128, 256:           22 40 24,  33 41 31,  58 42 31,  98 43 39
 int run(const P& p, cudaStream_t s) {
-  if ((is_few(p) ? few(p, s) : many(p, s)) != cudaSuccess) return SBP_ERR_CUDA;
+  const int64_t f = few_ns(p), m = many_ns(p), w = p.columns ? INT64_MAX : swap_ns(p);
+  if ((f <= m && f <= w ? few(p, s) : m <= w ? many(p, s) : swap(p, s)) != cudaSuccess) return SBP_ERR_CUDA;
   set_launch_count(1);
   return SBP_OK;
 }

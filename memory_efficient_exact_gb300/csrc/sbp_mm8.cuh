@@ -80,6 +80,9 @@ inline int64_t about_blocks(const P& p) {
 // The kernel for many rows (sbp_mm8_tc.cu): enqueues the status word's reset and the product.
 cudaError_t many(const P& p, cudaStream_t s);
 int64_t many_ns(const P& p);   // about how long it takes
+// Few rows of many experts (sbp_mm8_swap.cu; rows only): the same.
+cudaError_t swap(const P& p, cudaStream_t s);
+int64_t swap_ns(const P& p);
 
 }  // namespace mm8
 }  // namespace sbp

@@ -21,20 +21,10 @@
 // before this one's additions (1456, and 1946 against 1453 with narrow tiles).
 #include <algorithm>
 
-#include "sbp_mm8.cuh"
-#include "sbp_rows.cuh"
-#include "sbp_tc_common.cuh"
+#include "sbp_mm8_tc.cuh"
 
 namespace sbp {
 namespace tc {
-
-__device__ __forceinline__ void mma2_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 
 // Warp 0 loads the operands, warps 1 and 2 multiply, warp 3 loads the scales, warps 4 to 11 are the
 // epilogue's: 32 rows x 64 columns of each accumulator.  The block's 12 x 32 threads are launched
@@ -50,9 +40,7 @@ constexpr uint32_t mm8_stage_bytes(int halves) { return A_BYTES + halves * B_BYT
 constexpr int BUFS = 4, BUF_N = 128;     // accumulators of one block: 128 columns each
 constexpr int SC_KB = 4;                 // blocks of a stage of the scales' ring
 constexpr uint32_t STG_MM8 = 32 * 64;    // a warp's staging block: 32 rows of 64 bytes
-// Instruction descriptor of tcgen05.mma kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B e4m3 (bits
-// 7-9 and 10-12 = 0), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
-constexpr uint32_t IDESC_E4M3 = (1u << 4) | (uint32_t(BUF_N >> 3) << 17) | (uint32_t(256 >> 4) << 24);
+constexpr uint32_t IDESC_E4M3 = idesc_e4m3(256, BUF_N);
 
 struct Mm8Ctrl {
   uint64_t full[8], empty[8];
@@ -68,40 +56,6 @@ constexpr size_t SMEM_MM8 = 6 * STAGE_BYTES + MM8_EPI * STG_MM8 + sizeof(Mm8Ctrl
 static_assert(mm8_stages(1) * mm8_stage_bytes(1) == 6 * STAGE_BYTES && mm8_stages(2) * mm8_stage_bytes(2) == 6 * STAGE_BYTES &&
                   SMEM_MM8 <= 232448,
               "shared memory budget of one CTA");
-
-__device__ __forceinline__ void fail_mm8(Mm8Ctrl* c, int32_t* status) {
-  *(volatile int*)&c->abort = 1;
-  if (status) atomicCAS(status, 0, SBP_ERR_TIMEOUT);
-}
-// An arrival on a barrier of this CTA, or on one of the pair's (no branch).
-__device__ __forceinline__ void arrive_if(bool here, uint32_t local, bool there, uint32_t remote) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t@q mbarrier.arrive.shared::cluster.b64 _, [%3];\n\t}" ::"r"(
-          (int)here),
-      "r"(local), "r"((int)there), "r"(remote)
-      : "memory");
-}
-template <bool CLUSTER>
-__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, Mm8Ctrl* c, uint64_t limit) {
-  return __all_sync(0xffffffffu, wait_inl<CLUSTER>(b, parity & 1u, &c->abort, limit));
-}
-// Tiles are walked in bands of this many units of 256 rows, all columns of a band before the next:
-// the 76 pairs' tiles then share 8 blocks of A's rows and 9 or 10 of B's.  (16: 2% slower.)
-constexpr int BAND = 8;
-
-struct Tile {
-  mm8::Unit w;
-  int n0;
-};
-__device__ __forceinline__ Tile tile_of(const mm8::P& p, int units, int ntn, int bn, int t) {
-  const int band = t / (BAND * ntn), r = t - band * BAND * ntn;
-  const int high = min(BAND, units - band * BAND);
-  Tile o;
-  o.w = mm8::unit_of(p, 256, band * BAND + r % high);
-  o.n0 = r / high * bn;
-  return o;
-}
 
 template <int HALVES, int OUT, bool ACC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
@@ -168,7 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
       }
       const uint32_t ring = saddr(base), fb = mapa(saddr(&c->full[0]), 0);
       for (int t = pid; t < total && ok; t += npairs) {
-        const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
+        const Tile o = tile_of(p, 256, units, ntn, 128 * HALVES, t);
         const int arow = __shfl_sync(0xffffffffu, o.w.row0 + (int)rank * 128, 0);
         // of each 128 of the tile's columns, this CTA's 64 rows of B
         const int brow = __shfl_sync(0xffffffffu, (p.columns ? 0 : o.w.e * p.nb) + o.n0 + (int)rank * 64, 0);
@@ -205,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
         uint32_t done = 0, use = 15;   // blocks of the tiles before; the parity of each group's last release
         bool ok = !p.stall || warp_wait<false>(&c->mdone[j], 0, c, p.limit_ns);
         for (int t = pid; t < total && ok; t += npairs) {
-          const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
+          const Tile o = tile_of(p, 256, units, ntn, 128 * HALVES, t);
           const int nkb = o.w.kb1 - o.w.kb0;
           for (int kb = HALVES == 2 ? 0 : j; kb < nkb; kb += HALVES == 2 ? 1 : 2) {
             const uint32_t n = done + kb, stage = n % MM8_STAGES, phase = (n / MM8_STAGES) & 1u;
@@ -247,7 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
       bool ok = true;
       const bool quads = p.sa_pitch % SC_KB == 0 && reinterpret_cast<uintptr_t>(p.sa) % 16 == 0;
       for (int t = pid; t < total && ok; t += npairs) {
-        const Tile o = tile_of(p, units, ntn, 128 * HALVES, t);
+        const Tile o = tile_of(p, 256, units, ntn, 128 * HALVES, t);
         const float* sa[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -423,20 +377,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(c->tmem_base), "r"(TMEM_COLS)
                  : "memory");
   }
-}
-
-// Map over a row-major array of bytes, boxes of 128 bytes x `rows`, 128-byte swizzle, zeros outside.
-inline bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
-                        uint32_t rows) {
-  auto enc = encoder();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {pitch};
-  cuuint32_t box[2] = {128, rows};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace tc

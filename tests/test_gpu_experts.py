@@ -307,6 +307,16 @@ def test_product_of_experts_with_many_rows(sbp, lens, N, K, behind):
     check_product(sbp, off, N, K, "bf16", N + K + len(lens), T=off[-1] + behind)
 
 
+# few rows of several wide matrices: the kernel with the operands exchanged
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,N,K,behind", [
+    ([10, 0, 1, 33, 32, 31, 64, 9, 0, 17, 5, 3], 4096, 2064, 0), ([3] * 40, 2056, 2576, 7), ([20, 41, 7, 16], 8200, 1040, 0),
+    ([65, 0, 100, 2, 30, 8, 8, 70], 4104, 4112, 3), ([32], 24584, 1168, 0)])
+def test_product_of_experts_with_few_rows(sbp, lens, N, K, behind, dtype):
+    off = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    check_product(sbp, off, N, K, dtype, N + K + len(lens), T=off[-1] + behind)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("lens,N,K,behind", [
     ([1, 0, 2], 264, 272, 0), ([0, 0, 5, 0], 128, 128, 3), ([3] * 40, 136, 400, 0), ([0, 9, 17, 33, 1, 0], 512, 2064, 1),
@@ -362,21 +372,21 @@ def test_nothing_to_do(sbp):
     assert (host(keep) == 3).all()
 
 
-@pytest.mark.parametrize("T,N", [(6, 256), (2000, 4096)])
+@pytest.mark.parametrize("T,N,K", [(6, 256, 128), (2000, 4096, 128), (60, 8192, 2048)])
 @pytest.mark.parametrize("bad", [[1, 2, 4], [0, 5, 4], [0, 2, 100000], [0, -1, 4], [-2, 2, 4]])
-def test_bad_tables(sbp, bad, T, N):
+def test_bad_tables(sbp, bad, T, N, K):
     """A status, and nothing is read or written by a bad table."""
     off = torch.tensor(bad, dtype=torch.int32, device="cuda")
-    x = torch.randn(T, 128, device="cuda")
-    w = sbp.quant_e4m3_weight(torch.randn(2, N, 128, device="cuda"))
+    x = torch.randn(T, K, device="cuda")
+    w = sbp.quant_e4m3_weight(torch.randn(2, N, K, device="cuda"))
     q = sbp.quant_e4m3(x)
     C = torch.full((T, N), 5.0, device="cuda")
     r = sbp.matmul_e4m3(q["Y8"], q["scales"], w["W8"], w["scales"], offsets=off, C=C)
     nb = sbp.token_blocks(T, 2)
-    yt = torch.zeros((128, 128 * nb), device="cuda").to(F8)
+    yt = torch.zeros((K, 128 * nb), device="cuda").to(F8)
     c = sbp.quant_e4m3_columns(x, offsets=off, Yt8=yt)
     d = sbp.quant_e4m3_columns(x, offsets=off, tiles=True)
-    dW = torch.full((2, 128, 128), 5.0, device="cuda")
+    dW = torch.full((2, K, K), 5.0, device="cuda")
     m = sbp.matmul_e4m3_columns(c["Yt8"], c["scales_t"], d["Yt8"], d["scales_t"], T, offsets=off, dW=dW)
     torch.cuda.synchronize()
     for v in (r, c, d, m):
@@ -387,8 +397,8 @@ def test_bad_tables(sbp, bad, T, N):
 def test_values_that_are_not_finite(sbp):
     """A NaN reaches its own row and column of the product, and no other."""
     g = np.random.default_rng(8)
-    for T, N in ((5, 264), (300, 264), (1100, 4104)):
-        a, sa, b, sb = operands(g, T, N, 256, 1)
+    for T, N, K in ((5, 264, 256), (300, 264, 256), (1100, 4104, 256), (30, 24584, 1040)):
+        a, sa, b, sb = operands(g, T, N, K, 1)
         A, B = dev(a, F8), dev(b[0], F8)
         clean = host(sbp.matmul_e4m3(A, dev(sa, F32), B, dev(sb[0], F32))["C"])
         A.view(torch.uint8)[3, 200] = 0x7f

@@ -55,7 +55,8 @@ for i, (T, k, E) in enumerate([(1, 8, 64), (700, 3, 1000), (3000, 8, 33)]):
     done(f"route{i}", [Xs, Y, dYs, dw])
 
 for i, (lens, N, K) in enumerate([([1], 272, 272), ([0, 3, 9], 144, 400), ([40, 0, 300, 257], 528, 656), ([1700], 2064, 1168),
-                                  ([900, 0, 3, 1100], 1040, 1296)]):
+                                  ([900, 0, 3, 1100], 1040, 1296),
+                                  ([10, 0, 1, 33, 32, 31, 9, 17, 5], 4096, 2064)]):
     T, E = sum(lens), len(lens)
     off = None if E == 1 else torch.tensor([sum(lens[:j]) for j in range(E + 1)], dtype=i32).cuda()
     lead = () if E == 1 else (E,)
@@ -106,7 +107,7 @@ def test_guard_zones_and_output_padding():
     assert plain.pop("lib") == "libsbp.so" and checked.pop("lib") == "libsbp_checked.so"
     over = checked.pop("overrun")
     assert checked.pop("planted")[0] == over and checked.pop("after")[0] == 0
-    assert set(plain) == set(checked) and len(plain) == 16
+    assert set(plain) == set(checked) and len(plain) == 18
     for k, (status, padding, bits) in plain.items():
         assert status == 0 and padding, k
         assert checked[k] == [0, True, bits], k
@@ -121,7 +122,7 @@ _build.build_library()
 from memory_efficient_exact_gb300 import sbp
 g = torch.Generator(device="cuda").manual_seed(1)
 res = []
-for T, N, K, dt in [(600, 4096, 1024, torch.bfloat16), (4096, 4096, 1024, torch.float32)]:
+for T, N, K, dt in [(600, 4096, 1024, torch.bfloat16), (4096, 4096, 1024, torch.float32), (32, 24576, 4096, torch.bfloat16)]:
     n = lambda *s: torch.randn(s, generator=g, device="cuda")
     q, w = sbp.quant_e4m3(n(T, K)), sbp.quant_e4m3_weight(n(N, K))
     x, y = sbp.quant_e4m3_columns(n(T, N)), sbp.quant_e4m3_columns(n(T, K), tiles=True)
