@@ -74,34 +74,39 @@ def combine_backward(dY, Ys, rows, weights):
 
 def round_e4m3(x):
     """x (any floats) to e4m3's values, to nearest, ties to the even code; beyond 448: 448."""
-    x = _f64(x)
+    x = np.asarray(x)
     a = np.abs(x)
-    mid = (E4M3[:-1] + E4M3[1:]) / 2
-    i = np.searchsorted(mid, a, side="left")           # a <= mid[i]
-    tie = (i < mid.size) & (a == mid[np.minimum(i, mid.size - 1)])
-    i = np.where(tie & (i % 2 == 1), i + 1, i)
-    return np.where(np.isnan(x), np.nan, np.copysign(E4M3[np.minimum(i, E4M3.size - 1)], x))
+    # steps of 2^-3 of the value's power of two, 2^-9 below 2^-6; rint takes ties to the even step
+    step = np.ldexp(np.ones((), dtype=a.dtype), np.maximum(np.frexp(a)[1] - 1, -6) - 3)
+    with np.errstate(invalid="ignore"):
+        return np.copysign(np.minimum(np.rint(a / step) * step, 448), x).astype(np.float64)
 
 
 def block(x):
     """(values in 8 bits, scale) of one block of float32 values."""
     x = np.asarray(x, dtype=np.float32)
-    m = np.max(np.abs(x)) if x.size else np.float32(0)
-    s = np.maximum(m * (np.float32(1) / np.float32(448)), np.float32(2.0 ** -126)) if m > 0 else np.float32(1)
+    s = scale(np.max(np.abs(x)) if x.size else np.float32(0))
     return round_e4m3(x * (np.float32(1) / s)), s
+
+
+def scale(m):
+    """The scale of blocks whose largest magnitudes are m."""
+    m = np.asarray(m, dtype=np.float32)
+    s = np.maximum(m * (np.float32(1) / np.float32(448)), np.float32(2.0 ** -126))
+    return np.where(m > 0, s, np.float32(1))
 
 
 def quant(x, tall=1):
     """x [T, d]: blocks of `tall` rows x 128 columns -> values in 8 bits and scales."""
     x = np.asarray(x, dtype=np.float32)
     T, d = x.shape
-    q = np.zeros((T, d))
-    s = np.zeros(((T + tall - 1) // tall, (d + 127) // 128), dtype=np.float32)
-    for i in range(s.shape[0]):
-        for j in range(s.shape[1]):
-            r, c = slice(tall * i, tall * i + tall), slice(128 * j, 128 * j + 128)
-            q[r, c], s[i, j] = block(x[r, c])
-    return q, s
+    nr, nc = (T + tall - 1) // tall, (d + 127) // 128
+    full = np.zeros((nr * tall, nc * 128), dtype=np.float32)
+    full[:T, :d] = x
+    full = full.reshape(nr, tall, nc, 128)
+    s = scale(np.abs(full).max(axis=(1, 3), initial=0))
+    q = round_e4m3(full * (np.float32(1) / s)[:, None, :, None])
+    return q.reshape(nr * tall, nc * 128)[:T, :d], s
 
 
 def columns(x, offsets):

@@ -310,7 +310,7 @@ def test_product_of_experts_with_many_rows(sbp, lens, N, K, behind):
 # few rows of several wide matrices: the kernel with the operands exchanged
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("lens,N,K,behind", [
-    ([10, 0, 1, 33, 32, 31, 64, 9, 0, 17, 5, 3], 4096, 2064, 0), ([3] * 40, 2056, 2576, 7), ([20, 41, 7, 16], 8200, 1040, 0),
+    ([10, 0, 1, 33, 32, 31, 64, 9, 0, 17, 5, 3], 4096, 2064, 0), ([3] * 24, 2056, 2576, 7), ([20, 41, 7, 16], 8200, 1040, 0),
     ([65, 0, 100, 2, 30, 8, 8, 70], 4104, 4112, 3), ([32], 24584, 1168, 0)])
 def test_product_of_experts_with_few_rows(sbp, lens, N, K, behind, dtype):
     off = np.concatenate([[0], np.cumsum(lens)]).tolist()

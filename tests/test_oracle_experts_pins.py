@@ -29,6 +29,18 @@ def test_block_scale():
     assert s == np.float32(2.0 ** -126)
 
 
+def test_quant_is_block_by_block():
+    g = np.random.default_rng(1)
+    for T, d, tall in ((1, 5, 1), (7, 300, 1), (130, 140, 128), (0, 8, 1)):
+        x = (g.standard_normal((T, d)) * np.exp(3 * g.standard_normal((T, d)))).astype(np.float32)
+        q, s = X.quant(x, tall)
+        for i in range(s.shape[0]):
+            for j in range(s.shape[1]):
+                r, c = slice(tall * i, tall * i + tall), slice(128 * j, 128 * j + 128)
+                bq, bs = X.block(x[r, c])
+                assert np.array_equal(q[r, c], bq) and s[i, j] == bs
+
+
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (7, 2, 3), (40, 8, 16), (33, 3, 200)])
 def test_sort(T, k, E):
     g = np.random.default_rng(T)
