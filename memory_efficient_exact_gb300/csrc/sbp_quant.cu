@@ -301,39 +301,36 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
   }
 }
 
-// Y = q * scale: blocks of `tall` rows x 128 columns, 16 elements a thread (n16 of them a row).
-template <typename O>
+// Y = q * scale: blocks of 2^shift rows x 128 columns, 8 elements a thread (n8 of them a row) twice,
+// so that a warp's loads and stores are whole lines.
+template <typename O, typename I>
 __global__ void __launch_bounds__(256) k_quant_expand(const uint8_t* __restrict__ q, const float* __restrict__ scales,
-                                                      int64_t n, uint32_t n16, int d, int shift, int nblk,
-                                                      O* __restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int64_t row = i / n16;
-  const int c = (int)(i - row * n16) * 16;
-  const float s = scales[(row >> shift) * nblk + c / 128];
-  const int64_t at = row * d + c;
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  const uint2 lo = *reinterpret_cast<const uint2*>(q + at);
-  w[0] = lo.x;
-  w[1] = lo.y;
-  const bool two = c + 8 < d;   // d is a multiple of 8
-  if (two) {
-    const uint2 hi = *reinterpret_cast<const uint2*>(q + at + 8);
-    w[2] = hi.x;
-    w[3] = hi.y;
+                                                      I n, uint32_t n8, int shift, int nblk, O* __restrict__ out) {
+  uint2 u[2];
+  float s[2];
+  const I i0 = (I)blockIdx.x * 512 + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const I i = i0 + 256 * k;
+    if (i < n) {
+      const I row = i / n8;
+      u[k] = *reinterpret_cast<const uint2*>(q + (int64_t)i * 8);
+      s[k] = scales[(int64_t)(row >> shift) * nblk + (uint32_t)(i - row * n8) / 16];
+    }
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int k = 0; k < 2; ++k) {
+    const I i = i0 + 256 * k;
+    const uint32_t w[2] = {u[k].x, u[k].y};
     F8 f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __half2_raw r =
-          __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[2 * h + k / 2] >> (16 * (k % 2))), __NV_E4M3);
+    for (int j = 0; j < 4; ++j) {
+      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j / 2] >> (16 * (j % 2))), __NV_E4M3);
       const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&r));
-      f.v[2 * k] = x.x * s;
-      f.v[2 * k + 1] = x.y * s;
+      f.v[2 * j] = x.x * s[k];
+      f.v[2 * j + 1] = x.y * s[k];
     }
-    if (h == 0 || two) store8(out + at + 8 * h, f);
+    if (i < n) store8(out + (int64_t)i * 8, f);
   }
 }
 
@@ -394,21 +391,23 @@ int sbp_quant_e4m3_expand(const void* Y8, const float* scales, int64_t T, int64_
   const int rc = quant_check(T, d, dtype);
   if (rc != SBP_OK) return rc;
   if ((tiles != 0 && tiles != 1) || (T > 0 && (!Y8 || !scales || !Y))) return SBP_ERR_INVALID_ARG;
-  const int64_t n16 = (d + 15) / 16;
-  if ((T * n16 + 255) / 256 > INT32_MAX) return SBP_ERR_UNSUPPORTED;
+  const int64_t n = T * (d / 8), blocks = (n + 511) / 512;
+  if (blocks > INT32_MAX) return SBP_ERR_UNSUPPORTED;
   if (!aligned16(Y8) || !aligned16(Y) || !aligned4(scales)) return SBP_ERR_ALIGNMENT;
   NvtxRange nv("sbp_quant_e4m3_expand");
   set_launch_count(0);
   if (T == 0) return SBP_OK;
-  const unsigned grid = (unsigned)((T * n16 + 255) / 256);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint8_t* q = static_cast<const uint8_t*>(Y8);
-  if (dtype == SBP_BF16)
-    k_quant_expand<<<grid, 256, 0, s>>>(q, scales, T * n16, (uint32_t)n16, (int)d, tiles ? 7 : 0, (int)((d + 127) / 128),
-                                        static_cast<__nv_bfloat16*>(Y));
-  else
-    k_quant_expand<<<grid, 256, 0, s>>>(q, scales, T * n16, (uint32_t)n16, (int)d, tiles ? 7 : 0, (int)((d + 127) / 128),
-                                        static_cast<float*>(Y));
+  const int shift = tiles ? 7 : 0, nblk = (int)((d + 127) / 128);
+  auto go = [&](auto* y) {   // 32-bit indices where they do
+    if (n < (int64_t(1) << 31))
+      k_quant_expand<<<(unsigned)blocks, 256, 0, s>>>(q, scales, (uint32_t)n, (uint32_t)(d / 8), shift, nblk, y);
+    else
+      k_quant_expand<<<(unsigned)blocks, 256, 0, s>>>(q, scales, n, (uint32_t)(d / 8), shift, nblk, y);
+  };
+  if (dtype == SBP_BF16) go(static_cast<__nv_bfloat16*>(Y));
+  else go(static_cast<float*>(Y));
   return launched();
 }
 
