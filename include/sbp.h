@@ -448,7 +448,9 @@ int sbp_quant_e4m3_weight(const void* W, int64_t E, int64_t N, int64_t K, int dt
 /* C[i, n] = sum_b sa[i, b] sb[e, n / 128, b] sum_k A8[i, k] B8[e, n, k] over the blocks b of 128 k,
  * for the rows i of expert e.  A8 [T, K] e4m3 with sa [T, ceil(K / 128)]; B8 [E, N, K] with sb
  * [E, ceil(N / 128), ceil(K / 128)]; C [T, N] bf16 or fp32 (out_dtype).  A block's sum and the sum
- * over the blocks are fp32.  K must be a multiple of 16, N of 8.
+ * over the blocks are fp32, and so is sa sb, which is formed first: below 2^-126 it loses precision,
+ * from 2^128 on it is infinite.  Which of three kernels runs goes by the sizes (host values alone);
+ * they differ in the order of the fp32 sums.  K must be a multiple of 16, N of 8.
  * columns: dW[e] (+)= sum over expert e's tokens of At8 and Bt8, both as sbp_quant_e4m3_columns
  * leaves them for these offsets (At8 [N, 128 nb] without tiles, Bt8 [K, 128 nb] with): dW [E, N, K]
  * fp32, overwritten (accumulate = 0; zeros for an expert without rows) or added to (1).
