@@ -6,19 +6,20 @@
 // it back, and add it, times sa[row] sb[column block], to the tile's sums in their registers.
 //
 // What bounds it is not the products (512 cycles a block of a 256 x 256 tile) but this exchange:
-// 512 columns of tensor memory are in flight, and an accumulator takes some 1700 cycles from the
-// products' issue over the commit, the read and the arrival of both CTAs' warps to the next issue
-// (850 a block); the additions come on top in part (1080).  Hence the shape of the loops: two warps
-// issue, so that one tests its barriers while the other's products run; an epilogue warp asks for
-// its whole share of an accumulator at once (64 registers) and releases it before it adds anything
-// up; its loop is unrolled over the accumulators with no branches but the waits'; the scales are
-// multiplied and put in place by a warp of their own.  16384 x 24576 x 4096: 4130 us with two
-// accumulators of 256 columns, 16 epilogue warps that loaded 16 columns at a time and scales read
-// by each; 1785 with four accumulators of 128 and the scales' warp; 1717 with two issuing warps;
-// 1383 with eight epilogue warps of 224 registers and the unrolled loop; 1350 with the scales
-// multiplied in advance (2440 TFLOP/s; 1066 without the additions).  Not faster: packed additions of two values (1599
-// against 1620 TFLOP/s in an earlier form), 16 epilogue warps (1405), the next accumulator's load
-// before this one's additions (1456, and 1946 against 1453 with narrow tiles).
+// 512 columns of tensor memory are in flight, and an accumulator takes some 2000 cycles from the
+// products' issue over the commit, the read and the arrival of both CTAs' warps to the next issue,
+// so 1000 a block.  Hence the shape of the loops: two warps issue, so that one tests its barriers
+// while the other's products run; with tiles of 256 columns the two epilogue warps of a scheduler
+// take different accumulators, so that one adds while the other waits and loads; an epilogue warp
+// asks for 64 columns at once and releases an accumulator before it adds its last ones up; its loop
+// is unrolled over the accumulators with no branches but the waits'; the scales are multiplied and
+// put in place by a warp of their own.  16384 x 24576 x 4096: 4130 us with two accumulators of 256
+// columns, 16 epilogue warps that loaded 16 columns at a time and scales read by each; 1785 with
+// four accumulators of 128 and the scales' warp; 1717 with two issuing warps; 1383 with eight
+// epilogue warps of 224 registers and the unrolled loop; 1350 with the scales multiplied in advance;
+// 1285 with accumulators of their own (2570 TFLOP/s).  Not faster: packed additions of two values
+// (1599 against 1620 TFLOP/s in an earlier form), 16 epilogue warps (1405 against 1355), the next
+// columns' load before these are added (1352 against 1290).
 #include <algorithm>
 
 #include "sbp_mm8_tc.cuh"
@@ -27,7 +28,7 @@ namespace sbp {
 namespace tc {
 
 // Warp 0 loads the operands, warps 1 and 2 multiply, warp 3 loads the scales, warps 4 to 11 are the
-// epilogue's: 32 rows x 64 columns of each accumulator.  The block's 12 x 32 threads are launched
+// epilogue's: 32 rows x 64 columns of each accumulator, or x 128 of every other one.  The block's 12 x 32 threads are launched
 // with 168 registers each; the epilogue's 128 sums and 64 values in flight need more, so the first
 // four warps hand theirs over.  (Waits are inlined: a call would not know of the split.)
 constexpr int MM8_EPI = 8, MM8_THREADS = 128 + 32 * MM8_EPI;
@@ -84,8 +85,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
     }
     for (int i = 0; i < BUFS; ++i) {
       mbar_init(&c->tfull[i], 1);
-      mbar_init(&c->tempty_l[i], MM8_EPI);
-      mbar_init(&c->tempty_r[i], MM8_EPI);
+      mbar_init(&c->tempty_l[i], MM8_EPI / HALVES);
+      mbar_init(&c->tempty_r[i], MM8_EPI / HALVES);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->sfull[i], 1);
@@ -244,10 +245,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_MANY));
-    // warps 4 to 7: the first 64 columns of each accumulator, warps 8 to 11: the second
+    // warps 4 to 7: the first 128 columns of the tile (the first 64, where there are 128), warps 8 to
+    // 11: the second
     const int q = warp & 3, h = (warp - 4) >> 2;
     const uint32_t stg = saddr(stg_base + (warp - 4) * STG_MM8);
-    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 64);
+    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(HALVES == 2 ? 0 : h * 64);
     // where this warp's lane 0 says that it has read an accumulator: on the leader's barrier for its
     // own warps or for the other CTA's
     const bool p0 = lane == 0 && rank == 0, p1 = lane == 0 && rank != 0;
@@ -271,41 +273,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
           tile = c->tile[ss][0];
           nkb = c->tile[ss][1].x;
         }
-        float sk[HALVES][SC_KB];
-#pragma unroll
-        for (int j = 0; j < HALVES; ++j) {
-          const float4 v = c->scale[ss][j][q * 32 + lane];
-          sk[j][0] = v.x;
-          sk[j][1] = v.y;
-          sk[j][2] = v.z;
-          sk[j][3] = v.w;
-        }
+        const float4 sv = c->scale[ss][HALVES == 2 ? h : 0][q * 32 + lane];
+        const float sk[SC_KB] = {sv.x, sv.y, sv.z, sv.w};
         __syncwarp();
         arrive_if(lane == 0, saddr(&c->sempty[ss]), false, 0);
 #pragma unroll
         for (int k = 0; k < SC_KB; ++k) {
           if (kb + k >= nkb) break;
+          constexpr uint32_t S = sizeof(uint64_t);
+          const uint32_t g = k % GROUPS, buf = HALVES == 2 ? 2 * g + h : g;
+          ok = wait_inl<false>(&c->tfull[buf], (use >> g) & 1u, &c->abort, p.limit_ns) && ok;
+          __syncwarp();
+          tc_fence_after();
 #pragma unroll
           for (int j = 0; j < HALVES; ++j) {
-            constexpr uint32_t S = sizeof(uint64_t);
-            const uint32_t g = k % GROUPS, buf = HALVES * g + j;
-            ok = wait_inl<false>(&c->tfull[buf], (use >> g) & 1u, &c->abort, p.limit_ns) && ok;
-            __syncwarp();
-            tc_fence_after();
             uint32_t r[2][32];
-            tmem_ld32(tb + buf * BUF_N, r[0]);
-            tmem_ld32(tb + buf * BUF_N + 32, r[1]);
+            tmem_ld32(tb + buf * BUF_N + 64 * j, r[0]);
+            tmem_ld32(tb + buf * BUF_N + 64 * j + 32, r[1]);
             tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            arrive_if(p0, rel_l + buf * S, p1, rel_r + buf * S);
+            if (j == HALVES - 1) {
+              tc_fence_before();
+              __syncwarp();
+              arrive_if(p0, rel_l + buf * S, p1, rel_r + buf * S);
+            }
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                acc[j][32 * x + i] = fmaf(__uint_as_float(r[x][i]), sk[j][k], acc[j][32 * x + i]);
+                acc[j][32 * x + i] = fmaf(__uint_as_float(r[x][i]), sk[k], acc[j][32 * x + i]);
           }
-          use ^= 1u << (k % GROUPS);
+          use ^= 1u << g;
         }
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -319,13 +316,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MM8_THREADS, 1)
       constexpr int ES = OUT == SBP_BF16 ? 2 : 4, PASS = 64 / ES;   // columns a pass
       const int r0 = (int)rank * 128 + q * 32;            // this warp's first row of the unit
       const int rows = tile.z - r0 - lane / 4;            // how many there are from this lane's first on
-      const int col0 = tile.w + h * 64 + (lane % 4) * (16 / ES);
+      const int col0 = tile.w + h * (HALVES == 2 ? 128 : 64) + (lane % 4) * (16 / ES);
       uint8_t* out = static_cast<uint8_t*>(p.C) +
                      ((int64_t)tile.x * p.c_stride + (int64_t)(tile.y + r0 + lane / 4) * p.nb + col0) * ES;
       const int64_t down = (int64_t)8 * p.nb * ES;
 #pragma unroll
       for (int gg = 0; gg < HALVES * 64 / PASS; ++gg) {
-        const int j = gg / (64 / PASS), g = gg % (64 / PASS), cc = j * 128 + g * PASS;
+        const int j = gg / (64 / PASS), g = gg % (64 / PASS), cc = j * 64 + g * PASS;
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -418,12 +415,12 @@ cudaError_t launch_many(const P& p, cudaStream_t s) {
   return p.accumulate ? launch_many<HALVES, SBP_FP32, true>(p, s) : launch_many<HALVES, SBP_FP32, false>(p, s);
 }
 
-// Tiles of 256 columns take 522 ns a block on all pairs at once, tiles of 128 columns 281 (16384 x
-// 24576 x 4096: 1350 and 1453 us); the narrow ones leave fewer pairs idle (501 x 4096 x 12288: 53
+// Tiles of 256 columns take 496 ns a block on all pairs at once, tiles of 128 columns 281 (16384 x
+// 24576 x 4096: 1285 and 1453 us); the narrow ones leave fewer pairs idle (501 x 4096 x 12288: 53
 // and 33 us).  The shorter of the two sums of rounds is taken.
 int64_t rounds_ns(const P& p, int halves) {
   const int64_t bn = 128 * halves, pairs = num_sms() / 2;
-  return (about_units(p, 256) * ((p.nb + bn - 1) / bn) + pairs - 1) / pairs * about_blocks(p) * (halves == 2 ? 522 : 281);
+  return (about_units(p, 256) * ((p.nb + bn - 1) / bn) + pairs - 1) / pairs * about_blocks(p) * (halves == 2 ? 496 : 281);
 }
 int64_t many_ns(const P& p) { return 8000 + std::min(rounds_ns(p, 1), rounds_ns(p, 2)); }
 
