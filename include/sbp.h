@@ -397,7 +397,8 @@ int sbp_expert_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t
 
 /* Xs[rows[t, j]] = X[t].  X [T, d], Xs [n_rows, d] dtype (SBP_BF16, SBP_FP32, or SBP_E4M3 with scales
  * [T, ceil(d / 128)] fp32, which go to scales_s [n_rows, ceil(d / 128)]; NULL otherwise).  A place
- * outside [0, n_rows) is left out; rows of Xs that no slot goes to are left as they were.  d: a
+ * outside [0, n_rows) is left out; rows of Xs that no slot goes to are left as they were.  Where rows
+ * are written, here and in combine's backward, no place may come twice (the sort's do not).  d: a
  * multiple of 8 (e4m3: 16), at most 16384.  No workspace and no status word, here and below; the
  * gradient is sbp_expert_combine of dXs without weights. */
 int sbp_expert_gather(const void* X, const float* scales, const int32_t* rows, int64_t T, int64_t k, int64_t n_rows,

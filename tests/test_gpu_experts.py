@@ -98,6 +98,21 @@ def test_sort_one_expert_for_all_and_many_blocks(sbp):
         assert np.array_equal(host(r["rows"]).reshape(-1), rows)
 
 
+@pytest.mark.parametrize("T,E", [(63 * 2048, 40), (63 * 2048 + 1, 40), (64 * 2048 + 77, 1024), ((1 << 20) + 7, 33), ((1 << 22) + 1, 5)])
+def test_sort_blocks_whose_counts_are_summed_once(sbp, T, E):
+    ids = np.random.default_rng(T).integers(-1, E, (T, 1))
+    r = sbp.expert_sort(dev(ids, torch.int32), E)
+    ok(r)
+    flat = ids.reshape(-1)
+    n = int((flat >= 0).sum())
+    order = np.argsort(np.where(flat < 0, E, flat), kind="stable")[:n]
+    assert np.array_equal(host(r["slots"])[:n], order)
+    assert np.array_equal(host(r["offsets"]), np.concatenate([[0], np.cumsum(np.bincount(flat[flat >= 0], minlength=E))]))
+    rows = np.full(T, -1)
+    rows[order] = np.arange(n)
+    assert np.array_equal(host(r["rows"]).reshape(-1), rows)
+
+
 def test_sort_id_past_the_last_expert(sbp):
     for T in (3, 5000):
         ids = np.random.default_rng(2).integers(0, 4, (T, 2))
