@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256) k_quant_tile(const TileP p) {
     row0 = (int64_t)e * p.wrows + ib * 128;
     rows = min(128, p.wrows - ib * 128);
   } else {
-    const Group g = find_unit(p.offsets, p.E, p.T, 128, b);
+    const Group g = find_unit_of_block(p.offsets, p.E, p.T, 128, b);
     if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = g.bad ? SBP_ERR_SEQLENS : SBP_OK;
     if (g.bad || !g.found) return;
     row0 = (int64_t)g.row0 + g.i * 128;

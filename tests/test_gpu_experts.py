@@ -372,6 +372,57 @@ def test_product_of_columns(sbp, lens, N, K):
     near("twice", host(again).reshape(want.shape), 2 * want, 2 * (steps + 1) * 2.0 ** -23 * terms)
 
 
+# tables that are longer than a warp, with empty experts at both ends and in between
+@pytest.mark.parametrize("T,E", [(1500, 33), (700, 64), (2100, 300), (900, 1023), (3000, 1024)])
+def test_long_tables(sbp, T, E):
+    g = np.random.default_rng(E)
+    cuts = np.sort(np.concatenate([np.zeros(E // 5, dtype=np.int64), g.integers(0, T + 1, E - 1 - 2 * (E // 5)),
+                                   np.full(E // 5, T)]))
+    off = np.concatenate([[0], cuts, [T]])
+    check_product(sbp, list(off), 136, 144, "fp32", E)
+    d, nb = 136, sbp.token_blocks(T, E)
+    x = wide(g, (T, d), "bf16")
+    xt = X.columns(x, off)
+    W = xt.shape[1]
+    out = {}
+    for tiles in (False, True):
+        yt = torch.full((d, 128 * nb), 1.0, device="cuda").to(F8)
+        out[tiles] = sbp.quant_e4m3_columns(dev(x, BF), offsets=dev(off, torch.int32), tiles=tiles, Yt8=yt)
+        ok(out[tiles])
+        q, s = X.quant(xt, 128 if tiles else 1)
+        assert np.array_equal(host(yt)[:, :W], q) and (host(yt)[:, W:] == 1).all()
+        assert np.array_equal(host(out[tiles]["scales_t"])[:, :W // 128], s.astype(np.float64))
+    a, b = out[False], out[True]
+    r = sbp.matmul_e4m3_columns(a["Yt8"], a["scales_t"], b["Yt8"], b["scales_t"], T, offsets=dev(off, torch.int32))
+    ok(r)
+    (qa, sa), (qb, sb) = X.quant(xt), X.quant(xt, 128)
+    want, terms = X.matmul_columns(qa, sa, qb, sb, off)
+    steps = 128 + (int(np.diff(off).max()) + 127) // 128 + 16
+    near("dW", host(r["dW"]), want, steps * 2.0 ** -23 * terms)
+
+
+def test_long_tables_many_rows(sbp):
+    lens = np.random.default_rng(5).integers(0, 130, 130)
+    check_product(sbp, [0] + list(np.cumsum(lens)), 1024, 512, "bf16", 6)
+
+
+@pytest.mark.parametrize("at", [0, 1, 31, 32, 33, 64, 255, 256, 299, 300])
+def test_long_tables_that_are_bad(sbp, at):
+    off = torch.arange(301, dtype=torch.int32, device="cuda")
+    x = torch.randn(300, 128, device="cuda")
+    w = sbp.quant_e4m3_weight(torch.randn(300, 16, 128, device="cuda"))
+    q = sbp.quant_e4m3(x)
+    for value in (-1, 301):
+        off[at] = value
+        C = torch.full((300, 16), 5.0, device="cuda")
+        yt = torch.zeros((128, 128 * sbp.token_blocks(300, 300)), device="cuda").to(F8)
+        r = sbp.matmul_e4m3(q["Y8"], q["scales"], w["W8"], w["scales"], offsets=off, C=C)
+        c = sbp.quant_e4m3_columns(x, offsets=off, Yt8=yt)
+        torch.cuda.synchronize()
+        assert int(r["status"].item()) == int(c["status"].item()) == sbp.ERR_SEQLENS
+        assert (host(C) == 5).all() and (host(yt) == 0).all()
+
+
 def test_nothing_to_do(sbp):
     off = torch.zeros(5, dtype=torch.int32, device="cuda")
     w = sbp.quant_e4m3_weight(torch.randn(4, 64, 128, device="cuda"))
