@@ -581,6 +581,44 @@ def test_other_stream_and_graph_follows_its_table(sbp):
             assert torch.equal(a, b)
 
 
+def test_two_streams_at_once(sbp):
+    """Calls on streams given by name, each product's kernels among another's: the same bits."""
+    T, E, k = 3000, 8, 2
+    torch.manual_seed(3)
+    ids = torch.randint(0, E, (T, k), device="cuda", dtype=torch.int32)
+    x = torch.randn(T, 1024, device="cuda").to(BF)
+    w = sbp.quant_e4m3_weight(torch.randn(E, 4096, 1024, device="cuda").to(BF))
+    few = sbp.quant_e4m3(torch.randn(40, 1024, device="cuda").to(BF))
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda") * 5
+    ones = torch.ones(T, k, device="cuda")
+
+    def step(stream):
+        o = sbp.expert_sort(ids, E, stream=stream)
+        xs = sbp.expert_gather(x, o["rows"], stream=stream)["Xs"]
+        q = sbp.quant_e4m3_columns(xs, offsets=o["offsets"], rows=True, stream=stream)
+        t = sbp.quant_e4m3_columns(xs, offsets=o["offsets"], tiles=True, stream=stream)
+        C = sbp.matmul_e4m3(q["Y8"], q["scales"], w["W8"], w["scales"], offsets=o["offsets"], stream=stream)
+        c = sbp.matmul_e4m3(few["Y8"], few["scales"], w["W8"], w["scales"], offsets=off, dtype=F32, stream=stream)
+        W = sbp.matmul_e4m3_columns(q["Yt8"], q["scales_t"], t["Yt8"], t["scales_t"], T * k, offsets=o["offsets"], stream=stream)
+        y = sbp.expert_combine(C["C"], o["rows"], stream=stream)["Y"]
+        e = sbp.quant_e4m3_expand(q["Y8"], q["scales"], stream=stream)["Y"]
+        b = sbp.expert_combine_backward(y, C["C"], o["rows"], ones, stream=stream)
+        return [o["rows"], C["C"], c["C"], W["dW"], y, e, b["dYs"], b["dweights"]], [v["status"] for v in (o, q, t, C, c, W)]
+
+    want, _ = step(None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        for s in streams:
+            got.append(step(s))
+    torch.cuda.synchronize()
+    for out, status in got:
+        assert all(int(v.item()) == 0 for v in status)
+        for g, v in zip(out, want):
+            assert torch.equal(g, v)
+
+
 def test_run_of_an_expert_mlp(sbp):
     """Norm in 8 bits, sort, gather, both products around a gated activation, combine; then the
     gradients: every stage against the oracle on what the stage before it left."""
