@@ -114,6 +114,10 @@ __device__ __forceinline__ Group find_unit_of_block(const int32_t* off, int E, i
   return g;
 }
 
+// A call without rows (T = 0): the status of its table, which may hold nothing but zeros, and, where it
+// is good, n floats of zeros (a multiple of 4; null: none).
+int no_rows(const int32_t* offsets, int64_t E, float* zeros, int64_t n, int32_t* status, cudaStream_t s);
+
 // The most units of `unit` rows that T rows of E experts can make up.
 inline int64_t max_units(int64_t T, int64_t E, int64_t unit) {
   const int64_t used = E < T ? E : T;

@@ -196,6 +196,14 @@ int run(const P& p, cudaStream_t s) {
   return SBP_OK;
 }
 
+__global__ void __launch_bounds__(256) k_no_rows(const int32_t* off, int E, float4* zeros, int64_t n, int32_t* status) {
+  const bool bad = find_unit(off, E, 0, 1, 0).bad;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = bad ? SBP_ERR_SEQLENS : SBP_OK;
+  if (bad) return;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    zeros[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 int check_common(int64_t E, int64_t T, int64_t N, int64_t K, const void* A8, const void* sa, const void* B8,
                  const void* sb, const int32_t* offsets, const void* C, const int32_t* status) {
   for (const void* q : {A8, B8, C})
@@ -206,6 +214,16 @@ int check_common(int64_t E, int64_t T, int64_t N, int64_t K, const void* A8, con
 }
 
 }  // namespace mm8
+
+int no_rows(const int32_t* offsets, int64_t E, float* zeros, int64_t n, int32_t* status, cudaStream_t s) {
+  const int64_t n4 = zeros ? n / 4 : 0;
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n4 + 255) / 256, (int64_t)num_sms() * 8));
+  mm8::k_no_rows<<<grid, 256, 0, s>>>(offsets, (int)E, reinterpret_cast<float4*>(zeros), n4, status);
+  if (cudaGetLastError() != cudaSuccess) return SBP_ERR_CUDA;
+  set_launch_count(1);
+  return SBP_OK;
+}
+
 }  // namespace sbp
 
 using namespace sbp;
@@ -226,7 +244,7 @@ int sbp_matmul_e4m3(const void* A8, const float* sa, const void* B8, const float
   NvtxRange nv("sbp_matmul_e4m3");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   set_launch_count(0);
-  if (T == 0) return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? SBP_OK : SBP_ERR_CUDA;
+  if (T == 0) return no_rows(offsets, E, nullptr, 0, dev_status, s);
   mm8::P p{};
   const int64_t kb = (K + 127) / 128, nb = (N + 127) / 128;
   p.A = static_cast<const uint8_t*>(A8); p.sa = sa; p.lda = K; p.sa_pitch = kb;
@@ -249,11 +267,7 @@ int sbp_matmul_e4m3_columns(const void* At8, const float* sat, const void* Bt8, 
   NvtxRange nv("sbp_matmul_e4m3_columns");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   set_launch_count(0);
-  if (T == 0) {
-    if (cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return SBP_ERR_CUDA;
-    if (!accumulate && cudaMemsetAsync(dW, 0, (size_t)E * N * K * sizeof(float), s) != cudaSuccess) return SBP_ERR_CUDA;
-    return SBP_OK;
-  }
+  if (T == 0) return no_rows(offsets, E, accumulate ? nullptr : dW, E * N * K, dev_status, s);
   mm8::P p{};
   const int64_t blocks = max_units(T, E, 128);
   p.A = static_cast<const uint8_t*>(At8); p.sa = sat; p.lda = blocks * 128; p.sa_pitch = blocks;

@@ -428,7 +428,7 @@ int sbp_quant_e4m3_columns(const void* X, const int32_t* offsets, int64_t E, int
   NvtxRange nv("sbp_quant_e4m3_columns");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   set_launch_count(0);
-  if (T == 0) return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? SBP_OK : SBP_ERR_CUDA;
+  if (T == 0) return no_rows(offsets, E, nullptr, 0, dev_status, s);
   const int64_t nb = max_units(T, E, 128), nf = (d + 127) / 128;
   TileP p{X, offsets, T, (int)E, (int)d, (int)nf, 0, 0, static_cast<uint8_t*>(Y8), scales,
           static_cast<uint8_t*>(Yt8), nb * 128, scales_t, (int)nb, dev_status};
