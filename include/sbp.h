@@ -532,6 +532,15 @@ const char* sbp_status_string(int status);
 /* Number of kernel launches the last successful call on this host thread enqueued. */
 int sbp_last_launch_count(void);
 
+/* Which kernel the last successful sbp_matmul_e4m3 or sbp_matmul_e4m3_columns call on this host
+ * thread enqueued. */
+#define SBP_PRODUCT_NONE 0     /* none yet, or a call without rows                            */
+#define SBP_PRODUCT_FEW 1      /* few rows, or little work                                    */
+#define SBP_PRODUCT_SWAP 2     /* few rows of several matrices: the operands exchanged        */
+#define SBP_PRODUCT_MANY_128 3 /* many rows, tiles of 128 columns                             */
+#define SBP_PRODUCT_MANY_256 4 /* many rows, tiles of 256 columns                             */
+int sbp_last_product_kernel(void);
+
 #ifdef __cplusplus
 }
 #endif

@@ -152,11 +152,15 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, MINB) k_mm8_few(const P p) {
   }
 }
 
+thread_local int g_ran = SBP_PRODUCT_NONE;
+void ran(int kernel) { g_ran = kernel; }
+
 template <int NT, int MINB>
 cudaError_t launch_few(const P& p, int64_t units, cudaStream_t s) {
   const int64_t items = units * ((p.nb + 15) / 16);
   const int64_t most = (int64_t)num_sms() * MINB;
   k_mm8_few<NT, MINB><<<(unsigned)std::max<int64_t>(1, std::min(items, most)), 32 * FEW_WARPS, 0, s>>>(p);
+  ran(SBP_PRODUCT_FEW);
   return cudaGetLastError();
 }
 
@@ -244,6 +248,7 @@ int sbp_matmul_e4m3(const void* A8, const float* sa, const void* B8, const float
   NvtxRange nv("sbp_matmul_e4m3");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   set_launch_count(0);
+  mm8::ran(SBP_PRODUCT_NONE);
   if (T == 0) return no_rows(offsets, E, nullptr, 0, dev_status, s);
   mm8::P p{};
   const int64_t kb = (K + 127) / 128, nb = (N + 127) / 128;
@@ -267,6 +272,7 @@ int sbp_matmul_e4m3_columns(const void* At8, const float* sat, const void* Bt8, 
   NvtxRange nv("sbp_matmul_e4m3_columns");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   set_launch_count(0);
+  mm8::ran(SBP_PRODUCT_NONE);
   if (T == 0) return no_rows(offsets, E, accumulate ? nullptr : dW, E * N * K, dev_status, s);
   mm8::P p{};
   const int64_t blocks = max_units(T, E, 128);
@@ -277,5 +283,7 @@ int sbp_matmul_e4m3_columns(const void* At8, const float* sat, const void* Bt8, 
   p.columns = 1; p.out = SBP_FP32; p.accumulate = accumulate ? 1 : 0; p.C = dW; p.status = dev_status;
   return mm8::run(p, s);
 }
+
+int sbp_last_product_kernel(void) { return mm8::g_ran; }
 
 }  // extern "C"

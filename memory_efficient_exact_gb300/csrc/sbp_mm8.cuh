@@ -77,6 +77,8 @@ inline int64_t about_blocks(const P& p) {
   return p.columns ? (p.kblocks + p.E - 1) / p.E : p.kblocks;
 }
 
+void ran(int kernel);   // for sbp_last_product_kernel
+
 // The kernel for many rows (sbp_mm8_tc.cu): enqueues the status word's reset and the product.
 cudaError_t many(const P& p, cudaStream_t s);
 int64_t many_ns(const P& p);   // about how long it takes

@@ -274,6 +274,7 @@ cudaError_t launch_swap(const P& p, cudaStream_t s) {
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   const int pairs = (int)std::min<int64_t>(max_pairs((const void*)kern, SMEM_SWAP, SW_THREADS), tiles);
   kern<<<2 * pairs, SW_THREADS, SMEM_SWAP, s>>>(mA, mB, q);
+  ran(SBP_PRODUCT_SWAP);
   return cudaGetLastError();
 }
 

@@ -413,6 +413,7 @@ cudaError_t launch_many(const P& p, cudaStream_t s) {
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   const int pairs = (int)std::min<int64_t>(max_pairs((const void*)kern, SMEM_MM8, MM8_THREADS), tiles);
   kern<<<2 * pairs, MM8_THREADS, SMEM_MM8, s>>>(mA, mB, q);
+  ran(HALVES == 2 ? SBP_PRODUCT_MANY_256 : SBP_PRODUCT_MANY_128);
   return cudaGetLastError();
 }
 template <int HALVES>

@@ -128,6 +128,8 @@ def _load() -> ctypes.CDLL:
     lib.sbp_status_string.argtypes = [C]
     lib.sbp_last_launch_count.restype = C
     lib.sbp_last_launch_count.argtypes = []
+    lib.sbp_last_product_kernel.restype = C
+    lib.sbp_last_product_kernel.argtypes = []
     lib.sbp_profile_enable.restype = C
     lib.sbp_profile_enable.argtypes = [C]
     lib.sbp_profile_read.restype = C
@@ -151,6 +153,14 @@ def status_string(code: int) -> str:
 
 def last_launch_count() -> int:
     return int(_lib.sbp_last_launch_count())
+
+
+PRODUCT_KERNELS = ("none", "few", "swap", "many_128", "many_256")
+
+
+def last_product_kernel() -> str:
+    """Which kernel the last 8-bit product of this host thread ran on (``sbp_last_product_kernel``)."""
+    return PRODUCT_KERNELS[_lib.sbp_last_product_kernel()]
 
 
 KERNEL_CLASSES = ("forward_gemm", "backward_gemm", "logit_grad", "other")

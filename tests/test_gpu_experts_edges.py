@@ -1,8 +1,13 @@
 """GPU tests of the expert calls where their rules change: no rows at all, the sizes at which one
 kernel takes over from another, and what each of them does with values that are not finite."""
+import numpy as np
 import pytest
 
+from oracle import experts as X
+
 torch = pytest.importorskip("torch")
+from test_gpu_experts import check_product, dev, host, near, wide  # noqa: E402
+
 pytestmark = pytest.mark.gpu
 BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
@@ -73,3 +78,54 @@ def test_captured_call_without_rows_follows_its_table(sbp):
         graph.replay()
         torch.cuda.synchronize()
         assert int(st.item()) == (sbp.ERR_SEQLENS if bad else sbp.OK) and (dW == (7 if bad else 0)).all()
+
+
+# ------------------------------------------------------- every product kernel, known by name
+
+FEW, SWAP, NARROW, WIDE = "few", "swap", "many_128", "many_256"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kernel,lens,N,K", [
+    (FEW, [5], 264, 272), (FEW, [1, 0, 2, 0], 136, 144), (FEW, [31], 2048, 4112),
+    (SWAP, [20, 41, 7, 16], 8200, 1040), (SWAP, [20, 0, 64], 8200, 1040), (SWAP, [65, 0, 100, 2, 30, 8, 8, 70], 4104, 2064),
+    (NARROW, [600], 2056, 272), (NARROW, [700], 2568, 1040), (NARROW, [501, 529], 1544, 400), (NARROW, [1500], 4104, 128),
+    (WIDE, [600], 4104, 272), (WIDE, [300], 5128, 1040), (WIDE, [257, 0, 643, 300], 2568, 400), (WIDE, [1300], 1800, 144)])
+def test_each_kernel(sbp, kernel, lens, N, K, dtype):
+    off = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    check_product(sbp, off, N, K, dtype, N + K + len(lens))
+    assert sbp.last_product_kernel() == kernel
+
+
+@pytest.mark.parametrize("kernel,lens,N,K", [
+    (FEW, [5], 128, 128), (FEW, [300, 0, 200, 400], 72, 136),
+    (NARROW, [700], 520, 1544), (NARROW, [900, 0, 400], 264, 1032), (NARROW, [1500], 520, 1032),
+    (WIDE, [300], 1032, 2568), (WIDE, [130, 0, 570], 520, 1544), (WIDE, [1], 1032, 2568)])
+def test_each_kernel_of_columns(sbp, kernel, lens, N, K):
+    """dW against the oracle; accumulate adds it to what is there, in one rounding to fp32."""
+    g = np.random.default_rng(N + K)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    T = int(off[-1])
+    dy, x = wide(g, (T, N), "bf16") * 2.0 ** -14, wide(g, (T, K), "bf16")
+    kw = dict(offsets=None if len(lens) == 1 else dev(off, torch.int32))
+    a, b = sbp.quant_e4m3_columns(dev(dy, BF), **kw), sbp.quant_e4m3_columns(dev(x, BF), tiles=True, **kw)
+    args = [a["Yt8"], a["scales_t"], b["Yt8"], b["scales_t"], T]
+    r = sbp.matmul_e4m3_columns(*args, **kw)
+    assert sbp.last_product_kernel() == kernel and status(r) == sbp.OK
+    (qa, sa), (qb, sb) = X.quant(X.columns(dy, off)), X.quant(X.columns(x, off), 128)
+    want, terms = X.matmul_columns(qa, sa, qb, sb, off)
+    steps = 128 + max((n + 127) // 128 for n in lens) + 16
+    near("dW", host(r["dW"]).reshape(want.shape), want, steps * 2.0 ** -23 * terms)
+    before = torch.randn(r["dW"].shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    dW = before.clone()
+    assert status(sbp.matmul_e4m3_columns(*args, dW=dW, accumulate=True, **kw)) == sbp.OK
+    assert sbp.last_product_kernel() == kernel and torch.equal(dW, before + r["dW"])
+
+
+def test_kernel_of_a_call_without_rows(sbp):
+    f8 = lambda *s: torch.zeros(s, device="cuda").to(F8)
+    f32 = lambda *s: torch.zeros(s, device="cuda")
+    sbp.matmul_e4m3(f8(1, 32), f32(1, 1), f8(64, 32), f32(1, 1))
+    assert sbp.last_product_kernel() == FEW
+    sbp.matmul_e4m3(f8(0, 32), f32(0, 1), f8(64, 32), f32(1, 1))
+    assert sbp.last_product_kernel() == "none"
