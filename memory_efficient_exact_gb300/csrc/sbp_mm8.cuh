@@ -65,12 +65,14 @@ __device__ __forceinline__ Unit unit_of(const P& p, int unit, int u) {
 }
 
 // How many units of `unit` rows of A the call has, as far as the host knows: experts that few rows
-// go to have at least one each, long ones a last unit that is half full on average.
+// go to have at least one each, long ones a last unit that is half full on average, and there are no
+// more than T rows can make (one row to one of 64 experts is one unit and not 32).
 inline int64_t about_units(const P& p, int64_t unit) {
   if (p.columns) return (int64_t)p.E * ((p.na + unit - 1) / unit);
   if (p.E == 1) return (p.T + unit - 1) / unit;
   const int64_t used = p.E < p.T ? p.E : p.T, more = p.T / unit + p.E / 2;
-  return used > more ? used : more;
+  const int64_t units = used > more ? used : more, most = max_units(p.T, p.E, unit);
+  return units < most ? units : most;
 }
 // Blocks of 128 that a unit sums over, on average.
 inline int64_t about_blocks(const P& p) {

@@ -129,3 +129,18 @@ def test_kernel_of_a_call_without_rows(sbp):
     assert sbp.last_product_kernel() == FEW
     sbp.matmul_e4m3(f8(0, 32), f32(0, 1), f8(64, 32), f32(1, 1))
     assert sbp.last_product_kernel() == "none"
+
+
+# ----------------------------------------------------- where one kernel takes over from another
+
+@pytest.mark.parametrize("rows,E,N,K", [(1, 8, 4096, 4096), (2, 8, 4096, 4096), (1, 64, 4096, 2560), (2, 64, 4096, 2560),
+                                        (4, 64, 4096, 2560), (1, 256, 2048, 2048), (4, 256, 2048, 2048)])
+def test_fewer_rows_than_experts(sbp, rows, E, N, K):
+    """A token's rows make no more units than there are rows, however long the table is."""
+    lens = np.zeros(E, dtype=np.int64)
+    lens[np.arange(rows) * 37 % E] += 1
+    off = np.concatenate([[0], np.cumsum(lens)])
+    byte = lambda *s: torch.full(s, 0x38, dtype=torch.uint8, device="cuda").view(F8)      # ones
+    f32 = lambda *s: torch.ones(s, device="cuda")
+    r = sbp.matmul_e4m3(byte(rows, K), f32(rows, K // 128), byte(E, N, K), f32(E, N // 128, K // 128), offsets=dev(off, torch.int32))
+    assert sbp.last_product_kernel() == FEW and status(r) == sbp.OK and (host(r["C"]) == K).all()
