@@ -37,8 +37,9 @@ constexpr int FEW_WARPS = 8;
 // Few rows: what bounds the call is reading B once.  A block has 16 rows of B against 8 NT rows of
 // A, its warps sharing out the blocks of 128; they go straight from device memory into the
 // operands' registers.  (The order of k within a block of 128 is that of the 32 bytes a thread
-// loads, the same for A and B.)  8 rows x 24576 x 4096: 19.6 us, 5.2 TB/s.  Several blocks of 128 in
-// flight a warp, at the price of blocks an SM, were slower (28 us with two, 31 with four).
+// loads, the same for A and B.)  8 rows x 24576 x 4096: 22 us, 4.6 TB/s, with the matrix from memory;
+// 19.6 with the same one throughout, part of it in L2.  Several blocks of 128 in flight a warp, at the
+// price of blocks an SM, were slower than those 19.6 (28 us with two, 31 with four).
 // MINB blocks are resident an SM, and so many are launched.
 template <int NT, int MINB>
 __global__ void __launch_bounds__(32 * FEW_WARPS, MINB) k_mm8_few(const P p) {
@@ -155,11 +156,15 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, MINB) k_mm8_few(const P p) {
 thread_local int g_ran = SBP_PRODUCT_NONE;
 void ran(int kernel) { g_ran = kernel; }
 
-template <int NT, int MINB>
+// Blocks an SM, with the registers that leaves: 5 and 3 and 3 instead take 21.7 against 19.6 us for 8
+// rows and 16.2 against 10.9 for 32, N = 24576 and 4096, K = 4096, the same inputs throughout.
+constexpr int few_blocks(int nt) { return nt == 1 ? 4 : 2; }
+
+template <int NT>
 cudaError_t launch_few(const P& p, int64_t units, cudaStream_t s) {
   const int64_t items = units * ((p.nb + 15) / 16);
-  const int64_t most = (int64_t)num_sms() * MINB;
-  k_mm8_few<NT, MINB><<<(unsigned)std::max<int64_t>(1, std::min(items, most)), 32 * FEW_WARPS, 0, s>>>(p);
+  const int64_t most = (int64_t)num_sms() * few_blocks(NT);
+  k_mm8_few<NT, few_blocks(NT)><<<(unsigned)std::max<int64_t>(1, std::min(items, most)), 32 * FEW_WARPS, 0, s>>>(p);
   ran(SBP_PRODUCT_FEW);
   return cudaGetLastError();
 }
@@ -172,27 +177,35 @@ int few_tiles(const P& p) {
 cudaError_t few(const P& p, cudaStream_t s) {
   const int nt = few_tiles(p);
   const int64_t units = p.columns ? (int64_t)p.E * ((p.na + 8 * nt - 1) / (8 * nt)) : max_units(p.T, p.E, 8 * nt);
-  // (blocks an SM, with the registers that leaves: 5 and 3 and 3 instead of 4 and 2 and 2 take 21.7
-  // against 19.6 us for 8 rows and 16.2 against 10.9 for 32, N = 24576 and 4096, K = 4096)
-  if (nt == 1) return launch_few<1, 4>(p, units, s);
-  if (nt == 2) return launch_few<2, 2>(p, units, s);
-  return launch_few<4, 2>(p, units, s);
+  if (nt == 1) return launch_few<1>(p, units, s);
+  if (nt == 2) return launch_few<2>(p, units, s);
+  return launch_few<4>(p, units, s);
 }
 
-// k_mm8_few reads each unit's matrix at 5.2 TB/s (8 rows x 24576 x 4096: 19.6 us), and takes 1.55
-// and 2.65 times as long for units of 16 and 32 rows, whose values are converted for every strip.
+// k_mm8_few reads each unit's matrix at 5.5 TB/s behind a start of 4 us (8 rows x 24576 x 4096: 22
+// us), and takes 1.5 and 2.65 times as long for units of 16 and 32 rows, whose values are converted
+// for every strip.  Short sums are bound by the 2.1 us that a block takes for a strip of a unit at least
+// (1000 rows x 512 x 512: 10.5 us).
 int64_t few_ns(const P& p) {
   const int nt = few_tiles(p);
-  const int64_t bytes = (int64_t)p.nb * about_blocks(p) * 128;
-  return 4000 + about_units(p, 8 * nt) * bytes / 5200 * (nt == 1 ? 100 : nt == 2 ? 155 : 265) / 100;
+  const int64_t units = about_units(p, 8 * nt), blocks = (int64_t)num_sms() * few_blocks(nt);
+  const int64_t bytes = (int64_t)p.nb * about_blocks(p) * 128, items = units * ((p.nb + 15) / 16);
+  return std::max(4000 + units * bytes / 5500 * (nt == 1 ? 100 : nt == 2 ? 150 : 265) / 100,
+                  1600 + (items + blocks - 1) / blocks * 2100);
 }
 
-// The kernel that takes the least time by the three rules.  Measured, few / many / swap, in us:
-//   4096 x 4096, rows 1, 32, 48, 64:            6.8 17 16,  11 16 18,  16 16 18,  19 17 18
-//   24576 x 4096, rows 8, 32, 64:               21 33 23,  (33) 33 28,  - 34 39
-//   512 x 512, rows 300, 1000:                  5.7 10 -,  9.9 10 -
-//   64 experts, 4096 x 2560, rows 64, 192, 400, 1000, 2000:  74 92 68,  120 131 95,  149 133 97,  297 156 114,  555 159 139
-//   8 experts, 4096 x 4096, rows 16, 64, 128, 256:           22 40 24,  33 41 31,  58 42 31,  98 43 39
+// The kernel that takes the least time by the three rules.  Measured, few / many / swap, in us, with
+// other inputs from call to call, so that matrices come from memory (the kernel taken is within 5% of
+// the fastest in all of these and in 40 sizes more):
+//   4096 x 4096, rows 1, 32, 48, 64, 128:       6.7 19 15,  11.4 16.5 17.5,  17 16.5 18,  20 16.6 17.8,  35 17 18
+//   24576 x 4096, rows 8, 16, 32, 48, 64:       22 46 29,  32 42 31,  53 35 33,  81 35 39,  96 36 39
+//   4096 x 12288, rows 32, 64:                  28 31 37,  54 31 37
+//   512 x 512, rows 300, 1000:                  6.3 10.3 8.3,  10.5 10.3 8.3
+//   64 experts, 4096 x 2560, rows 1, 2, 4, 8, 16 of as many:  6.8 17 14,  7.9 19 14,  12.5 22 17,  22 32 23,  35 78 38
+//   the same, rows 64, 192, 400, 1000, 2000 of all:  123 144 107,  123 145 110,  125 147 111,  199 150 115,  352 155 122
+//   256 experts, 2048 x 2048, rows 1, 4, 16, 64 of as many:   5.7 16 12,  8.6 19 14,  19 31 21,  54 74 51
+//   8 experts, 4096 x 4096, rows 1, 4, 8, 16, 64, 128, 256:  7.7 20 16,  16 27 20,  28 44 31,  28 43 31,  30 40 31,  41 41 33,  65 42 35
+//   columns, 1024 x 1024 of 128 tokens, 512 x 512 of 1000, 128 x 256 of 1000 of 32 experts:  15 10 -,  7.6 11 -,  17 11 -
 int run(const P& p, cudaStream_t s) {
   const int64_t f = few_ns(p), m = many_ns(p), w = p.columns ? INT64_MAX : swap_ns(p);
   if ((f <= m && f <= w ? few(p, s) : m <= w ? many(p, s) : swap(p, s)) != cudaSuccess) return SBP_ERR_CUDA;

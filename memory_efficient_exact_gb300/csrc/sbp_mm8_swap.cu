@@ -5,8 +5,8 @@
 // the 256 rows of its products, 32 rows of A as their columns: per block of 128 it brings in 32 KB
 // of B and 4 KB of A through a ring of eleven stages, and its accumulators are 32 columns wide, so
 // that sixteen blocks are in flight in tensor memory and the exchange with the epilogue warps (one
-// row of B a thread, 32 sums in registers) never shows.  64 experts of 4096 x 2560, 192 rows: 95 us,
-// 6.7 TB/s over the experts that have rows; 120 with mma.sync, 131 with 256 rows of A a tile.
+// row of B a thread, 32 sums in registers) never shows.  64 experts of 4096 x 2560, three rows each, all
+// 671 MB from memory: 110 us, 6.1 TB/s; 123 with mma.sync, 145 with 256 rows of A a tile.
 #include <algorithm>
 
 #include "sbp_mm8_tc.cuh"
@@ -278,12 +278,13 @@ cudaError_t launch_swap(const P& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// A pair takes 340 ns for a block of 128 of its 256 rows of B where memory keeps up, which gives
-// 6.6 TB/s (64 experts of 4096 x 2560, 192 rows: 95 us).
+// A pair takes 310 ns for a block of 128 of its 256 rows of B where memory keeps up (32 rows x 4096 x
+// 12288: 36.7 us), and memory gives 6.0 TB/s, uneven last rounds included (8 experts of 4096 x 4096:
+// 30.7 us, 64 of 4096 x 2560: 107).
 int64_t swap_ns(const P& p) {
   const int64_t tiles = about_units(p, 32) * ((p.nb + 255) / 256), pairs = num_sms() / 2;
   const int64_t bytes = std::min<int64_t>(p.E, p.T) * p.nb * p.K;
-  return 6000 + std::max((tiles + pairs - 1) / pairs * about_blocks(p) * 340, bytes / 6600);
+  return 7400 + std::max((tiles + pairs - 1) / pairs * about_blocks(p) * 310, bytes / 6000);
 }
 
 cudaError_t swap(const P& p, cudaStream_t s) {

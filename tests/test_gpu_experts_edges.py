@@ -144,3 +144,28 @@ def test_fewer_rows_than_experts(sbp, rows, E, N, K):
     f32 = lambda *s: torch.ones(s, device="cuda")
     r = sbp.matmul_e4m3(byte(rows, K), f32(rows, K // 128), byte(E, N, K), f32(E, N // 128, K // 128), offsets=dev(off, torch.int32))
     assert sbp.last_product_kernel() == FEW and status(r) == sbp.OK and (host(r["C"]) == K).all()
+
+
+@pytest.mark.parametrize("kernel,lens,N,K", [
+    (NARROW, [48], 4096, 4096), (NARROW, [64], 4096, 4096), (NARROW, [128], 4096, 4096), (FEW, [32], 4096, 4096),
+    (FEW, [1] * 4 + [0] * 4, 4096, 4096), (FEW, [1] * 8, 4096, 4096), (SWAP, [16] * 8, 4096, 4096), (SWAP, [32], 24576, 4096),
+    (SWAP, [2000], 256, 256)])
+def test_kernel_that_measures_least(sbp, kernel, lens, N, K):
+    T, E = sum(lens), len(lens)
+    lead, off = ((), None) if E == 1 else ((E,), dev(np.concatenate([[0], np.cumsum(lens)]), torch.int32))
+    byte = lambda *s: torch.full(s, 0x38, dtype=torch.uint8, device="cuda").view(F8)
+    f32 = lambda *s: torch.ones(s, device="cuda")
+    r = sbp.matmul_e4m3(byte(T, K), f32(T, K // 128), byte(*lead, N, K), f32(*lead, N // 128, K // 128), offsets=off)
+    assert sbp.last_product_kernel() == kernel and status(r) == sbp.OK and (host(r["C"]) == K).all()
+
+
+@pytest.mark.parametrize("kernel,lens,N,K", [(NARROW, [128], 1024, 1024), (FEW, [1000], 512, 512), (NARROW, [30] * 32, 128, 256)])
+def test_kernel_of_columns_that_measures_least(sbp, kernel, lens, N, K):
+    T, E = sum(lens), len(lens)
+    off = None if E == 1 else dev(np.concatenate([[0], np.cumsum(lens)]), torch.int32)
+    a = sbp.quant_e4m3_columns(torch.ones(T, N, device="cuda"), offsets=off)
+    b = sbp.quant_e4m3_columns(torch.ones(T, K, device="cuda"), offsets=off, tiles=True)
+    r = sbp.matmul_e4m3_columns(a["Yt8"], a["scales_t"], b["Yt8"], b["scales_t"], T, offsets=off)
+    assert sbp.last_product_kernel() == kernel and status(r) == sbp.OK
+    # the scale fl(1 / 448) and its inverse are off by half a step of fp32 each, twice; sums of 448^2 n are exact
+    near("dW", host(r["dW"]).reshape(E, -1), np.array(lens, dtype=np.float64)[:, None], 2.0 ** -20 * np.array(lens)[:, None])
