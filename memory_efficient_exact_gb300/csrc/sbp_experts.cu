@@ -22,10 +22,14 @@ constexpr int SORT_WARPS = 16, SORT_PER_LANE = 4;
 constexpr int SORT_THREADS = 32 * SORT_WARPS;
 constexpr int SORT_SLOTS = SORT_THREADS * SORT_PER_LANE;   // slots of a block
 // From so many blocks on their counts are summed once (k_expert_scan) and not by every block, whose
-// work grows with their square.  64 experts, 32, 64, 128, 512, 2048 blocks: 14.0, 14.6, 14.7, 24.5, 60
-// us with the launch, 10.9, 12.5, 14.6, 41, 408 without; 8 experts 11.3, 12.0, 12.4, 17.4, 40 and 10.4,
-// 12.5, 14.5, 36, 191.
-constexpr int SCAN_BLOCKS = 64;
+// work grows with their square and with the experts that a thread has.  With the launch / without, us:
+//   blocks           32         48         64         96         128        256        512
+//   2 experts     11.3  9.4  11.3 10.3  11.3 10.3  11.3 11.4  11.3 12.3  12.3 16.5  15.7  31
+//   64 experts    13.4 11.9  14.4 12.3  14.4 12.4  14.4 14.4  14.8 15.0  16.5 20.5  23.7  42
+//   256 experts   15.2 13.1  15.4 14.4  15.4 14.4  16.2 15.6  16.4 16.4  18.5 22.6  27.7  55
+//   512 experts   16.4 14.4  16.4 15.2  16.4 16.4  17.3 16.5  17.4 18.5  20.5 27.3  30.8  68
+//   1024 experts  18.5 18.5  18.5 20.1  19.0 20.6  19.5 22.6  19.5 25.4  22.6 41.2  36.9 117
+bool sum_once(int64_t blocks, int64_t E) { return blocks >= std::min<int64_t>(128, 49152 / E); }
 
 struct SortP {
   const int32_t* ids;
@@ -435,7 +439,7 @@ int sbp_expert_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t
       }))
     return SBP_ERR_CUDA;
   SortP p{ids, L.n, (int)E, (int)std::max<int64_t>(L.blocks, 1), rows, slots, offsets,
-          reinterpret_cast<int32_t*>(w + L.off_counts), L.blocks >= SCAN_BLOCKS, dev_status};
+          reinterpret_cast<int32_t*>(w + L.off_counts), sum_once(L.blocks, E), dev_status};
   // (a block alone writes the status itself)
   if (p.blocks > 1 && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return SBP_ERR_CUDA;
   int st = workspace_guards(w, L.guards, 0, dev_status, s, &launches);

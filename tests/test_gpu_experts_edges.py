@@ -169,3 +169,17 @@ def test_kernel_of_columns_that_measures_least(sbp, kernel, lens, N, K):
     assert sbp.last_product_kernel() == kernel and status(r) == sbp.OK
     # the scale fl(1 / 448) and its inverse are off by half a step of fp32 each, twice; sums of 448^2 n are exact
     near("dW", host(r["dW"]).reshape(E, -1), np.array(lens, dtype=np.float64)[:, None], 2.0 ** -20 * np.array(lens)[:, None])
+
+
+@pytest.mark.parametrize("E,blocks,launches", [(64, 1, 1), (64, 2, 2), (64, 64, 2), (8, 96, 2), (300, 127, 2), (64, 128, 3), (384, 128, 3),
+                                               (512, 95, 2), (512, 96, 3), (1024, 47, 2), (1024, 48, 3)])
+def test_sort_sums_counts_once_where_that_is_shorter(sbp, E, blocks, launches):
+    ids = np.random.default_rng(E + blocks).integers(-1, E, (2048 * blocks - 5, 1))
+    r = sbp.expert_sort(dev(ids, torch.int32), E)
+    assert sbp.last_launch_count() == launches and status(r) == sbp.OK
+    n = int((ids >= 0).sum())
+    assert np.array_equal(host(r["slots"])[:n], np.argsort(np.where(ids < 0, E, ids).reshape(-1), kind="stable")[:n])
+    assert np.array_equal(host(r["offsets"]), np.concatenate([[0], np.cumsum(np.bincount(ids[ids >= 0], minlength=E))]))
+    rows = np.full(ids.size, -1)
+    rows[host(r["slots"])[:n].astype(np.int64)] = np.arange(n)
+    assert np.array_equal(host(r["rows"]).reshape(-1), rows)
