@@ -399,7 +399,8 @@ void launch_combine_bwd(const CombineBwdP& p, cudaStream_t s) {
   const dim3 b = token_block(p.d / 8), g((unsigned)((p.T + b.y - 1) / b.y));
   if (p.k == 1) k_expert_combine_bwd<E, 1><<<g, b, 0, s>>>(p);
   else if (p.k == 2) k_expert_combine_bwd<E, 2><<<g, b, 0, s>>>(p);
-  else if (p.k <= 4 || sizeof(E) == 4) k_expert_combine_bwd<E, 4><<<g, b, 0, s>>>(p);
+  else if constexpr (sizeof(E) == 4) k_expert_combine_bwd<E, 4><<<g, b, 0, s>>>(p);
+  else if (p.k <= 4) k_expert_combine_bwd<E, 4><<<g, b, 0, s>>>(p);
   else k_expert_combine_bwd<E, 8><<<g, b, 0, s>>>(p);
 }
 

@@ -252,8 +252,7 @@ int sbp_matmul_e4m3(const void* A8, const float* sa, const void* B8, const float
                     void* stream) {
   if (E < 1 || T < 0 || N < 1 || K < 1 || (!offsets && E != 1) || (out_dtype != SBP_BF16 && out_dtype != SBP_FP32))
     return SBP_ERR_INVALID_ARG;
-  if (E > MAX_GROUPS || K % 16 != 0 || N % 8 != 0 || T > (int64_t(1) << 30) || N > mm8::MAX_SIDE || K > mm8::MAX_SIDE ||
-      E * N > INT32_MAX - 256)
+  if (E > MAX_GROUPS || K % 16 != 0 || N % 8 != 0 || T > (int64_t(1) << 30) || N > mm8::MAX_SIDE || K > mm8::MAX_SIDE)
     return SBP_ERR_UNSUPPORTED;
   if (!dev_status || (T > 0 && (!A8 || !sa || !B8 || !sb || !C))) return SBP_ERR_INVALID_ARG;
   const int rc = mm8::check_common(E, T, N, K, A8, sa, B8, sb, offsets, C, dev_status);

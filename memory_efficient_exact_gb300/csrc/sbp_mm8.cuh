@@ -7,6 +7,7 @@ namespace sbp {
 namespace mm8 {
 
 constexpr int64_t MAX_SIDE = 1 << 20;
+static_assert(MAX_GROUPS * MAX_SIDE < INT32_MAX - 256, "rows of all matrices are counted in 32 bits");
 
 struct P {
   const uint8_t* A;   // rows: [T, K]; columns: [na, 128 * kblocks]

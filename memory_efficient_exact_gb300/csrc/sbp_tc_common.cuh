@@ -341,8 +341,7 @@ __device__ __forceinline__ void fail(Ctrl* c, int32_t* status) {
   if (status) atomicCAS(status, 0, SBP_ERR_TIMEOUT);
 }
 
-// epi_warps: the epilogue warps of one CTA, which release an accumulator.
-__device__ __forceinline__ void prologue(Ctrl* c, int warp, int epi_warps = NUM_EPI_WARPS) {
+__device__ __forceinline__ void prologue(Ctrl* c, int warp) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&c->full[i], 1);
@@ -350,7 +349,7 @@ __device__ __forceinline__ void prologue(Ctrl* c, int warp, int epi_warps = NUM_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->tfull[i], 1);
-      mbar_init(&c->tempty[i], 2 * epi_warps);
+      mbar_init(&c->tempty[i], 2 * NUM_EPI_WARPS);
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&c->rfull[i], 1);
