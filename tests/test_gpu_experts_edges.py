@@ -183,3 +183,110 @@ def test_sort_sums_counts_once_where_that_is_shorter(sbp, E, blocks, launches):
     rows = np.full(ids.size, -1)
     rows[host(r["slots"])[:n].astype(np.int64)] = np.arange(n)
     assert np.array_equal(host(r["rows"]).reshape(-1), rows)
+
+
+# -------------------------------------------------------------- values that are not ordinary
+
+def strange(dtype):
+    """[300, 264] values: a NaN, an infinity, subnormals, the type's largest and a column of NaN, each
+    in a tile of its own and several of them apart; the places of the NaNs and the infinities."""
+    big, tiny = (3.3895314e38, 2.0 ** -133) if dtype == BF else (3.4028235e38, 2.0 ** -149)
+    x = np.random.default_rng(4).standard_normal((300, 264)).astype(np.float32)
+    x = torch.from_numpy(x).to(dtype).float().numpy()
+    nan, inf = np.zeros(x.shape, dtype=bool), np.zeros(x.shape, dtype=bool)
+    nan[5, 7] = nan[5, 8] = nan[127, 127] = True       # in the first tile
+    nan[:128, 140] = True                              # a column's whole block
+    nan[200, 128:256] = True                           # a row's whole block
+    inf[130, 3] = inf[299, 263] = True
+    x[256:300, 0:128] = tiny                           # a tile of subnormals
+    x[256:300, 128:256] = 0
+    x[299, 130] = -tiny * 3
+    x[140, 260] = -big
+    x[inf] = np.inf
+    x[130, 3] = -np.inf
+    return x, nan, inf
+
+
+def same_but_for(q, s, nan, inf, rows, cols, want_q, want_s):
+    """Scales and values of blocks of rows x cols: those of the array with its NaNs as zeros; NaNs where
+    they were; blocks with an infinity stand for NaN."""
+    for i in range(0, nan.shape[0], rows):
+        for j in range(0, nan.shape[1], cols):
+            at = np.s_[i:i + rows, j:j + cols]
+            sq = s[i // rows, j // cols]
+            if inf[at].any():
+                with np.errstate(invalid="ignore"):
+                    assert np.isinf(sq) and np.isnan(q[at] * sq).all()
+                continue
+            assert sq == want_s[i // rows, j // cols], (i, j)
+            assert np.isnan(q[at][nan[at]]).all() and np.array_equal(q[at][~nan[at]], want_q[at][~nan[at]]), (i, j)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quantisers_with_strange_values(sbp, dtype):
+    x, nan, inf = strange(dtype)
+    plain = np.where(nan | inf, np.float32(0), x)
+    t = dev(np.where(nan, np.float32(np.nan), x), dtype)
+    assert torch.equal(t[~torch.from_numpy(nan).cuda()], dev(x, dtype)[~torch.from_numpy(nan).cuda()])
+    r = sbp.quant_e4m3(t)
+    same_but_for(host(r["Y8"]), host(r["scales"]), nan, inf, 1, 128, *X.quant(plain))
+    off = [0, 300]
+    xt = lambda a: X.columns(a, off)
+    pad = lambda m: np.pad(m, ((0, 84), (0, 0))).T
+    for tiles in (False, True):
+        for rows in (False, True):
+            c = sbp.quant_e4m3_columns(t, tiles=tiles, rows=rows)
+            assert status(c) == sbp.OK
+            same_but_for(host(c["Yt8"]), host(c["scales_t"]), pad(nan), pad(inf), 128 if tiles else 1, 128,
+                         *X.quant(xt(plain), 128 if tiles else 1))
+            if rows:
+                same_but_for(host(c["Y8"]), host(c["scales"]), nan, inf, 1, 128, *X.quant(plain))
+    w = sbp.quant_e4m3_weight(t[:288, :256].contiguous())
+    at = np.s_[:288, :256]
+    want_q, want_s = X.quant(plain[at], 128)
+    same_but_for(host(w["W8"]), host(w["scales"]), nan[at], inf[at], 128, 128, want_q, want_s)
+    same_but_for(host(w["Wt8"]), host(w["scales_t"]), nan[at].T, inf[at].T, 128, 128, want_q.T, want_s.T)
+    e = host(sbp.quant_e4m3_expand(w["W8"], w["scales"], F32, tiles=True)["Y"])
+    with np.errstate(invalid="ignore"):
+        v = host(w["W8"]) * np.repeat(np.repeat(host(w["scales"]), 128, 0)[:288], 128, 1)
+    assert np.array_equal(np.isnan(e), np.isnan(v))
+    near("expand", e[~np.isnan(v)], v[~np.isnan(v)], 2.0 ** -24 * np.abs(v[~np.isnan(v)]) + 2.0 ** -150)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weights_of_dropped_slots_are_not_read(sbp, dtype):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    T, k, E, d = 33, 3, 5, 136
+    ids = torch.randint(-1, E, (T, k), generator=g, device="cuda").int()
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")
+    o = sbp.expert_sort(ids, E)
+    ys, dy, w = n(T * k, d).to(dtype), n(T, d).to(dtype), n(T, k)
+    junk = torch.where(ids < 0, torch.full_like(w, float("nan")), w)
+    zero = torch.where(ids < 0, torch.zeros_like(w), w)
+    assert torch.equal(sbp.expert_combine(ys, o["rows"], junk)["Y"], sbp.expert_combine(ys, o["rows"], zero)["Y"])
+    back = [sbp.expert_combine_backward(dy, ys, o["rows"], v, dYs=torch.zeros_like(ys)) for v in (junk, zero)]
+    assert all(torch.equal(back[0][key], back[1][key]) for key in ("dYs", "dweights"))
+    assert (back[0]["dweights"][ids < 0] == 0).all() and torch.isfinite(back[0]["dYs"].float()).all()
+
+
+@pytest.mark.parametrize("kernel,lens,N,K", [(FEW, [300, 0, 200, 400], 72, 136), (NARROW, [900, 0, 400], 264, 1032), (WIDE, [130, 0, 570], 520, 1544)])
+def test_nan_in_columns(sbp, kernel, lens, N, K):
+    """A NaN among an expert's tokens reaches its own row or column of that expert's dW, and no other."""
+    g = np.random.default_rng(N)
+    off, T = dev(np.concatenate([[0], np.cumsum(lens)]), torch.int32), sum(lens)
+    dy, x = dev(g.standard_normal((T, N)), BF), dev(g.standard_normal((T, K)), BF)
+    def run():
+        a, b = sbp.quant_e4m3_columns(dy, offsets=off), sbp.quant_e4m3_columns(x, offsets=off, tiles=True)
+        r = sbp.matmul_e4m3_columns(a["Yt8"], a["scales_t"], b["Yt8"], b["scales_t"], T, offsets=off)
+        assert sbp.last_product_kernel() == kernel and status(r) == sbp.OK
+        return r["dW"]
+    for t in (dy[0, 3], dy[lens[0], N - 1], x[lens[0] + 1, 9]):     # (one must not be its block's largest)
+        t.zero_()
+    clean = run()
+    dy[0, 3], dy[lens[0], N - 1], x[lens[0] + 1, 9] = (float("nan"),) * 3
+    got = run()
+    nan = torch.zeros(clean.shape, dtype=torch.bool, device="cuda")
+    e = [i for i, n in enumerate(lens) if n][1]
+    nan[0, 3] = nan[e, N - 1] = True
+    nan[e, :, 9] = True
+    assert torch.isnan(got[nan]).all() and torch.equal(got[~nan], clean[~nan])
