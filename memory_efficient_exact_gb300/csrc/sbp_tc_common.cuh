@@ -628,13 +628,15 @@ inline bool once_per_device(int (&state)[64], std::mutex& mu, F set) {
 // device and kernel.
 inline int max_pairs(const void* kernel, size_t smem_bytes, int threads = NUM_THREADS) {
   struct Entry { const void* k; int dev; int n; };
-  static Entry cache[32] = {};
+  static Entry cache[64 * 32] = {};   // some 30 kernels on each of 64 devices
   static std::mutex mu;
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lk(mu);
-  for (auto& e : cache)
-    if (e.k == kernel && e.dev == dev && e.n > 0) return e.n;
+  for (auto& e : cache) {
+    if (e.k == nullptr) break;
+    if (e.k == kernel && e.dev == dev) return e.n;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * 76, 1, 1);
   cfg.blockDim = dim3((unsigned)threads, 1, 1);
