@@ -379,9 +379,10 @@ int sbp_rope_qkv_backward(const void* dQ, const void* dK, const void* dV, int kv
  *     quant_e4m3_columns(X, tiles), matmul_e4m3_columns                        dW
  *     combine                          the experts' rows back in token order, weighted
  * Rows of expert e are offsets[e] .. offsets[e+1] (device int32 [E+1], from 0, non-decreasing, at
- * most T; SBP_ERR_SEQLENS in the status otherwise and nothing is computed).  The table is read by
- * the device only, so a captured call follows its contents.  Experts without rows are allowed; rows
- * behind offsets[E] belong to none and outputs are left as they were there.  E is at most 1024.
+ * most T; SBP_ERR_SEQLENS in the status otherwise and nothing is computed; with T = 0 as well).  The
+ * table is read by the device only, so a captured call follows its contents.  Experts without rows are
+ * allowed; rows behind offsets[E] belong to none and outputs are left as they were there.  E is at
+ * most 1024.
  * Fixed order of every sum.  Stream and error rules as for the LM-head calls.
  *
  * Sort: ids [T, k] int32 (device), the experts of each token's k slots; a slot with a negative id
@@ -450,8 +451,8 @@ int sbp_quant_e4m3_weight(const void* W, int64_t E, int64_t N, int64_t K, int dt
  * for the rows i of expert e.  A8 [T, K] e4m3 with sa [T, ceil(K / 128)]; B8 [E, N, K] with sb
  * [E, ceil(N / 128), ceil(K / 128)]; C [T, N] bf16 or fp32 (out_dtype).  A block's sum and the sum
  * over the blocks are fp32, and so is sa sb, which is formed first: below 2^-126 it loses precision,
- * from 2^128 on it is infinite.  Which of three kernels runs goes by the sizes (host values alone);
- * they differ in the order of the fp32 sums.  K must be a multiple of 16, N of 8.
+ * from 2^128 on it is infinite.  Which of the kernels runs goes by the sizes (host values alone;
+ * sbp_last_product_kernel tells); they differ in the order of the fp32 sums.  K must be a multiple of 16, N of 8.
  * columns: dW[e] (+)= sum over expert e's tokens of At8 and Bt8, both as sbp_quant_e4m3_columns
  * leaves them for these offsets (At8 [N, 128 nb] without tiles, Bt8 [K, 128 nb] with): dW [E, N, K]
  * fp32, overwritten (accumulate = 0; zeros for an expert without rows) or added to (1).

@@ -233,7 +233,10 @@ struct CombineP {
 
 // KU slots' rows in flight at a time: first where they lie and their weights, then the rows, then
 // the sum.  Six blocks an SM and four rows in flight a thread do better than fewer blocks with eight
-// (8192 tokens, 8 slots, d = 4096: 88 us, 6850 GB/s; 103 to 117).
+// (8192 tokens, 8 slots, d = 4096: 88 us, 6850 GB/s; 103 to 117).  In fp32 the 40 registers that six
+// blocks leave do not hold four rows and the sums, and one or two slots spill 12 and 8 bytes; blocks
+// still count for more: 8192 tokens, d = 4096, one and two slots 47 and 60 us, 55 and 67 with four or
+// three blocks, 4096 tokens of 8 slots 88 either way; 4099 tokens, two slots, d = 2560 20.1, 22.5.
 template <typename E, int KU>
 __global__ void __launch_bounds__(256, 6) k_expert_combine(const CombineP p) {
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;

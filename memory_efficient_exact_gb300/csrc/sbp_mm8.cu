@@ -5,8 +5,9 @@
 //   columns  dW[e, m, n] (+)= the same sum over the blocks b of expert e's tokens, A and B being
 //            what the column quantiser leaves
 //
-// A has a scale for each row and block of 128, B one for each 128 x 128 tile.  The products of one
-// block are exact in fp32 but for the order of the sum; a block's sum is scaled and added in fp32.
+// A has a scale for each row and block of 128, B one for each 128 x 128 tile.  Each product of two
+// values is exact in fp32; the tensor cores add a block's up in fp32 (and may cut a sum off instead of
+// rounding it); a block's sum is scaled and added in fp32, rounded.
 #include <algorithm>
 
 #include "sbp_groups.cuh"

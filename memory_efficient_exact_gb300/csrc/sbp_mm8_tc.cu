@@ -17,9 +17,10 @@
 // columns, 16 epilogue warps that loaded 16 columns at a time and scales read by each; 1785 with
 // four accumulators of 128 and the scales' warp; 1717 with two issuing warps; 1383 with eight
 // epilogue warps of 224 registers and the unrolled loop; 1350 with the scales multiplied in advance;
-// 1285 with accumulators of their own (2570 TFLOP/s).  Not faster: packed additions of two values
-// (1599 against 1620 TFLOP/s in an earlier form), 16 epilogue warps (1405 against 1355), the next
-// columns' load before these are added (1352 against 1290).
+// 1285 with accumulators of their own (2570 TFLOP/s).  All of these with the same inputs throughout; with
+// other inputs from call to call, at the power cap, the last form takes 1300 to 1420 (2540 to 2320
+// TFLOP/s).  Not faster: packed additions of two values (1599 against 1620 TFLOP/s in an earlier form), 16
+// epilogue warps (1405 against 1355), the next columns' load before these are added (1352 against 1290).
 #include <algorithm>
 
 #include "sbp_mm8_tc.cuh"
@@ -31,7 +32,8 @@ namespace tc {
 // epilogue's: 32 rows x 64 columns of each accumulator, or x 128 of every other one.  The block's
 // 12 x 32 threads are launched with 168 registers each; the epilogue's 128 sums and 64 values in
 // flight need more, so the first four warps hand theirs over.  (Waits are inlined: a call would not
-// know of the split.)
+// know of the split.)  The split leaves the first four warps short: the compiler spills 104 bytes a
+// thread and loads 152 back in the forms of 256 columns, 304 in those of 128.
 constexpr int MM8_EPI = 8, MM8_THREADS = 128 + 32 * MM8_EPI;
 constexpr int REGS_LAUNCH = 168, REGS_FEW = 56, REGS_MANY = 224;
 static_assert(128 * REGS_FEW + 32 * MM8_EPI * REGS_MANY <= MM8_THREADS * REGS_LAUNCH, "no more than the block has");
@@ -423,8 +425,9 @@ cudaError_t launch_many(const P& p, cudaStream_t s) {
 }
 
 // Tiles of 256 columns take 496 ns a block on all pairs at once, tiles of 128 columns 281 (16384 x
-// 24576 x 4096: 1285 and 1453 us); the narrow ones leave fewer pairs idle (501 x 4096 x 12288: 53
-// and 33 us).  The shorter of the two sums of rounds is taken.
+// 24576 x 4096, the same inputs throughout: 1285 and 1453 us), where all eight epilogue warps take every
+// accumulator; the narrow ones leave fewer pairs idle (501 x 4096 x 12288: 53 and 33 us).  The shorter of
+// the two sums of rounds is taken.
 int64_t rounds_ns(const P& p, int halves) {
   const int64_t bn = 128 * halves, pairs = num_sms() / 2;
   return (about_units(p, 256) * ((p.nb + bn - 1) / bn) + pairs - 1) / pairs * about_blocks(p) * (halves == 2 ? 496 : 281);

@@ -26,7 +26,11 @@ __device__ __forceinline__ void fail_mm8(C* c, int32_t* status) {
   *(volatile int*)&c->abort = 1;
   if (status) atomicCAS(status, 0, SBP_ERR_TIMEOUT);
 }
-// An arrival on a barrier of this CTA, or on one of the pair's (no branch).
+// An arrival on a barrier of this CTA, or on one of the pair's (no branch).  The remote one has the
+// instruction's default semantics, as arrive_remote: nothing in memory is handed over with it, only an
+// accumulator whose values tcgen05.wait::ld has shown to be in registers.  A release at cluster scope
+// costs 548 us instead of 288 for 32768 x 2560 x 4096 of 32 experts, 99 instead of 33 for 501 x 4096 x
+// 12288, 233 instead of 108 for 64 rows of 64 experts.
 __device__ __forceinline__ void arrive_if(bool here, uint32_t local, bool there, uint32_t remote) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\tsetp.ne.b32 q, %2, 0;\n\t"

@@ -593,9 +593,10 @@ cudaError_t launch_early(void (*kernel)(P...), int grid, int threads, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Failure-detection test hook: SBP_FAULT_STALL=1 makes the next LM-head forward kernels,
-// norm backward kernels (rows of more than 2048 columns) and 8-bit products (many rows) stall on purpose (read at every launch, so a test can switch it off again).  Together with a
-// short SBP_WAIT_LIMIT_MS it exercises the bounded-wait abort path: status
+// Failure-detection test hook: SBP_FAULT_STALL=1 makes the next LM-head forward kernels, norm
+// backward kernels (rows of more than 2048 columns) and 8-bit products (all but the kernel of
+// SBP_PRODUCT_FEW) stall on purpose (read at every launch, so a test can switch it off again).
+// Together with a short SBP_WAIT_LIMIT_MS it exercises the bounded-wait abort path: status
 // SBP_ERR_TIMEOUT, copies drained, tensor memory freed, the context still usable.
 inline int fault_stall_requested() {
   const char* e = std::getenv("SBP_FAULT_STALL");
