@@ -533,8 +533,8 @@ const char* sbp_status_string(int status);
 /* Number of kernel launches the last successful call on this host thread enqueued. */
 int sbp_last_launch_count(void);
 
-/* Which kernel the last successful sbp_matmul_e4m3 or sbp_matmul_e4m3_columns call on this host
- * thread enqueued. */
+/* Which kernel the last sbp_matmul_e4m3 or sbp_matmul_e4m3_columns call on this host thread that
+ * passed its argument checks enqueued. */
 #define SBP_PRODUCT_NONE 0     /* none yet, or a call without rows                            */
 #define SBP_PRODUCT_FEW 1      /* few rows, or little work                                    */
 #define SBP_PRODUCT_SWAP 2     /* few rows of several matrices: the operands exchanged        */
